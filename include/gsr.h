@@ -144,6 +144,166 @@ gsr_status flash_attention_fwd(const void* Q, const void* K, const void* V, void
                                int64_t head_dim, float softmax_scale, int causal,
                                struct CUstream_st* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Attention of language models: masked attention with its gradient, a paged key/value cache, and
+ * attention of drafted tokens over it.  float16 or bfloat16, head_dim 64 or 128, any number of
+ * query heads per key/value head.  Scores, softmax and sums in float32.  Caller-owned buffers;
+ * asynchronous on `stream`; no memory shared between calls except the per-stream error word, so
+ * calls and graph replays on different streams may run at the same time.
+ * ------------------------------------------------------------------------------------------ */
+typedef enum gsr_dtype { GSR_F16 = 0, GSR_BF16 = 1 } gsr_dtype;
+
+/*
+ * A batch x head x row x D operand: element strides, multiples of 8, D contiguous, data 16-byte
+ * aligned.  Any order of the other three dimensions is fine (batch, row, head as a projection
+ * leaves it; the parts of a fused projection's output).  A dimension of size 1 has no stride; a
+ * stride of 0 (a broadcast) is refused with GSR_ERR_INVALID_ARG.
+ */
+typedef struct gsr_tensor {
+    void* data;
+    int64_t stride_batch, stride_head, stride_row;
+} gsr_tensor;
+
+/*
+ * Sizes, masks and scores of masked attention.  Query i stands at position p = i + (seq_kv -
+ * seq_q) among the keys; query head h reads key/value head h / (heads_q / heads_kv).
+ *
+ *   score(i, j) = s - slope[h] |p - j|,   s = softmax_scale q_i.k_j without a cap, else
+ *                                         s = softcap tanh(softmax_scale q_i.k_j / softcap)
+ *
+ * Keys a query sees: those of its document [start, end) (all of them without documents), cut with
+ * `causal` to j <= p or j < start + prefix, whichever reaches further.
+ *
+ *   softmax_scale  0 selects 1/sqrt(head_dim).
+ *   softcap        0: no cap; must not be negative.
+ *   alibi_slopes   NULL: no distance bias; else device pointer to heads_q float32.  Constants: no
+ *                  gradient is computed for them.
+ *   doc_bounds     NULL: no documents; else device pointer to batch x (num_docs + 1) int32,
+ *                  ascending within a batch row: document d of row b holds positions
+ *                  [doc_bounds[b][d], doc_bounds[b][d + 1]).  Positions outside all documents are
+ *                  padding: they see nothing and nothing sees them, whatever they hold (NaN too).
+ *                  Equal boundaries are an empty document.  Needs seq_q == seq_kv.  Boundaries
+ *                  that are not ascending give unspecified results, without a fault.
+ *   prefix_lens    NULL: none; else device pointer to batch x max(num_docs, 1) int32, the number
+ *                  of leading keys of each document (or row) that all its queries see.  Needs
+ *                  `causal`.
+ */
+typedef struct gsr_attention_desc {
+    int64_t batch, heads_q, heads_kv, seq_q, seq_kv, head_dim;
+    int32_t dtype; /* gsr_dtype */
+    int32_t causal;
+    float softmax_scale;
+    float softcap;
+    const float* alibi_slopes;
+    const int32_t* doc_bounds;
+    int64_t num_docs;
+    const int32_t* prefix_lens;
+} gsr_attention_desc;
+
+/*
+ * O = softmax(score) V over the keys each query sees.  Q, O: batch x heads_q x seq_q x head_dim;
+ * K, V: batch x heads_kv x seq_kv x head_dim; lse: batch x heads_q x seq_q float32, contiguous
+ * (NULL: not written), the natural log-sum-exp of the scores.  A query that sees no key gets O = 0
+ * and lse = -inf.  Keys a query does not see have no influence on it, also when they hold
+ * infinities or NaN.  Probabilities are rounded to the operands' type for the second product, the
+ * output once.  O must share no element with an input, lse lies apart from everything.
+ */
+gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor* Q, const gsr_tensor* K,
+                                const gsr_tensor* V, const gsr_tensor* O, float* lse,
+                                struct CUstream_st* stream);
+
+/*
+ * Gradients of masked_attention_fwd: dQ, dK, dV from dO and the forward's inputs, O and lse (dO,
+ * O, dQ shaped as Q; dK, dV as K).  dK and dV sum over the query heads of a group.  Results do not
+ * depend on the order of execution.  P and dS are rounded to the operands' type for the matrix
+ * products; in float16 dS carries a power of two that keeps it in range for any size of dO.
+ * Queries without keys get dQ = 0 and add nothing, whatever their dO holds.
+ *
+ *   workspace  device pointer, 16-byte aligned, masked_attention_bwd_workspace(desc) bytes, for
+ *              this call alone until it has finished.
+ */
+int64_t masked_attention_bwd_workspace(const gsr_attention_desc* desc);
+gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor* dO, const gsr_tensor* Q,
+                                const gsr_tensor* K, const gsr_tensor* V, const gsr_tensor* O,
+                                const float* lse, const gsr_tensor* dQ, const gsr_tensor* dK,
+                                const gsr_tensor* dV, void* workspace, int64_t workspace_bytes,
+                                struct CUstream_st* stream);
+
+/*
+ * Attention of drafted tokens over a paged cache.  Request b has kv_lens[b] tokens in the cache;
+ * the last T_b = q_starts[b + 1] - q_starts[b] of them are its drafted tokens, whose keys and
+ * values have been written like any other token's.  They are the nodes of a tree: row q_starts[b]
+ * + t of Q and O belongs to node t, parents[q_starts[b] + t] is the node above it (an earlier one,
+ * or -1 for the token before the tree).  A node sees every token before the tree, its ancestors
+ * and itself, and stands at position kv_lens[b] - T_b + its depth.  parents == NULL: a chain (each
+ * node below the one before it).  T_b = 1 is an ordinary decoding step; T_b = 0 is fine.
+ *
+ *   k_cache, v_cache  num_pages pages of page_size rows (a multiple of 8; stride_batch steps from
+ *                     page to page); row r of request b is row r % page_size of page
+ *                     block_tables[b][r / page_size].  Entries outside [0, num_pages) hold no
+ *                     tokens: nothing sees them.  Cache rows behind kv_lens[b] have no influence.
+ *   block_tables      batch x table_width int32.  Lengths above table_width x page_size are cut.
+ *   max_nodes         the most nodes of a request, 1 to GSR_TREE_MAX_NODES.  Rows of further
+ *                     nodes and rows behind q_starts[batch] are left as they were.
+ *   softcap, alibi_slopes, softmax_scale  as in gsr_attention_desc.
+ *   Q, O              total_q x heads_q x head_dim with the given strides; heads_q / heads_kv <= 128.
+ * kv_lens, q_starts (batch + 1), parents (total_q): device int32.  A node that sees nothing gets
+ * O = 0.
+ *
+ *   workspace  device pointer, 16-byte aligned, tree_attention_workspace(desc) bytes, for this
+ *              call alone until it has finished.
+ */
+#define GSR_TREE_MAX_NODES 64
+typedef struct gsr_tree_desc {
+    int64_t batch, total_q, heads_q, heads_kv, head_dim;
+    int64_t num_pages, page_size, table_width, max_nodes;
+    int64_t q_stride_row, q_stride_head, o_stride_row, o_stride_head;
+    int32_t dtype; /* gsr_dtype */
+    float softmax_scale;
+    float softcap;
+    const float* alibi_slopes;
+} gsr_tree_desc;
+int64_t tree_attention_workspace(const gsr_tree_desc* desc);
+gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gsr_tensor* k_cache,
+                              const gsr_tensor* v_cache, const int32_t* block_tables, const int32_t* kv_lens,
+                              const int32_t* q_starts, const int32_t* parents, void* O, void* workspace,
+                              int64_t workspace_bytes, struct CUstream_st* stream);
+
+/*
+ * One step's bookkeeping of a paged cache, on the device: request b has kv_lens[b] tokens and gets
+ * new_lens[b] more (negative lengths count as 0).  Pages are taken from free_blocks, from entry
+ * free_head[0] on, in request order.
+ *
+ *   block_tables   batch x table_width, updated in place: the new pages' entries are written.
+ *   kv_lens_out    batch: kv_lens + new_lens.           free_head_out  1: free_head + pages taken.
+ *   q_starts       batch + 1: where each request's new tokens start among all of them.
+ *   positions, slots  max_tokens: each new token's position in its request and its row in the
+ *                  cache, page x page_size + row; -1 behind the last token.
+ *   counts         3: new tokens, pages taken, pages missing.
+ * Pages are missing when the free list ends or a request outgrows table_width; their table
+ * entries (those inside the table) and their tokens' slots are -1.  All int32 device arrays;
+ * outputs overlap nothing (kv_lens_out and free_head_out are not the inputs: swap them between
+ * steps).  batch <= 8192; the sum of new_lens and num_pages x page_size below 2^31.
+ */
+gsr_status kv_block_tables(const int32_t* kv_lens, const int32_t* new_lens, const int32_t* free_blocks,
+                           const int32_t* free_head, int32_t* block_tables, int32_t* kv_lens_out,
+                           int32_t* free_head_out, int32_t* q_starts, int32_t* positions, int32_t* slots,
+                           int32_t* counts, int64_t batch, int64_t table_width, int64_t page_size,
+                           int64_t num_free, int64_t max_tokens, struct CUstream_st* stream);
+
+/*
+ * Writes new keys and values to their cache rows: row n of K (V) goes to row slots[n] % page_size
+ * of page slots[n] / page_size.  Slots outside the cache (-1: padding) are skipped; other cache
+ * rows are left as they were.  K, V: tokens x heads x head_dim (stride_row steps from token to
+ * token; stride_batch unused) of any 16-bit type, head_dim a multiple of 8.  Where two tokens have
+ * the same slot, the row holds pieces of either.  k_cache and v_cache may be the two halves of one
+ * buffer.
+ */
+gsr_status kv_cache_append(const gsr_tensor* K, const gsr_tensor* V, const int32_t* slots,
+                           const gsr_tensor* k_cache, const gsr_tensor* v_cache, int64_t tokens,
+                           int64_t heads, int64_t head_dim, int64_t num_pages, int64_t page_size,
+                           struct CUstream_st* stream);
+
 /*
  * gemm_scale_relu with the operands in host memory: copies A and B host ->
  * device into the caller's device buffers dA and dB, runs gemm_scale_relu
@@ -223,7 +383,8 @@ gsr_status gemm_scale_relu_noalloc(const void* A, const void* B, void* C, int64_
  * waiting for a free accumulator, 4 epilogue waiting for a finished
  * accumulator, 5 teardown drain, 6 shared-memory window not 1024-byte aligned:
  * the kernel returned at once), 0x100 = tiled kernel, 0x200 = small-M,
- * 0x300 = attention.
+ * 0x300 = attention, 0x400 = masked attention, 0x500 and 0x600 = its gradients of K, V and of Q,
+ * 0x700 = tree attention.
  */
 gsr_status gsr_device_status(struct CUstream_st* stream, int* code);
 

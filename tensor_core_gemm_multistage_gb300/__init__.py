@@ -13,6 +13,8 @@ from .binding import (KERNEL_PAIR, KERNEL_PAIR_128, KERNEL_SKINNY, KERNEL_TILED,
                       gemm_scale_relu_host_ptr, gemm_scale_relu_ptr, last_cuda_error, lib,
                       library_path, select_path, set_path_override, set_raster_group, set_split_k, set_test_flags,
                       set_wait_timeout_ns, shutdown, status_string, version)
+from .llm import (TREE_MAX_NODES, kv_block_tables, kv_cache_append, masked_attention_bwd,
+                  masked_attention_bwd_workspace, masked_attention_fwd, tree_attention_fwd)
 from ._build import build
 
 __all__ = [
@@ -20,6 +22,8 @@ __all__ = [
     "Status", "build", "device_status", "flash_attention_fwd", "gemm_bias_gelu", "gemm_bias_gelu_ptr", "gemm_scale",
     "gemm_scale_relu", "gemm_scale_relu_host",
     "gemm_scale_relu_host_ptr", "gemm_scale_relu_ptr", "last_cuda_error", "lib", "library_path",
+    "TREE_MAX_NODES", "kv_block_tables", "kv_cache_append", "masked_attention_bwd", "masked_attention_bwd_workspace",
+    "masked_attention_fwd", "tree_attention_fwd",
     "release_stream", "select_path", "set_path_override", "set_raster_group", "set_split_k", "set_test_flags", "set_wait_timeout_ns", "shutdown",
     "status_string", "version",
 ]

@@ -98,6 +98,8 @@ def lib() -> ctypes.CDLL:
         L.gsr_version.argtypes = []
         L.gsr_shutdown.restype = i32
         L.gsr_shutdown.argtypes = []
+        from . import llm
+        llm._declare(L)
         _lib = L
         return L
 

@@ -1,0 +1,175 @@
+// attention_common.cuh - what the masked, backward and tree attention kernels share: element
+// types, the interval of keys a query sees, the score function, and attention of single rows.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "device_common.cuh"
+#include "llm.h"
+
+namespace gsr {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ---------------------------------------------------------------------------
+// fp16 and bf16
+// ---------------------------------------------------------------------------
+template <class T>
+struct Elem;
+template <>
+struct Elem<__half> {
+    static constexpr bool bf16 = false;
+    static __device__ __forceinline__ float2 unpack(uint32_t v) {
+        return __half22float2(*reinterpret_cast<const __half2*>(&v));
+    }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+    static constexpr bool bf16 = true;
+    static __device__ __forceinline__ float2 unpack(uint32_t v) {
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+};
+
+// ---------------------------------------------------------------------------
+// The keys a query sees: one interval [lo, hi)
+// ---------------------------------------------------------------------------
+// A document mask keeps [start, end) of the query's own document; a causal mask ends the interval
+// behind the query's position p, a prefix behind the prefix if that is later.  With boundaries in
+// ascending order lo and hi never fall from one query to the next, so the keys of a block of
+// queries are [lo of its first, hi of its last).  A query outside every document gets an empty
+// interval at the nearest boundary, which keeps that order.
+__device__ __forceinline__ void row_interval(const MaskArgs& m, int b, int i, int& lo, int& hi) {
+    int s = 0, e = m.Skv, d = 0;
+    if (m.num_docs > 0) {
+        const int* bounds = m.doc_bounds + (long long)b * (m.num_docs + 1);
+        int left = 0, right = m.num_docs + 1;          // first boundary above i
+        while (left < right) {
+            const int mid = (left + right) >> 1;
+            if (__ldg(bounds + mid) <= i) left = mid + 1;
+            else right = mid;
+        }
+        d = left - 1;
+        if (d < 0 || d >= m.num_docs) {
+            lo = hi = min(max(__ldg(bounds + (d < 0 ? 0 : m.num_docs)), 0), m.Skv);
+            return;
+        }
+        s = max(__ldg(bounds + d), 0);
+        e = min(__ldg(bounds + d + 1), m.Skv);
+    }
+    lo = s;
+    hi = e;
+    if (m.causal) {
+        int limit = i + m.offset + 1;
+        if (m.prefix_lens) {
+            const long long n = m.num_docs > 0 ? m.num_docs : 1;
+            limit = max(limit, s + min(max(__ldg(m.prefix_lens + b * n + d), 0), m.Skv - s));
+        }
+        hi = min(e, limit);
+    }
+    hi = max(hi, lo);
+}
+
+// ---------------------------------------------------------------------------
+// Scores
+// ---------------------------------------------------------------------------
+// rcp.approx: within 1 ulp; +inf gives 0.
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// tanh(x) = 1 - 2 / (1 + e^(2x)): with r = 1 / (1 + 2^(cap_in s)) the capped score is
+// cap_out (1 - 2 r), and tanh's derivative 4 r (1 - r) has no cancellation.  The absolute error
+// of a score is a few units of cap 2^-24, which is what the softmax sees.
+__device__ __forceinline__ float cap_r(float s, float cap_in) { return rcp_approx(1.0f + ex2_approx(s * cap_in)); }
+
+// ---------------------------------------------------------------------------
+// One row by one warp
+// ---------------------------------------------------------------------------
+// Lane t holds elements [t D/32, (t + 1) D/32) of a row.
+template <class T, int D>
+__device__ __forceinline__ void load_row(const T* row, int lane, float (&x)[D / 32]) {
+    if constexpr (D == 128) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(row) + lane);
+        const float2 a = Elem<T>::unpack(v.x), b = Elem<T>::unpack(v.y);
+        x[0] = a.x;
+        x[1] = a.y;
+        x[2] = b.x;
+        x[3] = b.y;
+    } else {
+        const float2 a = Elem<T>::unpack(__ldg(reinterpret_cast<const uint32_t*>(row) + lane));
+        x[0] = a.x;
+        x[1] = a.y;
+    }
+}
+template <class T, int D>
+__device__ __forceinline__ void store_row(T* row, int lane, const float (&x)[D / 32]) {
+    if constexpr (D == 128)
+        reinterpret_cast<uint2*>(row)[lane] = make_uint2(Elem<T>::pack(x[0], x[1]), Elem<T>::pack(x[2], x[3]));
+    else
+        reinterpret_cast<uint32_t*>(row)[lane] = Elem<T>::pack(x[0], x[1]);
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+template <int N>
+__device__ __forceinline__ float warp_dot(const float (&a)[N], const float (&b)[N]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s = fmaf(a[i], b[i], s);
+    return warp_sum(s);
+}
+
+// The score of a raw product in log2 units, before the distance bias; `grad` is its derivative
+// with respect to scale * product.
+__device__ __forceinline__ float score_of(float s, const ScoreArgs& sc, float& grad) {
+    if (sc.cap_in == 0.0f) {
+        grad = 1.0f;
+        return s * sc.sl2;
+    }
+    const float r = cap_r(s, sc.cap_in);
+    grad = 4.0f * r * (1.0f - r);
+    return sc.cap_out * (1.0f - 2.0f * r);
+}
+
+// Softmax-weighted sum of the values of keys [lo, hi) that `at` lets the row see, in one pass with
+// the running maximum m and sum l.  at(j, k, v, dist) gives key j's rows and its distance.
+template <class T, int D, class At>
+__device__ __forceinline__ void row_forward(const float (&q)[D / 32], int lo, int hi, const ScoreArgs& sc,
+                                            float slope2, int lane, At at, float (&acc)[D / 32], float& m,
+                                            float& l) {
+    m = -INFINITY;
+    l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
+    for (int j = lo; j < hi; ++j) {
+        const T *k, *v;
+        float dist, grad, x[D / 32];
+        if (!at(j, k, v, dist)) continue;
+        load_row<T, D>(k, lane, x);
+        const float y = score_of(warp_dot(q, x), sc, grad) - slope2 * dist;
+        load_row<T, D>(v, lane, x);
+        const float mn = fmaxf(m, y);
+        const float f = mn == -INFINITY ? 0.0f : ex2_approx(m - mn);
+        const float p = mn == -INFINITY ? (isnan(y) ? y : 0.0f) : ex2_approx(y - mn);
+        l = fmaf(l, f, p);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(acc[i], f, p * x[i]);
+        m = mn;
+    }
+}
+
+}  // namespace gsr

@@ -17,6 +17,7 @@
 
 #include "gsr.h"
 #include "attention.h"
+#include "host_state.h"
 #include "kernels.h"
 
 namespace {
@@ -656,6 +657,42 @@ gsr_status host_pipe(int dev, HostPipe** out) {
 }
 
 }  // namespace
+
+namespace gsr {
+namespace host {
+
+gsr_status fail(cudaError_t e) { return cuda_fail(e); }
+
+gsr_status fail_encode(CUresult r) {
+    t_last_cuda_error = static_cast<int>(r);
+    return GSR_ERR_CUDA;
+}
+
+gsr_status current_device(int* dev, int* num_sms) {
+    DeviceInfo info;
+    const gsr_status s = device_info(dev, &info);
+    if (s == GSR_OK) *num_sms = info.num_sms;
+    return s;
+}
+
+gsr_status error_word(int dev, cudaStream_t stream, int** err) {
+    StreamState st;
+    const gsr_status s = stream_state(dev, stream, 0, 0, &st);
+    if (s == GSR_OK) *err = st.err;
+    return s;
+}
+
+gsr_status tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* encode) {
+    const gsr_status s = load_encoder();
+    *encode = g_encode;
+    return s;
+}
+
+uint64_t wait_timeout_ns() { return g_timeout_ns.load(std::memory_order_relaxed); }
+uint32_t test_flags() { return g_test_flags.load(std::memory_order_relaxed); }
+
+}  // namespace host
+}  // namespace gsr
 
 extern "C" {
 

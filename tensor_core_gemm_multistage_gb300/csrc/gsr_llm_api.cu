@@ -1,0 +1,380 @@
+// gsr_llm_api.cu - the C ABI of masked attention and its gradient, tree attention over a paged
+// cache, and the cache's bookkeeping: argument checks and launches.  See include/gsr.h for the
+// contract.
+#include <climits>
+#include <cmath>
+
+#include "host_state.h"
+#include "llm.h"
+
+namespace {
+
+using gsr::Strided;
+
+bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+bool bad_size(int64_t n) { return n < 0 || n > INT_MAX; }
+// The tensor maps' strides are below 2^40 bytes; no operand spans more than 2^60 elements.
+constexpr int64_t kMaxStride = ((int64_t)1 << 39) - 8;
+
+// Checks a strided operand of `batch` x `heads` x `rows` x d elements and fills in `out`; a
+// dimension of one element has no stride.  Rows, heads and batches of an output lie apart.
+gsr_status operand(const gsr_tensor* t, int64_t batch, int64_t heads, int64_t rows, int64_t d, bool output,
+                   Strided* out) {
+    if (!t) return GSR_ERR_INVALID_ARG;
+    *out = Strided{t->data, d, d, d};
+    if (batch == 0 || heads == 0 || rows == 0) return GSR_OK;
+    if (!t->data) return GSR_ERR_INVALID_ARG;
+    if (misaligned(t->data, 16)) return GSR_ERR_ALIGNMENT;
+    const int64_t n[3] = {batch, heads, rows}, stride[3] = {t->stride_batch, t->stride_head, t->stride_row};
+    long long* to[3] = {&out->batch, &out->head, &out->row};
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] == 1) continue;
+        if (stride[i] <= 0 || stride[i] > kMaxStride || (output && stride[i] < d)) return GSR_ERR_INVALID_ARG;
+        if (stride[i] & 7) return GSR_ERR_ALIGNMENT;
+        *to[i] = stride[i];
+    }
+    return GSR_OK;
+}
+
+// First byte and end of everything a strided operand may touch.
+struct Span {
+    uintptr_t lo, hi;
+};
+Span span_of(const Strided& t, int64_t batch, int64_t heads, int64_t rows, int64_t d, int64_t size) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(t.data);
+    if (!t.data || batch == 0 || heads == 0 || rows == 0) return {0, 0};
+    return {lo, lo + (uintptr_t)(((batch - 1) * t.batch + (heads - 1) * t.head + (rows - 1) * t.row + d) * size)};
+}
+bool meet(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// Whether two 16-bit operands may share elements.  Views of one buffer that lie side by side in
+// each row of it (the parts of a fused projection: equal row strides, heads inside the row) do not.
+bool share(const Strided& a, int64_t a_heads, int64_t a_rows, const Strided& b, int64_t b_heads, int64_t b_rows,
+           int64_t batch, int64_t d) {
+    if (!meet(span_of(a, batch, a_heads, a_rows, d, 2), span_of(b, batch, b_heads, b_rows, d, 2))) return false;
+    const int64_t a_wide = (a_heads - 1) * a.head + d, b_wide = (b_heads - 1) * b.head + d, pitch = a.row;
+    if (a_rows < 2 || b_rows < 2 || a.row != b.row || (batch > 1 && (a.batch != b.batch || a.batch % pitch))) return true;
+    const int64_t apart = (int64_t)(reinterpret_cast<uintptr_t>(a.data) - reinterpret_cast<uintptr_t>(b.data)) / 2;
+    const int64_t at = ((apart % pitch) + pitch) % pitch;      // a's columns, in b's rows
+    return !(at >= b_wide && at + a_wide <= pitch);
+}
+
+gsr_status check_desc(const gsr_attention_desc* d) {
+    if (!d) return GSR_ERR_INVALID_ARG;
+    for (int64_t n : {d->batch, d->heads_q, d->heads_kv, d->seq_q, d->seq_kv, d->num_docs})
+        if (bad_size(n)) return GSR_ERR_INVALID_ARG;
+    if (d->head_dim != 64 && d->head_dim != 128) return GSR_ERR_INVALID_ARG;
+    if (d->dtype != GSR_F16 && d->dtype != GSR_BF16) return GSR_ERR_INVALID_ARG;
+    if (d->heads_q > 0 && (d->heads_kv == 0 || d->heads_q % d->heads_kv)) return GSR_ERR_INVALID_ARG;
+    if (!std::isfinite(d->softmax_scale) || !std::isfinite(d->softcap) || d->softcap < 0.0f) return GSR_ERR_INVALID_ARG;
+    if (d->seq_q > INT_MAX - 256 || d->seq_kv > INT_MAX - 256) return GSR_ERR_INVALID_ARG;
+    if ((d->num_docs > 0) != (d->doc_bounds != nullptr)) return GSR_ERR_INVALID_ARG;
+    if (d->num_docs > 0 && d->seq_q != d->seq_kv) return GSR_ERR_INVALID_ARG;   // documents mask a row with itself
+    if (d->prefix_lens && !d->causal) return GSR_ERR_INVALID_ARG;               // nothing for a prefix to add
+    if (misaligned(d->alibi_slopes, 4) || misaligned(d->doc_bounds, 4) || misaligned(d->prefix_lens, 4))
+        return GSR_ERR_ALIGNMENT;
+    // work items and rows are counted in int (a row of the padded workspace, eight per CTA)
+    const double tiles = (double)d->batch * (double)d->heads_q * (double)((d->seq_q + 127) / 128);
+    const double key_tiles = (double)d->batch * (double)d->heads_kv * (double)((d->seq_kv + 127) / 128);
+    if (tiles > INT_MAX / 64 || key_tiles > INT_MAX / 64) return GSR_ERR_INVALID_ARG;
+    return GSR_OK;
+}
+
+gsr::MaskArgs mask_args(const gsr_attention_desc* d) {
+    gsr::MaskArgs m;
+    m.B = (int)d->batch;
+    m.Hq = (int)d->heads_q;
+    m.Hkv = (int)d->heads_kv;
+    m.group = d->heads_kv ? (int)(d->heads_q / d->heads_kv) : 1;
+    m.Sq = (int)d->seq_q;
+    m.Skv = (int)d->seq_kv;
+    m.offset = (int)(d->seq_kv - d->seq_q);
+    m.causal = d->causal ? 1 : 0;
+    m.num_docs = (int)d->num_docs;
+    m.doc_bounds = d->doc_bounds;
+    m.prefix_lens = d->prefix_lens;
+    return m;
+}
+
+gsr::ScoreArgs score_args(float softmax_scale, float softcap, const float* slopes, int64_t head_dim) {
+    constexpr double log2e = 1.4426950408889634;
+    const double scale = softmax_scale != 0.0f ? (double)softmax_scale : 1.0 / std::sqrt((double)head_dim);
+    gsr::ScoreArgs s;
+    s.scale = (float)scale;
+    s.sl2 = (float)(scale * log2e);
+    s.cap_in = softcap > 0.0f ? (float)(2.0 * log2e * scale / softcap) : 0.0f;
+    s.cap_out = (float)(softcap * log2e);
+    s.slopes = slopes;
+    return s;
+}
+
+// Layout of the backward pass's workspace, 256-byte pieces.
+struct BwdLayout {
+    int64_t sp, lse2, delta, lo, hi, total;
+};
+BwdLayout bwd_layout(const gsr_attention_desc* d) {
+    auto piece = [](int64_t bytes) { return (bytes + 255) / 256 * 256; };
+    BwdLayout w;
+    w.sp = (d->seq_q + 127) / 128 * 128;
+    w.lse2 = 256;                                                     // the norms come first
+    w.delta = w.lse2 + piece(4 * d->batch * d->heads_q * w.sp);
+    w.lo = w.delta + piece(4 * d->batch * d->heads_q * w.sp);
+    w.hi = w.lo + piece(4 * d->batch * w.sp);
+    w.total = w.hi + piece(4 * d->batch * w.sp);
+    return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor* Q, const gsr_tensor* K,
+                                const gsr_tensor* V, const gsr_tensor* O, float* lse, CUstream_st* stream) {
+    gsr_status s = check_desc(desc);
+    if (s != GSR_OK) return s;
+    const int64_t B = desc->batch, Hq = desc->heads_q, Hkv = desc->heads_kv, Sq = desc->seq_q, Skv = desc->seq_kv,
+                  D = desc->head_dim;
+    gsr::MaskedFwdParams p;
+    if ((s = operand(Q, B, Hq, Sq, D, false, &p.Q)) != GSR_OK || (s = operand(K, B, Hkv, Skv, D, false, &p.K)) != GSR_OK ||
+        (s = operand(V, B, Hkv, Skv, D, false, &p.V)) != GSR_OK || (s = operand(O, B, Hq, Sq, D, true, &p.O)) != GSR_OK)
+        return s;
+    if (B == 0 || Hq == 0 || Sq == 0) return GSR_OK;
+    if (misaligned(lse, 4)) return GSR_ERR_ALIGNMENT;
+    if (share(p.O, Hq, Sq, p.Q, Hq, Sq, B, D) || share(p.O, Hq, Sq, p.K, Hkv, Skv, B, D) ||
+        share(p.O, Hq, Sq, p.V, Hkv, Skv, B, D))
+        return GSR_ERR_ALIAS;
+    if (lse) {
+        const uintptr_t l0 = reinterpret_cast<uintptr_t>(lse);
+        const Span l{l0, l0 + (uintptr_t)(B * Hq * Sq * 4)};
+        if (meet(l, span_of(p.Q, B, Hq, Sq, D, 2)) || meet(l, span_of(p.K, B, Hkv, Skv, D, 2)) ||
+            meet(l, span_of(p.V, B, Hkv, Skv, D, 2)) || meet(l, span_of(p.O, B, Hq, Sq, D, 2)))
+            return GSR_ERR_ALIAS;
+    }
+    int dev = 0, sms = 0;
+    if ((s = gsr::host::current_device(&dev, &sms)) != GSR_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if ((s = gsr::host::error_word(dev, st, &p.err)) != GSR_OK) return s;
+    p.mask = mask_args(desc);
+    p.score = score_args(desc->softmax_scale, desc->softcap, desc->alibi_slopes, D);
+    p.lse = lse;
+    p.timeout_ns = gsr::host::wait_timeout_ns();
+    p.test_flags = gsr::host::test_flags();
+    const cudaError_t e = gsr::launch_masked_fwd(p, (int)D, desc->dtype == GSR_BF16, st);
+    return e == cudaSuccess ? GSR_OK : gsr::host::fail(e);
+}
+
+int64_t masked_attention_bwd_workspace(const gsr_attention_desc* desc) {
+    return check_desc(desc) == GSR_OK ? bwd_layout(desc).total : -1;
+}
+
+gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor* dO, const gsr_tensor* Q,
+                                const gsr_tensor* K, const gsr_tensor* V, const gsr_tensor* O, const float* lse,
+                                const gsr_tensor* dQ, const gsr_tensor* dK, const gsr_tensor* dV, void* workspace,
+                                int64_t workspace_bytes, CUstream_st* stream) {
+    gsr_status s = check_desc(desc);
+    if (s != GSR_OK) return s;
+    const int64_t B = desc->batch, Hq = desc->heads_q, Hkv = desc->heads_kv, Sq = desc->seq_q, Skv = desc->seq_kv,
+                  D = desc->head_dim;
+    gsr::MaskedBwdParams p;
+    struct {
+        const gsr_tensor* t;
+        bool q, out;
+        Strided* to;
+    } all[] = {{dO, true, false, &p.dO}, {Q, true, false, &p.Q},   {K, false, false, &p.K},  {V, false, false, &p.V},
+               {O, true, false, &p.O},   {dQ, true, true, &p.dQ},  {dK, false, true, &p.dK}, {dV, false, true, &p.dV}};
+    for (auto& a : all)
+        if ((s = operand(a.t, B, a.q ? Hq : Hkv, a.q ? Sq : Skv, D, a.out, a.to)) != GSR_OK) return s;
+    const bool no_q = B == 0 || Hq == 0 || Sq == 0, no_k = B == 0 || Hkv == 0 || Skv == 0;
+    if (no_q && no_k) return GSR_OK;
+    if (!no_q && !lse) return GSR_ERR_INVALID_ARG;
+    const BwdLayout w = bwd_layout(desc);
+    if (!workspace || workspace_bytes < w.total) return GSR_ERR_INVALID_ARG;
+    if (misaligned(lse, 4) || misaligned(workspace, 16)) return GSR_ERR_ALIGNMENT;
+    // outputs share elements with nothing; the workspace and lse lie apart from the operands
+    const uintptr_t w0 = reinterpret_cast<uintptr_t>(workspace), l0 = reinterpret_cast<uintptr_t>(lse);
+    const Span ws{w0, w0 + (uintptr_t)w.total}, ls{l0, lse ? l0 + (uintptr_t)(B * Hq * Sq * 4) : l0};
+    if (meet(ws, ls)) return GSR_ERR_ALIAS;
+    for (size_t i = 0; i < sizeof(all) / sizeof(all[0]); ++i) {
+        const auto& a = all[i];
+        const int64_t ah = a.q ? Hq : Hkv, ar = a.q ? Sq : Skv;
+        const Span sa = span_of(*a.to, B, ah, ar, D, 2);
+        if (meet(ws, sa) || (a.out && meet(ls, sa))) return GSR_ERR_ALIAS;
+        if (!a.out) continue;
+        for (size_t j = 0; j < i; ++j) {
+            const auto& b = all[j];
+            if (share(*a.to, ah, ar, *b.to, b.q ? Hq : Hkv, b.q ? Sq : Skv, B, D)) return GSR_ERR_ALIAS;
+        }
+    }
+    int dev = 0, sms = 0;
+    if ((s = gsr::host::current_device(&dev, &sms)) != GSR_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if ((s = gsr::host::error_word(dev, st, &p.err)) != GSR_OK) return s;
+    p.mask = mask_args(desc);
+    p.score = score_args(desc->softmax_scale, desc->softcap, desc->alibi_slopes, D);
+    p.lse = lse;
+    char* base = static_cast<char*>(workspace);
+    p.norms = reinterpret_cast<unsigned*>(base);
+    p.Sp = (int)w.sp;
+    p.lse2 = reinterpret_cast<float*>(base + w.lse2);
+    p.delta = reinterpret_cast<float*>(base + w.delta);
+    p.lo = reinterpret_cast<int*>(base + w.lo);
+    p.hi = reinterpret_cast<int*>(base + w.hi);
+    p.timeout_ns = gsr::host::wait_timeout_ns();
+    p.test_flags = gsr::host::test_flags();
+    const cudaError_t e = gsr::launch_masked_bwd(p, (int)D, desc->dtype == GSR_BF16, st);
+    return e == cudaSuccess ? GSR_OK : gsr::host::fail(e);
+}
+
+gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gsr_tensor* k_cache,
+                              const gsr_tensor* v_cache, const int32_t* block_tables, const int32_t* kv_lens,
+                              const int32_t* q_starts, const int32_t* parents, void* O, void* workspace,
+                              int64_t workspace_bytes, CUstream_st* stream) {
+    if (!desc) return GSR_ERR_INVALID_ARG;
+    const gsr_tree_desc& d = *desc;
+    for (int64_t n : {d.batch, d.total_q, d.heads_q, d.heads_kv, d.num_pages, d.page_size, d.table_width})
+        if (bad_size(n)) return GSR_ERR_INVALID_ARG;
+    if (d.head_dim != 64 && d.head_dim != 128) return GSR_ERR_INVALID_ARG;
+    if (d.dtype != GSR_F16 && d.dtype != GSR_BF16) return GSR_ERR_INVALID_ARG;
+    if (d.max_nodes < 1 || d.max_nodes > GSR_TREE_MAX_NODES) return GSR_ERR_INVALID_ARG;
+    if (d.heads_q > 0 && (d.heads_kv == 0 || d.heads_q % d.heads_kv || d.heads_q / d.heads_kv > 128))
+        return GSR_ERR_INVALID_ARG;
+    if (!std::isfinite(d.softmax_scale) || !std::isfinite(d.softcap) || d.softcap < 0.0f) return GSR_ERR_INVALID_ARG;
+    if (d.page_size < 8 || d.page_size % 8 || d.table_width * d.page_size > INT_MAX - 256) return GSR_ERR_INVALID_ARG;
+    if (d.batch == 0 || d.total_q == 0 || d.heads_q == 0) return GSR_OK;
+    if (!Q || !O || !kv_lens || !q_starts || (d.table_width > 0 && !block_tables)) return GSR_ERR_INVALID_ARG;
+    if (misaligned(Q, 16) || misaligned(O, 16) || misaligned(workspace, 16)) return GSR_ERR_ALIGNMENT;
+    for (const void* a : {(const void*)kv_lens, (const void*)q_starts, (const void*)parents, (const void*)block_tables,
+                          (const void*)d.alibi_slopes})
+        if (misaligned(a, 4)) return GSR_ERR_ALIGNMENT;
+    gsr::TreeParams p;
+    gsr_status s;
+    const gsr_tensor qt{const_cast<void*>(Q), 0, d.q_stride_head, d.q_stride_row}, ot{O, 0, d.o_stride_head, d.o_stride_row};
+    Strided qs, os;
+    if ((s = operand(&qt, 1, d.heads_q, d.total_q, d.head_dim, false, &qs)) != GSR_OK ||
+        (s = operand(&ot, 1, d.heads_q, d.total_q, d.head_dim, true, &os)) != GSR_OK ||
+        (s = operand(k_cache, d.num_pages, d.heads_kv, d.page_size, d.head_dim, false, &p.K)) != GSR_OK ||
+        (s = operand(v_cache, d.num_pages, d.heads_kv, d.page_size, d.head_dim, false, &p.V)) != GSR_OK)
+        return s;
+    const Span o = span_of(os, 1, d.heads_q, d.total_q, d.head_dim, 2);
+    if (share(os, d.heads_q, d.total_q, qs, d.heads_q, d.total_q, 1, d.head_dim) ||
+        meet(o, span_of(p.K, d.num_pages, d.heads_kv, d.page_size, d.head_dim, 2)) ||
+        meet(o, span_of(p.V, d.num_pages, d.heads_kv, d.page_size, d.head_dim, 2)))
+        return GSR_ERR_ALIAS;
+    const int64_t need = tree_attention_workspace(desc);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GSR_ERR_INVALID_ARG;
+    int dev = 0, sms = 0;
+    if ((s = gsr::host::current_device(&dev, &sms)) != GSR_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if ((s = gsr::host::error_word(dev, st, &p.err)) != GSR_OK) return s;
+    p.B = (int)d.batch;
+    p.Hq = (int)d.heads_q;
+    p.Hkv = (int)d.heads_kv;
+    p.group = p.Hq / p.Hkv;
+    p.D = (int)d.head_dim;
+    p.page = (int)d.page_size;
+    p.num_pages = (int)d.num_pages;
+    p.table_width = (int)d.table_width;
+    p.max_nodes = (int)d.max_nodes;
+    p.total_q = (int)d.total_q;
+    p.score = score_args(d.softmax_scale, d.softcap, d.alibi_slopes, d.head_dim);
+    p.Q = Q;
+    p.q_row = qs.row;
+    p.q_head = qs.head;
+    p.O = O;
+    p.o_row = os.row;
+    p.o_head = os.head;
+    p.table = block_tables;
+    p.kv_lens = kv_lens;
+    p.q_starts = q_starts;
+    p.parents = parents;
+    p.workspace = workspace;
+    p.timeout_ns = gsr::host::wait_timeout_ns();
+    p.test_flags = gsr::host::test_flags();
+    const cudaError_t e = gsr::launch_tree(p, d.dtype == GSR_BF16, st);
+    return e == cudaSuccess ? GSR_OK : gsr::host::fail(e);
+}
+
+int64_t tree_attention_workspace(const gsr_tree_desc* desc) { return desc ? 0 : -1; }
+
+gsr_status kv_block_tables(const int32_t* kv_lens, const int32_t* new_lens, const int32_t* free_blocks,
+                           const int32_t* free_head, int32_t* block_tables, int32_t* kv_lens_out,
+                           int32_t* free_head_out, int32_t* q_starts, int32_t* positions, int32_t* slots,
+                           int32_t* counts, int64_t batch, int64_t table_width, int64_t page_size, int64_t num_free,
+                           int64_t max_tokens, CUstream_st* stream) {
+    for (int64_t n : {batch, table_width, page_size, num_free, max_tokens})
+        if (bad_size(n)) return GSR_ERR_INVALID_ARG;
+    if (page_size == 0 || batch > gsr::kTablesMaxBatch) return GSR_ERR_INVALID_ARG;
+    if (!free_head || !free_head_out || !q_starts || !counts || (num_free > 0 && !free_blocks) ||
+        (max_tokens > 0 && (!positions || !slots)) || (batch > 0 && (!kv_lens || !new_lens || !kv_lens_out)) ||
+        (batch > 0 && table_width > 0 && !block_tables))
+        return GSR_ERR_INVALID_ARG;
+    struct Part {
+        const void* p;
+        int64_t n;
+    };
+    const Part in[] = {{kv_lens, batch}, {new_lens, batch}, {free_blocks, num_free}, {free_head, 1}};
+    const Part out[] = {{block_tables, batch * table_width}, {kv_lens_out, batch}, {free_head_out, 1},
+                        {q_starts, batch + 1}, {positions, max_tokens}, {slots, max_tokens}, {counts, 3}};
+    auto span = [](const Part& a) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(a.p);
+        return Span{lo, a.p ? lo + (uintptr_t)a.n * 4 : lo};
+    };
+    for (const Part& a : in)
+        if (misaligned(a.p, 4)) return GSR_ERR_ALIGNMENT;
+    for (const Part& a : out)
+        if (misaligned(a.p, 4)) return GSR_ERR_ALIGNMENT;
+    for (const Part& a : out) {
+        for (const Part& b : in)
+            if (meet(span(a), span(b))) return GSR_ERR_ALIAS;
+        for (const Part& b : out)
+            if (&a != &b && meet(span(a), span(b))) return GSR_ERR_ALIAS;
+    }
+    int dev = 0, sms = 0;
+    gsr_status s = gsr::host::current_device(&dev, &sms);
+    if (s != GSR_OK) return s;
+    const gsr::TablesParams p{(int)batch, (int)page_size, (int)table_width, (int)num_free, (int)max_tokens,
+                              kv_lens, new_lens, free_blocks, free_head, block_tables, kv_lens_out, free_head_out,
+                              q_starts, positions, slots, counts};
+    const cudaError_t e = gsr::launch_block_tables(p, sms, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GSR_OK : gsr::host::fail(e);
+}
+
+gsr_status kv_cache_append(const gsr_tensor* K, const gsr_tensor* V, const int32_t* slots, const gsr_tensor* k_cache,
+                           const gsr_tensor* v_cache, int64_t tokens, int64_t heads, int64_t head_dim,
+                           int64_t num_pages, int64_t page_size, CUstream_st* stream) {
+    for (int64_t n : {tokens, heads, head_dim, num_pages, page_size})
+        if (bad_size(n)) return GSR_ERR_INVALID_ARG;
+    if (page_size == 0 || num_pages * page_size > ((int64_t)1 << 31)) return GSR_ERR_INVALID_ARG;
+    if (head_dim % 8) return GSR_ERR_ALIGNMENT;
+    if (heads * head_dim > ((int64_t)1 << 20)) return GSR_ERR_INVALID_ARG;
+    if (tokens == 0 || heads == 0 || head_dim == 0) return GSR_OK;
+    gsr::AppendParams p;
+    gsr_status s;
+    if ((s = operand(K, 1, heads, tokens, head_dim, false, &p.K)) != GSR_OK ||
+        (s = operand(V, 1, heads, tokens, head_dim, false, &p.V)) != GSR_OK ||
+        (s = operand(k_cache, num_pages, heads, page_size, head_dim, true, &p.Kc)) != GSR_OK ||
+        (s = operand(v_cache, num_pages, heads, page_size, head_dim, true, &p.Vc)) != GSR_OK)
+        return s;
+    if (!slots) return GSR_ERR_INVALID_ARG;
+    if (misaligned(slots, 4)) return GSR_ERR_ALIGNMENT;
+    const Span kc = span_of(p.Kc, num_pages, heads, page_size, head_dim, 2),
+               vc = span_of(p.Vc, num_pages, heads, page_size, head_dim, 2);
+    const uintptr_t s0 = reinterpret_cast<uintptr_t>(slots);
+    const Span others[] = {span_of(p.K, 1, heads, tokens, head_dim, 2), span_of(p.V, 1, heads, tokens, head_dim, 2),
+                           Span{s0, s0 + (uintptr_t)tokens * 4}};
+    for (const Span& o : others)
+        if (meet(kc, o) || meet(vc, o)) return GSR_ERR_ALIAS;
+    if (num_pages > 0 && p.Kc.data == p.Vc.data) return GSR_ERR_ALIAS;
+    int dev = 0, sms = 0;
+    if ((s = gsr::host::current_device(&dev, &sms)) != GSR_OK) return s;
+    p.N = (int)tokens;
+    p.H = (int)heads;
+    p.D = (int)head_dim;
+    p.page = (int)page_size;
+    p.num_pages = (int)num_pages;
+    p.slots = slots;
+    const cudaError_t e = gsr::launch_cache_append(p, sms, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GSR_OK : gsr::host::fail(e);
+}
+
+}  // extern "C"

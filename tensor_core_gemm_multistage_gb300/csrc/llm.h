@@ -1,0 +1,113 @@
+// llm.h - internal interface between the C-ABI layer (gsr_llm_api.cu) and the kernels of masked
+// attention, tree attention over a paged cache, and the cache's bookkeeping.  Not installed; not
+// part of the ABI.
+#pragma once
+
+#include "kernels.h"
+
+namespace gsr {
+
+// Which kernel an error word comes from, beside those of kernels.h.
+enum LlmDeviceError : int {
+    kDevErrKernelMaskedFwd = 0x400,
+    kDevErrKernelMaskedDkv = 0x500,
+    kDevErrKernelMaskedDq = 0x600,
+    kDevErrKernelTree = 0x700,
+};
+
+// A (batch, head, row, D) operand: element strides, D contiguous.
+struct Strided {
+    void* data;
+    long long batch, head, row;
+};
+
+// Which keys a query sees, and how a raw product becomes a score.  Query i of a batch row stands
+// at position p = i + offset among the keys and sees one interval [lo, hi) of them (row_interval
+// in attention_common.cuh).
+struct MaskArgs {
+    int B, Hq, Hkv, group;      // group = Hq / Hkv
+    int Sq, Skv, offset;        // offset = Skv - Sq
+    int causal;
+    int num_docs;               // 0: no document mask
+    const int* doc_bounds;      // (B, num_docs + 1)
+    const int* prefix_lens;     // (B, max(num_docs, 1)) or null
+};
+
+// Scores in log2 units: y = score * log2(e).
+struct ScoreArgs {
+    float scale;                // softmax scale
+    float sl2;                  // scale * log2(e): y = sl2 * (q.k) without a cap
+    float cap_in;               // 2 log2(e) scale / cap: tanh's exponent, 0 without a cap
+    float cap_out;              // cap * log2(e)
+    const float* slopes;        // per query head, or null
+};
+
+struct MaskedFwdParams {
+    MaskArgs mask;
+    ScoreArgs score;
+    Strided Q, K, V, O;
+    float* lse;                 // (B, Hq, Sq) or null
+    int head_group;             // item order, as in AttnParams
+    int num_items;
+    int* err;
+    uint64_t timeout_ns;
+    uint32_t test_flags;
+};
+
+// Rows of the backward pass's workspace are padded to whole 128-row tiles.
+struct MaskedBwdParams {
+    MaskArgs mask;
+    ScoreArgs score;
+    Strided dO, Q, K, V, O, dQ, dK, dV;
+    const float* lse;           // (B, Hq, Sq)
+    int Sp;                     // Sq rounded up to a multiple of 128
+    float* lse2;                // (B, Hq, Sp): lse log2(e); +inf for rows without keys and padding
+    float* delta;               // (B, Hq, Sp): rowsum(dO * O)
+    int* lo;                    // (B, Sp): each query's interval
+    int* hi;
+    unsigned* norms;            // [0] max |dO_i|^2, [1] max |V_j|^2, as the bits of a float
+    int* err;
+    uint64_t timeout_ns;
+    uint32_t test_flags;
+};
+
+struct TreeParams {
+    int B, Hq, Hkv, group, D;
+    int page, num_pages, table_width, max_nodes, total_q;
+    ScoreArgs score;
+    const void* Q;              // (total_q, Hq, D), element strides q_row, q_head
+    long long q_row, q_head;
+    void* O;
+    long long o_row, o_head;
+    Strided K, V;               // cache: batch = page stride, row = stride of a page's rows
+    const int* table;           // (B, table_width)
+    const int* kv_lens;         // (B): cached tokens, the drafted ones among them
+    const int* q_starts;        // (B + 1)
+    const int* parents;         // (total_q) or null: a chain
+    void* workspace;
+    int* err;
+    uint64_t timeout_ns;
+    uint32_t test_flags;
+};
+
+cudaError_t launch_masked_fwd(const MaskedFwdParams& p, int D, bool bf16, cudaStream_t stream);
+cudaError_t launch_masked_bwd(const MaskedBwdParams& p, int D, bool bf16, cudaStream_t stream);
+cudaError_t launch_tree(const TreeParams& p, bool bf16, cudaStream_t stream);
+
+struct TablesParams {
+    int B, page, table_width, num_free, max_tokens;
+    const int *kv_lens, *new_lens, *free_blocks, *free_head;
+    int *table, *kv_out, *head_out, *q_starts, *positions, *slots, *counts;
+};
+constexpr int kTablesMaxBatch = 8192;
+cudaError_t launch_block_tables(const TablesParams& p, int sms, cudaStream_t stream);
+
+struct AppendParams {
+    int N, H, D, page, num_pages;
+    Strided K, V;               // new rows: row = token stride; batch unused
+    Strided Kc, Vc;             // cache: batch = page stride
+    const int* slots;
+};
+cudaError_t launch_cache_append(const AppendParams& p, int sms, cudaStream_t stream);
+
+}  // namespace gsr

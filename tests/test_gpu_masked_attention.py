@@ -1,0 +1,308 @@
+"""GPU parity of masked_attention_fwd and _bwd against the fp64 oracle.
+
+Tolerances, from the arithmetic: with u = eps / 2 of the operands' type, a probability (or dS) is
+rounded once to that type before the matrix product, and the result once at the end, so per element
+    |got - want| <= u sum|terms| + u |want| + small,
+where the sum runs over the rounded factor's terms.  `small` covers fp32: a score is a sum of D
+products in fp32 (D 2^-24 relative to sum|q k| at worst, scores here below 2^5 in absolute terms)
+and a probability's relative error equals its score's absolute one: 2^-13 of the sum of |terms| is
+above all of it, as is 2^-13 of the terms of dS's own two parts.  In float16 a result below 2^-14
+is subnormal: its rounding is 2^-25 absolute.  lse is fp32 throughout: 2^-14 absolute for scores
+below 2^5 and distance biases below 2^9 (2^-24 relative, a few roundings).
+"""
+import numpy as np
+import pytest
+import torch
+
+import tensor_core_gemm_multistage_gb300 as gsr
+from oracle import llm
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    gsr.build()
+    yield
+
+
+def make(B, H, n, D, dtype, g, order="bhsd", scale=1.0):
+    x = (torch.randn(B, H, n, D, generator=g) * scale).to(dtype).to(DEV)
+    if order == "bshd":
+        return x.transpose(1, 2).contiguous().transpose(1, 2)
+    if order == "hbsd":
+        return x.transpose(0, 1).contiguous().transpose(0, 1)
+    return x
+
+
+class Case:
+    def __init__(self, B, Hq, Hkv, Sq, Skv, D, dtype=F16, causal=False, docs=None, prefix=None, cap=0.0, alibi=False,
+                 scale=0.0, order="bhsd", seed=0, grad=1.0):
+        g = torch.Generator().manual_seed(seed * 1000 + Sq + 7 * Skv + D)
+        self.q, self.k, self.v = (make(B, h, n, D, dtype, g, order, s) for h, n, s in
+                                  ((Hq, Sq, 1.5), (Hkv, Skv, 1.0), (Hkv, Skv, 1.0)))
+        self.do = make(B, Hq, Sq, D, dtype, g, order, grad)
+        self.docs, self.prefix, self.causal, self.cap, self.scale = docs, prefix, causal, cap, scale
+        self.slopes = (2.0 ** -torch.linspace(1, 8, Hq)).to(DEV) if alibi else None
+        self.see = llm.visible(B, Sq, Skv, causal, docs, prefix)
+        self.kw = dict(softmax_scale=scale, causal=causal, softcap=cap, alibi_slopes=self.slopes,
+                       doc_bounds=None if docs is None else torch.tensor(docs, dtype=torch.int32, device=DEV),
+                       prefix_lens=None if prefix is None else torch.tensor(prefix, dtype=torch.int32, device=DEV))
+        self.u = torch.finfo(dtype).eps / 2
+        self.tiny = 2.0 ** -25 if dtype == F16 else 0.0
+        self.host = dict(scale=float(np.float32(scale)), cap=float(np.float32(cap)),
+                         slopes=None if self.slopes is None else self.slopes.cpu().numpy())
+
+    def forward(self):
+        self.o = torch.full_like(self.q, float("nan"))
+        self.lse = torch.full(self.q.shape[:3], float("nan"), device=DEV)
+        gsr.masked_attention_fwd(self.q, self.k, self.v, self.o, self.lse, **self.kw)
+        status, code = gsr.device_status()
+        assert status == gsr.Status.OK, hex(code)
+        return self
+
+    def backward(self):
+        self.grads = [torch.full_like(t, float("nan")) for t in (self.q, self.k, self.v)]
+        gsr.masked_attention_bwd(self.do, self.q, self.k, self.v, self.o, self.lse, *self.grads, **self.kw)
+        status, code = gsr.device_status()
+        assert status == gsr.Status.OK, hex(code)
+        return self
+
+    def check_forward(self):
+        want, lse, terms = llm.masked_attention(self.q, self.k, self.v, self.see, **self.host)
+        got = llm.f64(self.o)
+        assert not np.isnan(got).any(), "unwritten or NaN outputs"
+        assert np.all(np.abs(got - want) <= self.u * (terms + np.abs(want)) + 2.0 ** -13 * terms + self.tiny), \
+            np.abs(got - want).max()
+        gl = llm.f64(self.lse)
+        fin = np.isfinite(lse)
+        assert np.array_equal(np.isneginf(gl), ~fin) and not np.isnan(gl).any()
+        assert np.all(np.abs(gl[fin] - lse[fin]) <= 2.0 ** -14), np.abs(gl[fin] - lse[fin]).max()
+        return self
+
+    def check_backward(self):
+        want, terms, wide = llm.masked_attention_bwd(self.do, self.q, self.k, self.v, self.o, self.lse, self.see, **self.host)
+        for name, t, w, a, b in zip(("dQ", "dK", "dV"), self.grads, want, terms, wide):
+            got = llm.f64(t)
+            assert not np.isnan(got).any(), name
+            tol = self.u * (a + np.abs(w)) + 2.0 ** -13 * b + self.tiny
+            assert np.all(np.abs(got - w) <= tol), (name, np.abs(got - w).max(), (np.abs(got - w) / tol).max())
+        return self
+
+    def check(self):
+        return self.forward().check_forward().backward().check_backward()
+
+
+CASES = {
+    "one_key": dict(B=1, Hq=1, Hkv=1, Sq=1, Skv=1, D=64),
+    "one_query": dict(B=2, Hq=8, Hkv=2, Sq=1, Skv=515, D=128, causal=True, dtype=BF16),
+    "tile": dict(B=1, Hq=2, Hkv=2, Sq=128, Skv=128, D=128),
+    "full_odd": dict(B=2, Hq=3, Hkv=1, Sq=333, Skv=200, D=64, order="bshd"),
+    "causal_odd": dict(B=1, Hq=4, Hkv=2, Sq=385, Skv=385, D=128, causal=True, dtype=BF16),
+    "causal_more_keys": dict(B=1, Hq=2, Hkv=1, Sq=100, Skv=333, D=64, causal=True, order="hbsd"),
+    "causal_more_queries": dict(B=1, Hq=2, Hkv=2, Sq=400, Skv=130, D=128, causal=True),
+    "docs": dict(B=2, Hq=4, Hkv=2, Sq=500, Skv=500, D=64, docs=[[0, 3, 200, 200, 500], [0, 100, 257, 300, 411]], causal=True),
+    "docs_two_way": dict(B=1, Hq=2, Hkv=1, Sq=700, Skv=700, D=128, docs=[[0, 127, 128, 129, 390, 700]], dtype=BF16),
+    "docs_padding_in_front": dict(B=1, Hq=2, Hkv=1, Sq=300, Skv=300, D=64, docs=[[140, 150, 290]]),
+    "docs_none_left": dict(B=2, Hq=2, Hkv=1, Sq=150, Skv=150, D=64, docs=[[0, 0, 0], [0, 0, 150]]),
+    "padded_batch": dict(B=4, Hq=2, Hkv=2, Sq=260, Skv=260, D=128, docs=[[0, 260], [0, 1], [0, 129], [0, 0]], dtype=BF16),
+    "prefix": dict(B=3, Hq=4, Hkv=4, Sq=270, Skv=270, D=64, causal=True, prefix=[0, 131, 400]),
+    "prefix_more_queries": dict(B=1, Hq=1, Hkv=1, Sq=300, Skv=140, D=64, causal=True, prefix=[37]),
+    "prefix_docs": dict(B=1, Hq=4, Hkv=1, Sq=520, Skv=520, D=128, causal=True, docs=[[0, 130, 400, 515]], prefix=[[20, 200, 500]]),
+    "cap": dict(B=1, Hq=4, Hkv=2, Sq=300, Skv=300, D=128, cap=2.0, causal=True),
+    "cap_saturated": dict(B=1, Hq=2, Hkv=2, Sq=200, Skv=200, D=64, cap=0.5, scale=2.0, dtype=BF16),
+    "alibi": dict(B=1, Hq=8, Hkv=2, Sq=400, Skv=400, D=64, alibi=True, causal=True, dtype=BF16),
+    "alibi_two_way": dict(B=1, Hq=4, Hkv=4, Sq=200, Skv=330, D=128, alibi=True),
+    "all": dict(B=2, Hq=6, Hkv=2, Sq=390, Skv=390, D=128, cap=3.0, alibi=True, causal=True, order="bshd", dtype=BF16,
+                docs=[[0, 200, 380], [5, 6, 390]], prefix=[[50, 10], [1, 300]]),
+    "negative_scale": dict(B=1, Hq=2, Hkv=1, Sq=200, Skv=200, D=64, scale=-0.2, causal=True),
+    "peaked": dict(B=1, Hq=2, Hkv=2, Sq=257, Skv=257, D=64, scale=0.4),
+    "many_items": dict(B=2, Hq=48, Hkv=24, Sq=520, Skv=520, D=64, causal=True),
+    "small_gradients": dict(B=1, Hq=2, Hkv=1, Sq=600, Skv=600, D=128, grad=2.0 ** -11),
+    "large_gradients": dict(B=1, Hq=2, Hkv=1, Sq=300, Skv=300, D=64, grad=2.0 ** 7, causal=True),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_parity(name):
+    Case(**CASES[name]).check()
+
+
+def _random_cases(n, seed):
+    r = np.random.default_rng(seed)
+    out = []
+    for _ in range(n):
+        B, Hkv, g = int(r.integers(1, 3)), int(r.integers(1, 4)), int(r.choice([1, 2, 5]))
+        S = int(r.integers(1, 600))
+        c = dict(B=B, Hq=Hkv * g, Hkv=Hkv, Sq=S, Skv=S, D=int(r.choice([64, 128])), seed=int(r.integers(1000)),
+                 dtype=[F16, BF16][int(r.integers(2))], order=str(r.choice(["bhsd", "bshd", "hbsd"])),
+                 cap=float(r.choice([0.0, 0.0, 4.0])), alibi=bool(r.integers(2)))
+        kind = r.integers(4)
+        if kind == 0:
+            c["Skv"], c["causal"] = int(r.integers(1, 700)), bool(r.integers(2))
+        elif kind == 1:
+            c["causal"], c["prefix"] = True, [int(x) for x in r.integers(0, S + 2, B)]
+        else:
+            n_docs = int(r.integers(1, 6))
+            c["docs"] = [sorted(int(x) for x in r.integers(0, S + 1, n_docs + 1)) for _ in range(B)]
+            c["causal"] = bool(r.integers(2))
+            if c["causal"] and kind == 3:
+                c["prefix"] = [[int(x) for x in r.integers(0, S, n_docs)] for _ in range(B)]
+        out.append(c)
+    return out
+
+
+@pytest.mark.parametrize("c", _random_cases(14, 77))
+def test_random_cases(c):
+    Case(**c).check()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("D", [64, 128])
+def test_masked_positions_have_no_influence(bad, D):
+    # padding, and a whole document: whatever they hold, the others' results are what they were
+    docs = [[0, 70, 200, 290]]
+    c = Case(1, 4, 2, 300, 300, D, docs=docs, causal=True)
+    for rows in (slice(290, 300), slice(70, 200)):
+        for t in (c.q, c.k, c.v, c.do):
+            t[:, :, rows] = bad
+    c.forward().backward()
+    keep = torch.ones(300, dtype=torch.bool)
+    keep[70:200] = False
+    clean = Case(1, 4, 2, 300, 300, D, docs=docs, causal=True).forward().check_forward().backward().check_backward()
+    tol = lambda x: 2 * c.u * x.float().abs() + 1e-3
+    for got, want in ((c.o, clean.o), *zip(c.grads, clean.grads)):
+        a, b = got[:, :, keep].float(), want[:, :, keep].float()
+        assert torch.isfinite(a).all() and torch.all((a - b).abs() <= tol(b))
+    assert torch.all(c.o[:, :, 290:] == 0) and torch.all(c.lse[:, :, 290:] == -float("inf"))
+    assert all(torch.all(t[:, :, 290:] == 0) for t in c.grads)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_later_keys_have_no_influence(D):
+    # causal: a NaN from position 200 on reaches no earlier query, inside the same tile either
+    c = Case(1, 2, 1, 260, 260, D, causal=True)
+    clean = Case(1, 2, 1, 260, 260, D, causal=True).forward()
+    for t in (c.k, c.v):
+        t[:, :, 200:] = float("nan")
+    c.forward()
+    assert torch.equal(c.lse[:, :, :200], clean.lse[:, :, :200])
+    a, b = c.o[:, :, :200].float(), clean.o[:, :, :200].float()
+    assert torch.all((a - b).abs() <= 2 * c.u * b.abs() + 1e-3)
+    assert torch.isnan(c.o[:, :, 200:]).all()
+
+
+def test_padding_rows_of_the_gradient():
+    # rows without keys may hold anything in dO and in the given O
+    c = Case(2, 4, 2, 200, 200, 64, docs=[[0, 150], [0, 200]])
+    c.forward()
+    c.do[0, :, 150:] = float("nan")
+    c.o[0, :, 150:] = float("inf")
+    c.backward()
+    c.o[0, :, 150:] = 0
+    c.do[0, :, 150:] = 0
+    c.check_backward()
+
+
+def test_fused_projection_views():
+    # Q, K, V and their gradients as the parts of one buffer; O in (batch, row, head) order
+    B, S, Hq, Hkv, D = 2, 150, 4, 2, 64
+    g = torch.Generator().manual_seed(9)
+    qkv = torch.randn(B, S, Hq + 2 * Hkv, D, generator=g).to(F16).to(DEV)
+    dqkv = torch.full_like(qkv, float("nan"))
+    part = lambda t: [x.transpose(1, 2) for x in t.split([Hq, Hkv, Hkv], 2)]
+    c = Case(B, Hq, Hkv, S, S, D, causal=True)
+    (c.q, c.k, c.v), grads = part(qkv), part(dqkv)
+    c.do = torch.randn(B, S, Hq, D, generator=g).to(F16).to(DEV).transpose(1, 2)
+    c.o, c.lse = torch.empty_like(c.do), torch.empty(B, Hq, S, device=DEV)
+    gsr.masked_attention_fwd(c.q, c.k, c.v, c.o, c.lse, **c.kw)
+    gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *grads, **c.kw)
+    c.grads = grads
+    c.check_forward().check_backward()
+    with pytest.raises(gsr.GsrError) as e:      # in place of an input
+        gsr.masked_attention_fwd(c.q, c.k, c.v, c.q, c.lse, **c.kw)
+    assert e.value.status == gsr.Status.ERR_ALIAS
+
+
+def test_rows_behind_the_output_view_are_left():
+    # O is a view of a wider buffer: what lies between its rows stays
+    buf = torch.full((1, 100, 3, 64), 7.0, dtype=F16, device=DEV)
+    c = Case(1, 2, 1, 100, 100, 64)
+    c.o, c.lse = buf[:, :, :2].transpose(1, 2), torch.empty(1, 2, 100, device=DEV)
+    gsr.masked_attention_fwd(c.q, c.k, c.v, c.o, c.lse, **c.kw)
+    c.check_forward()
+    assert torch.all(buf[:, :, 2] == 7.0)
+
+
+def test_no_keys_and_no_queries():
+    q = torch.randn(1, 2, 5, 64, device=DEV, dtype=F16)
+    none = torch.empty(1, 1, 0, 64, device=DEV, dtype=F16)
+    o, lse = torch.full_like(q, float("nan")), torch.zeros(1, 2, 5, device=DEV)
+    gsr.masked_attention_fwd(q, none, none, o, lse)
+    assert torch.all(o == 0) and torch.all(lse == -float("inf"))
+    dq = torch.full_like(q, float("nan"))
+    gsr.masked_attention_bwd(q, q, none, none, o, lse, dq, none.clone(), none.clone())
+    assert torch.all(dq == 0)
+    k = torch.randn(1, 1, 9, 64, device=DEV, dtype=F16)
+    noq = torch.empty(1, 2, 0, 64, device=DEV, dtype=F16)
+    dk, dv = torch.full_like(k, float("nan")), torch.full_like(k, float("nan"))
+    gsr.masked_attention_bwd(noq, noq, k, k, noq, torch.empty(1, 2, 0, device=DEV), noq.clone(), dk, dv)
+    assert torch.all(dk == 0) and torch.all(dv == 0)
+    gsr.masked_attention_fwd(noq, k, k, noq.clone())
+
+
+def test_one_query_equals_the_last_row():
+    c = Case(2, 4, 2, 300, 300, 64, causal=True, cap=3.0, alibi=True).forward()
+    o1, l1 = torch.empty_like(c.q[:, :, -1:]).contiguous(), torch.empty(2, 4, 1, device=DEV)
+    gsr.masked_attention_fwd(c.q[:, :, -1:], c.k, c.v, o1, l1, **c.kw)
+    assert torch.all((o1.float() - c.o[:, :, -1:].float()).abs() <= 4 * c.u * c.o[:, :, -1:].float().abs() + 1e-3)
+    assert torch.all((l1 - c.lse[:, :, -1:]).abs() <= 2.0 ** -13)
+
+
+def test_repeatable_and_on_two_streams_at_once():
+    cases = [Case(2, 8, 2, 700, 700, 128, causal=True, seed=1), Case(1, 6, 3, 555, 555, 64, dtype=BF16, cap=5.0, seed=2)]
+    for c in cases:
+        c.forward().backward()
+    first = [[t.clone() for t in (c.o, c.lse, *c.grads)] for c in cases]
+    streams = [torch.cuda.Stream(DEV), torch.cuda.Stream(DEV)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for c, s in zip(cases, streams):
+            gsr.masked_attention_fwd(c.q, c.k, c.v, c.o, c.lse, stream=s, **c.kw)
+            gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *c.grads, stream=s, **c.kw)
+    for s in streams:
+        assert gsr.device_status(s)[0] == gsr.Status.OK
+    for c, want in zip(cases, first):
+        for a, b in zip((c.o, c.lse, *c.grads), want):
+            assert torch.equal(a, b)
+
+
+def test_two_captured_graphs_replayed_at_once():
+    cases = [Case(1, 8, 2, 512, 512, 128, causal=True, seed=3), Case(1, 4, 4, 640, 640, 128, docs=[[0, 300, 640]], seed=4)]
+    graphs, first = [], []
+    side = torch.cuda.Stream(DEV)
+    for c in cases:
+        c.forward().backward()
+        first.append([t.clone() for t in (c.o, *c.grads)])
+        with torch.cuda.stream(side):
+            gsr.masked_attention_fwd(c.q, c.k, c.v, c.o, c.lse, **c.kw)    # the stream's error word
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            gsr.masked_attention_fwd(c.q, c.k, c.v, c.o, c.lse, **c.kw)
+            gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *c.grads, **c.kw)
+        graphs.append(graph)
+    for c in cases:
+        for t in (c.o, c.lse, *c.grads):
+            t.fill_(float("nan"))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(DEV), torch.cuda.Stream(DEV)]
+    for graph, s in zip(graphs, streams):
+        with torch.cuda.stream(s):
+            for _ in range(3):
+                graph.replay()
+    torch.cuda.synchronize()
+    for c, want in zip(cases, first):
+        assert all(torch.equal(a, b) for a, b in zip((c.o, *c.grads), want))

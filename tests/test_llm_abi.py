@@ -1,0 +1,168 @@
+"""Refusals of masked attention, tree attention, block tables and cache writes, without a GPU: the
+device addresses are fake, and every call is refused before any CUDA call."""
+import ctypes
+
+import pytest
+
+import tensor_core_gemm_multistage_gb300 as gsr
+from tensor_core_gemm_multistage_gb300 import llm
+from tensor_core_gemm_multistage_gb300.llm import _AttentionDesc, _Tensor, _TreeDesc
+
+INVALID, ALIGN, ALIAS, OK = (gsr.Status.ERR_INVALID_ARG, gsr.Status.ERR_ALIGNMENT, gsr.Status.ERR_ALIAS, gsr.Status.OK)
+GB = 1 << 30
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    gsr.build()
+    yield
+
+
+def dense(addr, B, H, S, D):
+    return _Tensor(addr, H * S * D, S * D, D)
+
+
+def fwd(desc=None, lse=None, **t):
+    d = dict(batch=2, heads_q=4, heads_kv=2, seq_q=100, seq_kv=100, head_dim=64, dtype=0, causal=1)
+    d.update(desc or {})
+    ops = dict(Q=dense(1 * GB, 2, 4, 100, 64), K=dense(2 * GB, 2, 2, 100, 64), V=dense(3 * GB, 2, 2, 100, 64),
+               O=dense(4 * GB, 2, 4, 100, 64))
+    ops.update(t)
+    return gsr.lib().masked_attention_fwd(_AttentionDesc(**d), ops["Q"], ops["K"], ops["V"], ops["O"], lse, None)
+
+
+def bwd(desc=None, lse=9 * GB, ws=10 * GB, ws_bytes=1 << 20, **t):
+    d = dict(batch=2, heads_q=4, heads_kv=2, seq_q=100, seq_kv=100, head_dim=64, dtype=0, causal=1)
+    d.update(desc or {})
+    ops = {n: dense((i + 1) * GB, 2, 4 if n in ("dO", "Q", "O", "dQ") else 2, 100, 64)
+           for i, n in enumerate(("dO", "Q", "K", "V", "O", "dQ", "dK", "dV"))}
+    ops.update(t)
+    o = ops
+    return gsr.lib().masked_attention_bwd(_AttentionDesc(**d), o["dO"], o["Q"], o["K"], o["V"], o["O"], lse, o["dQ"],
+                                          o["dK"], o["dV"], ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("desc", [
+    dict(batch=-1), dict(seq_q=2 ** 31), dict(head_dim=96), dict(dtype=2), dict(heads_kv=3), dict(heads_kv=0),
+    dict(softcap=-1.0), dict(softcap=float("nan")), dict(softmax_scale=float("inf")),
+    dict(doc_bounds=16 * GB, num_docs=0), dict(num_docs=2), dict(doc_bounds=16 * GB, num_docs=2, seq_q=99),
+    dict(prefix_lens=16 * GB, causal=0), dict(batch=2 ** 20, heads_q=2 ** 12)])
+def test_attention_descriptions(desc):
+    assert fwd(desc) == INVALID and bwd(desc) == INVALID
+    d = dict(batch=2, heads_q=4, heads_kv=2, seq_q=100, seq_kv=100, head_dim=64, dtype=0, causal=1)
+    d.update(desc)
+    assert gsr.lib().masked_attention_bwd_workspace(_AttentionDesc(**d)) == -1
+
+
+def test_attention_pointers_strides_and_alignment():
+    assert fwd(Q=_Tensor(None, 25600, 6400, 64)) == INVALID
+    assert fwd(K=_Tensor(2 * GB + 8, 12800, 6400, 64)) == ALIGN
+    assert fwd(V=_Tensor(3 * GB, 12800, 6404, 64)) == ALIGN
+    assert fwd(Q=_Tensor(1 * GB, 0, 6400, 64)) == INVALID              # a broadcast
+    assert fwd(Q=_Tensor(1 * GB, 25600, 6400, -64)) == INVALID
+    assert fwd(O=_Tensor(4 * GB, 25600, 6400, 32)) == INVALID          # rows of O on top of each other
+    assert fwd(Q=_Tensor(1 * GB, 1 << 45, 6400, 64)) == INVALID
+    assert fwd(lse=9 * GB + 2) == ALIGN
+    assert fwd(dict(alibi_slopes=9 * GB + 2)) == ALIGN
+    assert gsr.lib().masked_attention_fwd(None, None, None, None, None, None, None) == INVALID
+    assert bwd(lse=None) == INVALID
+    assert bwd(ws=None) == INVALID
+    assert bwd(ws_bytes=llm.masked_attention_bwd_workspace(2, 4, 2, 100, 100, 64) - 1) == INVALID
+    assert bwd(ws=10 * GB + 8) == ALIGN
+
+
+def test_attention_aliases():
+    assert fwd(O=dense(1 * GB, 2, 4, 100, 64)) == ALIAS
+    assert fwd(O=dense(2 * GB - 64, 2, 4, 100, 64)) == ALIAS
+    assert fwd(lse=4 * GB + 16) == ALIAS
+    assert bwd(dQ=dense(2 * GB, 2, 4, 100, 64)) == ALIAS
+    assert bwd(dV=dense(7 * GB, 2, 2, 100, 64)) == ALIAS               # dK and dV in one place
+    assert bwd(ws=3 * GB) == ALIAS
+    assert bwd(lse=10 * GB) == ALIAS
+    assert bwd(lse=6 * GB) == ALIAS
+    # the parts of one fused buffer lie side by side unless they overlap in its rows
+    part = lambda base, col: _Tensor(base + 2 * 64 * col, 100 * 8 * 64, 64, 8 * 64)
+    assert bwd(dQ=part(20 * GB, 0), dK=part(20 * GB, 3), dV=part(20 * GB, 6)) == ALIAS
+    assert fwd(Q=part(20 * GB, 0), K=part(20 * GB, 4), V=part(20 * GB, 6), O=part(20 * GB, 2)) == ALIAS
+
+
+def test_empty_attention_is_a_no_op():
+    assert fwd(dict(batch=0)) == OK and fwd(dict(seq_q=0)) == OK
+    assert bwd(dict(batch=0)) == OK
+    assert fwd(dict(seq_q=0), Q=_Tensor(), O=_Tensor()) == OK
+
+
+def tree(desc=None, q=1 * GB, k=None, v=None, table=5 * GB, lens=6 * GB, starts=7 * GB, parents=8 * GB, o=4 * GB,
+         ws=10 * GB, ws_bytes=1 << 34):
+    d = dict(batch=2, total_q=6, heads_q=4, heads_kv=2, head_dim=64, num_pages=10, page_size=16, table_width=5,
+             max_nodes=3, q_stride_row=256, q_stride_head=64, o_stride_row=256, o_stride_head=64)
+    d.update(desc or {})
+    cache = lambda addr: _Tensor(addr, 16 * 2 * 64, 64, 2 * 64)
+    return gsr.lib().tree_attention_fwd(_TreeDesc(**d), q, k or cache(2 * GB), v or cache(3 * GB), table, lens, starts,
+                                        parents, o, ws, ws_bytes, None)
+
+
+def test_tree_refusals():
+    for bad in (dict(batch=-1), dict(head_dim=32), dict(dtype=3), dict(max_nodes=0), dict(max_nodes=65), dict(heads_kv=3),
+                dict(heads_kv=0), dict(softcap=-2.0), dict(page_size=12), dict(page_size=0), dict(page_size=4),
+                dict(table_width=2 ** 30), dict(total_q=2 ** 31), dict(q_stride_row=0), dict(o_stride_row=32),
+                dict(heads_q=258, heads_kv=2)):
+        assert tree(bad) == INVALID, bad
+    assert tree(q=None) == INVALID and tree(lens=None) == INVALID and tree(starts=None) == INVALID
+    assert tree(table=None) == INVALID and tree(o=None) == INVALID
+    assert tree(q=GB + 8) == ALIGN and tree(parents=8 * GB + 1) == ALIGN and tree(ws=10 * GB + 4) == ALIGN
+    assert tree(dict(q_stride_head=68)) == ALIGN
+    assert tree(k=_Tensor(None, 2048, 64, 128)) == INVALID
+    assert tree(o=1 * GB) == ALIAS and tree(o=2 * GB + 128) == ALIAS
+    assert tree(dict(batch=0)) == OK and tree(dict(total_q=0)) == OK
+    assert gsr.lib().tree_attention_workspace(None) == -1
+
+
+def tables(B=4, W=5, page=16, free=10, tokens=9, over=None):
+    at = [(i + 1) * GB for i in range(11)]
+    for i, a in (over or {}).items():
+        at[i] = a
+    return gsr.lib().kv_block_tables(*at, B, W, page, free, tokens, None)
+
+
+def test_block_table_refusals():
+    assert tables(B=-1) == INVALID and tables(page=0) == INVALID and tables(B=8193) == INVALID
+    assert tables(tokens=2 ** 31) == INVALID
+    for i in range(11):
+        assert tables(over={i: None}) == INVALID, i
+        assert tables(over={i: (i + 1) * GB + 2}) == ALIGN, i
+    assert tables(over={5: 1 * GB}) == ALIAS          # kv_lens_out in place of kv_lens
+    assert tables(over={6: 4 * GB}) == ALIAS          # free_head_out in place of free_head
+    assert tables(over={9: 9 * GB}) == ALIAS          # slots in place of positions
+
+
+def append(tokens=9, H=2, D=64, pages=10, page=16, slots=5 * GB, k=None, kc=None, vc=None):
+    c = lambda a: _Tensor(a, page * H * D, D, H * D)
+    return gsr.lib().kv_cache_append(k or _Tensor(1 * GB, 0, D, 3 * H * D), _Tensor(2 * GB, 0, D, 3 * H * D), slots,
+                                     kc or c(3 * GB), vc or c(4 * GB), tokens, H, D, pages, page, None)
+
+
+def test_append_refusals():
+    assert append(tokens=-1) == INVALID and append(page=0) == INVALID and append(slots=None) == INVALID
+    assert append(D=60) == ALIGN and append(slots=5 * GB + 2) == ALIGN
+    assert append(pages=2 ** 28) == INVALID and append(H=2 ** 15) == INVALID
+    assert append(k=_Tensor(GB + 2, 0, 64, 128)) == ALIGN and append(k=_Tensor(GB, 0, 0, 128)) == INVALID
+    assert append(kc=_Tensor(4 * GB, 2048, 64, 128)) == ALIAS         # one cache for both
+    assert append(kc=_Tensor(1 * GB, 2048, 64, 128)) == ALIAS
+    assert append(kc=_Tensor(3 * GB, 2048, 64, 32)) == INVALID        # cache rows on top of each other
+    assert append(tokens=0) == OK
+
+
+def test_binding_refusals():
+    import torch
+    t = torch.zeros(1, 2, 4, 64, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        gsr.masked_attention_fwd(t, t, t, t)                           # not on a GPU
+    with pytest.raises(TypeError):
+        gsr.masked_attention_fwd(t.float(), t, t, t)
+    with pytest.raises(ValueError):
+        gsr.tree_attention_fwd(t[0], t, t, t, t, t, t, t, 1)
+    with pytest.raises(ValueError):
+        gsr.kv_cache_append(t[0], t[0], t, t, t)
+    with pytest.raises(ValueError):
+        gsr.kv_block_tables(*[torch.zeros(1, dtype=torch.int32)] * 4, t, 16, *[t] * 6)
