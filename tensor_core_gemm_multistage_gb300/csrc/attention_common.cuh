@@ -2,6 +2,8 @@
 // types, the interval of keys a query sees, the score function, and attention of single rows.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 
 #include "device_common.cuh"
@@ -93,6 +95,49 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // cap_out (1 - 2 r), and tanh's derivative 4 r (1 - r) has no cancellation.  The absolute error
 // of a score is a few units of cap 2^-24, which is what the softmax sees.
 __device__ __forceinline__ float cap_r(float s, float cap_in) { return rcp_approx(1.0f + ex2_approx(s * cap_in)); }
+
+enum ScoreMode : int { kScorePlain = 0, kScoreBias = 1, kScoreCap = 2 };   // kScoreCap: a bias too, if there is one
+
+// 32 raw products of one row and consecutive keys -> scores in log2 units, in place.  `base` is the
+// first key's distance from the row's position (later keys are closer by 1 each).  With a cap two
+// reciprocals come from one: 1 / a = b / (a b); 2^60 keeps a b finite and is tanh = 1 to the last
+// bit (a NaN passes by the minimum and is put back).
+template <int MODE>
+__device__ __forceinline__ void score_chunk(uint32_t (&rr)[32], const ScoreArgs& sc, float slope2, float base) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        float y0 = __uint_as_float(rr[i]), y1 = __uint_as_float(rr[i + 1]);
+        if (MODE == kScoreCap) {
+            const float a = 1.0f + ex2_approx(fminf(y0 * sc.cap_in, 60.0f));
+            const float b = 1.0f + ex2_approx(fminf(y1 * sc.cap_in, 60.0f));
+            const float ab = -2.0f * sc.cap_out * rcp_approx(a * b);
+            y0 = (y0 != y0) ? y0 : fmaf(ab, b, sc.cap_out);
+            y1 = (y1 != y1) ? y1 : fmaf(ab, a, sc.cap_out);
+        } else {
+            y0 *= sc.sl2;
+            y1 *= sc.sl2;
+        }
+        if (MODE != kScorePlain) {
+            y0 = fmaf(-slope2, fabsf(base - (float)i), y0);
+            y1 = fmaf(-slope2, fabsf(base - (float)(i + 1)), y1);
+        }
+        rr[i] = __float_as_uint(y0);
+        rr[i + 1] = __float_as_uint(y1);
+    }
+}
+
+// Once per device: lets `kernel` use `bytes` of dynamic shared memory.
+template <class K>
+cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
 
 // ---------------------------------------------------------------------------
 // One row by one warp

@@ -1,0 +1,598 @@
+// attention_masked_fwd.cuh - attention forward with a document or prefix mask, capped scores, a
+// distance bias and grouped heads:  O = softmax(score(Q K^T)) V.  Instantiated per element type.
+//
+// Every mask here leaves a query one interval of keys [lo, hi), and intervals never step back from
+// one query to the next (row_interval), so a block of queries reads the key tiles from its first
+// row's lo to its last row's hi and skips the rest: a packed row of documents costs what its
+// documents cost, whatever the row's length.
+//
+//  * one CTA per SM, 320 threads: warp 0 takes work items and issues TMA copies, one lane of warp 1
+//    issues every MMA, warps 2-5 run the softmax of query tile 0 and warps 6-9 that of tile 1, one
+//    thread per query row (= TMEM lane).  A work item is two 128-query tiles of one head;
+//  * items are CTAs of the grid that a running CTA takes over by cluster launch control: the
+//    hardware keeps the count, so nothing in memory is shared between launches, captured ones too;
+//  * per query tile, S(t) = Q K_t^T lands in 128 TMEM columns, the softmax writes P(t) over the
+//    last 64 of them, and O += P(t) V_t reads P from TMEM.  The two tiles alternate on the tensor
+//    core: while one is exponentiated, the other's products run;
+//  * the exponent base moves only when a tile's maximum exceeds it by more than 2^8, so P <= 256
+//    and O is rarely rescaled.  P is rounded to the operands' type for the second product (the
+//    tensor core takes both operands in one type); its sum l is kept in fp32 from unrounded values.
+//
+// Masked scores are replaced by -inf, so what K holds there is never used.  A masked V row enters
+// the product as 0 V, which is NaN where V is not finite: a row whose output is not finite is
+// computed again by its warp from the keys it sees alone (masked_row).
+#pragma once
+
+#include <atomic>
+
+#include "attention_common.cuh"
+#include "ptx_attention.cuh"
+
+namespace gsr {
+
+template <class T_, int D_, int MODE_>
+struct MaskedFwdCfg {
+    using T = T_;
+    static constexpr int D = D_;
+    static constexpr int MODE = MODE_;
+    static constexpr int BQ = 128, BKV = 128;
+    static constexpr int NQ = 2;
+    static constexpr int DCH = D / 64;                // 64-column (128-byte) chunks per row
+    static constexpr int CHUNK_BYTES = 128 * 128;
+    static constexpr int Q_BYTES = BQ * D * 2;
+    static constexpr int KV_BYTES = BKV * D * 2;
+    static constexpr int SM_THREADS = 128 * NQ;
+    static constexpr int NUM_THREADS = 64 + SM_THREADS;
+    static constexpr int QBUF = D == 64 ? 2 : 1;      // Q sets that fit: with two, the next item's loads early
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = OFF_Q + QBUF * NQ * Q_BYTES;   // ring of 2 entries {K_t, V_(t-1)}
+    static constexpr int OFF_V = OFF_K + 2 * KV_BYTES;
+    static constexpr int OFF_BAR = OFF_V + 2 * KV_BYTES;
+    static constexpr int NUM_BARS = 20;
+    static constexpr int OFF_CLC = OFF_BAR + NUM_BARS * 8;      // 16-byte aligned
+    static constexpr int OFF_ITEM = OFF_CLC + 16;               // 2 x 8 ints
+    static constexpr int OFF_MISC = OFF_ITEM + 64;
+    static constexpr int SMEM_BYTES = OFF_MISC + 16;
+    static constexpr int TMEM_COLS = 512;
+    static constexpr uint32_t T_S = 0, T_O = 256, P_COL = 64;
+    static constexpr uint32_t IDESC_S = idesc_16_f32(Elem<T>::bf16, BQ, BKV, false, false);
+    static constexpr uint32_t IDESC_PV = idesc_16_f32(Elem<T>::bf16, BQ, D, false, true);
+    static constexpr float RESCALE_LOG2 = 8.0f;
+    static_assert(D == 64 || D == 128, "head_dim 64 or 128");
+    static_assert(SMEM_BYTES <= 232448 && OFF_CLC % 16 == 0, "shared memory");
+    static_assert(T_O + NQ * D <= TMEM_COLS, "TMEM budget");
+};
+
+// One query row by one warp: every key it sees, in fp32.
+template <class T, int D>
+__device__ __noinline__ void masked_row(const MaskedFwdParams& p, int b, int h, int i, int lane) {
+    const int hk = h / p.mask.group;
+    float q[D / 32], acc[D / 32], m, l;
+    load_row<T, D>(static_cast<const T*>(p.Q.data) + b * p.Q.batch + h * p.Q.head + i * p.Q.row, lane, q);
+    const T* kb = static_cast<const T*>(p.K.data) + b * p.K.batch + hk * p.K.head;
+    const T* vb = static_cast<const T*>(p.V.data) + b * p.V.batch + hk * p.V.head;
+    const float slope2 = p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
+    int lo, hi;
+    row_interval(p.mask, b, i, lo, hi);
+    const int pos = i + p.mask.offset;
+    row_forward<T, D>(q, lo, hi, p.score, slope2, lane,
+                      [&](int j, const T*& k, const T*& v, float& dist) {
+                          k = kb + j * p.K.row;
+                          v = vb + j * p.V.row;
+                          dist = fabsf((float)(pos - j));
+                          return true;
+                      },
+                      acc, m, l);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[e] *= inv;
+    store_row<T, D>(static_cast<T*>(p.O.data) + b * p.O.batch + h * p.O.head + i * p.O.row, lane, acc);
+    if (p.lse && lane == 0)
+        p.lse[((long long)b * p.mask.Hq + h) * p.mask.Sq + i] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// No keys at all: O = 0, lse = -inf.  One warp per row.
+template <class T, int D>
+__global__ void __launch_bounds__(256) gsr_masked_empty_kernel(const MaskedFwdParams p) {
+    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= (long long)p.mask.B * p.mask.Hq * p.mask.Sq) return;
+    const int i = (int)(row % p.mask.Sq), bh = (int)(row / p.mask.Sq);
+    const float zero[D / 32] = {};
+    store_row<T, D>(static_cast<T*>(p.O.data) + (bh / p.mask.Hq) * p.O.batch + (bh % p.mask.Hq) * p.O.head + i * p.O.row,
+                    threadIdx.x & 31, zero);
+    if (p.lse && (threadIdx.x & 31) == 0) p.lse[row] = -INFINITY;
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
+    gsr_masked_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ MaskedFwdParams p) {
+    using T = typename Cfg::T;
+    constexpr int D = Cfg::D;
+    constexpr int NQ = Cfg::NQ;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {                    // the 128-byte-swizzled operands need it
+        if (threadIdx.x == 0) atomicCAS(p.err, 0, kDevErrKernelMaskedFwd | kDevErrLayout);
+        return;
+    }
+    const uint32_t sb = smem_u32(smem);
+    auto bar = [&](int i) { return sb + Cfg::OFF_BAR + 8u * i; };
+    auto full = [&](int s) { return bar(0 + s); };
+    auto empty = [&](int s) { return bar(2 + s); };
+    auto sfull = [&](int q) { return bar(4 + q); };
+    auto pfull = [&](int q) { return bar(6 + q); };
+    auto odone = [&](int q) { return bar(8 + q); };
+    auto item_pub = [&](int i) { return bar(10 + i); };
+    auto item_read = [&](int i) { return bar(12 + i); };
+    auto qfull = [&](int b) { return bar(14 + b); };
+    auto qfree = [&](int b) { return bar(16 + b); };
+    const uint32_t clc = bar(18), drain = bar(19);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_MISC + 4);
+    volatile int* item_box = reinterpret_cast<volatile int*>(smem + Cfg::OFF_ITEM);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const MaskArgs& mk = p.mask;
+
+    // What the producer publishes of an item; b < 0: no more items.  Query tile q reads key tiles
+    // [t0[q], t1[q]).
+    struct Item {
+        int b, h, q_base, t0[NQ], t1[NQ];
+        __device__ __forceinline__ int first() const {
+            return t1[0] > t0[0] ? (t1[1] > t0[1] ? min(t0[0], t0[1]) : t0[0]) : t0[1];
+        }
+        __device__ __forceinline__ int last() const {
+            return t1[0] > t0[0] ? (t1[1] > t0[1] ? max(t1[0], t1[1]) : t1[0]) : t1[1];
+        }
+    };
+    auto read_item = [&](int box) {
+        volatile int* v = item_box + 8 * box;
+        return Item{v[0], v[1], v[2], {v[3], v[4]}, {v[5], v[6]}};
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+            mbar_init(sfull(s), 1);
+            mbar_init(pfull(s), 128);
+            mbar_init(odone(s), 1);
+            mbar_init(item_pub(s), 1);
+            mbar_init(item_read(s), 1 + Cfg::SM_THREADS / 32);   // the MMA lane and every softmax warp
+            mbar_init(qfull(s), 1);
+            mbar_init(qfree(s), 1);
+        }
+        mbar_init(clc, 1);
+        mbar_init(drain, 1);
+        *abort_flag = 0u;
+        fence_mbarrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), Cfg::TMEM_COLS);
+        tmem_relinquish_alloc_permit();
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const Waiter w{p.err, p.timeout_ns, abort_flag, kDevErrKernelMaskedFwd};
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ items + TMA producer
+        // The whole warp walks the items (lanes 0-3 find the intervals of the query tiles' first
+        // and last rows); lane 0 waits, publishes and copies.
+        const uint64_t pol = l2_policy_evict_last();     // K and V are read by every query block
+        const int n_qb = (mk.Sq + NQ * Cfg::BQ - 1) / (NQ * Cfg::BQ);
+        uint32_t n_pub = 0, n_q = 0, g = 0, n_clc = 0;   // items published, Q loads, ring entries, answers
+        uint32_t armed = 0, parity = 0, q_armed = 0, q_parity = 0;
+        bool drop_q = (p.test_flags & kTestDropFirstLoad) && blockIdx.x == 0;
+        bool asked = false;
+        int item = blockIdx.x;
+        while (true) {
+            Item it{-1, 0, 0, {0, 0}, {0, 0}};
+            if (item >= 0) {
+                // query blocks from the last (under a causal mask the longest) to the first, in
+                // groups of heads whose K and V stay in L2 together
+                const int per_group = p.head_group * n_qb, grp = item / per_group, r_in = item - grp * per_group;
+                const int gsz = min(mk.B * mk.Hq - grp * p.head_group, p.head_group);
+                const int bh = grp * p.head_group + r_in % gsz;
+                it.b = bh / mk.Hq;
+                it.h = bh - it.b * mk.Hq;
+                it.q_base = (n_qb - 1 - r_in / gsz) * NQ * Cfg::BQ;
+                // lane 2q: first row of tile q, lane 2q + 1: its last row
+                int lo = 0, hi = 0;
+                const int first = it.q_base + (lane >> 1 & 1) * Cfg::BQ;
+                const int row = lane & 1 ? min(first + Cfg::BQ, mk.Sq) - 1 : first;
+                if (lane < 4 && first < mk.Sq) row_interval(mk, it.b, row, lo, hi);
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    const int l = __shfl_sync(0xffffffffu, lo, 2 * q), e = __shfl_sync(0xffffffffu, hi, 2 * q + 1);
+                    it.t0[q] = l / Cfg::BKV;
+                    it.t1[q] = e > l ? (e + Cfg::BKV - 1) / Cfg::BKV : it.t0[q];
+                }
+            }
+            const uint32_t box = n_pub & 1u;
+            // the box's previous item has been read by every role
+            bool ok = lane != 0 || w.wait(item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (lane == 0) {
+                volatile int* v = item_box + 8 * box;
+                v[0] = it.b;
+                v[1] = it.h;
+                v[2] = it.q_base;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    v[3 + q] = it.t0[q];
+                    v[5 + q] = it.t1[q];
+                }
+                mbar_arrive(item_pub(box));              // release: the consumers read the box after
+            }
+            ++n_pub;
+            if (item < 0) break;
+            if (lane == 0) {
+                fence_proxy_async_smem();                // the last answer has been read
+                mbar_arrive_expect_tx(clc, 16);
+                clc_try_cancel(sb + Cfg::OFF_CLC, clc);
+                asked = true;
+                const int t_begin = it.first(), t_end = it.last();
+                if (t_begin < t_end) {
+                    const int qb = (int)(n_q % Cfg::QBUF);
+                    if (n_q >= (uint32_t)Cfg::QBUF)
+                        ok = w.wait(qfree(qb), ((n_q - Cfg::QBUF) / Cfg::QBUF) & 1u, kDevErrProducerEmpty);
+                    if (ok) {
+                        if (drop_q) {
+                            drop_q = false;              // test hook: this Q is never loaded
+                        } else {
+                            const uint32_t qbase = sb + Cfg::OFF_Q + qb * NQ * Cfg::Q_BYTES;
+                            mbar_arrive_expect_tx(qfull(qb), NQ * Cfg::Q_BYTES);
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                                for (int c = 0; c < Cfg::DCH; ++c)
+                                    tma_load_4d(qbase + q * Cfg::Q_BYTES + c * Cfg::CHUNK_BYTES, &tmQ, qfull(qb), c * 64,
+                                                it.q_base + q * Cfg::BQ, it.h, it.b, pol);
+                            q_armed |= 1u << qb;
+                            q_parity = (q_parity & ~(1u << qb)) | ((n_q / Cfg::QBUF) & 1u) << qb;
+                        }
+                        ++n_q;
+                    }
+                    const int hk = it.h / mk.group;
+                    // entry t: K_t (t < t_end) and V_(t-1) (t > t_begin)
+                    for (int t = t_begin; ok && t <= t_end; ++t, ++g) {
+                        const int s = (int)(g & 1u);
+                        const uint32_t ph = (g >> 1) & 1u;
+                        if (!(ok = w.wait(empty(s), ph ^ 1u, kDevErrProducerEmpty))) break;
+                        const bool has_k = t < t_end, has_v = t > t_begin;
+                        mbar_arrive_expect_tx(full(s), (has_k ? Cfg::KV_BYTES : 0) + (has_v ? Cfg::KV_BYTES : 0));
+                        if (has_k) {
+#pragma unroll
+                            for (int c = 0; c < Cfg::DCH; ++c)
+                                tma_load_4d(sb + Cfg::OFF_K + s * Cfg::KV_BYTES + c * Cfg::CHUNK_BYTES, &tmK, full(s), c * 64,
+                                            t * Cfg::BKV, hk, it.b, pol);
+                        }
+                        if (has_v) {
+#pragma unroll
+                            for (int c = 0; c < Cfg::DCH; ++c)
+                                tma_load_4d(sb + Cfg::OFF_V + s * Cfg::KV_BYTES + c * Cfg::CHUNK_BYTES, &tmV, full(s), c * 64,
+                                            (t - 1) * Cfg::BKV, hk, it.b, pol);
+                        }
+                        armed |= 1u << s;
+                        parity = (parity & ~(1u << s)) | ph << s;
+                    }
+                }
+                if (ok && (ok = w.wait(clc, n_clc & 1u, kDevErrProducerEmpty))) {
+                    asked = false;
+                    item = clc_taken(sb + Cfg::OFF_CLC);
+                }
+            }
+            ++n_clc;
+            if (!__all_sync(0xffffffffu, ok)) break;
+            item = __shfl_sync(0xffffffffu, item, 0);
+        }
+        // every copy and answer under way must land before the CTA may exit
+        if (lane == 0) {
+            if (asked) w.drain(clc, (n_clc - 1) & 1u);
+            for (int b = 0; b < Cfg::QBUF; ++b)
+                if (q_armed & (1u << b)) w.drain(qfull(b), (q_parity >> b) & 1u);
+            for (int s = 0; s < 2; ++s)
+                if (armed & (1u << s)) w.drain(full(s), (parity >> s) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            uint32_t n_item = 0, n_q = 0, g = 0;
+            uint32_t pv_n[NQ] = {0u, 0u};                // pfull phases waited for, per query tile
+            bool ok = true;
+            while (ok) {
+                const uint32_t box = n_item & 1u;
+                if (!w.wait(item_pub(box), (n_item >> 1) & 1u, kDevErrMmaFull)) break;
+                const Item it = read_item(box);
+                mbar_arrive(item_read(box));
+                ++n_item;
+                if (it.b < 0) break;
+                const int t_begin = it.first(), t_end = it.last();
+                if (t_begin >= t_end) continue;
+                const int qb = (int)(n_q % Cfg::QBUF);
+                if (!w.wait(qfull(qb), (n_q / Cfg::QBUF) & 1u, kDevErrMmaFull)) break;
+                ++n_q;
+                tcgen05_fence_after();
+                for (int t = t_begin; ok && t <= t_end; ++t, ++g) {
+                    const int s = (int)(g & 1u);
+                    if (!(ok = w.wait(full(s), (g >> 1) & 1u, kDevErrMmaFull))) break;   // K_t and V_(t-1)
+                    tcgen05_fence_after();
+                    const uint32_t k_s = sb + Cfg::OFF_K + s * Cfg::KV_BYTES;
+                    const uint32_t v_s = sb + Cfg::OFF_V + s * Cfg::KV_BYTES;
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        if (t > it.t0[q] && t <= it.t1[q]) {
+                            // O_q += P_q(t-1) V_(t-1)
+                            if (!(ok = w.wait(pfull(q), pv_n[q] & 1u, kDevErrMmaFull))) break;
+                            ++pv_n[q];
+                            tcgen05_fence_after();
+                            const uint32_t p_t = tmem_base + Cfg::T_S + q * 128 + Cfg::P_COL;
+#pragma unroll
+                            for (int k = 0; k < Cfg::BKV / 16; ++k)
+                                mma_f16_ts(tmem_base + Cfg::T_O + q * D, p_t + k * 8,
+                                           smem_desc_sw128(v_s + k * 2048, Cfg::CHUNK_BYTES, 1024), Cfg::IDESC_PV,
+                                           (t - 1 > it.t0[q] || k > 0) ? 1u : 0u);
+                            if (t == it.t1[q]) mma_commit(odone(q));
+                        }
+                        if (t >= it.t0[q] && t < it.t1[q]) {
+                            // S_q(t) = Q_q K_t^T, over P_q(t-1): one thread's products complete in order
+                            const uint32_t q_s = sb + Cfg::OFF_Q + (qb * NQ + q) * Cfg::Q_BYTES;
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = (k >> 2) * Cfg::CHUNK_BYTES + (k & 3) * 32;
+                                mma_f16_ss(tmem_base + Cfg::T_S + q * 128, smem_desc_sw128(q_s + off, 16, 1024),
+                                           smem_desc_sw128(k_s + off, 16, 1024), Cfg::IDESC_S, k > 0 ? 1u : 0u);
+                            }
+                            mma_commit(sfull(q));
+                        }
+                    }
+                    if (!ok) break;
+                    if (t == t_end - 1) mma_commit(qfree(qb));   // the item's last Q K^T products are issued
+                    mma_commit(empty(s));
+                }
+            }
+            mma_commit(drain);
+            w.drain(drain, 0);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax + output (warps 2-9)
+        const int q = (warp - 2) >> 2;
+        const int quad = warp & 3;
+        const int r = quad * 32 + lane;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
+        const uint32_t s_col = lane_base + Cfg::T_S + q * 128;
+        const uint32_t o_col = lane_base + Cfg::T_O + q * D;
+        const ScoreArgs& sc = p.score;
+        const float sl2 = sc.sl2;
+        const bool scale_pos = sl2 >= 0.0f;
+        uint32_t n_item = 0, s_n = 0, o_n = 0;
+        bool ok = true;
+        while (ok) {
+            const uint32_t box = n_item & 1u;
+            if (!__all_sync(0xffffffffu, w.wait(item_pub(box), (n_item >> 1) & 1u, kDevErrEpilogueFull))) break;
+            const Item it = read_item(box);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(item_read(box));
+            ++n_item;
+            if (it.b < 0) break;
+            const int qi = it.q_base + q * Cfg::BQ + r;
+            const int t0 = q == 0 ? it.t0[0] : it.t0[1], t1 = q == 0 ? it.t1[0] : it.t1[1];
+            int lo = 0, hi = 0;
+            if (qi < mk.Sq && t0 < t1) row_interval(mk, it.b, qi, lo, hi);
+            const float slope2 = Cfg::MODE != kScorePlain && sc.slopes ? __ldg(sc.slopes + it.h) * kLog2e : 0.0f;
+            float m = -INFINITY, l = 0.0f;
+
+            for (int t = t0; t < t1; ++t) {
+                // the warp agrees before any .sync.aligned TMEM access
+                if (!__all_sync(0xffffffffu, w.wait(sfull(q), s_n & 1u, kDevErrEpilogueFull))) {
+                    ok = false;
+                    break;
+                }
+                ++s_n;
+                tcgen05_fence_after();
+                const int k0 = t * Cfg::BKV;
+                const bool masked = k0 < lo || k0 + Cfg::BKV > hi;
+                uint32_t sc0[32], sc1[32], sc2[32], sc3[32];
+                tmem_ld_32x32b_x32(s_col + 0, sc0);
+                tmem_ld_32x32b_x32(s_col + 32, sc1);
+                tmem_ld_32x32b_x32(s_col + 64, sc2);
+                tmem_ld_32x32b_x32(s_col + 96, sc3);
+                tmem_ld_wait(sc0);
+                reg_tie(sc1);
+                reg_tie(sc2);
+                reg_tie(sc3);
+                // scores in log2 units in place, -inf where the row sees nothing; an unmasked tile of
+                // plain scores keeps the raw products (scaled in the exponent below)
+                const float base = (float)(qi + mk.offset - k0);
+                auto transform = [&](uint32_t (&rr)[32], int c) {
+                    score_chunk<Cfg::MODE>(rr, sc, slope2, base - (float)(c * 32));
+                    if (masked) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c * 32 + i < lo - k0 || c * 32 + i >= hi - k0) rr[i] = 0xff800000u;
+                    }
+                };
+                const bool raw = Cfg::MODE == kScorePlain && !masked;
+                if (!raw) {
+                    transform(sc0, 0);
+                    transform(sc1, 1);
+                    transform(sc2, 2);
+                    transform(sc3, 3);
+                }
+                // the row's maximum; of raw products under a negative scale their minimum
+                float mt;
+                if (raw && !scale_pos) {
+                    float e0 = INFINITY, e1 = e0;
+                    auto fold = [&](const uint32_t (&rr)[32]) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            e0 = min3f(e0, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]));
+                            e1 = min3f(e1, __uint_as_float(rr[i + 2]), __uint_as_float(rr[i + 3]));
+                        }
+                    };
+                    fold(sc0);
+                    fold(sc1);
+                    fold(sc2);
+                    fold(sc3);
+                    mt = fminf(e0, e1) * sl2;
+                } else {
+                    float e0 = -INFINITY, e1 = e0, e2 = e0, e3 = e0;
+                    auto fold = [&](const uint32_t (&rr)[32]) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            e0 = max3f(e0, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]));
+                            e1 = max3f(e1, __uint_as_float(rr[i + 2]), __uint_as_float(rr[i + 3]));
+                            e2 = max3f(e2, __uint_as_float(rr[i + 4]), __uint_as_float(rr[i + 5]));
+                            e3 = max3f(e3, __uint_as_float(rr[i + 6]), __uint_as_float(rr[i + 7]));
+                        }
+                    };
+                    fold(sc0);
+                    fold(sc1);
+                    fold(sc2);
+                    fold(sc3);
+                    mt = max3f(fmaxf(e0, e1), e2, e3);
+                    if (raw) mt *= sl2;
+                }
+                // lazy move of the exponent base: only by more than 2^RESCALE_LOG2 (always from -inf)
+                float factor = 1.0f;
+                const bool bump = mt > m + Cfg::RESCALE_LOG2;
+                if (bump) {
+                    factor = (m == -INFINITY) ? 0.0f : ex2_approx(m - mt);
+                    m = mt;
+                }
+                l *= factor;
+                const float neg_m = (m == -INFINITY) ? 0.0f : -m;
+                const float mul = raw ? sl2 : 1.0f;
+                float ls0 = 0.0f, ls1 = 0.0f;
+                auto chunk_p = [&](const uint32_t (&rr)[32], int c) {
+                    uint32_t packed[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x0, x1;
+                        ffma2(x0, x1, __uint_as_float(rr[2 * i]), __uint_as_float(rr[2 * i + 1]), mul, mul, neg_m, neg_m);
+                        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                        fadd2(ls0, ls1, p0, p1);
+                        packed[i] = Elem<T>::pack(p0, p1);
+                    }
+                    tmem_st_32x32b_x16(s_col + Cfg::P_COL + c * 16, packed);
+                };
+                chunk_p(sc0, 0);
+                chunk_p(sc1, 1);
+                chunk_p(sc2, 2);
+                chunk_p(sc3, 3);
+                if (t > t0 && __any_sync(0xffffffffu, bump)) {
+                    // O_q (this warp's rows) *= factor: PV_q(t-1) completed before S_q(t) did, and
+                    // PV_q(t) waits for the arrival below; done after the exponentials, when the
+                    // scores are dead
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t rr[32];
+                        tmem_ld_32x32b_x32(o_col + c * 32, rr);
+                        tmem_ld_wait(rr);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float y0, y1;
+                            fmul2(y0, y1, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]), factor, factor);
+                            rr[i] = __float_as_uint(y0);
+                            rr[i + 1] = __float_as_uint(y1);
+                        }
+                        tmem_st_32x32b_x32(o_col + c * 32, rr);
+                    }
+                }
+                tmem_st_wait();
+                tcgen05_fence_before();
+                mbar_arrive(pfull(q));           // P_q(t) (and a rescaled O_q) ready for the MMA
+                l += ls0 + ls1;
+            }
+            // output: O_q / l, and the log-sum-exp.  The next item's first PV_q, which overwrites
+            // O_q, waits for this group's next P, issued only after these loads.
+            if (ok && t0 < t1) {
+                ok = __all_sync(0xffffffffu, w.wait(odone(q), o_n & 1u, kDevErrEpilogueFull));
+                ++o_n;
+                tcgen05_fence_after();
+            }
+            if (!ok) break;
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            bool bad = !(l < INFINITY);          // l or an element of O is infinite or NaN
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.O.data) + it.b * p.O.batch + it.h * p.O.head +
+                                                  (long long)qi * p.O.row);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t rr[32];
+                if (t0 < t1) {
+                    tmem_ld_32x32b_x32(o_col + c * 32, rr);
+                    tmem_ld_wait(rr);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) rr[i] = 0u;
+                }
+                if (lo >= hi) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) rr[i] = 0u;     // 0 V of a row without keys
+                }
+                if (qi < mk.Sq) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float a = __uint_as_float(rr[8 * k + 2 * i]), b = __uint_as_float(rr[8 * k + 2 * i + 1]);
+                            bad |= !(fabsf(a) < INFINITY) | !(fabsf(b) < INFINITY);
+                            v[i] = Elem<T>::pack(a * inv, b * inv);
+                        }
+                        dst[c * 4 + k] = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+            }
+            if (p.lse && qi < mk.Sq)
+                p.lse[((long long)it.b * mk.Hq + it.h) * mk.Sq + qi] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+            tcgen05_fence_before();
+            // rows that are not finite, again from the keys they see
+            __syncwarp();
+            for (uint32_t again = __ballot_sync(0xffffffffu, bad && qi < mk.Sq && lo < hi); again; again &= again - 1)
+                masked_row<T, D>(p, it.b, it.h, it.q_base + q * Cfg::BQ + quad * 32 + __ffs(again) - 1, lane);
+        }
+    }
+
+    tcgen05_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tcgen05_fence_after();
+        tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+    }
+}
+
+template <class Cfg>
+cudaError_t launch_masked_cfg(const MaskedFwdMaps& tm, const MaskedFwdParams& p, cudaStream_t stream) {
+    static std::atomic<uint64_t> attr_done{0};
+    const cudaError_t e = allow_smem(gsr_masked_fwd_kernel<Cfg>, Cfg::SMEM_BYTES, attr_done);
+    if (e != cudaSuccess) return e;
+    gsr_masked_fwd_kernel<Cfg><<<(unsigned)p.num_items, Cfg::NUM_THREADS, Cfg::SMEM_BYTES, stream>>>(tm.q, tm.k, tm.v, p);
+    return cudaGetLastError();
+}
+
+template <class T, int D>
+cudaError_t launch_masked_type(const MaskedFwdMaps& tm, const MaskedFwdParams& p, cudaStream_t stream) {
+    if (p.mask.Skv == 0) {
+        const long long rows = (long long)p.mask.B * p.mask.Hq * p.mask.Sq;
+        gsr_masked_empty_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
+    if (p.score.cap_in != 0.0f) return launch_masked_cfg<MaskedFwdCfg<T, D, kScoreCap>>(tm, p, stream);
+    if (p.score.slopes) return launch_masked_cfg<MaskedFwdCfg<T, D, kScoreBias>>(tm, p, stream);
+    return launch_masked_cfg<MaskedFwdCfg<T, D, kScorePlain>>(tm, p, stream);
+}
+
+}  // namespace gsr

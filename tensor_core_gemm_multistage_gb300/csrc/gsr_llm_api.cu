@@ -108,6 +108,22 @@ gsr::ScoreArgs score_args(float softmax_scale, float softcap, const float* slope
     return s;
 }
 
+// Tensor map of a strided operand, box 64 x box_rows, 128-byte swizzle, zero fill outside.
+gsr_status encode(CUtensorMap* map, const Strided& t, int32_t dtype, int64_t batch, int64_t heads, int64_t rows,
+                  int64_t d, uint32_t box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 encoder = nullptr;
+    const gsr_status s = gsr::host::tensor_map_encoder(&encoder);
+    if (s != GSR_OK) return s;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads, (cuuint64_t)batch};
+    const cuuint64_t strides[3] = {(cuuint64_t)t.row * 2, (cuuint64_t)t.head * 2, (cuuint64_t)t.batch * 2};
+    const cuuint32_t box[4] = {64, box_rows, 1, 1}, unit[4] = {1, 1, 1, 1};
+    const CUresult r = encoder(map, dtype == GSR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                               4, t.data, dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GSR_OK : gsr::host::fail_encode(r);
+}
+
 // Layout of the backward pass's workspace, 256-byte pieces.
 struct BwdLayout {
     int64_t sp, lse2, delta, lo, hi, total;
@@ -159,7 +175,21 @@ gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor
     p.lse = lse;
     p.timeout_ns = gsr::host::wait_timeout_ns();
     p.test_flags = gsr::host::test_flags();
-    const cudaError_t e = gsr::launch_masked_fwd(p, (int)D, desc->dtype == GSR_BF16, st);
+    gsr::MaskedFwdMaps tm;
+    if (Skv > 0 && ((s = encode(&tm.q, p.Q, desc->dtype, B, Hq, Sq, D, 128)) != GSR_OK ||
+                    (s = encode(&tm.k, p.K, desc->dtype, B, Hkv, Skv, D, 128)) != GSR_OK ||
+                    (s = encode(&tm.v, p.V, desc->dtype, B, Hkv, Skv, D, 128)) != GSR_OK))
+        return s;
+    p.num_items = (int)((Sq + 255) / 256 * B * Hq);
+    // Causal items run longest first across as many heads as keep their K and V within ~48 MiB of
+    // L2; without a mask every item is equally long and one group's heads run together.
+    const int64_t kv_bytes = Skv * D * 4;
+    int64_t heads = desc->causal ? ((int64_t)48 << 20) / (kv_bytes > 0 ? kv_bytes : 1) * p.mask.group : 1;
+    if (heads < 1) heads = 1;
+    if (heads > B * Hq) heads = B * Hq;
+    p.head_group = (int)heads;
+    const cudaError_t e = desc->dtype == GSR_BF16 ? gsr::launch_masked_fwd_bf16(tm, p, (int)D, st)
+                                                  : gsr::launch_masked_fwd_f16(tm, p, (int)D, st);
     return e == cudaSuccess ? GSR_OK : gsr::host::fail(e);
 }
 

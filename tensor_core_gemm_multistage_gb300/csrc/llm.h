@@ -90,7 +90,13 @@ struct TreeParams {
     uint32_t test_flags;
 };
 
-cudaError_t launch_masked_fwd(const MaskedFwdParams& p, int D, bool bf16, cudaStream_t stream);
+// 4-D tensor maps {D, rows, heads, batch} with 64 x 128 x 1 x 1 boxes, one per operand.
+struct MaskedFwdMaps {
+    CUtensorMap q, k, v;
+};
+// Skv == 0: no maps are read, O = 0 and lse = -inf.
+cudaError_t launch_masked_fwd_f16(const MaskedFwdMaps& tm, const MaskedFwdParams& p, int D, cudaStream_t stream);
+cudaError_t launch_masked_fwd_bf16(const MaskedFwdMaps& tm, const MaskedFwdParams& p, int D, cudaStream_t stream);
 cudaError_t launch_masked_bwd(const MaskedBwdParams& p, int D, bool bf16, cudaStream_t stream);
 cudaError_t launch_tree(const TreeParams& p, bool bf16, cudaStream_t stream);
 

@@ -146,10 +146,13 @@ class Tree:
         assert status == gsr.Status.OK, hex(code)
         return self
 
-    def check(self):
+    def check(self, rows=None):
+        """`rows`: the rows that are compared (the others may hold NaN)."""
         want, terms = llm.tree_attention(self.q, self.kc, self.vc, self.table, self.kv, self.starts, self.parents, self.scale,
                                          self.cap, None if self.slopes is None else self.slopes.cpu().numpy(), self.max_nodes)
         got = llm.f64(self.o)
+        if rows is not None:
+            got, want, terms = got[rows], want[rows], terms[rows]
         real = ~np.isnan(want)
         assert np.all(got[~real] == 7.0), "rows of no request were written"
         got, want, terms = got[real], want[real], terms[real]
@@ -220,14 +223,13 @@ def test_rows_nothing_sees_have_no_influence(bad):
     assert torch.equal(t.run().o, clean)
     # a sibling no other node sees: only its own row changes
     t.parents[5 + 11] = t.parents[5 + 10] = -1
-    clean = t.run().check().o.clone()
+    t.run().check()
     j = t.kv[1] - 1
     t.kc[int(t.table[1][j // 16]), j % 16] = bad
     t.vc[int(t.table[1][j // 16]), j % 16] = bad
-    o = t.run().o
-    keep = [n for n in range(t.N) if n != 5 + 11]
-    assert torch.all((o[keep].float() - clean[keep].float()).abs() <= 2 * t.u * clean[keep].float().abs() + 1e-3)
-    assert torch.isnan(o[5 + 11]).all()
+    t.run().check([n for n in range(t.N) if n != 5 + 11])
+    if bad != bad:
+        assert torch.isnan(t.o[5 + 11]).all()
 
 
 def test_pages_outside_the_pool_hold_nothing():
