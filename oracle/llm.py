@@ -78,8 +78,8 @@ def masked_attention(Q, K, V, see, scale=0.0, cap=0.0, slopes=None):
 
 
 def masked_attention_bwd(dO, Q, K, V, O, lse, see, scale=0.0, cap=0.0, slopes=None):
-    """((dQ, dK, dV), sums of |terms| of each: once over P or |dS| (the rounded factor) and once with
-    dS's own two terms apart)."""
+    """((dQ, dK, dV), three sums of |terms| of each: over P or |dS| (the rounded factor), with dS's own
+    two terms apart, and with 1 in place of the rounded factor)."""
     dO, Q, K, V, O, lse = (f64(t) for t in (dO, Q, K, V, O, lse))
     B, Hq, Sq, D = Q.shape
     Hkv, Skv = K.shape[1], K.shape[2]
@@ -106,7 +106,11 @@ def masked_attention_bwd(dO, Q, K, V, O, lse, see, scale=0.0, cap=0.0, slopes=No
              fold(np.einsum("bhqk,bhqd->bhkd", P, np.abs(dO))))
     wide = (abs(scale) * np.einsum("bhqk,bhkd->bhqd", aS, np.abs(Kg)),
             abs(scale) * fold(np.einsum("bhqk,bhqd->bhkd", aS, np.abs(Q))), terms[2])
-    return (dQ, dK, dV), terms, wide
+    seen = np.repeat(see[:, None], Hq, axis=1).astype(np.float64)
+    plain = (abs(scale) * np.einsum("bhqk,bhkd->bhqd", seen, np.abs(Kg)),
+             abs(scale) * fold(np.einsum("bhqk,bhqd->bhkd", seen, np.abs(Q))),
+             fold(np.einsum("bhqk,bhqd->bhkd", seen, np.abs(dO))))
+    return (dQ, dK, dV), terms, wide, plain
 
 
 def tree_attention(Q, k_cache, v_cache, table, kv_lens, q_starts, parents, scale=0.0, cap=0.0, slopes=None,

@@ -1,0 +1,1096 @@
+// attention_masked_bwd.cuh - gradients of attention with a document or prefix mask, capped scores,
+// a distance bias and grouped heads.  Instantiated per element type.
+//
+// With P_ij = exp(y_ij - lse_i) from the forward pass's log-sum-exp and delta_i = dO_i . O_i,
+//     dV_j = sum_i P_ij dO_i
+//     dS_ij = P_ij (dO_i . V_j - delta_i) c_ij          c = 1 - tanh^2 with a cap, else 1
+//     dQ_i = scale sum_j dS_ij K_j        dK_j = scale sum_i dS_ij Q_i
+// dK and dV of a key/value head sum over the query heads of its group.
+//
+// Three launches: one pass over the rows (delta, intervals), then dK and dV by the CTA that owns
+// the keys and dQ by the CTA that owns the queries.  The two recompute S and dP, seven products of
+// 128 x 128 x D instead of the five that one pass with atomically added dQ would take; in return
+// no result depends on the order of atomics, dQ needs no fp32 buffer, and every accumulator stays
+// in TMEM from the first product to the last.
+//
+// fp16: P is carried as 2^12 P and dS as 2^(12 + e) dS with one e a call, so that neither goes
+// subnormal where a row has many keys or dO is small.  |dO_i . V_j - delta_i| <= 2 max|dO| max|V|
+// (Cauchy-Schwarz; O is a mean of V rows), and e is the largest power that keeps dS below 2^15 by
+// this bound.  bf16 has fp32's range and needs neither.
+//
+// Masked pairs get P = dS = 0 by selection, but a row of dO, Q or K that is not finite turns 0
+// times itself into NaN inside a product: a result row that is not finite is computed again by its
+// warp from the pairs it sees alone (row_dq, row_dkv).
+#pragma once
+
+#include "attention_common.cuh"
+#include "ptx_attention.cuh"
+
+namespace gsr {
+
+template <class T>
+constexpr float kPShift = Elem<T>::bf16 ? 0.0f : 12.0f;      // log2 of P's factor
+
+// log2 of dS's further factor.
+template <class T>
+__device__ __forceinline__ float ds_shift(const unsigned* norms) {
+    if (Elem<T>::bf16) return 0.0f;
+    const float n = __uint_as_float(norms[0]) * __uint_as_float(norms[1]);   // squares of the bound's factors
+    if (!(n > 0.0f && n < INFINITY)) return 0.0f;
+    return fminf(fmaxf(floorf(2.0f - 0.5f * log2f(n)), -100.0f), 100.0f);    // 15 - 12 - 1 - log2(bound / 2)
+}
+
+// ---------------------------------------------------------------------------
+// Rows: exponent offsets, delta, intervals, and the norms that bound dS
+// ---------------------------------------------------------------------------
+// One warp per query row (b, h, i), rows padded to Sp, then (fp16) one per value row.  Bound by the
+// read of dO and O.  Maxima are order-free, so the atomics are deterministic.
+template <class T, int D>
+__global__ void __launch_bounds__(256) gsr_masked_bwd_rows_kernel(const __grid_constant__ MaskedBwdParams p) {
+    const int lane = threadIdx.x & 31;
+    const MaskArgs& mk = p.mask;
+    const long long q_rows = (long long)mk.B * mk.Hq * p.Sp;
+    long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row < q_rows) {
+        const int i = (int)(row % p.Sp), bh = (int)(row / p.Sp), b = bh / mk.Hq, h = bh % mk.Hq;
+        float offset = -INFINITY, delta = 0.0f;
+        int lo = mk.Skv, hi = mk.Skv;
+        if (i < mk.Sq) {
+            row_interval(mk, b, i, lo, hi);
+            if (lo < hi) {
+                float x[D / 32], y[D / 32];
+                load_row<T, D>(static_cast<const T*>(p.dO.data) + b * p.dO.batch + h * p.dO.head + i * p.dO.row, lane, x);
+                load_row<T, D>(static_cast<const T*>(p.O.data) + b * p.O.batch + h * p.O.head + i * p.O.row, lane, y);
+                delta = warp_dot(x, y);
+                const float lse = __ldg(p.lse + ((long long)b * mk.Hq + h) * mk.Sq + i);
+                if (lse != -INFINITY) offset = kPShift<T> - lse * kLog2e;
+                if (!Elem<T>::bf16) {
+                    const float n = warp_dot(x, x);
+                    if (lane == 0 && n < INFINITY) atomicMax(p.norms, __float_as_uint(n));
+                }
+            }
+        }
+        if (lane == 0) {
+            p.offset[row] = offset;
+            p.neg_delta[row] = -delta;
+            if (h == 0) {
+                p.lo[(long long)b * p.Sp + i] = lo;
+                p.hi[(long long)b * p.Sp + i] = hi;
+            }
+        }
+        return;
+    }
+    row -= q_rows;
+    if (!Elem<T>::bf16 && row < (long long)mk.B * mk.Hkv * mk.Skv) {
+        const int j = (int)(row % mk.Skv), bh = (int)(row / mk.Skv), b = bh / mk.Hkv, h = bh % mk.Hkv;
+        float x[D / 32];
+        load_row<T, D>(static_cast<const T*>(p.V.data) + b * p.V.batch + h * p.V.head + j * p.V.row, lane, x);
+        const float n = warp_dot(x, x);
+        if (lane == 0 && n < INFINITY) atomicMax(p.norms + 1, __float_as_uint(n));
+    }
+}
+
+// Zero rows of a strided output (no queries, or no keys).  One warp per row.
+template <class T, int D>
+__global__ void __launch_bounds__(256) gsr_masked_zero_kernel(Strided t, int heads, int rows, long long total) {
+    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= total) return;
+    const float zero[D / 32] = {};
+    const int i = (int)(row % rows), bh = (int)(row / rows);
+    store_row<T, D>(static_cast<T*>(t.data) + (bh / heads) * t.batch + (bh % heads) * t.head + i * t.row, threadIdx.x & 31, zero);
+}
+
+// ---------------------------------------------------------------------------
+// Single rows, in fp32, by one warp
+// ---------------------------------------------------------------------------
+// P_ij and dS_ij (without their powers of two).
+template <class T, int D>
+__device__ __forceinline__ void pair_grad(const ScoreArgs& sc, float slope2, int dist, const float (&q)[D / 32],
+                                          const float (&k)[D / 32], const float (&dO)[D / 32],
+                                          const float (&v)[D / 32], float offset, float neg_delta, float& P, float& dS) {
+    float grad;
+    const float y = score_of(warp_dot(q, k), sc, grad) - slope2 * fabsf((float)dist);
+    P = ex2_approx(y + (offset - kPShift<T>));
+    dS = P * (warp_dot(dO, v) + neg_delta) * grad;
+}
+
+template <class T, int D>
+__device__ __noinline__ void row_dq(const MaskedBwdParams& p, int b, int h, int i, int lane) {
+    const MaskArgs& mk = p.mask;
+    const int hk = h / mk.group;
+    float q[D / 32], dO[D / 32], k[D / 32], v[D / 32], acc[D / 32] = {};
+    load_row<T, D>(static_cast<const T*>(p.Q.data) + b * p.Q.batch + h * p.Q.head + i * p.Q.row, lane, q);
+    load_row<T, D>(static_cast<const T*>(p.dO.data) + b * p.dO.batch + h * p.dO.head + i * p.dO.row, lane, dO);
+    const T* kb = static_cast<const T*>(p.K.data) + b * p.K.batch + hk * p.K.head;
+    const T* vb = static_cast<const T*>(p.V.data) + b * p.V.batch + hk * p.V.head;
+    const float slope2 = p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
+    const long long row = ((long long)b * mk.Hq + h) * p.Sp + i;
+    const float offset = p.offset[row], neg_delta = p.neg_delta[row];
+    const int lo = p.lo[(long long)b * p.Sp + i], hi = p.hi[(long long)b * p.Sp + i];
+    for (int j = lo; j < hi; ++j) {
+        load_row<T, D>(kb + j * p.K.row, lane, k);
+        load_row<T, D>(vb + j * p.V.row, lane, v);
+        float P, dS;
+        pair_grad<T, D>(p.score, slope2, i + mk.offset - j, q, k, dO, v, offset, neg_delta, P, dS);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(dS, k[e], acc[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[e] *= p.score.scale;
+    store_row<T, D>(static_cast<T*>(p.dQ.data) + b * p.dQ.batch + h * p.dQ.head + i * p.dQ.row, lane, acc);
+}
+
+// dK (or dV) of one key row: the queries that see key j lie between the first whose interval ends
+// behind it and the first whose interval starts behind it.
+template <class T, int D>
+__device__ __noinline__ void row_dkv(const MaskedBwdParams& p, int b, int hk, int j, bool want_dk, int lane) {
+    const MaskArgs& mk = p.mask;
+    float q[D / 32], dO[D / 32], k[D / 32], v[D / 32], acc[D / 32] = {};
+    load_row<T, D>(static_cast<const T*>(p.K.data) + b * p.K.batch + hk * p.K.head + j * p.K.row, lane, k);
+    load_row<T, D>(static_cast<const T*>(p.V.data) + b * p.V.batch + hk * p.V.head + j * p.V.row, lane, v);
+    const int* los = p.lo + (long long)b * p.Sp;
+    const int* his = p.hi + (long long)b * p.Sp;
+    for (int h = hk * mk.group; h < (hk + 1) * mk.group; ++h) {
+        const T* qb = static_cast<const T*>(p.Q.data) + b * p.Q.batch + h * p.Q.head;
+        const T* ob = static_cast<const T*>(p.dO.data) + b * p.dO.batch + h * p.dO.head;
+        const float slope2 = p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
+        const long long row = ((long long)b * mk.Hq + h) * p.Sp;
+        for (int i = 0; i < mk.Sq; ++i) {
+            if (j < los[i] || j >= his[i]) continue;
+            load_row<T, D>(qb + i * p.Q.row, lane, q);
+            load_row<T, D>(ob + i * p.dO.row, lane, dO);
+            float P, dS;
+            pair_grad<T, D>(p.score, slope2, i + mk.offset - j, q, k, dO, v, p.offset[row + i], p.neg_delta[row + i], P, dS);
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) acc[e] = want_dk ? fmaf(dS, q[e], acc[e]) : fmaf(P, dO[e], acc[e]);
+        }
+    }
+    if (want_dk) {
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) acc[e] *= p.score.scale;
+    }
+    const Strided& to = want_dk ? p.dK : p.dV;
+    store_row<T, D>(static_cast<T*>(to.data) + b * to.batch + hk * to.head + j * to.row, lane, acc);
+}
+
+// ---------------------------------------------------------------------------
+// Shared by the two tensor-core kernels
+// ---------------------------------------------------------------------------
+// 320 threads: warp 0 copies, one lane of warp 1 issues the products, warps 2-9 do the arithmetic
+// between them.  Warps w and w + 4 share 32 TMEM lanes and take 64 of the 128 columns each.
+constexpr int kBwdThreads = 320;
+constexpr int kBwdMathWarps = 8;
+constexpr int kTile = 128;
+constexpr int kChunkBytes = 128 * 128;
+
+// 32 raw products -> in place W = 2^x c with x = y + off (`off` per column or, where it is one row's,
+// a broadcast of one value), c the cap's derivative; `packed`, where wanted, gets 2^x alone in
+// pairs.  `base` as in score_chunk.
+template <class T, int MODE, bool PACK, class Off>
+__device__ __forceinline__ void weights_chunk(uint32_t (&rr)[32], const ScoreArgs& sc, float slope2, float base, Off off,
+                                              uint32_t (&packed)[16]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        float y0 = __uint_as_float(rr[i]), y1 = __uint_as_float(rr[i + 1]), c0 = 1.0f, c1 = 1.0f;
+        const float2 o = off(i);
+        if (MODE == kScoreCap) {
+            const bool n0 = y0 != y0, n1 = y1 != y1;
+            const float a = 1.0f + ex2_approx(fminf(y0 * sc.cap_in, 60.0f));
+            const float b = 1.0f + ex2_approx(fminf(y1 * sc.cap_in, 60.0f));
+            const float ab = rcp_approx(a * b);
+            const float r0 = ab * b, r1 = ab * a;
+            c0 = 4.0f * fmaf(-r0, r0, r0);
+            c1 = 4.0f * fmaf(-r1, r1, r1);
+            y0 = n0 ? y0 : fmaf(-2.0f * sc.cap_out, r0, sc.cap_out + o.x);
+            y1 = n1 ? y1 : fmaf(-2.0f * sc.cap_out, r1, sc.cap_out + o.y);
+        } else {
+            ffma2(y0, y1, y0, y1, sc.sl2, sc.sl2, o.x, o.y);
+        }
+        if (MODE != kScorePlain) {
+            y0 = fmaf(-slope2, fabsf(base - (float)i), y0);
+            y1 = fmaf(-slope2, fabsf(base - (float)(i + 1)), y1);
+        }
+        const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
+        if (PACK) packed[i / 2] = Elem<T>::pack(p0, p1);
+        rr[i] = __float_as_uint(MODE == kScoreCap ? p0 * c0 : p0);
+        rr[i + 1] = __float_as_uint(MODE == kScoreCap ? p1 * c1 : p1);
+    }
+}
+
+// The first index x of [0, n] with values[x] > v, or n (values ascending).  Whole warp, 32-way.
+__device__ __forceinline__ int warp_first_above(const int* values, int n, int v, int lane) {
+    int base = 0, len = n;
+    while (len > 0) {
+        const int chunk = (len + 31) >> 5, start = lane * chunk;      // a lane's piece; its last value decides
+        const bool above = start >= len || __ldg(values + base + min(start + chunk, len) - 1) > v;
+        const uint32_t pieces = __ballot_sync(0xffffffffu, above);
+        const int first = pieces ? (__ffs(pieces) - 1) * chunk : len;
+        if (first >= len) return base + len;
+        base += first;
+        len = min(chunk, len - first) - 1;                            // that last value is the answer if no earlier one is
+    }
+    return base;
+}
+
+// ---------------------------------------------------------------------------
+// dK and dV
+// ---------------------------------------------------------------------------
+// A work item is 128 keys of one key/value head; its steps are the query tiles that see any of them,
+// for every query head of the group.  Per step
+//     S^T = K Q^T,  dP^T = V dO^T       [128 keys x 128 queries] into 128 TMEM columns each
+//     P^T over S^T's columns, dV += P^T dO;   dS^T over dP^T's columns, dK += dS^T Q
+// with P^T and dS^T read from TMEM.  At D = 128 the four fill all 512 columns.  The products are
+// issued in the order S(n), dK(n-1), dP(n), dV(n): each finds its operand ready because the
+// arithmetic of the step before it runs meanwhile, and a region is overwritten only after the
+// product that reads it (one thread's products complete in order).  Q is read by S(n) and, a step
+// later, by dK(n), so its ring has three entries where dO's has two.
+template <class T_, int D_, int MODE_>
+struct DkvCfg {
+    using T = T_;
+    static constexpr int D = D_, MODE = MODE_;
+    static constexpr int DCH = D / 64;
+    static constexpr int TILE_BYTES = kTile * D * 2;
+    static constexpr int NQ = 3, NO = 2;              // ring entries of Q and of dO (with the rows' values)
+    static constexpr int OFF_K = 0;
+    static constexpr int OFF_V = OFF_K + TILE_BYTES;
+    static constexpr int OFF_Q = OFF_V + TILE_BYTES;
+    static constexpr int OFF_O = OFF_Q + NQ * TILE_BYTES;
+    static constexpr int OFF_ROWS = OFF_O + NO * TILE_BYTES;    // per entry: 128 offsets, 128 -delta
+    static constexpr int OFF_BAR = OFF_ROWS + NO * 1024;
+    static constexpr int NUM_BARS = 26;
+    static constexpr int OFF_CLC = OFF_BAR + NUM_BARS * 8;
+    static constexpr int OFF_ITEM = OFF_CLC + 16;
+    static constexpr int OFF_MISC = OFF_ITEM + 64;
+    static constexpr int SMEM_BYTES = OFF_MISC + 16;
+    static constexpr uint32_t T_S = 0, T_DP = 128, T_DV = 256, T_DK = 256 + D;
+    static constexpr uint32_t IDESC_S = idesc_16_f32(Elem<T>::bf16, kTile, kTile, false, false);
+    static constexpr uint32_t IDESC_ACC = idesc_16_f32(Elem<T>::bf16, kTile, D, false, true);
+    static_assert(SMEM_BYTES <= 232448 && OFF_CLC % 16 == 0, "shared memory");
+};
+
+// Products of a 128 x D by a 128 x D operand, both K-major: 128 x 128 into `d`.
+template <int D>
+__device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = (k >> 2) * kChunkBytes + (k & 3) * 32;
+        mma_f16_ss(d, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off, 16, 1024), idesc, k > 0 ? 1u : 0u);
+    }
+}
+
+// d (+)= A B with A 128 x 128 in TMEM, its k columns 0-63 packed from `a` on and 64-127 from
+// a + 64 on (each half overlays the fp32 columns of the warps that wrote it), and B's rows (k) at `b`.
+__device__ __forceinline__ void mma_overlay(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+#pragma unroll
+    for (int k = 0; k < kTile / 16; ++k)
+        mma_f16_ts(d, a + (k >> 2) * 64 + (k & 3) * 8, smem_desc_sw128(b + k * 2048, kChunkBytes, 1024), idesc,
+                   (accumulate || k > 0) ? 1u : 0u);
+}
+
+// Rows of an accumulator to a strided output, one row per thread; true if a value is not finite.
+template <class T, int D>
+__device__ __forceinline__ bool store_accumulator(uint32_t col, float factor, bool zero, bool write, T* row) {
+    uint4* dst = reinterpret_cast<uint4*>(row);
+    bool bad = false;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        uint32_t rr[32];
+        tmem_ld_32x32b_x32(col + c * 32, rr);
+        tmem_ld_wait(rr);
+        if (zero) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) rr[i] = 0u;
+        }
+        if (write) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a = __uint_as_float(rr[8 * k + 2 * i]), b = __uint_as_float(rr[8 * k + 2 * i + 1]);
+                    bad |= !(fabsf(a) < INFINITY) | !(fabsf(b) < INFINITY);
+                    v[i] = Elem<T>::pack(a * factor, b * factor);
+                }
+                dst[c * 4 + k] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+        }
+    }
+    return bad;
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    gsr_masked_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                          const __grid_constant__ MaskedBwdParams p) {
+    using T = typename Cfg::T;
+    constexpr int D = Cfg::D, DCH = Cfg::DCH, NQ = Cfg::NQ, NO = Cfg::NO;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0) atomicCAS(p.err, 0, kDevErrKernelMaskedDkv | kDevErrLayout);
+        return;
+    }
+    const uint32_t sb = smem_u32(smem);
+    auto bar = [&](int i) { return sb + Cfg::OFF_BAR + 8u * i; };
+    auto q_full = [&](int s) { return bar(0 + s); };
+    auto q_empty = [&](int s) { return bar(3 + s); };
+    auto o_full = [&](int s) { return bar(6 + s); };
+    auto o_empty = [&](int s) { return bar(8 + s); };
+    auto rows_empty = [&](int s) { return bar(10 + s); };
+    auto item_pub = [&](int i) { return bar(12 + i); };
+    auto item_read = [&](int i) { return bar(14 + i); };
+    const uint32_t kv_full = bar(16), kv_empty = bar(17), s_full = bar(18), p_full = bar(19), dp_full = bar(20),
+                   ds_full = bar(21), done = bar(22), clc = bar(23), drain = bar(24);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_MISC + 4);
+    volatile int* item_box = reinterpret_cast<volatile int*>(smem + Cfg::OFF_ITEM);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const MaskArgs& mk = p.mask;
+
+    // What the producer publishes; b < 0: no more items.  Query tiles [t0, t1) see some of the keys.
+    struct Item {
+        int b, hk, k0, t0, t1;
+    };
+    auto read_item = [&](int box) {
+        volatile int* v = item_box + 8 * box;
+        return Item{v[0], v[1], v[2], v[3], v[4]};
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NQ; ++s) {
+            mbar_init(q_full(s), 1);
+            mbar_init(q_empty(s), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(o_full(s), 1);
+            mbar_init(o_empty(s), 1);
+            mbar_init(rows_empty(s), 1);
+            mbar_init(item_pub(s), 1);
+            mbar_init(item_read(s), 1 + kBwdMathWarps);
+        }
+        mbar_init(kv_full, 1);
+        mbar_init(kv_empty, 1);
+        mbar_init(s_full, 1);
+        mbar_init(p_full, kBwdMathWarps);
+        mbar_init(dp_full, 1);
+        mbar_init(ds_full, kBwdMathWarps);
+        mbar_init(done, 1);
+        mbar_init(clc, 1);
+        mbar_init(drain, 1);
+        *abort_flag = 0u;
+        fence_mbarrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+        tma_prefetch_desc(&tmO);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish_alloc_permit();
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const Waiter w{p.err, p.timeout_ns, abort_flag, kDevErrKernelMaskedDkv};
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ items + TMA producer
+        const uint64_t pol = l2_policy_evict_last();     // Q and dO are read by every key tile
+        const int n_kt = (mk.Skv + kTile - 1) / kTile;
+        uint32_t n_pub = 0, n_item = 0, n_clc = 0, n = 0;   // items published, items with steps, answers, steps
+        uint32_t armed = 0, parity = 0;                  // per barrier q_full 0-2, o_full 3-4, kv_full 5
+        bool drop = (p.test_flags & kTestDropFirstLoad) && blockIdx.x == 0;
+        bool asked = false;
+        int item = blockIdx.x;
+        auto arm = [&](int i, uint32_t ph) {
+            armed |= 1u << i;
+            parity = (parity & ~(1u << i)) | (ph & 1u) << i;
+        };
+        while (true) {
+            Item it{-1, 0, 0, 0, 0};
+            if (item >= 0) {
+                // key tiles from the first (under a causal mask the most queries see it) to the last,
+                // in groups of key/value heads whose Q and dO stay in L2 together
+                const int per_group = p.kv_head_group * n_kt, grp = item / per_group, r_in = item - grp * per_group;
+                const int gsz = min(mk.B * mk.Hkv - grp * p.kv_head_group, p.kv_head_group);
+                const int bh = grp * p.kv_head_group + r_in % gsz;
+                it.b = bh / mk.Hkv;
+                it.hk = bh - it.b * mk.Hkv;
+                it.k0 = r_in / gsz * kTile;
+                // the first query whose interval ends behind the tile's first key, and the first whose
+                // interval starts behind its last
+                const int first = warp_first_above(p.hi + (long long)it.b * p.Sp, mk.Sq, it.k0, lane);
+                const int end = warp_first_above(p.lo + (long long)it.b * p.Sp, mk.Sq, it.k0 + kTile - 1, lane);
+                it.t0 = first / kTile;
+                it.t1 = first < end ? (end + kTile - 1) / kTile : it.t0;
+            }
+            const uint32_t box = n_pub & 1u;
+            bool ok = lane != 0 || w.wait(item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (lane == 0) {
+                volatile int* v = item_box + 8 * box;
+                v[0] = it.b;
+                v[1] = it.hk;
+                v[2] = it.k0;
+                v[3] = it.t0;
+                v[4] = it.t1;
+                mbar_arrive(item_pub(box));
+            }
+            ++n_pub;
+            if (item < 0) break;
+            if (lane == 0) {
+                fence_proxy_async_smem();
+                mbar_arrive_expect_tx(clc, 16);
+                clc_try_cancel(sb + Cfg::OFF_CLC, clc);
+                asked = true;
+                if (it.t0 < it.t1) {
+                    ok = w.wait(kv_empty, (n_item & 1u) ^ 1u, kDevErrProducerEmpty);
+                    if (ok && !drop) {
+                        mbar_arrive_expect_tx(kv_full, 2 * Cfg::TILE_BYTES);
+#pragma unroll
+                        for (int c = 0; c < DCH; ++c) {
+                            tma_load_4d(sb + Cfg::OFF_K + c * kChunkBytes, &tmK, kv_full, c * 64, it.k0, it.hk, it.b, pol);
+                            tma_load_4d(sb + Cfg::OFF_V + c * kChunkBytes, &tmV, kv_full, c * 64, it.k0, it.hk, it.b, pol);
+                        }
+                        arm(5, n_item);
+                    }
+                    drop = false;                        // test hook: the first K and V are never loaded
+                    ++n_item;
+                    for (int h = it.hk * mk.group; ok && h < (it.hk + 1) * mk.group; ++h) {
+                        const long long row0 = ((long long)it.b * mk.Hq + h) * p.Sp;
+                        for (int t = it.t0; t < it.t1; ++t, ++n) {
+                            const int sq = (int)(n % NQ), so = (int)(n % NO);
+                            const uint32_t ph_q = n / NQ, ph_o = n / NO;
+                            if (!(ok = w.wait(q_empty(sq), (ph_q & 1u) ^ 1u, kDevErrProducerEmpty))) break;
+                            mbar_arrive_expect_tx(q_full(sq), Cfg::TILE_BYTES);
+#pragma unroll
+                            for (int c = 0; c < DCH; ++c)
+                                tma_load_4d(sb + Cfg::OFF_Q + sq * Cfg::TILE_BYTES + c * kChunkBytes, &tmQ, q_full(sq), c * 64,
+                                            t * kTile, h, it.b, pol);
+                            arm(sq, ph_q);
+                            if (!(ok = w.wait(o_empty(so), (ph_o & 1u) ^ 1u, kDevErrProducerEmpty) &&
+                                       w.wait(rows_empty(so), (ph_o & 1u) ^ 1u, kDevErrProducerEmpty)))
+                                break;
+                            mbar_arrive_expect_tx(o_full(so), Cfg::TILE_BYTES + 1024);
+#pragma unroll
+                            for (int c = 0; c < DCH; ++c)
+                                tma_load_4d(sb + Cfg::OFF_O + so * Cfg::TILE_BYTES + c * kChunkBytes, &tmO, o_full(so), c * 64,
+                                            t * kTile, h, it.b, pol);
+                            bulk_load(sb + Cfg::OFF_ROWS + so * 1024, p.offset + row0 + t * kTile, 512, o_full(so));
+                            bulk_load(sb + Cfg::OFF_ROWS + so * 1024 + 512, p.neg_delta + row0 + t * kTile, 512, o_full(so));
+                            arm(3 + so, ph_o);
+                        }
+                    }
+                }
+                if (ok && (ok = w.wait(clc, n_clc & 1u, kDevErrProducerEmpty))) {
+                    asked = false;
+                    item = clc_taken(sb + Cfg::OFF_CLC);
+                }
+            }
+            ++n_clc;
+            if (!__all_sync(0xffffffffu, ok)) break;
+            item = __shfl_sync(0xffffffffu, item, 0);
+        }
+        if (lane == 0) {   // every copy and answer under way must land before the CTA may exit
+            if (asked) w.drain(clc, (n_clc - 1) & 1u);
+            for (int i = 0; i < 6; ++i)
+                if (armed & (1u << i)) w.drain(i < 3 ? q_full(i) : (i < 5 ? o_full(i - 3) : kv_full), (parity >> i) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            uint32_t n_box = 0, n_item = 0, n = 0;
+            bool ok = true;
+            const uint32_t k_s = sb + Cfg::OFF_K, v_s = sb + Cfg::OFF_V;
+            while (ok) {
+                const uint32_t box = n_box & 1u;
+                if (!w.wait(item_pub(box), (n_box >> 1) & 1u, kDevErrMmaFull)) break;
+                const Item it = read_item(box);
+                mbar_arrive(item_read(box));
+                ++n_box;
+                if (it.b < 0) break;
+                const int steps = (it.t1 - it.t0) * mk.group;
+                if (steps <= 0) continue;
+                if (!w.wait(kv_full, n_item & 1u, kDevErrMmaFull)) break;
+                ++n_item;
+                // dK += dS^T(m) Q(m), once dS^T(m) is written; the step's Q and row values are then free
+                auto issue_dk = [&](uint32_t m, bool first) {
+                    if (!w.wait(ds_full, m & 1u, kDevErrMmaFull)) return false;
+                    tcgen05_fence_after();
+                    mma_overlay(tmem_base + Cfg::T_DK, tmem_base + Cfg::T_DP, sb + Cfg::OFF_Q + (m % NQ) * Cfg::TILE_BYTES,
+                                Cfg::IDESC_ACC, !first);
+                    mma_commit(q_empty((int)(m % NQ)));
+                    mma_commit(rows_empty((int)(m % NO)));
+                    return true;
+                };
+                for (int i = 0; i < steps; ++i, ++n) {
+                    const int sq = (int)(n % NQ), so = (int)(n % NO);
+                    if (!(ok = w.wait(q_full(sq), (n / NQ) & 1u, kDevErrMmaFull))) break;
+                    tcgen05_fence_after();
+                    mma_tiles<D>(tmem_base + Cfg::T_S, k_s, sb + Cfg::OFF_Q + sq * Cfg::TILE_BYTES, Cfg::IDESC_S);
+                    mma_commit(s_full);
+                    if (i > 0 && !(ok = issue_dk(n - 1, i == 1))) break;
+                    if (!(ok = w.wait(o_full(so), (n / NO) & 1u, kDevErrMmaFull))) break;
+                    tcgen05_fence_after();
+                    const uint32_t o_s = sb + Cfg::OFF_O + so * Cfg::TILE_BYTES;
+                    mma_tiles<D>(tmem_base + Cfg::T_DP, v_s, o_s, Cfg::IDESC_S);
+                    mma_commit(dp_full);
+                    if (!(ok = w.wait(p_full, n & 1u, kDevErrMmaFull))) break;
+                    tcgen05_fence_after();
+                    mma_overlay(tmem_base + Cfg::T_DV, tmem_base + Cfg::T_S, o_s, Cfg::IDESC_ACC, i > 0);
+                    mma_commit(o_empty(so));
+                }
+                if (!ok || !(ok = issue_dk(n - 1, steps == 1))) break;
+                mma_commit(kv_empty);
+                mma_commit(done);
+            }
+            mma_commit(drain);
+            w.drain(drain, 0);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ P, dS and the output (warps 2-9)
+        const int half = (warp - 2) >> 2;                // query columns 64 half .. + 63
+        const int quad = warp & 3;
+        const int r = quad * 32 + lane;                  // key of the tile
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
+        const uint32_t s_col = lane_base + Cfg::T_S + half * 64, dp_col = lane_base + Cfg::T_DP + half * 64;
+        const float shift = ds_shift<T>(p.norms), ds_mul = exp2f(shift);
+        uint32_t n_box = 0, n = 0, n_done = 0;
+        bool ok = true;
+        while (ok) {
+            const uint32_t box = n_box & 1u;
+            if (!__all_sync(0xffffffffu, w.wait(item_pub(box), (n_box >> 1) & 1u, kDevErrEpilogueFull))) break;
+            const Item it = read_item(box);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(item_read(box));
+            ++n_box;
+            if (it.b < 0) break;
+            const int j = it.k0 + r;
+            const int* los = p.lo + (long long)it.b * p.Sp;
+            const int* his = p.hi + (long long)it.b * p.Sp;
+            for (int h = it.hk * mk.group; ok && h < (it.hk + 1) * mk.group; ++h) {
+                const float slope2 = Cfg::MODE != kScorePlain && p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
+                for (int t = it.t0; t < it.t1; ++t, ++n) {
+                    const int i0 = t * kTile + half * 64;
+                    // every query of the tile sees every key of the tile (intervals are ordered)
+                    const bool masked = __ldg(los + t * kTile + kTile - 1) > it.k0 || __ldg(his + t * kTile) < it.k0 + kTile;
+                    if (!__all_sync(0xffffffffu, w.wait(o_full((int)(n % NO)), (n / NO) & 1u, kDevErrEpilogueFull) &&
+                                                     w.wait(s_full, n & 1u, kDevErrEpilogueFull))) {
+                        ok = false;
+                        break;
+                    }
+                    tcgen05_fence_after();
+                    const float* rows = reinterpret_cast<const float*>(smem + Cfg::OFF_ROWS + (n % NO) * 1024) + half * 64;
+                    const float base = (float)(j - mk.offset - i0);
+                    uint32_t w0[32], w1[32], see0 = 0xffffffffu, see1 = 0xffffffffu;
+                    tmem_ld_32x32b_x32(s_col, w0);
+                    tmem_ld_32x32b_x32(s_col + 32, w1);
+                    if (masked) {
+                        see0 = see1 = 0u;
+#pragma unroll 8
+                        for (int i = 0; i < 32; ++i) {
+                            see0 |= (uint32_t)(j >= __ldg(los + i0 + i) && j < __ldg(his + i0 + i)) << i;
+                            see1 |= (uint32_t)(j >= __ldg(los + i0 + 32 + i) && j < __ldg(his + i0 + 32 + i)) << i;
+                        }
+                    }
+                    tmem_ld_wait(w0);
+                    reg_tie(w1);
+                    auto p_chunk = [&](uint32_t (&rr)[32], int c, uint32_t see) {
+                        uint32_t packed[16];
+                        weights_chunk<T, Cfg::MODE, true>(rr, p.score, slope2, base - (float)(c * 32),
+                                                          [&](int i) { return *reinterpret_cast<const float2*>(rows + c * 32 + i); },
+                                                          packed);
+                        if (masked) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(see >> i & 1u)) {
+                                    rr[i] = 0u;
+                                    packed[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+                                }
+                        }
+                        tmem_st_32x32b_x16(s_col + c * 16, packed);
+                        if (!Elem<T>::bf16) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) rr[i] = __float_as_uint(__uint_as_float(rr[i]) * ds_mul);
+                        }
+                    };
+                    p_chunk(w0, 0, see0);
+                    p_chunk(w1, 1, see1);
+                    tmem_st_wait();
+                    tcgen05_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full);
+                    if (!__all_sync(0xffffffffu, w.wait(dp_full, n & 1u, kDevErrEpilogueFull))) {
+                        ok = false;
+                        break;
+                    }
+                    tcgen05_fence_after();
+                    auto ds_chunk = [&](const uint32_t (&ww)[32], int c, uint32_t see) {
+                        uint32_t dp[32], packed[16];
+                        tmem_ld_32x32b_x32(dp_col + c * 32, dp);
+                        tmem_ld_wait(dp);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 nd = *reinterpret_cast<const float2*>(rows + 128 + c * 32 + i);
+                            float d0 = __uint_as_float(dp[i]), d1 = __uint_as_float(dp[i + 1]);
+                            fadd2(d0, d1, nd.x, nd.y);
+                            fmul2(d0, d1, d0, d1, __uint_as_float(ww[i]), __uint_as_float(ww[i + 1]));
+                            packed[i / 2] = Elem<T>::pack(d0, d1);
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(see >> i & 1u)) packed[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+                        }
+                        // columns 0-15 of this half hold dP values of chunk 0 only: read above
+                        tmem_st_32x32b_x16(dp_col + c * 16, packed);
+                    };
+                    ds_chunk(w0, 0, see0);
+                    ds_chunk(w1, 1, see1);
+                    tmem_st_wait();
+                    tcgen05_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ds_full);
+                }
+            }
+            if (!ok) break;
+            const bool none = it.t0 >= it.t1;
+            if (!none) {
+                ok = __all_sync(0xffffffffu, w.wait(done, n_done & 1u, kDevErrEpilogueFull));
+                ++n_done;
+                tcgen05_fence_after();
+                if (!ok) break;
+            }
+            // half 0 writes dV's rows, half 1 dK's.  The next item's products overwrite the accumulators
+            // only after this warp's next P and dS.
+            const Strided& out = half == 0 ? p.dV : p.dK;
+            const float factor = half == 0 ? exp2f(-kPShift<T>) : p.score.scale * exp2f(-kPShift<T> - shift);
+            T* row = static_cast<T*>(out.data) + it.b * out.batch + it.hk * out.head + (long long)j * out.row;
+            const bool bad = store_accumulator<T, D>(lane_base + (half == 0 ? Cfg::T_DV : Cfg::T_DK), factor, none, j < mk.Skv, row);
+            tcgen05_fence_before();
+            __syncwarp();
+            for (uint32_t again = __ballot_sync(0xffffffffu, bad); again; again &= again - 1)
+                row_dkv<T, D>(p, it.b, it.hk, it.k0 + quad * 32 + __ffs(again) - 1, half == 1, lane);
+        }
+    }
+
+    tcgen05_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tcgen05_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dQ
+// ---------------------------------------------------------------------------
+// A work item is 128 queries of one head; its steps are the key tiles they see.  Per step
+//     S = Q K^T,  dP = dO V^T,  dS over dP's columns,  dQ += dS K
+// S has one region (the arithmetic takes it into registers at once) and dP two, so that S(n+1) and
+// dP(n+1) run on the tensor core while dS(n) is computed; dQ(n) follows.  K is read by S(n) and,
+// after that, by dQ(n): three ring entries, two for V.
+template <class T_, int D_, int MODE_>
+struct DqCfg {
+    using T = T_;
+    static constexpr int D = D_, MODE = MODE_;
+    static constexpr int DCH = D / 64;
+    static constexpr int TILE_BYTES = kTile * D * 2;
+    static constexpr int NK = 3, NV = 2;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_O = OFF_Q + TILE_BYTES;
+    static constexpr int OFF_K = OFF_O + TILE_BYTES;
+    static constexpr int OFF_V = OFF_K + NK * TILE_BYTES;
+    static constexpr int OFF_BAR = OFF_V + NV * TILE_BYTES;
+    static constexpr int NUM_BARS = 26;
+    static constexpr int OFF_CLC = OFF_BAR + NUM_BARS * 8;
+    static constexpr int OFF_ITEM = OFF_CLC + 16;
+    static constexpr int OFF_MISC = OFF_ITEM + 64;
+    static constexpr int SMEM_BYTES = OFF_MISC + 16;
+    static constexpr uint32_t T_S = 0, T_DP = 128, T_DQ = 384;
+    static constexpr uint32_t IDESC_S = idesc_16_f32(Elem<T>::bf16, kTile, kTile, false, false);
+    static constexpr uint32_t IDESC_ACC = idesc_16_f32(Elem<T>::bf16, kTile, D, false, true);
+    static_assert(SMEM_BYTES <= 232448 && OFF_CLC % 16 == 0, "shared memory");
+};
+
+template <class Cfg>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    gsr_masked_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                         const __grid_constant__ MaskedBwdParams p) {
+    using T = typename Cfg::T;
+    constexpr int D = Cfg::D, DCH = Cfg::DCH, NK = Cfg::NK, NV = Cfg::NV;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0) atomicCAS(p.err, 0, kDevErrKernelMaskedDq | kDevErrLayout);
+        return;
+    }
+    const uint32_t sb = smem_u32(smem);
+    auto bar = [&](int i) { return sb + Cfg::OFF_BAR + 8u * i; };
+    auto k_full = [&](int s) { return bar(0 + s); };
+    auto k_empty = [&](int s) { return bar(3 + s); };
+    auto v_full = [&](int s) { return bar(6 + s); };
+    auto v_empty = [&](int s) { return bar(8 + s); };
+    auto dp_full = [&](int s) { return bar(10 + s); };
+    auto item_pub = [&](int i) { return bar(12 + i); };
+    auto item_read = [&](int i) { return bar(14 + i); };
+    const uint32_t q_full = bar(16), q_empty = bar(17), s_full = bar(18), s_read = bar(19), ds_full = bar(20),
+                   done = bar(21), clc = bar(22), drain = bar(23);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_MISC + 4);
+    volatile int* item_box = reinterpret_cast<volatile int*>(smem + Cfg::OFF_ITEM);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const MaskArgs& mk = p.mask;
+
+    struct Item {
+        int b, h, q_base, t0, t1;
+    };
+    auto read_item = [&](int box) {
+        volatile int* v = item_box + 8 * box;
+        return Item{v[0], v[1], v[2], v[3], v[4]};
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NK; ++s) {
+            mbar_init(k_full(s), 1);
+            mbar_init(k_empty(s), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(v_full(s), 1);
+            mbar_init(v_empty(s), 1);
+            mbar_init(dp_full(s), 1);
+            mbar_init(item_pub(s), 1);
+            mbar_init(item_read(s), 1 + kBwdMathWarps);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(s_full, 1);
+        mbar_init(s_read, kBwdMathWarps);
+        mbar_init(ds_full, kBwdMathWarps);
+        mbar_init(done, 1);
+        mbar_init(clc, 1);
+        mbar_init(drain, 1);
+        *abort_flag = 0u;
+        fence_mbarrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+        tma_prefetch_desc(&tmO);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish_alloc_permit();
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const Waiter w{p.err, p.timeout_ns, abort_flag, kDevErrKernelMaskedDq};
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ items + TMA producer
+        if (lane == 0) {
+            const uint64_t pol = l2_policy_evict_last();
+            const int n_qb = (mk.Sq + kTile - 1) / kTile;
+            uint32_t n_pub = 0, n_item = 0, n_clc = 0, n = 0;
+            uint32_t armed = 0, parity = 0;              // k_full 0-2, v_full 3-4, q_full 5
+            bool drop = (p.test_flags & kTestDropFirstLoad) && blockIdx.x == 0;
+            bool asked = false, ok = true;
+            int item = blockIdx.x;
+            auto arm = [&](int i, uint32_t ph) {
+                armed |= 1u << i;
+                parity = (parity & ~(1u << i)) | (ph & 1u) << i;
+            };
+            while (ok) {
+                Item it{-1, 0, 0, 0, 0};
+                if (item >= 0) {
+                    const int per_group = p.q_head_group * n_qb, grp = item / per_group, r_in = item - grp * per_group;
+                    const int gsz = min(mk.B * mk.Hq - grp * p.q_head_group, p.q_head_group);
+                    const int bh = grp * p.q_head_group + r_in % gsz;
+                    it.b = bh / mk.Hq;
+                    it.h = bh - it.b * mk.Hq;
+                    it.q_base = (n_qb - 1 - r_in / gsz) * kTile;
+                    const int lo = __ldg(p.lo + (long long)it.b * p.Sp + it.q_base);
+                    const int hi = __ldg(p.hi + (long long)it.b * p.Sp + min(it.q_base + kTile, mk.Sq) - 1);
+                    it.t0 = lo / kTile;
+                    it.t1 = hi > lo ? (hi + kTile - 1) / kTile : it.t0;
+                }
+                const uint32_t box = n_pub & 1u;
+                if (!(ok = w.wait(item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty))) break;
+                volatile int* v = item_box + 8 * box;
+                v[0] = it.b;
+                v[1] = it.h;
+                v[2] = it.q_base;
+                v[3] = it.t0;
+                v[4] = it.t1;
+                mbar_arrive(item_pub(box));
+                ++n_pub;
+                if (item < 0) break;
+                fence_proxy_async_smem();
+                mbar_arrive_expect_tx(clc, 16);
+                clc_try_cancel(sb + Cfg::OFF_CLC, clc);
+                asked = true;
+                ++n_clc;
+                if (it.t0 < it.t1) {
+                    if (!(ok = w.wait(q_empty, (n_item & 1u) ^ 1u, kDevErrProducerEmpty))) break;
+                    if (!drop) {
+                        mbar_arrive_expect_tx(q_full, 2 * Cfg::TILE_BYTES);
+#pragma unroll
+                        for (int c = 0; c < DCH; ++c) {
+                            tma_load_4d(sb + Cfg::OFF_Q + c * kChunkBytes, &tmQ, q_full, c * 64, it.q_base, it.h, it.b, pol);
+                            tma_load_4d(sb + Cfg::OFF_O + c * kChunkBytes, &tmO, q_full, c * 64, it.q_base, it.h, it.b, pol);
+                        }
+                        arm(5, n_item);
+                    }
+                    drop = false;                        // test hook: the first Q and dO are never loaded
+                    ++n_item;
+                    const int hk = it.h / mk.group;
+                    for (int t = it.t0; t < it.t1; ++t, ++n) {
+                        const int sk = (int)(n % NK), sv = (int)(n % NV);
+                        if (!(ok = w.wait(k_empty(sk), ((n / NK) & 1u) ^ 1u, kDevErrProducerEmpty))) break;
+                        mbar_arrive_expect_tx(k_full(sk), Cfg::TILE_BYTES);
+#pragma unroll
+                        for (int c = 0; c < DCH; ++c)
+                            tma_load_4d(sb + Cfg::OFF_K + sk * Cfg::TILE_BYTES + c * kChunkBytes, &tmK, k_full(sk), c * 64, t * kTile,
+                                        hk, it.b, pol);
+                        arm(sk, n / NK);
+                        if (!(ok = w.wait(v_empty(sv), ((n / NV) & 1u) ^ 1u, kDevErrProducerEmpty))) break;
+                        mbar_arrive_expect_tx(v_full(sv), Cfg::TILE_BYTES);
+#pragma unroll
+                        for (int c = 0; c < DCH; ++c)
+                            tma_load_4d(sb + Cfg::OFF_V + sv * Cfg::TILE_BYTES + c * kChunkBytes, &tmV, v_full(sv), c * 64, t * kTile,
+                                        hk, it.b, pol);
+                        arm(3 + sv, n / NV);
+                    }
+                    if (!ok) break;
+                }
+                if (!(ok = w.wait(clc, (n_clc - 1) & 1u, kDevErrProducerEmpty))) break;
+                asked = false;
+                item = clc_taken(sb + Cfg::OFF_CLC);
+            }
+            if (asked) w.drain(clc, (n_clc - 1) & 1u);
+            for (int i = 0; i < 6; ++i)
+                if (armed & (1u << i)) w.drain(i < 3 ? k_full(i) : (i < 5 ? v_full(i - 3) : q_full), (parity >> i) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            uint32_t n_box = 0, n_item = 0, n = 0;
+            bool ok = true;
+            const uint32_t q_s = sb + Cfg::OFF_Q, o_s = sb + Cfg::OFF_O;
+            // S(m) and dP(m), once their operands have landed and S(m-1) is in registers
+            auto issue_scores = [&](uint32_t m, bool first) {
+                if (!w.wait(k_full((int)(m % NK)), (m / NK) & 1u, kDevErrMmaFull)) return false;
+                if (!first && !w.wait(s_read, (m - 1) & 1u, kDevErrMmaFull)) return false;
+                tcgen05_fence_after();
+                mma_tiles<D>(tmem_base + Cfg::T_S, q_s, sb + Cfg::OFF_K + (m % NK) * Cfg::TILE_BYTES, Cfg::IDESC_S);
+                mma_commit(s_full);
+                if (!w.wait(v_full((int)(m % NV)), (m / NV) & 1u, kDevErrMmaFull)) return false;
+                tcgen05_fence_after();
+                mma_tiles<D>(tmem_base + Cfg::T_DP + (m & 1u) * 128, o_s, sb + Cfg::OFF_V + (m % NV) * Cfg::TILE_BYTES, Cfg::IDESC_S);
+                mma_commit(dp_full((int)(m & 1u)));
+                mma_commit(v_empty((int)(m % NV)));
+                return true;
+            };
+            while (ok) {
+                const uint32_t box = n_box & 1u;
+                if (!w.wait(item_pub(box), (n_box >> 1) & 1u, kDevErrMmaFull)) break;
+                const Item it = read_item(box);
+                mbar_arrive(item_read(box));
+                ++n_box;
+                if (it.b < 0) break;
+                const int steps = it.t1 - it.t0;
+                if (steps <= 0) continue;
+                if (!w.wait(q_full, n_item & 1u, kDevErrMmaFull)) break;
+                ++n_item;
+                // the step before an item's first has been read too: its dS was waited for
+                if (!(ok = issue_scores(n, n == 0))) break;
+                for (int i = 0; i < steps; ++i, ++n) {
+                    if (i + 1 < steps && !(ok = issue_scores(n + 1, false))) break;
+                    if (!(ok = w.wait(ds_full, n & 1u, kDevErrMmaFull))) break;
+                    tcgen05_fence_after();
+                    mma_overlay(tmem_base + Cfg::T_DQ, tmem_base + Cfg::T_DP + (n & 1u) * 128,
+                                sb + Cfg::OFF_K + (n % NK) * Cfg::TILE_BYTES, Cfg::IDESC_ACC, i > 0);
+                    mma_commit(k_empty((int)(n % NK)));
+                }
+                if (!ok) break;
+                mma_commit(q_empty);
+                mma_commit(done);
+            }
+            mma_commit(drain);
+            w.drain(drain, 0);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ dS and the output (warps 2-9)
+        const int half = (warp - 2) >> 2;                // key columns 64 half .. + 63
+        const int quad = warp & 3;
+        const int r = quad * 32 + lane;                  // query of the tile
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
+        const uint32_t s_col = lane_base + Cfg::T_S + half * 64;
+        const float shift = ds_shift<T>(p.norms);
+        uint32_t n_box = 0, n = 0, n_done = 0;
+        bool ok = true;
+        while (ok) {
+            const uint32_t box = n_box & 1u;
+            if (!__all_sync(0xffffffffu, w.wait(item_pub(box), (n_box >> 1) & 1u, kDevErrEpilogueFull))) break;
+            const Item it = read_item(box);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(item_read(box));
+            ++n_box;
+            if (it.b < 0) break;
+            const int qi = it.q_base + r;                // below Sp
+            const long long row = ((long long)it.b * mk.Hq + it.h) * p.Sp + qi;
+            const int lo = p.lo[(long long)it.b * p.Sp + qi], hi = p.hi[(long long)it.b * p.Sp + qi];
+            const float off = p.offset[row] + shift, neg_delta = p.neg_delta[row];
+            const float slope2 = Cfg::MODE != kScorePlain && p.score.slopes ? __ldg(p.score.slopes + it.h) * kLog2e : 0.0f;
+            for (int t = it.t0; t < it.t1; ++t, ++n) {
+                const int k0 = t * kTile + half * 64;
+                const bool masked = k0 < lo || k0 + 64 > hi;
+                if (!__all_sync(0xffffffffu, w.wait(s_full, n & 1u, kDevErrEpilogueFull))) {
+                    ok = false;
+                    break;
+                }
+                tcgen05_fence_after();
+                uint32_t w0[32], w1[32], none[16];
+                tmem_ld_32x32b_x32(s_col, w0);
+                tmem_ld_32x32b_x32(s_col + 32, w1);
+                tmem_ld_wait(w0);
+                reg_tie(w1);
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_read);
+                const float base = (float)(qi + mk.offset - k0);
+                auto offset = [&](int) { return make_float2(off, off); };
+                weights_chunk<T, Cfg::MODE, false>(w0, p.score, slope2, base, offset, none);
+                weights_chunk<T, Cfg::MODE, false>(w1, p.score, slope2, base - 32.0f, offset, none);
+                const int buf = (int)(n & 1u);
+                if (!__all_sync(0xffffffffu, w.wait(dp_full(buf), (n >> 1) & 1u, kDevErrEpilogueFull))) {
+                    ok = false;
+                    break;
+                }
+                tcgen05_fence_after();
+                const uint32_t dp_col = lane_base + Cfg::T_DP + buf * 128 + half * 64;
+                auto ds_chunk = [&](const uint32_t (&ww)[32], int c) {
+                    uint32_t dp[32], packed[16];
+                    tmem_ld_32x32b_x32(dp_col + c * 32, dp);
+                    tmem_ld_wait(dp);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float d0 = __uint_as_float(dp[i]), d1 = __uint_as_float(dp[i + 1]);
+                        fadd2(d0, d1, neg_delta, neg_delta);
+                        fmul2(d0, d1, d0, d1, __uint_as_float(ww[i]), __uint_as_float(ww[i + 1]));
+                        if (masked) {
+                            if (c * 32 + i < lo - k0 || c * 32 + i >= hi - k0) d0 = 0.0f;
+                            if (c * 32 + i + 1 < lo - k0 || c * 32 + i + 1 >= hi - k0) d1 = 0.0f;
+                        }
+                        packed[i / 2] = Elem<T>::pack(d0, d1);
+                    }
+                    tmem_st_32x32b_x16(dp_col + c * 16, packed);
+                };
+                ds_chunk(w0, 0);
+                ds_chunk(w1, 1);
+                tmem_st_wait();
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ds_full);
+            }
+            if (!ok) break;
+            const bool none = it.t0 >= it.t1;
+            if (!none) {
+                ok = __all_sync(0xffffffffu, w.wait(done, n_done & 1u, kDevErrEpilogueFull));
+                ++n_done;
+                tcgen05_fence_after();
+                if (!ok) break;
+            }
+            // half 0 writes the rows; the next item's products overwrite the accumulator only after its
+            // next dS
+            const bool empty = none || lo >= hi;
+            T* out = static_cast<T*>(p.dQ.data) + it.b * p.dQ.batch + it.h * p.dQ.head + (long long)qi * p.dQ.row;
+            const float factor = p.score.scale * exp2f(-kPShift<T> - shift);
+            if (half == 0) {
+                const bool bad = store_accumulator<T, D>(lane_base + Cfg::T_DQ, factor, empty, qi < mk.Sq, out);
+                __syncwarp();
+                for (uint32_t again = __ballot_sync(0xffffffffu, bad); again; again &= again - 1)
+                    row_dq<T, D>(p, it.b, it.h, it.q_base + quad * 32 + __ffs(again) - 1, lane);
+            }
+            tcgen05_fence_before();
+        }
+    }
+
+    tcgen05_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tcgen05_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+template <class Cfg>
+cudaError_t launch_dkv(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream) {
+    static std::atomic<uint64_t> attr_done{0};
+    const cudaError_t e = allow_smem(gsr_masked_dkv_kernel<Cfg>, Cfg::SMEM_BYTES, attr_done);
+    if (e != cudaSuccess) return e;
+    const int items = (p.mask.Skv + kTile - 1) / kTile * p.mask.B * p.mask.Hkv;
+    gsr_masked_dkv_kernel<Cfg><<<(unsigned)items, kBwdThreads, Cfg::SMEM_BYTES, stream>>>(tm.q, tm.k, tm.v, tm.dO, p);
+    return cudaGetLastError();
+}
+
+template <class Cfg>
+cudaError_t launch_dq(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream) {
+    static std::atomic<uint64_t> attr_done{0};
+    const cudaError_t e = allow_smem(gsr_masked_dq_kernel<Cfg>, Cfg::SMEM_BYTES, attr_done);
+    if (e != cudaSuccess) return e;
+    const int items = p.Sp / kTile * p.mask.B * p.mask.Hq;
+    gsr_masked_dq_kernel<Cfg><<<(unsigned)items, kBwdThreads, Cfg::SMEM_BYTES, stream>>>(tm.q, tm.k, tm.v, tm.dO, p);
+    return cudaGetLastError();
+}
+
+template <class T, int D, int MODE>
+cudaError_t launch_bwd_mode(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream) {
+    const cudaError_t e = launch_dkv<DkvCfg<T, D, MODE>>(tm, p, stream);
+    return e == cudaSuccess ? launch_dq<DqCfg<T, D, MODE>>(tm, p, stream) : e;
+}
+
+template <class T, int D>
+cudaError_t launch_bwd_type(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream) {
+    const MaskArgs& mk = p.mask;
+    const long long q_rows = (long long)mk.B * mk.Hq * mk.Sq, k_rows = (long long)mk.B * mk.Hkv * mk.Skv;
+    if (q_rows == 0 || k_rows == 0) {                    // no pairs: every gradient is zero
+        if (k_rows > 0) {
+            const unsigned grid = (unsigned)((k_rows + 7) / 8);
+            gsr_masked_zero_kernel<T, D><<<grid, 256, 0, stream>>>(p.dK, mk.Hkv, mk.Skv, k_rows);
+            gsr_masked_zero_kernel<T, D><<<grid, 256, 0, stream>>>(p.dV, mk.Hkv, mk.Skv, k_rows);
+        }
+        if (q_rows > 0)
+            gsr_masked_zero_kernel<T, D><<<(unsigned)((q_rows + 7) / 8), 256, 0, stream>>>(p.dQ, mk.Hq, mk.Sq, q_rows);
+        return cudaGetLastError();
+    }
+    long long rows = (long long)mk.B * mk.Hq * p.Sp;
+    if (!Elem<T>::bf16) {
+        const cudaError_t e = cudaMemsetAsync(p.norms, 0, 2 * sizeof(unsigned), stream);
+        if (e != cudaSuccess) return e;
+        rows += k_rows;
+    }
+    gsr_masked_bwd_rows_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (p.score.cap_in != 0.0f) return launch_bwd_mode<T, D, kScoreCap>(tm, p, stream);
+    if (p.score.slopes) return launch_bwd_mode<T, D, kScoreBias>(tm, p, stream);
+    return launch_bwd_mode<T, D, kScorePlain>(tm, p, stream);
+}
+
+}  // namespace gsr

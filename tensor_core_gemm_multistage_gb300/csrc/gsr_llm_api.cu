@@ -124,16 +124,25 @@ gsr_status encode(CUtensorMap* map, const Strided& t, int32_t dtype, int64_t bat
     return r == CUDA_SUCCESS ? GSR_OK : gsr::host::fail_encode(r);
 }
 
+// How many heads' items are taken together.  Causal items run longest first across as many heads
+// as keep what they share (`bytes` per `group` heads) within ~48 MiB of L2; without a causal mask
+// every item of a head is equally long and one group's heads run together.
+int heads_in_l2(int causal, int64_t bytes, int64_t group, int64_t heads) {
+    int64_t n = causal ? ((int64_t)48 << 20) / (bytes > 0 ? bytes : 1) * group : group;
+    if (n < 1) n = 1;
+    return (int)(n < heads ? n : heads);
+}
+
 // Layout of the backward pass's workspace, 256-byte pieces.
 struct BwdLayout {
-    int64_t sp, lse2, delta, lo, hi, total;
+    int64_t sp, offset, delta, lo, hi, total;
 };
 BwdLayout bwd_layout(const gsr_attention_desc* d) {
     auto piece = [](int64_t bytes) { return (bytes + 255) / 256 * 256; };
     BwdLayout w;
     w.sp = (d->seq_q + 127) / 128 * 128;
-    w.lse2 = 256;                                                     // the norms come first
-    w.delta = w.lse2 + piece(4 * d->batch * d->heads_q * w.sp);
+    w.offset = 256;                                                     // the norms come first
+    w.delta = w.offset + piece(4 * d->batch * d->heads_q * w.sp);
     w.lo = w.delta + piece(4 * d->batch * d->heads_q * w.sp);
     w.hi = w.lo + piece(4 * d->batch * w.sp);
     w.total = w.hi + piece(4 * d->batch * w.sp);
@@ -181,13 +190,7 @@ gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor
                     (s = encode(&tm.v, p.V, desc->dtype, B, Hkv, Skv, D, 128)) != GSR_OK))
         return s;
     p.num_items = (int)((Sq + 255) / 256 * B * Hq);
-    // Causal items run longest first across as many heads as keep their K and V within ~48 MiB of
-    // L2; without a mask every item is equally long and one group's heads run together.
-    const int64_t kv_bytes = Skv * D * 4;
-    int64_t heads = desc->causal ? ((int64_t)48 << 20) / (kv_bytes > 0 ? kv_bytes : 1) * p.mask.group : 1;
-    if (heads < 1) heads = 1;
-    if (heads > B * Hq) heads = B * Hq;
-    p.head_group = (int)heads;
+    p.head_group = heads_in_l2(desc->causal, Skv * D * 4, p.mask.group, B * Hq);
     const cudaError_t e = desc->dtype == GSR_BF16 ? gsr::launch_masked_fwd_bf16(tm, p, (int)D, st)
                                                   : gsr::launch_masked_fwd_f16(tm, p, (int)D, st);
     return e == cudaSuccess ? GSR_OK : gsr::host::fail(e);
@@ -245,13 +248,23 @@ gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor
     char* base = static_cast<char*>(workspace);
     p.norms = reinterpret_cast<unsigned*>(base);
     p.Sp = (int)w.sp;
-    p.lse2 = reinterpret_cast<float*>(base + w.lse2);
-    p.delta = reinterpret_cast<float*>(base + w.delta);
+    p.offset = reinterpret_cast<float*>(base + w.offset);
+    p.neg_delta = reinterpret_cast<float*>(base + w.delta);
     p.lo = reinterpret_cast<int*>(base + w.lo);
     p.hi = reinterpret_cast<int*>(base + w.hi);
     p.timeout_ns = gsr::host::wait_timeout_ns();
     p.test_flags = gsr::host::test_flags();
-    const cudaError_t e = gsr::launch_masked_bwd(p, (int)D, desc->dtype == GSR_BF16, st);
+    gsr::MaskedBwdMaps tm;
+    if (!no_q && !no_k && ((s = encode(&tm.q, p.Q, desc->dtype, B, Hq, Sq, D, 128)) != GSR_OK ||
+                           (s = encode(&tm.k, p.K, desc->dtype, B, Hkv, Skv, D, 128)) != GSR_OK ||
+                           (s = encode(&tm.v, p.V, desc->dtype, B, Hkv, Skv, D, 128)) != GSR_OK ||
+                           (s = encode(&tm.dO, p.dO, desc->dtype, B, Hq, Sq, D, 128)) != GSR_OK))
+        return s;
+    p.q_head_group = heads_in_l2(desc->causal, Skv * D * 4, p.mask.group, B * Hq);
+    p.kv_head_group = heads_in_l2(desc->causal, Sq * D * 4 * p.mask.group, 1, B * Hkv);
+    const bool bf16 = desc->dtype == GSR_BF16;
+    const cudaError_t e = D == 64 ? (bf16 ? gsr::launch_masked_bwd_bf16_64(tm, p, st) : gsr::launch_masked_bwd_f16_64(tm, p, st))
+                                  : (bf16 ? gsr::launch_masked_bwd_bf16_128(tm, p, st) : gsr::launch_masked_bwd_f16_128(tm, p, st));
     return e == cudaSuccess ? GSR_OK : gsr::host::fail(e);
 }
 

@@ -61,11 +61,12 @@ struct MaskedBwdParams {
     Strided dO, Q, K, V, O, dQ, dK, dV;
     const float* lse;           // (B, Hq, Sq)
     int Sp;                     // Sq rounded up to a multiple of 128
-    float* lse2;                // (B, Hq, Sp): lse log2(e); +inf for rows without keys and padding
-    float* delta;               // (B, Hq, Sp): rowsum(dO * O)
+    float* offset;              // (B, Hq, Sp): P's power of two less lse log2(e); -inf for rows without keys and padding
+    float* neg_delta;           // (B, Hq, Sp): -rowsum(dO * O)
     int* lo;                    // (B, Sp): each query's interval
     int* hi;
-    unsigned* norms;            // [0] max |dO_i|^2, [1] max |V_j|^2, as the bits of a float
+    unsigned* norms;            // [0] max |dO_i|^2, [1] max |V_j|^2, as the bits of a float (fp16 only)
+    int q_head_group, kv_head_group;   // item order of dQ, of dK and dV: heads taken together
     int* err;
     uint64_t timeout_ns;
     uint32_t test_flags;
@@ -97,7 +98,16 @@ struct MaskedFwdMaps {
 // Skv == 0: no maps are read, O = 0 and lse = -inf.
 cudaError_t launch_masked_fwd_f16(const MaskedFwdMaps& tm, const MaskedFwdParams& p, int D, cudaStream_t stream);
 cudaError_t launch_masked_fwd_bf16(const MaskedFwdMaps& tm, const MaskedFwdParams& p, int D, cudaStream_t stream);
-cudaError_t launch_masked_bwd(const MaskedBwdParams& p, int D, bool bf16, cudaStream_t stream);
+
+// Tensor maps as MaskedFwdMaps; not read where there are no queries or no keys.
+struct MaskedBwdMaps {
+    CUtensorMap q, k, v, dO;
+};
+cudaError_t launch_masked_bwd_f16_64(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream);
+cudaError_t launch_masked_bwd_f16_128(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream);
+cudaError_t launch_masked_bwd_bf16_64(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream);
+cudaError_t launch_masked_bwd_bf16_128(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream);
+
 cudaError_t launch_tree(const TreeParams& p, bool bf16, cudaStream_t stream);
 
 struct TablesParams {

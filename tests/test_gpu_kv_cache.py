@@ -1,8 +1,9 @@
 """GPU tests of the paged cache: block tables, cache writes, and attention of drafted tokens.
 
 Whole numbers and copies are compared exactly.  Attention's tolerance per element, with u = eps / 2
-of the type: u sum|terms| (probabilities rounded for the second product) + u |want| (the output) +
-2^-13 sum|terms| (fp32 scores, below 2^5 here, and sums), 2^-25 for float16 subnormals.
+of the type: e (1 + u) + u |want|, e = u sum|terms| (probabilities rounded for the second product) +
+2^-13 sum|terms| (fp32 scores, below 2^5 here, and sums); the result before its own rounding is at
+most |want| + e.  2^-25 for float16 subnormals.
 """
 import numpy as np
 import pytest
@@ -157,7 +158,7 @@ class Tree:
         assert np.all(got[~real] == 7.0), "rows of no request were written"
         got, want, terms = got[real], want[real], terms[real]
         assert not np.isnan(got).any()
-        tol = self.u * (terms + np.abs(want)) + 2.0 ** -13 * terms + self.tiny
+        tol = (self.u + 2.0 ** -13) * terms * (1 + self.u) + self.u * np.abs(want) + self.tiny
         assert np.all(np.abs(got - want) <= tol), (np.abs(got - want).max(), (np.abs(got - want) / np.maximum(tol, 1e-30)).max())
         return self
 

@@ -2,12 +2,14 @@
 
 Tolerances, from the arithmetic: with u = eps / 2 of the operands' type, a probability (or dS) is
 rounded once to that type before the matrix product, and the result once at the end, so per element
-    |got - want| <= u sum|terms| + u |want| + small,
-where the sum runs over the rounded factor's terms.  `small` covers fp32: a score is a sum of D
+    |got - want| <= e (1 + u) + u |want|,   e = u sum|terms| + small,
+where the sum runs over the rounded factor's terms (the result before its own rounding is off by at
+most e, so it is at most |want| + e, and its rounding adds u times that).  `small` covers fp32: a score is a sum of D
 products in fp32 (D 2^-24 relative to sum|q k| at worst, scores here below 2^5 in absolute terms)
 and a probability's relative error equals its score's absolute one: 2^-13 of the sum of |terms| is
 above all of it, as is 2^-13 of the terms of dS's own two parts.  In float16 a result below 2^-14
-is subnormal: its rounding is 2^-25 absolute.  lse is fp32 throughout: 2^-14 absolute for scores
+is subnormal: its rounding is 2^-25 absolute.  So are P and dS there, after the powers of two they are
+scaled by: 2^12, and for dS at least 2^14 over 2 max|dO_i| max|V_j|, each error entering once per term.  lse is fp32 throughout: 2^-14 absolute for scores
 below 2^5 and distance biases below 2^9 (2^-24 relative, a few roundings).
 """
 import numpy as np
@@ -55,6 +57,9 @@ class Case:
         self.host = dict(scale=float(np.float32(scale)), cap=float(np.float32(cap)),
                          slopes=None if self.slopes is None else self.slopes.cpu().numpy())
 
+    def tol(self, want, terms, wide):
+        return (self.u * terms + 2.0 ** -13 * wide) * (1 + self.u) + self.u * np.abs(want) + self.tiny
+
     def forward(self):
         self.o = torch.full_like(self.q, float("nan"))
         self.lse = torch.full(self.q.shape[:3], float("nan"), device=DEV)
@@ -75,8 +80,7 @@ class Case:
         want, lse, terms = (t[:, :, rows] for t in llm.masked_attention(self.q, self.k, self.v, self.see, **self.host))
         got = llm.f64(self.o)[:, :, rows]
         assert not np.isnan(got).any(), "unwritten or NaN outputs"
-        assert np.all(np.abs(got - want) <= self.u * (terms + np.abs(want)) + 2.0 ** -13 * terms + self.tiny), \
-            np.abs(got - want).max()
+        assert np.all(np.abs(got - want) <= self.tol(want, terms, terms)), np.abs(got - want).max()
         gl = llm.f64(self.lse)[:, :, rows]
         fin = np.isfinite(lse)
         assert np.array_equal(np.isneginf(gl), ~fin) and not np.isnan(gl).any()
@@ -84,11 +88,13 @@ class Case:
         return self
 
     def check_backward(self, rows=slice(None)):
-        want, terms, wide = llm.masked_attention_bwd(self.do, self.q, self.k, self.v, self.o, self.lse, self.see, **self.host)
-        for name, t, w, a, b in zip(("dQ", "dK", "dV"), self.grads, want, terms, wide):
-            got, w, a, b = (x[:, :, rows] for x in (llm.f64(t), w, a, b))
+        want, terms, wide, plain = llm.masked_attention_bwd(self.do, self.q, self.k, self.v, self.o, self.lse, self.see, **self.host)
+        norm = lambda t: np.sqrt((np.nan_to_num(llm.f64(t), nan=0.0, posinf=0.0, neginf=0.0) ** 2).sum(-1)).max()
+        low = [self.tiny * 2 * norm(self.do) * norm(self.v) * 2.0 ** -14] * 2 + [self.tiny * 2.0 ** -12]
+        for name, t, w, a, b, c, x in zip(("dQ", "dK", "dV"), self.grads, want, terms, wide, plain, low):
+            got, w, a, b, c = (y[:, :, rows] for y in (llm.f64(t), w, a, b, c))
             assert not np.isnan(got).any(), name
-            tol = self.u * (a + np.abs(w)) + 2.0 ** -13 * b + self.tiny
+            tol = self.tol(w, a, b) + x * c
             assert np.all(np.abs(got - w) <= tol), (name, np.abs(got - w).max(), (np.abs(got - w) / tol).max())
         return self
 
@@ -251,7 +257,7 @@ def test_one_query_equals_the_last_row():
     o1, l1 = torch.empty_like(c.q[:, :, -1:]).contiguous(), torch.empty(2, 4, 1, device=DEV)
     gsr.masked_attention_fwd(c.q[:, :, -1:], c.k, c.v, o1, l1, **c.kw)
     _, _, terms = llm.masked_attention(c.q, c.k, c.v, c.see, **c.host)       # each within the bound of check_forward
-    tol = 2 * (c.u * (terms[:, :, -1:] + np.abs(llm.f64(o1))) + 2.0 ** -13 * terms[:, :, -1:] + c.tiny)
+    tol = 2 * c.tol(llm.f64(o1), terms[:, :, -1:], terms[:, :, -1:])
     assert np.all(np.abs(llm.f64(o1) - llm.f64(c.o[:, :, -1:])) <= tol)
     assert torch.all((l1 - c.lse[:, :, -1:]).abs() <= 2.0 ** -13)
 

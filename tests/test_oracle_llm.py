@@ -29,7 +29,7 @@ def test_gradient_against_autograd_and_differences(cap, alibi, docs):
     see = llm.visible(B, S, S, True, bounds, [[2, 1], [0, 2]] if docs else [[3], [0]])
     slopes = np.array([0.5, 0.25, 0.1, 0.05]) if alibi else None
     o, lse, _ = llm.masked_attention(q, k, v, see, 0.0, cap, slopes)
-    (dq, dk, dv), _, _ = llm.masked_attention_bwd(do, q, k, v, o, lse, see, 0.0, cap, slopes)
+    (dq, dk, dv), _, _, _ = llm.masked_attention_bwd(do, q, k, v, o, lse, see, 0.0, cap, slopes)
 
     tq, tk, tv = (torch.tensor(t, requires_grad=True) for t in (q, k, v))
     x = tq @ tk.repeat_interleave(2, 1).transpose(-1, -2) / np.sqrt(D)
