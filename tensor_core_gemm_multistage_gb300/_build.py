@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(OUT_DIR, "libgsr.so")
 SOURCES = ["gsr_api.cu", "gsr_llm_api.cu", "gemm_tiled.cu", "gemm_pair.cu", "gemm_skinny.cu", "attention_fwd.cu",
            "attention_masked_fwd_f16.cu", "attention_masked_fwd_bf16.cu", "attention_masked_bwd_f16_64.cu",
            "attention_masked_bwd_f16_128.cu", "attention_masked_bwd_bf16_64.cu", "attention_masked_bwd_bf16_128.cu",
-           "attention_tree.cu", "kv_cache.cu"]
+           "attention_tree_f16_64.cu", "attention_tree_f16_128.cu", "attention_tree_bf16_64.cu",
+           "attention_tree_bf16_128.cu", "kv_cache.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-I" + INCLUDE, "-I" + CSRC]

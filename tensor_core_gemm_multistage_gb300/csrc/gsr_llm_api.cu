@@ -108,20 +108,28 @@ gsr::ScoreArgs score_args(float softmax_scale, float softcap, const float* slope
     return s;
 }
 
-// Tensor map of a strided operand, box 64 x box_rows, 128-byte swizzle, zero fill outside.
-gsr_status encode(CUtensorMap* map, const Strided& t, int32_t dtype, int64_t batch, int64_t heads, int64_t rows,
-                  int64_t d, uint32_t box_rows) {
+// 4-D tensor map of 16-bit elements, innermost contiguous (strides in elements of the other three),
+// 128-byte swizzle, zero fill outside.
+gsr_status encode_4d(CUtensorMap* map, const void* data, int32_t dtype, const int64_t (&n)[4], const int64_t (&stride)[3],
+                     const uint32_t (&box)[4]) {
     PFN_cuTensorMapEncodeTiled_v12000 encoder = nullptr;
     const gsr_status s = gsr::host::tensor_map_encoder(&encoder);
     if (s != GSR_OK) return s;
-    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads, (cuuint64_t)batch};
-    const cuuint64_t strides[3] = {(cuuint64_t)t.row * 2, (cuuint64_t)t.head * 2, (cuuint64_t)t.batch * 2};
-    const cuuint32_t box[4] = {64, box_rows, 1, 1}, unit[4] = {1, 1, 1, 1};
+    cuuint64_t dims[4], strides[3];
+    for (int i = 0; i < 4; ++i) dims[i] = (cuuint64_t)n[i];
+    for (int i = 0; i < 3; ++i) strides[i] = (cuuint64_t)stride[i] * 2;
+    const cuuint32_t unit[4] = {1, 1, 1, 1};
     const CUresult r = encoder(map, dtype == GSR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                               4, t.data, dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                               4, const_cast<void*>(data), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? GSR_OK : gsr::host::fail_encode(r);
+}
+
+// A strided operand {d, rows, heads, batch}, box 64 x box_rows.
+gsr_status encode(CUtensorMap* map, const Strided& t, int32_t dtype, int64_t batch, int64_t heads, int64_t rows,
+                  int64_t d, uint32_t box_rows) {
+    return encode_4d(map, t.data, dtype, {d, rows, heads, batch}, {t.row, t.head, t.batch}, {64, box_rows, 1, 1});
 }
 
 // How many heads' items are taken together.  Causal items run longest first across as many heads
@@ -147,6 +155,50 @@ BwdLayout bwd_layout(const gsr_attention_desc* d) {
     w.hi = w.lo + piece(4 * d->batch * w.sp);
     w.total = w.hi + piece(4 * d->batch * w.sp);
     return w;
+}
+
+// Tiling of a tree attention call, and its workspace in 256-byte pieces.
+struct TreePlan {
+    int group, nq, tile_nodes, piece, tile_keys;
+    int64_t grid;                       // CTAs at most
+    int64_t starts, ml, parts, total;   // bytes: the pieces' offsets, the sum
+};
+TreePlan tree_plan(const gsr_tree_desc& d) {
+    auto piece = [](int64_t bytes) { return (bytes + 255) / 256 * 256; };
+    TreePlan t;
+    t.group = (int)(d.heads_q / d.heads_kv);
+    t.tile_nodes = 128 / t.group;
+    // more rows than one query tile holds: two tiles share a pass over the keys
+    t.nq = d.max_nodes > t.tile_nodes ? 2 : 1;
+    // one copy takes a page, or the largest part of it in whole 8-row swizzle units that divides it
+    t.piece = (int)(d.page_size < 128 ? d.page_size : 128);
+    while (d.page_size % t.piece) t.piece -= 8;
+    t.tile_keys = 128 / t.piece * t.piece;
+    const int64_t passes = (d.max_nodes + t.tile_nodes * t.nq - 1) / (t.tile_nodes * t.nq);
+    const int64_t tiles = (d.table_width * d.page_size + t.tile_keys - 1) / t.tile_keys;
+    const double units = (double)d.batch * (double)d.heads_kv * (double)passes * (double)(tiles > 0 ? tiles : 1);
+    t.grid = units < gsr::kTreeMaxGrid ? (int64_t)units : gsr::kTreeMaxGrid;
+    const int64_t rows = 2 * t.grid * t.nq * 128;
+    t.starts = 0;
+    t.ml = piece((d.batch + 1) * 8);
+    t.parts = t.ml + piece(rows * 8);
+    t.total = t.parts + piece(rows * d.head_dim * 4);
+    return t;
+}
+
+gsr_status check_tree_desc(const gsr_tree_desc* desc) {
+    if (!desc) return GSR_ERR_INVALID_ARG;
+    const gsr_tree_desc& d = *desc;
+    for (int64_t n : {d.batch, d.total_q, d.heads_q, d.heads_kv, d.num_pages, d.page_size, d.table_width})
+        if (bad_size(n)) return GSR_ERR_INVALID_ARG;
+    if (d.head_dim != 64 && d.head_dim != 128) return GSR_ERR_INVALID_ARG;
+    if (d.dtype != GSR_F16 && d.dtype != GSR_BF16) return GSR_ERR_INVALID_ARG;
+    if (d.max_nodes < 1 || d.max_nodes > GSR_TREE_MAX_NODES) return GSR_ERR_INVALID_ARG;
+    if (d.heads_q > 0 && (d.heads_kv == 0 || d.heads_q % d.heads_kv || d.heads_q / d.heads_kv > 128 || d.heads_q > 65535))
+        return GSR_ERR_INVALID_ARG;
+    if (!std::isfinite(d.softmax_scale) || !std::isfinite(d.softcap) || d.softcap < 0.0f) return GSR_ERR_INVALID_ARG;
+    if (d.page_size < 8 || d.page_size % 8 || d.table_width * d.page_size > INT_MAX - 256) return GSR_ERR_INVALID_ARG;
+    return GSR_OK;
 }
 
 }  // namespace
@@ -272,17 +324,9 @@ gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gs
                               const gsr_tensor* v_cache, const int32_t* block_tables, const int32_t* kv_lens,
                               const int32_t* q_starts, const int32_t* parents, void* O, void* workspace,
                               int64_t workspace_bytes, CUstream_st* stream) {
-    if (!desc) return GSR_ERR_INVALID_ARG;
+    gsr_status s = check_tree_desc(desc);
+    if (s != GSR_OK) return s;
     const gsr_tree_desc& d = *desc;
-    for (int64_t n : {d.batch, d.total_q, d.heads_q, d.heads_kv, d.num_pages, d.page_size, d.table_width})
-        if (bad_size(n)) return GSR_ERR_INVALID_ARG;
-    if (d.head_dim != 64 && d.head_dim != 128) return GSR_ERR_INVALID_ARG;
-    if (d.dtype != GSR_F16 && d.dtype != GSR_BF16) return GSR_ERR_INVALID_ARG;
-    if (d.max_nodes < 1 || d.max_nodes > GSR_TREE_MAX_NODES) return GSR_ERR_INVALID_ARG;
-    if (d.heads_q > 0 && (d.heads_kv == 0 || d.heads_q % d.heads_kv || d.heads_q / d.heads_kv > 128))
-        return GSR_ERR_INVALID_ARG;
-    if (!std::isfinite(d.softmax_scale) || !std::isfinite(d.softcap) || d.softcap < 0.0f) return GSR_ERR_INVALID_ARG;
-    if (d.page_size < 8 || d.page_size % 8 || d.table_width * d.page_size > INT_MAX - 256) return GSR_ERR_INVALID_ARG;
     if (d.batch == 0 || d.total_q == 0 || d.heads_q == 0) return GSR_OK;
     if (!Q || !O || !kv_lens || !q_starts || (d.table_width > 0 && !block_tables)) return GSR_ERR_INVALID_ARG;
     if (misaligned(Q, 16) || misaligned(O, 16) || misaligned(workspace, 16)) return GSR_ERR_ALIGNMENT;
@@ -290,7 +334,6 @@ gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gs
                           (const void*)d.alibi_slopes})
         if (misaligned(a, 4)) return GSR_ERR_ALIGNMENT;
     gsr::TreeParams p;
-    gsr_status s;
     const gsr_tensor qt{const_cast<void*>(Q), 0, d.q_stride_head, d.q_stride_row}, ot{O, 0, d.o_stride_head, d.o_stride_row};
     Strided qs, os;
     if ((s = operand(&qt, 1, d.heads_q, d.total_q, d.head_dim, false, &qs)) != GSR_OK ||
@@ -303,8 +346,14 @@ gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gs
         meet(o, span_of(p.K, d.num_pages, d.heads_kv, d.page_size, d.head_dim, 2)) ||
         meet(o, span_of(p.V, d.num_pages, d.heads_kv, d.page_size, d.head_dim, 2)))
         return GSR_ERR_ALIAS;
-    const int64_t need = tree_attention_workspace(desc);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return GSR_ERR_INVALID_ARG;
+    const TreePlan plan = tree_plan(d);
+    if (!workspace || workspace_bytes < plan.total) return GSR_ERR_INVALID_ARG;
+    const uintptr_t w0 = reinterpret_cast<uintptr_t>(workspace);
+    const Span ws{w0, w0 + (uintptr_t)plan.total};
+    if (meet(ws, o) || meet(ws, span_of(qs, 1, d.heads_q, d.total_q, d.head_dim, 2)) ||
+        meet(ws, span_of(p.K, d.num_pages, d.heads_kv, d.page_size, d.head_dim, 2)) ||
+        meet(ws, span_of(p.V, d.num_pages, d.heads_kv, d.page_size, d.head_dim, 2)))
+        return GSR_ERR_ALIAS;
     int dev = 0, sms = 0;
     if ((s = gsr::host::current_device(&dev, &sms)) != GSR_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -312,8 +361,11 @@ gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gs
     p.B = (int)d.batch;
     p.Hq = (int)d.heads_q;
     p.Hkv = (int)d.heads_kv;
-    p.group = p.Hq / p.Hkv;
-    p.D = (int)d.head_dim;
+    p.group = plan.group;
+    p.nq = plan.nq;
+    p.tile_nodes = plan.tile_nodes;
+    p.piece = plan.piece;
+    p.tile_keys = plan.tile_keys;
     p.page = (int)d.page_size;
     p.num_pages = (int)d.num_pages;
     p.table_width = (int)d.table_width;
@@ -330,14 +382,31 @@ gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gs
     p.kv_lens = kv_lens;
     p.q_starts = q_starts;
     p.parents = parents;
-    p.workspace = workspace;
+    p.unit_starts = reinterpret_cast<long long*>(static_cast<char*>(workspace) + plan.starts);
+    p.parts_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.ml);
+    p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.parts);
     p.timeout_ns = gsr::host::wait_timeout_ns();
     p.test_flags = gsr::host::test_flags();
-    const cudaError_t e = gsr::launch_tree(p, d.dtype == GSR_BF16, st);
+    gsr::TreeMaps tm;
+    if ((s = encode_4d(&tm.q, Q, d.dtype, {d.head_dim, plan.group, d.heads_kv, d.total_q},
+                       {p.q_head, p.q_head * plan.group, p.q_row},
+                       {64, (uint32_t)plan.group, 1, (uint32_t)plan.tile_nodes})) != GSR_OK)
+        return s;
+    tm.k = tm.v = tm.q;                 // a pool without pages: never read
+    if (d.num_pages > 0 && ((s = encode(&tm.k, p.K, d.dtype, d.num_pages, d.heads_kv, d.page_size, d.head_dim, plan.piece)) != GSR_OK ||
+                            (s = encode(&tm.v, p.V, d.dtype, d.num_pages, d.heads_kv, d.page_size, d.head_dim, plan.piece)) != GSR_OK))
+        return s;
+    const int grid = (int)(plan.grid < sms ? plan.grid : sms);
+    const bool bf16 = d.dtype == GSR_BF16;
+    const cudaError_t e = d.head_dim == 64 ? (bf16 ? gsr::launch_tree_bf16_64(tm, p, grid, st) : gsr::launch_tree_f16_64(tm, p, grid, st))
+                                           : (bf16 ? gsr::launch_tree_bf16_128(tm, p, grid, st) : gsr::launch_tree_f16_128(tm, p, grid, st));
     return e == cudaSuccess ? GSR_OK : gsr::host::fail(e);
 }
 
-int64_t tree_attention_workspace(const gsr_tree_desc* desc) { return desc ? 0 : -1; }
+int64_t tree_attention_workspace(const gsr_tree_desc* desc) {
+    if (check_tree_desc(desc) != GSR_OK) return -1;
+    return desc->heads_q > 0 ? tree_plan(*desc).total : 0;
+}
 
 gsr_status kv_block_tables(const int32_t* kv_lens, const int32_t* new_lens, const int32_t* free_blocks,
                            const int32_t* free_head, int32_t* block_tables, int32_t* kv_lens_out,

@@ -73,7 +73,7 @@ struct MaskedBwdParams {
 };
 
 struct TreeParams {
-    int B, Hq, Hkv, group, D;
+    int B, Hq, Hkv, group;
     int page, num_pages, table_width, max_nodes, total_q;
     ScoreArgs score;
     const void* Q;              // (total_q, Hq, D), element strides q_row, q_head
@@ -85,7 +85,13 @@ struct TreeParams {
     const int* kv_lens;         // (B): cached tokens, the drafted ones among them
     const int* q_starts;        // (B + 1)
     const int* parents;         // (total_q) or null: a chain
-    void* workspace;
+    int nq;                     // query tiles a pass
+    int tile_nodes;             // nodes of a 128-row query tile: 128 / group
+    int piece;                  // rows of one page copy: the page, or a part of it
+    int tile_keys;              // keys of a key tile: the pieces that fit in 128 rows
+    long long* unit_starts;     // workspace: (B + 1) first units, written by the first launch for the second,
+    float2* parts_ml;           // and two slots of nq x 128 rows per CTA: (m, l),
+    float* parts;               // O
     int* err;
     uint64_t timeout_ns;
     uint32_t test_flags;
@@ -108,7 +114,16 @@ cudaError_t launch_masked_bwd_f16_128(const MaskedBwdMaps& tm, const MaskedBwdPa
 cudaError_t launch_masked_bwd_bf16_64(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream);
 cudaError_t launch_masked_bwd_bf16_128(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream);
 
-cudaError_t launch_tree(const TreeParams& p, bool bf16, cudaStream_t stream);
+// Query map {D, group, Hkv, total_q}, box {64, group, 1, tile_nodes}; cache maps {D, page, Hkv,
+// pages}, box {64, piece, 1, 1}.
+struct TreeMaps {
+    CUtensorMap q, k, v;
+};
+constexpr int kTreeMaxGrid = 160;   // CTAs at most: one per SM, bounds the workspace
+cudaError_t launch_tree_f16_64(const TreeMaps& tm, const TreeParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_tree_f16_128(const TreeMaps& tm, const TreeParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_tree_bf16_64(const TreeMaps& tm, const TreeParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_tree_bf16_128(const TreeMaps& tm, const TreeParams& p, int grid, cudaStream_t stream);
 
 struct TablesParams {
     int B, page, table_width, num_free, max_tokens;
