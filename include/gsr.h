@@ -175,7 +175,7 @@ typedef struct gsr_tensor {
  * `causal` to j <= p or j < start + prefix, whichever reaches further.
  *
  *   softmax_scale  0 selects 1/sqrt(head_dim).
- *   softcap        0: no cap; must not be negative.
+ *   softcap        0: no cap; else 0 < softcap <= 1024 (a capped score is off by about softcap 2^-23).
  *   alibi_slopes   NULL: no distance bias; else device pointer to heads_q float32.  Constants: no
  *                  gradient is computed for them.
  *   doc_bounds     NULL: no documents; else device pointer to batch x (num_docs + 1) int32,

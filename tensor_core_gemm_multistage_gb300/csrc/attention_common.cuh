@@ -81,6 +81,38 @@ __device__ __forceinline__ void row_interval(const MaskArgs& m, int b, int i, in
     hi = max(hi, lo);
 }
 
+// The other way round: the queries that see key j are the interval [first, end).
+__device__ __forceinline__ void key_interval(const MaskArgs& m, int b, int j, int& first, int& end) {
+    int s = 0, d = 0;
+    first = 0;
+    end = m.Sq;
+    if (m.num_docs > 0) {                              // offset 0: documents need Sq == Skv
+        const int* bounds = m.doc_bounds + (long long)b * (m.num_docs + 1);
+        int left = 0, right = m.num_docs + 1;          // first boundary above j
+        while (left < right) {
+            const int mid = (left + right) >> 1;
+            if (__ldg(bounds + mid) <= j) left = mid + 1;
+            else right = mid;
+        }
+        d = left - 1;
+        if (d < 0 || d >= m.num_docs) {
+            first = end = min(max(__ldg(bounds + (d < 0 ? 0 : m.num_docs)), 0), m.Sq);
+            return;
+        }
+        s = first = max(__ldg(bounds + d), 0);
+        end = min(__ldg(bounds + d + 1), m.Sq);
+    }
+    if (m.causal) {
+        bool all = false;
+        if (m.prefix_lens) {
+            const long long n = m.num_docs > 0 ? m.num_docs : 1;
+            all = j < s + min(max(__ldg(m.prefix_lens + b * n + d), 0), m.Skv - s);
+        }
+        if (!all) first = max(first, min(j - m.offset, m.Sq));
+    }
+    end = max(end, first);
+}
+
 // ---------------------------------------------------------------------------
 // Scores
 // ---------------------------------------------------------------------------
@@ -98,32 +130,99 @@ __device__ __forceinline__ float cap_r(float s, float cap_in) { return rcp_appro
 
 enum ScoreMode : int { kScorePlain = 0, kScoreBias = 1, kScoreCap = 2 };   // kScoreCap: a bias too, if there is one
 
-// 32 raw products of one row and consecutive keys -> scores in log2 units, in place.  `base` is the
-// first key's distance from the row's position (later keys are closer by 1 each).  With a cap two
-// reciprocals come from one: 1 / a = b / (a b); 2^60 keeps a b finite and is tanh = 1 to the last
-// bit (a NaN passes by the minimum and is put back).
+// A row's scores while its softmax runs: registers hold v with score = mul v + add in log2 units, so
+// that the scaling is part of the exponent's multiply-add.  Plain scores keep the raw products;
+// capped ones without a bias keep r; anything with a bias holds the score itself.  A score's order is
+// v's where mul >= 0 and the reverse elsewhere.
+struct ScoreForm {
+    float mul, add;
+    bool ascending;
+    __device__ __forceinline__ uint32_t hidden() const { return ascending ? 0xff800000u : 0x7f800000u; }   // score -inf
+};
+template <int MODE>
+__device__ __forceinline__ ScoreForm score_form(const ScoreArgs& sc) {
+    if (MODE == kScorePlain) return {sc.sl2, 0.0f, sc.sl2 >= 0.0f};
+    if (MODE == kScoreCap && !sc.slopes) return {-2.0f * sc.cap_out, sc.cap_out, false};
+    return {1.0f, 0.0f, true};
+}
+
+// 32 raw products of one row and consecutive keys -> v, in place.  `base` is the first key's
+// distance from the row's position (later keys are closer by 1 each).
 template <int MODE>
 __device__ __forceinline__ void score_chunk(uint32_t (&rr)[32], const ScoreArgs& sc, float slope2, float base) {
+    if (MODE == kScorePlain) return;
+    if (MODE == kScoreBias && base >= 31.0f) {           // no key behind the row: the bias is linear
+        const float at0 = -slope2 * base;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            float w0, w1, y0 = __uint_as_float(rr[i]), y1 = __uint_as_float(rr[i + 1]);
+            ffma2(w0, w1, slope2, slope2, (float)i, (float)(i + 1), at0, at0);
+            ffma2(y0, y1, y0, y1, sc.sl2, sc.sl2, w0, w1);
+            rr[i] = __float_as_uint(y0);
+            rr[i + 1] = __float_as_uint(y1);
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
         float y0 = __uint_as_float(rr[i]), y1 = __uint_as_float(rr[i + 1]);
         if (MODE == kScoreCap) {
-            const float a = 1.0f + ex2_approx(fminf(y0 * sc.cap_in, 60.0f));
-            const float b = 1.0f + ex2_approx(fminf(y1 * sc.cap_in, 60.0f));
-            const float ab = -2.0f * sc.cap_out * rcp_approx(a * b);
-            y0 = (y0 != y0) ? y0 : fmaf(ab, b, sc.cap_out);
-            y1 = (y1 != y1) ? y1 : fmaf(ab, a, sc.cap_out);
+            fmul2(y0, y1, y0, y1, sc.cap_in, sc.cap_in);
+            y0 = ex2_approx(y0);
+            y1 = ex2_approx(y1);
+            fadd2(y0, y1, 1.0f, 1.0f);
+            y0 = rcp_approx(y0);
+            y1 = rcp_approx(y1);
         } else {
-            y0 *= sc.sl2;
-            y1 *= sc.sl2;
+            fmul2(y0, y1, y0, y1, sc.sl2, sc.sl2);
         }
-        if (MODE != kScorePlain) {
+        if (MODE == kScoreBias || sc.slopes) {
+            if (MODE == kScoreCap)
+                ffma2(y0, y1, y0, y1, -2.0f * sc.cap_out, -2.0f * sc.cap_out, sc.cap_out, sc.cap_out);
             y0 = fmaf(-slope2, fabsf(base - (float)i), y0);
             y1 = fmaf(-slope2, fabsf(base - (float)(i + 1)), y1);
         }
         rr[i] = __float_as_uint(y0);
         rr[i + 1] = __float_as_uint(y1);
     }
+}
+
+// Largest and smallest of a row's 128 values, in four chains of three-input instructions.
+__device__ __forceinline__ float row_max(const uint32_t (&a)[32], const uint32_t (&b)[32], const uint32_t (&c)[32],
+                                         const uint32_t (&d)[32]) {
+    float e0 = -INFINITY, e1 = e0, e2 = e0, e3 = e0;
+    auto fold = [&](const uint32_t (&rr)[32]) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            e0 = max3f(e0, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]));
+            e1 = max3f(e1, __uint_as_float(rr[i + 2]), __uint_as_float(rr[i + 3]));
+            e2 = max3f(e2, __uint_as_float(rr[i + 4]), __uint_as_float(rr[i + 5]));
+            e3 = max3f(e3, __uint_as_float(rr[i + 6]), __uint_as_float(rr[i + 7]));
+        }
+    };
+    fold(a);
+    fold(b);
+    fold(c);
+    fold(d);
+    return max3f(fmaxf(e0, e1), e2, e3);
+}
+__device__ __forceinline__ float row_min(const uint32_t (&a)[32], const uint32_t (&b)[32], const uint32_t (&c)[32],
+                                         const uint32_t (&d)[32]) {
+    float e0 = INFINITY, e1 = e0, e2 = e0, e3 = e0;
+    auto fold = [&](const uint32_t (&rr)[32]) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            e0 = min3f(e0, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]));
+            e1 = min3f(e1, __uint_as_float(rr[i + 2]), __uint_as_float(rr[i + 3]));
+            e2 = min3f(e2, __uint_as_float(rr[i + 4]), __uint_as_float(rr[i + 5]));
+            e3 = min3f(e3, __uint_as_float(rr[i + 6]), __uint_as_float(rr[i + 7]));
+        }
+    };
+    fold(a);
+    fold(b);
+    fold(c);
+    fold(d);
+    return min3f(fminf(e0, e1), e2, e3);
 }
 
 // Once per device: lets `kernel` use `bytes` of dynamic shared memory.

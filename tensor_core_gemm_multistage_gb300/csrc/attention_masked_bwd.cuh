@@ -7,8 +7,8 @@
 //     dQ_i = scale sum_j dS_ij K_j        dK_j = scale sum_i dS_ij Q_i
 // dK and dV of a key/value head sum over the query heads of its group.
 //
-// Three launches: one pass over the rows (delta, intervals), then dK and dV by the CTA that owns
-// the keys and dQ by the CTA that owns the queries.  The two recompute S and dP, seven products of
+// Three launches: one pass over the rows (delta), then dK and dV by the CTA that owns the keys and
+// dQ by the CTA that owns the queries.  The two recompute S and dP, seven products of
 // 128 x 128 x D instead of the five that one pass with atomically added dQ would take; in return
 // no result depends on the order of atomics, dQ needs no fp32 buffer, and every accumulator stays
 // in TMEM from the first product to the last.
@@ -40,53 +40,110 @@ __device__ __forceinline__ float ds_shift(const unsigned* norms) {
     return fminf(fmaxf(floorf(2.0f - 0.5f * log2f(n)), -100.0f), 100.0f);    // 15 - 12 - 1 - log2(bound / 2)
 }
 
+// What a row's exponent offset holds beside -lse: P's power of two, and the constant of a capped
+// score without a bias (weights_chunk).
+template <class T>
+__device__ __forceinline__ float row_offset(const ScoreArgs& sc) {
+    return kPShift<T> + (sc.cap_in != 0.0f ? sc.cap_out : 0.0f);
+}
+
 // ---------------------------------------------------------------------------
-// Rows: exponent offsets, delta, intervals, and the norms that bound dS
+// Rows: exponent offsets, delta, and the norms that bound dS
 // ---------------------------------------------------------------------------
-// One warp per query row (b, h, i), rows padded to Sp, then (fp16) one per value row.  Bound by the
-// read of dO and O.  Maxima are order-free, so the atomics are deterministic.
+// A warp takes kWarpRows rows of one head, 16 bytes a lane (D / 8 lanes a row), all loads before the
+// first sum; bound by the read of dO and O.  Rows padded to Sp first, then (fp16) the value rows.
+// Maxima are order-free, so the atomics are deterministic.
+constexpr int kWarpRows = 8;
+
+// Row r's 8 elements of this lane; zero outside [0, rows).
+template <class T>
+__device__ __forceinline__ uint4 row_piece(const Strided& t, int b, int h, int r, int rows, int piece) {
+    if (r >= rows) return make_uint4(0, 0, 0, 0);
+    return __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(t.data) + b * t.batch + h * t.head + r * t.row) + piece);
+}
+template <class T>
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 u = Elem<T>::unpack(x[i]), v = Elem<T>::unpack(y[i]);
+        s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
+    }
+    return s;
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+__device__ __forceinline__ void max_norm(unsigned* to, float n, int lane) {
+    unsigned bits = n < INFINITY ? __float_as_uint(n) : 0u;      // infinite and NaN rows do not count
+    bits = __reduce_max_sync(0xffffffffu, bits);
+    if (lane == 0 && bits) atomicMax(to, bits);
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(256) gsr_masked_bwd_rows_kernel(const __grid_constant__ MaskedBwdParams p) {
-    const int lane = threadIdx.x & 31;
+    constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, N = kWarpRows / AT_ONCE;
+    const int lane = threadIdx.x & 31, sub = lane / LANES, piece = lane % LANES;
     const MaskArgs& mk = p.mask;
-    const long long q_rows = (long long)mk.B * mk.Hq * p.Sp;
-    long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row < q_rows) {
-        const int i = (int)(row % p.Sp), bh = (int)(row / p.Sp), b = bh / mk.Hq, h = bh % mk.Hq;
-        float offset = -INFINITY, delta = 0.0f;
-        int lo = mk.Skv, hi = mk.Skv;
-        if (i < mk.Sq) {
+    const int groups = p.Sp / kWarpRows, v_groups = (mk.Skv + kWarpRows - 1) / kWarpRows;
+    long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const long long q_groups = (long long)mk.B * mk.Hq * groups;
+    if (id < q_groups) {
+        const int bh = (int)(id / groups), i0 = (int)(id - (long long)bh * groups) * kWarpRows, b = bh / mk.Hq, h = bh - b * mk.Hq;
+        uint4 x[N], y[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            x[n] = row_piece<T>(p.dO, b, h, i0 + n * AT_ONCE + sub, mk.Sq, piece);
+            y[n] = row_piece<T>(p.O, b, h, i0 + n * AT_ONCE + sub, mk.Sq, piece);
+        }
+        // lane r < kWarpRows: row r's interval and lse
+        int lo = 0, hi = 0;
+        float lse = -INFINITY;
+        const int i = i0 + lane;
+        if (lane < kWarpRows && i < mk.Sq) {
             row_interval(mk, b, i, lo, hi);
-            if (lo < hi) {
-                float x[D / 32], y[D / 32];
-                load_row<T, D>(static_cast<const T*>(p.dO.data) + b * p.dO.batch + h * p.dO.head + i * p.dO.row, lane, x);
-                load_row<T, D>(static_cast<const T*>(p.O.data) + b * p.O.batch + h * p.O.head + i * p.O.row, lane, y);
-                delta = warp_dot(x, y);
-                const float lse = __ldg(p.lse + ((long long)b * mk.Hq + h) * mk.Sq + i);
-                if (lse != -INFINITY) offset = kPShift<T> - lse * kLog2e;
-                if (!Elem<T>::bf16) {
-                    const float n = warp_dot(x, x);
-                    if (lane == 0 && n < INFINITY) atomicMax(p.norms, __float_as_uint(n));
+            lse = __ldg(p.lse + ((long long)b * mk.Hq + h) * mk.Sq + i);
+        }
+        const bool keys = lo < hi && lse != -INFINITY;
+        float delta = 0.0f, norm = 0.0f;                 // of row `lane`
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const float d = lanes_sum<LANES>(dot8<T>(x[n], y[n]));
+            const float q = Elem<T>::bf16 ? 0.0f : lanes_sum<LANES>(dot8<T>(x[n], x[n]));
+#pragma unroll
+            for (int k = 0; k < AT_ONCE; ++k) {
+                const float dk = __shfl_sync(0xffffffffu, d, k * LANES), qk = __shfl_sync(0xffffffffu, q, k * LANES);
+                if (lane == n * AT_ONCE + k) {
+                    delta = dk;
+                    norm = qk;
                 }
             }
         }
-        if (lane == 0) {
-            p.offset[row] = offset;
-            p.neg_delta[row] = -delta;
-            if (h == 0) {
-                p.lo[(long long)b * p.Sp + i] = lo;
-                p.hi[(long long)b * p.Sp + i] = hi;
-            }
+        if (lane < kWarpRows) {
+            const long long row = (long long)bh * p.Sp + i;
+            p.offset[row] = keys ? row_offset<T>(p.score) - lse * kLog2e : -INFINITY;
+            p.neg_delta[row] = keys ? -delta : 0.0f;
         }
+        if (!Elem<T>::bf16) max_norm(p.norms, keys ? norm : 0.0f, lane);
         return;
     }
-    row -= q_rows;
-    if (!Elem<T>::bf16 && row < (long long)mk.B * mk.Hkv * mk.Skv) {
-        const int j = (int)(row % mk.Skv), bh = (int)(row / mk.Skv), b = bh / mk.Hkv, h = bh % mk.Hkv;
-        float x[D / 32];
-        load_row<T, D>(static_cast<const T*>(p.V.data) + b * p.V.batch + h * p.V.head + j * p.V.row, lane, x);
-        const float n = warp_dot(x, x);
-        if (lane == 0 && n < INFINITY) atomicMax(p.norms + 1, __float_as_uint(n));
+    id -= q_groups;
+    if (!Elem<T>::bf16 && id < (long long)mk.B * mk.Hkv * v_groups) {
+        const int bh = (int)(id / v_groups), j0 = (int)(id - (long long)bh * v_groups) * kWarpRows, b = bh / mk.Hkv, h = bh - b * mk.Hkv;
+        uint4 x[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) x[n] = row_piece<T>(p.V, b, h, j0 + n * AT_ONCE + sub, mk.Skv, piece);
+        float most = 0.0f;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const float q = lanes_sum<LANES>(dot8<T>(x[n], x[n]));
+            if (q < INFINITY) most = fmaxf(most, q);
+        }
+        max_norm(p.norms + 1, most, lane);
     }
 }
 
@@ -110,7 +167,7 @@ __device__ __forceinline__ void pair_grad(const ScoreArgs& sc, float slope2, int
                                           const float (&v)[D / 32], float offset, float neg_delta, float& P, float& dS) {
     float grad;
     const float y = score_of(warp_dot(q, k), sc, grad) - slope2 * fabsf((float)dist);
-    P = ex2_approx(y + (offset - kPShift<T>));
+    P = ex2_approx(y + (offset - row_offset<T>(sc)));
     dS = P * (warp_dot(dO, v) + neg_delta) * grad;
 }
 
@@ -126,7 +183,8 @@ __device__ __noinline__ void row_dq(const MaskedBwdParams& p, int b, int h, int 
     const float slope2 = p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
     const long long row = ((long long)b * mk.Hq + h) * p.Sp + i;
     const float offset = p.offset[row], neg_delta = p.neg_delta[row];
-    const int lo = p.lo[(long long)b * p.Sp + i], hi = p.hi[(long long)b * p.Sp + i];
+    int lo, hi;
+    row_interval(mk, b, i, lo, hi);
     for (int j = lo; j < hi; ++j) {
         load_row<T, D>(kb + j * p.K.row, lane, k);
         load_row<T, D>(vb + j * p.V.row, lane, v);
@@ -140,23 +198,21 @@ __device__ __noinline__ void row_dq(const MaskedBwdParams& p, int b, int h, int 
     store_row<T, D>(static_cast<T*>(p.dQ.data) + b * p.dQ.batch + h * p.dQ.head + i * p.dQ.row, lane, acc);
 }
 
-// dK (or dV) of one key row: the queries that see key j lie between the first whose interval ends
-// behind it and the first whose interval starts behind it.
+// dK (or dV) of one key row.
 template <class T, int D>
 __device__ __noinline__ void row_dkv(const MaskedBwdParams& p, int b, int hk, int j, bool want_dk, int lane) {
     const MaskArgs& mk = p.mask;
     float q[D / 32], dO[D / 32], k[D / 32], v[D / 32], acc[D / 32] = {};
     load_row<T, D>(static_cast<const T*>(p.K.data) + b * p.K.batch + hk * p.K.head + j * p.K.row, lane, k);
     load_row<T, D>(static_cast<const T*>(p.V.data) + b * p.V.batch + hk * p.V.head + j * p.V.row, lane, v);
-    const int* los = p.lo + (long long)b * p.Sp;
-    const int* his = p.hi + (long long)b * p.Sp;
+    int first, end;
+    key_interval(mk, b, j, first, end);
     for (int h = hk * mk.group; h < (hk + 1) * mk.group; ++h) {
         const T* qb = static_cast<const T*>(p.Q.data) + b * p.Q.batch + h * p.Q.head;
         const T* ob = static_cast<const T*>(p.dO.data) + b * p.dO.batch + h * p.dO.head;
         const float slope2 = p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
         const long long row = ((long long)b * mk.Hq + h) * p.Sp;
-        for (int i = 0; i < mk.Sq; ++i) {
-            if (j < los[i] || j >= his[i]) continue;
+        for (int i = first; i < end; ++i) {
             load_row<T, D>(qb + i * p.Q.row, lane, q);
             load_row<T, D>(ob + i * p.dO.row, lane, dO);
             float P, dS;
@@ -183,54 +239,43 @@ constexpr int kBwdMathWarps = 8;
 constexpr int kTile = 128;
 constexpr int kChunkBytes = 128 * 128;
 
-// 32 raw products -> in place W = 2^x c with x = y + off (`off` per column or, where it is one row's,
-// a broadcast of one value), c the cap's derivative; `packed`, where wanted, gets 2^x alone in
-// pairs.  `base` as in score_chunk.
+// 32 raw products -> in place W = 2^x c, where x is the score plus the row's offset less the part of
+// it that row_offset holds, and c a quarter of the cap's derivative (r (1 - r); the factor 4 is
+// applied with the accumulator's).  `off` gives the offsets of columns i and i + 1; `packed`, where
+// wanted, gets 2^x alone in pairs.  `base` as in score_chunk.
 template <class T, int MODE, bool PACK, class Off>
 __device__ __forceinline__ void weights_chunk(uint32_t (&rr)[32], const ScoreArgs& sc, float slope2, float base, Off off,
                                               uint32_t (&packed)[16]) {
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-        float y0 = __uint_as_float(rr[i]), y1 = __uint_as_float(rr[i + 1]), c0 = 1.0f, c1 = 1.0f;
+        float y0 = __uint_as_float(rr[i]), y1 = __uint_as_float(rr[i + 1]), c0, c1;
         const float2 o = off(i);
         if (MODE == kScoreCap) {
-            const bool n0 = y0 != y0, n1 = y1 != y1;
-            const float a = 1.0f + ex2_approx(fminf(y0 * sc.cap_in, 60.0f));
-            const float b = 1.0f + ex2_approx(fminf(y1 * sc.cap_in, 60.0f));
-            const float ab = rcp_approx(a * b);
-            const float r0 = ab * b, r1 = ab * a;
-            c0 = 4.0f * fmaf(-r0, r0, r0);
-            c1 = 4.0f * fmaf(-r1, r1, r1);
-            y0 = n0 ? y0 : fmaf(-2.0f * sc.cap_out, r0, sc.cap_out + o.x);
-            y1 = n1 ? y1 : fmaf(-2.0f * sc.cap_out, r1, sc.cap_out + o.y);
+            fmul2(y0, y1, y0, y1, sc.cap_in, sc.cap_in);
+            y0 = ex2_approx(y0);
+            y1 = ex2_approx(y1);
+            fadd2(y0, y1, 1.0f, 1.0f);
+            y0 = rcp_approx(y0);
+            y1 = rcp_approx(y1);
+            ffma2(c0, c1, y0, y1, -y0, -y1, y0, y1);
+            ffma2(y0, y1, y0, y1, -2.0f * sc.cap_out, -2.0f * sc.cap_out, o.x, o.y);
         } else {
             ffma2(y0, y1, y0, y1, sc.sl2, sc.sl2, o.x, o.y);
         }
-        if (MODE != kScorePlain) {
+        if (MODE == kScoreBias || (MODE == kScoreCap && sc.slopes)) {
             y0 = fmaf(-slope2, fabsf(base - (float)i), y0);
             y1 = fmaf(-slope2, fabsf(base - (float)(i + 1)), y1);
         }
-        const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
-        if (PACK) packed[i / 2] = Elem<T>::pack(p0, p1);
-        rr[i] = __float_as_uint(MODE == kScoreCap ? p0 * c0 : p0);
-        rr[i + 1] = __float_as_uint(MODE == kScoreCap ? p1 * c1 : p1);
+        y0 = ex2_approx(y0);
+        y1 = ex2_approx(y1);
+        if (PACK) packed[i / 2] = Elem<T>::pack(y0, y1);
+        if (MODE == kScoreCap) fmul2(y0, y1, y0, y1, c0, c1);
+        rr[i] = __float_as_uint(y0);
+        rr[i + 1] = __float_as_uint(y1);
     }
 }
-
-// The first index x of [0, n] with values[x] > v, or n (values ascending).  Whole warp, 32-way.
-__device__ __forceinline__ int warp_first_above(const int* values, int n, int v, int lane) {
-    int base = 0, len = n;
-    while (len > 0) {
-        const int chunk = (len + 31) >> 5, start = lane * chunk;      // a lane's piece; its last value decides
-        const bool above = start >= len || __ldg(values + base + min(start + chunk, len) - 1) > v;
-        const uint32_t pieces = __ballot_sync(0xffffffffu, above);
-        const int first = pieces ? (__ffs(pieces) - 1) * chunk : len;
-        if (first >= len) return base + len;
-        base += first;
-        len = min(chunk, len - first) - 1;                            // that last value is the answer if no earlier one is
-    }
-    return base;
-}
+template <int MODE>
+constexpr float kCapFactor = MODE == kScoreCap ? 4.0f : 1.0f;
 
 // ---------------------------------------------------------------------------
 // dK and dV
@@ -420,10 +465,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 it.b = bh / mk.Hkv;
                 it.hk = bh - it.b * mk.Hkv;
                 it.k0 = r_in / gsz * kTile;
-                // the first query whose interval ends behind the tile's first key, and the first whose
-                // interval starts behind its last
-                const int first = warp_first_above(p.hi + (long long)it.b * p.Sp, mk.Sq, it.k0, lane);
-                const int end = warp_first_above(p.lo + (long long)it.b * p.Sp, mk.Sq, it.k0 + kTile - 1, lane);
+                // lane 0: the queries that see the tile's first key, lane 1: its last
+                int first = 0, end = 0;
+                if (lane < 2) key_interval(mk, it.b, lane == 0 ? it.k0 : min(it.k0 + kTile, mk.Skv) - 1, first, end);
+                end = __shfl_sync(0xffffffffu, end, 1);
+                first = __shfl_sync(0xffffffffu, first, 0);
                 it.t0 = first / kTile;
                 it.t1 = first < end ? (end + kTile - 1) / kTile : it.t0;
             }
@@ -442,10 +488,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             ++n_pub;
             if (item < 0) break;
             if (lane == 0) {
-                fence_proxy_async_smem();
-                mbar_arrive_expect_tx(clc, 16);
-                clc_try_cancel(sb + Cfg::OFF_CLC, clc);
-                asked = true;
                 if (it.t0 < it.t1) {
                     ok = w.wait(kv_empty, (n_item & 1u) ^ 1u, kDevErrProducerEmpty);
                     if (ok && !drop) {
@@ -485,9 +527,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         }
                     }
                 }
-                if (ok && (ok = w.wait(clc, n_clc & 1u, kDevErrProducerEmpty))) {
-                    asked = false;
-                    item = clc_taken(sb + Cfg::OFF_CLC);
+                // the next item, asked for once this one's copies are issued: earlier, a CTA busy with a
+                // long item would hold one that another could start
+                if (ok) {
+                    fence_proxy_async_smem();            // the last answer has been read
+                    mbar_arrive_expect_tx(clc, 16);
+                    clc_try_cancel(sb + Cfg::OFF_CLC, clc);
+                    asked = true;
+                    if ((ok = w.wait(clc, n_clc & 1u, kDevErrProducerEmpty))) {
+                        asked = false;
+                        item = clc_taken(sb + Cfg::OFF_CLC);
+                    }
                 }
             }
             ++n_clc;
@@ -571,14 +621,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             ++n_box;
             if (it.b < 0) break;
             const int j = it.k0 + r;
-            const int* los = p.lo + (long long)it.b * p.Sp;
-            const int* his = p.hi + (long long)it.b * p.Sp;
+            int first = 0, end = 0;                      // the queries that see this thread's key
+            if (j < mk.Skv) key_interval(mk, it.b, j, first, end);
             for (int h = it.hk * mk.group; ok && h < (it.hk + 1) * mk.group; ++h) {
                 const float slope2 = Cfg::MODE != kScorePlain && p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
                 for (int t = it.t0; t < it.t1; ++t, ++n) {
                     const int i0 = t * kTile + half * 64;
-                    // every query of the tile sees every key of the tile (intervals are ordered)
-                    const bool masked = __ldg(los + t * kTile + kTile - 1) > it.k0 || __ldg(his + t * kTile) < it.k0 + kTile;
+                    const bool masked = i0 < first || i0 + 64 > end;
                     if (!__all_sync(0xffffffffu, w.wait(o_full((int)(n % NO)), (n / NO) & 1u, kDevErrEpilogueFull) &&
                                                      w.wait(s_full, n & 1u, kDevErrEpilogueFull))) {
                         ok = false;
@@ -587,20 +636,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     tcgen05_fence_after();
                     const float* rows = reinterpret_cast<const float*>(smem + Cfg::OFF_ROWS + (n % NO) * 1024) + half * 64;
                     const float base = (float)(j - mk.offset - i0);
-                    uint32_t w0[32], w1[32], see0 = 0xffffffffu, see1 = 0xffffffffu;
+                    uint32_t w0[32], w1[32];
                     tmem_ld_32x32b_x32(s_col, w0);
                     tmem_ld_32x32b_x32(s_col + 32, w1);
-                    if (masked) {
-                        see0 = see1 = 0u;
-#pragma unroll 8
-                        for (int i = 0; i < 32; ++i) {
-                            see0 |= (uint32_t)(j >= __ldg(los + i0 + i) && j < __ldg(his + i0 + i)) << i;
-                            see1 |= (uint32_t)(j >= __ldg(los + i0 + 32 + i) && j < __ldg(his + i0 + 32 + i)) << i;
-                        }
-                    }
                     tmem_ld_wait(w0);
                     reg_tie(w1);
-                    auto p_chunk = [&](uint32_t (&rr)[32], int c, uint32_t see) {
+                    auto p_chunk = [&](uint32_t (&rr)[32], int c) {
                         uint32_t packed[16];
                         weights_chunk<T, Cfg::MODE, true>(rr, p.score, slope2, base - (float)(c * 32),
                                                           [&](int i) { return *reinterpret_cast<const float2*>(rows + c * 32 + i); },
@@ -608,7 +649,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         if (masked) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (!(see >> i & 1u)) {
+                                if (c * 32 + i < first - i0 || c * 32 + i >= end - i0) {
                                     rr[i] = 0u;
                                     packed[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
                                 }
@@ -616,11 +657,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         tmem_st_32x32b_x16(s_col + c * 16, packed);
                         if (!Elem<T>::bf16) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) rr[i] = __float_as_uint(__uint_as_float(rr[i]) * ds_mul);
+                            for (int i = 0; i < 32; i += 2) {
+                                float a, b;
+                                fmul2(a, b, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]), ds_mul, ds_mul);
+                                rr[i] = __float_as_uint(a);
+                                rr[i + 1] = __float_as_uint(b);
+                            }
                         }
                     };
-                    p_chunk(w0, 0, see0);
-                    p_chunk(w1, 1, see1);
+                    p_chunk(w0, 0);
+                    p_chunk(w1, 1);
                     tmem_st_wait();
                     tcgen05_fence_before();
                     __syncwarp();
@@ -630,7 +676,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         break;
                     }
                     tcgen05_fence_after();
-                    auto ds_chunk = [&](const uint32_t (&ww)[32], int c, uint32_t see) {
+                    auto ds_chunk = [&](const uint32_t (&ww)[32], int c) {
                         uint32_t dp[32], packed[16];
                         tmem_ld_32x32b_x32(dp_col + c * 32, dp);
                         tmem_ld_wait(dp);
@@ -645,13 +691,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         if (masked) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (!(see >> i & 1u)) packed[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+                                if (c * 32 + i < first - i0 || c * 32 + i >= end - i0) packed[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
                         }
                         // columns 0-15 of this half hold dP values of chunk 0 only: read above
                         tmem_st_32x32b_x16(dp_col + c * 16, packed);
                     };
-                    ds_chunk(w0, 0, see0);
-                    ds_chunk(w1, 1, see1);
+                    ds_chunk(w0, 0);
+                    ds_chunk(w1, 1);
                     tmem_st_wait();
                     tcgen05_fence_before();
                     __syncwarp();
@@ -669,7 +715,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             // half 0 writes dV's rows, half 1 dK's.  The next item's products overwrite the accumulators
             // only after this warp's next P and dS.
             const Strided& out = half == 0 ? p.dV : p.dK;
-            const float factor = half == 0 ? exp2f(-kPShift<T>) : p.score.scale * exp2f(-kPShift<T> - shift);
+            const float factor = half == 0 ? exp2f(-kPShift<T>) : kCapFactor<Cfg::MODE> * p.score.scale * exp2f(-kPShift<T> - shift);
             T* row = static_cast<T*>(out.data) + it.b * out.batch + it.hk * out.head + (long long)j * out.row;
             const bool bad = store_accumulator<T, D>(lane_base + (half == 0 ? Cfg::T_DV : Cfg::T_DK), factor, none, j < mk.Skv, row);
             tcgen05_fence_before();
@@ -818,8 +864,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     it.b = bh / mk.Hq;
                     it.h = bh - it.b * mk.Hq;
                     it.q_base = (n_qb - 1 - r_in / gsz) * kTile;
-                    const int lo = __ldg(p.lo + (long long)it.b * p.Sp + it.q_base);
-                    const int hi = __ldg(p.hi + (long long)it.b * p.Sp + min(it.q_base + kTile, mk.Sq) - 1);
+                    int lo, hi, none;
+                    row_interval(mk, it.b, it.q_base, lo, none);
+                    row_interval(mk, it.b, min(it.q_base + kTile, mk.Sq) - 1, none, hi);
                     it.t0 = lo / kTile;
                     it.t1 = hi > lo ? (hi + kTile - 1) / kTile : it.t0;
                 }
@@ -834,11 +881,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 mbar_arrive(item_pub(box));
                 ++n_pub;
                 if (item < 0) break;
-                fence_proxy_async_smem();
-                mbar_arrive_expect_tx(clc, 16);
-                clc_try_cancel(sb + Cfg::OFF_CLC, clc);
-                asked = true;
-                ++n_clc;
                 if (it.t0 < it.t1) {
                     if (!(ok = w.wait(q_empty, (n_item & 1u) ^ 1u, kDevErrProducerEmpty))) break;
                     if (!drop) {
@@ -872,6 +914,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     }
                     if (!ok) break;
                 }
+                fence_proxy_async_smem();                // the last answer has been read
+                mbar_arrive_expect_tx(clc, 16);
+                clc_try_cancel(sb + Cfg::OFF_CLC, clc);
+                asked = true;
+                ++n_clc;
                 if (!(ok = w.wait(clc, (n_clc - 1) & 1u, kDevErrProducerEmpty))) break;
                 asked = false;
                 item = clc_taken(sb + Cfg::OFF_CLC);
@@ -950,7 +997,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (it.b < 0) break;
             const int qi = it.q_base + r;                // below Sp
             const long long row = ((long long)it.b * mk.Hq + it.h) * p.Sp + qi;
-            const int lo = p.lo[(long long)it.b * p.Sp + qi], hi = p.hi[(long long)it.b * p.Sp + qi];
+            int lo = 0, hi = 0;
+            if (qi < mk.Sq) row_interval(mk, it.b, qi, lo, hi);
             const float off = p.offset[row] + shift, neg_delta = p.neg_delta[row];
             const float slope2 = Cfg::MODE != kScorePlain && p.score.slopes ? __ldg(p.score.slopes + it.h) * kLog2e : 0.0f;
             for (int t = it.t0; t < it.t1; ++t, ++n) {
@@ -1016,7 +1064,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             // next dS
             const bool empty = none || lo >= hi;
             T* out = static_cast<T*>(p.dQ.data) + it.b * p.dQ.batch + it.h * p.dQ.head + (long long)qi * p.dQ.row;
-            const float factor = p.score.scale * exp2f(-kPShift<T> - shift);
+            const float factor = kCapFactor<Cfg::MODE> * p.score.scale * exp2f(-kPShift<T> - shift);
             if (half == 0) {
                 const bool bad = store_accumulator<T, D>(lane_base + Cfg::T_DQ, factor, empty, qi < mk.Sq, out);
                 __syncwarp();
@@ -1079,13 +1127,13 @@ cudaError_t launch_bwd_type(const MaskedBwdMaps& tm, const MaskedBwdParams& p, c
             gsr_masked_zero_kernel<T, D><<<(unsigned)((q_rows + 7) / 8), 256, 0, stream>>>(p.dQ, mk.Hq, mk.Sq, q_rows);
         return cudaGetLastError();
     }
-    long long rows = (long long)mk.B * mk.Hq * p.Sp;
+    long long warps = (long long)mk.B * mk.Hq * (p.Sp / kWarpRows);
     if (!Elem<T>::bf16) {
         const cudaError_t e = cudaMemsetAsync(p.norms, 0, 2 * sizeof(unsigned), stream);
         if (e != cudaSuccess) return e;
-        rows += k_rows;
+        warps += (long long)mk.B * mk.Hkv * ((mk.Skv + kWarpRows - 1) / kWarpRows);
     }
-    gsr_masked_bwd_rows_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p);
+    gsr_masked_bwd_rows_kernel<T, D><<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (p.score.cap_in != 0.0f) return launch_bwd_mode<T, D, kScoreCap>(tm, p, stream);

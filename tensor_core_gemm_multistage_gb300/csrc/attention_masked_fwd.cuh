@@ -236,10 +236,6 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
             ++n_pub;
             if (item < 0) break;
             if (lane == 0) {
-                fence_proxy_async_smem();                // the last answer has been read
-                mbar_arrive_expect_tx(clc, 16);
-                clc_try_cancel(sb + Cfg::OFF_CLC, clc);
-                asked = true;
                 const int t_begin = it.first(), t_end = it.last();
                 if (t_begin < t_end) {
                     const int qb = (int)(n_q % Cfg::QBUF);
@@ -286,9 +282,17 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                         parity = (parity & ~(1u << s)) | ph << s;
                     }
                 }
-                if (ok && (ok = w.wait(clc, n_clc & 1u, kDevErrProducerEmpty))) {
-                    asked = false;
-                    item = clc_taken(sb + Cfg::OFF_CLC);
+                // the next item, asked for once this one's copies are issued: earlier, a CTA busy with a
+                // long item would hold one that another could start
+                if (ok) {
+                    fence_proxy_async_smem();            // the last answer has been read
+                    mbar_arrive_expect_tx(clc, 16);
+                    clc_try_cancel(sb + Cfg::OFF_CLC, clc);
+                    asked = true;
+                    if ((ok = w.wait(clc, n_clc & 1u, kDevErrProducerEmpty))) {
+                        asked = false;
+                        item = clc_taken(sb + Cfg::OFF_CLC);
+                    }
                 }
             }
             ++n_clc;
@@ -374,8 +378,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
         const uint32_t s_col = lane_base + Cfg::T_S + q * 128;
         const uint32_t o_col = lane_base + Cfg::T_O + q * D;
         const ScoreArgs& sc = p.score;
-        const float sl2 = sc.sl2;
-        const bool scale_pos = sl2 >= 0.0f;
+        const ScoreForm form = score_form<Cfg::MODE>(sc);
+        const uint32_t hidden = form.hidden();
         uint32_t n_item = 0, s_n = 0, o_n = 0;
         bool ok = true;
         while (ok) {
@@ -412,58 +416,21 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                 reg_tie(sc1);
                 reg_tie(sc2);
                 reg_tie(sc3);
-                // scores in log2 units in place, -inf where the row sees nothing; an unmasked tile of
-                // plain scores keeps the raw products (scaled in the exponent below)
                 const float base = (float)(qi + mk.offset - k0);
                 auto transform = [&](uint32_t (&rr)[32], int c) {
                     score_chunk<Cfg::MODE>(rr, sc, slope2, base - (float)(c * 32));
                     if (masked) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (c * 32 + i < lo - k0 || c * 32 + i >= hi - k0) rr[i] = 0xff800000u;
+                            if (c * 32 + i < lo - k0 || c * 32 + i >= hi - k0) rr[i] = hidden;
                     }
                 };
-                const bool raw = Cfg::MODE == kScorePlain && !masked;
-                if (!raw) {
-                    transform(sc0, 0);
-                    transform(sc1, 1);
-                    transform(sc2, 2);
-                    transform(sc3, 3);
-                }
-                // the row's maximum; of raw products under a negative scale their minimum
-                float mt;
-                if (raw && !scale_pos) {
-                    float e0 = INFINITY, e1 = e0;
-                    auto fold = [&](const uint32_t (&rr)[32]) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            e0 = min3f(e0, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]));
-                            e1 = min3f(e1, __uint_as_float(rr[i + 2]), __uint_as_float(rr[i + 3]));
-                        }
-                    };
-                    fold(sc0);
-                    fold(sc1);
-                    fold(sc2);
-                    fold(sc3);
-                    mt = fminf(e0, e1) * sl2;
-                } else {
-                    float e0 = -INFINITY, e1 = e0, e2 = e0, e3 = e0;
-                    auto fold = [&](const uint32_t (&rr)[32]) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            e0 = max3f(e0, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]));
-                            e1 = max3f(e1, __uint_as_float(rr[i + 2]), __uint_as_float(rr[i + 3]));
-                            e2 = max3f(e2, __uint_as_float(rr[i + 4]), __uint_as_float(rr[i + 5]));
-                            e3 = max3f(e3, __uint_as_float(rr[i + 6]), __uint_as_float(rr[i + 7]));
-                        }
-                    };
-                    fold(sc0);
-                    fold(sc1);
-                    fold(sc2);
-                    fold(sc3);
-                    mt = max3f(fmaxf(e0, e1), e2, e3);
-                    if (raw) mt *= sl2;
-                }
+                transform(sc0, 0);
+                transform(sc1, 1);
+                transform(sc2, 2);
+                transform(sc3, 3);
+                float mt = form.ascending ? row_max(sc0, sc1, sc2, sc3) : row_min(sc0, sc1, sc2, sc3);
+                mt = fmaf(mt, form.mul, form.add);
                 // lazy move of the exponent base: only by more than 2^RESCALE_LOG2 (always from -inf)
                 float factor = 1.0f;
                 const bool bump = mt > m + Cfg::RESCALE_LOG2;
@@ -472,8 +439,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                     m = mt;
                 }
                 l *= factor;
-                const float neg_m = (m == -INFINITY) ? 0.0f : -m;
-                const float mul = raw ? sl2 : 1.0f;
+                const float neg_m = form.add - ((m == -INFINITY) ? 0.0f : m), mul = form.mul;
                 float ls0 = 0.0f, ls1 = 0.0f;
                 auto chunk_p = [&](const uint32_t (&rr)[32], int c) {
                     uint32_t packed[16];

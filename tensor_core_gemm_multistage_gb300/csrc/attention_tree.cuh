@@ -477,6 +477,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
         const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
         const uint32_t o_col = lane_base + Cfg::T_O + q * D;
         const ScoreArgs& sc = p.score;
+        const ScoreForm form = score_form<Cfg::MODE>(sc);
+        const uint32_t hidden = form.hidden();
         const int node_in = rq / p.group, hg = rq - node_in * p.group;
         uint32_t n_item = 0, n = 0, s_n[2] = {0u, 0u}, o_n = 0;
         bool ok = true;
@@ -535,7 +537,6 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                     reg_tie(sc2);
                     reg_tie(sc3);
                     const float base = (float)(pos - k0);
-                    // scores in log2 units, -inf where the row sees nothing
                     auto transform = [&](uint32_t (&rr)[32], int c) {
                         score_chunk<Cfg::MODE>(rr, sc, slope2, base - (float)(c * 32));
                         if (!masked) return;
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                             tree &= ~below(it.ctx);
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                if (tree >> j & 1u) {
+                                if (slope2 != 0.0f && (tree >> j & 1u)) {
                                     const float at = (float)(pos - it.ctx - depth_of(see, kk + j - it.ctx));
                                     rr[j] = __float_as_uint(fmaf(slope2, fabsf(base - (float)(c * 32 + j)) - at, __uint_as_float(rr[j])));
                                 }
@@ -565,41 +566,28 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                         const uint32_t vis = (tree | below(it.ctx)) & below(it.kv) & have;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (!(vis >> j & 1u)) rr[j] = 0xff800000u;
+                            if (!(vis >> j & 1u)) rr[j] = hidden;
                     };
                     transform(sc0, 0);
                     transform(sc1, 1);
                     transform(sc2, 2);
                     transform(sc3, 3);
-                    float e0 = -INFINITY, e1 = e0, e2 = e0, e3 = e0;
-                    auto fold = [&](const uint32_t (&rr)[32]) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            e0 = max3f(e0, __uint_as_float(rr[j]), __uint_as_float(rr[j + 1]));
-                            e1 = max3f(e1, __uint_as_float(rr[j + 2]), __uint_as_float(rr[j + 3]));
-                            e2 = max3f(e2, __uint_as_float(rr[j + 4]), __uint_as_float(rr[j + 5]));
-                            e3 = max3f(e3, __uint_as_float(rr[j + 6]), __uint_as_float(rr[j + 7]));
-                        }
-                    };
-                    fold(sc0);
-                    fold(sc1);
-                    fold(sc2);
-                    fold(sc3);
-                    const float mt = max3f(fmaxf(e0, e1), e2, e3);
+                    const float mt = fmaf(form.ascending ? row_max(sc0, sc1, sc2, sc3) : row_min(sc0, sc1, sc2, sc3), form.mul, form.add);
                     bump = mt > m + Cfg::RESCALE_LOG2;   // always from -inf
                     if (bump) {
                         factor = (m == -INFINITY) ? 0.0f : ex2_approx(m - mt);
                         m = mt;
                     }
                     l *= factor;
-                    const float neg_m = (m == -INFINITY) ? 0.0f : -m;
+                    const float neg_m = form.add - ((m == -INFINITY) ? 0.0f : m), mul = form.mul;
                     float ls0 = 0.0f, ls1 = 0.0f;
                     auto chunk_p = [&](const uint32_t (&rr)[32], int c) {
                         uint32_t packed[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            const float p0 = ex2_approx(__uint_as_float(rr[2 * j]) + neg_m);
-                            const float p1 = ex2_approx(__uint_as_float(rr[2 * j + 1]) + neg_m);
+                            float x0, x1;
+                            ffma2(x0, x1, __uint_as_float(rr[2 * j]), __uint_as_float(rr[2 * j + 1]), mul, mul, neg_m, neg_m);
+                            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
                             fadd2(ls0, ls1, p0, p1);
                             packed[j] = Elem<T>::pack(p0, p1);
                         }

@@ -59,6 +59,13 @@ bool share(const Strided& a, int64_t a_heads, int64_t a_rows, const Strided& b, 
     return !(at >= b_wide && at + a_wide <= pitch);
 }
 
+// A capped score is off by about cap 2^-23, so caps end at 1024; one so small that scale / cap
+// overflows has no use.
+bool bad_score(float scale, float cap) {
+    return !std::isfinite(scale) || !(cap >= 0.0f) || cap > 1024.0f ||
+           (cap > 0.0f && std::fabs((double)(scale != 0.0f ? scale : 1.0f)) / (double)cap > 1e30);
+}
+
 gsr_status check_desc(const gsr_attention_desc* d) {
     if (!d) return GSR_ERR_INVALID_ARG;
     for (int64_t n : {d->batch, d->heads_q, d->heads_kv, d->seq_q, d->seq_kv, d->num_docs})
@@ -66,7 +73,7 @@ gsr_status check_desc(const gsr_attention_desc* d) {
     if (d->head_dim != 64 && d->head_dim != 128) return GSR_ERR_INVALID_ARG;
     if (d->dtype != GSR_F16 && d->dtype != GSR_BF16) return GSR_ERR_INVALID_ARG;
     if (d->heads_q > 0 && (d->heads_kv == 0 || d->heads_q % d->heads_kv)) return GSR_ERR_INVALID_ARG;
-    if (!std::isfinite(d->softmax_scale) || !std::isfinite(d->softcap) || d->softcap < 0.0f) return GSR_ERR_INVALID_ARG;
+    if (bad_score(d->softmax_scale, d->softcap)) return GSR_ERR_INVALID_ARG;
     if (d->seq_q > INT_MAX - 256 || d->seq_kv > INT_MAX - 256) return GSR_ERR_INVALID_ARG;
     if ((d->num_docs > 0) != (d->doc_bounds != nullptr)) return GSR_ERR_INVALID_ARG;
     if (d->num_docs > 0 && d->seq_q != d->seq_kv) return GSR_ERR_INVALID_ARG;   // documents mask a row with itself
@@ -143,7 +150,7 @@ int heads_in_l2(int causal, int64_t bytes, int64_t group, int64_t heads) {
 
 // Layout of the backward pass's workspace, 256-byte pieces.
 struct BwdLayout {
-    int64_t sp, offset, delta, lo, hi, total;
+    int64_t sp, offset, delta, total;
 };
 BwdLayout bwd_layout(const gsr_attention_desc* d) {
     auto piece = [](int64_t bytes) { return (bytes + 255) / 256 * 256; };
@@ -151,9 +158,7 @@ BwdLayout bwd_layout(const gsr_attention_desc* d) {
     w.sp = (d->seq_q + 127) / 128 * 128;
     w.offset = 256;                                                     // the norms come first
     w.delta = w.offset + piece(4 * d->batch * d->heads_q * w.sp);
-    w.lo = w.delta + piece(4 * d->batch * d->heads_q * w.sp);
-    w.hi = w.lo + piece(4 * d->batch * w.sp);
-    w.total = w.hi + piece(4 * d->batch * w.sp);
+    w.total = w.delta + piece(4 * d->batch * d->heads_q * w.sp);
     return w;
 }
 
@@ -196,7 +201,7 @@ gsr_status check_tree_desc(const gsr_tree_desc* desc) {
     if (d.max_nodes < 1 || d.max_nodes > GSR_TREE_MAX_NODES) return GSR_ERR_INVALID_ARG;
     if (d.heads_q > 0 && (d.heads_kv == 0 || d.heads_q % d.heads_kv || d.heads_q / d.heads_kv > 128 || d.heads_q > 65535))
         return GSR_ERR_INVALID_ARG;
-    if (!std::isfinite(d.softmax_scale) || !std::isfinite(d.softcap) || d.softcap < 0.0f) return GSR_ERR_INVALID_ARG;
+    if (bad_score(d.softmax_scale, d.softcap)) return GSR_ERR_INVALID_ARG;
     if (d.page_size < 8 || d.page_size % 8 || d.table_width * d.page_size > INT_MAX - 256) return GSR_ERR_INVALID_ARG;
     return GSR_OK;
 }
@@ -302,8 +307,6 @@ gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor
     p.Sp = (int)w.sp;
     p.offset = reinterpret_cast<float*>(base + w.offset);
     p.neg_delta = reinterpret_cast<float*>(base + w.delta);
-    p.lo = reinterpret_cast<int*>(base + w.lo);
-    p.hi = reinterpret_cast<int*>(base + w.hi);
     p.timeout_ns = gsr::host::wait_timeout_ns();
     p.test_flags = gsr::host::test_flags();
     gsr::MaskedBwdMaps tm;

@@ -61,10 +61,8 @@ struct MaskedBwdParams {
     Strided dO, Q, K, V, O, dQ, dK, dV;
     const float* lse;           // (B, Hq, Sq)
     int Sp;                     // Sq rounded up to a multiple of 128
-    float* offset;              // (B, Hq, Sp): P's power of two less lse log2(e); -inf for rows without keys and padding
+    float* offset;              // (B, Hq, Sp): row_offset less lse log2(e); -inf for rows without keys and padding
     float* neg_delta;           // (B, Hq, Sp): -rowsum(dO * O)
-    int* lo;                    // (B, Sp): each query's interval
-    int* hi;
     unsigned* norms;            // [0] max |dO_i|^2, [1] max |V_j|^2, as the bits of a float (fp16 only)
     int q_head_group, kv_head_group;   // item order of dQ, of dK and dV: heads taken together
     int* err;
