@@ -41,7 +41,7 @@ __device__ __forceinline__ float ds_shift(const unsigned* norms) {
 }
 
 // What a row's exponent offset holds beside -lse: P's power of two, and the constant of a capped
-// score without a bias (weights_chunk).
+// score (weights_chunk).
 template <class T>
 __device__ __forceinline__ float row_offset(const ScoreArgs& sc) {
     return kPShift<T> + (sc.cap_in != 0.0f ? sc.cap_out : 0.0f);
@@ -251,12 +251,7 @@ __device__ __forceinline__ void weights_chunk(uint32_t (&rr)[32], const ScoreArg
         float y0 = __uint_as_float(rr[i]), y1 = __uint_as_float(rr[i + 1]), c0, c1;
         const float2 o = off(i);
         if (MODE == kScoreCap) {
-            fmul2(y0, y1, y0, y1, sc.cap_in, sc.cap_in);
-            y0 = ex2_approx(y0);
-            y1 = ex2_approx(y1);
-            fadd2(y0, y1, 1.0f, 1.0f);
-            y0 = rcp_approx(y0);
-            y1 = rcp_approx(y1);
+            cap_r2(y0, y1, sc.cap_in);
             ffma2(c0, c1, y0, y1, -y0, -y1, y0, y1);
             ffma2(y0, y1, y0, y1, -2.0f * sc.cap_out, -2.0f * sc.cap_out, o.x, o.y);
         } else {

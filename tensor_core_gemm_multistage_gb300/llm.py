@@ -5,7 +5,9 @@ from __future__ import annotations
 
 import ctypes
 
-from .binding import GsrError, Status, _stream_handle, lib
+import torch
+
+from .binding import GsrError, Status, lib
 
 TREE_MAX_NODES = 64
 
@@ -52,32 +54,38 @@ def _declare(L) -> None:
     L.kv_cache_append.argtypes = [ts, ts, vp, ts, ts] + [i64] * 5 + [vp]
 
 
-def _call(dev, stream, name, run):
-    """run(library, stream handle) with `dev` current; raises GsrError unless it returns GSR_OK."""
-    import torch
-    L = lib()
-    if torch.cuda.current_device() == dev.index:
-        s = run(L, _stream_handle(stream, dev) or None)
+def _handle(stream, index):
+    """The CUDA handle of `stream` (None: the current stream of the device), or None for the default
+    stream.  The raw query is the one behind torch.cuda.current_stream, without the Stream object."""
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return (raw(index) if raw else torch.cuda.current_stream(index).cuda_stream) or None
+    return (stream if isinstance(stream, int) else stream.cuda_stream) or None
+
+
+def _call(index, stream, name, function, *args):
+    """function(*args, stream handle) with the device current; raises GsrError unless it returns GSR_OK."""
+    if torch.cuda.current_device() == index:
+        s = function(*args, _handle(stream, index))
     else:
-        with torch.cuda.device(dev):
-            s = run(L, _stream_handle(stream, dev) or None)
-    if s != Status.OK:
+        with torch.cuda.device(index):
+            s = function(*args, _handle(stream, index))
+    if s != 0:
         raise GsrError(s, name)
 
 
 def _dtype_code(t, name):
-    import torch
-    if t.dtype == torch.float16:
+    if t.dtype is torch.float16:
         return 0
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return 1
     raise TypeError("%s must be float16 or bfloat16, got %s" % (name, t.dtype))
 
 
-def _operand(t, name, shape, dtype, dev):
+def _operand(t, name, shape, dtype, index):
     """The C view of a 4-D operand (batch, head, row, D) of the given shape."""
-    if t.dtype != dtype or t.device != dev:
-        raise ValueError("%s must be %s on %s, got %s on %s" % (name, dtype, dev, t.dtype, t.device))
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError("%s must be %s on cuda:%d, got %s on %s" % (name, dtype, index, t.dtype, t.device))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     sb, sh, sr, sd = t.stride()
@@ -86,50 +94,57 @@ def _operand(t, name, shape, dtype, dev):
     return _Tensor(t.data_ptr() or None, sb, sh, sr)
 
 
-def _vector(t, name, shape, dtype, dev):
-    """The address of a contiguous device array of the given shape, or None."""
+def _vector(t, name, count, dtype, index):
+    """The address of a contiguous device array of `count` values, or None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != dev or not t.is_contiguous() or tuple(t.shape) not in shape:
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, got %s %s on %s"
-                         % (name, dtype, " or ".join(str(s) for s in shape), dev, t.dtype, tuple(t.shape), t.device))
+    if t.dtype is not dtype or t.get_device() != index or t.numel() != count or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of %d values on cuda:%d, got %s %s on %s"
+                         % (name, dtype, count, index, t.dtype, tuple(t.shape), t.device))
     return t.data_ptr() or None
 
 
-def _scratch(workspace, nbytes, dev, stream):
-    """The caller's workspace, or a new one that lives until the work queued on `stream` is done."""
-    import torch
+def _scratch(workspace, nbytes, index, stream):
+    """Address and size of the caller's workspace, or of a new one that lives until the work queued on
+    `stream` is done."""
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on %s" % dev)
-        return workspace
-    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on cuda:%d" % index)
+        return workspace, workspace.numel() * workspace.element_size()
+    nbytes = max(nbytes, 16)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
     if stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream)
-    return ws
+        ws.record_stream(torch.cuda.ExternalStream(stream, device=ws.device) if isinstance(stream, int) else stream)
+    return ws, nbytes
 
 
 def _attention_desc(Q, K, softmax_scale, causal, softcap, alibi_slopes, doc_bounds, prefix_lens):
-    import torch
-    code = _dtype_code(Q, "Q")
-    if Q.dim() != 4 or K.dim() != 4:
-        raise ValueError("Q and K must be 4-D (batch, heads, seq, head_dim)")
-    B, Hq, Sq, D = Q.shape
-    Hkv, Skv = K.shape[1], K.shape[2]
-    dev = Q.device
-    if dev.type != "cuda":
+    """The C description, Q's and K's shapes, and the device."""
+    code, index = _dtype_code(Q, "Q"), Q.get_device()
+    if index < 0:
         raise ValueError("Q must be a CUDA tensor")
+    qs, ks = Q.shape, K.shape
+    if len(qs) != 4 or len(ks) != 4:
+        raise ValueError("Q and K must be 4-D (batch, heads, seq, head_dim)")
+    B, Hq, Sq, D = qs
     docs = 0
     if doc_bounds is not None:
-        if doc_bounds.dim() != 2 or doc_bounds.shape[1] < 2:
+        if doc_bounds.dim() != 2 or doc_bounds.shape[0] != B or doc_bounds.shape[1] < 2:
             raise ValueError("doc_bounds must be (batch, documents + 1), got %s" % (tuple(doc_bounds.shape),))
         docs = doc_bounds.shape[1] - 1
-    prefix_shapes = ((B, max(docs, 1)), (B,)) if docs <= 1 else ((B, docs),)
-    return _AttentionDesc(
-        B, Hq, Hkv, Sq, Skv, D, code, 1 if causal else 0, softmax_scale, softcap,
-        _vector(alibi_slopes, "alibi_slopes", ((Hq,),), torch.float32, dev),
-        _vector(doc_bounds, "doc_bounds", ((B, docs + 1),), torch.int32, dev), docs,
-        _vector(prefix_lens, "prefix_lens", prefix_shapes, torch.int32, dev)), (B, Hq, Sq, D), (B, Hkv, Skv, D)
+    if prefix_lens is not None and prefix_lens.shape != (B, docs or 1) and (docs > 1 or prefix_lens.shape != (B,)):
+        raise ValueError("prefix_lens must be (batch, %d), got %s" % (docs or 1, tuple(prefix_lens.shape)))
+    desc = _AttentionDesc(B, Hq, ks[1], Sq, ks[2], D, code, 1 if causal else 0, softmax_scale, softcap,
+                          _vector(alibi_slopes, "alibi_slopes", Hq, torch.float32, index),
+                          _vector(doc_bounds, "doc_bounds", B * (docs + 1), torch.int32, index), docs,
+                          _vector(prefix_lens, "prefix_lens", B * (docs or 1), torch.int32, index))
+    return desc, qs, (B, ks[1], ks[2], D), index
+
+
+def _lse(lse, qs, index):
+    if lse is not None and lse.shape != qs[:3]:
+        raise ValueError("lse must have shape %s, got %s" % (tuple(qs[:3]), tuple(lse.shape)))
+    return _vector(lse, "lse", qs[0] * qs[1] * qs[2], torch.float32, index)
 
 
 def masked_attention_fwd(Q, K, V, O, lse=None, softmax_scale: float = 0.0, causal: bool = False,
@@ -143,13 +158,10 @@ def masked_attention_fwd(Q, K, V, O, lse=None, softmax_scale: float = 0.0, causa
     queries inside their document (positions outside all documents are padding); ``prefix_lens``
     (B,) or (B, n) int32, with ``causal``, lets every query see that many leading keys.
     """
-    import torch
-    d, qs, ks = _attention_desc(Q, K, softmax_scale, causal, softcap, alibi_slopes, doc_bounds, prefix_lens)
-    dt, dev = Q.dtype, Q.device
-    args = [_operand(Q, "Q", qs, dt, dev), _operand(K, "K", ks, dt, dev), _operand(V, "V", ks, dt, dev),
-            _operand(O, "O", qs, dt, dev)]
-    lse_ptr = _vector(lse, "lse", (qs[:3],), torch.float32, dev)
-    _call(dev, stream, "masked_attention_fwd", lambda L, st: L.masked_attention_fwd(d, *args, lse_ptr, st))
+    d, qs, ks, dev = _attention_desc(Q, K, softmax_scale, causal, softcap, alibi_slopes, doc_bounds, prefix_lens)
+    dt = Q.dtype
+    _call(dev, stream, "masked_attention_fwd", lib().masked_attention_fwd, d, _operand(Q, "Q", qs, dt, dev),
+          _operand(K, "K", ks, dt, dev), _operand(V, "V", ks, dt, dev), _operand(O, "O", qs, dt, dev), _lse(lse, qs, dev))
     return O
 
 
@@ -162,17 +174,13 @@ def masked_attention_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, softmax_scale: float =
     ``workspace``: optional device buffer of masked_attention_bwd_workspace(...) bytes; without one
     the call takes it from PyTorch's allocator.
     """
-    import torch
-    d, qs, ks = _attention_desc(Q, K, softmax_scale, causal, softcap, alibi_slopes, doc_bounds, prefix_lens)
-    dt, dev = Q.dtype, Q.device
-    dO_, Q_, O_, dQ_ = (_operand(t, n, qs, dt, dev) for t, n in ((dO, "dO"), (Q, "Q"), (O, "O"), (dQ, "dQ")))
-    K_, V_, dK_, dV_ = (_operand(t, n, ks, dt, dev) for t, n in ((K, "K"), (V, "V"), (dK, "dK"), (dV, "dV")))
-    lse_ptr = _vector(lse, "lse", (qs[:3],), torch.float32, dev)
-    need = lib().masked_attention_bwd_workspace(d)
-    ws = _scratch(workspace, need, dev, stream)
-    _call(dev, stream, "masked_attention_bwd",
-          lambda L, st: L.masked_attention_bwd(d, dO_, Q_, K_, V_, O_, lse_ptr, dQ_, dK_, dV_, ws.data_ptr(),
-                                               ws.numel() * ws.element_size(), st))
+    d, qs, ks, dev = _attention_desc(Q, K, softmax_scale, causal, softcap, alibi_slopes, doc_bounds, prefix_lens)
+    dt, L = Q.dtype, lib()
+    ws, size = _scratch(workspace, L.masked_attention_bwd_workspace(d), dev, stream)
+    _call(dev, stream, "masked_attention_bwd", L.masked_attention_bwd, d, _operand(dO, "dO", qs, dt, dev),
+          _operand(Q, "Q", qs, dt, dev), _operand(K, "K", ks, dt, dev), _operand(V, "V", ks, dt, dev),
+          _operand(O, "O", qs, dt, dev), _lse(lse, qs, dev), _operand(dQ, "dQ", qs, dt, dev),
+          _operand(dK, "dK", ks, dt, dev), _operand(dV, "dV", ks, dt, dev), ws.data_ptr(), size)
     return dQ, dK, dV
 
 
@@ -184,14 +192,14 @@ def masked_attention_bwd_workspace(B: int, Hq: int, Hkv: int, Sq: int, Skv: int,
     return n
 
 
-def _cache(t, name, H, D, dtype, dev):
+def _cache(t, name, shape, dtype, index):
     """The C view of a cache (pages, page_size, heads, D)."""
-    if t.dtype != dtype or t.device != dev:
-        raise ValueError("%s must be %s on %s, got %s on %s" % (name, dtype, dev, t.dtype, t.device))
-    if t.dim() != 4 or t.shape[2] != H or t.shape[3] != D:
-        raise ValueError("%s must be (pages, page_size, %d, %d), got %s" % (name, H, D, tuple(t.shape)))
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError("%s must be %s on cuda:%d, got %s on %s" % (name, dtype, index, t.dtype, t.device))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     sp, sr, sh, sd = t.stride()
-    if sd != 1 and D > 1:
+    if sd != 1 and shape[3] > 1:
         raise ValueError("%s: the last dimension must be contiguous" % name)
     return _Tensor(t.data_ptr() or None, sp, sh, sr)
 
@@ -208,16 +216,14 @@ def tree_attention_fwd(Q, k_cache, v_cache, block_tables, kv_lens, q_starts, par
     tree, its ancestors and itself.  ``max_nodes`` bounds the nodes of one request (at most 64); 1 is
     ordinary decoding.
     """
-    import torch
-    code, dev = _dtype_code(Q, "Q"), Q.device
-    if Q.dim() != 3 or dev.type != "cuda":
+    code, dev, dt, i32 = _dtype_code(Q, "Q"), Q.get_device(), Q.dtype, torch.int32
+    if Q.dim() != 3 or dev < 0:
         raise ValueError("Q must be a 3-D CUDA tensor (tokens, heads, head_dim)")
     N, Hq, D = Q.shape
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must be 4-D of one shape, got %s and %s"
-                         % (tuple(k_cache.shape), tuple(v_cache.shape)))
-    pages, page, Hkv = k_cache.shape[:3]
-    if O.shape != Q.shape or O.dtype != Q.dtype or O.device != dev:
+    cache = k_cache.shape
+    if len(cache) != 4 or cache[3] != D:
+        raise ValueError("k_cache must be (pages, page_size, heads, %d), got %s" % (D, tuple(cache)))
+    if O.shape != Q.shape or O.dtype is not dt or O.get_device() != dev:
         raise ValueError("O must be like Q")
     (qr, qh, qd), (orow, oh, od) = Q.stride(), O.stride()
     if qd != 1 or od != 1:
@@ -225,17 +231,15 @@ def tree_attention_fwd(Q, k_cache, v_cache, block_tables, kv_lens, q_starts, par
     if block_tables.dim() != 2:
         raise ValueError("block_tables must be (requests, width)")
     B, W = block_tables.shape
-    i32 = torch.int32
-    K_, V_ = _cache(k_cache, "k_cache", Hkv, D, Q.dtype, dev), _cache(v_cache, "v_cache", Hkv, D, Q.dtype, dev)
-    ptrs = [_vector(block_tables, "block_tables", ((B, W),), i32, dev), _vector(kv_lens, "kv_lens", ((B,),), i32, dev),
-            _vector(q_starts, "q_starts", ((B + 1,),), i32, dev), _vector(parents, "parents", ((N,),), i32, dev)]
-    d = _TreeDesc(B, N, Hq, Hkv, D, pages, page, W, max_nodes, qr, qh, orow, oh, code, softmax_scale, softcap,
-                  _vector(alibi_slopes, "alibi_slopes", ((Hq,),), torch.float32, dev))
-    need = lib().tree_attention_workspace(d)
-    ws = _scratch(workspace, need, dev, stream)
-    _call(dev, stream, "tree_attention_fwd",
-          lambda L, st: L.tree_attention_fwd(d, Q.data_ptr() or None, K_, V_, *ptrs, O.data_ptr() or None,
-                                             ws.data_ptr(), ws.numel() * ws.element_size(), st))
+    d = _TreeDesc(B, N, Hq, cache[2], D, cache[0], cache[1], W, max_nodes, qr, qh, orow, oh, code, softmax_scale, softcap,
+                  _vector(alibi_slopes, "alibi_slopes", Hq, torch.float32, dev))
+    L = lib()
+    ws, size = _scratch(workspace, L.tree_attention_workspace(d), dev, stream)
+    _call(dev, stream, "tree_attention_fwd", L.tree_attention_fwd, d, Q.data_ptr() or None,
+          _cache(k_cache, "k_cache", cache, dt, dev), _cache(v_cache, "v_cache", cache, dt, dev),
+          _vector(block_tables, "block_tables", B * W, i32, dev), _vector(kv_lens, "kv_lens", B, i32, dev),
+          _vector(q_starts, "q_starts", B + 1, i32, dev), _vector(parents, "parents", N, i32, dev),
+          O.data_ptr() or None, ws.data_ptr(), size)
     return O
 
 
@@ -249,39 +253,38 @@ def kv_block_tables(kv_lens, new_lens, free_blocks, free_head, block_tables, pag
     last), counts = (new tokens, pages taken, pages missing).  All int32; nothing is read back to the
     host.  Returns slots.
     """
-    import torch
-    i32, dev = torch.int32, kv_lens.device
-    if dev.type != "cuda":
+    i32, dev = torch.int32, kv_lens.get_device()
+    if dev < 0:
         raise ValueError("kv_lens must be a CUDA tensor")
-    B = kv_lens.shape[0]
-    W, F, N = block_tables.shape[-1], free_blocks.shape[0], slots.shape[0]
-    ptrs = [_vector(t, n, (s,), i32, dev) for t, n, s in (
-        (kv_lens, "kv_lens", (B,)), (new_lens, "new_lens", (B,)), (free_blocks, "free_blocks", (F,)),
-        (free_head, "free_head", (1,)), (block_tables, "block_tables", (B, W)), (kv_lens_out, "kv_lens_out", (B,)),
-        (free_head_out, "free_head_out", (1,)), (q_starts, "q_starts", (B + 1,)), (positions, "positions", (N,)),
-        (slots, "slots", (N,)), (counts, "counts", (3,)))]
-    _call(dev, stream, "kv_block_tables", lambda L, st: L.kv_block_tables(*ptrs, B, W, page_size, F, N, st))
+    B, F, N = kv_lens.numel(), free_blocks.numel(), slots.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be (%d, width), got %s" % (B, tuple(block_tables.shape)))
+    W = block_tables.shape[1]
+    _call(dev, stream, "kv_block_tables", lib().kv_block_tables, _vector(kv_lens, "kv_lens", B, i32, dev),
+          _vector(new_lens, "new_lens", B, i32, dev), _vector(free_blocks, "free_blocks", F, i32, dev),
+          _vector(free_head, "free_head", 1, i32, dev), _vector(block_tables, "block_tables", B * W, i32, dev),
+          _vector(kv_lens_out, "kv_lens_out", B, i32, dev), _vector(free_head_out, "free_head_out", 1, i32, dev),
+          _vector(q_starts, "q_starts", B + 1, i32, dev), _vector(positions, "positions", N, i32, dev),
+          _vector(slots, "slots", N, i32, dev), _vector(counts, "counts", 3, i32, dev), B, W, page_size, F, N)
     return slots
 
 
 def kv_cache_append(K, V, slots, k_cache, v_cache, stream=None):
     """Writes the rows of K and V (N, H, D) to the cache rows slots (N,) int32 names (page *
     page_size + row; negative: skipped).  Caches (pages, page_size, H, D); any 16-bit type."""
-    import torch
-    dev, dt = k_cache.device, k_cache.dtype
-    if dev.type != "cuda" or dt not in (torch.float16, torch.bfloat16):
-        raise ValueError("k_cache must be a float16 or bfloat16 CUDA tensor")
-    if K.dim() != 3 or K.shape != V.shape:
-        raise ValueError("K and V must be (tokens, heads, head_dim), got %s and %s" % (tuple(K.shape), tuple(V.shape)))
-    N, H, D = K.shape
+    dev, dt, cache = k_cache.get_device(), k_cache.dtype, k_cache.shape
+    if dev < 0 or dt not in (torch.float16, torch.bfloat16) or len(cache) != 4:
+        raise ValueError("k_cache must be a 4-D float16 or bfloat16 CUDA tensor (pages, page_size, heads, head_dim)")
+    rows = K.shape
+    if len(rows) != 3 or rows[1:] != cache[2:] or V.shape != rows:
+        raise ValueError("K and V must be (tokens, %d, %d), got %s and %s"
+                         % (cache[2], cache[3], tuple(rows), tuple(V.shape)))
     views = []
     for t, name in ((K, "K"), (V, "V")):
-        if t.dtype != dt or t.device != dev or (t.stride(2) != 1 and D > 1):
-            raise ValueError("%s must be %s on %s with a contiguous last dimension" % (name, dt, dev))
-        views.append(_Tensor(t.data_ptr() or None, 0, t.stride(1), t.stride(0)))
-    kc, vc = _cache(k_cache, "k_cache", H, D, dt, dev), _cache(v_cache, "v_cache", H, D, dt, dev)
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache differ in shape")
-    at = _vector(slots, "slots", ((N,),), torch.int32, dev)
-    _call(dev, stream, "kv_cache_append",
-          lambda L, st: L.kv_cache_append(*views, at, kc, vc, N, H, D, k_cache.shape[0], k_cache.shape[1], st))
+        row, head, one = t.stride()
+        if t.dtype is not dt or t.get_device() != dev or (one != 1 and rows[2] > 1):
+            raise ValueError("%s must be %s on cuda:%d with a contiguous last dimension" % (name, dt, dev))
+        views.append(_Tensor(t.data_ptr() or None, 0, head, row))
+    _call(dev, stream, "kv_cache_append", lib().kv_cache_append, views[0], views[1],
+          _vector(slots, "slots", rows[0], torch.int32, dev), _cache(k_cache, "k_cache", cache, dt, dev),
+          _cache(v_cache, "v_cache", cache, dt, dev), rows[0], rows[1], rows[2], cache[0], cache[1])
