@@ -147,7 +147,14 @@ __device__ __forceinline__ void cap_r2(float& s0, float& s1, float cap_in) {
     fmul2(s0, s1, r, r, b, a);
 }
 
-enum ScoreMode : int { kScorePlain = 0, kScoreBias = 1, kScoreCap = 2 };   // kScoreCap: a bias too, if there is one
+enum ScoreMode : int { kScorePlain = 0, kScoreBias = 1, kScoreCap = 2, kScoreCapBias = 3 };
+template <int MODE>
+constexpr bool kHasCap = MODE == kScoreCap || MODE == kScoreCapBias;
+template <int MODE>
+constexpr bool kHasBias = MODE == kScoreBias || MODE == kScoreCapBias;
+inline ScoreMode score_mode(const ScoreArgs& sc) {
+    return sc.cap_in != 0.0f ? (sc.slopes ? kScoreCapBias : kScoreCap) : (sc.slopes ? kScoreBias : kScorePlain);
+}
 
 // A row's scores while its softmax runs: registers hold v with score = mul v + add in log2 units, so
 // that the scaling is part of the exponent's multiply-add.  Plain scores keep the raw products;
@@ -161,7 +168,7 @@ struct ScoreForm {
 template <int MODE>
 __device__ __forceinline__ ScoreForm score_form(const ScoreArgs& sc) {
     if (MODE == kScorePlain) return {sc.sl2, 0.0f, sc.sl2 >= 0.0f};
-    if (MODE == kScoreCap && !sc.slopes) return {-2.0f * sc.cap_out, sc.cap_out, false};
+    if (MODE == kScoreCap) return {-2.0f * sc.cap_out, sc.cap_out, false};
     return {1.0f, 0.0f, true};
 }
 
@@ -185,7 +192,7 @@ __device__ __forceinline__ void score_chunk(uint32_t (&rr)[32], const ScoreArgs&
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
         float y0 = __uint_as_float(rr[i]), y1 = __uint_as_float(rr[i + 1]);
-        if (MODE == kScoreCap) {
+        if (kHasCap<MODE>) {
             fmul2(y0, y1, y0, y1, sc.cap_in, sc.cap_in);
             y0 = ex2_approx(y0);
             y1 = ex2_approx(y1);
@@ -195,8 +202,8 @@ __device__ __forceinline__ void score_chunk(uint32_t (&rr)[32], const ScoreArgs&
         } else {
             fmul2(y0, y1, y0, y1, sc.sl2, sc.sl2);
         }
-        if (MODE == kScoreBias || sc.slopes) {
-            if (MODE == kScoreCap)
+        if (kHasBias<MODE>) {
+            if (kHasCap<MODE>)
                 ffma2(y0, y1, y0, y1, -2.0f * sc.cap_out, -2.0f * sc.cap_out, sc.cap_out, sc.cap_out);
             y0 = fmaf(-slope2, fabsf(base - (float)i), y0);
             y1 = fmaf(-slope2, fabsf(base - (float)(i + 1)), y1);

@@ -250,27 +250,27 @@ __device__ __forceinline__ void weights_chunk(uint32_t (&rr)[32], const ScoreArg
     for (int i = 0; i < 32; i += 2) {
         float y0 = __uint_as_float(rr[i]), y1 = __uint_as_float(rr[i + 1]), c0, c1;
         const float2 o = off(i);
-        if (MODE == kScoreCap) {
+        if (kHasCap<MODE>) {
             cap_r2(y0, y1, sc.cap_in);
             ffma2(c0, c1, y0, y1, -y0, -y1, y0, y1);
             ffma2(y0, y1, y0, y1, -2.0f * sc.cap_out, -2.0f * sc.cap_out, o.x, o.y);
         } else {
             ffma2(y0, y1, y0, y1, sc.sl2, sc.sl2, o.x, o.y);
         }
-        if (MODE == kScoreBias || (MODE == kScoreCap && sc.slopes)) {
+        if (kHasBias<MODE>) {
             y0 = fmaf(-slope2, fabsf(base - (float)i), y0);
             y1 = fmaf(-slope2, fabsf(base - (float)(i + 1)), y1);
         }
         y0 = ex2_approx(y0);
         y1 = ex2_approx(y1);
         if (PACK) packed[i / 2] = Elem<T>::pack(y0, y1);
-        if (MODE == kScoreCap) fmul2(y0, y1, y0, y1, c0, c1);
+        if (kHasCap<MODE>) fmul2(y0, y1, y0, y1, c0, c1);
         rr[i] = __float_as_uint(y0);
         rr[i + 1] = __float_as_uint(y1);
     }
 }
 template <int MODE>
-constexpr float kCapFactor = MODE == kScoreCap ? 4.0f : 1.0f;
+constexpr float kCapFactor = kHasCap<MODE> ? 4.0f : 1.0f;
 
 // ---------------------------------------------------------------------------
 // dK and dV
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             int first = 0, end = 0;                      // the queries that see this thread's key
             if (j < mk.Skv) key_interval(mk, it.b, j, first, end);
             for (int h = it.hk * mk.group; ok && h < (it.hk + 1) * mk.group; ++h) {
-                const float slope2 = Cfg::MODE != kScorePlain && p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
+                const float slope2 = kHasBias<Cfg::MODE> ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
                 for (int t = it.t0; t < it.t1; ++t, ++n) {
                     const int i0 = t * kTile + half * 64;
                     const bool masked = i0 < first || i0 + 64 > end;
@@ -995,7 +995,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             int lo = 0, hi = 0;
             if (qi < mk.Sq) row_interval(mk, it.b, qi, lo, hi);
             const float off = p.offset[row] + shift, neg_delta = p.neg_delta[row];
-            const float slope2 = Cfg::MODE != kScorePlain && p.score.slopes ? __ldg(p.score.slopes + it.h) * kLog2e : 0.0f;
+            const float slope2 = kHasBias<Cfg::MODE> ? __ldg(p.score.slopes + it.h) * kLog2e : 0.0f;
             for (int t = it.t0; t < it.t1; ++t, ++n) {
                 const int k0 = t * kTile + half * 64;
                 const bool masked = k0 < lo || k0 + 64 > hi;
@@ -1131,9 +1131,12 @@ cudaError_t launch_bwd_type(const MaskedBwdMaps& tm, const MaskedBwdParams& p, c
     gsr_masked_bwd_rows_kernel<T, D><<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (p.score.cap_in != 0.0f) return launch_bwd_mode<T, D, kScoreCap>(tm, p, stream);
-    if (p.score.slopes) return launch_bwd_mode<T, D, kScoreBias>(tm, p, stream);
-    return launch_bwd_mode<T, D, kScorePlain>(tm, p, stream);
+    switch (score_mode(p.score)) {
+        case kScorePlain: return launch_bwd_mode<T, D, kScorePlain>(tm, p, stream);
+        case kScoreBias: return launch_bwd_mode<T, D, kScoreBias>(tm, p, stream);
+        case kScoreCap: return launch_bwd_mode<T, D, kScoreCap>(tm, p, stream);
+        default: return launch_bwd_mode<T, D, kScoreCapBias>(tm, p, stream);
+    }
 }
 
 }  // namespace gsr

@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
             const int t0 = q == 0 ? it.t0[0] : it.t0[1], t1 = q == 0 ? it.t1[0] : it.t1[1];
             int lo = 0, hi = 0;
             if (qi < mk.Sq && t0 < t1) row_interval(mk, it.b, qi, lo, hi);
-            const float slope2 = Cfg::MODE != kScorePlain && sc.slopes ? __ldg(sc.slopes + it.h) * kLog2e : 0.0f;
+            const float slope2 = kHasBias<Cfg::MODE> ? __ldg(sc.slopes + it.h) * kLog2e : 0.0f;
             float m = -INFINITY, l = 0.0f;
 
             for (int t = t0; t < t1; ++t) {
@@ -556,9 +556,12 @@ cudaError_t launch_masked_type(const MaskedFwdMaps& tm, const MaskedFwdParams& p
         gsr_masked_empty_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    if (p.score.cap_in != 0.0f) return launch_masked_cfg<MaskedFwdCfg<T, D, kScoreCap>>(tm, p, stream);
-    if (p.score.slopes) return launch_masked_cfg<MaskedFwdCfg<T, D, kScoreBias>>(tm, p, stream);
-    return launch_masked_cfg<MaskedFwdCfg<T, D, kScorePlain>>(tm, p, stream);
+    switch (score_mode(p.score)) {
+        case kScorePlain: return launch_masked_cfg<MaskedFwdCfg<T, D, kScorePlain>>(tm, p, stream);
+        case kScoreBias: return launch_masked_cfg<MaskedFwdCfg<T, D, kScoreBias>>(tm, p, stream);
+        case kScoreCap: return launch_masked_cfg<MaskedFwdCfg<T, D, kScoreCap>>(tm, p, stream);
+        default: return launch_masked_cfg<MaskedFwdCfg<T, D, kScoreCapBias>>(tm, p, stream);
+    }
 }
 
 }  // namespace gsr

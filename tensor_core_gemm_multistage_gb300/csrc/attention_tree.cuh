@@ -11,6 +11,11 @@
 // which an SM gets its share of HBM bandwidth for the tile, even with one row of the 128 in use.
 // Requests of more than 128 rows run two query tiles per pass (NQ = 2).
 //
+// Two softmax groups of four warps work on alternate products.  With two query tiles each has its
+// own; with one they take turns over the key tiles, each with its own maximum, sum and accumulator
+// (even and odd key tiles are two parts of one softmax), and add up at the end: one group alone
+// took 2500 cycles a key tile at D = 64, where HBM brings one in 1500.
+//
 //  * Work is split evenly whatever the lengths: all (request, key/value head, pair of query tiles)
 //    items' key tiles are laid end to end, and CTA c of G takes the range [U c / G, U (c+1) / G).
 //    Every CTA finds its range from kv_lens and q_starts by one sum over the requests, so the host
@@ -75,9 +80,10 @@ __device__ __forceinline__ uint64_t ancestors(const int* parents, int start, int
 // The depth of node t's ancestor (or of t itself) u: its own ancestors are those of t before it.
 __device__ __forceinline__ int depth_of(uint64_t see, int u) { return __popcll(see & ((1ull << u) - 1)); }
 
-// Node t, query head h, by one warp: every key it sees, in fp32.
+// Node t, query head h, by one warp: every key it sees, in fp32.  `half` 0 or 1 writes that half of
+// the columns, -1 all.
 template <class T, int D>
-__device__ __noinline__ void tree_row(const TreeParams& p, int b, const TreeRequest& r, int t, int h, int lane) {
+__device__ __noinline__ void tree_row(const TreeParams& p, int b, const TreeRequest& r, int t, int h, int half, int lane) {
     const uint64_t see = ancestors(p.parents, r.start, t);
     const int ctx = r.ctx, pos = ctx + __popcll(see) - 1;
     const float slope2 = p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
@@ -106,7 +112,7 @@ __device__ __noinline__ void tree_row(const TreeParams& p, int b, const TreeRequ
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] *= inv;
-    store_row<T, D>(static_cast<T*>(p.O) + row * p.o_row + h * p.o_head, lane, acc);
+    if (half < 0 || half == lane >> 4) store_row<T, D>(static_cast<T*>(p.O) + row * p.o_row + h * p.o_head, lane, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -120,8 +126,11 @@ struct TreeCfg {
     static constexpr int CHUNK_BYTES = 128 * 128;
     static constexpr int TILE_BYTES = 128 * D * 2;
     static constexpr int NB = D == 128 ? (NQ == 1 ? 6 : 5) : 12;   // ring of K and V tiles
-    static constexpr int SM_THREADS = 128 * NQ;
-    static constexpr int NUM_THREADS = 64 + SM_THREADS;
+    static constexpr int SM_THREADS = 256;            // two softmax groups of four warps
+    static constexpr int NUM_THREADS = 128 + SM_THREADS;
+    // 384 threads start with 168 registers each; the copying and issuing warps' group gives some to
+    // the softmax groups, whose threads hold a row of 128 scores: 72 + 2 x 216 = 3 x 168
+    static constexpr int CONTROL_REGS = 72, SOFTMAX_REGS = 216;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = OFF_Q + NQ * TILE_BYTES;
     static constexpr int OFF_BAR = OFF_RING + NB * TILE_BYTES;
@@ -129,7 +138,8 @@ struct TreeCfg {
     static constexpr int OFF_VALID = OFF_BAR + NUM_BARS * 8;       // per ring entry: which pieces of the tile exist
     static constexpr int OFF_ITEM = OFF_VALID + NB * 4;            // 2 x 12 ints
     static constexpr int OFF_SCAN = (OFF_ITEM + 96 + 7) / 8 * 8;   // 16 partial sums, then the CTA's first unit
-    static constexpr int OFF_MISC = OFF_SCAN + 16 * 8 + 16;
+    static constexpr int OFF_ML = OFF_SCAN + 16 * 8 + 16;          // 2 groups x 128 rows of (m, l)
+    static constexpr int OFF_MISC = OFF_ML + 2 * 128 * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16;
     static constexpr uint32_t T_S = 0, T_O = 256, P_COL = 64;
     static constexpr uint32_t IDESC_S = idesc_16_f32(Elem<T>::bf16, 128, 128, false, false);
@@ -175,8 +185,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
     auto odone = [&](int q) { return bar(2 * NB + 4 + q); };
     auto item_pub = [&](int i) { return bar(2 * NB + 6 + i); };
     auto item_read = [&](int i) { return bar(2 * NB + 8 + i); };
-    const uint32_t q_full = bar(2 * NB + 10), q_free = bar(2 * NB + 11), drain = bar(2 * NB + 12);
-    auto pv_done = [&](uint32_t m) { return bar(2 * NB + 13 + (int)(m & 1u)); };   // PV of tile m (NQ = 1)
+    const uint32_t q_full = bar(2 * NB + 10), q_free = bar(2 * NB + 11), drain = bar(2 * NB + 12), ml_full = bar(2 * NB + 13),
+                   ml_free = bar(2 * NB + 14);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_MISC + 4);
     volatile int* item_box = reinterpret_cast<volatile int*>(smem + Cfg::OFF_ITEM);
@@ -211,8 +221,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
         }
         mbar_init(q_full, 1);
         mbar_init(q_free, 1);
-        mbar_init(pv_done(0), 1);
-        mbar_init(pv_done(1), 1);
+        mbar_init(ml_full, Cfg::SM_THREADS / 32);
+        mbar_init(ml_free, Cfg::SM_THREADS / 32);
         mbar_init(drain, 1);
         *abort_flag = 0u;
         fence_mbarrier_init();
@@ -271,207 +281,214 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
         return Item{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], v[8], v[9], v[10], v[11]};
     };
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ items + TMA producer
-        const uint64_t pol = l2_policy_evict_normal();
-        const int pieces = p.tile_keys / p.piece, per_page = p.page / p.piece;
-        uint32_t n_pub = 0, n = 0;                       // items published, tiles
-        uint32_t armed = 0, parity = 0;
-        bool drop = (p.test_flags & kTestDropFirstLoad) && blockIdx.x == 0;
-        bool ok = true;
-        int b = (int)first_box[0];
-        long long off = first_box[1];
-        TreeRequest r = tree_request(p, b);
-        for (long long u = u_begin;;) {
-            Item it{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, -1, 0};
-            while (u < u_end && b < p.B && off >= r.units(p.Hkv)) {      // the range goes on in a later request
-                off = 0;
-                if (++b < p.B) r = tree_request(p, b);
-            }
-            if (u < u_end && b < p.B) {
-                const int index = (int)(off / r.key_tiles);
-                it.b = b;
-                it.hk = index / r.q_pairs;
-                it.n0 = (index - it.hk * r.q_pairs) * p.tile_nodes * NQ;
-                it.t0 = (int)(off - (long long)index * r.key_tiles);
-                it.t1 = (int)min((long long)r.key_tiles, it.t0 + (u_end - u));
-                it.tiles = r.key_tiles;
-                it.start = r.start;
-                it.nodes = r.nodes;
-                it.kv = r.kv;
-                it.ctx = r.ctx;
-                it.q_tiles = NQ == 1 || r.nodes - it.n0 <= p.tile_nodes ? 1 : 2;
-                if (it.t0 > 0 || it.t1 < it.tiles) it.slot = 2 * blockIdx.x + (u > u_begin ? 1 : 0);
-            }
-            const uint32_t box = n_pub & 1u;
-            ok = lane != 0 || w.wait(item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            if (lane == 0) {
-                volatile int* v = item_box + 12 * box;
-                v[0] = it.b;
-                v[1] = it.hk;
-                v[2] = it.n0;
-                v[3] = it.t0;
-                v[4] = it.t1;
-                v[5] = it.tiles;
-                v[6] = it.start;
-                v[7] = it.nodes;
-                v[8] = it.kv;
-                v[9] = it.ctx;
-                v[10] = it.slot;
-                v[11] = it.q_tiles;
-                mbar_arrive(item_pub(box));
-            }
-            ++n_pub;
-            if (it.b < 0) break;
-            // this lane's piece of the next tile: its page, and whether it exists
-            auto look_up = [&](int t, int& page, int& row) {
-                const int at = t * pieces + lane;        // piece of the request
-                page = -1;
-                if (lane < pieces && at * p.piece < it.kv) page = __ldg(p.table + (long long)it.b * p.table_width + at / per_page);
-                if (page >= p.num_pages) page = -1;
-                row = at % per_page * p.piece;
-            };
-            int page, row, next_page, next_row;
-            look_up(it.t0, page, row);
-            if (lane == 0) {
-                ok = n_pub == 1 || w.wait(q_free, n_pub & 1u, kDevErrProducerEmpty);   // the previous item's
-                if (ok && !drop) {
-                    mbar_arrive_expect_tx(q_full, it.q_tiles * p.tile_nodes * p.group * 128 * DCH);
-                    for (int q = 0; q < it.q_tiles; ++q)
-#pragma unroll
-                        for (int c = 0; c < DCH; ++c)
-                            tma_load_4d(sb + Cfg::OFF_Q + q * Cfg::TILE_BYTES + c * Cfg::CHUNK_BYTES, &tmQ, q_full, c * 64, 0,
-                                        it.hk, it.start + it.n0 + q * p.tile_nodes, pol);
-                    armed |= 1u << NB;
-                    parity = (parity & ~(1u << NB)) | ((n_pub - 1) & 1u) << NB;
+    if (warp < 4) {
+        reg_dec<Cfg::CONTROL_REGS>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ items + TMA producer
+            const uint64_t pol = l2_policy_evict_normal();
+            const int pieces = p.tile_keys / p.piece, per_page = p.page / p.piece;
+            uint32_t n_pub = 0, n = 0;                       // items published, tiles
+            uint32_t armed = 0, parity = 0;
+            bool drop = (p.test_flags & kTestDropFirstLoad) && blockIdx.x == 0;
+            bool ok = true;
+            int b = (int)first_box[0];
+            long long off = first_box[1];
+            TreeRequest r = tree_request(p, b);
+            for (long long u = u_begin;;) {
+                Item it{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, -1, 0};
+                while (u < u_end && b < p.B && off >= r.units(p.Hkv)) {      // the range goes on in a later request
+                    off = 0;
+                    if (++b < p.B) r = tree_request(p, b);
                 }
-                drop = false;                            // test hook: the first Q is never loaded
-            }
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            for (int t = it.t0; t < it.t1; ++t, ++n) {
-                look_up(t + 1 < it.t1 ? t + 1 : t, next_page, next_row);
-                const uint32_t exists = __ballot_sync(0xffffffffu, page >= 0);
-                const uint32_t bytes = __popc(exists) * p.piece * 128 * DCH;
+                if (u < u_end && b < p.B) {
+                    const int index = (int)(off / r.key_tiles);
+                    it.b = b;
+                    it.hk = index / r.q_pairs;
+                    it.n0 = (index - it.hk * r.q_pairs) * p.tile_nodes * NQ;
+                    it.t0 = (int)(off - (long long)index * r.key_tiles);
+                    it.t1 = (int)min((long long)r.key_tiles, it.t0 + (u_end - u));
+                    it.tiles = r.key_tiles;
+                    it.start = r.start;
+                    it.nodes = r.nodes;
+                    it.kv = r.kv;
+                    it.ctx = r.ctx;
+                    it.q_tiles = NQ == 1 || r.nodes - it.n0 <= p.tile_nodes ? 1 : 2;
+                    if (it.t0 > 0 || it.t1 < it.tiles) it.slot = 2 * blockIdx.x + (u > u_begin ? 1 : 0);
+                }
+                const uint32_t box = n_pub & 1u;
+                ok = lane != 0 || w.wait(item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (lane == 0) {
+                    volatile int* v = item_box + 12 * box;
+                    v[0] = it.b;
+                    v[1] = it.hk;
+                    v[2] = it.n0;
+                    v[3] = it.t0;
+                    v[4] = it.t1;
+                    v[5] = it.tiles;
+                    v[6] = it.start;
+                    v[7] = it.nodes;
+                    v[8] = it.kv;
+                    v[9] = it.ctx;
+                    v[10] = it.slot;
+                    v[11] = it.q_tiles;
+                    mbar_arrive(item_pub(box));
+                }
+                ++n_pub;
+                if (it.b < 0) break;
+                // this lane's piece of the next tile: its page, and whether it exists
+                auto look_up = [&](int t, int& page, int& row) {
+                    const int at = t * pieces + lane;        // piece of the request
+                    page = -1;
+                    if (lane < pieces && at * p.piece < it.kv) page = __ldg(p.table + (long long)it.b * p.table_width + at / per_page);
+                    if (page >= p.num_pages) page = -1;
+                    row = at % per_page * p.piece;
+                };
+                int page, row, next_page, next_row;
+                look_up(it.t0, page, row);
+                if (lane == 0) {
+                    ok = n_pub == 1 || w.wait(q_free, n_pub & 1u, kDevErrProducerEmpty);   // the previous item's
+                    if (ok && !drop) {
+                        mbar_arrive_expect_tx(q_full, it.q_tiles * p.tile_nodes * p.group * 128 * DCH);
+                        for (int q = 0; q < it.q_tiles; ++q)
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const uint32_t e = 2 * n + kv;
-                    const int s = (int)(e % NB);
-                    if (lane == 0) {
-                        ok = w.wait(empty(s), ((e / NB) & 1u) ^ 1u, kDevErrProducerEmpty);
-                        if (ok) {
-                            valid_box[s] = exists;
-                            mbar_arrive_expect_tx(full(s), bytes);
+                            for (int c = 0; c < DCH; ++c)
+                                tma_load_4d(sb + Cfg::OFF_Q + q * Cfg::TILE_BYTES + c * Cfg::CHUNK_BYTES, &tmQ, q_full, c * 64, 0,
+                                            it.hk, it.start + it.n0 + q * p.tile_nodes, pol);
+                        armed |= 1u << NB;
+                        parity = (parity & ~(1u << NB)) | ((n_pub - 1) & 1u) << NB;
+                    }
+                    drop = false;                            // test hook: the first Q is never loaded
+                }
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                for (int t = it.t0; t < it.t1; ++t, ++n) {
+                    look_up(t + 1 < it.t1 ? t + 1 : t, next_page, next_row);
+                    const uint32_t exists = __ballot_sync(0xffffffffu, page >= 0);
+                    const uint32_t bytes = __popc(exists) * p.piece * 128 * DCH;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint32_t e = 2 * n + kv;
+                        const int s = (int)(e % NB);
+                        if (lane == 0) {
+                            ok = w.wait(empty(s), ((e / NB) & 1u) ^ 1u, kDevErrProducerEmpty);
+                            if (ok) {
+                                valid_box[s] = exists;
+                                mbar_arrive_expect_tx(full(s), bytes);
+                            }
                         }
-                    }
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    armed |= 1u << s;
-                    parity = (parity & ~(1u << s)) | ((e / NB) & 1u) << s;
-                    if (page >= 0) {
+                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                        armed |= 1u << s;
+                        parity = (parity & ~(1u << s)) | ((e / NB) & 1u) << s;
+                        if (page >= 0) {
 #pragma unroll
-                        for (int c = 0; c < DCH; ++c)
-                            tma_load_4d(sb + Cfg::OFF_RING + s * Cfg::TILE_BYTES + c * Cfg::CHUNK_BYTES + lane * p.piece * 128,
-                                        kv ? &tmV : &tmK, full(s), c * 64, row, it.hk, page, pol);
+                            for (int c = 0; c < DCH; ++c)
+                                tma_load_4d(sb + Cfg::OFF_RING + s * Cfg::TILE_BYTES + c * Cfg::CHUNK_BYTES + lane * p.piece * 128,
+                                            kv ? &tmV : &tmK, full(s), c * 64, row, it.hk, page, pol);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (!ok) break;
+                    page = next_page;
+                    row = next_row;
                 }
                 if (!ok) break;
-                page = next_page;
-                row = next_row;
+                u += it.t1 - it.t0;
+                off += it.t1 - it.t0;
             }
-            if (!ok) break;
-            u += it.t1 - it.t0;
-            off += it.t1 - it.t0;
-        }
-        if (lane == 0) {   // every copy under way must land before the CTA may exit
-            for (int s = 0; s < NB; ++s)
-                if (armed & (1u << s)) w.drain(full(s), (parity >> s) & 1u);
-            if (armed & (1u << NB)) w.drain(q_full, (parity >> NB) & 1u);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            uint32_t n_item = 0, n = 0;
-            uint32_t p_n[2] = {0u, 0u};                  // pfull phases waited for, per S region
-            bool ok = true;
-            auto wait_full = [&](uint32_t e) { return w.wait(full((int)(e % NB)), (e / NB) & 1u, kDevErrMmaFull); };
-            auto tile = [&](uint32_t e) { return sb + Cfg::OFF_RING + (e % NB) * Cfg::TILE_BYTES; };
-            auto issue_s = [&](int q, int region, uint32_t m) {
-                const uint32_t q_s = sb + Cfg::OFF_Q + q * Cfg::TILE_BYTES, k_s = tile(2 * m);
+            if (lane == 0) {   // every copy under way must land before the CTA may exit
+                for (int s = 0; s < NB; ++s)
+                    if (armed & (1u << s)) w.drain(full(s), (parity >> s) & 1u);
+                if (armed & (1u << NB)) w.drain(q_full, (parity >> NB) & 1u);
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issuer
+            if (lane == 0) {
+                uint32_t n_item = 0, n = 0;
+                uint32_t p_n[2] = {0u, 0u};                  // pfull phases waited for, per S region
+                bool ok = true;
+                auto wait_full = [&](uint32_t e) { return w.wait(full((int)(e % NB)), (e / NB) & 1u, kDevErrMmaFull); };
+                auto tile = [&](uint32_t e) { return sb + Cfg::OFF_RING + (e % NB) * Cfg::TILE_BYTES; };
+                auto issue_s = [&](int q, int region, uint32_t m) {
+                    const uint32_t q_s = sb + Cfg::OFF_Q + q * Cfg::TILE_BYTES, k_s = tile(2 * m);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t o = (k >> 2) * Cfg::CHUNK_BYTES + (k & 3) * 32;
-                    mma_f16_ss(tmem_base + Cfg::T_S + region * 128, smem_desc_sw128(q_s + o, 16, 1024),
-                               smem_desc_sw128(k_s + o, 16, 1024), Cfg::IDESC_S, k > 0 ? 1u : 0u);
-                }
-                mma_commit(sfull(region));
-            };
-            auto issue_pv = [&](int q, int region, uint32_t m, bool first) {
-                if (!w.wait(pfull(region), p_n[region] & 1u, kDevErrMmaFull)) return false;
-                ++p_n[region];
-                tcgen05_fence_after();
-                const uint32_t v_s = tile(2 * m + 1), p_t = tmem_base + Cfg::T_S + region * 128 + Cfg::P_COL;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_f16_ts(tmem_base + Cfg::T_O + q * D, p_t + k * 8, smem_desc_sw128(v_s + k * 2048, Cfg::CHUNK_BYTES, 1024),
-                               Cfg::IDESC_PV, (!first || k > 0) ? 1u : 0u);
-                return true;
-            };
-            while (ok) {
-                const uint32_t box = n_item & 1u;
-                if (!w.wait(item_pub(box), (n_item >> 1) & 1u, kDevErrMmaFull)) break;
-                const Item it = read_item(box);
-                mbar_arrive(item_read(box));
-                if (it.b < 0) break;
-                if (!w.wait(q_full, n_item & 1u, kDevErrMmaFull)) break;
-                ++n_item;
-                tcgen05_fence_after();
-                const int steps = it.t1 - it.t0;
-                for (int i = 0; i <= steps && ok; ++i) {
-                    // K of step i and V of step i - 1
-                    if (i < steps && !(ok = wait_full(2 * (n + i)))) break;
-                    tcgen05_fence_after();
-                    if (NQ == 1) {
-                        // two S regions in turn: S(i) runs while the softmax of step i - 1 does
-                        if (i < steps) {
-                            issue_s(0, (int)((n + i) & 1u), n + i);
-                            mma_commit(empty((int)(2 * (n + i) % NB)));
-                            if (i == steps - 1) mma_commit(q_free);
-                        }
-                        if (i > 0) {
-                            const uint32_t m = n + i - 1;
-                            if (!(ok = wait_full(2 * m + 1) && issue_pv(0, (int)(m & 1u), m, i == 1))) break;
-                            mma_commit(pv_done(m));
-                            mma_commit(empty((int)((2 * m + 1) % NB)));
-                            if (i == steps) mma_commit(odone(0));
-                        }
-                    } else {
-                        // a region per query tile: the tiles alternate on the tensor core
-                        if (i > 0 && !(ok = wait_full(2 * (n + i) - 1))) break;
-                        tcgen05_fence_after();
-                        for (int q = 0; q < it.q_tiles && ok; ++q) {
-                            if (i > 0) {
-                                if (!(ok = issue_pv(q, q, n + i - 1, i == 1))) break;
-                                if (i == steps) mma_commit(odone(q));
-                            }
-                            if (i < steps) issue_s(q, q, n + i);
-                        }
-                        if (!ok) break;
-                        if (i < steps) mma_commit(empty((int)(2 * (n + i) % NB)));
-                        if (i == steps - 1) mma_commit(q_free);
-                        if (i > 0) mma_commit(empty((int)((2 * (n + i) - 1) % NB)));
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t o = (k >> 2) * Cfg::CHUNK_BYTES + (k & 3) * 32;
+                        mma_f16_ss(tmem_base + Cfg::T_S + region * 128, smem_desc_sw128(q_s + o, 16, 1024),
+                                   smem_desc_sw128(k_s + o, 16, 1024), Cfg::IDESC_S, k > 0 ? 1u : 0u);
                     }
+                    mma_commit(sfull(region));
+                };
+                auto issue_pv = [&](int q, int region, uint32_t m, bool first) {
+                    if (!w.wait(pfull(region), p_n[region] & 1u, kDevErrMmaFull)) return false;
+                    ++p_n[region];
+                    tcgen05_fence_after();
+                    const uint32_t v_s = tile(2 * m + 1), p_t = tmem_base + Cfg::T_S + region * 128 + Cfg::P_COL;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_f16_ts(tmem_base + Cfg::T_O + q * D, p_t + k * 8, smem_desc_sw128(v_s + k * 2048, Cfg::CHUNK_BYTES, 1024),
+                                   Cfg::IDESC_PV, (!first || k > 0) ? 1u : 0u);
+                    return true;
+                };
+                while (ok) {
+                    const uint32_t box = n_item & 1u;
+                    if (!w.wait(item_pub(box), (n_item >> 1) & 1u, kDevErrMmaFull)) break;
+                    const Item it = read_item(box);
+                    mbar_arrive(item_read(box));
+                    if (it.b < 0) break;
+                    if (!w.wait(q_full, n_item & 1u, kDevErrMmaFull)) break;
+                    ++n_item;
+                    tcgen05_fence_after();
+                    const int steps = it.t1 - it.t0;
+                    for (int i = 0; i <= steps && ok; ++i) {
+                        // K of step i and V of step i - 1
+                        if (i < steps && !(ok = wait_full(2 * (n + i)))) break;
+                        tcgen05_fence_after();
+                        if (it.q_tiles == 1) {
+                            // key tiles in turn: S(i) runs while the other group's softmax does
+                            if (i < steps) {
+                                issue_s(0, i & 1, n + i);
+                                mma_commit(empty((int)(2 * (n + i) % NB)));
+                                if (i == steps - 1) mma_commit(q_free);
+                            }
+                            if (i > 0) {
+                                const uint32_t m = n + i - 1;
+                                const int g = (i - 1) & 1;
+                                if (!(ok = wait_full(2 * m + 1) && issue_pv(g, g, m, i <= 2))) break;
+                                mma_commit(empty((int)((2 * m + 1) % NB)));
+                                if (i == steps) {
+                                    mma_commit(odone(0));
+                                    mma_commit(odone(1));
+                                }
+                            }
+                        } else {
+                            // a region per query tile: the tiles alternate on the tensor core
+                            if (i > 0 && !(ok = wait_full(2 * (n + i) - 1))) break;
+                            tcgen05_fence_after();
+                            for (int q = 0; q < 2 && ok; ++q) {
+                                if (i > 0) {
+                                    if (!(ok = issue_pv(q, q, n + i - 1, i == 1))) break;
+                                    if (i == steps) mma_commit(odone(q));
+                                }
+                                if (i < steps) issue_s(q, q, n + i);
+                            }
+                            if (!ok) break;
+                            if (i < steps) mma_commit(empty((int)(2 * (n + i) % NB)));
+                            if (i == steps - 1) mma_commit(q_free);
+                            if (i > 0) mma_commit(empty((int)((2 * (n + i) - 1) % NB)));
+                        }
+                    }
+                    n += steps;
                 }
-                n += steps;
+                mma_commit(drain);
+                w.drain(drain, 0);
             }
-            mma_commit(drain);
-            w.drain(drain, 0);
+            __syncwarp();
         }
-        __syncwarp();
     } else {
+        reg_inc<Cfg::SOFTMAX_REGS>();
         // ------------------------------------------------------------ softmax + output
-        const int q = (warp - 2) >> 2;
+        const int q = (warp - 4) >> 2;
         const int quad = warp & 3;
         const int rq = quad * 32 + lane;                 // row of the query tile == TMEM lane
         const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
@@ -480,7 +497,9 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
         const ScoreForm form = score_form<Cfg::MODE>(sc);
         const uint32_t hidden = form.hidden();
         const int node_in = rq / p.group, hg = rq - node_in * p.group;
-        uint32_t n_item = 0, n = 0, s_n[2] = {0u, 0u}, o_n = 0;
+        const uint32_t s_col = lane_base + Cfg::T_S + q * 128;
+        float2* ml_box = reinterpret_cast<float2*>(smem + Cfg::OFF_ML);
+        uint32_t n_item = 0, n_first = 0, s_n = 0, n_ml = 0;     // items, the item's first tile, S phases, exchanges
         bool ok = true;
         while (ok) {
             const uint32_t box = n_item & 1u;
@@ -491,35 +510,29 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
             ++n_item;
             if (it.b < 0) break;
             const int steps = it.t1 - it.t0;
-            if (q >= it.q_tiles) {                       // no second query tile in this item
-                n += steps;
-                continue;
-            }
-            const int node = it.n0 + q * p.tile_nodes + node_in;
+            const bool turns = it.q_tiles == 1;          // the groups take turns over the key tiles
+            const int node = it.n0 + (turns ? 0 : q * p.tile_nodes) + node_in;
             const bool real = node_in < p.tile_nodes && node < it.nodes;
             const bool busy = __any_sync(0xffffffffu, real);     // warps without rows only keep the barriers
             const int h = it.hk * p.group + hg;
             const uint64_t see = real ? ancestors(p.parents, it.start, node) : 0ull;
-            const float slope2 = Cfg::MODE != kScorePlain && sc.slopes && real ? __ldg(sc.slopes + h) * kLog2e : 0.0f;
+            const float slope2 = kHasBias<Cfg::MODE> && real ? __ldg(sc.slopes + h) * kLog2e : 0.0f;
             const int pos = it.ctx + __popcll(see) - 1;
             const int seen_by_all = min(it.ctx, it.kv);  // keys before it are visible to every node
             float m = -INFINITY, l = 0.0f;
 
-            for (int i = 0; i < steps; ++i, ++n) {
-                const int region = NQ == 1 ? (int)(n & 1u) : q;
-                const uint32_t s_col = lane_base + Cfg::T_S + region * 128;
-                const uint32_t e = 2 * n;
+            const int i_first = turns ? q : 0, i_step = turns ? 2 : 1;
+            for (int i = i_first; i < steps; i += i_step) {
+                const uint32_t e = 2 * (n_first + i) + 1;        // V's ring entry
                 const int k0 = (it.t0 + i) * p.tile_keys;
-                // V's entry tells which pieces exist, and stays until this step's P is used; PV(n-2) came
-                // before S(n), and waiting for it every step leaves each pv_done one phase to tell apart
-                if (!__all_sync(0xffffffffu, w.wait(sfull(region), s_n[region] & 1u, kDevErrEpilogueFull) &&
-                                                 w.wait(full((int)((e + 1) % NB)), ((e + 1) / NB) & 1u, kDevErrEpilogueFull) &&
-                                                 (NQ == 2 || n < 2 || w.wait(pv_done(n), ((n - 2) >> 1) & 1u, kDevErrEpilogueFull)))) {
+                // V's entry tells which pieces exist, and stays until this step's P is used
+                if (!__all_sync(0xffffffffu, w.wait(sfull(q), s_n & 1u, kDevErrEpilogueFull) &&
+                                                 w.wait(full((int)(e % NB)), (e / NB) & 1u, kDevErrEpilogueFull))) {
                     ok = false;
                     break;
                 }
-                const uint32_t exists = valid_box[(e + 1) % NB];
-                ++s_n[region];
+                ++s_n;
+                const uint32_t exists = valid_box[e % NB];
                 tcgen05_fence_after();
                 const bool all_exist = exists == (1u << (p.tile_keys / p.piece)) - 1u;
                 const bool partial = !all_exist || k0 + p.tile_keys > it.kv;      // some V rows hold no token
@@ -541,29 +554,29 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                         score_chunk<Cfg::MODE>(rr, sc, slope2, base - (float)(c * 32));
                         if (!masked) return;
                         const int kk = k0 + c * 32;
-                        uint32_t tree = 0u;              // the tree's keys among these 32
-                        const int sh = kk - it.ctx;
-                        if (sh >= 0 && sh < 64) tree = (uint32_t)(see >> sh);
-                        if (sh < 0 && sh > -32) tree = (uint32_t)(see << -sh);
                         auto below = [&](int limit) {    // keys before `limit`
                             const int k = limit - kk;
                             return k >= 32 ? 0xffffffffu : (k <= 0 ? 0u : (1u << k) - 1u);
                         };
-                        if (Cfg::MODE != kScorePlain) {
+                        uint32_t tree = 0u;              // the tree's keys among these 32
+                        const int sh = kk - it.ctx;
+                        if (sh >= 0 && sh < 64) tree = (uint32_t)(see >> sh);
+                        if (sh < 0 && sh > -32) tree = (uint32_t)(see << -sh);
+                        if (kHasBias<Cfg::MODE> && tree) {
                             // a node's distance counts its depth, not its place in the cache
-                            tree &= ~below(it.ctx);
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                if (slope2 != 0.0f && (tree >> j & 1u)) {
-                                    const float at = (float)(pos - it.ctx - depth_of(see, kk + j - it.ctx));
+                                if (tree >> j & 1u) {
+                                    const float at = (float)(pos - it.ctx - depth_of(see, sh + j));
                                     rr[j] = __float_as_uint(fmaf(slope2, fabsf(base - (float)(c * 32 + j)) - at, __uint_as_float(rr[j])));
                                 }
                         }
-                        uint32_t have = 0u;
-#pragma unroll
-                        for (int g8 = 0; g8 < 4; ++g8)
-                            if (exists >> ((c * 32 + g8 * 8) / p.piece) & 1u) have |= 0xffu << (8 * g8);
-                        const uint32_t vis = (tree | below(it.ctx)) & below(it.kv) & have;
+                        uint32_t vis = (tree | below(it.ctx)) & below(min(it.kv, k0 + p.tile_keys));
+                        if (!all_exist) {
+#pragma unroll 1
+                            for (int g8 = 0; g8 < 4; ++g8)
+                                if (!(exists >> ((c * 32 + g8 * 8) / p.piece) & 1u)) vis &= ~(0xffu << (8 * g8));
+                        }
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (!(vis >> j & 1u)) rr[j] = hidden;
@@ -599,14 +612,9 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                     chunk_p(sc3, 3);
                     l += ls0 + ls1;
                 }
-                if (i > 0 && __any_sync(0xffffffffu, bump)) {
-                    // O (this warp's rows) *= factor, after PV(i-1) and before PV(i); with a region per
-                    // query tile S(i) was issued after PV(i-1), with two in turn it was not
-                    if (NQ == 1 && !__all_sync(0xffffffffu, w.wait(pv_done(n - 1), ((n - 1) >> 1) & 1u, kDevErrEpilogueFull))) {
-                        ok = false;
-                        break;
-                    }
-                    tcgen05_fence_after();
+                if (i > i_first && __any_sync(0xffffffffu, bump)) {
+                    // O (this warp's rows) *= factor: the group's last PV was issued before this S, and
+                    // its next waits for the arrival below
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t rr[32];
@@ -629,63 +637,87 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                         for (int c = 0; c < DCH; ++c)
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
-                                *reinterpret_cast<uint4*>(smem + Cfg::OFF_RING + ((e + 1) % NB) * Cfg::TILE_BYTES +
+                                *reinterpret_cast<uint4*>(smem + Cfg::OFF_RING + (e % NB) * Cfg::TILE_BYTES +
                                                           c * Cfg::CHUNK_BYTES + rq * 128 + j * 16) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                 }
                 tmem_st_wait();
                 tcgen05_fence_before();
-                mbar_arrive(pfull(region));
+                mbar_arrive(pfull(q));
             }
             if (!ok) break;
-            ok = __all_sync(0xffffffffu, w.wait(odone(q), o_n & 1u, kDevErrEpilogueFull));
-            ++o_n;
+            n_first += steps;
+            if (turns) {
+                // the two groups' maxima and sums, once both have read the last exchange's
+                if (!(ok = __all_sync(0xffffffffu, w.wait(ml_free, (n_ml & 1u) ^ 1u, kDevErrEpilogueFull)))) break;
+                ml_box[q * 128 + rq] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ml_full);
+            }
+            if (!(ok = __all_sync(0xffffffffu, w.wait(odone(q), (n_item - 1) & 1u, kDevErrEpilogueFull)))) break;
+            float f0 = 1.0f, f1 = 0.0f;                  // factors of the two accumulators
+            if (turns) {
+                if (!(ok = __all_sync(0xffffffffu, w.wait(ml_full, n_ml & 1u, kDevErrEpilogueFull)))) break;
+                const float2 a = ml_box[rq], b = ml_box[128 + rq];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ml_free);
+                ++n_ml;
+                m = fmaxf(a.x, b.x);
+                f0 = m == -INFINITY ? 0.0f : ex2_approx(a.x - m);
+                f1 = m == -INFINITY ? 0.0f : ex2_approx(b.x - m);
+                l = (f0 == 0.0f && a.y == a.y ? 0.0f : a.y * f0) + (f1 == 0.0f && b.y == b.y ? 0.0f : b.y * f1);
+            }
             tcgen05_fence_after();
-            if (!ok) break;
-            // a whole item's rows, or this CTA's part of them
+            // the rows, or this CTA's part of them; of one query tile's rows each group writes half the
+            // columns
             bool bad = false;
             if (busy) {
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const float inv = it.slot >= 0 ? 1.0f : (l > 0.0f ? 1.0f / l : 0.0f);
                 const bool none = l == 0.0f;             // nothing seen here: O holds 0 V
                 bad = !(l < INFINITY);
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.O) + (long long)(it.start + node) * p.o_row + h * p.o_head);
-                float4* part = reinterpret_cast<float4*>(it.slot < 0 ? nullptr : part_o(p, it.slot, q * 128 + rq, D));
+                f0 *= inv;
+                f1 *= inv;
+                const int c_first = turns ? q * (D / 64) : 0, c_end = turns ? c_first + D / 64 : D / 32;
+                const uint32_t o0 = turns ? lane_base + Cfg::T_O : o_col, o1 = lane_base + Cfg::T_O + D;
+                T* row = static_cast<T*>(p.O) + (long long)(it.start + node) * p.o_row + h * p.o_head;
+                float* part = it.slot < 0 ? nullptr : part_o(p, it.slot, (turns ? 0 : q * 128) + rq, D);
+                for (int c = c_first; c < c_end; ++c) {
+                    uint32_t r0[32], r1[32];
+                    tmem_ld_32x32b_x32(o0 + c * 32, r0);
+                    if (turns && steps > 1) tmem_ld_32x32b_x32(o1 + c * 32, r1);
+                    tmem_ld_wait(r0);
+                    reg_tie(r1);
+                    float y[32];
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t rr[32];
-                    tmem_ld_32x32b_x32(o_col + c * 32, rr);
-                    tmem_ld_wait(rr);
-                    if (none) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) rr[j] = 0u;
+                    for (int j = 0; j < 32; ++j) {
+                        // an accumulator whose factor is 0 may hold anything
+                        y[j] = f0 == 0.0f || none ? 0.0f : __uint_as_float(r0[j]) * f0;
+                        if (turns && steps > 1 && f1 != 0.0f && !none) y[j] = fmaf(__uint_as_float(r1[j]), f1, y[j]);
+                        bad |= !(fabsf(y[j]) < INFINITY);
                     }
-                    if (real && it.slot >= 0) {
+                    if (!real) continue;
+                    if (it.slot >= 0) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            part[c * 8 + j] = make_float4(__uint_as_float(rr[4 * j]), __uint_as_float(rr[4 * j + 1]),
-                                                          __uint_as_float(rr[4 * j + 2]), __uint_as_float(rr[4 * j + 3]));
-                    } else if (real) {
+                            reinterpret_cast<float4*>(part)[c * 8 + j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                    } else {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t v[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float a = __uint_as_float(rr[8 * k + 2 * j]), b = __uint_as_float(rr[8 * k + 2 * j + 1]);
-                                bad |= !(fabsf(a) < INFINITY) | !(fabsf(b) < INFINITY);
-                                v[j] = Elem<T>::pack(a * inv, b * inv);
-                            }
-                            dst[c * 4 + k] = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            reinterpret_cast<uint4*>(row)[c * 4 + k] =
+                                make_uint4(Elem<T>::pack(y[8 * k], y[8 * k + 1]), Elem<T>::pack(y[8 * k + 2], y[8 * k + 3]),
+                                           Elem<T>::pack(y[8 * k + 4], y[8 * k + 5]), Elem<T>::pack(y[8 * k + 6], y[8 * k + 7]));
                     }
                 }
-                if (real && it.slot >= 0) *part_ml(p, it.slot, q * 128 + rq) = make_float2(m, l);
+                if (real && it.slot >= 0 && (!turns || q == 0))
+                    *part_ml(p, it.slot, (turns ? 0 : q * 128) + rq) = make_float2(m, l);
             }
             tcgen05_fence_before();
             __syncwarp();
             for (uint32_t again = __ballot_sync(0xffffffffu, bad && real && it.slot < 0); again; again &= again - 1) {
                 const int src = __ffs(again) - 1;
-                tree_row<T, D>(p, it.b, tree_request(p, it.b), __shfl_sync(0xffffffffu, node, src), __shfl_sync(0xffffffffu, h, src), lane);
+                tree_row<T, D>(p, it.b, tree_request(p, it.b), __shfl_sync(0xffffffffu, node, src), __shfl_sync(0xffffffffu, h, src),
+                               turns ? q : -1, lane);
             }
         }
     }
@@ -702,12 +734,19 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
 // ---------------------------------------------------------------------------
 // Their sum
 // ---------------------------------------------------------------------------
-// One CTA per (query row, head): its item's parts, in the order of their CTAs, warp by warp.
-constexpr int kJoinWarps = 4;
-template <class T, int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) gsr_tree_join_kernel(const __grid_constant__ TreeParams p, int grid) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");           // the parts' launch has finished
-    const int n = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// WARPS warps per (query row, head) take its item's parts in the order of their CTAs, warp by warp, and
+// add up through shared memory.  A row has few parts where there are many rows, and one warp is
+// enough (10 000 rows of 2 or 3 parts: 29 us with four warps a row); a few rows of a long context may
+// have a part from every CTA.
+constexpr int kJoinThreads = 128;
+template <class T, int D, int WARPS>
+__global__ void __launch_bounds__(kJoinThreads) gsr_tree_join_kernel(const __grid_constant__ TreeParams p, int grid) {
+    constexpr int ROWS = kJoinThreads / 32 / WARPS;
+    __shared__ float sm[WARPS > 1 ? WARPS : 1][D + 2];
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS;
+    const long long id = (long long)blockIdx.x * ROWS + (threadIdx.x >> 5) / WARPS;
+    if (id >= (long long)p.total_q * p.Hq) return;
+    const int n = (int)(id / p.Hq), h = (int)(id - (long long)n * p.Hq);
     int left = 0, right = p.B;                                   // first request that ends behind row n
     while (left < right) {
         const int mid = (left + right) >> 1;
@@ -721,56 +760,55 @@ __global__ void __launch_bounds__(32 * kJoinWarps) gsr_tree_join_kernel(const __
     if (t < 0 || t >= r.nodes) return;
     const int per_pass = p.tile_nodes * p.nq, pair = t / per_pass, in_pass = t - pair * per_pass;
     const int row = in_pass / p.tile_nodes * 128 + in_pass % p.tile_nodes * p.group + (h - hk * p.group);
+    asm volatile("griddepcontrol.wait;" ::: "memory");           // the parts' launch has finished
     const long long U = p.unit_starts[p.B];
     const long long s = p.unit_starts[b] + ((long long)hk * r.q_pairs + pair) * r.key_tiles;
     if (U <= 0) return;
     const int G = busy_ctas(U, grid);
     const int c0 = max(cta_of(U, s, G), 0), c1 = min(cta_of(U, s + r.key_tiles - 1, G), G - 1);
     if (c0 >= c1) return;                                        // written whole
-    __shared__ float sm[kJoinWarps][D + 2];
-    auto slot_of = [&](int c) { return 2ll * c + (first_unit(U, c, G) < s ? 1 : 0); };
     float m = -INFINITY, l = 0.0f, acc[D / 32] = {};
-    for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
-        const long long slot = slot_of(c);
-        const float2 ml = *part_ml(p, slot, row);
-        const float* o = part_o(p, slot, row, D) + lane * (D / 32);
-        const float mn = fmaxf(m, ml.x);
-        const float f0 = mn == -INFINITY ? 0.0f : ex2_approx(m - mn), f1 = mn == -INFINITY ? 0.0f : ex2_approx(ml.x - mn);
-        l = l * f0 + (f1 == 0.0f && ml.y == ml.y ? 0.0f : ml.y * f1);
+    auto add = [&](float pm, float pl, const float* o) {
+        const float mn = fmaxf(m, pm);
+        const float f0 = mn == -INFINITY ? 0.0f : ex2_approx(m - mn), f1 = mn == -INFINITY ? 0.0f : ex2_approx(pm - mn);
+        l = l * f0 + (f1 == 0.0f && pl == pl ? 0.0f : pl * f1);
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) acc[e] = acc[e] * f0 + (f1 == 0.0f ? 0.0f : o[e] * f1);
         m = mn;
+    };
+    for (int c = c0 + warp; c <= c1; c += WARPS) {
+        const long long slot = 2ll * c + (first_unit(U, c, G) < s ? 1 : 0);
+        const float2 ml = *part_ml(p, slot, row);
+        const float* o = part_o(p, slot, row, D) + lane * (D / 32);
+        float x[D / 32];
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) x[e] = o[e];
+        add(ml.x, ml.y, x);
     }
+    if (WARPS > 1) {
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) sm[warp][lane * (D / 32) + e] = acc[e];
-    if (lane == 0) {
-        sm[warp][D] = m;
-        sm[warp][D + 1] = l;
+        for (int e = 0; e < D / 32; ++e) sm[warp][lane * (D / 32) + e] = acc[e];
+        if (lane == 0) {
+            sm[warp][D] = m;
+            sm[warp][D + 1] = l;
+        }
+        __syncthreads();
+        if (warp != 0) return;
+#pragma unroll
+        for (int i = 1; i < WARPS; ++i) add(sm[i][D], sm[i][D + 1], &sm[i][lane * (D / 32)]);
     }
-    __syncthreads();
-    if (warp != 0) return;
-    float top = -INFINITY, total = 0.0f, out[D / 32] = {};
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, sm[i][D]);
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) {
-        const float f = sm[i][D] == -INFINITY ? 0.0f : ex2_approx(sm[i][D] - top);
-        total += sm[i][D + 1] * f;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) out[e] += sm[i][lane * (D / 32) + e] * f;
-    }
-    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-    bool bad = !(total < INFINITY);
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    bool bad = !(l < INFINITY);
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) {
-        bad |= !(fabsf(out[e]) < INFINITY);
-        out[e] *= inv;
+        bad |= !(fabsf(acc[e]) < INFINITY);
+        acc[e] *= inv;
     }
     if (__any_sync(0xffffffffu, bad)) {
-        tree_row<T, D>(p, b, r, t, h, lane);
+        tree_row<T, D>(p, b, r, t, h, -1, lane);
         return;
     }
-    store_row<T, D>(static_cast<T*>(p.O) + (long long)n * p.o_row + h * p.o_head, lane, out);
+    store_row<T, D>(static_cast<T*>(p.O) + (long long)n * p.o_row + h * p.o_head, lane, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -784,23 +822,29 @@ cudaError_t launch_tree_cfg(const TreeMaps& tm, const TreeParams& p, int grid, c
     gsr_tree_kernel<Cfg><<<(unsigned)grid, Cfg::NUM_THREADS, Cfg::SMEM_BYTES, stream>>>(tm.q, tm.k, tm.v, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // the joining CTAs start while the parts' last CTAs finish, and wait for them there
+    const long long rows = (long long)p.total_q * p.Hq;
+    const bool many = rows >= 2048;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.total_q, (unsigned)p.Hq);
-    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.gridDim = dim3((unsigned)(many ? (rows + 3) / 4 : rows));
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gsr_tree_join_kernel<typename Cfg::T, Cfg::D>, p, grid);
+    return many ? cudaLaunchKernelEx(&cfg, gsr_tree_join_kernel<typename Cfg::T, Cfg::D, 1>, p, grid)
+                : cudaLaunchKernelEx(&cfg, gsr_tree_join_kernel<typename Cfg::T, Cfg::D, 4>, p, grid);
 }
 
 template <class T, int D, int NQ>
 cudaError_t launch_tree_mode(const TreeMaps& tm, const TreeParams& p, int grid, cudaStream_t stream) {
-    if (p.score.cap_in != 0.0f) return launch_tree_cfg<TreeCfg<T, D, kScoreCap, NQ>>(tm, p, grid, stream);
-    if (p.score.slopes) return launch_tree_cfg<TreeCfg<T, D, kScoreBias, NQ>>(tm, p, grid, stream);
-    return launch_tree_cfg<TreeCfg<T, D, kScorePlain, NQ>>(tm, p, grid, stream);
+    switch (score_mode(p.score)) {
+        case kScorePlain: return launch_tree_cfg<TreeCfg<T, D, kScorePlain, NQ>>(tm, p, grid, stream);
+        case kScoreBias: return launch_tree_cfg<TreeCfg<T, D, kScoreBias, NQ>>(tm, p, grid, stream);
+        case kScoreCap: return launch_tree_cfg<TreeCfg<T, D, kScoreCap, NQ>>(tm, p, grid, stream);
+        default: return launch_tree_cfg<TreeCfg<T, D, kScoreCapBias, NQ>>(tm, p, grid, stream);
+    }
 }
 
 template <class T, int D>

@@ -199,9 +199,10 @@ gsr_status check_tree_desc(const gsr_tree_desc* desc) {
     if (d.head_dim != 64 && d.head_dim != 128) return GSR_ERR_INVALID_ARG;
     if (d.dtype != GSR_F16 && d.dtype != GSR_BF16) return GSR_ERR_INVALID_ARG;
     if (d.max_nodes < 1 || d.max_nodes > GSR_TREE_MAX_NODES) return GSR_ERR_INVALID_ARG;
-    if (d.heads_q > 0 && (d.heads_kv == 0 || d.heads_q % d.heads_kv || d.heads_q / d.heads_kv > 128 || d.heads_q > 65535))
+    if (d.heads_q > 0 && (d.heads_kv == 0 || d.heads_q % d.heads_kv || d.heads_q / d.heads_kv > 128))
         return GSR_ERR_INVALID_ARG;
     if (bad_score(d.softmax_scale, d.softcap)) return GSR_ERR_INVALID_ARG;
+    if ((double)d.total_q * (double)d.heads_q > INT_MAX) return GSR_ERR_INVALID_ARG;   // one joining CTA a row
     if (d.page_size < 8 || d.page_size % 8 || d.table_width * d.page_size > INT_MAX - 256) return GSR_ERR_INVALID_ARG;
     return GSR_OK;
 }

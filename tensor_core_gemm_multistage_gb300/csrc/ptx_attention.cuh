@@ -45,6 +45,18 @@ __device__ __forceinline__ int clc_taken(uint32_t src) {
     return x;
 }
 
+// Moves registers between warpgroups: every warp of one gives registers back (dec) or takes them (inc,
+// which waits until they are there).  The shares times 128 threads stay within what the CTA was
+// launched with.
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Instruction descriptor as idesc_f16_f32, for f16 (0) or bf16 (1) operands, both of one type.
 __host__ __device__ constexpr uint32_t idesc_16_f32(bool bf16, int M, int N, bool a_mn_major, bool b_mn_major) {
     return idesc_f16_f32(M, N, a_mn_major, b_mn_major) | (bf16 ? (1u << 7) | (1u << 10) : 0u);
