@@ -6,8 +6,8 @@
 // row's lo to its last row's hi and skips the rest: a packed row of documents costs what its
 // documents cost, whatever the row's length.
 //
-//  * one CTA per SM, 320 threads: warp 0 takes work items and issues TMA copies, one lane of warp 1
-//    issues every MMA, warps 2-5 run the softmax of query tile 0 and warps 6-9 that of tile 1, one
+//  * one CTA per SM, 384 threads: warp 0 takes work items and issues TMA copies, one lane of warp 1
+//    issues every MMA, warps 4-7 run the softmax of query tile 0 and warps 8-11 that of tile 1, one
 //    thread per query row (= TMEM lane).  A work item is two 128-query tiles of one head;
 //  * items are CTAs of the grid that a running CTA takes over by cluster launch control: the
 //    hardware keeps the count, so nothing in memory is shared between launches, captured ones too;
@@ -42,7 +42,10 @@ struct MaskedFwdCfg {
     static constexpr int Q_BYTES = BQ * D * 2;
     static constexpr int KV_BYTES = BKV * D * 2;
     static constexpr int SM_THREADS = 128 * NQ;
-    static constexpr int NUM_THREADS = 64 + SM_THREADS;
+    static constexpr int NUM_THREADS = 128 + SM_THREADS;
+    // 384 threads start with 168 registers each; the copying and issuing warps' group gives some to
+    // the softmax groups, whose threads hold a row of 128 scores: 72 + 2 x 216 = 3 x 168
+    static constexpr int CONTROL_REGS = 72, SOFTMAX_REGS = 216;
     static constexpr int QBUF = D == 64 ? 2 : 1;      // Q sets that fit: with two, the next item's loads early
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = OFF_Q + QBUF * NQ * Q_BYTES;   // ring of 2 entries {K_t, V_(t-1)}
@@ -183,195 +186,199 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
     const uint32_t tmem_base = *tmem_slot;
     const Waiter w{p.err, p.timeout_ns, abort_flag, kDevErrKernelMaskedFwd};
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ items + TMA producer
-        // The whole warp walks the items (lanes 0-3 find the intervals of the query tiles' first
-        // and last rows); lane 0 waits, publishes and copies.
-        const uint64_t pol = l2_policy_evict_last();     // K and V are read by every query block
-        const int n_qb = (mk.Sq + NQ * Cfg::BQ - 1) / (NQ * Cfg::BQ);
-        uint32_t n_pub = 0, n_q = 0, g = 0, n_clc = 0;   // items published, Q loads, ring entries, answers
-        uint32_t armed = 0, parity = 0, q_armed = 0, q_parity = 0;
-        bool drop_q = (p.test_flags & kTestDropFirstLoad) && blockIdx.x == 0;
-        bool asked = false;
-        int item = blockIdx.x;
-        while (true) {
-            Item it{-1, 0, 0, {0, 0}, {0, 0}};
-            if (item >= 0) {
-                // query blocks from the last (under a causal mask the longest) to the first, in
-                // groups of heads whose K and V stay in L2 together
-                const int per_group = p.head_group * n_qb, grp = item / per_group, r_in = item - grp * per_group;
-                const int gsz = min(mk.B * mk.Hq - grp * p.head_group, p.head_group);
-                const int bh = grp * p.head_group + r_in % gsz;
-                it.b = bh / mk.Hq;
-                it.h = bh - it.b * mk.Hq;
-                it.q_base = (n_qb - 1 - r_in / gsz) * NQ * Cfg::BQ;
-                // lane 2q: first row of tile q, lane 2q + 1: its last row
-                int lo = 0, hi = 0;
-                const int first = it.q_base + (lane >> 1 & 1) * Cfg::BQ;
-                const int row = lane & 1 ? min(first + Cfg::BQ, mk.Sq) - 1 : first;
-                if (lane < 4 && first < mk.Sq) row_interval(mk, it.b, row, lo, hi);
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    const int l = __shfl_sync(0xffffffffu, lo, 2 * q), e = __shfl_sync(0xffffffffu, hi, 2 * q + 1);
-                    it.t0[q] = l / Cfg::BKV;
-                    it.t1[q] = e > l ? (e + Cfg::BKV - 1) / Cfg::BKV : it.t0[q];
-                }
-            }
-            const uint32_t box = n_pub & 1u;
-            // the box's previous item has been read by every role
-            bool ok = lane != 0 || w.wait(item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            if (lane == 0) {
-                volatile int* v = item_box + 8 * box;
-                v[0] = it.b;
-                v[1] = it.h;
-                v[2] = it.q_base;
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    v[3 + q] = it.t0[q];
-                    v[5 + q] = it.t1[q];
-                }
-                mbar_arrive(item_pub(box));              // release: the consumers read the box after
-            }
-            ++n_pub;
-            if (item < 0) break;
-            if (lane == 0) {
-                const int t_begin = it.first(), t_end = it.last();
-                if (t_begin < t_end) {
-                    const int qb = (int)(n_q % Cfg::QBUF);
-                    if (n_q >= (uint32_t)Cfg::QBUF)
-                        ok = w.wait(qfree(qb), ((n_q - Cfg::QBUF) / Cfg::QBUF) & 1u, kDevErrProducerEmpty);
-                    if (ok) {
-                        if (drop_q) {
-                            drop_q = false;              // test hook: this Q is never loaded
-                        } else {
-                            const uint32_t qbase = sb + Cfg::OFF_Q + qb * NQ * Cfg::Q_BYTES;
-                            mbar_arrive_expect_tx(qfull(qb), NQ * Cfg::Q_BYTES);
-#pragma unroll
-                            for (int q = 0; q < NQ; ++q)
-#pragma unroll
-                                for (int c = 0; c < Cfg::DCH; ++c)
-                                    tma_load_4d(qbase + q * Cfg::Q_BYTES + c * Cfg::CHUNK_BYTES, &tmQ, qfull(qb), c * 64,
-                                                it.q_base + q * Cfg::BQ, it.h, it.b, pol);
-                            q_armed |= 1u << qb;
-                            q_parity = (q_parity & ~(1u << qb)) | ((n_q / Cfg::QBUF) & 1u) << qb;
-                        }
-                        ++n_q;
-                    }
-                    const int hk = it.h / mk.group;
-                    // entry t: K_t (t < t_end) and V_(t-1) (t > t_begin)
-                    for (int t = t_begin; ok && t <= t_end; ++t, ++g) {
-                        const int s = (int)(g & 1u);
-                        const uint32_t ph = (g >> 1) & 1u;
-                        if (!(ok = w.wait(empty(s), ph ^ 1u, kDevErrProducerEmpty))) break;
-                        const bool has_k = t < t_end, has_v = t > t_begin;
-                        mbar_arrive_expect_tx(full(s), (has_k ? Cfg::KV_BYTES : 0) + (has_v ? Cfg::KV_BYTES : 0));
-                        if (has_k) {
-#pragma unroll
-                            for (int c = 0; c < Cfg::DCH; ++c)
-                                tma_load_4d(sb + Cfg::OFF_K + s * Cfg::KV_BYTES + c * Cfg::CHUNK_BYTES, &tmK, full(s), c * 64,
-                                            t * Cfg::BKV, hk, it.b, pol);
-                        }
-                        if (has_v) {
-#pragma unroll
-                            for (int c = 0; c < Cfg::DCH; ++c)
-                                tma_load_4d(sb + Cfg::OFF_V + s * Cfg::KV_BYTES + c * Cfg::CHUNK_BYTES, &tmV, full(s), c * 64,
-                                            (t - 1) * Cfg::BKV, hk, it.b, pol);
-                        }
-                        armed |= 1u << s;
-                        parity = (parity & ~(1u << s)) | ph << s;
-                    }
-                }
-                // the next item, asked for once this one's copies are issued: earlier, a CTA busy with a
-                // long item would hold one that another could start
-                if (ok) {
-                    fence_proxy_async_smem();            // the last answer has been read
-                    mbar_arrive_expect_tx(clc, 16);
-                    clc_try_cancel(sb + Cfg::OFF_CLC, clc);
-                    asked = true;
-                    if ((ok = w.wait(clc, n_clc & 1u, kDevErrProducerEmpty))) {
-                        asked = false;
-                        item = clc_taken(sb + Cfg::OFF_CLC);
-                    }
-                }
-            }
-            ++n_clc;
-            if (!__all_sync(0xffffffffu, ok)) break;
-            item = __shfl_sync(0xffffffffu, item, 0);
-        }
-        // every copy and answer under way must land before the CTA may exit
-        if (lane == 0) {
-            if (asked) w.drain(clc, (n_clc - 1) & 1u);
-            for (int b = 0; b < Cfg::QBUF; ++b)
-                if (q_armed & (1u << b)) w.drain(qfull(b), (q_parity >> b) & 1u);
-            for (int s = 0; s < 2; ++s)
-                if (armed & (1u << s)) w.drain(full(s), (parity >> s) & 1u);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            uint32_t n_item = 0, n_q = 0, g = 0;
-            uint32_t pv_n[NQ] = {0u, 0u};                // pfull phases waited for, per query tile
-            bool ok = true;
-            while (ok) {
-                const uint32_t box = n_item & 1u;
-                if (!w.wait(item_pub(box), (n_item >> 1) & 1u, kDevErrMmaFull)) break;
-                const Item it = read_item(box);
-                mbar_arrive(item_read(box));
-                ++n_item;
-                if (it.b < 0) break;
-                const int t_begin = it.first(), t_end = it.last();
-                if (t_begin >= t_end) continue;
-                const int qb = (int)(n_q % Cfg::QBUF);
-                if (!w.wait(qfull(qb), (n_q / Cfg::QBUF) & 1u, kDevErrMmaFull)) break;
-                ++n_q;
-                tcgen05_fence_after();
-                for (int t = t_begin; ok && t <= t_end; ++t, ++g) {
-                    const int s = (int)(g & 1u);
-                    if (!(ok = w.wait(full(s), (g >> 1) & 1u, kDevErrMmaFull))) break;   // K_t and V_(t-1)
-                    tcgen05_fence_after();
-                    const uint32_t k_s = sb + Cfg::OFF_K + s * Cfg::KV_BYTES;
-                    const uint32_t v_s = sb + Cfg::OFF_V + s * Cfg::KV_BYTES;
+    if (warp < 4) {
+        reg_dec<Cfg::CONTROL_REGS>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ items + TMA producer
+            // The whole warp walks the items (lanes 0-3 find the intervals of the query tiles' first
+            // and last rows); lane 0 waits, publishes and copies.
+            const uint64_t pol = l2_policy_evict_last();     // K and V are read by every query block
+            const int n_qb = (mk.Sq + NQ * Cfg::BQ - 1) / (NQ * Cfg::BQ);
+            uint32_t n_pub = 0, n_q = 0, g = 0, n_clc = 0;   // items published, Q loads, ring entries, answers
+            uint32_t armed = 0, parity = 0, q_armed = 0, q_parity = 0;
+            bool drop_q = (p.test_flags & kTestDropFirstLoad) && blockIdx.x == 0;
+            bool asked = false;
+            int item = blockIdx.x;
+            while (true) {
+                Item it{-1, 0, 0, {0, 0}, {0, 0}};
+                if (item >= 0) {
+                    // query blocks from the last (under a causal mask the longest) to the first, in
+                    // groups of heads whose K and V stay in L2 together
+                    const int per_group = p.head_group * n_qb, grp = item / per_group, r_in = item - grp * per_group;
+                    const int gsz = min(mk.B * mk.Hq - grp * p.head_group, p.head_group);
+                    const int bh = grp * p.head_group + r_in % gsz;
+                    it.b = bh / mk.Hq;
+                    it.h = bh - it.b * mk.Hq;
+                    it.q_base = (n_qb - 1 - r_in / gsz) * NQ * Cfg::BQ;
+                    // lane 2q: first row of tile q, lane 2q + 1: its last row
+                    int lo = 0, hi = 0;
+                    const int first = it.q_base + (lane >> 1 & 1) * Cfg::BQ;
+                    const int row = lane & 1 ? min(first + Cfg::BQ, mk.Sq) - 1 : first;
+                    if (lane < 4 && first < mk.Sq) row_interval(mk, it.b, row, lo, hi);
 #pragma unroll
                     for (int q = 0; q < NQ; ++q) {
-                        if (t > it.t0[q] && t <= it.t1[q]) {
-                            // O_q += P_q(t-1) V_(t-1)
-                            if (!(ok = w.wait(pfull(q), pv_n[q] & 1u, kDevErrMmaFull))) break;
-                            ++pv_n[q];
-                            tcgen05_fence_after();
-                            const uint32_t p_t = tmem_base + Cfg::T_S + q * 128 + Cfg::P_COL;
+                        const int l = __shfl_sync(0xffffffffu, lo, 2 * q), e = __shfl_sync(0xffffffffu, hi, 2 * q + 1);
+                        it.t0[q] = l / Cfg::BKV;
+                        it.t1[q] = e > l ? (e + Cfg::BKV - 1) / Cfg::BKV : it.t0[q];
+                    }
+                }
+                const uint32_t box = n_pub & 1u;
+                // the box's previous item has been read by every role
+                bool ok = lane != 0 || w.wait(item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                if (lane == 0) {
+                    volatile int* v = item_box + 8 * box;
+                    v[0] = it.b;
+                    v[1] = it.h;
+                    v[2] = it.q_base;
 #pragma unroll
-                            for (int k = 0; k < Cfg::BKV / 16; ++k)
-                                mma_f16_ts(tmem_base + Cfg::T_O + q * D, p_t + k * 8,
-                                           smem_desc_sw128(v_s + k * 2048, Cfg::CHUNK_BYTES, 1024), Cfg::IDESC_PV,
-                                           (t - 1 > it.t0[q] || k > 0) ? 1u : 0u);
-                            if (t == it.t1[q]) mma_commit(odone(q));
-                        }
-                        if (t >= it.t0[q] && t < it.t1[q]) {
-                            // S_q(t) = Q_q K_t^T, over P_q(t-1): one thread's products complete in order
-                            const uint32_t q_s = sb + Cfg::OFF_Q + (qb * NQ + q) * Cfg::Q_BYTES;
+                    for (int q = 0; q < NQ; ++q) {
+                        v[3 + q] = it.t0[q];
+                        v[5 + q] = it.t1[q];
+                    }
+                    mbar_arrive(item_pub(box));              // release: the consumers read the box after
+                }
+                ++n_pub;
+                if (item < 0) break;
+                if (lane == 0) {
+                    const int t_begin = it.first(), t_end = it.last();
+                    if (t_begin < t_end) {
+                        const int qb = (int)(n_q % Cfg::QBUF);
+                        if (n_q >= (uint32_t)Cfg::QBUF)
+                            ok = w.wait(qfree(qb), ((n_q - Cfg::QBUF) / Cfg::QBUF) & 1u, kDevErrProducerEmpty);
+                        if (ok) {
+                            if (drop_q) {
+                                drop_q = false;              // test hook: this Q is never loaded
+                            } else {
+                                const uint32_t qbase = sb + Cfg::OFF_Q + qb * NQ * Cfg::Q_BYTES;
+                                mbar_arrive_expect_tx(qfull(qb), NQ * Cfg::Q_BYTES);
 #pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                const uint32_t off = (k >> 2) * Cfg::CHUNK_BYTES + (k & 3) * 32;
-                                mma_f16_ss(tmem_base + Cfg::T_S + q * 128, smem_desc_sw128(q_s + off, 16, 1024),
-                                           smem_desc_sw128(k_s + off, 16, 1024), Cfg::IDESC_S, k > 0 ? 1u : 0u);
+                                for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                                    for (int c = 0; c < Cfg::DCH; ++c)
+                                        tma_load_4d(qbase + q * Cfg::Q_BYTES + c * Cfg::CHUNK_BYTES, &tmQ, qfull(qb), c * 64,
+                                                    it.q_base + q * Cfg::BQ, it.h, it.b, pol);
+                                q_armed |= 1u << qb;
+                                q_parity = (q_parity & ~(1u << qb)) | ((n_q / Cfg::QBUF) & 1u) << qb;
                             }
-                            mma_commit(sfull(q));
+                            ++n_q;
+                        }
+                        const int hk = it.h / mk.group;
+                        // entry t: K_t (t < t_end) and V_(t-1) (t > t_begin)
+                        for (int t = t_begin; ok && t <= t_end; ++t, ++g) {
+                            const int s = (int)(g & 1u);
+                            const uint32_t ph = (g >> 1) & 1u;
+                            if (!(ok = w.wait(empty(s), ph ^ 1u, kDevErrProducerEmpty))) break;
+                            const bool has_k = t < t_end, has_v = t > t_begin;
+                            mbar_arrive_expect_tx(full(s), (has_k ? Cfg::KV_BYTES : 0) + (has_v ? Cfg::KV_BYTES : 0));
+                            if (has_k) {
+#pragma unroll
+                                for (int c = 0; c < Cfg::DCH; ++c)
+                                    tma_load_4d(sb + Cfg::OFF_K + s * Cfg::KV_BYTES + c * Cfg::CHUNK_BYTES, &tmK, full(s), c * 64,
+                                                t * Cfg::BKV, hk, it.b, pol);
+                            }
+                            if (has_v) {
+#pragma unroll
+                                for (int c = 0; c < Cfg::DCH; ++c)
+                                    tma_load_4d(sb + Cfg::OFF_V + s * Cfg::KV_BYTES + c * Cfg::CHUNK_BYTES, &tmV, full(s), c * 64,
+                                                (t - 1) * Cfg::BKV, hk, it.b, pol);
+                            }
+                            armed |= 1u << s;
+                            parity = (parity & ~(1u << s)) | ph << s;
                         }
                     }
-                    if (!ok) break;
-                    if (t == t_end - 1) mma_commit(qfree(qb));   // the item's last Q K^T products are issued
-                    mma_commit(empty(s));
+                    // the next item, asked for once this one's copies are issued: earlier, a CTA busy with a
+                    // long item would hold one that another could start
+                    if (ok) {
+                        fence_proxy_async_smem();            // the last answer has been read
+                        mbar_arrive_expect_tx(clc, 16);
+                        clc_try_cancel(sb + Cfg::OFF_CLC, clc);
+                        asked = true;
+                        if ((ok = w.wait(clc, n_clc & 1u, kDevErrProducerEmpty))) {
+                            asked = false;
+                            item = clc_taken(sb + Cfg::OFF_CLC);
+                        }
+                    }
                 }
+                ++n_clc;
+                if (!__all_sync(0xffffffffu, ok)) break;
+                item = __shfl_sync(0xffffffffu, item, 0);
             }
-            mma_commit(drain);
-            w.drain(drain, 0);
+            // every copy and answer under way must land before the CTA may exit
+            if (lane == 0) {
+                if (asked) w.drain(clc, (n_clc - 1) & 1u);
+                for (int b = 0; b < Cfg::QBUF; ++b)
+                    if (q_armed & (1u << b)) w.drain(qfull(b), (q_parity >> b) & 1u);
+                for (int s = 0; s < 2; ++s)
+                    if (armed & (1u << s)) w.drain(full(s), (parity >> s) & 1u);
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issuer
+            if (lane == 0) {
+                uint32_t n_item = 0, n_q = 0, g = 0;
+                uint32_t pv_n[NQ] = {0u, 0u};                // pfull phases waited for, per query tile
+                bool ok = true;
+                while (ok) {
+                    const uint32_t box = n_item & 1u;
+                    if (!w.wait(item_pub(box), (n_item >> 1) & 1u, kDevErrMmaFull)) break;
+                    const Item it = read_item(box);
+                    mbar_arrive(item_read(box));
+                    ++n_item;
+                    if (it.b < 0) break;
+                    const int t_begin = it.first(), t_end = it.last();
+                    if (t_begin >= t_end) continue;
+                    const int qb = (int)(n_q % Cfg::QBUF);
+                    if (!w.wait(qfull(qb), (n_q / Cfg::QBUF) & 1u, kDevErrMmaFull)) break;
+                    ++n_q;
+                    tcgen05_fence_after();
+                    for (int t = t_begin; ok && t <= t_end; ++t, ++g) {
+                        const int s = (int)(g & 1u);
+                        if (!(ok = w.wait(full(s), (g >> 1) & 1u, kDevErrMmaFull))) break;   // K_t and V_(t-1)
+                        tcgen05_fence_after();
+                        const uint32_t k_s = sb + Cfg::OFF_K + s * Cfg::KV_BYTES;
+                        const uint32_t v_s = sb + Cfg::OFF_V + s * Cfg::KV_BYTES;
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) {
+                            if (t > it.t0[q] && t <= it.t1[q]) {
+                                // O_q += P_q(t-1) V_(t-1)
+                                if (!(ok = w.wait(pfull(q), pv_n[q] & 1u, kDevErrMmaFull))) break;
+                                ++pv_n[q];
+                                tcgen05_fence_after();
+                                const uint32_t p_t = tmem_base + Cfg::T_S + q * 128 + Cfg::P_COL;
+#pragma unroll
+                                for (int k = 0; k < Cfg::BKV / 16; ++k)
+                                    mma_f16_ts(tmem_base + Cfg::T_O + q * D, p_t + k * 8,
+                                               smem_desc_sw128(v_s + k * 2048, Cfg::CHUNK_BYTES, 1024), Cfg::IDESC_PV,
+                                               (t - 1 > it.t0[q] || k > 0) ? 1u : 0u);
+                                if (t == it.t1[q]) mma_commit(odone(q));
+                            }
+                            if (t >= it.t0[q] && t < it.t1[q]) {
+                                // S_q(t) = Q_q K_t^T, over P_q(t-1): one thread's products complete in order
+                                const uint32_t q_s = sb + Cfg::OFF_Q + (qb * NQ + q) * Cfg::Q_BYTES;
+#pragma unroll
+                                for (int k = 0; k < D / 16; ++k) {
+                                    const uint32_t off = (k >> 2) * Cfg::CHUNK_BYTES + (k & 3) * 32;
+                                    mma_f16_ss(tmem_base + Cfg::T_S + q * 128, smem_desc_sw128(q_s + off, 16, 1024),
+                                               smem_desc_sw128(k_s + off, 16, 1024), Cfg::IDESC_S, k > 0 ? 1u : 0u);
+                                }
+                                mma_commit(sfull(q));
+                            }
+                        }
+                        if (!ok) break;
+                        if (t == t_end - 1) mma_commit(qfree(qb));   // the item's last Q K^T products are issued
+                        mma_commit(empty(s));
+                    }
+                }
+                mma_commit(drain);
+                w.drain(drain, 0);
+            }
+            __syncwarp();
         }
-        __syncwarp();
     } else {
-        // ------------------------------------------------------------ softmax + output (warps 2-9)
-        const int q = (warp - 2) >> 2;
+        reg_inc<Cfg::SOFTMAX_REGS>();
+        // ------------------------------------------------------------ softmax + output (warps 4-11)
+        const int q = (warp - 4) >> 2;
         const int quad = warp & 3;
         const int r = quad * 32 + lane;
         const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
