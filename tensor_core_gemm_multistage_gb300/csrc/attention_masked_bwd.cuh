@@ -276,7 +276,11 @@ constexpr float kCapFactor = kHasCap<MODE> ? 4.0f : 1.0f;
 // dK and dV
 // ---------------------------------------------------------------------------
 // A work item is 128 keys of one key/value head; its steps are the query tiles that see any of them,
-// for every query head of the group.  Per step
+// for every query head of the group.  Where such items are few for the SMs (grouped heads, one
+// batch row), their steps are cut into p.splits equal runs, each an item that leaves its sums in
+// fp32 in the workspace, and another launch adds them up in order: 8192 tokens in 4 documents, 4
+// key/value heads, have 256 items of 4 to 168 steps, and the longest alone took 1.5 times an SM's
+// even share.  Per step
 //     S^T = K Q^T,  dP^T = V dO^T       [128 keys x 128 queries] into 128 TMEM columns each
 //     P^T over S^T's columns, dV += P^T dO;   dS^T over dP^T's columns, dK += dS^T Q
 // with P^T and dS^T read from TMEM.  At D = 128 the four fill all 512 columns.  The products are
@@ -358,6 +362,47 @@ __device__ __forceinline__ bool store_accumulator(uint32_t col, float factor, bo
     return bad;
 }
 
+// Row j of part `split` of dV (which 0) or dK (1) in the workspace.
+__device__ __forceinline__ float* part_row(const MaskedBwdParams& p, int which, int split, int bh, int j, int D) {
+    return p.parts + ((((long long)which * p.splits + split) * (p.mask.B * p.mask.Hkv) + bh) * p.mask.Skv + j) * D;
+}
+
+// The parts' sums, in order.  One warp a row of dK or dV; bound by the read of the parts.
+template <class T, int D>
+__global__ void __launch_bounds__(256) gsr_masked_dkv_sum_kernel(const __grid_constant__ MaskedBwdParams p) {
+    const MaskArgs& mk = p.mask;
+    const int lane = threadIdx.x & 31;
+    const long long rows = (long long)mk.B * mk.Hkv * mk.Skv, id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (id >= 2 * rows) return;
+    const int which = id >= rows;
+    const long long row = id - (which ? rows : 0);
+    const int bh = (int)(row / mk.Skv), j = (int)(row - (long long)bh * mk.Skv), b = bh / mk.Hkv, hk = bh - b * mk.Hkv;
+    float acc[D / 32] = {};
+    for (int s = 0; s < p.splits; ++s) {
+        const float* x = part_row(p, which, s, bh, j, D) + lane * (D / 32);
+        if constexpr (D == 128) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(x));
+            acc[0] += v.x;
+            acc[1] += v.y;
+            acc[2] += v.z;
+            acc[3] += v.w;
+        } else {
+            const float2 v = __ldg(reinterpret_cast<const float2*>(x));
+            acc[0] += v.x;
+            acc[1] += v.y;
+        }
+    }
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) bad |= !(fabsf(acc[e]) < INFINITY);
+    if (__any_sync(0xffffffffu, bad)) {
+        row_dkv<T, D>(p, b, hk, j, which == 1, lane);
+        return;
+    }
+    const Strided& out = which ? p.dK : p.dV;
+    store_row<T, D>(static_cast<T*>(out.data) + b * out.batch + hk * out.head + (long long)j * out.row, lane, acc);
+}
+
 template <class Cfg>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     gsr_masked_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -387,13 +432,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const MaskArgs& mk = p.mask;
 
-    // What the producer publishes; b < 0: no more items.  Query tiles [t0, t1) see some of the keys.
+    // What the producer publishes; b < 0: no more items.  Query tiles [t0, t1) see some of the keys;
+    // step k is tile t0 + k % (t1 - t0) of the group's head k / (t1 - t0), and the item runs steps
+    // [begin, end) of them, as part `split` of p.splits.
     struct Item {
-        int b, hk, k0, t0, t1;
+        int b, hk, k0, t0, t1, begin, end, split;
     };
     auto read_item = [&](int box) {
         volatile int* v = item_box + 8 * box;
-        return Item{v[0], v[1], v[2], v[3], v[4]};
+        return Item{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
     };
 
     if (threadIdx.x == 0) {
@@ -450,16 +497,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             parity = (parity & ~(1u << i)) | (ph & 1u) << i;
         };
         while (true) {
-            Item it{-1, 0, 0, 0, 0};
+            Item it{-1, 0, 0, 0, 0, 0, 0, 0};
             if (item >= 0) {
                 // key tiles from the first (under a causal mask the most queries see it) to the last,
                 // in groups of key/value heads whose Q and dO stay in L2 together
-                const int per_group = p.kv_head_group * n_kt, grp = item / per_group, r_in = item - grp * per_group;
+                const int per_group = p.kv_head_group * n_kt * p.splits, grp = item / per_group, r_in = item - grp * per_group;
                 const int gsz = min(mk.B * mk.Hkv - grp * p.kv_head_group, p.kv_head_group);
                 const int bh = grp * p.kv_head_group + r_in % gsz;
                 it.b = bh / mk.Hkv;
                 it.hk = bh - it.b * mk.Hkv;
-                it.k0 = r_in / gsz * kTile;
+                it.split = r_in / gsz % p.splits;
+                it.k0 = r_in / gsz / p.splits * kTile;
                 // lane 0: the queries that see the tile's first key, lane 1: its last
                 int first = 0, end = 0;
                 if (lane < 2) key_interval(mk, it.b, lane == 0 ? it.k0 : min(it.k0 + kTile, mk.Skv) - 1, first, end);
@@ -467,6 +515,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 first = __shfl_sync(0xffffffffu, first, 0);
                 it.t0 = first / kTile;
                 it.t1 = first < end ? (end + kTile - 1) / kTile : it.t0;
+                const long long steps = (long long)(it.t1 - it.t0) * mk.group;
+                it.begin = (int)(steps * it.split / p.splits);
+                it.end = (int)(steps * (it.split + 1) / p.splits);
             }
             const uint32_t box = n_pub & 1u;
             bool ok = lane != 0 || w.wait(item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty);
@@ -478,12 +529,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 v[2] = it.k0;
                 v[3] = it.t0;
                 v[4] = it.t1;
+                v[5] = it.begin;
+                v[6] = it.end;
+                v[7] = it.split;
                 mbar_arrive(item_pub(box));
             }
             ++n_pub;
             if (item < 0) break;
             if (lane == 0) {
-                if (it.t0 < it.t1) {
+                if (it.begin < it.end) {
                     ok = w.wait(kv_empty, (n_item & 1u) ^ 1u, kDevErrProducerEmpty);
                     if (ok && !drop) {
                         mbar_arrive_expect_tx(kv_full, 2 * Cfg::TILE_BYTES);
@@ -496,30 +550,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     }
                     drop = false;                        // test hook: the first K and V are never loaded
                     ++n_item;
-                    for (int h = it.hk * mk.group; ok && h < (it.hk + 1) * mk.group; ++h) {
+                    const int tiles = it.t1 - it.t0;
+                    for (int k = it.begin; ok && k < it.end; ++k, ++n) {
+                        const int h = it.hk * mk.group + k / tiles, t = it.t0 + k % tiles;
                         const long long row0 = ((long long)it.b * mk.Hq + h) * p.Sp;
-                        for (int t = it.t0; t < it.t1; ++t, ++n) {
-                            const int sq = (int)(n % NQ), so = (int)(n % NO);
-                            const uint32_t ph_q = n / NQ, ph_o = n / NO;
-                            if (!(ok = w.wait(q_empty(sq), (ph_q & 1u) ^ 1u, kDevErrProducerEmpty))) break;
-                            mbar_arrive_expect_tx(q_full(sq), Cfg::TILE_BYTES);
+                        const int sq = (int)(n % NQ), so = (int)(n % NO);
+                        const uint32_t ph_q = n / NQ, ph_o = n / NO;
+                        if (!(ok = w.wait(q_empty(sq), (ph_q & 1u) ^ 1u, kDevErrProducerEmpty))) break;
+                        mbar_arrive_expect_tx(q_full(sq), Cfg::TILE_BYTES);
 #pragma unroll
-                            for (int c = 0; c < DCH; ++c)
-                                tma_load_4d(sb + Cfg::OFF_Q + sq * Cfg::TILE_BYTES + c * kChunkBytes, &tmQ, q_full(sq), c * 64,
-                                            t * kTile, h, it.b, pol);
-                            arm(sq, ph_q);
-                            if (!(ok = w.wait(o_empty(so), (ph_o & 1u) ^ 1u, kDevErrProducerEmpty) &&
-                                       w.wait(rows_empty(so), (ph_o & 1u) ^ 1u, kDevErrProducerEmpty)))
-                                break;
-                            mbar_arrive_expect_tx(o_full(so), Cfg::TILE_BYTES + 1024);
+                        for (int c = 0; c < DCH; ++c)
+                            tma_load_4d(sb + Cfg::OFF_Q + sq * Cfg::TILE_BYTES + c * kChunkBytes, &tmQ, q_full(sq), c * 64,
+                                        t * kTile, h, it.b, pol);
+                        arm(sq, ph_q);
+                        if (!(ok = w.wait(o_empty(so), (ph_o & 1u) ^ 1u, kDevErrProducerEmpty) &&
+                                   w.wait(rows_empty(so), (ph_o & 1u) ^ 1u, kDevErrProducerEmpty)))
+                            break;
+                        mbar_arrive_expect_tx(o_full(so), Cfg::TILE_BYTES + 1024);
 #pragma unroll
-                            for (int c = 0; c < DCH; ++c)
-                                tma_load_4d(sb + Cfg::OFF_O + so * Cfg::TILE_BYTES + c * kChunkBytes, &tmO, o_full(so), c * 64,
-                                            t * kTile, h, it.b, pol);
-                            bulk_load(sb + Cfg::OFF_ROWS + so * 1024, p.offset + row0 + t * kTile, 512, o_full(so));
-                            bulk_load(sb + Cfg::OFF_ROWS + so * 1024 + 512, p.neg_delta + row0 + t * kTile, 512, o_full(so));
-                            arm(3 + so, ph_o);
-                        }
+                        for (int c = 0; c < DCH; ++c)
+                            tma_load_4d(sb + Cfg::OFF_O + so * Cfg::TILE_BYTES + c * kChunkBytes, &tmO, o_full(so), c * 64,
+                                        t * kTile, h, it.b, pol);
+                        bulk_load(sb + Cfg::OFF_ROWS + so * 1024, p.offset + row0 + t * kTile, 512, o_full(so));
+                        bulk_load(sb + Cfg::OFF_ROWS + so * 1024 + 512, p.neg_delta + row0 + t * kTile, 512, o_full(so));
+                        arm(3 + so, ph_o);
                     }
                 }
                 // the next item, asked for once this one's copies are issued: earlier, a CTA busy with a
@@ -558,7 +612,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 mbar_arrive(item_read(box));
                 ++n_box;
                 if (it.b < 0) break;
-                const int steps = (it.t1 - it.t0) * mk.group;
+                const int steps = it.end - it.begin;
                 if (steps <= 0) continue;
                 if (!w.wait(kv_full, n_item & 1u, kDevErrMmaFull)) break;
                 ++n_item;
@@ -618,89 +672,93 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int j = it.k0 + r;
             int first = 0, end = 0;                      // the queries that see this thread's key
             if (j < mk.Skv) key_interval(mk, it.b, j, first, end);
-            for (int h = it.hk * mk.group; ok && h < (it.hk + 1) * mk.group; ++h) {
+            const int tiles = max(it.t1 - it.t0, 1);
+            int h = it.hk * mk.group + it.begin / tiles, t = it.t0 + it.begin % tiles;
+            for (int k = it.begin; k < it.end; ++k, ++n, ++t) {
+                if (t == it.t1) {
+                    t = it.t0;
+                    ++h;
+                }
                 const float slope2 = kHasBias<Cfg::MODE> ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
-                for (int t = it.t0; t < it.t1; ++t, ++n) {
-                    const int i0 = t * kTile + half * 64;
-                    const bool masked = i0 < first || i0 + 64 > end;
-                    if (!__all_sync(0xffffffffu, w.wait(o_full((int)(n % NO)), (n / NO) & 1u, kDevErrEpilogueFull) &&
-                                                     w.wait(s_full, n & 1u, kDevErrEpilogueFull))) {
-                        ok = false;
-                        break;
-                    }
-                    tcgen05_fence_after();
-                    const float* rows = reinterpret_cast<const float*>(smem + Cfg::OFF_ROWS + (n % NO) * 1024) + half * 64;
-                    const float base = (float)(j - mk.offset - i0);
-                    uint32_t w0[32], w1[32];
-                    tmem_ld_32x32b_x32(s_col, w0);
-                    tmem_ld_32x32b_x32(s_col + 32, w1);
-                    tmem_ld_wait(w0);
-                    reg_tie(w1);
-                    auto p_chunk = [&](uint32_t (&rr)[32], int c) {
-                        uint32_t packed[16];
-                        weights_chunk<T, Cfg::MODE, true>(rr, p.score, slope2, base - (float)(c * 32),
-                                                          [&](int i) { return *reinterpret_cast<const float2*>(rows + c * 32 + i); },
-                                                          packed);
-                        if (masked) {
+                const int i0 = t * kTile + half * 64;
+                const bool masked = i0 < first || i0 + 64 > end;
+                if (!__all_sync(0xffffffffu, w.wait(o_full((int)(n % NO)), (n / NO) & 1u, kDevErrEpilogueFull) &&
+                                                 w.wait(s_full, n & 1u, kDevErrEpilogueFull))) {
+                    ok = false;
+                    break;
+                }
+                tcgen05_fence_after();
+                const float* rows = reinterpret_cast<const float*>(smem + Cfg::OFF_ROWS + (n % NO) * 1024) + half * 64;
+                const float base = (float)(j - mk.offset - i0);
+                uint32_t w0[32], w1[32];
+                tmem_ld_32x32b_x32(s_col, w0);
+                tmem_ld_32x32b_x32(s_col + 32, w1);
+                tmem_ld_wait(w0);
+                reg_tie(w1);
+                auto p_chunk = [&](uint32_t (&rr)[32], int c) {
+                    uint32_t packed[16];
+                    weights_chunk<T, Cfg::MODE, true>(rr, p.score, slope2, base - (float)(c * 32),
+                                                      [&](int i) { return *reinterpret_cast<const float2*>(rows + c * 32 + i); },
+                                                      packed);
+                    if (masked) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c * 32 + i < first - i0 || c * 32 + i >= end - i0) {
-                                    rr[i] = 0u;
-                                    packed[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
-                                }
-                        }
-                        tmem_st_32x32b_x16(s_col + c * 16, packed);
-                        if (!Elem<T>::bf16) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float a, b;
-                                fmul2(a, b, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]), ds_mul, ds_mul);
-                                rr[i] = __float_as_uint(a);
-                                rr[i + 1] = __float_as_uint(b);
+                        for (int i = 0; i < 32; ++i)
+                            if (c * 32 + i < first - i0 || c * 32 + i >= end - i0) {
+                                rr[i] = 0u;
+                                packed[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
                             }
-                        }
-                    };
-                    p_chunk(w0, 0);
-                    p_chunk(w1, 1);
-                    tmem_st_wait();
-                    tcgen05_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_full);
-                    if (!__all_sync(0xffffffffu, w.wait(dp_full, n & 1u, kDevErrEpilogueFull))) {
-                        ok = false;
-                        break;
                     }
-                    tcgen05_fence_after();
-                    auto ds_chunk = [&](const uint32_t (&ww)[32], int c) {
-                        uint32_t dp[32], packed[16];
-                        tmem_ld_32x32b_x32(dp_col + c * 32, dp);
-                        tmem_ld_wait(dp);
+                    tmem_st_32x32b_x16(s_col + c * 16, packed);
+                    if (!Elem<T>::bf16) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
-                            const float2 nd = *reinterpret_cast<const float2*>(rows + 128 + c * 32 + i);
-                            float d0 = __uint_as_float(dp[i]), d1 = __uint_as_float(dp[i + 1]);
-                            fadd2(d0, d1, nd.x, nd.y);
-                            fmul2(d0, d1, d0, d1, __uint_as_float(ww[i]), __uint_as_float(ww[i + 1]));
-                            packed[i / 2] = Elem<T>::pack(d0, d1);
+                            float a, b;
+                            fmul2(a, b, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]), ds_mul, ds_mul);
+                            rr[i] = __float_as_uint(a);
+                            rr[i + 1] = __float_as_uint(b);
                         }
-                        if (masked) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c * 32 + i < first - i0 || c * 32 + i >= end - i0) packed[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
-                        }
-                        // columns 0-15 of this half hold dP values of chunk 0 only: read above
-                        tmem_st_32x32b_x16(dp_col + c * 16, packed);
-                    };
-                    ds_chunk(w0, 0);
-                    ds_chunk(w1, 1);
-                    tmem_st_wait();
-                    tcgen05_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(ds_full);
+                    }
+                };
+                p_chunk(w0, 0);
+                p_chunk(w1, 1);
+                tmem_st_wait();
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full);
+                if (!__all_sync(0xffffffffu, w.wait(dp_full, n & 1u, kDevErrEpilogueFull))) {
+                    ok = false;
+                    break;
                 }
+                tcgen05_fence_after();
+                auto ds_chunk = [&](const uint32_t (&ww)[32], int c) {
+                    uint32_t dp[32], packed[16];
+                    tmem_ld_32x32b_x32(dp_col + c * 32, dp);
+                    tmem_ld_wait(dp);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 nd = *reinterpret_cast<const float2*>(rows + 128 + c * 32 + i);
+                        float d0 = __uint_as_float(dp[i]), d1 = __uint_as_float(dp[i + 1]);
+                        fadd2(d0, d1, nd.x, nd.y);
+                        fmul2(d0, d1, d0, d1, __uint_as_float(ww[i]), __uint_as_float(ww[i + 1]));
+                        packed[i / 2] = Elem<T>::pack(d0, d1);
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c * 32 + i < first - i0 || c * 32 + i >= end - i0) packed[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+                    }
+                    // columns 0-15 of this half hold dP values of chunk 0 only: read above
+                    tmem_st_32x32b_x16(dp_col + c * 16, packed);
+                };
+                ds_chunk(w0, 0);
+                ds_chunk(w1, 1);
+                tmem_st_wait();
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ds_full);
             }
             if (!ok) break;
-            const bool none = it.t0 >= it.t1;
+            const bool none = it.begin >= it.end;
             if (!none) {
                 ok = __all_sync(0xffffffffu, w.wait(done, n_done & 1u, kDevErrEpilogueFull));
                 ++n_done;
@@ -709,10 +767,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             // half 0 writes dV's rows, half 1 dK's.  The next item's products overwrite the accumulators
             // only after this warp's next P and dS.
-            const Strided& out = half == 0 ? p.dV : p.dK;
+            const uint32_t col = lane_base + (half == 0 ? Cfg::T_DV : Cfg::T_DK);
             const float factor = half == 0 ? exp2f(-kPShift<T>) : kCapFactor<Cfg::MODE> * p.score.scale * exp2f(-kPShift<T> - shift);
+            if (p.splits > 1) {
+                float* row = part_row(p, half, it.split, it.b * mk.Hkv + it.hk, j, D);
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t rr[32];
+                    tmem_ld_32x32b_x32(col + c * 32, rr);
+                    tmem_ld_wait(rr);
+                    if (j < mk.Skv) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 v = make_float4(__uint_as_float(rr[i]) * factor, __uint_as_float(rr[i + 1]) * factor,
+                                                         __uint_as_float(rr[i + 2]) * factor, __uint_as_float(rr[i + 3]) * factor);
+                            *reinterpret_cast<float4*>(row + c * 32 + i) = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : v;
+                        }
+                    }
+                }
+                tcgen05_fence_before();
+                continue;
+            }
+            const Strided& out = half == 0 ? p.dV : p.dK;
             T* row = static_cast<T*>(out.data) + it.b * out.batch + it.hk * out.head + (long long)j * out.row;
-            const bool bad = store_accumulator<T, D>(lane_base + (half == 0 ? Cfg::T_DV : Cfg::T_DK), factor, none, j < mk.Skv, row);
+            const bool bad = store_accumulator<T, D>(col, factor, none, j < mk.Skv, row);
             tcgen05_fence_before();
             __syncwarp();
             for (uint32_t again = __ballot_sync(0xffffffffu, bad); again; again &= again - 1)
@@ -1087,8 +1165,12 @@ cudaError_t launch_dkv(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaSt
     static std::atomic<uint64_t> attr_done{0};
     const cudaError_t e = allow_smem(gsr_masked_dkv_kernel<Cfg>, Cfg::SMEM_BYTES, attr_done);
     if (e != cudaSuccess) return e;
-    const int items = (p.mask.Skv + kTile - 1) / kTile * p.mask.B * p.mask.Hkv;
+    const int items = (p.mask.Skv + kTile - 1) / kTile * p.mask.B * p.mask.Hkv * p.splits;
     gsr_masked_dkv_kernel<Cfg><<<(unsigned)items, kBwdThreads, Cfg::SMEM_BYTES, stream>>>(tm.q, tm.k, tm.v, tm.dO, p);
+    if (p.splits > 1) {
+        const long long rows = 2ll * p.mask.B * p.mask.Hkv * p.mask.Skv;
+        gsr_masked_dkv_sum_kernel<typename Cfg::T, Cfg::D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p);
+    }
     return cudaGetLastError();
 }
 

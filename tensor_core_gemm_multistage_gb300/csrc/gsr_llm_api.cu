@@ -13,6 +13,7 @@ using gsr::Strided;
 
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 bool bad_size(int64_t n) { return n < 0 || n > INT_MAX; }
+constexpr int64_t kSms = 152;   // of a GB300, where sizes are planned without a device
 // The tensor maps' strides are below 2^40 bytes; no operand spans more than 2^60 elements.
 constexpr int64_t kMaxStride = ((int64_t)1 << 39) - 8;
 
@@ -150,7 +151,7 @@ int heads_in_l2(int causal, int64_t bytes, int64_t group, int64_t heads) {
 
 // Layout of the backward pass's workspace, 256-byte pieces.
 struct BwdLayout {
-    int64_t sp, offset, delta, total;
+    int64_t sp, splits, offset, delta, parts, total;
 };
 BwdLayout bwd_layout(const gsr_attention_desc* d) {
     auto piece = [](int64_t bytes) { return (bytes + 255) / 256 * 256; };
@@ -158,7 +159,17 @@ BwdLayout bwd_layout(const gsr_attention_desc* d) {
     w.sp = (d->seq_q + 127) / 128 * 128;
     w.offset = 256;                                                     // the norms come first
     w.delta = w.offset + piece(4 * d->batch * d->heads_q * w.sp);
-    w.total = w.delta + piece(4 * d->batch * d->heads_q * w.sp);
+    w.parts = w.delta + piece(4 * d->batch * d->heads_q * w.sp);
+    // A key tile's steps are cut into parts until there are four items an SM, at most four parts
+    // (each costs a write and a read of dK and dV in fp32) of four steps or more.  8192 tokens in 4
+    // documents, 16 heads over 4 (256 items): 709 us whole, DKV_SPLIT_FIGURE.
+    const int64_t items = d->batch * d->heads_kv * ((d->seq_kv + 127) / 128);
+    const int64_t steps = d->heads_kv > 0 ? d->heads_q / d->heads_kv * (w.sp / 128) : 0;
+    int64_t n = items > 0 ? (4 * kSms + items - 1) / items : 1;
+    if (n > 4) n = 4;
+    if (n > steps / 4) n = steps / 4;
+    w.splits = n < 1 ? 1 : n;
+    w.total = w.parts + (w.splits > 1 ? piece(8 * w.splits * d->batch * d->heads_kv * d->seq_kv * d->head_dim) : 0);
     return w;
 }
 
@@ -308,6 +319,8 @@ gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor
     p.Sp = (int)w.sp;
     p.offset = reinterpret_cast<float*>(base + w.offset);
     p.neg_delta = reinterpret_cast<float*>(base + w.delta);
+    p.splits = (int)w.splits;
+    p.parts = reinterpret_cast<float*>(base + w.parts);
     p.timeout_ns = gsr::host::wait_timeout_ns();
     p.test_flags = gsr::host::test_flags();
     gsr::MaskedBwdMaps tm;

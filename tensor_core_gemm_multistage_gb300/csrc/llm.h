@@ -65,6 +65,8 @@ struct MaskedBwdParams {
     float* neg_delta;           // (B, Hq, Sp): -rowsum(dO * O)
     unsigned* norms;            // [0] max |dO_i|^2, [1] max |V_j|^2, as the bits of a float (fp16 only)
     int q_head_group, kv_head_group;   // item order of dQ, of dK and dV: heads taken together
+    int splits;                 // parts of a key tile's steps
+    float* parts;               // splits > 1: (2, splits, B, Hkv, Skv, D) partial dV and dK
     int* err;
     uint64_t timeout_ns;
     uint32_t test_flags;
