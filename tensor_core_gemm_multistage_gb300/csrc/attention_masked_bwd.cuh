@@ -23,6 +23,8 @@
 // warp from the pairs it sees alone (row_dq, row_dkv).
 #pragma once
 
+#include <type_traits>
+
 #include "attention_common.cuh"
 #include "ptx_attention.cuh"
 
@@ -232,10 +234,13 @@ __device__ __noinline__ void row_dkv(const MaskedBwdParams& p, int b, int hk, in
 // ---------------------------------------------------------------------------
 // Shared by the two tensor-core kernels
 // ---------------------------------------------------------------------------
-// 320 threads: warp 0 copies, one lane of warp 1 issues the products, warps 2-9 do the arithmetic
-// between them.  Warps w and w + 4 share 32 TMEM lanes and take 64 of the 128 columns each.
-constexpr int kBwdThreads = 320;
+// 384 threads: warp 0 copies, one lane of warp 1 issues the products, warps 4-11 do the arithmetic
+// between them.  Warps w and w + 4 share 32 TMEM lanes and take 64 of the 128 columns each.  The
+// threads start with 168 registers each and the first four warps give some to the others: 72 + 2 x
+// 216 = 3 x 168.
+constexpr int kBwdThreads = 384;
 constexpr int kBwdMathWarps = 8;
+constexpr int kBwdControlRegs = 72, kBwdMathRegs = 216;
 constexpr int kTile = 128;
 constexpr int kChunkBytes = 128 * 128;
 
@@ -367,40 +372,49 @@ __device__ __forceinline__ float* part_row(const MaskedBwdParams& p, int which, 
     return p.parts + ((((long long)which * p.splits + split) * (p.mask.B * p.mask.Hkv) + bh) * p.mask.Skv + j) * D;
 }
 
-// The parts' sums, in order.  One warp a row of dK or dV; bound by the read of the parts.
+// The parts' sums, in order.  A warp takes kSumRows rows of dK or dV, all loads before the first sum;
+// bound by the read of the parts.
+constexpr int kSumRows = 2, kMaxSplits = 4;
 template <class T, int D>
 __global__ void __launch_bounds__(256) gsr_masked_dkv_sum_kernel(const __grid_constant__ MaskedBwdParams p) {
+    using V = typename std::conditional<D == 128, float4, float2>::type;
     const MaskArgs& mk = p.mask;
     const int lane = threadIdx.x & 31;
-    const long long rows = (long long)mk.B * mk.Hkv * mk.Skv, id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (id >= 2 * rows) return;
-    const int which = id >= rows;
-    const long long row = id - (which ? rows : 0);
-    const int bh = (int)(row / mk.Skv), j = (int)(row - (long long)bh * mk.Skv), b = bh / mk.Hkv, hk = bh - b * mk.Hkv;
-    float acc[D / 32] = {};
-    for (int s = 0; s < p.splits; ++s) {
-        const float* x = part_row(p, which, s, bh, j, D) + lane * (D / 32);
-        if constexpr (D == 128) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(x));
-            acc[0] += v.x;
-            acc[1] += v.y;
-            acc[2] += v.z;
-            acc[3] += v.w;
-        } else {
-            const float2 v = __ldg(reinterpret_cast<const float2*>(x));
-            acc[0] += v.x;
-            acc[1] += v.y;
-        }
-    }
-    bool bad = false;
+    const long long rows = (long long)mk.B * mk.Hkv * mk.Skv, first = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kSumRows;
+    V x[kSumRows][kMaxSplits];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) bad |= !(fabsf(acc[e]) < INFINITY);
-    if (__any_sync(0xffffffffu, bad)) {
-        row_dkv<T, D>(p, b, hk, j, which == 1, lane);
-        return;
+    for (int k = 0; k < kSumRows; ++k)
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s) {
+            const long long id = first + k;
+            x[k][s] = V{};
+            if (s < p.splits && id < 2 * rows) {         // dV's parts lie before dK's
+                const long long part = id < rows ? s : p.splits + s, row = id < rows ? id : id - rows;
+                x[k][s] = __ldg(reinterpret_cast<const V*>(p.parts + (part * rows + row) * D) + lane);
+            }
+        }
+#pragma unroll
+    for (int k = 0; k < kSumRows; ++k) {
+        const long long id = first + k;
+        if (id >= 2 * rows) return;
+        const int which = id >= rows;
+        const long long row = id - (which ? rows : 0);
+        const int bh = (int)(row / mk.Skv), j = (int)(row - (long long)bh * mk.Skv), b = bh / mk.Hkv, hk = bh - b * mk.Hkv;
+        float acc[D / 32] = {};
+        bool bad = false;
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s)
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) acc[e] += reinterpret_cast<const float*>(&x[k][s])[e];
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) bad |= !(fabsf(acc[e]) < INFINITY);
+        if (__any_sync(0xffffffffu, bad)) {
+            row_dkv<T, D>(p, b, hk, j, which == 1, lane);
+            continue;
+        }
+        const Strided& out = which ? p.dK : p.dV;
+        store_row<T, D>(static_cast<T*>(out.data) + b * out.batch + hk * out.head + (long long)j * out.row, lane, acc);
     }
-    const Strided& out = which ? p.dK : p.dV;
-    store_row<T, D>(static_cast<T*>(out.data) + b * out.batch + hk * out.head + (long long)j * out.row, lane, acc);
 }
 
 template <class Cfg>
@@ -483,177 +497,181 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t tmem_base = *tmem_slot;
     const Waiter w{p.err, p.timeout_ns, abort_flag, kDevErrKernelMaskedDkv};
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ items + TMA producer
-        const uint64_t pol = l2_policy_evict_last();     // Q and dO are read by every key tile
-        const int n_kt = (mk.Skv + kTile - 1) / kTile;
-        uint32_t n_pub = 0, n_item = 0, n_clc = 0, n = 0;   // items published, items with steps, answers, steps
-        uint32_t armed = 0, parity = 0;                  // per barrier q_full 0-2, o_full 3-4, kv_full 5
-        bool drop = (p.test_flags & kTestDropFirstLoad) && blockIdx.x == 0;
-        bool asked = false;
-        int item = blockIdx.x;
-        auto arm = [&](int i, uint32_t ph) {
-            armed |= 1u << i;
-            parity = (parity & ~(1u << i)) | (ph & 1u) << i;
-        };
-        while (true) {
-            Item it{-1, 0, 0, 0, 0, 0, 0, 0};
-            if (item >= 0) {
-                // key tiles from the first (under a causal mask the most queries see it) to the last,
-                // in groups of key/value heads whose Q and dO stay in L2 together
-                const int per_group = p.kv_head_group * n_kt * p.splits, grp = item / per_group, r_in = item - grp * per_group;
-                const int gsz = min(mk.B * mk.Hkv - grp * p.kv_head_group, p.kv_head_group);
-                const int bh = grp * p.kv_head_group + r_in % gsz;
-                it.b = bh / mk.Hkv;
-                it.hk = bh - it.b * mk.Hkv;
-                it.split = r_in / gsz % p.splits;
-                it.k0 = r_in / gsz / p.splits * kTile;
-                // lane 0: the queries that see the tile's first key, lane 1: its last
-                int first = 0, end = 0;
-                if (lane < 2) key_interval(mk, it.b, lane == 0 ? it.k0 : min(it.k0 + kTile, mk.Skv) - 1, first, end);
-                end = __shfl_sync(0xffffffffu, end, 1);
-                first = __shfl_sync(0xffffffffu, first, 0);
-                it.t0 = first / kTile;
-                it.t1 = first < end ? (end + kTile - 1) / kTile : it.t0;
-                const long long steps = (long long)(it.t1 - it.t0) * mk.group;
-                it.begin = (int)(steps * it.split / p.splits);
-                it.end = (int)(steps * (it.split + 1) / p.splits);
-            }
-            const uint32_t box = n_pub & 1u;
-            bool ok = lane != 0 || w.wait(item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            if (lane == 0) {
-                volatile int* v = item_box + 8 * box;
-                v[0] = it.b;
-                v[1] = it.hk;
-                v[2] = it.k0;
-                v[3] = it.t0;
-                v[4] = it.t1;
-                v[5] = it.begin;
-                v[6] = it.end;
-                v[7] = it.split;
-                mbar_arrive(item_pub(box));
-            }
-            ++n_pub;
-            if (item < 0) break;
-            if (lane == 0) {
-                if (it.begin < it.end) {
-                    ok = w.wait(kv_empty, (n_item & 1u) ^ 1u, kDevErrProducerEmpty);
-                    if (ok && !drop) {
-                        mbar_arrive_expect_tx(kv_full, 2 * Cfg::TILE_BYTES);
+    if (warp < 4) {
+        reg_dec<kBwdControlRegs>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ items + TMA producer
+            const uint64_t pol = l2_policy_evict_last();     // Q and dO are read by every key tile
+            const int n_kt = (mk.Skv + kTile - 1) / kTile;
+            uint32_t n_pub = 0, n_item = 0, n_clc = 0, n = 0;   // items published, items with steps, answers, steps
+            uint32_t armed = 0, parity = 0;                  // per barrier q_full 0-2, o_full 3-4, kv_full 5
+            bool drop = (p.test_flags & kTestDropFirstLoad) && blockIdx.x == 0;
+            bool asked = false;
+            int item = blockIdx.x;
+            auto arm = [&](int i, uint32_t ph) {
+                armed |= 1u << i;
+                parity = (parity & ~(1u << i)) | (ph & 1u) << i;
+            };
+            while (true) {
+                Item it{-1, 0, 0, 0, 0, 0, 0, 0};
+                if (item >= 0) {
+                    // key tiles from the first (under a causal mask the most queries see it) to the last,
+                    // in groups of key/value heads whose Q and dO stay in L2 together
+                    const int per_group = p.kv_head_group * n_kt * p.splits, grp = item / per_group, r_in = item - grp * per_group;
+                    const int gsz = min(mk.B * mk.Hkv - grp * p.kv_head_group, p.kv_head_group);
+                    const int bh = grp * p.kv_head_group + r_in % gsz;
+                    it.b = bh / mk.Hkv;
+                    it.hk = bh - it.b * mk.Hkv;
+                    it.split = r_in / gsz % p.splits;
+                    it.k0 = r_in / gsz / p.splits * kTile;
+                    // lane 0: the queries that see the tile's first key, lane 1: its last
+                    int first = 0, end = 0;
+                    if (lane < 2) key_interval(mk, it.b, lane == 0 ? it.k0 : min(it.k0 + kTile, mk.Skv) - 1, first, end);
+                    end = __shfl_sync(0xffffffffu, end, 1);
+                    first = __shfl_sync(0xffffffffu, first, 0);
+                    it.t0 = first / kTile;
+                    it.t1 = first < end ? (end + kTile - 1) / kTile : it.t0;
+                    const long long steps = (long long)(it.t1 - it.t0) * mk.group;
+                    it.begin = (int)(steps * it.split / p.splits);
+                    it.end = (int)(steps * (it.split + 1) / p.splits);
+                }
+                const uint32_t box = n_pub & 1u;
+                bool ok = lane != 0 || w.wait(item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                if (lane == 0) {
+                    volatile int* v = item_box + 8 * box;
+                    v[0] = it.b;
+                    v[1] = it.hk;
+                    v[2] = it.k0;
+                    v[3] = it.t0;
+                    v[4] = it.t1;
+                    v[5] = it.begin;
+                    v[6] = it.end;
+                    v[7] = it.split;
+                    mbar_arrive(item_pub(box));
+                }
+                ++n_pub;
+                if (item < 0) break;
+                if (lane == 0) {
+                    if (it.begin < it.end) {
+                        ok = w.wait(kv_empty, (n_item & 1u) ^ 1u, kDevErrProducerEmpty);
+                        if (ok && !drop) {
+                            mbar_arrive_expect_tx(kv_full, 2 * Cfg::TILE_BYTES);
 #pragma unroll
-                        for (int c = 0; c < DCH; ++c) {
-                            tma_load_4d(sb + Cfg::OFF_K + c * kChunkBytes, &tmK, kv_full, c * 64, it.k0, it.hk, it.b, pol);
-                            tma_load_4d(sb + Cfg::OFF_V + c * kChunkBytes, &tmV, kv_full, c * 64, it.k0, it.hk, it.b, pol);
+                            for (int c = 0; c < DCH; ++c) {
+                                tma_load_4d(sb + Cfg::OFF_K + c * kChunkBytes, &tmK, kv_full, c * 64, it.k0, it.hk, it.b, pol);
+                                tma_load_4d(sb + Cfg::OFF_V + c * kChunkBytes, &tmV, kv_full, c * 64, it.k0, it.hk, it.b, pol);
+                            }
+                            arm(5, n_item);
                         }
-                        arm(5, n_item);
+                        drop = false;                        // test hook: the first K and V are never loaded
+                        ++n_item;
+                        const int tiles = it.t1 - it.t0;
+                        for (int k = it.begin; ok && k < it.end; ++k, ++n) {
+                            const int h = it.hk * mk.group + k / tiles, t = it.t0 + k % tiles;
+                            const long long row0 = ((long long)it.b * mk.Hq + h) * p.Sp;
+                            const int sq = (int)(n % NQ), so = (int)(n % NO);
+                            const uint32_t ph_q = n / NQ, ph_o = n / NO;
+                            if (!(ok = w.wait(q_empty(sq), (ph_q & 1u) ^ 1u, kDevErrProducerEmpty))) break;
+                            mbar_arrive_expect_tx(q_full(sq), Cfg::TILE_BYTES);
+#pragma unroll
+                            for (int c = 0; c < DCH; ++c)
+                                tma_load_4d(sb + Cfg::OFF_Q + sq * Cfg::TILE_BYTES + c * kChunkBytes, &tmQ, q_full(sq), c * 64,
+                                            t * kTile, h, it.b, pol);
+                            arm(sq, ph_q);
+                            if (!(ok = w.wait(o_empty(so), (ph_o & 1u) ^ 1u, kDevErrProducerEmpty) &&
+                                       w.wait(rows_empty(so), (ph_o & 1u) ^ 1u, kDevErrProducerEmpty)))
+                                break;
+                            mbar_arrive_expect_tx(o_full(so), Cfg::TILE_BYTES + 1024);
+#pragma unroll
+                            for (int c = 0; c < DCH; ++c)
+                                tma_load_4d(sb + Cfg::OFF_O + so * Cfg::TILE_BYTES + c * kChunkBytes, &tmO, o_full(so), c * 64,
+                                            t * kTile, h, it.b, pol);
+                            bulk_load(sb + Cfg::OFF_ROWS + so * 1024, p.offset + row0 + t * kTile, 512, o_full(so));
+                            bulk_load(sb + Cfg::OFF_ROWS + so * 1024 + 512, p.neg_delta + row0 + t * kTile, 512, o_full(so));
+                            arm(3 + so, ph_o);
+                        }
                     }
-                    drop = false;                        // test hook: the first K and V are never loaded
+                    // the next item, asked for once this one's copies are issued: earlier, a CTA busy with a
+                    // long item would hold one that another could start
+                    if (ok) {
+                        fence_proxy_async_smem();            // the last answer has been read
+                        mbar_arrive_expect_tx(clc, 16);
+                        clc_try_cancel(sb + Cfg::OFF_CLC, clc);
+                        asked = true;
+                        if ((ok = w.wait(clc, n_clc & 1u, kDevErrProducerEmpty))) {
+                            asked = false;
+                            item = clc_taken(sb + Cfg::OFF_CLC);
+                        }
+                    }
+                }
+                ++n_clc;
+                if (!__all_sync(0xffffffffu, ok)) break;
+                item = __shfl_sync(0xffffffffu, item, 0);
+            }
+            if (lane == 0) {   // every copy and answer under way must land before the CTA may exit
+                if (asked) w.drain(clc, (n_clc - 1) & 1u);
+                for (int i = 0; i < 6; ++i)
+                    if (armed & (1u << i)) w.drain(i < 3 ? q_full(i) : (i < 5 ? o_full(i - 3) : kv_full), (parity >> i) & 1u);
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issuer
+            if (lane == 0) {
+                uint32_t n_box = 0, n_item = 0, n = 0;
+                bool ok = true;
+                const uint32_t k_s = sb + Cfg::OFF_K, v_s = sb + Cfg::OFF_V;
+                while (ok) {
+                    const uint32_t box = n_box & 1u;
+                    if (!w.wait(item_pub(box), (n_box >> 1) & 1u, kDevErrMmaFull)) break;
+                    const Item it = read_item(box);
+                    mbar_arrive(item_read(box));
+                    ++n_box;
+                    if (it.b < 0) break;
+                    const int steps = it.end - it.begin;
+                    if (steps <= 0) continue;
+                    if (!w.wait(kv_full, n_item & 1u, kDevErrMmaFull)) break;
                     ++n_item;
-                    const int tiles = it.t1 - it.t0;
-                    for (int k = it.begin; ok && k < it.end; ++k, ++n) {
-                        const int h = it.hk * mk.group + k / tiles, t = it.t0 + k % tiles;
-                        const long long row0 = ((long long)it.b * mk.Hq + h) * p.Sp;
+                    // dK += dS^T(m) Q(m), once dS^T(m) is written; the step's Q and row values are then free
+                    auto issue_dk = [&](uint32_t m, bool first) {
+                        if (!w.wait(ds_full, m & 1u, kDevErrMmaFull)) return false;
+                        tcgen05_fence_after();
+                        mma_overlay(tmem_base + Cfg::T_DK, tmem_base + Cfg::T_DP, sb + Cfg::OFF_Q + (m % NQ) * Cfg::TILE_BYTES,
+                                    Cfg::IDESC_ACC, !first);
+                        mma_commit(q_empty((int)(m % NQ)));
+                        mma_commit(rows_empty((int)(m % NO)));
+                        return true;
+                    };
+                    for (int i = 0; i < steps; ++i, ++n) {
                         const int sq = (int)(n % NQ), so = (int)(n % NO);
-                        const uint32_t ph_q = n / NQ, ph_o = n / NO;
-                        if (!(ok = w.wait(q_empty(sq), (ph_q & 1u) ^ 1u, kDevErrProducerEmpty))) break;
-                        mbar_arrive_expect_tx(q_full(sq), Cfg::TILE_BYTES);
-#pragma unroll
-                        for (int c = 0; c < DCH; ++c)
-                            tma_load_4d(sb + Cfg::OFF_Q + sq * Cfg::TILE_BYTES + c * kChunkBytes, &tmQ, q_full(sq), c * 64,
-                                        t * kTile, h, it.b, pol);
-                        arm(sq, ph_q);
-                        if (!(ok = w.wait(o_empty(so), (ph_o & 1u) ^ 1u, kDevErrProducerEmpty) &&
-                                   w.wait(rows_empty(so), (ph_o & 1u) ^ 1u, kDevErrProducerEmpty)))
-                            break;
-                        mbar_arrive_expect_tx(o_full(so), Cfg::TILE_BYTES + 1024);
-#pragma unroll
-                        for (int c = 0; c < DCH; ++c)
-                            tma_load_4d(sb + Cfg::OFF_O + so * Cfg::TILE_BYTES + c * kChunkBytes, &tmO, o_full(so), c * 64,
-                                        t * kTile, h, it.b, pol);
-                        bulk_load(sb + Cfg::OFF_ROWS + so * 1024, p.offset + row0 + t * kTile, 512, o_full(so));
-                        bulk_load(sb + Cfg::OFF_ROWS + so * 1024 + 512, p.neg_delta + row0 + t * kTile, 512, o_full(so));
-                        arm(3 + so, ph_o);
+                        if (!(ok = w.wait(q_full(sq), (n / NQ) & 1u, kDevErrMmaFull))) break;
+                        tcgen05_fence_after();
+                        mma_tiles<D>(tmem_base + Cfg::T_S, k_s, sb + Cfg::OFF_Q + sq * Cfg::TILE_BYTES, Cfg::IDESC_S);
+                        mma_commit(s_full);
+                        if (i > 0 && !(ok = issue_dk(n - 1, i == 1))) break;
+                        if (!(ok = w.wait(o_full(so), (n / NO) & 1u, kDevErrMmaFull))) break;
+                        tcgen05_fence_after();
+                        const uint32_t o_s = sb + Cfg::OFF_O + so * Cfg::TILE_BYTES;
+                        mma_tiles<D>(tmem_base + Cfg::T_DP, v_s, o_s, Cfg::IDESC_S);
+                        mma_commit(dp_full);
+                        if (!(ok = w.wait(p_full, n & 1u, kDevErrMmaFull))) break;
+                        tcgen05_fence_after();
+                        mma_overlay(tmem_base + Cfg::T_DV, tmem_base + Cfg::T_S, o_s, Cfg::IDESC_ACC, i > 0);
+                        mma_commit(o_empty(so));
                     }
+                    if (!ok || !(ok = issue_dk(n - 1, steps == 1))) break;
+                    mma_commit(kv_empty);
+                    mma_commit(done);
                 }
-                // the next item, asked for once this one's copies are issued: earlier, a CTA busy with a
-                // long item would hold one that another could start
-                if (ok) {
-                    fence_proxy_async_smem();            // the last answer has been read
-                    mbar_arrive_expect_tx(clc, 16);
-                    clc_try_cancel(sb + Cfg::OFF_CLC, clc);
-                    asked = true;
-                    if ((ok = w.wait(clc, n_clc & 1u, kDevErrProducerEmpty))) {
-                        asked = false;
-                        item = clc_taken(sb + Cfg::OFF_CLC);
-                    }
-                }
+                mma_commit(drain);
+                w.drain(drain, 0);
             }
-            ++n_clc;
-            if (!__all_sync(0xffffffffu, ok)) break;
-            item = __shfl_sync(0xffffffffu, item, 0);
+            __syncwarp();
         }
-        if (lane == 0) {   // every copy and answer under way must land before the CTA may exit
-            if (asked) w.drain(clc, (n_clc - 1) & 1u);
-            for (int i = 0; i < 6; ++i)
-                if (armed & (1u << i)) w.drain(i < 3 ? q_full(i) : (i < 5 ? o_full(i - 3) : kv_full), (parity >> i) & 1u);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            uint32_t n_box = 0, n_item = 0, n = 0;
-            bool ok = true;
-            const uint32_t k_s = sb + Cfg::OFF_K, v_s = sb + Cfg::OFF_V;
-            while (ok) {
-                const uint32_t box = n_box & 1u;
-                if (!w.wait(item_pub(box), (n_box >> 1) & 1u, kDevErrMmaFull)) break;
-                const Item it = read_item(box);
-                mbar_arrive(item_read(box));
-                ++n_box;
-                if (it.b < 0) break;
-                const int steps = it.end - it.begin;
-                if (steps <= 0) continue;
-                if (!w.wait(kv_full, n_item & 1u, kDevErrMmaFull)) break;
-                ++n_item;
-                // dK += dS^T(m) Q(m), once dS^T(m) is written; the step's Q and row values are then free
-                auto issue_dk = [&](uint32_t m, bool first) {
-                    if (!w.wait(ds_full, m & 1u, kDevErrMmaFull)) return false;
-                    tcgen05_fence_after();
-                    mma_overlay(tmem_base + Cfg::T_DK, tmem_base + Cfg::T_DP, sb + Cfg::OFF_Q + (m % NQ) * Cfg::TILE_BYTES,
-                                Cfg::IDESC_ACC, !first);
-                    mma_commit(q_empty((int)(m % NQ)));
-                    mma_commit(rows_empty((int)(m % NO)));
-                    return true;
-                };
-                for (int i = 0; i < steps; ++i, ++n) {
-                    const int sq = (int)(n % NQ), so = (int)(n % NO);
-                    if (!(ok = w.wait(q_full(sq), (n / NQ) & 1u, kDevErrMmaFull))) break;
-                    tcgen05_fence_after();
-                    mma_tiles<D>(tmem_base + Cfg::T_S, k_s, sb + Cfg::OFF_Q + sq * Cfg::TILE_BYTES, Cfg::IDESC_S);
-                    mma_commit(s_full);
-                    if (i > 0 && !(ok = issue_dk(n - 1, i == 1))) break;
-                    if (!(ok = w.wait(o_full(so), (n / NO) & 1u, kDevErrMmaFull))) break;
-                    tcgen05_fence_after();
-                    const uint32_t o_s = sb + Cfg::OFF_O + so * Cfg::TILE_BYTES;
-                    mma_tiles<D>(tmem_base + Cfg::T_DP, v_s, o_s, Cfg::IDESC_S);
-                    mma_commit(dp_full);
-                    if (!(ok = w.wait(p_full, n & 1u, kDevErrMmaFull))) break;
-                    tcgen05_fence_after();
-                    mma_overlay(tmem_base + Cfg::T_DV, tmem_base + Cfg::T_S, o_s, Cfg::IDESC_ACC, i > 0);
-                    mma_commit(o_empty(so));
-                }
-                if (!ok || !(ok = issue_dk(n - 1, steps == 1))) break;
-                mma_commit(kv_empty);
-                mma_commit(done);
-            }
-            mma_commit(drain);
-            w.drain(drain, 0);
-        }
-        __syncwarp();
     } else {
-        // ------------------------------------------------------------ P, dS and the output (warps 2-9)
-        const int half = (warp - 2) >> 2;                // query columns 64 half .. + 63
+        reg_inc<kBwdMathRegs>();
+        // ------------------------------------------------------------ P, dS and the output (warps 4-11)
+        const int half = (warp - 4) >> 2;                // query columns 64 half .. + 63
         const int quad = warp & 3;
         const int r = quad * 32 + lane;                  // key of the tile
         const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
@@ -730,10 +748,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     break;
                 }
                 tcgen05_fence_after();
-                auto ds_chunk = [&](const uint32_t (&ww)[32], int c) {
-                    uint32_t dp[32], packed[16];
-                    tmem_ld_32x32b_x32(dp_col + c * 32, dp);
-                    tmem_ld_wait(dp);
+                uint32_t dp0[32], dp1[32];
+                tmem_ld_32x32b_x32(dp_col, dp0);
+                tmem_ld_32x32b_x32(dp_col + 32, dp1);
+                tmem_ld_wait(dp0);
+                reg_tie(dp1);
+                auto ds_chunk = [&](const uint32_t (&ww)[32], const uint32_t (&dp)[32], int c) {
+                    uint32_t packed[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         const float2 nd = *reinterpret_cast<const float2*>(rows + 128 + c * 32 + i);
@@ -747,11 +768,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         for (int i = 0; i < 32; ++i)
                             if (c * 32 + i < first - i0 || c * 32 + i >= end - i0) packed[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
                     }
-                    // columns 0-15 of this half hold dP values of chunk 0 only: read above
                     tmem_st_32x32b_x16(dp_col + c * 16, packed);
                 };
-                ds_chunk(w0, 0);
-                ds_chunk(w1, 1);
+                ds_chunk(w0, dp0, 0);
+                ds_chunk(w1, dp1, 1);
                 tmem_st_wait();
                 tcgen05_fence_before();
                 __syncwarp();
@@ -914,145 +934,149 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t tmem_base = *tmem_slot;
     const Waiter w{p.err, p.timeout_ns, abort_flag, kDevErrKernelMaskedDq};
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ items + TMA producer
-        if (lane == 0) {
-            const uint64_t pol = l2_policy_evict_last();
-            const int n_qb = (mk.Sq + kTile - 1) / kTile;
-            uint32_t n_pub = 0, n_item = 0, n_clc = 0, n = 0;
-            uint32_t armed = 0, parity = 0;              // k_full 0-2, v_full 3-4, q_full 5
-            bool drop = (p.test_flags & kTestDropFirstLoad) && blockIdx.x == 0;
-            bool asked = false, ok = true;
-            int item = blockIdx.x;
-            auto arm = [&](int i, uint32_t ph) {
-                armed |= 1u << i;
-                parity = (parity & ~(1u << i)) | (ph & 1u) << i;
-            };
-            while (ok) {
-                Item it{-1, 0, 0, 0, 0};
-                if (item >= 0) {
-                    const int per_group = p.q_head_group * n_qb, grp = item / per_group, r_in = item - grp * per_group;
-                    const int gsz = min(mk.B * mk.Hq - grp * p.q_head_group, p.q_head_group);
-                    const int bh = grp * p.q_head_group + r_in % gsz;
-                    it.b = bh / mk.Hq;
-                    it.h = bh - it.b * mk.Hq;
-                    it.q_base = (n_qb - 1 - r_in / gsz) * kTile;
-                    int lo, hi, none;
-                    row_interval(mk, it.b, it.q_base, lo, none);
-                    row_interval(mk, it.b, min(it.q_base + kTile, mk.Sq) - 1, none, hi);
-                    it.t0 = lo / kTile;
-                    it.t1 = hi > lo ? (hi + kTile - 1) / kTile : it.t0;
-                }
-                const uint32_t box = n_pub & 1u;
-                if (!(ok = w.wait(item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty))) break;
-                volatile int* v = item_box + 8 * box;
-                v[0] = it.b;
-                v[1] = it.h;
-                v[2] = it.q_base;
-                v[3] = it.t0;
-                v[4] = it.t1;
-                mbar_arrive(item_pub(box));
-                ++n_pub;
-                if (item < 0) break;
-                if (it.t0 < it.t1) {
-                    if (!(ok = w.wait(q_empty, (n_item & 1u) ^ 1u, kDevErrProducerEmpty))) break;
-                    if (!drop) {
-                        mbar_arrive_expect_tx(q_full, 2 * Cfg::TILE_BYTES);
-#pragma unroll
-                        for (int c = 0; c < DCH; ++c) {
-                            tma_load_4d(sb + Cfg::OFF_Q + c * kChunkBytes, &tmQ, q_full, c * 64, it.q_base, it.h, it.b, pol);
-                            tma_load_4d(sb + Cfg::OFF_O + c * kChunkBytes, &tmO, q_full, c * 64, it.q_base, it.h, it.b, pol);
-                        }
-                        arm(5, n_item);
+    if (warp < 4) {
+        reg_dec<kBwdControlRegs>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ items + TMA producer
+            if (lane == 0) {
+                const uint64_t pol = l2_policy_evict_last();
+                const int n_qb = (mk.Sq + kTile - 1) / kTile;
+                uint32_t n_pub = 0, n_item = 0, n_clc = 0, n = 0;
+                uint32_t armed = 0, parity = 0;              // k_full 0-2, v_full 3-4, q_full 5
+                bool drop = (p.test_flags & kTestDropFirstLoad) && blockIdx.x == 0;
+                bool asked = false, ok = true;
+                int item = blockIdx.x;
+                auto arm = [&](int i, uint32_t ph) {
+                    armed |= 1u << i;
+                    parity = (parity & ~(1u << i)) | (ph & 1u) << i;
+                };
+                while (ok) {
+                    Item it{-1, 0, 0, 0, 0};
+                    if (item >= 0) {
+                        const int per_group = p.q_head_group * n_qb, grp = item / per_group, r_in = item - grp * per_group;
+                        const int gsz = min(mk.B * mk.Hq - grp * p.q_head_group, p.q_head_group);
+                        const int bh = grp * p.q_head_group + r_in % gsz;
+                        it.b = bh / mk.Hq;
+                        it.h = bh - it.b * mk.Hq;
+                        it.q_base = (n_qb - 1 - r_in / gsz) * kTile;
+                        int lo, hi, none;
+                        row_interval(mk, it.b, it.q_base, lo, none);
+                        row_interval(mk, it.b, min(it.q_base + kTile, mk.Sq) - 1, none, hi);
+                        it.t0 = lo / kTile;
+                        it.t1 = hi > lo ? (hi + kTile - 1) / kTile : it.t0;
                     }
-                    drop = false;                        // test hook: the first Q and dO are never loaded
+                    const uint32_t box = n_pub & 1u;
+                    if (!(ok = w.wait(item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty))) break;
+                    volatile int* v = item_box + 8 * box;
+                    v[0] = it.b;
+                    v[1] = it.h;
+                    v[2] = it.q_base;
+                    v[3] = it.t0;
+                    v[4] = it.t1;
+                    mbar_arrive(item_pub(box));
+                    ++n_pub;
+                    if (item < 0) break;
+                    if (it.t0 < it.t1) {
+                        if (!(ok = w.wait(q_empty, (n_item & 1u) ^ 1u, kDevErrProducerEmpty))) break;
+                        if (!drop) {
+                            mbar_arrive_expect_tx(q_full, 2 * Cfg::TILE_BYTES);
+#pragma unroll
+                            for (int c = 0; c < DCH; ++c) {
+                                tma_load_4d(sb + Cfg::OFF_Q + c * kChunkBytes, &tmQ, q_full, c * 64, it.q_base, it.h, it.b, pol);
+                                tma_load_4d(sb + Cfg::OFF_O + c * kChunkBytes, &tmO, q_full, c * 64, it.q_base, it.h, it.b, pol);
+                            }
+                            arm(5, n_item);
+                        }
+                        drop = false;                        // test hook: the first Q and dO are never loaded
+                        ++n_item;
+                        const int hk = it.h / mk.group;
+                        for (int t = it.t0; t < it.t1; ++t, ++n) {
+                            const int sk = (int)(n % NK), sv = (int)(n % NV);
+                            if (!(ok = w.wait(k_empty(sk), ((n / NK) & 1u) ^ 1u, kDevErrProducerEmpty))) break;
+                            mbar_arrive_expect_tx(k_full(sk), Cfg::TILE_BYTES);
+#pragma unroll
+                            for (int c = 0; c < DCH; ++c)
+                                tma_load_4d(sb + Cfg::OFF_K + sk * Cfg::TILE_BYTES + c * kChunkBytes, &tmK, k_full(sk), c * 64, t * kTile,
+                                            hk, it.b, pol);
+                            arm(sk, n / NK);
+                            if (!(ok = w.wait(v_empty(sv), ((n / NV) & 1u) ^ 1u, kDevErrProducerEmpty))) break;
+                            mbar_arrive_expect_tx(v_full(sv), Cfg::TILE_BYTES);
+#pragma unroll
+                            for (int c = 0; c < DCH; ++c)
+                                tma_load_4d(sb + Cfg::OFF_V + sv * Cfg::TILE_BYTES + c * kChunkBytes, &tmV, v_full(sv), c * 64, t * kTile,
+                                            hk, it.b, pol);
+                            arm(3 + sv, n / NV);
+                        }
+                        if (!ok) break;
+                    }
+                    fence_proxy_async_smem();                // the last answer has been read
+                    mbar_arrive_expect_tx(clc, 16);
+                    clc_try_cancel(sb + Cfg::OFF_CLC, clc);
+                    asked = true;
+                    ++n_clc;
+                    if (!(ok = w.wait(clc, (n_clc - 1) & 1u, kDevErrProducerEmpty))) break;
+                    asked = false;
+                    item = clc_taken(sb + Cfg::OFF_CLC);
+                }
+                if (asked) w.drain(clc, (n_clc - 1) & 1u);
+                for (int i = 0; i < 6; ++i)
+                    if (armed & (1u << i)) w.drain(i < 3 ? k_full(i) : (i < 5 ? v_full(i - 3) : q_full), (parity >> i) & 1u);
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issuer
+            if (lane == 0) {
+                uint32_t n_box = 0, n_item = 0, n = 0;
+                bool ok = true;
+                const uint32_t q_s = sb + Cfg::OFF_Q, o_s = sb + Cfg::OFF_O;
+                // S(m) and dP(m), once their operands have landed and S(m-1) is in registers
+                auto issue_scores = [&](uint32_t m, bool first) {
+                    if (!w.wait(k_full((int)(m % NK)), (m / NK) & 1u, kDevErrMmaFull)) return false;
+                    if (!first && !w.wait(s_read, (m - 1) & 1u, kDevErrMmaFull)) return false;
+                    tcgen05_fence_after();
+                    mma_tiles<D>(tmem_base + Cfg::T_S, q_s, sb + Cfg::OFF_K + (m % NK) * Cfg::TILE_BYTES, Cfg::IDESC_S);
+                    mma_commit(s_full);
+                    if (!w.wait(v_full((int)(m % NV)), (m / NV) & 1u, kDevErrMmaFull)) return false;
+                    tcgen05_fence_after();
+                    mma_tiles<D>(tmem_base + Cfg::T_DP + (m & 1u) * 128, o_s, sb + Cfg::OFF_V + (m % NV) * Cfg::TILE_BYTES, Cfg::IDESC_S);
+                    mma_commit(dp_full((int)(m & 1u)));
+                    mma_commit(v_empty((int)(m % NV)));
+                    return true;
+                };
+                while (ok) {
+                    const uint32_t box = n_box & 1u;
+                    if (!w.wait(item_pub(box), (n_box >> 1) & 1u, kDevErrMmaFull)) break;
+                    const Item it = read_item(box);
+                    mbar_arrive(item_read(box));
+                    ++n_box;
+                    if (it.b < 0) break;
+                    const int steps = it.t1 - it.t0;
+                    if (steps <= 0) continue;
+                    if (!w.wait(q_full, n_item & 1u, kDevErrMmaFull)) break;
                     ++n_item;
-                    const int hk = it.h / mk.group;
-                    for (int t = it.t0; t < it.t1; ++t, ++n) {
-                        const int sk = (int)(n % NK), sv = (int)(n % NV);
-                        if (!(ok = w.wait(k_empty(sk), ((n / NK) & 1u) ^ 1u, kDevErrProducerEmpty))) break;
-                        mbar_arrive_expect_tx(k_full(sk), Cfg::TILE_BYTES);
-#pragma unroll
-                        for (int c = 0; c < DCH; ++c)
-                            tma_load_4d(sb + Cfg::OFF_K + sk * Cfg::TILE_BYTES + c * kChunkBytes, &tmK, k_full(sk), c * 64, t * kTile,
-                                        hk, it.b, pol);
-                        arm(sk, n / NK);
-                        if (!(ok = w.wait(v_empty(sv), ((n / NV) & 1u) ^ 1u, kDevErrProducerEmpty))) break;
-                        mbar_arrive_expect_tx(v_full(sv), Cfg::TILE_BYTES);
-#pragma unroll
-                        for (int c = 0; c < DCH; ++c)
-                            tma_load_4d(sb + Cfg::OFF_V + sv * Cfg::TILE_BYTES + c * kChunkBytes, &tmV, v_full(sv), c * 64, t * kTile,
-                                        hk, it.b, pol);
-                        arm(3 + sv, n / NV);
+                    // the step before an item's first has been read too: its dS was waited for
+                    if (!(ok = issue_scores(n, n == 0))) break;
+                    for (int i = 0; i < steps; ++i, ++n) {
+                        if (i + 1 < steps && !(ok = issue_scores(n + 1, false))) break;
+                        if (!(ok = w.wait(ds_full, n & 1u, kDevErrMmaFull))) break;
+                        tcgen05_fence_after();
+                        mma_overlay(tmem_base + Cfg::T_DQ, tmem_base + Cfg::T_DP + (n & 1u) * 128,
+                                    sb + Cfg::OFF_K + (n % NK) * Cfg::TILE_BYTES, Cfg::IDESC_ACC, i > 0);
+                        mma_commit(k_empty((int)(n % NK)));
                     }
                     if (!ok) break;
+                    mma_commit(q_empty);
+                    mma_commit(done);
                 }
-                fence_proxy_async_smem();                // the last answer has been read
-                mbar_arrive_expect_tx(clc, 16);
-                clc_try_cancel(sb + Cfg::OFF_CLC, clc);
-                asked = true;
-                ++n_clc;
-                if (!(ok = w.wait(clc, (n_clc - 1) & 1u, kDevErrProducerEmpty))) break;
-                asked = false;
-                item = clc_taken(sb + Cfg::OFF_CLC);
+                mma_commit(drain);
+                w.drain(drain, 0);
             }
-            if (asked) w.drain(clc, (n_clc - 1) & 1u);
-            for (int i = 0; i < 6; ++i)
-                if (armed & (1u << i)) w.drain(i < 3 ? k_full(i) : (i < 5 ? v_full(i - 3) : q_full), (parity >> i) & 1u);
+            __syncwarp();
         }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            uint32_t n_box = 0, n_item = 0, n = 0;
-            bool ok = true;
-            const uint32_t q_s = sb + Cfg::OFF_Q, o_s = sb + Cfg::OFF_O;
-            // S(m) and dP(m), once their operands have landed and S(m-1) is in registers
-            auto issue_scores = [&](uint32_t m, bool first) {
-                if (!w.wait(k_full((int)(m % NK)), (m / NK) & 1u, kDevErrMmaFull)) return false;
-                if (!first && !w.wait(s_read, (m - 1) & 1u, kDevErrMmaFull)) return false;
-                tcgen05_fence_after();
-                mma_tiles<D>(tmem_base + Cfg::T_S, q_s, sb + Cfg::OFF_K + (m % NK) * Cfg::TILE_BYTES, Cfg::IDESC_S);
-                mma_commit(s_full);
-                if (!w.wait(v_full((int)(m % NV)), (m / NV) & 1u, kDevErrMmaFull)) return false;
-                tcgen05_fence_after();
-                mma_tiles<D>(tmem_base + Cfg::T_DP + (m & 1u) * 128, o_s, sb + Cfg::OFF_V + (m % NV) * Cfg::TILE_BYTES, Cfg::IDESC_S);
-                mma_commit(dp_full((int)(m & 1u)));
-                mma_commit(v_empty((int)(m % NV)));
-                return true;
-            };
-            while (ok) {
-                const uint32_t box = n_box & 1u;
-                if (!w.wait(item_pub(box), (n_box >> 1) & 1u, kDevErrMmaFull)) break;
-                const Item it = read_item(box);
-                mbar_arrive(item_read(box));
-                ++n_box;
-                if (it.b < 0) break;
-                const int steps = it.t1 - it.t0;
-                if (steps <= 0) continue;
-                if (!w.wait(q_full, n_item & 1u, kDevErrMmaFull)) break;
-                ++n_item;
-                // the step before an item's first has been read too: its dS was waited for
-                if (!(ok = issue_scores(n, n == 0))) break;
-                for (int i = 0; i < steps; ++i, ++n) {
-                    if (i + 1 < steps && !(ok = issue_scores(n + 1, false))) break;
-                    if (!(ok = w.wait(ds_full, n & 1u, kDevErrMmaFull))) break;
-                    tcgen05_fence_after();
-                    mma_overlay(tmem_base + Cfg::T_DQ, tmem_base + Cfg::T_DP + (n & 1u) * 128,
-                                sb + Cfg::OFF_K + (n % NK) * Cfg::TILE_BYTES, Cfg::IDESC_ACC, i > 0);
-                    mma_commit(k_empty((int)(n % NK)));
-                }
-                if (!ok) break;
-                mma_commit(q_empty);
-                mma_commit(done);
-            }
-            mma_commit(drain);
-            w.drain(drain, 0);
-        }
-        __syncwarp();
     } else {
-        // ------------------------------------------------------------ dS and the output (warps 2-9)
-        const int half = (warp - 2) >> 2;                // key columns 64 half .. + 63
+        reg_inc<kBwdMathRegs>();
+        // ------------------------------------------------------------ dS and the output (warps 4-11)
+        const int half = (warp - 4) >> 2;                // key columns 64 half .. + 63
         const int quad = warp & 3;
         const int r = quad * 32 + lane;                  // query of the tile
         const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
@@ -1101,10 +1125,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 }
                 tcgen05_fence_after();
                 const uint32_t dp_col = lane_base + Cfg::T_DP + buf * 128 + half * 64;
-                auto ds_chunk = [&](const uint32_t (&ww)[32], int c) {
-                    uint32_t dp[32], packed[16];
-                    tmem_ld_32x32b_x32(dp_col + c * 32, dp);
-                    tmem_ld_wait(dp);
+                uint32_t dp0[32], dp1[32];
+                tmem_ld_32x32b_x32(dp_col, dp0);
+                tmem_ld_32x32b_x32(dp_col + 32, dp1);
+                tmem_ld_wait(dp0);
+                reg_tie(dp1);
+                auto ds_chunk = [&](const uint32_t (&ww)[32], const uint32_t (&dp)[32], int c) {
+                    uint32_t packed[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         float d0 = __uint_as_float(dp[i]), d1 = __uint_as_float(dp[i + 1]);
@@ -1118,8 +1145,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     }
                     tmem_st_32x32b_x16(dp_col + c * 16, packed);
                 };
-                ds_chunk(w0, 0);
-                ds_chunk(w1, 1);
+                ds_chunk(w0, dp0, 0);
+                ds_chunk(w1, dp1, 1);
                 tmem_st_wait();
                 tcgen05_fence_before();
                 __syncwarp();
@@ -1169,7 +1196,8 @@ cudaError_t launch_dkv(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaSt
     gsr_masked_dkv_kernel<Cfg><<<(unsigned)items, kBwdThreads, Cfg::SMEM_BYTES, stream>>>(tm.q, tm.k, tm.v, tm.dO, p);
     if (p.splits > 1) {
         const long long rows = 2ll * p.mask.B * p.mask.Hkv * p.mask.Skv;
-        gsr_masked_dkv_sum_kernel<typename Cfg::T, Cfg::D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p);
+        gsr_masked_dkv_sum_kernel<typename Cfg::T, Cfg::D>
+            <<<(unsigned)((rows + 8 * kSumRows - 1) / (8 * kSumRows)), 256, 0, stream>>>(p);
     }
     return cudaGetLastError();
 }

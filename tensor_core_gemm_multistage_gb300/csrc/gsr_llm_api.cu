@@ -149,6 +149,34 @@ int heads_in_l2(int causal, int64_t bytes, int64_t group, int64_t heads) {
     return (int)(n < heads ? n : heads);
 }
 
+// Parts that a key tile's steps are cut into: items that the SMs cannot share out evenly cost up to an
+// item's time at the end, parts cost a write and a read of dK and dV in fp32.  Causal and document
+// masks leave items of unequal length: parts until there are four items an SM.  Without them items
+// are equal and what counts is how full the last wave is: parts where they save a tenth.  At most
+// four parts of four steps or more.  16 heads over 4, 8192 tokens, bf16: 4 documents 709 us whole,
+// 607 in three parts; causal 1018 and 902; without a mask 1620 whole (1.7 waves of items) and 1707 in
+// three parts (5.05).
+int64_t bwd_splits(const gsr_attention_desc* d) {
+    if (d->batch == 0 || d->heads_kv == 0 || d->seq_kv == 0) return 1;
+    const int64_t items = d->batch * d->heads_kv * ((d->seq_kv + 127) / 128);
+    const int64_t steps = d->heads_q / d->heads_kv * ((d->seq_q + 127) / 128);
+    const int64_t most = steps / 4 < 4 ? steps / 4 : 4;
+    int64_t best = 1;
+    if (d->causal || d->num_docs > 0) {
+        while (best < most && items * best < 4 * kSms) ++best;
+    } else {
+        double least = (double)((items + kSms - 1) / kSms);
+        for (int64_t n = 2; n <= most; ++n) {
+            const double waves = (double)((items * n + kSms - 1) / kSms) / (double)n;
+            if (waves < 0.9 * least) {
+                least = waves;
+                best = n;
+            }
+        }
+    }
+    return best;
+}
+
 // Layout of the backward pass's workspace, 256-byte pieces.
 struct BwdLayout {
     int64_t sp, splits, offset, delta, parts, total;
@@ -160,15 +188,7 @@ BwdLayout bwd_layout(const gsr_attention_desc* d) {
     w.offset = 256;                                                     // the norms come first
     w.delta = w.offset + piece(4 * d->batch * d->heads_q * w.sp);
     w.parts = w.delta + piece(4 * d->batch * d->heads_q * w.sp);
-    // A key tile's steps are cut into parts until there are four items an SM, at most four parts
-    // (each costs a write and a read of dK and dV in fp32) of four steps or more.  8192 tokens in 4
-    // documents, 16 heads over 4 (256 items): 709 us whole, DKV_SPLIT_FIGURE.
-    const int64_t items = d->batch * d->heads_kv * ((d->seq_kv + 127) / 128);
-    const int64_t steps = d->heads_kv > 0 ? d->heads_q / d->heads_kv * (w.sp / 128) : 0;
-    int64_t n = items > 0 ? (4 * kSms + items - 1) / items : 1;
-    if (n > 4) n = 4;
-    if (n > steps / 4) n = steps / 4;
-    w.splits = n < 1 ? 1 : n;
+    w.splits = bwd_splits(d);
     w.total = w.parts + (w.splits > 1 ? piece(8 * w.splits * d->batch * d->heads_kv * d->seq_kv * d->head_dim) : 0);
     return w;
 }
