@@ -213,6 +213,24 @@ __device__ __forceinline__ void score_chunk(uint32_t (&rr)[32], const ScoreArgs&
     }
 }
 
+// A launch whose CTAs may start before the launch ahead of it on the stream has finished (they wait
+// for it themselves, grid_wait).
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, unsigned block, int smem, cudaStream_t stream,
+                         const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Largest and smallest of a row's 128 values, in four chains of three-input instructions.
 __device__ __forceinline__ float row_max(const uint32_t (&a)[32], const uint32_t (&b)[32], const uint32_t (&c)[32],
                                          const uint32_t (&d)[32]) {

@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(256) gsr_masked_dkv_sum_kernel(const __grid_co
     const MaskArgs& mk = p.mask;
     const int lane = threadIdx.x & 31;
     const long long rows = (long long)mk.B * mk.Hkv * mk.Skv, first = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kSumRows;
+    grid_wait();                                         // dQ has finished, and dK and dV before it
     V x[kSumRows][kMaxSplits];
 #pragma unroll
     for (int k = 0; k < kSumRows; ++k)
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(256) gsr_masked_dkv_sum_kernel(const __grid_co
             x[k][s] = V{};
             if (s < p.splits && id < 2 * rows) {         // dV's parts lie before dK's
                 const long long part = id < rows ? s : p.splits + s, row = id < rows ? id : id - rows;
-                x[k][s] = __ldg(reinterpret_cast<const V*>(p.parts + (part * rows + row) * D) + lane);
+                x[k][s] = *(reinterpret_cast<const V*>(p.parts + (part * rows + row) * D) + lane);
             }
         }
 #pragma unroll
@@ -491,6 +492,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish_alloc_permit();
     }
+    grid_wait();                                         // the rows' values
+    grid_launch_next();                                  // dQ needs no more than they
     tcgen05_fence_before();
     __syncthreads();
     tcgen05_fence_after();
@@ -1175,6 +1178,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
     }
 
+    grid_wait();                                         // whoever waits for dQ waits for dK and dV too
     tcgen05_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -1187,35 +1191,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
-template <class Cfg>
-cudaError_t launch_dkv(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream) {
-    static std::atomic<uint64_t> attr_done{0};
-    const cudaError_t e = allow_smem(gsr_masked_dkv_kernel<Cfg>, Cfg::SMEM_BYTES, attr_done);
-    if (e != cudaSuccess) return e;
-    const int items = (p.mask.Skv + kTile - 1) / kTile * p.mask.B * p.mask.Hkv * p.splits;
-    gsr_masked_dkv_kernel<Cfg><<<(unsigned)items, kBwdThreads, Cfg::SMEM_BYTES, stream>>>(tm.q, tm.k, tm.v, tm.dO, p);
-    if (p.splits > 1) {
-        const long long rows = 2ll * p.mask.B * p.mask.Hkv * p.mask.Skv;
-        gsr_masked_dkv_sum_kernel<typename Cfg::T, Cfg::D>
-            <<<(unsigned)((rows + 8 * kSumRows - 1) / (8 * kSumRows)), 256, 0, stream>>>(p);
-    }
-    return cudaGetLastError();
-}
-
-template <class Cfg>
-cudaError_t launch_dq(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream) {
-    static std::atomic<uint64_t> attr_done{0};
-    const cudaError_t e = allow_smem(gsr_masked_dq_kernel<Cfg>, Cfg::SMEM_BYTES, attr_done);
-    if (e != cudaSuccess) return e;
-    const int items = p.Sp / kTile * p.mask.B * p.mask.Hq;
-    gsr_masked_dq_kernel<Cfg><<<(unsigned)items, kBwdThreads, Cfg::SMEM_BYTES, stream>>>(tm.q, tm.k, tm.v, tm.dO, p);
-    return cudaGetLastError();
-}
-
+// The rows, then dK and dV, then dQ, then the sums of parts.  dK and dV start while the rows' last CTAs
+// finish and wait for them; dQ's CTAs need the rows alone (finished when dK's and dV's CTAs have come
+// past their wait, which is when dQ's may start) and fill the SMs that run out of dK and dV items.
 template <class T, int D, int MODE>
 cudaError_t launch_bwd_mode(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream) {
-    const cudaError_t e = launch_dkv<DkvCfg<T, D, MODE>>(tm, p, stream);
-    return e == cudaSuccess ? launch_dq<DqCfg<T, D, MODE>>(tm, p, stream) : e;
+    using Dkv = DkvCfg<T, D, MODE>;
+    using Dq = DqCfg<T, D, MODE>;
+    static std::atomic<uint64_t> dkv_done{0}, dq_done{0};
+    const int k_items = (p.mask.Skv + kTile - 1) / kTile * p.mask.B * p.mask.Hkv * p.splits;
+    const int q_items = p.Sp / kTile * p.mask.B * p.mask.Hq;
+    cudaError_t e;
+    if ((e = allow_smem(gsr_masked_dkv_kernel<Dkv>, Dkv::SMEM_BYTES, dkv_done)) != cudaSuccess ||
+        (e = allow_smem(gsr_masked_dq_kernel<Dq>, Dq::SMEM_BYTES, dq_done)) != cudaSuccess ||
+        (e = launch_early(gsr_masked_dkv_kernel<Dkv>, (unsigned)k_items, kBwdThreads, Dkv::SMEM_BYTES, stream, tm.q, tm.k, tm.v,
+                          tm.dO, p)) != cudaSuccess ||
+        (e = launch_early(gsr_masked_dq_kernel<Dq>, (unsigned)q_items, kBwdThreads, Dq::SMEM_BYTES, stream, tm.q, tm.k, tm.v,
+                          tm.dO, p)) != cudaSuccess)
+        return e;
+    if (p.splits > 1) {
+        const long long rows = 2ll * p.mask.B * p.mask.Hkv * p.mask.Skv;
+        return launch_early(gsr_masked_dkv_sum_kernel<T, D>, (unsigned)((rows + 8 * kSumRows - 1) / (8 * kSumRows)), 256, 0,
+                            stream, p);
+    }
+    return cudaSuccess;
 }
 
 template <class T, int D>

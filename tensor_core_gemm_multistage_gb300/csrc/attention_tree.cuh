@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
         if (threadIdx.x == 0) atomicCAS(p.err, 0, kDevErrKernelTree | kDevErrLayout);
         return;
     }
+    grid_launch_next();                                          // the joining CTAs, as SMs fall free
     const uint32_t sb = smem_u32(smem);
     auto bar = [&](int i) { return sb + Cfg::OFF_BAR + 8u * i; };
     auto full = [&](int s) { return bar(s); };
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(kJoinThreads) gsr_tree_join_kernel(const __gri
     if (t < 0 || t >= r.nodes) return;
     const int per_pass = p.tile_nodes * p.nq, pair = t / per_pass, in_pass = t - pair * per_pass;
     const int row = in_pass / p.tile_nodes * 128 + in_pass % p.tile_nodes * p.group + (h - hk * p.group);
-    asm volatile("griddepcontrol.wait;" ::: "memory");           // the parts' launch has finished
+    grid_wait();                                                 // the parts' launch has finished
     const long long U = p.unit_starts[p.B];
     const long long s = p.unit_starts[b] + ((long long)hk * r.q_pairs + pair) * r.key_tiles;
     if (U <= 0) return;
@@ -823,18 +824,9 @@ cudaError_t launch_tree_cfg(const TreeMaps& tm, const TreeParams& p, int grid, c
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // the joining CTAs start while the parts' last CTAs finish, and wait for them there
     const long long rows = (long long)p.total_q * p.Hq;
-    const bool many = rows >= 2048;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(many ? (rows + 3) / 4 : rows));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return many ? cudaLaunchKernelEx(&cfg, gsr_tree_join_kernel<typename Cfg::T, Cfg::D, 1>, p, grid)
-                : cudaLaunchKernelEx(&cfg, gsr_tree_join_kernel<typename Cfg::T, Cfg::D, 4>, p, grid);
+    return rows >= 2048
+               ? launch_early(gsr_tree_join_kernel<typename Cfg::T, Cfg::D, 1>, (unsigned)((rows + 3) / 4), kJoinThreads, 0, stream, p, grid)
+               : launch_early(gsr_tree_join_kernel<typename Cfg::T, Cfg::D, 4>, (unsigned)rows, kJoinThreads, 0, stream, p, grid);
 }
 
 template <class T, int D, int NQ>

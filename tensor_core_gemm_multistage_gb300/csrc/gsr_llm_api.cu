@@ -161,14 +161,14 @@ int heads_together(bool unequal, int64_t bytes, int64_t group, int64_t items_a_h
 // item's time at the end, parts cost a write and a read of dK and dV in fp32.  Causal and document
 // masks leave items of unequal length: parts until there are four items an SM.  Without them items
 // are equal and what counts is how full the last wave is: parts where they save a tenth.  At most
-// four parts of four steps or more.  16 heads over 4, 8192 tokens, bf16: 4 documents 709 us whole,
+// four parts of two steps or more.  16 heads over 4, 8192 tokens, bf16: 4 documents 709 us whole,
 // 607 in three parts; causal 1018 and 902; without a mask 1620 whole (1.7 waves of items), 1707 in
 // three parts (5.05 waves of thirds), 1554 in four (6.7 of quarters).
 int64_t bwd_splits(const gsr_attention_desc* d) {
     if (d->batch == 0 || d->heads_kv == 0 || d->seq_kv == 0) return 1;
     const int64_t items = d->batch * d->heads_kv * ((d->seq_kv + 127) / 128);
     const int64_t steps = d->heads_q / d->heads_kv * ((d->seq_q + 127) / 128);
-    const int64_t most = steps / 4 < 4 ? steps / 4 : 4;
+    const int64_t most = steps / 2 < 4 ? steps / 2 : 4;
     int64_t best = 1;
     if (d->causal || d->num_docs > 0) {
         while (best < most && items * best < 4 * kSms) ++best;

@@ -57,6 +57,11 @@ __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Programmatic dependent launch: waits until the launches this one depends on have finished and their
+// writes are visible; lets the next one's CTAs start once every CTA has come here (or ended).
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Instruction descriptor as idesc_f16_f32, for f16 (0) or bf16 (1) operands, both of one type.
 __host__ __device__ constexpr uint32_t idesc_16_f32(bool bf16, int M, int N, bool a_mn_major, bool b_mn_major) {
     return idesc_f16_f32(M, N, a_mn_major, b_mn_major) | (bf16 ? (1u << 7) | (1u << 10) : 0u);
