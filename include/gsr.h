@@ -239,7 +239,8 @@ gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor
  * node below the one before it).  T_b = 1 is an ordinary decoding step; T_b = 0 is fine.
  *
  *   k_cache, v_cache  num_pages pages of page_size rows (a multiple of 8; stride_batch steps from
- *                     page to page); row r of request b is row r % page_size of page
+ *                     page to page, and it or else stride_head is a multiple of 8 stride_row, as in
+ *                     every dense layout); row r of request b is row r % page_size of page
  *                     block_tables[b][r / page_size].  Entries outside [0, num_pages) hold no
  *                     tokens: nothing sees them.  Cache rows behind kv_lens[b] have no influence.
  *   block_tables      batch x table_width int32.  Lengths above table_width x page_size are cut.

@@ -24,7 +24,10 @@
 //    part (sum, maximum, O in fp32) in the workspace, at most two a CTA (its range's first and last
 //    item), and a second launch joins them in the order of the CTAs.
 //  * Pages arrive by TMA, one box per page (or piece of one), a ring of key and value tiles ahead of
-//    the tensor core; lane i of the producer warp looks up and copies piece i of the tile.
+//    the tensor core; lane i of the producer warp looks up and copies piece i of the tile.  A box
+//    costs the copy unit about 85 cycles whatever it holds, so at head_dim 128 it takes both 64-column
+//    chunks of its rows: a tile lies in shared memory as groups of 8 rows, each group's chunks side by
+//    side (one box a chunk: pages of 8 rows 321 us where HBM needs 170, of 16 rows 214).
 //  * Rows of the last tile behind kv_lens, and pieces whose page is not in the pool, are masked, and
 //    their V rows set to zero in shared memory before the product (0 times what a page holds there
 //    may be NaN).  A row that is not finite all the same (a hidden sibling's V) is computed again
@@ -123,8 +126,9 @@ struct TreeCfg {
     using T = T_;
     static constexpr int D = D_, MODE = MODE_, NQ = NQ_;
     static constexpr int DCH = D / 64;
-    static constexpr int CHUNK_BYTES = 128 * 128;
+    static constexpr int CHUNK_BYTES = 128 * 128;     // a query tile's 64 columns
     static constexpr int TILE_BYTES = 128 * D * 2;
+    static constexpr int GROUP_BYTES = 8 * D * 2;     // 8 rows of a key or value tile
     static constexpr int NB = D == 128 ? (NQ == 1 ? 6 : 5) : 12;   // ring of K and V tiles
     static constexpr int SM_THREADS = 256;            // two softmax groups of four warps
     static constexpr int NUM_THREADS = 128 + SM_THREADS;
@@ -261,10 +265,9 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
         tmem_relinquish_alloc_permit();
     }
     // rows behind the tile's last piece are never copied: zero for good
-    for (int i = threadIdx.x; i < NB * DCH * (128 - p.tile_keys) * 8; i += Cfg::NUM_THREADS) {
-        const int unit = i & 7, rest = i >> 3, row = p.tile_keys + rest % (128 - p.tile_keys), chunk = rest / (128 - p.tile_keys);
-        *reinterpret_cast<uint4*>(smem + Cfg::OFF_RING + chunk * Cfg::CHUNK_BYTES + row * 128 + unit * 16) = make_uint4(0, 0, 0, 0);
-    }
+    for (int s = 0; s < NB; ++s)
+        for (int i = p.tile_keys * D / 8 + threadIdx.x; i < 128 * D / 8; i += Cfg::NUM_THREADS)
+            reinterpret_cast<uint4*>(smem + Cfg::OFF_RING + s * Cfg::TILE_BYTES)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     tcgen05_fence_before();
     __syncthreads();
@@ -381,10 +384,11 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                         armed |= 1u << s;
                         parity = (parity & ~(1u << s)) | ((e / NB) & 1u) << s;
                         if (page >= 0) {
-#pragma unroll
-                            for (int c = 0; c < DCH; ++c)
-                                tma_load_4d(sb + Cfg::OFF_RING + s * Cfg::TILE_BYTES + c * Cfg::CHUNK_BYTES + lane * p.piece * 128,
-                                            kv ? &tmV : &tmK, full(s), c * 64, row, it.hk, page, pol);
+                            const CacheAxes& ax = kv ? p.v_axes : p.k_axes;
+                            const int outer = ax.by_head ? it.hk : page;      // what the groups of 8 rows are counted in
+                            tma_load_5d(sb + Cfg::OFF_RING + s * Cfg::TILE_BYTES + lane * (p.piece / 8) * Cfg::GROUP_BYTES,
+                                        kv ? &tmV : &tmK, full(s), 0, 0, 0, outer * ax.step + row / 8,
+                                        ax.by_head ? page : it.hk, pol);
                         }
                         __syncwarp();
                     }
@@ -416,7 +420,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t o = (k >> 2) * Cfg::CHUNK_BYTES + (k & 3) * 32;
                         mma_f16_ss(tmem_base + Cfg::T_S + region * 128, smem_desc_sw128(q_s + o, 16, 1024),
-                                   smem_desc_sw128(k_s + o, 16, 1024), Cfg::IDESC_S, k > 0 ? 1u : 0u);
+                                   smem_desc_sw128(k_s + (k >> 2) * 1024 + (k & 3) * 32, 16, Cfg::GROUP_BYTES), Cfg::IDESC_S,
+                                   k > 0 ? 1u : 0u);
                     }
                     mma_commit(sfull(region));
                 };
@@ -427,8 +432,9 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                     const uint32_t v_s = tile(2 * m + 1), p_t = tmem_base + Cfg::T_S + region * 128 + Cfg::P_COL;
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_f16_ts(tmem_base + Cfg::T_O + q * D, p_t + k * 8, smem_desc_sw128(v_s + k * 2048, Cfg::CHUNK_BYTES, 1024),
-                                   Cfg::IDESC_PV, (!first || k > 0) ? 1u : 0u);
+                        mma_f16_ts(tmem_base + Cfg::T_O + q * D, p_t + k * 8,
+                                   smem_desc_sw128(v_s + k * 2 * Cfg::GROUP_BYTES, 1024, Cfg::GROUP_BYTES), Cfg::IDESC_PV,
+                                   (!first || k > 0) ? 1u : 0u);
                     return true;
                 };
                 while (ok) {
@@ -639,7 +645,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
                                 *reinterpret_cast<uint4*>(smem + Cfg::OFF_RING + (e % NB) * Cfg::TILE_BYTES +
-                                                          c * Cfg::CHUNK_BYTES + rq * 128 + j * 16) = make_uint4(0, 0, 0, 0);
+                                                          (rq >> 3) * Cfg::GROUP_BYTES + c * 1024 + (rq & 7) * 128 + j * 16) =
+                                    make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                 }

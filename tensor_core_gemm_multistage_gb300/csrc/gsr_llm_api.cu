@@ -116,19 +116,23 @@ gsr::ScoreArgs score_args(float softmax_scale, float softcap, const float* slope
     return s;
 }
 
-// 4-D tensor map of 16-bit elements, innermost contiguous (strides in elements of the other three),
+// Tensor map of 16-bit elements, innermost contiguous (strides in elements of the other dimensions),
 // 128-byte swizzle, zero fill outside.
-gsr_status encode_4d(CUtensorMap* map, const void* data, int32_t dtype, const int64_t (&n)[4], const int64_t (&stride)[3],
-                     const uint32_t (&box)[4]) {
+template <int RANK>
+gsr_status encode_nd(CUtensorMap* map, const void* data, int32_t dtype, const int64_t (&n)[RANK],
+                     const int64_t (&stride)[RANK - 1], const uint32_t (&box)[RANK]) {
     PFN_cuTensorMapEncodeTiled_v12000 encoder = nullptr;
     const gsr_status s = gsr::host::tensor_map_encoder(&encoder);
     if (s != GSR_OK) return s;
-    cuuint64_t dims[4], strides[3];
-    for (int i = 0; i < 4; ++i) dims[i] = (cuuint64_t)n[i];
-    for (int i = 0; i < 3; ++i) strides[i] = (cuuint64_t)stride[i] * 2;
-    const cuuint32_t unit[4] = {1, 1, 1, 1};
+    cuuint64_t dims[RANK], strides[RANK - 1];
+    cuuint32_t unit[RANK];
+    for (int i = 0; i < RANK; ++i) {
+        dims[i] = (cuuint64_t)n[i];
+        unit[i] = 1;
+    }
+    for (int i = 0; i < RANK - 1; ++i) strides[i] = (cuuint64_t)stride[i] * 2;
     const CUresult r = encoder(map, dtype == GSR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                               4, const_cast<void*>(data), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                               RANK, const_cast<void*>(data), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? GSR_OK : gsr::host::fail_encode(r);
@@ -137,7 +141,23 @@ gsr_status encode_4d(CUtensorMap* map, const void* data, int32_t dtype, const in
 // A strided operand {d, rows, heads, batch}, box 64 x box_rows.
 gsr_status encode(CUtensorMap* map, const Strided& t, int32_t dtype, int64_t batch, int64_t heads, int64_t rows,
                   int64_t d, uint32_t box_rows) {
-    return encode_4d(map, t.data, dtype, {d, rows, heads, batch}, {t.row, t.head, t.batch}, {64, box_rows, 1, 1});
+    return encode_nd<4>(map, t.data, dtype, {d, rows, heads, batch}, {t.row, t.head, t.batch}, {64, box_rows, 1, 1});
+}
+
+// A paged cache in groups of 8 rows (gsr::TreeMaps): pages, or else heads, lie whole groups apart.
+bool cache_axes(const Strided& t, int64_t pages, int64_t heads, gsr::CacheAxes* ax) {
+    const int64_t group = 8 * t.row;
+    ax->by_head = !(pages == 1 || t.batch % group == 0);
+    if (ax->by_head && !(heads == 1 || t.head % group == 0)) return false;
+    const int64_t step = ax->by_head ? (heads > 1 ? t.head / group : 0) : (pages > 1 ? t.batch / group : 0);
+    ax->step = (int)step;
+    return step * ((ax->by_head ? heads : pages) - 1) < INT_MAX - 65536;
+}
+gsr_status encode_cache(CUtensorMap* map, const Strided& t, const gsr::CacheAxes& ax, int32_t dtype, int64_t pages,
+                        int64_t heads, int64_t rows, int64_t d, uint32_t piece) {
+    const int64_t counted = ax.by_head ? heads : pages, other = ax.by_head ? pages : heads;
+    return encode_nd<5>(map, t.data, dtype, {64, 8, d / 64, (counted - 1) * ax.step + rows / 8, other},
+                        {t.row, 64, 8 * t.row, ax.by_head ? t.batch : t.head}, {64, 8, (uint32_t)(d / 64), piece / 8, 1});
 }
 
 // How many heads' items are taken together.  Items of unequal length run longest first across as
@@ -390,6 +410,8 @@ gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gs
         (s = operand(k_cache, d.num_pages, d.heads_kv, d.page_size, d.head_dim, false, &p.K)) != GSR_OK ||
         (s = operand(v_cache, d.num_pages, d.heads_kv, d.page_size, d.head_dim, false, &p.V)) != GSR_OK)
         return s;
+    if (!cache_axes(p.K, d.num_pages, d.heads_kv, &p.k_axes) || !cache_axes(p.V, d.num_pages, d.heads_kv, &p.v_axes))
+        return GSR_ERR_INVALID_ARG;
     const Span o = span_of(os, 1, d.heads_q, d.total_q, d.head_dim, 2);
     if (share(os, d.heads_q, d.total_q, qs, d.heads_q, d.total_q, 1, d.head_dim) ||
         meet(o, span_of(p.K, d.num_pages, d.heads_kv, d.page_size, d.head_dim, 2)) ||
@@ -437,13 +459,15 @@ gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gs
     p.timeout_ns = gsr::host::wait_timeout_ns();
     p.test_flags = gsr::host::test_flags();
     gsr::TreeMaps tm;
-    if ((s = encode_4d(&tm.q, Q, d.dtype, {d.head_dim, plan.group, d.heads_kv, d.total_q},
+    if ((s = encode_nd<4>(&tm.q, Q, d.dtype, {d.head_dim, plan.group, d.heads_kv, d.total_q},
                        {p.q_head, p.q_head * plan.group, p.q_row},
                        {64, (uint32_t)plan.group, 1, (uint32_t)plan.tile_nodes})) != GSR_OK)
         return s;
     tm.k = tm.v = tm.q;                 // a pool without pages: never read
-    if (d.num_pages > 0 && ((s = encode(&tm.k, p.K, d.dtype, d.num_pages, d.heads_kv, d.page_size, d.head_dim, plan.piece)) != GSR_OK ||
-                            (s = encode(&tm.v, p.V, d.dtype, d.num_pages, d.heads_kv, d.page_size, d.head_dim, plan.piece)) != GSR_OK))
+    if (d.num_pages > 0 && ((s = encode_cache(&tm.k, p.K, p.k_axes, d.dtype, d.num_pages, d.heads_kv, d.page_size, d.head_dim,
+                                              plan.piece)) != GSR_OK ||
+                            (s = encode_cache(&tm.v, p.V, p.v_axes, d.dtype, d.num_pages, d.heads_kv, d.page_size, d.head_dim,
+                                              plan.piece)) != GSR_OK))
         return s;
     const int grid = (int)(plan.grid < sms ? plan.grid : sms);
     const bool bf16 = d.dtype == GSR_BF16;

@@ -72,6 +72,13 @@ struct MaskedBwdParams {
     uint32_t test_flags;
 };
 
+// How a cache's tensor map counts its rows in groups of 8: by page (group index page x step + row / 8,
+// then the head) or by head (head x step + row / 8, then the page).
+struct CacheAxes {
+    bool by_head;
+    int step;
+};
+
 struct TreeParams {
     int B, Hq, Hkv, group;
     int page, num_pages, table_width, max_nodes, total_q;
@@ -81,6 +88,7 @@ struct TreeParams {
     void* O;
     long long o_row, o_head;
     Strided K, V;               // cache: batch = page stride, row = stride of a page's rows
+    CacheAxes k_axes, v_axes;
     const int* table;           // (B, table_width)
     const int* kv_lens;         // (B): cached tokens, the drafted ones among them
     const int* q_starts;        // (B + 1)
@@ -114,8 +122,8 @@ cudaError_t launch_masked_bwd_f16_128(const MaskedBwdMaps& tm, const MaskedBwdPa
 cudaError_t launch_masked_bwd_bf16_64(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream);
 cudaError_t launch_masked_bwd_bf16_128(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream);
 
-// Query map {D, group, Hkv, total_q}, box {64, group, 1, tile_nodes}; cache maps {D, page, Hkv,
-// pages}, box {64, piece, 1, 1}.
+// Query map {D, group, Hkv, total_q}, box {64, group, 1, tile_nodes}; cache maps {64 columns, 8 rows,
+// chunks, groups of 8 rows, heads or pages}, box {64, 8, chunks, piece / 8, 1}.
 struct TreeMaps {
     CUtensorMap q, k, v;
 };
