@@ -155,10 +155,10 @@ struct TreeCfg {
 // Part of an item in the workspace: for each row of its query tiles O (fp32, not normalised) and
 // the exponent base m and sum l.
 __device__ __forceinline__ float* part_o(const TreeParams& p, long long slot, int row, int D) {
-    return p.parts + (slot * p.nq * 128 + row) * D;
+    return p.parts + (slot * p.part_rows + row) * D;
 }
 __device__ __forceinline__ float2* part_ml(const TreeParams& p, long long slot, int row) {
-    return p.parts_ml + slot * p.nq * 128 + row;
+    return p.parts_ml + slot * p.part_rows + row;
 }
 // Of a grid's CTAs as many as there are units take part, so each has one at least.  CTA c's first
 // unit of U, and the CTA that holds unit u.

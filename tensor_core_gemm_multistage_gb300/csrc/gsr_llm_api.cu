@@ -223,7 +223,7 @@ BwdLayout bwd_layout(const gsr_attention_desc* d) {
 
 // Tiling of a tree attention call, and its workspace in 256-byte pieces.
 struct TreePlan {
-    int group, nq, tile_nodes, piece, tile_keys;
+    int group, nq, tile_nodes, piece, tile_keys, part_rows;
     int64_t grid;                       // CTAs at most
     int64_t starts, ml, parts, total;   // bytes: the pieces' offsets, the sum
 };
@@ -242,7 +242,8 @@ TreePlan tree_plan(const gsr_tree_desc& d) {
     const int64_t tiles = (d.table_width * d.page_size + t.tile_keys - 1) / t.tile_keys;
     const double units = (double)d.batch * (double)d.heads_kv * (double)passes * (double)(tiles > 0 ? tiles : 1);
     t.grid = units < gsr::kTreeMaxGrid ? (int64_t)units : gsr::kTreeMaxGrid;
-    const int64_t rows = 2 * t.grid * t.nq * 128;
+    t.part_rows = t.nq == 2 ? 256 : (int)(d.max_nodes < t.tile_nodes ? d.max_nodes : t.tile_nodes) * t.group;
+    const int64_t rows = 2 * t.grid * t.part_rows;
     t.starts = 0;
     t.ml = piece((d.batch + 1) * 8);
     t.parts = t.ml + piece(rows * 8);
@@ -437,6 +438,7 @@ gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gs
     p.tile_nodes = plan.tile_nodes;
     p.piece = plan.piece;
     p.tile_keys = plan.tile_keys;
+    p.part_rows = plan.part_rows;
     p.page = (int)d.page_size;
     p.num_pages = (int)d.num_pages;
     p.table_width = (int)d.table_width;

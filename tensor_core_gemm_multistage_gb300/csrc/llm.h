@@ -98,7 +98,8 @@ struct TreeParams {
     int piece;                  // rows of one page copy: the page, or a part of it
     int tile_keys;              // keys of a key tile: the pieces that fit in 128 rows
     long long* unit_starts;     // workspace: (B + 1) first units, written by the first launch for the second,
-    float2* parts_ml;           // and two slots of nq x 128 rows per CTA: (m, l),
+    int part_rows;              // query rows of a slot
+    float2* parts_ml;           // and two slots of part_rows per CTA: (m, l),
     float* parts;               // O
     int* err;
     uint64_t timeout_ns;
