@@ -148,8 +148,8 @@ gsr_status flash_attention_fwd(const void* Q, const void* K, const void* V, void
  * Attention of language models: masked attention with its gradient, a paged key/value cache, and
  * attention of drafted tokens over it.  float16 or bfloat16, head_dim 64 or 128, any number of
  * query heads per key/value head.  Scores, softmax and sums in float32.  Caller-owned buffers;
- * asynchronous on `stream`; no memory shared between calls except the per-stream error word, so
- * calls and graph replays on different streams may run at the same time.
+ * asynchronous on `stream`; with workspaces of their own, calls and graph replays share no memory
+ * but the error word and may run at the same time on different streams.
  * ------------------------------------------------------------------------------------------ */
 typedef enum gsr_dtype { GSR_F16 = 0, GSR_BF16 = 1 } gsr_dtype;
 
@@ -220,7 +220,10 @@ gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor
  * Queries without keys get dQ = 0 and add nothing, whatever their dO holds.
  *
  *   workspace  device pointer, 16-byte aligned, masked_attention_bwd_workspace(desc) bytes, for
- *              this call alone until it has finished.
+ *              this call alone until it has finished; or NULL: one that the library keeps for the
+ *              stream (grown after a wait for the stream, so not for a first call of its size in a
+ *              capture; released by gsr_release_stream; graphs captured with it must not run at the
+ *              same time as each other or as other calls on that stream).
  */
 int64_t masked_attention_bwd_workspace(const gsr_attention_desc* desc);
 gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor* dO, const gsr_tensor* Q,
@@ -252,7 +255,7 @@ gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor
  * O = 0.
  *
  *   workspace  device pointer, 16-byte aligned, tree_attention_workspace(desc) bytes, for this
- *              call alone until it has finished.
+ *              call alone until it has finished; or NULL, as for masked_attention_bwd.
  */
 #define GSR_TREE_MAX_NODES 64
 typedef struct gsr_tree_desc {
@@ -391,7 +394,8 @@ gsr_status gsr_device_status(struct CUstream_st* stream, int* code);
 
 /*
  * Releases the library's state for the (current device, stream) pair: the
- * stream's 16 bytes of words and, if a small-M call ran on it, its workspace.
+ * stream's 16 bytes of words and the workspaces of small-M calls, masked-attention
+ * gradients and tree attention, if any ran on it.
  * Waits for the stream first (queued kernels may still use them).  For callers
  * that create and destroy streams: call it before destroying a stream the
  * library was used on, from no other thread launching on that stream at the same

@@ -51,6 +51,8 @@ struct StreamState {
     size_t partial_floats = 0;
     int* tickets = nullptr;      // small-M per-tile ticket counters (zero between launches)
     size_t ticket_count = 0;
+    void* scratch = nullptr;     // workspace of masked-attention gradients and tree attention
+    size_t scratch_bytes = 0;
 };
 
 struct DeviceInfo {
@@ -682,6 +684,26 @@ gsr_status error_word(int dev, cudaStream_t stream, int** err) {
     return s;
 }
 
+gsr_status stream_scratch(int dev, cudaStream_t stream, size_t bytes, void** scratch) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    StreamState& s = g_streams[{dev, stream}];
+    if (bytes > s.scratch_bytes) {
+        cudaError_t e;
+        // Earlier launches on this stream may still use the old buffer.
+        if ((e = cudaStreamSynchronize(stream)) != cudaSuccess) return cuda_fail(e);
+        cudaFree(s.scratch);
+        s.scratch = nullptr;
+        s.scratch_bytes = 0;
+        if ((e = cudaMalloc(&s.scratch, bytes)) != cudaSuccess) {
+            s.scratch = nullptr;
+            return cuda_fail(e);
+        }
+        s.scratch_bytes = bytes;
+    }
+    *scratch = s.scratch;
+    return GSR_OK;
+}
+
 gsr_status tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* encode) {
     const gsr_status s = load_encoder();
     *encode = g_encode;
@@ -995,8 +1017,8 @@ gsr_status gsr_release_stream(CUstream_st* stream) {
     }
     // Kernels queued earlier on the stream may still use the memory.
     e = cudaStreamSynchronize(st);
-    cudaError_t e1 = cudaFree(s.err), e2 = cudaFree(s.partials), e3 = cudaFree(s.tickets);
-    if (e == cudaSuccess) e = e1 != cudaSuccess ? e1 : (e2 != cudaSuccess ? e2 : e3);
+    cudaError_t e1 = cudaFree(s.err), e2 = cudaFree(s.partials), e3 = cudaFree(s.tickets), e4 = cudaFree(s.scratch);
+    if (e == cudaSuccess) e = e1 != cudaSuccess ? e1 : (e2 != cudaSuccess ? e2 : (e3 != cudaSuccess ? e3 : e4));
     return e == cudaSuccess ? GSR_OK : cuda_fail(e);
 }
 
@@ -1051,10 +1073,9 @@ gsr_status gsr_shutdown(void) {
     for (auto& kv : g_streams) {
         if (cudaSetDevice(kv.first.first) != cudaSuccess) continue;
         StreamState& s = kv.second;
-        cudaError_t e1 = cudaFree(s.err), e2 = cudaFree(s.partials), e3 = cudaFree(s.tickets);
-        if (e1 != cudaSuccess || e2 != cudaSuccess || e3 != cudaSuccess) {
-            result = cuda_fail(e1 != cudaSuccess ? e1 : (e2 != cudaSuccess ? e2 : e3));
-        }
+        cudaError_t e1 = cudaFree(s.err), e2 = cudaFree(s.partials), e3 = cudaFree(s.tickets), e4 = cudaFree(s.scratch);
+        for (cudaError_t e : {e1, e2, e3, e4})
+            if (e != cudaSuccess) result = cuda_fail(e);
     }
     g_streams.clear();
     for (auto& kv : g_pipes) {

@@ -3,6 +3,7 @@
 // contract.
 #include <climits>
 #include <cmath>
+#include <mutex>
 
 #include "host_state.h"
 #include "llm.h"
@@ -10,6 +11,10 @@
 namespace {
 
 using gsr::Strided;
+
+// Held while a call that uses its stream's own workspace queues its launches: two threads' calls on
+// one stream then follow each other whole.
+std::mutex g_scratch_mu;
 
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 bool bad_size(int64_t n) { return n < 0 || n > INT_MAX; }
@@ -340,11 +345,11 @@ gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor
     if (no_q && no_k) return GSR_OK;
     if (!no_q && !lse) return GSR_ERR_INVALID_ARG;
     const BwdLayout w = bwd_layout(desc);
-    if (!workspace || workspace_bytes < w.total) return GSR_ERR_INVALID_ARG;
+    if (workspace && workspace_bytes < w.total) return GSR_ERR_INVALID_ARG;
     if (misaligned(lse, 4) || misaligned(workspace, 16)) return GSR_ERR_ALIGNMENT;
     // outputs share elements with nothing; the workspace and lse lie apart from the operands
     const uintptr_t w0 = reinterpret_cast<uintptr_t>(workspace), l0 = reinterpret_cast<uintptr_t>(lse);
-    const Span ws{w0, w0 + (uintptr_t)w.total}, ls{l0, lse ? l0 + (uintptr_t)(B * Hq * Sq * 4) : l0};
+    const Span ws{w0, workspace ? w0 + (uintptr_t)w.total : w0}, ls{l0, lse ? l0 + (uintptr_t)(B * Hq * Sq * 4) : l0};
     if (meet(ws, ls)) return GSR_ERR_ALIAS;
     for (size_t i = 0; i < sizeof(all) / sizeof(all[0]); ++i) {
         const auto& a = all[i];
@@ -364,6 +369,11 @@ gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor
     p.mask = mask_args(desc);
     p.score = score_args(desc->softmax_scale, desc->softcap, desc->alibi_slopes, D);
     p.lse = lse;
+    std::unique_lock<std::mutex> lock(g_scratch_mu, std::defer_lock);
+    if (!workspace) {
+        lock.lock();
+        if ((s = gsr::host::stream_scratch(dev, st, (size_t)w.total, &workspace)) != GSR_OK) return s;
+    }
     char* base = static_cast<char*>(workspace);
     p.norms = reinterpret_cast<unsigned*>(base);
     p.Sp = (int)w.sp;
@@ -419,9 +429,9 @@ gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gs
         meet(o, span_of(p.V, d.num_pages, d.heads_kv, d.page_size, d.head_dim, 2)))
         return GSR_ERR_ALIAS;
     const TreePlan plan = tree_plan(d);
-    if (!workspace || workspace_bytes < plan.total) return GSR_ERR_INVALID_ARG;
+    if (workspace && workspace_bytes < plan.total) return GSR_ERR_INVALID_ARG;
     const uintptr_t w0 = reinterpret_cast<uintptr_t>(workspace);
-    const Span ws{w0, w0 + (uintptr_t)plan.total};
+    const Span ws{w0, workspace ? w0 + (uintptr_t)plan.total : w0};
     if (meet(ws, o) || meet(ws, span_of(qs, 1, d.heads_q, d.total_q, d.head_dim, 2)) ||
         meet(ws, span_of(p.K, d.num_pages, d.heads_kv, d.page_size, d.head_dim, 2)) ||
         meet(ws, span_of(p.V, d.num_pages, d.heads_kv, d.page_size, d.head_dim, 2)))
@@ -455,6 +465,11 @@ gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gs
     p.kv_lens = kv_lens;
     p.q_starts = q_starts;
     p.parents = parents;
+    std::unique_lock<std::mutex> lock(g_scratch_mu, std::defer_lock);
+    if (!workspace) {
+        lock.lock();
+        if ((s = gsr::host::stream_scratch(dev, st, (size_t)plan.total, &workspace)) != GSR_OK) return s;
+    }
     p.unit_starts = reinterpret_cast<long long*>(static_cast<char*>(workspace) + plan.starts);
     p.parts_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.ml);
     p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.parts);

@@ -105,17 +105,20 @@ def _vector(t, name, count, dtype, index):
 
 
 def _scratch(workspace, nbytes, index, stream):
-    """Address and size of the caller's workspace, or of a new one that lives until the work queued on
-    `stream` is done."""
+    """A tensor to keep until the call returns, its address and its size: the caller's workspace; None
+    (the library's own for the current stream); or, in a capture and for an explicit stream, a new
+    one, so that no two graphs share it."""
     if workspace is not None:
         if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on cuda:%d" % index)
-        return workspace, workspace.numel() * workspace.element_size()
-    nbytes = max(nbytes, 16)
+        return workspace, workspace.data_ptr() or None, workspace.numel() * workspace.element_size()
+    if stream is None and not torch.cuda.is_current_stream_capturing():
+        return None, None, 0
+    nbytes = max(nbytes(), 16)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
     if stream is not None:
         ws.record_stream(torch.cuda.ExternalStream(stream, device=ws.device) if isinstance(stream, int) else stream)
-    return ws, nbytes
+    return ws, ws.data_ptr(), nbytes
 
 
 def _attention_desc(Q, K, softmax_scale, causal, softcap, alibi_slopes, doc_bounds, prefix_lens):
@@ -172,15 +175,16 @@ def masked_attention_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, softmax_scale: float =
 
     dO, O and dQ are shaped as Q, dK and dV as K; masks and scores as in the forward call.
     ``workspace``: optional device buffer of masked_attention_bwd_workspace(...) bytes; without one
-    the call takes it from PyTorch's allocator.
+    the library keeps one for the current stream, and a call with ``stream`` or inside a capture takes
+    one from PyTorch's allocator.
     """
     d, qs, ks, dev = _attention_desc(Q, K, softmax_scale, causal, softcap, alibi_slopes, doc_bounds, prefix_lens)
     dt, L = Q.dtype, lib()
-    ws, size = _scratch(workspace, L.masked_attention_bwd_workspace(d), dev, stream)
+    ws, scratch, size = _scratch(workspace, lambda: L.masked_attention_bwd_workspace(d), dev, stream)
     _call(dev, stream, "masked_attention_bwd", L.masked_attention_bwd, d, _operand(dO, "dO", qs, dt, dev),
           _operand(Q, "Q", qs, dt, dev), _operand(K, "K", ks, dt, dev), _operand(V, "V", ks, dt, dev),
           _operand(O, "O", qs, dt, dev), _lse(lse, qs, dev), _operand(dQ, "dQ", qs, dt, dev),
-          _operand(dK, "dK", ks, dt, dev), _operand(dV, "dV", ks, dt, dev), ws.data_ptr(), size)
+          _operand(dK, "dK", ks, dt, dev), _operand(dV, "dV", ks, dt, dev), scratch, size)
     return dQ, dK, dV
 
 
@@ -214,7 +218,7 @@ def tree_attention_fwd(Q, k_cache, v_cache, block_tables, kv_lens, q_starts, par
     block_tables (B, W), kv_lens (B,) with the drafted tokens, q_starts (B + 1,), parents (N,) (an
     earlier node of the request or -1; None: a chain), all int32.  A token sees what is before the
     tree, its ancestors and itself.  ``max_nodes`` bounds the nodes of one request (at most 64); 1 is
-    ordinary decoding.
+    ordinary decoding.  ``workspace``: as for masked_attention_bwd, tree_attention_workspace bytes.
     """
     code, dev, dt, i32 = _dtype_code(Q, "Q"), Q.get_device(), Q.dtype, torch.int32
     if Q.dim() != 3 or dev < 0:
@@ -234,13 +238,22 @@ def tree_attention_fwd(Q, k_cache, v_cache, block_tables, kv_lens, q_starts, par
     d = _TreeDesc(B, N, Hq, cache[2], D, cache[0], cache[1], W, max_nodes, qr, qh, orow, oh, code, softmax_scale, softcap,
                   _vector(alibi_slopes, "alibi_slopes", Hq, torch.float32, dev))
     L = lib()
-    ws, size = _scratch(workspace, L.tree_attention_workspace(d), dev, stream)
+    ws, scratch, size = _scratch(workspace, lambda: L.tree_attention_workspace(d), dev, stream)
     _call(dev, stream, "tree_attention_fwd", L.tree_attention_fwd, d, Q.data_ptr() or None,
           _cache(k_cache, "k_cache", cache, dt, dev), _cache(v_cache, "v_cache", cache, dt, dev),
           _vector(block_tables, "block_tables", B * W, i32, dev), _vector(kv_lens, "kv_lens", B, i32, dev),
           _vector(q_starts, "q_starts", B + 1, i32, dev), _vector(parents, "parents", N, i32, dev),
-          O.data_ptr() or None, ws.data_ptr(), size)
+          O.data_ptr() or None, scratch, size)
     return O
+
+
+def tree_attention_workspace(B: int, N: int, Hq: int, Hkv: int, D: int, pages: int, page_size: int, W: int,
+                             max_nodes: int) -> int:
+    """Bytes of workspace a tree_attention_fwd call of these sizes needs."""
+    n = lib().tree_attention_workspace(_TreeDesc(B, N, Hq, Hkv, D, pages, page_size, W, max_nodes))
+    if n < 0:
+        raise GsrError(Status.ERR_INVALID_ARG, "tree_attention_workspace")
+    return n
 
 
 def kv_block_tables(kv_lens, new_lens, free_blocks, free_head, block_tables, page_size: int, kv_lens_out,
