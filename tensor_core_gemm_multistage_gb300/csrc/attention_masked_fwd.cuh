@@ -138,10 +138,13 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
     const int lane = threadIdx.x & 31;
     const MaskArgs& mk = p.mask;
 
-    // What the producer publishes of an item; b < 0: no more items.  Query tile q reads key tiles
-    // [t0[q], t1[q]).
+    // What the producer publishes of an item; b < 0: no more items.  Query tile q takes steps
+    // [t0[q], t1[q]) and step t reads key tile key_tile(t).  A distance bias grows towards the row's own
+    // position, which under a causal mask is its last key: from the first tile on, the maximum would
+    // move and O be rescaled at nearly every step, so these kernels walk the keys backwards.
     struct Item {
-        int b, h, q_base, t0[NQ], t1[NQ];
+        int b, h, q_base, t0[NQ], t1[NQ], flip;
+        __device__ __forceinline__ int key_tile(int t) const { return kHasBias<Cfg::MODE> ? flip - t : t; }
         __device__ __forceinline__ int first() const {
             return t1[0] > t0[0] ? (t1[1] > t0[1] ? min(t0[0], t0[1]) : t0[0]) : t0[1];
         }
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
     };
     auto read_item = [&](int box) {
         volatile int* v = item_box + 8 * box;
-        return Item{v[0], v[1], v[2], {v[3], v[4]}, {v[5], v[6]}};
+        return Item{v[0], v[1], v[2], {v[3], v[4]}, {v[5], v[6]}, v[7]};
     };
 
     if (threadIdx.x == 0) {
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
             bool asked = false;
             int item = blockIdx.x;
             while (true) {
-                Item it{-1, 0, 0, {0, 0}, {0, 0}};
+                Item it{-1, 0, 0, {0, 0}, {0, 0}, 0};
                 if (item >= 0) {
                     // query blocks from the last (under a causal mask the longest) to the first, in
                     // groups of heads whose K and V stay in L2 together
@@ -221,6 +224,16 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                         it.t0[q] = l / Cfg::BKV;
                         it.t1[q] = e > l ? (e + Cfg::BKV - 1) / Cfg::BKV : it.t0[q];
                     }
+                    if (kHasBias<Cfg::MODE>) {
+                        const int both = it.first() + it.last();
+                        it.flip = both - 1;
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) {
+                            const int t0 = it.t0[q];
+                            it.t0[q] = both - it.t1[q];
+                            it.t1[q] = both - t0;
+                        }
+                    }
                 }
                 const uint32_t box = n_pub & 1u;
                 // the box's previous item has been read by every role
@@ -236,6 +249,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                         v[3 + q] = it.t0[q];
                         v[5 + q] = it.t1[q];
                     }
+                    v[7] = it.flip;
                     mbar_arrive(item_pub(box));              // release: the consumers read the box after
                 }
                 ++n_pub;
@@ -275,13 +289,13 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
 #pragma unroll
                                 for (int c = 0; c < Cfg::DCH; ++c)
                                     tma_load_4d(sb + Cfg::OFF_K + s * Cfg::KV_BYTES + c * Cfg::CHUNK_BYTES, &tmK, full(s), c * 64,
-                                                t * Cfg::BKV, hk, it.b, pol);
+                                                it.key_tile(t) * Cfg::BKV, hk, it.b, pol);
                             }
                             if (has_v) {
 #pragma unroll
                                 for (int c = 0; c < Cfg::DCH; ++c)
                                     tma_load_4d(sb + Cfg::OFF_V + s * Cfg::KV_BYTES + c * Cfg::CHUNK_BYTES, &tmV, full(s), c * 64,
-                                                (t - 1) * Cfg::BKV, hk, it.b, pol);
+                                                it.key_tile(t - 1) * Cfg::BKV, hk, it.b, pol);
                             }
                             armed |= 1u << s;
                             parity = (parity & ~(1u << s)) | ph << s;
@@ -412,7 +426,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                 }
                 ++s_n;
                 tcgen05_fence_after();
-                const int k0 = t * Cfg::BKV;
+                const int k0 = it.key_tile(t) * Cfg::BKV;
                 const bool masked = k0 < lo || k0 + Cfg::BKV > hi;
                 uint32_t sc0[32], sc1[32], sc2[32], sc3[32];
                 tmem_ld_32x32b_x32(s_col + 0, sc0);
