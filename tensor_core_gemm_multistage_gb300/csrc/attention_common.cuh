@@ -128,16 +128,60 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // of a score is a few units of cap 2^-24, which is what the softmax sees.
 __device__ __forceinline__ float cap_r(float s, float cap_in) { return rcp_approx(1.0f + ex2_approx(s * cap_in)); }
 
-// cap_r of two products, in place, with one reciprocal: 1 / a = b / (a b).  The reciprocal runs at
-// half the exponential's rate (16 against 32 a clock and SM, measured).  2^60 keeps a b finite and is
-// tanh = 1 to the last bit.  A NaN stays one and takes its partner along; the row is then not finite
-// and is computed again.
+// Capped scores of a row are taken through z = (8/3) scale q.k / cap, so that bit 30 of a z, set where
+// its magnitude is 2 or more (or it is infinite or NaN), says that the tanh's argument is beyond 3/4.
+//
+// tanh(3/8 z) for |z| < 2, two values in place: z times a polynomial in z^2, whose six coefficients
+// minimise the largest relative error over the range (3e-8; a weighted least-squares fit with the
+// weights moved to where the error is).  Off by 1e-7 at most in fp32.  Seven FMA slots a score, where
+// 1 / (1 + e^(2x)) takes an exponential and a reciprocal, three slots of the exponential's size on the
+// special-function unit (32 and 16 a clock and SM, measured), which two softmax groups share with the
+// probabilities' exponentials.
+__device__ __forceinline__ void tanh_small2(float& z0, float& z1) {
+    float u0, u1, p0, p1;
+    fmul2(u0, u1, z0, z1, z0, z1);
+    ffma2(p0, p1, u0, u1, -9.72615837e-08f, -9.72615837e-08f, 2.87182866e-06f, 2.87182866e-06f);
+    ffma2(p0, p1, p0, p1, u0, u1, -5.5629851e-05f, -5.5629851e-05f);
+    ffma2(p0, p1, p0, p1, u0, u1, 0.00098818168f, 0.00098818168f);
+    ffma2(p0, p1, p0, p1, u0, u1, -0.0175779276f, -0.0175779276f);
+    ffma2(p0, p1, p0, p1, u0, u1, 0.375f, 0.375f);
+    fmul2(z0, z1, z0, z1, p0, p1);
+}
+// The same for any z: 1 - 2 r.
+__device__ __forceinline__ void tanh_any2(float& z0, float& z1) {
+    constexpr float kExponent = 2.0f * 0.375f * kLog2e;
+    fmul2(z0, z1, z0, z1, kExponent, kExponent);
+    z0 = ex2_approx(z0);
+    z1 = ex2_approx(z1);
+    fadd2(z0, z1, 1.0f, 1.0f);
+    z0 = rcp_approx(z0);
+    z1 = rcp_approx(z1);
+    ffma2(z0, z1, z0, z1, -2.0f, -2.0f, 1.0f, 1.0f);
+}
+// 32 products -> z in place; returns the bits set in any of them.
+__device__ __forceinline__ uint32_t cap_scale(uint32_t (&rr)[32], float cap_z) {
+    uint32_t bits = 0u;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        float y0, y1;
+        fmul2(y0, y1, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]), cap_z, cap_z);
+        rr[i] = __float_as_uint(y0);
+        rr[i + 1] = __float_as_uint(y1);
+        bits |= rr[i] | rr[i + 1];
+    }
+    return bits;
+}
+
+// cap_r of two products, in place, with one reciprocal, 1 / a = b / (a b).  2^60 keeps a b finite and is tanh = 1 to the last
+// bit.  A NaN stays one and takes its partner along; the row is then not finite and is computed again.
+// In the gradients' kernels, whose special-function unit has room, it beats both the polynomial
+// (4 x 32 x 4096 x 128 capped: 3757 us) and two reciprocals (3634): 3557.
 __device__ __forceinline__ float min_nan(float a, float b) {
     float y;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
-__device__ __forceinline__ void cap_r2(float& s0, float& s1, float cap_in) {
+__device__ __forceinline__ void cap_r_pair(float& s0, float& s1, float cap_in) {
     float a, b;
     fmul2(a, b, s0, s1, cap_in, cap_in);
     a = ex2_approx(min_nan(a, 60.0f));
@@ -146,7 +190,6 @@ __device__ __forceinline__ void cap_r2(float& s0, float& s1, float cap_in) {
     const float r = rcp_approx(a * b);
     fmul2(s0, s1, r, r, b, a);
 }
-
 enum ScoreMode : int { kScorePlain = 0, kScoreBias = 1, kScoreCap = 2, kScoreCapBias = 3 };
 template <int MODE>
 constexpr bool kHasCap = MODE == kScoreCap || MODE == kScoreCapBias;
@@ -156,25 +199,26 @@ inline ScoreMode score_mode(const ScoreArgs& sc) {
     return sc.cap_in != 0.0f ? (sc.slopes ? kScoreCapBias : kScoreCap) : (sc.slopes ? kScoreBias : kScorePlain);
 }
 
-// A row's scores while its softmax runs: registers hold v with score = mul v + add in log2 units, so
+// A row's scores while its softmax runs: registers hold v with score = mul v in log2 units, so
 // that the scaling is part of the exponent's multiply-add.  Plain scores keep the raw products;
-// capped ones without a bias keep r; anything with a bias holds the score itself.  A score's order is
-// v's where mul >= 0 and the reverse elsewhere.
+// capped ones without a bias keep the tanh; anything with a bias holds the score itself.  A score's
+// order is v's where mul >= 0 and the reverse elsewhere.
 struct ScoreForm {
-    float mul, add;
+    float mul;
     bool ascending;
     __device__ __forceinline__ uint32_t hidden() const { return ascending ? 0xff800000u : 0x7f800000u; }   // score -inf
 };
 template <int MODE>
 __device__ __forceinline__ ScoreForm score_form(const ScoreArgs& sc) {
-    if (MODE == kScorePlain) return {sc.sl2, 0.0f, sc.sl2 >= 0.0f};
-    if (MODE == kScoreCap) return {-2.0f * sc.cap_out, sc.cap_out, false};
-    return {1.0f, 0.0f, true};
+    if (MODE == kScorePlain) return {sc.sl2, sc.sl2 >= 0.0f};
+    if (MODE == kScoreCap) return {sc.cap_out, true};
+    return {1.0f, true};
 }
 
 // 32 raw products of one row and consecutive keys -> v, in place.  `base` is the first key's
-// distance from the row's position (later keys are closer by 1 each).
-template <int MODE>
+// distance from the row's position (later keys are closer by 1 each).  With a cap the registers hold
+// z; SMALL: every z of the row is below 2.
+template <int MODE, bool SMALL>
 __device__ __forceinline__ void score_chunk(uint32_t (&rr)[32], const ScoreArgs& sc, float slope2, float base) {
     if (MODE == kScorePlain) return;
     if (MODE == kScoreBias && base >= 31.0f) {           // no key behind the row: the bias is linear
@@ -192,19 +236,15 @@ __device__ __forceinline__ void score_chunk(uint32_t (&rr)[32], const ScoreArgs&
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
         float y0 = __uint_as_float(rr[i]), y1 = __uint_as_float(rr[i + 1]);
-        if (kHasCap<MODE>) {
-            fmul2(y0, y1, y0, y1, sc.cap_in, sc.cap_in);
-            y0 = ex2_approx(y0);
-            y1 = ex2_approx(y1);
-            fadd2(y0, y1, 1.0f, 1.0f);
-            y0 = rcp_approx(y0);
-            y1 = rcp_approx(y1);
+        if (kHasCap<MODE> && SMALL) {
+            tanh_small2(y0, y1);
+        } else if (kHasCap<MODE>) {
+            tanh_any2(y0, y1);
         } else {
             fmul2(y0, y1, y0, y1, sc.sl2, sc.sl2);
         }
         if (kHasBias<MODE>) {
-            if (kHasCap<MODE>)
-                ffma2(y0, y1, y0, y1, -2.0f * sc.cap_out, -2.0f * sc.cap_out, sc.cap_out, sc.cap_out);
+            if (kHasCap<MODE>) fmul2(y0, y1, y0, y1, sc.cap_out, sc.cap_out);
             y0 = fmaf(-slope2, fabsf(base - (float)i), y0);
             y1 = fmaf(-slope2, fabsf(base - (float)(i + 1)), y1);
         }
@@ -229,6 +269,27 @@ cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, unsigned bloc
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// A row's 128 products.  With POLY the warp takes tanh's polynomial where all its rows may.
+template <int MODE, bool POLY>
+__device__ __forceinline__ void score_row(uint32_t (&a)[32], uint32_t (&b)[32], uint32_t (&c)[32], uint32_t (&d)[32],
+                                          const ScoreArgs& sc, float slope2, float base) {
+    if (MODE == kScorePlain) return;
+    if (kHasCap<MODE>) {
+        const uint32_t bits = cap_scale(a, sc.cap_z) | cap_scale(b, sc.cap_z) | cap_scale(c, sc.cap_z) | cap_scale(d, sc.cap_z);
+        if (POLY && __all_sync(0xffffffffu, !(bits & 0x40000000u))) {
+            score_chunk<MODE, true>(a, sc, slope2, base);
+            score_chunk<MODE, true>(b, sc, slope2, base - 32.0f);
+            score_chunk<MODE, true>(c, sc, slope2, base - 64.0f);
+            score_chunk<MODE, true>(d, sc, slope2, base - 96.0f);
+            return;
+        }
+    }
+    score_chunk<MODE, false>(a, sc, slope2, base);
+    score_chunk<MODE, false>(b, sc, slope2, base - 32.0f);
+    score_chunk<MODE, false>(c, sc, slope2, base - 64.0f);
+    score_chunk<MODE, false>(d, sc, slope2, base - 96.0f);
 }
 
 // Largest and smallest of a row's 128 values, in four chains of three-input instructions.

@@ -256,7 +256,7 @@ __device__ __forceinline__ void weights_chunk(uint32_t (&rr)[32], const ScoreArg
         float y0 = __uint_as_float(rr[i]), y1 = __uint_as_float(rr[i + 1]), c0, c1;
         const float2 o = off(i);
         if (kHasCap<MODE>) {
-            cap_r2(y0, y1, sc.cap_in);
+            cap_r_pair(y0, y1, sc.cap_in);
             ffma2(c0, c1, y0, y1, -y0, -y1, y0, y1);
             ffma2(y0, y1, y0, y1, -2.0f * sc.cap_out, -2.0f * sc.cap_out, o.x, o.y);
         } else {

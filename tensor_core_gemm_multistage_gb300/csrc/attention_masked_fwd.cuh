@@ -438,20 +438,23 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                 reg_tie(sc2);
                 reg_tie(sc3);
                 const float base = (float)(qi + mk.offset - k0);
-                auto transform = [&](uint32_t (&rr)[32], int c) {
-                    score_chunk<Cfg::MODE>(rr, sc, slope2, base - (float)(c * 32));
-                    if (masked) {
+                score_row<Cfg::MODE, true>(sc0, sc1, sc2, sc3, sc, slope2, base);
+                if (masked) {
+                    // of a boundary tile's four chunks few hold the boundary, and the warp's rows share it
+                    auto hide = [&](uint32_t (&rr)[32], int c) {
+                        const int from = lo - k0 - c * 32, to = hi - k0 - c * 32;
+                        if (from <= 0 && to >= 32) return;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (c * 32 + i < lo - k0 || c * 32 + i >= hi - k0) rr[i] = hidden;
-                    }
-                };
-                transform(sc0, 0);
-                transform(sc1, 1);
-                transform(sc2, 2);
-                transform(sc3, 3);
+                            if (i < from || i >= to) rr[i] = hidden;
+                    };
+                    hide(sc0, 0);
+                    hide(sc1, 1);
+                    hide(sc2, 2);
+                    hide(sc3, 3);
+                }
                 float mt = form.ascending ? row_max(sc0, sc1, sc2, sc3) : row_min(sc0, sc1, sc2, sc3);
-                mt = fmaf(mt, form.mul, form.add);
+                mt *= form.mul;
                 // lazy move of the exponent base: only by more than 2^RESCALE_LOG2 (always from -inf)
                 float factor = 1.0f;
                 const bool bump = mt > m + Cfg::RESCALE_LOG2;
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                     m = mt;
                 }
                 l *= factor;
-                const float neg_m = form.add - ((m == -INFINITY) ? 0.0f : m), mul = form.mul;
+                const float neg_m = (m == -INFINITY) ? 0.0f : -m, mul = form.mul;
                 float ls0 = 0.0f, ls1 = 0.0f;
                 auto chunk_p = [&](const uint32_t (&rr)[32], int c) {
                     uint32_t packed[16];

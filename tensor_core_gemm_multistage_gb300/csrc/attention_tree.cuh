@@ -557,9 +557,10 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                     reg_tie(sc2);
                     reg_tie(sc3);
                     const float base = (float)(pos - k0);
-                    auto transform = [&](uint32_t (&rr)[32], int c) {
-                        score_chunk<Cfg::MODE>(rr, sc, slope2, base - (float)(c * 32));
-                        if (!masked) return;
+                    // the polynomial's second copy of the code costs more here, where items are short and find it
+                    // cold, than it saves (16 trees of up to 40 nodes: 121 us with it, 112 without)
+                    score_row<Cfg::MODE, false>(sc0, sc1, sc2, sc3, sc, slope2, base);
+                    auto hide = [&](uint32_t (&rr)[32], int c) {
                         const int kk = k0 + c * 32;
                         auto below = [&](int limit) {    // keys before `limit`
                             const int k = limit - kk;
@@ -588,18 +589,20 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                         for (int j = 0; j < 32; ++j)
                             if (!(vis >> j & 1u)) rr[j] = hidden;
                     };
-                    transform(sc0, 0);
-                    transform(sc1, 1);
-                    transform(sc2, 2);
-                    transform(sc3, 3);
-                    const float mt = fmaf(form.ascending ? row_max(sc0, sc1, sc2, sc3) : row_min(sc0, sc1, sc2, sc3), form.mul, form.add);
+                    if (masked) {
+                        hide(sc0, 0);
+                        hide(sc1, 1);
+                        hide(sc2, 2);
+                        hide(sc3, 3);
+                    }
+                    const float mt = (form.ascending ? row_max(sc0, sc1, sc2, sc3) : row_min(sc0, sc1, sc2, sc3)) * form.mul;
                     bump = mt > m + Cfg::RESCALE_LOG2;   // always from -inf
                     if (bump) {
                         factor = (m == -INFINITY) ? 0.0f : ex2_approx(m - mt);
                         m = mt;
                     }
                     l *= factor;
-                    const float neg_m = form.add - ((m == -INFINITY) ? 0.0f : m), mul = form.mul;
+                    const float neg_m = (m == -INFINITY) ? 0.0f : -m, mul = form.mul;
                     float ls0 = 0.0f, ls1 = 0.0f;
                     auto chunk_p = [&](const uint32_t (&rr)[32], int c) {
                         uint32_t packed[16];

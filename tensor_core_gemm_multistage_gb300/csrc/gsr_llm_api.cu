@@ -115,6 +115,7 @@ gsr::ScoreArgs score_args(float softmax_scale, float softcap, const float* slope
     gsr::ScoreArgs s;
     s.scale = (float)scale;
     s.sl2 = (float)(scale * log2e);
+    s.cap_z = softcap > 0.0f ? (float)(8.0 / 3.0 * scale / softcap) : 0.0f;
     s.cap_in = softcap > 0.0f ? (float)(2.0 * log2e * scale / softcap) : 0.0f;
     s.cap_out = (float)(softcap * log2e);
     s.slopes = slopes;

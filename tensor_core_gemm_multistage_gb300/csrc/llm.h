@@ -38,6 +38,7 @@ struct ScoreArgs {
     float scale;                // softmax scale
     float sl2;                  // scale * log2(e): y = sl2 * (q.k) without a cap
     float cap_in;               // 2 log2(e) scale / cap: tanh's exponent, 0 without a cap
+    float cap_z;                // (8/3) scale / cap
     float cap_out;              // cap * log2(e)
     const float* slopes;        // per query head, or null
 };
