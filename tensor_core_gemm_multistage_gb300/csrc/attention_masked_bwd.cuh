@@ -339,7 +339,6 @@ __device__ __forceinline__ void mma_overlay(uint32_t d, uint32_t a, uint32_t b, 
 // Rows of an accumulator to a strided output, one row per thread; true if a value is not finite.
 template <class T, int D>
 __device__ __forceinline__ bool store_accumulator(uint32_t col, float factor, bool zero, bool write, T* row) {
-    uint4* dst = reinterpret_cast<uint4*>(row);
     bool bad = false;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
@@ -351,17 +350,14 @@ __device__ __forceinline__ bool store_accumulator(uint32_t col, float factor, bo
             for (int i = 0; i < 32; ++i) rr[i] = 0u;
         }
         if (write) {
+            uint32_t v[16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = __uint_as_float(rr[8 * k + 2 * i]), b = __uint_as_float(rr[8 * k + 2 * i + 1]);
-                    bad |= !(fabsf(a) < INFINITY) | !(fabsf(b) < INFINITY);
-                    v[i] = Elem<T>::pack(a * factor, b * factor);
-                }
-                dst[c * 4 + k] = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int i = 0; i < 16; ++i) {
+                const float a = __uint_as_float(rr[2 * i]), b = __uint_as_float(rr[2 * i + 1]);
+                bad |= !(fabsf(a) < INFINITY) | !(fabsf(b) < INFINITY);
+                v[i] = Elem<T>::pack(a * factor, b * factor);
             }
+            store_64_bytes(row + c * 32, v);
         }
     }
     return bad;

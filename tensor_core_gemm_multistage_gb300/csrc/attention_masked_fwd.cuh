@@ -515,8 +515,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
             if (!ok) break;
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
             bool bad = !(l < INFINITY);          // l or an element of O is infinite or NaN
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.O.data) + it.b * p.O.batch + it.h * p.O.head +
-                                                  (long long)qi * p.O.row);
+            T* dst = static_cast<T*>(p.O.data) + it.b * p.O.batch + it.h * p.O.head + (long long)qi * p.O.row;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t rr[32];
@@ -532,17 +531,14 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                     for (int i = 0; i < 32; ++i) rr[i] = 0u;     // 0 V of a row without keys
                 }
                 if (qi < mk.Sq) {
+                    uint32_t v[16];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t v[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float a = __uint_as_float(rr[8 * k + 2 * i]), b = __uint_as_float(rr[8 * k + 2 * i + 1]);
-                            bad |= !(fabsf(a) < INFINITY) | !(fabsf(b) < INFINITY);
-                            v[i] = Elem<T>::pack(a * inv, b * inv);
-                        }
-                        dst[c * 4 + k] = make_uint4(v[0], v[1], v[2], v[3]);
+                    for (int i = 0; i < 16; ++i) {
+                        const float a = __uint_as_float(rr[2 * i]), b = __uint_as_float(rr[2 * i + 1]);
+                        bad |= !(fabsf(a) < INFINITY) | !(fabsf(b) < INFINITY);
+                        v[i] = Elem<T>::pack(a * inv, b * inv);
                     }
+                    store_64_bytes(dst + c * 32, v);
                 }
             }
             if (p.lse && qi < mk.Sq)

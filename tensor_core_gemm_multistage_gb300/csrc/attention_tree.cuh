@@ -585,6 +585,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                             for (int g8 = 0; g8 < 4; ++g8)
                                 if (!(exists >> ((c * 32 + g8 * 8) / p.piece) & 1u)) vis &= ~(0xffu << (8 * g8));
                         }
+                        if (vis == 0xffffffffu) return;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (!(vis >> j & 1u)) rr[j] = hidden;
@@ -713,11 +714,10 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                         for (int j = 0; j < 8; ++j)
                             reinterpret_cast<float4*>(part)[c * 8 + j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
                     } else {
+uint32_t v[16];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            reinterpret_cast<uint4*>(row)[c * 4 + k] =
-                                make_uint4(Elem<T>::pack(y[8 * k], y[8 * k + 1]), Elem<T>::pack(y[8 * k + 2], y[8 * k + 3]),
-                                           Elem<T>::pack(y[8 * k + 4], y[8 * k + 5]), Elem<T>::pack(y[8 * k + 6], y[8 * k + 7]));
+                        for (int k = 0; k < 16; ++k) v[k] = Elem<T>::pack(y[2 * k], y[2 * k + 1]);
+                        store_64_bytes(row + c * 32, v);
                     }
                 }
                 if (real && it.slot >= 0 && (!turns || q == 0))

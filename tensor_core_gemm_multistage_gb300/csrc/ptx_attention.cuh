@@ -67,6 +67,23 @@ __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// 64 bytes of one thread to global memory: whole 32-byte sectors in two instructions where the address
+// allows it, else in four of 16 bytes.
+__device__ __forceinline__ void store_64_bytes(void* to, const uint32_t (&v)[16]) {
+    if ((reinterpret_cast<uintptr_t>(to) & 31u) == 0u) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<uint32_t*>(to) + i),
+                         "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]),
+                         "r"(v[i + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<uint4*>(static_cast<uint32_t*>(to) + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+}
+
 // Programmatic dependent launch: waits until the launches this one depends on have finished and their
 // writes are visible; lets the next one's CTAs start once every CTA has come here (or ended).
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
