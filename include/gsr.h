@@ -221,9 +221,8 @@ gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor
  *
  *   workspace  device pointer, 16-byte aligned, masked_attention_bwd_workspace(desc) bytes, for
  *              this call alone until it has finished; or NULL: one that the library keeps for the
- *              stream (grown after a wait for the stream, so not for a first call of its size in a
- *              capture; released by gsr_release_stream; graphs captured with it must not run at the
- *              same time as each other or as other calls on that stream).
+ *              stream (grown after a wait for the stream; released by gsr_release_stream).  In a
+ *              stream capture NULL gives GSR_ERR_INVALID_ARG: a graph has a workspace of its own.
  */
 int64_t masked_attention_bwd_workspace(const gsr_attention_desc* desc);
 gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor* dO, const gsr_tensor* Q,

@@ -37,7 +37,7 @@ constexpr float kPShift = Elem<T>::bf16 ? 0.0f : 12.0f;      // log2 of P's fact
 template <class T>
 __device__ __forceinline__ float ds_shift(const unsigned* norms) {
     if (Elem<T>::bf16) return 0.0f;
-    const float n = __uint_as_float(norms[0]) * __uint_as_float(norms[1]);   // squares of the bound's factors
+    const float n = __uint_as_float(__ldcg(norms)) * __uint_as_float(__ldcg(norms + 1));   // squares of the bound's factors
     if (!(n > 0.0f && n < INFINITY)) return 0.0f;
     return fminf(fmaxf(floorf(2.0f - 0.5f * log2f(n)), -100.0f), 100.0f);    // 15 - 12 - 1 - log2(bound / 2)
 }
@@ -140,10 +140,17 @@ __global__ void __launch_bounds__(256) gsr_masked_bwd_rows_kernel(const __grid_c
 #pragma unroll
         for (int n = 0; n < N; ++n) x[n] = row_piece<T>(p.V, b, h, j0 + n * AT_ONCE + sub, mk.Skv, piece);
         float most = 0.0f;
+        bool seen = true;                                // row j0 + lane: padding does not count
+        if (mk.num_docs > 0 && lane < kWarpRows) {
+            int first = 0, end = 0;
+            if (j0 + lane < mk.Skv) key_interval(mk, b, j0 + lane, first, end);
+            seen = first < end;
+        }
+        const unsigned rows_seen = __ballot_sync(0xffffffffu, seen);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const float q = lanes_sum<LANES>(dot8<T>(x[n], x[n]));
-            if (q < INFINITY) most = fmaxf(most, q);
+            if (q < INFINITY && (rows_seen >> (n * AT_ONCE + sub) & 1u)) most = fmaxf(most, q);
         }
         max_norm(p.norms + 1, most, lane);
     }
@@ -184,7 +191,7 @@ __device__ __noinline__ void row_dq(const MaskedBwdParams& p, int b, int h, int 
     const T* vb = static_cast<const T*>(p.V.data) + b * p.V.batch + hk * p.V.head;
     const float slope2 = p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
     const long long row = ((long long)b * mk.Hq + h) * p.Sp + i;
-    const float offset = p.offset[row], neg_delta = p.neg_delta[row];
+    const float offset = __ldcg(p.offset + row), neg_delta = __ldcg(p.neg_delta + row);
     int lo, hi;
     row_interval(mk, b, i, lo, hi);
     for (int j = lo; j < hi; ++j) {
@@ -218,7 +225,8 @@ __device__ __noinline__ void row_dkv(const MaskedBwdParams& p, int b, int hk, in
             load_row<T, D>(qb + i * p.Q.row, lane, q);
             load_row<T, D>(ob + i * p.dO.row, lane, dO);
             float P, dS;
-            pair_grad<T, D>(p.score, slope2, i + mk.offset - j, q, k, dO, v, p.offset[row + i], p.neg_delta[row + i], P, dS);
+            pair_grad<T, D>(p.score, slope2, i + mk.offset - j, q, k, dO, v, __ldcg(p.offset + row + i),
+                            __ldcg(p.neg_delta + row + i), P, dS);
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) acc[e] = want_dk ? fmaf(dS, q[e], acc[e]) : fmaf(P, dO[e], acc[e]);
         }
@@ -1095,7 +1103,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const long long row = ((long long)it.b * mk.Hq + it.h) * p.Sp + qi;
             int lo = 0, hi = 0;
             if (qi < mk.Sq) row_interval(mk, it.b, qi, lo, hi);
-            const float off = p.offset[row] + shift, neg_delta = p.neg_delta[row];
+            const float off = __ldcg(p.offset + row) + shift, neg_delta = __ldcg(p.neg_delta + row);
             const float slope2 = kHasBias<Cfg::MODE> ? __ldg(p.score.slopes + it.h) * kLog2e : 0.0f;
             for (int t = it.t0; t < it.t1; ++t, ++n) {
                 const int k0 = t * kTile + half * 64;

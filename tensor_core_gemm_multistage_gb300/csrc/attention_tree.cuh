@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                         for (int j = 0; j < 8; ++j)
                             reinterpret_cast<float4*>(part)[c * 8 + j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
                     } else {
-uint32_t v[16];
+                        uint32_t v[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) v[k] = Elem<T>::pack(y[2 * k], y[2 * k + 1]);
                         store_64_bytes(row + c * 32, v);
@@ -756,7 +756,12 @@ __global__ void __launch_bounds__(kJoinThreads) gsr_tree_join_kernel(const __gri
     __shared__ float sm[WARPS > 1 ? WARPS : 1][D + 2];
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS;
     const long long id = (long long)blockIdx.x * ROWS + (threadIdx.x >> 5) / WARPS;
-    if (id >= (long long)p.total_q * p.Hq) return;
+    // Every CTA waits, also those without a row here: this launch then ends after the parts' launch, and
+    // whatever follows it on the stream begins after both.
+    if (id >= (long long)p.total_q * p.Hq) {
+        grid_wait();
+        return;
+    }
     const int n = (int)(id / p.Hq), h = (int)(id - (long long)n * p.Hq);
     int left = 0, right = p.B;                                   // first request that ends behind row n
     while (left < right) {
@@ -764,14 +769,13 @@ __global__ void __launch_bounds__(kJoinThreads) gsr_tree_join_kernel(const __gri
         if (__ldg(p.q_starts + mid + 1) <= n) left = mid + 1;
         else right = mid;
     }
-    if (left >= p.B) return;
-    const int b = left;
+    const int b = min(left, p.B - 1);
     const TreeRequest r = tree_request(p, b);
     const int t = n - r.start, hk = h / p.group;
-    if (t < 0 || t >= r.nodes) return;
     const int per_pass = p.tile_nodes * p.nq, pair = t / per_pass, in_pass = t - pair * per_pass;
     const int row = in_pass / p.tile_nodes * 128 + in_pass % p.tile_nodes * p.group + (h - hk * p.group);
     grid_wait();                                                 // the parts' launch has finished
+    if (left >= p.B || t < 0 || t >= r.nodes) return;            // a row of no request, or of a further node
     const long long U = p.unit_starts[p.B];
     const long long s = p.unit_starts[b] + ((long long)hk * r.q_pairs + pair) * r.key_tiles;
     if (U <= 0) return;

@@ -687,8 +687,12 @@ gsr_status error_word(int dev, cudaStream_t stream, int** err) {
 gsr_status stream_scratch(int dev, cudaStream_t stream, size_t bytes, void** scratch) {
     std::lock_guard<std::mutex> lock(g_mu);
     StreamState& s = g_streams[{dev, stream}];
+    cudaError_t e;
+    // A graph would keep the buffer's address, which a later, larger call frees.
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if ((e = cudaStreamIsCapturing(stream, &capture)) != cudaSuccess) return cuda_fail(e);
+    if (capture != cudaStreamCaptureStatusNone) return GSR_ERR_INVALID_ARG;
     if (bytes > s.scratch_bytes) {
-        cudaError_t e;
         // Earlier launches on this stream may still use the old buffer.
         if ((e = cudaStreamSynchronize(stream)) != cudaSuccess) return cuda_fail(e);
         cudaFree(s.scratch);

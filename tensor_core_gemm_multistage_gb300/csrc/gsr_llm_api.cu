@@ -19,11 +19,13 @@ std::mutex g_scratch_mu;
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 bool bad_size(int64_t n) { return n < 0 || n > INT_MAX; }
 constexpr int64_t kSms = 152;   // of a GB300, where sizes are planned without a device
-// The tensor maps' strides are below 2^40 bytes; no operand spans more than 2^60 elements.
+// The tensor maps' strides are below 2^40 bytes; offsets in bytes stay inside 62 bits.
 constexpr int64_t kMaxStride = ((int64_t)1 << 39) - 8;
+constexpr double kMaxSpan = 1152921504606846976.0;    // 2^60 elements
 
 // Checks a strided operand of `batch` x `heads` x `rows` x d elements and fills in `out`; a
-// dimension of one element has no stride.  Rows, heads and batches of an output lie apart.
+// dimension of one element has no stride.  Rows, heads and batches of an output lie apart: each
+// dimension steps over all of the one with the next smaller stride.
 gsr_status operand(const gsr_tensor* t, int64_t batch, int64_t heads, int64_t rows, int64_t d, bool output,
                    Strided* out) {
     if (!t) return GSR_ERR_INVALID_ARG;
@@ -33,11 +35,30 @@ gsr_status operand(const gsr_tensor* t, int64_t batch, int64_t heads, int64_t ro
     if (misaligned(t->data, 16)) return GSR_ERR_ALIGNMENT;
     const int64_t n[3] = {batch, heads, rows}, stride[3] = {t->stride_batch, t->stride_head, t->stride_row};
     long long* to[3] = {&out->batch, &out->head, &out->row};
+    double span = (double)d;
     for (int i = 0; i < 3; ++i) {
         if (n[i] == 1) continue;
-        if (stride[i] <= 0 || stride[i] > kMaxStride || (output && stride[i] < d)) return GSR_ERR_INVALID_ARG;
+        if (stride[i] <= 0 || stride[i] > kMaxStride) return GSR_ERR_INVALID_ARG;
         if (stride[i] & 7) return GSR_ERR_ALIGNMENT;
         *to[i] = stride[i];
+        span += (double)(n[i] - 1) * (double)stride[i];
+    }
+    if (span > kMaxSpan) return GSR_ERR_INVALID_ARG;
+    if (output) {
+        int64_t wide = d, below = 0;                   // elements that the dimensions of smaller strides span
+        for (int k = 0; k < 3; ++k) {
+            int next = -1;
+            for (int i = 0; i < 3; ++i)
+                if (n[i] > 1 && stride[i] > below && (next < 0 || stride[i] < stride[next])) next = i;
+            if (next < 0) {
+                for (int i = 0; i < 3; ++i) k += n[i] == 1;
+                if (k < 3) return GSR_ERR_INVALID_ARG;   // two of one stride
+                break;
+            }
+            below = stride[next];
+            if (below < wide) return GSR_ERR_INVALID_ARG;
+            wide += (n[next] - 1) * below;
+        }
     }
     return GSR_OK;
 }
@@ -52,6 +73,15 @@ Span span_of(const Strided& t, int64_t batch, int64_t heads, int64_t rows, int64
     return {lo, lo + (uintptr_t)(((batch - 1) * t.batch + (heads - 1) * t.head + (rows - 1) * t.row + d) * size)};
 }
 bool meet(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+Span words(const void* p, int64_t n) {      // of 4 bytes
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, p ? lo + (uintptr_t)n * 4 : lo};
+}
+// Whether what a call writes meets the arrays of its masks and scores.
+bool meets_masks(const Span& s, const gsr_attention_desc* d) {
+    return meet(s, words(d->alibi_slopes, d->heads_q)) || meet(s, words(d->doc_bounds, d->batch * (d->num_docs + 1))) ||
+           meet(s, words(d->prefix_lens, d->batch * (d->num_docs > 0 ? d->num_docs : 1)));
+}
 
 // Whether two 16-bit operands may share elements.  Views of one buffer that lie side by side in
 // each row of it (the parts of a fused projection: equal row strides, heads inside the row) do not.
@@ -80,7 +110,7 @@ gsr_status check_desc(const gsr_attention_desc* d) {
     if (d->dtype != GSR_F16 && d->dtype != GSR_BF16) return GSR_ERR_INVALID_ARG;
     if (d->heads_q > 0 && (d->heads_kv == 0 || d->heads_q % d->heads_kv)) return GSR_ERR_INVALID_ARG;
     if (bad_score(d->softmax_scale, d->softcap)) return GSR_ERR_INVALID_ARG;
-    if (d->seq_q > INT_MAX - 256 || d->seq_kv > INT_MAX - 256) return GSR_ERR_INVALID_ARG;
+    if (d->seq_q + d->seq_kv > INT_MAX - 512) return GSR_ERR_INVALID_ARG;      // positions are counted in int
     if ((d->num_docs > 0) != (d->doc_bounds != nullptr)) return GSR_ERR_INVALID_ARG;
     if (d->num_docs > 0 && d->seq_q != d->seq_kv) return GSR_ERR_INVALID_ARG;   // documents mask a row with itself
     if (d->prefix_lens && !d->causal) return GSR_ERR_INVALID_ARG;               // nothing for a prefix to add
@@ -289,16 +319,13 @@ gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor
         return s;
     if (B == 0 || Hq == 0 || Sq == 0) return GSR_OK;
     if (misaligned(lse, 4)) return GSR_ERR_ALIGNMENT;
+    const Span o = span_of(p.O, B, Hq, Sq, D, 2), l = words(lse, B * Hq * Sq);
     if (share(p.O, Hq, Sq, p.Q, Hq, Sq, B, D) || share(p.O, Hq, Sq, p.K, Hkv, Skv, B, D) ||
-        share(p.O, Hq, Sq, p.V, Hkv, Skv, B, D))
+        share(p.O, Hq, Sq, p.V, Hkv, Skv, B, D) || meets_masks(o, desc))
         return GSR_ERR_ALIAS;
-    if (lse) {
-        const uintptr_t l0 = reinterpret_cast<uintptr_t>(lse);
-        const Span l{l0, l0 + (uintptr_t)(B * Hq * Sq * 4)};
-        if (meet(l, span_of(p.Q, B, Hq, Sq, D, 2)) || meet(l, span_of(p.K, B, Hkv, Skv, D, 2)) ||
-            meet(l, span_of(p.V, B, Hkv, Skv, D, 2)) || meet(l, span_of(p.O, B, Hq, Sq, D, 2)))
-            return GSR_ERR_ALIAS;
-    }
+    if (lse && (meet(l, span_of(p.Q, B, Hq, Sq, D, 2)) || meet(l, span_of(p.K, B, Hkv, Skv, D, 2)) ||
+                meet(l, span_of(p.V, B, Hkv, Skv, D, 2)) || meet(l, o) || meets_masks(l, desc)))
+        return GSR_ERR_ALIAS;
     int dev = 0, sms = 0;
     if ((s = gsr::host::current_device(&dev, &sms)) != GSR_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -349,15 +376,15 @@ gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor
     if (workspace && workspace_bytes < w.total) return GSR_ERR_INVALID_ARG;
     if (misaligned(lse, 4) || misaligned(workspace, 16)) return GSR_ERR_ALIGNMENT;
     // outputs share elements with nothing; the workspace and lse lie apart from the operands
-    const uintptr_t w0 = reinterpret_cast<uintptr_t>(workspace), l0 = reinterpret_cast<uintptr_t>(lse);
-    const Span ws{w0, workspace ? w0 + (uintptr_t)w.total : w0}, ls{l0, lse ? l0 + (uintptr_t)(B * Hq * Sq * 4) : l0};
-    if (meet(ws, ls)) return GSR_ERR_ALIAS;
+    const Span ws = words(workspace, w.total / 4), ls = words(lse, B * Hq * Sq);
+    if (meet(ws, ls) || meets_masks(ws, desc)) return GSR_ERR_ALIAS;
     for (size_t i = 0; i < sizeof(all) / sizeof(all[0]); ++i) {
         const auto& a = all[i];
         const int64_t ah = a.q ? Hq : Hkv, ar = a.q ? Sq : Skv;
         const Span sa = span_of(*a.to, B, ah, ar, D, 2);
         if (meet(ws, sa) || (a.out && meet(ls, sa))) return GSR_ERR_ALIAS;
         if (!a.out) continue;
+        if (meets_masks(sa, desc)) return GSR_ERR_ALIAS;
         for (size_t j = 0; j < i; ++j) {
             const auto& b = all[j];
             if (share(*a.to, ah, ar, *b.to, b.q ? Hq : Hkv, b.q ? Sq : Skv, B, D)) return GSR_ERR_ALIAS;
@@ -431,8 +458,10 @@ gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gs
         return GSR_ERR_ALIAS;
     const TreePlan plan = tree_plan(d);
     if (workspace && workspace_bytes < plan.total) return GSR_ERR_INVALID_ARG;
-    const uintptr_t w0 = reinterpret_cast<uintptr_t>(workspace);
-    const Span ws{w0, workspace ? w0 + (uintptr_t)plan.total : w0};
+    const Span ws = words(workspace, plan.total / 4);
+    for (const Span& in : {words(kv_lens, d.batch), words(q_starts, d.batch + 1), words(parents, d.total_q),
+                           words(block_tables, d.batch * d.table_width), words(d.alibi_slopes, d.heads_q)})
+        if (meet(o, in) || meet(ws, in)) return GSR_ERR_ALIAS;
     if (meet(ws, o) || meet(ws, span_of(qs, 1, d.heads_q, d.total_q, d.head_dim, 2)) ||
         meet(ws, span_of(p.K, d.num_pages, d.heads_kv, d.page_size, d.head_dim, 2)) ||
         meet(ws, span_of(p.V, d.num_pages, d.heads_kv, d.page_size, d.head_dim, 2)))
@@ -506,7 +535,7 @@ gsr_status kv_block_tables(const int32_t* kv_lens, const int32_t* new_lens, cons
                            int64_t max_tokens, CUstream_st* stream) {
     for (int64_t n : {batch, table_width, page_size, num_free, max_tokens})
         if (bad_size(n)) return GSR_ERR_INVALID_ARG;
-    if (page_size == 0 || batch > gsr::kTablesMaxBatch) return GSR_ERR_INVALID_ARG;
+    if (page_size == 0 || batch > gsr::kTablesMaxBatch || batch * table_width > INT_MAX) return GSR_ERR_INVALID_ARG;
     if (!free_head || !free_head_out || !q_starts || !counts || (num_free > 0 && !free_blocks) ||
         (max_tokens > 0 && (!positions || !slots)) || (batch > 0 && (!kv_lens || !new_lens || !kv_lens_out)) ||
         (batch > 0 && table_width > 0 && !block_tables))
@@ -518,10 +547,7 @@ gsr_status kv_block_tables(const int32_t* kv_lens, const int32_t* new_lens, cons
     const Part in[] = {{kv_lens, batch}, {new_lens, batch}, {free_blocks, num_free}, {free_head, 1}};
     const Part out[] = {{block_tables, batch * table_width}, {kv_lens_out, batch}, {free_head_out, 1},
                         {q_starts, batch + 1}, {positions, max_tokens}, {slots, max_tokens}, {counts, 3}};
-    auto span = [](const Part& a) {
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(a.p);
-        return Span{lo, a.p ? lo + (uintptr_t)a.n * 4 : lo};
-    };
+    auto span = [](const Part& a) { return words(a.p, a.n); };
     for (const Part& a : in)
         if (misaligned(a.p, 4)) return GSR_ERR_ALIGNMENT;
     for (const Part& a : out)
@@ -562,9 +588,8 @@ gsr_status kv_cache_append(const gsr_tensor* K, const gsr_tensor* V, const int32
     if (misaligned(slots, 4)) return GSR_ERR_ALIGNMENT;
     const Span kc = span_of(p.Kc, num_pages, heads, page_size, head_dim, 2),
                vc = span_of(p.Vc, num_pages, heads, page_size, head_dim, 2);
-    const uintptr_t s0 = reinterpret_cast<uintptr_t>(slots);
     const Span others[] = {span_of(p.K, 1, heads, tokens, head_dim, 2), span_of(p.V, 1, heads, tokens, head_dim, 2),
-                           Span{s0, s0 + (uintptr_t)tokens * 4}};
+                           words(slots, tokens)};
     for (const Span& o : others)
         if (meet(kc, o) || meet(vc, o)) return GSR_ERR_ALIAS;
     if (num_pages > 0 && p.Kc.data == p.Vc.data) return GSR_ERR_ALIAS;

@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kTablesThreads) gsr_block_tables_kernel(const 
             pos = old_len + (n - start[r]);
             const int col = pos / p.page;
             int block = -1;
-            if (col < have) {
+            if (pos < 0) {                                       // more tokens than 2^31
+            } else if (col < have) {
                 block = p.table[(long long)r * p.table_width + col];     // in hand before the call: nothing writes it
             } else if (col < want) {
                 const int q = first[r] + (col - have);

@@ -106,13 +106,12 @@ def _vector(t, name, count, dtype, index):
 
 def _scratch(workspace, nbytes, index, stream):
     """A tensor to keep until the call returns, its address and its size: the caller's workspace; None
-    (the library's own for the current stream); or, in a capture and for an explicit stream, a new
-    one, so that no two graphs share it."""
+    (the library's own for the stream); or, in a capture, a new one from the graph's memory."""
     if workspace is not None:
         if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on cuda:%d" % index)
         return workspace, workspace.data_ptr() or None, workspace.numel() * workspace.element_size()
-    if stream is None and not torch.cuda.is_current_stream_capturing():
+    if not torch.cuda.is_current_stream_capturing():
         return None, None, 0
     nbytes = max(nbytes(), 16)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
@@ -175,8 +174,8 @@ def masked_attention_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, softmax_scale: float =
 
     dO, O and dQ are shaped as Q, dK and dV as K; masks and scores as in the forward call.
     ``workspace``: optional device buffer of masked_attention_bwd_workspace(...) bytes; without one
-    the library keeps one for the current stream, and a call with ``stream`` or inside a capture takes
-    one from PyTorch's allocator.
+    the library keeps one for the stream, and a call inside torch.cuda.graph takes one from the graph's
+    memory.
     """
     d, qs, ks, dev = _attention_desc(Q, K, softmax_scale, causal, softcap, alibi_slopes, doc_bounds, prefix_lens)
     dt, L = Q.dtype, lib()

@@ -268,6 +268,59 @@ def test_repeatable_and_on_two_streams_at_once():
     assert all(torch.equal(t.o, f) for t, f in zip(ts, first))
 
 
+@pytest.mark.parametrize("T", [1, 40])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(T):
+    t = Tree(kv=[900, 200], T=[T, T], Hq=8, Hkv=2, D=64, page=16).run()
+    gsr.set_wait_timeout_ns(50_000_000)
+    gsr.set_test_flags(1)                          # the first query tile is never copied
+    try:
+        gsr.tree_attention_fwd(*t.args, **t.kw)
+        status, code = gsr.device_status()
+    finally:
+        gsr.set_test_flags(0)
+        gsr.set_wait_timeout_ns(1_000_000_000)
+    assert status == gsr.Status.ERR_DEVICE_TIMEOUT and code & 0xF00 == 0x700
+    t.run().check()
+
+
+def test_workspaces():
+    t = Tree(kv=[3000, 77], T=[1, 9], Hq=8, Hkv=2, D=128, page=16).run().check()
+    want = t.o.clone()
+    size = gsr.tree_attention_workspace(2, t.N, 8, 2, 128, t.kc.shape[0], 16, t.table.shape[1], t.max_nodes)
+    own = torch.full((size + 64,), 255, dtype=torch.uint8, device=DEV)
+    assert torch.equal(t.run(workspace=own[:size]).o, want) and torch.all(own[size:] == 255)
+    s = torch.cuda.Stream(DEV)
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(2):
+        t.o.fill_(7.0)
+        torch.cuda.synchronize()
+        gsr.tree_attention_fwd(*t.args, **t.kw, stream=s)
+        assert gsr.device_status(s)[0] == gsr.Status.OK and torch.equal(t.o, want)
+        gsr.release_stream(s)
+    with pytest.raises(gsr.GsrError):
+        t.run(workspace=own[:size - 16])
+
+
+def test_a_cache_past_32_bits():
+    """The last pages of a cache of more than 2^31 elements: written and read as in a small one."""
+    t = Tree(kv=[150, 61], T=[3, 1], Hq=8, Hkv=8, D=128, page=16, dtype=BF16).run().check()
+    want, pool = t.o.clone(), t.kc.shape[0]
+    pages = 2 ** 31 // (16 * 8 * 128) + pool
+    kc, vc = (torch.empty(pages, 16, 8, 128, dtype=BF16, device=DEV) for _ in range(2))
+    k, v = (x.reshape(-1, 8, 128) for x in (t.kc, t.vc))
+    first = pages - pool
+    gsr.kv_cache_append(k, v, torch.arange(first * 16, pages * 16, dtype=torch.int32, device=DEV), kc, vc)
+    assert torch.equal(kc[first:], t.kc) and torch.equal(vc[first:], t.vc)
+    t.kc, t.vc = kc, vc
+    t.table[t.table >= 0] += first
+    assert torch.equal(t.run().o, want)
+
+
+def test_rows_of_no_request():
+    t = Tree(kv=[40, 9], T=[0, 0], Hq=4, Hkv=2, D=64, page=16, extra_rows=6).run()
+    assert torch.all(t.o == 7.0)
+
+
 # ---------------------------------------------------------------------------- the path together
 
 @pytest.mark.parametrize("captured", [False, True])

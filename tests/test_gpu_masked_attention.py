@@ -307,3 +307,149 @@ def test_two_captured_graphs_replayed_at_once():
     torch.cuda.synchronize()
     for c, want in zip(cases, first):
         assert all(torch.equal(a, b) for a, b in zip((c.o, *c.grads), want))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_padding_values_do_not_reach_the_gradients_scale(dtype):
+    # large finite values where nothing looks: not a bit of the result changes
+    c = Case(1, 4, 2, 300, 300, 64, dtype=dtype, docs=[[10, 100, 290]], causal=True)
+    pads = (slice(0, 10), slice(290, 300))
+    for value in (0.0, 60000.0):
+        for rows in pads:
+            for t in (c.q, c.k, c.v, c.do):
+                t[:, :, rows] = value
+        c.forward().check_forward().backward().check_backward()
+        got = [t.clone() for t in (c.o, *c.grads)]
+        if value:
+            assert all(torch.equal(a, b) for a, b in zip(got, first))
+        first = got
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("backward", [False, True])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(D, backward):
+    c = Case(1, 2, 1, 700, 700, D, causal=True).forward()
+    gsr.set_wait_timeout_ns(50_000_000)
+    gsr.set_test_flags(1)                          # each kernel's first copy is never made
+    try:
+        if backward:
+            gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *(torch.empty_like(t) for t in (c.q, c.k, c.v)), **c.kw)
+        else:
+            gsr.masked_attention_fwd(c.q, c.k, c.v, torch.empty_like(c.o), None, **c.kw)
+        status, code = gsr.device_status()
+    finally:
+        gsr.set_test_flags(0)
+        gsr.set_wait_timeout_ns(1_000_000_000)
+    assert status == gsr.Status.ERR_DEVICE_TIMEOUT and code & 0xF00 in ((0x500, 0x600) if backward else (0x400,))
+    c.check()
+
+
+def test_workspaces():
+    """The caller's, the library's of two streams, one that grows, one released: the same gradients."""
+    c = Case(1, 8, 2, 500, 500, 64, causal=True).forward().backward()
+    want = [t.clone() for t in c.grads]
+
+    def run(**kw):
+        for t in c.grads:
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *c.grads, **c.kw, **kw)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(c.grads, want))
+
+    size = gsr.masked_attention_bwd_workspace(1, 8, 2, 500, 500, 64)
+    own = torch.full((max(size, 2 ** 24) + 64,), 255, dtype=torch.uint8, device=DEV)     # NaN everywhere
+    run(workspace=own[:size])
+    s = torch.cuda.Stream(DEV)
+    run(workspace=own[:2 ** 24], stream=s)
+    assert torch.all(own[2 ** 24:] == 255)
+    run(stream=s)
+    big = Case(2, 8, 2, 900, 900, 128).forward()
+    gsr.masked_attention_bwd(big.do, big.q, big.k, big.v, big.o, big.lse, *(torch.empty_like(t) for t in (big.q, big.k, big.v)),
+                             stream=s)
+    run(stream=s)
+    gsr.release_stream(s)
+    run(stream=s)
+    with pytest.raises(gsr.GsrError):
+        run(workspace=own[:size - 256])
+
+
+def test_a_capture_needs_a_workspace_of_its_own():
+    # through the C interface NULL is refused, since the library's may be freed under the graph; the
+    # capture goes on
+    from tensor_core_gemm_multistage_gb300 import llm as L
+    c = Case(1, 4, 2, 300, 300, 64, causal=True).forward().backward()
+    want = [t.clone() for t in c.grads]
+    d, qs, ks, dev = L._attention_desc(c.q, c.k, 0.0, True, 0.0, None, None, None)
+    q, k = (lambda t: L._operand(t, "t", qs, t.dtype, dev)), (lambda t: L._operand(t, "t", ks, t.dtype, dev))
+    side = torch.cuda.Stream(DEV)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *c.grads, **c.kw)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        s = gsr.lib().masked_attention_bwd(d, q(c.do), q(c.q), k(c.k), k(c.v), q(c.o), c.lse.data_ptr(), q(c.grads[0]),
+                                           k(c.grads[1]), k(c.grads[2]), None, 0, side.cuda_stream)
+        gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *c.grads, **c.kw)
+    assert s == gsr.Status.ERR_INVALID_ARG
+    for t in c.grads:
+        t.fill_(float("nan"))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(c.grads, want))
+
+
+def test_threads_on_one_stream():
+    """Two threads' backward calls on one stream share its workspace: each call's launches stay together."""
+    import threading
+    cases = [Case(1, 4, 2, 600, 600, 64, causal=True, seed=5), Case(1, 4, 4, 333, 333, 128, seed=6, dtype=BF16)]
+    for c in cases:
+        c.forward().backward()
+    want = [[t.clone() for t in c.grads] for c in cases]
+    wrong = []
+
+    def loop(c, w):
+        try:
+            for _ in range(20):
+                grads = [torch.full_like(t, float("nan")) for t in c.grads]
+                gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *grads, **c.kw)
+                wrong.extend(not torch.equal(a, b) for a, b in zip(grads, w))
+        except Exception as e:
+            wrong.append(e)
+
+    threads = [threading.Thread(target=loop, args=a) for a in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(wrong) == 120 and not any(wrong), wrong
+
+
+def test_offsets_past_32_bits():
+    """A batch row 2^31 elements behind the first, all operands the parts of one buffer: the results of
+    dense copies."""
+    B, H, S, D, parts = 2, 2, 260, 64, 8
+    pitch = parts * H * D
+    step = (2 ** 31 // pitch + 1) * pitch
+    buf = torch.empty(step + S * pitch, dtype=F16, device=DEV)
+    view = lambda i: buf.as_strided((B, H, S, D), (step, D, pitch, 1), i * H * D)
+    c = Case(B, H, H, S, S, D, causal=True).forward().backward()
+    q, k, v, do, o, dq, dk, dv = (view(i) for i in range(parts))
+    for to, t in ((q, c.q), (k, c.k), (v, c.v), (do, c.do)):
+        to.copy_(t)
+    lse = torch.empty_like(c.lse)
+    gsr.masked_attention_fwd(q, k, v, o, lse, **c.kw)
+    gsr.masked_attention_bwd(do, q, k, v, o, lse, dq, dk, dv, **c.kw)
+    assert torch.equal(lse, c.lse)
+    for a, b in zip((o, dq, dk, dv), (c.o, *c.grads)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,scale", [(F16, 0.3), (BF16, 0.3)])
+def test_capped_scores_large_and_small(dtype, scale):
+    # rows whose scores stay far below the cap next to rows far beyond it, in one tile
+    c = Case(1, 2, 1, 300, 300, 64, cap=4.0, scale=scale, dtype=dtype, causal=True)
+    c.q[:, :, ::3] *= 0.01
+    c.q[:, :, 1::7] *= 8
+    c.check()

@@ -152,6 +152,32 @@ def test_append_refusals():
     assert append(tokens=0) == OK
 
 
+def test_outputs_that_overlap_themselves():
+    assert fwd(O=_Tensor(4 * GB, 25600, 64, 64)) == INVALID            # heads on rows
+    assert fwd(O=_Tensor(4 * GB, 25600, 64, 128)) == INVALID           # four heads in rows of two
+    assert fwd(O=_Tensor(4 * GB, 6400, 6400, 64)) == INVALID           # batches on heads
+    assert bwd(dK=_Tensor(7 * GB, 12800, 6336, 64)) == INVALID         # a head's last row on the next head's first
+    assert append(kc=_Tensor(3 * GB, 1024, 64, 128)) == INVALID        # pages of 16 rows every 8 rows
+
+
+def test_spans_and_positions_that_are_too_large():
+    assert fwd(dict(batch=2 ** 22, heads_q=1, heads_kv=1), Q=_Tensor(1 * GB, 2 ** 39 - 8, 64, 64)) == INVALID
+    assert fwd(dict(batch=1, heads_q=1, heads_kv=1, seq_q=2 ** 30, seq_kv=2 ** 30)) == INVALID
+    assert tree(dict(num_pages=2 ** 23), k=_Tensor(2 * GB, 2 ** 38, 64, 128)) == INVALID
+    assert fwd(dict(softcap=1025.0)) == INVALID and tree(dict(softcap=1025.0)) == INVALID
+    # neither pages nor heads lie a multiple of 8 rows apart
+    assert tree(k=_Tensor(2 * GB, 2056, 64, 128)) == INVALID
+    assert tables(B=8192, W=2 ** 19) == INVALID
+
+
+def test_masks_and_lengths_in_the_way_of_outputs():
+    assert fwd(dict(alibi_slopes=4 * GB)) == ALIAS and fwd(dict(prefix_lens=4 * GB + 64)) == ALIAS
+    assert fwd(dict(doc_bounds=9 * GB, num_docs=3), lse=9 * GB + 16) == ALIAS
+    assert bwd(dict(alibi_slopes=6 * GB)) == ALIAS and bwd(dict(prefix_lens=10 * GB)) == ALIAS
+    assert tree(lens=4 * GB) == ALIAS and tree(starts=4 * GB) == ALIAS and tree(parents=4 * GB) == ALIAS
+    assert tree(table=10 * GB) == ALIAS and tree(dict(alibi_slopes=10 * GB)) == ALIAS
+
+
 def test_binding_refusals():
     import torch
     t = torch.zeros(1, 2, 4, 64, dtype=torch.float16)
