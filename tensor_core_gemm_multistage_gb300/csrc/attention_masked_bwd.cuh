@@ -841,7 +841,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 //     S = Q K^T,  dP = dO V^T,  dS over dP's columns,  dQ += dS K
 // S has one region (the arithmetic takes it into registers at once) and dP two, so that S(n+1) and
 // dP(n+1) run on the tensor core while dS(n) is computed; dQ(n) follows.  K is read by S(n) and,
-// after that, by dQ(n): three ring entries, two for V.
+// after that, by dQ(n): three ring entries, two for V.  dS(n+1) may be there before the issuing lane
+// looks for dS(n), so the two have a barrier each (on one, its phase would be back where it was).
 template <class T_, int D_, int MODE_>
 struct DqCfg {
     using T = T_;
@@ -886,8 +887,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     auto dp_full = [&](int s) { return bar(10 + s); };
     auto item_pub = [&](int i) { return bar(12 + i); };
     auto item_read = [&](int i) { return bar(14 + i); };
-    const uint32_t q_full = bar(16), q_empty = bar(17), s_full = bar(18), s_read = bar(19), ds_full = bar(20),
-                   done = bar(21), clc = bar(22), drain = bar(23);
+    auto ds_full = [&](int s) { return bar(16 + s); };
+    const uint32_t q_full = bar(18), q_empty = bar(19), s_full = bar(20), s_read = bar(21), done = bar(22), clc = bar(23),
+                   drain = bar(24);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_MISC + 4);
     volatile int* item_box = reinterpret_cast<volatile int*>(smem + Cfg::OFF_ITEM);
@@ -911,6 +913,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             mbar_init(v_full(s), 1);
             mbar_init(v_empty(s), 1);
             mbar_init(dp_full(s), 1);
+            mbar_init(ds_full(s), kBwdMathWarps);
             mbar_init(item_pub(s), 1);
             mbar_init(item_read(s), 1 + kBwdMathWarps);
         }
@@ -918,7 +921,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         mbar_init(q_empty, 1);
         mbar_init(s_full, 1);
         mbar_init(s_read, kBwdMathWarps);
-        mbar_init(ds_full, kBwdMathWarps);
         mbar_init(done, 1);
         mbar_init(clc, 1);
         mbar_init(drain, 1);
@@ -1065,7 +1067,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     if (!(ok = issue_scores(n, n == 0))) break;
                     for (int i = 0; i < steps; ++i, ++n) {
                         if (i + 1 < steps && !(ok = issue_scores(n + 1, false))) break;
-                        if (!(ok = w.wait(ds_full, n & 1u, kDevErrMmaFull))) break;
+                        if (!(ok = w.wait(ds_full((int)(n & 1u)), (n >> 1) & 1u, kDevErrMmaFull))) break;
                         tcgen05_fence_after();
                         mma_overlay(tmem_base + Cfg::T_DQ, tmem_base + Cfg::T_DP + (n & 1u) * 128,
                                     sb + Cfg::OFF_K + (n % NK) * Cfg::TILE_BYTES, Cfg::IDESC_ACC, i > 0);
@@ -1157,7 +1159,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 tmem_st_wait();
                 tcgen05_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(ds_full);
+                if (lane == 0) mbar_arrive(ds_full(buf));
             }
             if (!ok) break;
             const bool none = it.t0 >= it.t1;

@@ -138,7 +138,7 @@ struct TreeCfg {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = OFF_Q + NQ * TILE_BYTES;
     static constexpr int OFF_BAR = OFF_RING + NB * TILE_BYTES;
-    static constexpr int NUM_BARS = 2 * NB + 15;
+    static constexpr int NUM_BARS = 2 * NB + 17;
     static constexpr int OFF_VALID = OFF_BAR + NUM_BARS * 8;       // per ring entry: which pieces of the tile exist
     static constexpr int OFF_ITEM = OFF_VALID + NB * 4;            // 2 x 12 ints
     static constexpr int OFF_SCAN = (OFF_ITEM + 96 + 7) / 8 * 8;   // 16 partial sums, then the CTA's first unit
@@ -187,11 +187,13 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
     auto empty = [&](int s) { return bar(NB + s); };
     auto sfull = [&](int i) { return bar(2 * NB + i); };        // per S region
     auto pfull = [&](int i) { return bar(2 * NB + 2 + i); };
-    auto odone = [&](int q) { return bar(2 * NB + 4 + q); };
-    auto item_pub = [&](int i) { return bar(2 * NB + 6 + i); };
-    auto item_read = [&](int i) { return bar(2 * NB + 8 + i); };
-    const uint32_t q_full = bar(2 * NB + 10), q_free = bar(2 * NB + 11), drain = bar(2 * NB + 12), ml_full = bar(2 * NB + 13),
-                   ml_free = bar(2 * NB + 14);
+    // per softmax group and parity of the item: a group without a key tile of its own (an item of one) holds
+    // nothing up, and the next item's products may be done before it looks
+    auto odone = [&](int q, uint32_t item) { return bar(2 * NB + 4 + 2 * q + (int)(item & 1u)); };
+    auto item_pub = [&](int i) { return bar(2 * NB + 8 + i); };
+    auto item_read = [&](int i) { return bar(2 * NB + 10 + i); };
+    const uint32_t q_full = bar(2 * NB + 12), q_free = bar(2 * NB + 13), drain = bar(2 * NB + 14), ml_full = bar(2 * NB + 15),
+                   ml_free = bar(2 * NB + 16);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_MISC + 4);
     volatile int* item_box = reinterpret_cast<volatile int*>(smem + Cfg::OFF_ITEM);
@@ -220,7 +222,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(sfull(s), 1);
             mbar_init(pfull(s), 128);
-            mbar_init(odone(s), 1);
+            mbar_init(odone(s, 0), 1);
+            mbar_init(odone(s, 1), 1);
             mbar_init(item_pub(s), 1);
             mbar_init(item_read(s), 1 + Cfg::SM_THREADS / 32);
         }
@@ -464,8 +467,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                                 if (!(ok = wait_full(2 * m + 1) && issue_pv(g, g, m, i <= 2))) break;
                                 mma_commit(empty((int)((2 * m + 1) % NB)));
                                 if (i == steps) {
-                                    mma_commit(odone(0));
-                                    mma_commit(odone(1));
+                                    mma_commit(odone(0, n_item - 1));
+                                    mma_commit(odone(1, n_item - 1));
                                 }
                             }
                         } else {
@@ -475,7 +478,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                             for (int q = 0; q < 2 && ok; ++q) {
                                 if (i > 0) {
                                     if (!(ok = issue_pv(q, q, n + i - 1, i == 1))) break;
-                                    if (i == steps) mma_commit(odone(q));
+                                    if (i == steps) mma_commit(odone(q, n_item - 1));
                                 }
                                 if (i < steps) issue_s(q, q, n + i);
                             }
@@ -667,7 +670,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ml_full);
             }
-            if (!(ok = __all_sync(0xffffffffu, w.wait(odone(q), (n_item - 1) & 1u, kDevErrEpilogueFull)))) break;
+            if (!(ok = __all_sync(0xffffffffu, w.wait(odone(q, n_item - 1), ((n_item - 1) >> 1) & 1u, kDevErrEpilogueFull)))) break;
             float f0 = 1.0f, f1 = 0.0f;                  // factors of the two accumulators
             if (turns) {
                 if (!(ok = __all_sync(0xffffffffu, w.wait(ml_full, n_ml & 1u, kDevErrEpilogueFull)))) break;

@@ -453,3 +453,16 @@ def test_capped_scores_large_and_small(dtype, scale):
     c.q[:, :, ::3] *= 0.01
     c.q[:, :, 1::7] *= 8
     c.check()
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (128, F16)])
+def test_many_backward_calls_finish_alike(D, dtype):
+    # hundreds of launches next to one another: every wait ends, and no result depends on who was first
+    c = Case(4, 16, 8, 1024, 1024, D, dtype=dtype, causal=True).forward().backward()
+    want = [t.clone() for t in c.grads]
+    for _ in range(10):
+        for _ in range(60):
+            gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *c.grads, **c.kw)
+        status, code = gsr.device_status()
+        assert status == gsr.Status.OK, hex(code)
+        assert all(torch.equal(a, b) for a, b in zip(c.grads, want))
