@@ -113,6 +113,12 @@ __device__ __forceinline__ void key_interval(const MaskArgs& m, int b, int j, in
     end = max(end, first);
 }
 
+// Bits [from, to) of 32.
+__device__ __forceinline__ uint32_t between(int from, int to) {
+    auto below = [](int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
+    return below(to) & ~below(from);
+}
+
 // ---------------------------------------------------------------------------
 // Scores
 // ---------------------------------------------------------------------------

@@ -348,9 +348,10 @@ __device__ __forceinline__ void mma_overlay(uint32_t d, uint32_t a, uint32_t b, 
 template <class T, int D>
 __device__ __forceinline__ bool store_accumulator(uint32_t col, float factor, bool zero, bool write, T* row) {
     bool bad = false;
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {                   // one copy of the code: it runs cold, once an item
         uint32_t rr[32];
+        __syncwarp();                                    // whole warps at the TMEM accesses
         tmem_ld_32x32b_x32(col + c * 32, rr);
         tmem_ld_wait(rr);
         if (zero) {
@@ -706,7 +707,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 }
                 const float slope2 = kHasBias<Cfg::MODE> ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
                 const int i0 = t * kTile + half * 64;
-                const bool masked = i0 < first || i0 + 64 > end;
+                const bool masked = __any_sync(0xffffffffu, i0 < first || i0 + 64 > end);
                 if (!__all_sync(0xffffffffu, w.wait(o_full((int)(n % NO)), (n / NO) & 1u, kDevErrEpilogueFull) &&
                                                  w.wait(s_full, n & 1u, kDevErrEpilogueFull))) {
                     ok = false;
@@ -726,9 +727,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                                       [&](int i) { return *reinterpret_cast<const float2*>(rows + c * 32 + i); },
                                                       packed);
                     if (masked) {
+                        const uint32_t vis = between(first - i0 - c * 32, end - i0 - c * 32);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (c * 32 + i < first - i0 || c * 32 + i >= end - i0) {
+                            if (!(vis >> i & 1u)) {
                                 rr[i] = 0u;
                                 packed[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
                             }
@@ -771,9 +773,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         packed[i / 2] = Elem<T>::pack(d0, d1);
                     }
                     if (masked) {
+                        const uint32_t vis = between(first - i0 - c * 32, end - i0 - c * 32);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (c * 32 + i < first - i0 || c * 32 + i >= end - i0) packed[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+                            if (!(vis >> i & 1u)) packed[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
                     }
                     tmem_st_32x32b_x16(dp_col + c * 16, packed);
                 };
@@ -801,6 +804,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t rr[32];
+                    __syncwarp();
                     tmem_ld_32x32b_x32(col + c * 32, rr);
                     tmem_ld_wait(rr);
                     if (j < mk.Skv) {
@@ -1109,7 +1113,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const float slope2 = kHasBias<Cfg::MODE> ? __ldg(p.score.slopes + it.h) * kLog2e : 0.0f;
             for (int t = it.t0; t < it.t1; ++t, ++n) {
                 const int k0 = t * kTile + half * 64;
-                const bool masked = k0 < lo || k0 + 64 > hi;
+                const bool masked = __any_sync(0xffffffffu, k0 < lo || k0 + 64 > hi);
                 if (!__all_sync(0xffffffffu, w.wait(s_full, n & 1u, kDevErrEpilogueFull))) {
                     ok = false;
                     break;
@@ -1146,11 +1150,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         float d0 = __uint_as_float(dp[i]), d1 = __uint_as_float(dp[i + 1]);
                         fadd2(d0, d1, neg_delta, neg_delta);
                         fmul2(d0, d1, d0, d1, __uint_as_float(ww[i]), __uint_as_float(ww[i + 1]));
-                        if (masked) {
-                            if (c * 32 + i < lo - k0 || c * 32 + i >= hi - k0) d0 = 0.0f;
-                            if (c * 32 + i + 1 < lo - k0 || c * 32 + i + 1 >= hi - k0) d1 = 0.0f;
-                        }
                         packed[i / 2] = Elem<T>::pack(d0, d1);
+                    }
+                    if (masked) {
+                        const uint32_t vis = between(lo - k0 - c * 32, hi - k0 - c * 32);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(vis >> i & 1u)) packed[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
                     }
                     tmem_st_32x32b_x16(dp_col + c * 16, packed);
                 };

@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                 ++s_n;
                 tcgen05_fence_after();
                 const int k0 = it.key_tile(t) * Cfg::BKV;
-                const bool masked = k0 < lo || k0 + Cfg::BKV > hi;
+                const bool masked = __any_sync(0xffffffffu, k0 < lo || k0 + Cfg::BKV > hi);
                 uint32_t sc0[32], sc1[32], sc2[32], sc3[32];
                 tmem_ld_32x32b_x32(s_col + 0, sc0);
                 tmem_ld_32x32b_x32(s_col + 32, sc1);
@@ -442,11 +442,11 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                 if (masked) {
                     // of a boundary tile's four chunks few hold the boundary, and the warp's rows share it
                     auto hide = [&](uint32_t (&rr)[32], int c) {
-                        const int from = lo - k0 - c * 32, to = hi - k0 - c * 32;
-                        if (from <= 0 && to >= 32) return;
+                        const uint32_t vis = between(lo - k0 - c * 32, hi - k0 - c * 32);
+                        if (__all_sync(0xffffffffu, vis == 0xffffffffu)) return;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (i < from || i >= to) rr[i] = hidden;
+                            if (!(vis >> i & 1u)) rr[i] = hidden;
                     };
                     hide(sc0, 0);
                     hide(sc1, 1);
@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                     }
                     tmem_st_32x32b_x16(s_col + Cfg::P_COL + c * 16, packed);
                 };
+                __syncwarp();                    // whole warps at the TMEM accesses
                 chunk_p(sc0, 0);
                 chunk_p(sc1, 1);
                 chunk_p(sc2, 2);
@@ -516,9 +517,10 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
             bool bad = !(l < INFINITY);          // l or an element of O is infinite or NaN
             T* dst = static_cast<T*>(p.O.data) + it.b * p.O.batch + it.h * p.O.head + (long long)qi * p.O.row;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {   // one copy of the code: it runs cold, once an item
                 uint32_t rr[32];
+                __syncwarp();
                 if (t0 < t1) {
                     tmem_ld_32x32b_x32(o_col + c * 32, rr);
                     tmem_ld_wait(rr);

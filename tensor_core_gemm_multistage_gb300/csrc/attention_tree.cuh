@@ -620,6 +620,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                         }
                         tmem_st_32x32b_x16(s_col + Cfg::P_COL + c * 16, packed);
                     };
+                    __syncwarp();                        // whole warps at the TMEM accesses
                     chunk_p(sc0, 0);
                     chunk_p(sc1, 1);
                     chunk_p(sc2, 2);
@@ -697,8 +698,10 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                 const uint32_t o0 = turns ? lane_base + Cfg::T_O : o_col, o1 = lane_base + Cfg::T_O + D;
                 T* row = static_cast<T*>(p.O) + (long long)(it.start + node) * p.o_row + h * p.o_head;
                 float* part = it.slot < 0 ? nullptr : part_o(p, it.slot, (turns ? 0 : q * 128) + rq, D);
+#pragma unroll 1
                 for (int c = c_first; c < c_end; ++c) {
                     uint32_t r0[32], r1[32];
+                    __syncwarp();
                     tmem_ld_32x32b_x32(o0 + c * 32, r0);
                     if (turns && steps > 1) tmem_ld_32x32b_x32(o1 + c * 32, r1);
                     tmem_ld_wait(r0);
