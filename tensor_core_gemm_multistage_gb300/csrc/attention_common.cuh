@@ -400,6 +400,16 @@ __device__ __forceinline__ float score_of(float s, const ScoreArgs& sc, float& g
     return sc.cap_out * (1.0f - 2.0f * r);
 }
 
+// Whether a row's sum is NaN in every element, and so stays it: rows are computed again because they
+// are not finite, and where that is the result itself (a NaN in the query, say) the first keys tell.
+template <int N>
+__device__ __forceinline__ bool all_nan(const float (&acc)[N]) {
+    bool nan = true;
+#pragma unroll
+    for (int i = 0; i < N; ++i) nan &= acc[i] != acc[i];
+    return __all_sync(0xffffffffu, nan);
+}
+
 // Softmax-weighted sum of the values of keys [lo, hi) that `at` lets the row see, in one pass with
 // the running maximum m and sum l.  at(j, k, v, dist) gives key j's rows and its distance.
 template <class T, int D, class At>
@@ -424,6 +434,7 @@ __device__ __forceinline__ void row_forward(const float (&q)[D / 32], int lo, in
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(acc[i], f, p * x[i]);
         m = mn;
+        if (l != l || all_nan(acc)) break;
     }
 }
 

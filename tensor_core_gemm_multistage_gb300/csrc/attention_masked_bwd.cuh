@@ -201,6 +201,7 @@ __device__ __noinline__ void row_dq(const MaskedBwdParams& p, int b, int h, int 
         pair_grad<T, D>(p.score, slope2, i + mk.offset - j, q, k, dO, v, offset, neg_delta, P, dS);
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(dS, k[e], acc[e]);
+        if (all_nan(acc)) break;
     }
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] *= p.score.scale;
@@ -216,7 +217,7 @@ __device__ __noinline__ void row_dkv(const MaskedBwdParams& p, int b, int hk, in
     load_row<T, D>(static_cast<const T*>(p.V.data) + b * p.V.batch + hk * p.V.head + j * p.V.row, lane, v);
     int first, end;
     key_interval(mk, b, j, first, end);
-    for (int h = hk * mk.group; h < (hk + 1) * mk.group; ++h) {
+    for (int h = hk * mk.group; h < (hk + 1) * mk.group && !all_nan(acc); ++h) {
         const T* qb = static_cast<const T*>(p.Q.data) + b * p.Q.batch + h * p.Q.head;
         const T* ob = static_cast<const T*>(p.dO.data) + b * p.dO.batch + h * p.dO.head;
         const float slope2 = p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
@@ -229,6 +230,7 @@ __device__ __noinline__ void row_dkv(const MaskedBwdParams& p, int b, int hk, in
                             __ldcg(p.neg_delta + row + i), P, dS);
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) acc[e] = want_dk ? fmaf(dS, q[e], acc[e]) : fmaf(P, dO[e], acc[e]);
+            if (all_nan(acc)) break;
         }
     }
     if (want_dk) {

@@ -466,3 +466,21 @@ def test_many_backward_calls_finish_alike(D, dtype):
         status, code = gsr.device_status()
         assert status == gsr.Status.OK, hex(code)
         assert all(torch.equal(a, b) for a, b in zip(c.grads, want))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_everywhere_is_not_slow(D):
+    # rows that are NaN by themselves are not computed key by key: no wait of 0.1 s runs out
+    S = 32768
+    q, k, v, do = (torch.full((1, 1, S, D), float("nan"), dtype=BF16, device=DEV) for _ in range(4))
+    o, lse = torch.zeros_like(q), torch.zeros(1, 1, S, device=DEV)
+    grads = [torch.zeros_like(q) for _ in range(3)]
+    gsr.set_wait_timeout_ns(100_000_000)
+    try:
+        gsr.masked_attention_fwd(q, k, v, o, lse, causal=True)
+        gsr.masked_attention_bwd(do, q, k, v, o, lse, *grads, causal=True)
+        status, code = gsr.device_status()
+    finally:
+        gsr.set_wait_timeout_ns(1_000_000_000)
+    assert status == gsr.Status.OK, hex(code)
+    assert all(torch.isnan(t).all() for t in (o, lse, *grads))
