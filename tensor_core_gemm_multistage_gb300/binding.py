@@ -314,8 +314,8 @@ def gemm_scale_relu_host(hA, hB, hC, dA, dB, dC, alpha: float, stream=None):
 
 
 def release_stream(stream=None, device=None):
-    """Frees the library's error word and small-M workspace of ``stream`` (after waiting
-    for it); a later call on the stream allocates afresh."""
+    """Frees the library's error word and workspaces of ``stream`` (after waiting for it); a later
+    call on the stream allocates afresh."""
     import torch
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(dev):

@@ -8,10 +8,12 @@
 // dK and dV of a key/value head sum over the query heads of its group.
 //
 // Three launches: one pass over the rows (delta), then dK and dV by the CTA that owns the keys and
-// dQ by the CTA that owns the queries.  The two recompute S and dP, seven products of
-// 128 x 128 x D instead of the five that one pass with atomically added dQ would take; in return
-// no result depends on the order of atomics, dQ needs no fp32 buffer, and every accumulator stays
-// in TMEM from the first product to the last.
+// dQ by the CTA that owns the queries (and a fourth where dK and dV are cut into parts).  The two
+// recompute S and dP, seven products of 128 x 128 x D instead of the five that one pass with atomically
+// added dQ would take; in return no result depends on the order of atomics, dQ needs no fp32 buffer,
+// and every accumulator stays in TMEM from the first product to the last.  dQ's CTAs start on the SMs that
+// run out of dK and dV items.  4 x 32 x 4096 x 128 without a mask: 2797 us, 983 TFLOP/s of the five
+// products, 1376 of the seven (72 % of the measured peak); causal 1532 and 897.
 //
 // fp16: P is carried as 2^12 P and dS as 2^(12 + e) dS with one e a call, so that neither goes
 // subnormal where a row has many keys or dO is small.  |dO_i . V_j - delta_i| <= 2 max|dO| max|V|
@@ -291,11 +293,9 @@ constexpr float kCapFactor = kHasCap<MODE> ? 4.0f : 1.0f;
 // dK and dV
 // ---------------------------------------------------------------------------
 // A work item is 128 keys of one key/value head; its steps are the query tiles that see any of them,
-// for every query head of the group.  Where such items are few for the SMs (grouped heads, one
+// for every query head of the group.  Where such items are few for the SMs (few key/value heads, one
 // batch row), their steps are cut into p.splits equal runs, each an item that leaves its sums in
-// fp32 in the workspace, and another launch adds them up in order: 8192 tokens in 4 documents, 4
-// key/value heads, have 256 items of 4 to 168 steps, and the longest alone took 1.5 times an SM's
-// even share.  Per step
+// fp32 in the workspace, and another launch adds them up in order.  Per step
 //     S^T = K Q^T,  dP^T = V dO^T       [128 keys x 128 queries] into 128 TMEM columns each
 //     P^T over S^T's columns, dV += P^T dO;   dS^T over dP^T's columns, dK += dS^T Q
 // with P^T and dS^T read from TMEM.  At D = 128 the four fill all 512 columns.  The products are
@@ -379,9 +379,9 @@ __device__ __forceinline__ float* part_row(const MaskedBwdParams& p, int which, 
     return p.parts + ((((long long)which * p.splits + split) * (p.mask.B * p.mask.Hkv) + bh) * p.mask.Skv + j) * D;
 }
 
-// The parts' sums, in order.  A warp takes kSumRows rows of dK or dV, all loads before the first sum;
-// bound by the read of the parts.
-constexpr int kSumRows = 2, kMaxSplits = 4;
+// The parts' sums, in order.  A warp takes kSumRows rows of dK or dV, the loads of kSumParts parts before
+// their sums; bound by the read of the parts.
+constexpr int kSumRows = 2, kSumParts = 4;
 template <class T, int D>
 __global__ void __launch_bounds__(256) gsr_masked_dkv_sum_kernel(const __grid_constant__ MaskedBwdParams p) {
     using V = typename std::conditional<D == 128, float4, float2>::type;
@@ -389,18 +389,27 @@ __global__ void __launch_bounds__(256) gsr_masked_dkv_sum_kernel(const __grid_co
     const int lane = threadIdx.x & 31;
     const long long rows = (long long)mk.B * mk.Hkv * mk.Skv, first = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kSumRows;
     grid_wait();                                         // dQ has finished, and dK and dV before it
-    V x[kSumRows][kMaxSplits];
+    float sum[kSumRows][D / 32] = {};
+    for (int s0 = 0; s0 < p.splits; s0 += kSumParts) {
+        V x[kSumRows][kSumParts];
 #pragma unroll
-    for (int k = 0; k < kSumRows; ++k)
+        for (int k = 0; k < kSumRows; ++k)
 #pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s) {
-            const long long id = first + k;
-            x[k][s] = V{};
-            if (s < p.splits && id < 2 * rows) {         // dV's parts lie before dK's
-                const long long part = id < rows ? s : p.splits + s, row = id < rows ? id : id - rows;
-                x[k][s] = *(reinterpret_cast<const V*>(p.parts + (part * rows + row) * D) + lane);
+            for (int s = 0; s < kSumParts; ++s) {
+                const long long id = first + k;
+                x[k][s] = V{};
+                if (s0 + s < p.splits && id < 2 * rows) {    // dV's parts lie before dK's
+                    const long long part = (id < rows ? 0 : p.splits) + s0 + s, row = id < rows ? id : id - rows;
+                    x[k][s] = *(reinterpret_cast<const V*>(p.parts + (part * rows + row) * D) + lane);
+                }
             }
-        }
+#pragma unroll
+        for (int k = 0; k < kSumRows; ++k)
+#pragma unroll
+            for (int s = 0; s < kSumParts; ++s)
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) sum[k][e] += reinterpret_cast<const float*>(&x[k][s])[e];
+    }
 #pragma unroll
     for (int k = 0; k < kSumRows; ++k) {
         const long long id = first + k;
@@ -408,20 +417,15 @@ __global__ void __launch_bounds__(256) gsr_masked_dkv_sum_kernel(const __grid_co
         const int which = id >= rows;
         const long long row = id - (which ? rows : 0);
         const int bh = (int)(row / mk.Skv), j = (int)(row - (long long)bh * mk.Skv), b = bh / mk.Hkv, hk = bh - b * mk.Hkv;
-        float acc[D / 32] = {};
         bool bad = false;
 #pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s)
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) acc[e] += reinterpret_cast<const float*>(&x[k][s])[e];
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) bad |= !(fabsf(acc[e]) < INFINITY);
+        for (int e = 0; e < D / 32; ++e) bad |= !(fabsf(sum[k][e]) < INFINITY);
         if (__any_sync(0xffffffffu, bad)) {
             row_dkv<T, D>(p, b, hk, j, which == 1, lane);
             continue;
         }
         const Strided& out = which ? p.dK : p.dV;
-        store_row<T, D>(static_cast<T*>(out.data) + b * out.batch + hk * out.head + (long long)j * out.row, lane, acc);
+        store_row<T, D>(static_cast<T*>(out.data) + b * out.batch + hk * out.head + (long long)j * out.row, lane, sum[k]);
     }
 }
 

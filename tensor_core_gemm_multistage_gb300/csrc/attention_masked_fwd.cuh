@@ -141,10 +141,11 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
     // What the producer publishes of an item; b < 0: no more items.  Query tile q takes steps
     // [t0[q], t1[q]) and step t reads key tile key_tile(t).  A distance bias grows towards the row's own
     // position, which under a causal mask is its last key: from the first tile on, the maximum would
-    // move and O be rescaled at nearly every step, so these kernels walk the keys backwards.
+    // move and O be rescaled at nearly every step, so the keys are walked backwards there (flip >= 0; 4 x
+    // 32 x 4096 x 128: 489 us, forwards 541).  Without a causal mask forwards: 975 us, backwards 1014.
     struct Item {
         int b, h, q_base, t0[NQ], t1[NQ], flip;
-        __device__ __forceinline__ int key_tile(int t) const { return kHasBias<Cfg::MODE> ? flip - t : t; }
+        __device__ __forceinline__ int key_tile(int t) const { return kHasBias<Cfg::MODE> && flip >= 0 ? flip - t : t; }
         __device__ __forceinline__ int first() const {
             return t1[0] > t0[0] ? (t1[1] > t0[1] ? min(t0[0], t0[1]) : t0[0]) : t0[1];
         }
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
             bool asked = false;
             int item = blockIdx.x;
             while (true) {
-                Item it{-1, 0, 0, {0, 0}, {0, 0}, 0};
+                Item it{-1, 0, 0, {0, 0}, {0, 0}, -1};
                 if (item >= 0) {
                     // query blocks from the last (under a causal mask the longest) to the first, in
                     // groups of heads whose K and V stay in L2 together
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                         it.t0[q] = l / Cfg::BKV;
                         it.t1[q] = e > l ? (e + Cfg::BKV - 1) / Cfg::BKV : it.t0[q];
                     }
-                    if (kHasBias<Cfg::MODE>) {
+                    if (kHasBias<Cfg::MODE> && mk.causal) {
                         const int both = it.first() + it.last();
                         it.flip = both - 1;
 #pragma unroll

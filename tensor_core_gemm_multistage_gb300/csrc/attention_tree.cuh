@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                     reg_tie(sc3);
                     const float base = (float)(pos - k0);
                     // the polynomial's second copy of the code costs more here, where items are short and find it
-                    // cold, than it saves (16 trees of up to 40 nodes: 121 us with it, 112 without)
+                    // cold, than it saves (16 trees of up to 40 nodes: 121 us with it, 111 without)
                     score_row<Cfg::MODE, false>(sc0, sc1, sc2, sc3, sc, slope2, base);
                     auto hide = [&](uint32_t (&rr)[32], int c) {
                         const int kk = k0 + c * 32;

@@ -199,9 +199,9 @@ gsr_status encode_cache(CUtensorMap* map, const Strided& t, const gsr::CacheAxes
 // How many heads' items are taken together.  Items of unequal length run longest first across as
 // many heads as keep what they share (`bytes` per `group` heads) within ~48 MiB of L2, but across
 // at least four items an SM, so that short ones are left to even out the end; without a mask every
-// item of a head is equally long and one group's heads run together.  Against L2 alone: 8192 tokens
-// in 4 documents, gradients 569 -> 501 us; 4 x 32 x 4096 x 128 causal, forward 473 -> 456 us, with
-// 8 key/value heads gradients 1713 -> 1608; more (96 MiB of L2) lost up to 2x on some runs.
+// item of a head is equally long and one group's heads run together.  4 x 32 x 4096 x 128 causal,
+// forward: by L2 alone 445 us, so 428; gradients measure the same.  96 MiB of L2 measured 424, but on some
+// runs up to 2x more.
 int heads_together(bool unequal, int64_t bytes, int64_t group, int64_t items_a_head, int64_t heads) {
     int64_t n = group;
     if (unequal) {
@@ -213,32 +213,26 @@ int heads_together(bool unequal, int64_t bytes, int64_t group, int64_t items_a_h
     return (int)(n < heads ? n : heads);
 }
 
-// Parts that a key tile's steps are cut into: items that the SMs cannot share out evenly cost up to an
-// item's time at the end, parts cost a write and a read of dK and dV in fp32.  Causal and document
-// masks leave items of unequal length: parts until there are four items an SM.  Without them items
-// are equal and what counts is how full the last wave is: parts where they save a tenth.  At most
-// four parts of two steps or more.  16 heads over 4, 8192 tokens, bf16: 4 documents 709 us whole,
-// 607 in three parts; causal 1018 and 902; without a mask 1620 whole (1.7 waves of items), 1707 in
-// three parts (5.05 waves of thirds), 1554 in four (6.7 of quarters).
+// Parts that a key tile's steps are cut into.  dK's and dV's items come first and dQ's fill the SMs that
+// they leave, so all of the work (dQ's steps cost 0.72 of dK's and dV's; under a causal or document
+// mask about half of the steps are left) is shared out evenly as long as no item alone is longer than an
+// SM's share: items are cut until they are not.  Parts cost a launch and a write and read of dK and dV
+// in fp32, about 12 us, which a run of fewer than 24 steps (1 us each) does not win back, and parts
+// are eight steps or more.  In one piece and cut (D = 128, bf16):
+//   causal, 4 items of 128 steps 234 us, in 4 parts 75, in 16 (the rule) 34; 16 of 512 899, in 4 245, in
+//   11 122; 64 of 128 236, in 3 120; 128 of 128 239, in 2 218, in 3 227; 160 of 160 300, in 2 324;
+//   256 of 256 706, in 2 751
+//   no mask, 32 of 256 457, in 3 212; 64 of 128 235, in 2 222, in 3 232; 96 of 384 798, in 2 819
+//   4 x 4 heads of 1024 at D = 64 (128 of 8) 25 us, in 2 38
 int64_t bwd_splits(const gsr_attention_desc* d) {
     if (d->batch == 0 || d->heads_kv == 0 || d->seq_kv == 0) return 1;
     const int64_t items = d->batch * d->heads_kv * ((d->seq_kv + 127) / 128);
     const int64_t steps = d->heads_q / d->heads_kv * ((d->seq_q + 127) / 128);
-    const int64_t most = steps / 2 < 4 ? steps / 2 : 4;
-    int64_t best = 1;
-    if (d->causal || d->num_docs > 0) {
-        while (best < most && items * best < 4 * kSms) ++best;
-    } else {
-        double least = (double)((items + kSms - 1) / kSms);
-        for (int64_t n = 2; n <= most; ++n) {
-            const double waves = (double)((items * n + kSms - 1) / kSms) / (double)n;
-            if (waves < 0.9 * least) {
-                least = waves;
-                best = n;
-            }
-        }
-    }
-    return best;
+    const double left = d->causal || d->num_docs > 0 ? 0.5 : 1.0;
+    int64_t n = (int64_t)std::ceil((double)kSms / (1.72 * left * (double)items) - 0.2);   // a fifth over is not worth it
+    if (n > steps / 8) n = steps / 8;
+    if (n > 32) n = 32;
+    return n > 1 && steps - steps / n >= 24 ? n : 1;
 }
 
 // Layout of the backward pass's workspace, 256-byte pieces.

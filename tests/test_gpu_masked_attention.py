@@ -127,6 +127,9 @@ CASES = {
     "negative_scale": dict(B=1, Hq=2, Hkv=1, Sq=200, Skv=200, D=64, scale=-0.2, causal=True),
     "peaked": dict(B=1, Hq=2, Hkv=2, Sq=257, Skv=257, D=64, scale=0.4),
     "many_items": dict(B=2, Hq=48, Hkv=24, Sq=520, Skv=520, D=64, causal=True),
+    "one_kv_head": dict(B=1, Hq=32, Hkv=1, Sq=520, Skv=520, D=128, causal=True, dtype=BF16),
+    "one_kv_head_docs": dict(B=1, Hq=24, Hkv=1, Sq=700, Skv=700, D=64, docs=[[3, 40, 600, 690]]),
+    "few_kv_heads": dict(B=1, Hq=16, Hkv=2, Sq=1000, Skv=700, D=64, causal=True, cap=4.0),
     "small_gradients": dict(B=1, Hq=2, Hkv=1, Sq=600, Skv=600, D=128, grad=2.0 ** -11),
     "large_gradients": dict(B=1, Hq=2, Hkv=1, Sq=300, Skv=300, D=64, grad=2.0 ** 7, causal=True),
 }
