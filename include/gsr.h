@@ -207,10 +207,17 @@ typedef struct gsr_attention_desc {
  * and lse = -inf.  Keys a query does not see have no influence on it, also when they hold
  * infinities or NaN.  Probabilities are rounded to the operands' type for the second product, the
  * output once.  O must share no element with an input, lse lies apart from everything.
+ *
+ *   workspace  device pointer, 16-byte aligned, masked_attention_fwd_workspace(desc) bytes (0 where
+ *              there are queries enough for the SMs; it depends on the sizes alone), for this call
+ *              alone until it has finished; or NULL: where one is needed, one that the library keeps for
+ *              the stream (grown after a wait for the stream; released by gsr_release_stream).  In a
+ *              stream capture NULL then gives GSR_ERR_INVALID_ARG: a graph has a workspace of its own.
  */
+int64_t masked_attention_fwd_workspace(const gsr_attention_desc* desc);
 gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor* Q, const gsr_tensor* K,
-                                const gsr_tensor* V, const gsr_tensor* O, float* lse,
-                                struct CUstream_st* stream);
+                                const gsr_tensor* V, const gsr_tensor* O, float* lse, void* workspace,
+                                int64_t workspace_bytes, struct CUstream_st* stream);
 
 /*
  * Gradients of masked_attention_fwd: dQ, dK, dV from dO and the forward's inputs, O and lse (dO,
@@ -219,10 +226,7 @@ gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor
  * products; in float16 dS carries a power of two that keeps it in range for any size of dO.
  * Queries without keys get dQ = 0 and add nothing, whatever their dO holds.
  *
- *   workspace  device pointer, 16-byte aligned, masked_attention_bwd_workspace(desc) bytes, for
- *              this call alone until it has finished; or NULL: one that the library keeps for the
- *              stream (grown after a wait for the stream; released by gsr_release_stream).  In a
- *              stream capture NULL gives GSR_ERR_INVALID_ARG: a graph has a workspace of its own.
+ *   workspace  masked_attention_bwd_workspace(desc) bytes, as for masked_attention_fwd.
  */
 int64_t masked_attention_bwd_workspace(const gsr_attention_desc* desc);
 gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor* dO, const gsr_tensor* Q,
@@ -254,7 +258,7 @@ gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor
  * O = 0.
  *
  *   workspace  device pointer, 16-byte aligned, tree_attention_workspace(desc) bytes, for this
- *              call alone until it has finished; or NULL, as for masked_attention_bwd.
+ *              call alone until it has finished; or NULL, as for masked_attention_fwd.
  */
 #define GSR_TREE_MAX_NODES 64
 typedef struct gsr_tree_desc {
@@ -393,7 +397,7 @@ gsr_status gsr_device_status(struct CUstream_st* stream, int* code);
 
 /*
  * Releases the library's state for the (current device, stream) pair: the
- * stream's 16 bytes of words and the workspaces of small-M calls, masked-attention
+ * stream's 16 bytes of words and the workspaces of small-M calls, masked attention, its
  * gradients and tree attention, if any ran on it.
  * Waits for the stream first (queued kernels may still use them).  For callers
  * that create and destroy streams: call it before destroying a stream the

@@ -14,7 +14,8 @@ from .binding import (KERNEL_PAIR, KERNEL_PAIR_128, KERNEL_SKINNY, KERNEL_TILED,
                       library_path, select_path, set_path_override, set_raster_group, set_split_k, set_test_flags,
                       set_wait_timeout_ns, shutdown, status_string, version)
 from .llm import (TREE_MAX_NODES, kv_block_tables, kv_cache_append, masked_attention_bwd,
-                  masked_attention_bwd_workspace, masked_attention_fwd, tree_attention_fwd, tree_attention_workspace)
+                  masked_attention_bwd_workspace, masked_attention_fwd, masked_attention_fwd_workspace,
+                  tree_attention_fwd, tree_attention_workspace)
 from ._build import build
 
 __all__ = [
@@ -23,7 +24,7 @@ __all__ = [
     "gemm_scale_relu", "gemm_scale_relu_host",
     "gemm_scale_relu_host_ptr", "gemm_scale_relu_ptr", "last_cuda_error", "lib", "library_path",
     "TREE_MAX_NODES", "kv_block_tables", "kv_cache_append", "masked_attention_bwd", "masked_attention_bwd_workspace",
-    "masked_attention_fwd", "tree_attention_fwd", "tree_attention_workspace",
+    "masked_attention_fwd", "masked_attention_fwd_workspace", "tree_attention_fwd", "tree_attention_workspace",
     "release_stream", "select_path", "set_path_override", "set_raster_group", "set_split_k", "set_test_flags", "set_wait_timeout_ns", "shutdown",
     "status_string", "version",
 ]

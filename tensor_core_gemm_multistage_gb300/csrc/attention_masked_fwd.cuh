@@ -16,7 +16,9 @@
 //    core: while one is exponentiated, the other's products run;
 //  * the exponent base moves only when a tile's maximum exceeds it by more than 2^8, so P <= 256
 //    and O is rarely rescaled.  P is rounded to the operands' type for the second product (the
-//    tensor core takes both operands in one type); its sum l is kept in fp32 from unrounded values.
+//    tensor core takes both operands in one type); its sum l is kept in fp32 from unrounded values;
+//  * where items are few for the SMs, their key tiles are cut into p.splits runs, each an item that
+//    leaves its part (maximum, sum, O in fp32) in the workspace, and a second launch joins them.
 //
 // Masked scores are replaced by -inf, so what K holds there is never used.  A masked V row enters
 // the product as 0 V, which is NaN where V is not finite: a row whose output is not finite is
@@ -24,6 +26,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "attention_common.cuh"
 #include "ptx_attention.cuh"
@@ -53,8 +56,8 @@ struct MaskedFwdCfg {
     static constexpr int OFF_BAR = OFF_V + 2 * KV_BYTES;
     static constexpr int NUM_BARS = 20;
     static constexpr int OFF_CLC = OFF_BAR + NUM_BARS * 8;      // 16-byte aligned
-    static constexpr int OFF_ITEM = OFF_CLC + 16;               // 2 x 8 ints
-    static constexpr int OFF_MISC = OFF_ITEM + 64;
+    static constexpr int OFF_ITEM = OFF_CLC + 16;               // 2 x 12 ints
+    static constexpr int OFF_MISC = OFF_ITEM + 96;
     static constexpr int SMEM_BYTES = OFF_MISC + 16;
     static constexpr int TMEM_COLS = 512;
     static constexpr uint32_t T_S = 0, T_O = 256, P_COL = 64;
@@ -92,6 +95,51 @@ __device__ __noinline__ void masked_row(const MaskedFwdParams& p, int b, int h, 
     store_row<T, D>(static_cast<T*>(p.O.data) + b * p.O.batch + h * p.O.head + i * p.O.row, lane, acc);
     if (p.lse && lane == 0)
         p.lse[((long long)b * p.mask.Hq + h) * p.mask.Sq + i] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// Part `split` of a row in the workspace.
+__device__ __forceinline__ long long part_index(const MaskedFwdParams& p, int b, int h, int split, int i) {
+    return (((long long)b * p.mask.Hq + h) * p.splits + split) * p.mask.Sq + i;
+}
+
+// Rows from their parts, one warp each, in the parts' order; lane s holds the factor of part s.
+template <class T, int D>
+__global__ void __launch_bounds__(256) gsr_masked_fwd_join_kernel(const __grid_constant__ MaskedFwdParams p) {
+    using V = typename std::conditional<D == 128, float4, float2>::type;
+    const int lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    grid_wait();                                         // the parts' launch has finished
+    if (row >= (long long)p.mask.B * p.mask.Hq * p.mask.Sq) return;
+    const int i = (int)(row % p.mask.Sq), bh = (int)(row / p.mask.Sq), b = bh / p.mask.Hq, h = bh - b * p.mask.Hq;
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (lane < p.splits) ml = p.parts_ml[part_index(p, b, h, lane, i)];
+    float m = ml.x;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float f = m == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
+    const float l = warp_sum(f == 0.0f && ml.y == ml.y ? 0.0f : ml.y * f);
+    float acc[D / 32] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+        const float fs = __shfl_sync(0xffffffffu, f, s);
+        if (fs == 0.0f) continue;                        // may hold anything
+        const V x = *(reinterpret_cast<const V*>(p.parts + part_index(p, b, h, s, i) * D) + lane);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(reinterpret_cast<const float*>(&x)[e], fs, acc[e]);
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    bool bad = !(l < INFINITY);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+        bad |= !(fabsf(acc[e]) < INFINITY);
+        acc[e] *= inv;
+    }
+    if (__any_sync(0xffffffffu, bad)) {
+        masked_row<T, D>(p, b, h, i, lane);
+        return;
+    }
+    store_row<T, D>(static_cast<T*>(p.O.data) + b * p.O.batch + h * p.O.head + (long long)i * p.O.row, lane, acc);
+    if (p.lse && lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // No keys at all: O = 0, lse = -inf.  One warp per row.
@@ -144,7 +192,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
     // move and O be rescaled at nearly every step, so the keys are walked backwards there (flip >= 0; 4 x
     // 32 x 4096 x 128: 489 us, forwards 541).  Without a causal mask forwards: 975 us, backwards 1014.
     struct Item {
-        int b, h, q_base, t0[NQ], t1[NQ], flip;
+        int b, h, q_base, t0[NQ], t1[NQ], flip, split;
         __device__ __forceinline__ int key_tile(int t) const { return kHasBias<Cfg::MODE> && flip >= 0 ? flip - t : t; }
         __device__ __forceinline__ int first() const {
             return t1[0] > t0[0] ? (t1[1] > t0[1] ? min(t0[0], t0[1]) : t0[0]) : t0[1];
@@ -154,8 +202,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
         }
     };
     auto read_item = [&](int box) {
-        volatile int* v = item_box + 8 * box;
-        return Item{v[0], v[1], v[2], {v[3], v[4]}, {v[5], v[6]}, v[7]};
+        volatile int* v = item_box + 12 * box;
+        return Item{v[0], v[1], v[2], {v[3], v[4]}, {v[5], v[6]}, v[7], v[8]};
     };
 
     if (threadIdx.x == 0) {
@@ -204,16 +252,17 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
             bool asked = false;
             int item = blockIdx.x;
             while (true) {
-                Item it{-1, 0, 0, {0, 0}, {0, 0}, -1};
+                Item it{-1, 0, 0, {0, 0}, {0, 0}, -1, 0};
                 if (item >= 0) {
                     // query blocks from the last (under a causal mask the longest) to the first, in
                     // groups of heads whose K and V stay in L2 together
-                    const int per_group = p.head_group * n_qb, grp = item / per_group, r_in = item - grp * per_group;
+                    const int per_group = p.head_group * n_qb * p.splits, grp = item / per_group, r_in = item - grp * per_group;
                     const int gsz = min(mk.B * mk.Hq - grp * p.head_group, p.head_group);
                     const int bh = grp * p.head_group + r_in % gsz;
                     it.b = bh / mk.Hq;
                     it.h = bh - it.b * mk.Hq;
-                    it.q_base = (n_qb - 1 - r_in / gsz) * NQ * Cfg::BQ;
+                    it.split = r_in / gsz % p.splits;
+                    it.q_base = (n_qb - 1 - r_in / gsz / p.splits) * NQ * Cfg::BQ;
                     // lane 2q: first row of tile q, lane 2q + 1: its last row
                     int lo = 0, hi = 0;
                     const int first = it.q_base + (lane >> 1 & 1) * Cfg::BQ;
@@ -235,13 +284,22 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                             it.t1[q] = both - t0;
                         }
                     }
+                    if (p.splits > 1) {
+                        const int from = it.first(), len = it.last() - from;
+                        const int begin = from + len * it.split / p.splits, end = from + len * (it.split + 1) / p.splits;
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) {
+                            it.t0[q] = min(max(it.t0[q], begin), end);
+                            it.t1[q] = min(max(it.t1[q], begin), end);
+                        }
+                    }
                 }
                 const uint32_t box = n_pub & 1u;
                 // the box's previous item has been read by every role
                 bool ok = lane != 0 || w.wait(item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 if (lane == 0) {
-                    volatile int* v = item_box + 8 * box;
+                    volatile int* v = item_box + 12 * box;
                     v[0] = it.b;
                     v[1] = it.h;
                     v[2] = it.q_base;
@@ -251,6 +309,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                         v[5 + q] = it.t1[q];
                     }
                     v[7] = it.flip;
+                    v[8] = it.split;
                     mbar_arrive(item_pub(box));              // release: the consumers read the box after
                 }
                 ++n_pub;
@@ -515,6 +574,25 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                 tcgen05_fence_after();
             }
             if (!ok) break;
+            if (p.splits > 1) {
+                const long long part = part_index(p, it.b, it.h, it.split, qi);
+                if (t0 < t1) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t rr[32];
+                        __syncwarp();
+                        tmem_ld_32x32b_x32(o_col + c * 32, rr);
+                        tmem_ld_wait(rr);
+                        if (qi < mk.Sq)
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                *reinterpret_cast<uint4*>(p.parts + part * D + c * 32 + i) = make_uint4(rr[i], rr[i + 1], rr[i + 2], rr[i + 3]);
+                    }
+                }
+                if (qi < mk.Sq) p.parts_ml[part] = make_float2(m, l);
+                tcgen05_fence_before();
+                continue;
+            }
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
             bool bad = !(l < INFINITY);          // l or an element of O is infinite or NaN
             T* dst = static_cast<T*>(p.O.data) + it.b * p.O.batch + it.h * p.O.head + (long long)qi * p.O.row;
@@ -566,10 +644,12 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
 template <class Cfg>
 cudaError_t launch_masked_cfg(const MaskedFwdMaps& tm, const MaskedFwdParams& p, cudaStream_t stream) {
     static std::atomic<uint64_t> attr_done{0};
-    const cudaError_t e = allow_smem(gsr_masked_fwd_kernel<Cfg>, Cfg::SMEM_BYTES, attr_done);
+    cudaError_t e = allow_smem(gsr_masked_fwd_kernel<Cfg>, Cfg::SMEM_BYTES, attr_done);
     if (e != cudaSuccess) return e;
     gsr_masked_fwd_kernel<Cfg><<<(unsigned)p.num_items, Cfg::NUM_THREADS, Cfg::SMEM_BYTES, stream>>>(tm.q, tm.k, tm.v, p);
-    return cudaGetLastError();
+    if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
+    const long long rows = (long long)p.mask.B * p.mask.Hq * p.mask.Sq;
+    return launch_early(gsr_masked_fwd_join_kernel<typename Cfg::T, Cfg::D>, (unsigned)((rows + 7) / 8), 256, 0, stream, p);
 }
 
 template <class T, int D>

@@ -214,6 +214,49 @@ int heads_together(bool unequal, int64_t bytes, int64_t group, int64_t items_a_h
     return (int)(n < heads ? n : heads);
 }
 
+// Parts that the forward pass cuts its items' keys into: where 256-query items are few for the SMs, the
+// longest one alone sets the time.  The estimate counts steps of two query tiles and a key tile (1.3 us, 2.3
+// with a cap) and 2.5 us an item: the longest item or an SM's share where a mask makes items unequal,
+// else the waves of equal items.  Parts cost a launch and the write and read of their O (6 us, 6 TB/s
+// through L2).  Whole and in parts, us, D = 128 (batch, heads over key/value heads, queries x keys):
+//   1, 8/1, 1 x 32768: 435, 38.  1, 16/16, 512 x 8192: 116, 44.  1, 4/4, 3816 x 3816 causal: 58, 38; capped
+//   89, 46.  D = 64: 1, 8/8, 16 x 16384: 198, 23; 1, 8/2, 5337 x 5337: 122, 111, causal 73, 64
+int64_t fwd_splits(const gsr_attention_desc* d, bool capped, bool unequal) {
+    const int64_t items = d->batch * d->heads_q * ((d->seq_q + 255) / 256), steps = (d->seq_kv + 127) / 128;
+    if (items == 0 || items >= 4 * kSms || steps < 4) return 1;
+    // a causal mask leaves nearly all keys to the last few queries
+    if (d->num_docs == 0 && d->seq_q * 8 <= d->seq_kv) unequal = false;
+    const double step = capped ? 2.3 : 1.3, fixed = 2.5, sms = (double)kSms;
+    const double rows = (double)std::min(d->seq_q, (int64_t)256), work = 0.5 * step * (double)(items * steps);
+    auto cost = [&](int64_t n) {
+        const double longest = step * (double)((steps + n - 1) / n) + fixed;
+        const double run = unequal ? std::max(longest, (work + fixed * (double)(items * n)) / sms)
+                                   : (double)((items * n + kSms - 1) / kSms) * longest;
+        return run + (n > 1 ? 6.0 + (double)(items * n) * rows * (double)d->head_dim * 8.0 / 6e6 : 0.0);
+    };
+    int64_t best = 1;
+    double least = 0.9 * cost(1);
+    for (int64_t n = 2; n <= std::min(steps / 2, (int64_t)32); ++n) {
+        const double c = cost(n);
+        if (c < least) {
+            least = c;
+            best = n;
+        }
+    }
+    return best;
+}
+
+// Layout of the forward pass's workspace: maxima and sums, then O's parts.
+struct FwdLayout {
+    int64_t splits, parts, total;
+};
+FwdLayout fwd_layout(const gsr_attention_desc* d, bool capped, bool unequal) {
+    const int64_t splits = fwd_splits(d, capped, unequal), rows = d->batch * d->heads_q * splits * d->seq_q;
+    if (splits == 1) return {1, 0, 0};
+    const int64_t ml = (rows * 8 + 255) / 256 * 256;
+    return {splits, ml, ml + rows * d->head_dim * 4};
+}
+
 // Parts that a key tile's steps are cut into.  dK's and dV's items come first and dQ's fill the SMs that
 // they leave, so all of the work (dQ's steps cost 0.72 of dK's and dV's; under a causal or document
 // mask about half of the steps are left) is shared out evenly as long as no item alone is longer than an
@@ -226,11 +269,11 @@ int heads_together(bool unequal, int64_t bytes, int64_t group, int64_t items_a_h
 //   256 of 256 706, in 2 751; 8 of 32 64, in 4 29, in 8 23; 32 of 32 66, in 4 38, in 6 41
 //   no mask, 32 of 256 457, in 3 212; 64 of 128 235, in 2 222, in 3 232; 96 of 384 798, in 2 819
 //   4 x 4 heads of 1024 at D = 64 (128 of 8) 25 us, in 2 38
-int64_t bwd_splits(const gsr_attention_desc* d) {
+int64_t bwd_splits(const gsr_attention_desc* d, bool unequal) {
     if (d->batch == 0 || d->heads_kv == 0 || d->seq_kv == 0) return 1;
     const int64_t items = d->batch * d->heads_kv * ((d->seq_kv + 127) / 128);
     const int64_t steps = d->heads_q / d->heads_kv * ((d->seq_q + 127) / 128);
-    const double left = d->causal || d->num_docs > 0 ? 0.5 : 1.0;
+    const double left = unequal ? 0.5 : 1.0;
     int64_t n = (int64_t)std::ceil((double)kSms / (1.72 * left * (double)items) - 0.2);   // a fifth over is not worth it
     const int64_t at_once = std::min(steps / 4, kSms / items);
     n = std::min({n, std::max(steps / 8, at_once), (int64_t)32});
@@ -241,14 +284,14 @@ int64_t bwd_splits(const gsr_attention_desc* d) {
 struct BwdLayout {
     int64_t sp, splits, offset, delta, parts, total;
 };
-BwdLayout bwd_layout(const gsr_attention_desc* d) {
+BwdLayout bwd_layout(const gsr_attention_desc* d, bool unequal) {
     auto piece = [](int64_t bytes) { return (bytes + 255) / 256 * 256; };
     BwdLayout w;
     w.sp = (d->seq_q + 127) / 128 * 128;
     w.offset = 256;                                                     // the norms come first
     w.delta = w.offset + piece(4 * d->batch * d->heads_q * w.sp);
     w.parts = w.delta + piece(4 * d->batch * d->heads_q * w.sp);
-    w.splits = bwd_splits(d);
+    w.splits = bwd_splits(d, unequal);
     w.total = w.parts + (w.splits > 1 ? piece(8 * w.splits * d->batch * d->heads_kv * d->seq_kv * d->head_dim) : 0);
     return w;
 }
@@ -303,8 +346,16 @@ gsr_status check_tree_desc(const gsr_tree_desc* desc) {
 
 extern "C" {
 
+int64_t masked_attention_fwd_workspace(const gsr_attention_desc* desc) {
+    if (check_desc(desc) != GSR_OK) return -1;
+    int64_t most = 0;                                  // enough for these sizes with any mask and score
+    for (int i = 0; i < 4; ++i) most = std::max(most, fwd_layout(desc, i & 1, i & 2).total);
+    return most;
+}
+
 gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor* Q, const gsr_tensor* K,
-                                const gsr_tensor* V, const gsr_tensor* O, float* lse, CUstream_st* stream) {
+                                const gsr_tensor* V, const gsr_tensor* O, float* lse, void* workspace,
+                                int64_t workspace_bytes, CUstream_st* stream) {
     gsr_status s = check_desc(desc);
     if (s != GSR_OK) return s;
     const int64_t B = desc->batch, Hq = desc->heads_q, Hkv = desc->heads_kv, Sq = desc->seq_q, Skv = desc->seq_kv,
@@ -315,7 +366,14 @@ gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor
         return s;
     if (B == 0 || Hq == 0 || Sq == 0) return GSR_OK;
     if (misaligned(lse, 4)) return GSR_ERR_ALIGNMENT;
-    const Span o = span_of(p.O, B, Hq, Sq, D, 2), l = words(lse, B * Hq * Sq);
+    const bool unequal = desc->causal || desc->num_docs > 0;
+    const FwdLayout w = fwd_layout(desc, desc->softcap > 0.0f, unequal);
+    if (workspace && workspace_bytes < w.total) return GSR_ERR_INVALID_ARG;
+    if (misaligned(workspace, 16)) return GSR_ERR_ALIGNMENT;
+    const Span o = span_of(p.O, B, Hq, Sq, D, 2), l = words(lse, B * Hq * Sq), ws = words(workspace, w.total / 4);
+    if (meet(ws, o) || meet(ws, l) || meets_masks(ws, desc) || meet(ws, span_of(p.Q, B, Hq, Sq, D, 2)) ||
+        meet(ws, span_of(p.K, B, Hkv, Skv, D, 2)) || meet(ws, span_of(p.V, B, Hkv, Skv, D, 2)))
+        return GSR_ERR_ALIAS;
     if (share(p.O, Hq, Sq, p.Q, Hq, Sq, B, D) || share(p.O, Hq, Sq, p.K, Hkv, Skv, B, D) ||
         share(p.O, Hq, Sq, p.V, Hkv, Skv, B, D) || meets_masks(o, desc))
         return GSR_ERR_ALIAS;
@@ -336,16 +394,23 @@ gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor
                     (s = encode(&tm.k, p.K, desc->dtype, B, Hkv, Skv, D, 128)) != GSR_OK ||
                     (s = encode(&tm.v, p.V, desc->dtype, B, Hkv, Skv, D, 128)) != GSR_OK))
         return s;
-    p.num_items = (int)((Sq + 255) / 256 * B * Hq);
-    const bool unequal = desc->causal || desc->num_docs > 0;
-    p.head_group = heads_together(unequal, Skv * D * 4, p.mask.group, (Sq + 255) / 256, B * Hq);
+    std::unique_lock<std::mutex> lock(g_scratch_mu, std::defer_lock);
+    if (w.splits > 1 && !workspace) {
+        lock.lock();
+        if ((s = gsr::host::stream_scratch(dev, st, (size_t)w.total, &workspace)) != GSR_OK) return s;
+    }
+    p.splits = (int)w.splits;
+    p.parts_ml = reinterpret_cast<float2*>(workspace);
+    p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.parts);
+    p.num_items = (int)((Sq + 255) / 256 * B * Hq * w.splits);
+    p.head_group = heads_together(unequal, Skv * D * 4, p.mask.group, (Sq + 255) / 256 * w.splits, B * Hq);
     const cudaError_t e = desc->dtype == GSR_BF16 ? gsr::launch_masked_fwd_bf16(tm, p, (int)D, st)
                                                   : gsr::launch_masked_fwd_f16(tm, p, (int)D, st);
     return e == cudaSuccess ? GSR_OK : gsr::host::fail(e);
 }
 
 int64_t masked_attention_bwd_workspace(const gsr_attention_desc* desc) {
-    return check_desc(desc) == GSR_OK ? bwd_layout(desc).total : -1;
+    return check_desc(desc) == GSR_OK ? bwd_layout(desc, true).total : -1;     // without a mask no more parts
 }
 
 gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor* dO, const gsr_tensor* Q,
@@ -368,7 +433,8 @@ gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor
     const bool no_q = B == 0 || Hq == 0 || Sq == 0, no_k = B == 0 || Hkv == 0 || Skv == 0;
     if (no_q && no_k) return GSR_OK;
     if (!no_q && !lse) return GSR_ERR_INVALID_ARG;
-    const BwdLayout w = bwd_layout(desc);
+    const bool unequal = desc->causal || desc->num_docs > 0;
+    const BwdLayout w = bwd_layout(desc, unequal);
     if (workspace && workspace_bytes < w.total) return GSR_ERR_INVALID_ARG;
     if (misaligned(lse, 4) || misaligned(workspace, 16)) return GSR_ERR_ALIGNMENT;
     // outputs share elements with nothing; the workspace and lse lie apart from the operands
@@ -413,7 +479,6 @@ gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor
                            (s = encode(&tm.v, p.V, desc->dtype, B, Hkv, Skv, D, 128)) != GSR_OK ||
                            (s = encode(&tm.dO, p.dO, desc->dtype, B, Hq, Sq, D, 128)) != GSR_OK))
         return s;
-    const bool unequal = desc->causal || desc->num_docs > 0;
     if (!no_q && !no_k) {
         p.q_head_group = heads_together(unequal, Skv * D * 4, p.mask.group, w.sp / 128, B * Hq);
         p.kv_head_group = heads_together(unequal, Sq * D * 4 * p.mask.group, 1, (Skv + 127) / 128 * w.splits, B * Hkv);

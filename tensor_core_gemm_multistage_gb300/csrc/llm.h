@@ -50,6 +50,9 @@ struct MaskedFwdParams {
     float* lse;                 // (B, Hq, Sq) or null
     int head_group;             // item order, as in AttnParams
     int num_items;
+    int splits;                 // parts of an item's keys; above 1, parts go to the workspace:
+    float2* parts_ml;           // (B, Hq, splits, Sq): exponent base and sum
+    float* parts;               // (B, Hq, splits, Sq, D): O, not normalised
     int* err;
     uint64_t timeout_ns;
     uint32_t test_flags;

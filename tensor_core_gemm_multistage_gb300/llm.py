@@ -39,7 +39,9 @@ def _declare(L) -> None:
     vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
     ts, ds, tr = ctypes.POINTER(_Tensor), ctypes.POINTER(_AttentionDesc), ctypes.POINTER(_TreeDesc)
     L.masked_attention_fwd.restype = i32
-    L.masked_attention_fwd.argtypes = [ds, ts, ts, ts, ts, vp, vp]
+    L.masked_attention_fwd.argtypes = [ds, ts, ts, ts, ts, vp, vp, i64, vp]
+    L.masked_attention_fwd_workspace.restype = i64
+    L.masked_attention_fwd_workspace.argtypes = [ds]
     L.masked_attention_bwd_workspace.restype = i64
     L.masked_attention_bwd_workspace.argtypes = [ds]
     L.masked_attention_bwd.restype = i32
@@ -150,7 +152,8 @@ def _lse(lse, qs, index):
 
 
 def masked_attention_fwd(Q, K, V, O, lse=None, softmax_scale: float = 0.0, causal: bool = False,
-                         softcap: float = 0.0, alibi_slopes=None, doc_bounds=None, prefix_lens=None, stream=None):
+                         softcap: float = 0.0, alibi_slopes=None, doc_bounds=None, prefix_lens=None, workspace=None,
+                         stream=None):
     """O = softmax(score) V over the keys each query sees; returns O.
 
     Q, O (B, Hq, Sq, D), K and V (B, Hkv, Skv, D): float16 or bfloat16 CUDA tensors, D 64 or 128 and
@@ -159,12 +162,26 @@ def masked_attention_fwd(Q, K, V, O, lse=None, softmax_scale: float = 0.0, causa
     ``alibi_slopes`` (Hq,) float32 subtracts slope * distance; ``doc_bounds`` (B, n + 1) int32 keeps
     queries inside their document (positions outside all documents are padding); ``prefix_lens``
     (B,) or (B, n) int32, with ``causal``, lets every query see that many leading keys.
+
+    ``workspace``: optional device buffer of masked_attention_fwd_workspace(...) bytes (few queries, many
+    keys); without one the library keeps one for the stream, and a call inside torch.cuda.graph takes
+    one from the graph's memory.
     """
     d, qs, ks, dev = _attention_desc(Q, K, softmax_scale, causal, softcap, alibi_slopes, doc_bounds, prefix_lens)
-    dt = Q.dtype
-    _call(dev, stream, "masked_attention_fwd", lib().masked_attention_fwd, d, _operand(Q, "Q", qs, dt, dev),
-          _operand(K, "K", ks, dt, dev), _operand(V, "V", ks, dt, dev), _operand(O, "O", qs, dt, dev), _lse(lse, qs, dev))
+    dt, L = Q.dtype, lib()
+    ws, scratch, size = _scratch(workspace, lambda: L.masked_attention_fwd_workspace(d), dev, stream)
+    _call(dev, stream, "masked_attention_fwd", L.masked_attention_fwd, d, _operand(Q, "Q", qs, dt, dev),
+          _operand(K, "K", ks, dt, dev), _operand(V, "V", ks, dt, dev), _operand(O, "O", qs, dt, dev), _lse(lse, qs, dev),
+          scratch, size)
     return O
+
+
+def masked_attention_fwd_workspace(B: int, Hq: int, Hkv: int, Sq: int, Skv: int, D: int) -> int:
+    """Bytes of workspace a masked_attention_fwd call of these sizes needs, whatever its masks."""
+    n = lib().masked_attention_fwd_workspace(_AttentionDesc(B, Hq, Hkv, Sq, Skv, D))
+    if n < 0:
+        raise GsrError(Status.ERR_INVALID_ARG, "masked_attention_fwd_workspace")
+    return n
 
 
 def masked_attention_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, softmax_scale: float = 0.0, causal: bool = False,
@@ -173,9 +190,8 @@ def masked_attention_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, softmax_scale: float =
     """Gradients dQ, dK, dV (returned) of masked_attention_fwd from dO, its inputs, O and lse.
 
     dO, O and dQ are shaped as Q, dK and dV as K; masks and scores as in the forward call.
-    ``workspace``: optional device buffer of masked_attention_bwd_workspace(...) bytes; without one
-    the library keeps one for the stream, and a call inside torch.cuda.graph takes one from the graph's
-    memory.
+    ``workspace``: optional device buffer of masked_attention_bwd_workspace(...) bytes, as for
+    masked_attention_fwd.
     """
     d, qs, ks, dev = _attention_desc(Q, K, softmax_scale, causal, softcap, alibi_slopes, doc_bounds, prefix_lens)
     dt, L = Q.dtype, lib()
@@ -188,7 +204,7 @@ def masked_attention_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, softmax_scale: float =
 
 
 def masked_attention_bwd_workspace(B: int, Hq: int, Hkv: int, Sq: int, Skv: int, D: int) -> int:
-    """Bytes of workspace a masked_attention_bwd call of these sizes needs."""
+    """Bytes of workspace a masked_attention_bwd call of these sizes needs, whatever its masks."""
     n = lib().masked_attention_bwd_workspace(_AttentionDesc(B, Hq, Hkv, Sq, Skv, D))
     if n < 0:
         raise GsrError(Status.ERR_INVALID_ARG, "masked_attention_bwd_workspace")

@@ -130,6 +130,10 @@ CASES = {
     "one_kv_head": dict(B=1, Hq=32, Hkv=1, Sq=520, Skv=520, D=128, causal=True, dtype=BF16),
     "one_kv_head_docs": dict(B=1, Hq=24, Hkv=1, Sq=700, Skv=700, D=64, docs=[[3, 40, 600, 690]]),
     "few_kv_heads": dict(B=1, Hq=16, Hkv=2, Sq=1000, Skv=700, D=64, causal=True, cap=4.0),
+    "few_queries": dict(B=1, Hq=4, Hkv=2, Sq=3, Skv=5000, D=128, causal=True, dtype=BF16),
+    "few_queries_two_way": dict(B=2, Hq=2, Hkv=1, Sq=130, Skv=2600, D=64, cap=3.0),
+    "few_heads": dict(B=1, Hq=2, Hkv=1, Sq=1500, Skv=1500, D=128, causal=True, alibi=True, prefix=[300]),
+    "few_heads_docs": dict(B=1, Hq=2, Hkv=2, Sq=2000, Skv=2000, D=64, causal=True, docs=[[3, 900, 901, 1990]], dtype=BF16),
     "small_gradients": dict(B=1, Hq=2, Hkv=1, Sq=600, Skv=600, D=128, grad=2.0 ** -11),
     "large_gradients": dict(B=1, Hq=2, Hkv=1, Sq=300, Skv=300, D=64, grad=2.0 ** 7, causal=True),
 }
@@ -487,3 +491,37 @@ def test_nan_everywhere_is_not_slow(D):
         gsr.set_wait_timeout_ns(1_000_000_000)
     assert status == gsr.Status.OK, hex(code)
     assert all(torch.isnan(t).all() for t in (o, lse, *grads))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_keys_in_parts(D):
+    """Few queries over many keys: with the library's workspace, the caller's, in a graph; NaN among keys that
+    nothing sees, and in one that all see."""
+    c = Case(1, 4, 2, 5, 6000, D, causal=True, cap=2.0).forward().check_forward()
+    want = c.o.clone()
+    size = gsr.masked_attention_fwd_workspace(1, 4, 2, 5, 6000, D)
+    own = torch.full((size + 64,), 255, dtype=torch.uint8, device=DEV)
+    c.o.fill_(float("nan"))
+    gsr.masked_attention_fwd(c.q, c.k, c.v, c.o, c.lse, workspace=own[:size], **c.kw)
+    assert torch.equal(c.o, want) and torch.all(own[size:] == 255)
+    with pytest.raises(gsr.GsrError):
+        gsr.masked_attention_fwd(c.q, c.k, c.v, c.o, c.lse, workspace=own[:size // 64], **c.kw)
+    side = torch.cuda.Stream(DEV)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        gsr.masked_attention_fwd(c.q, c.k, c.v, c.o, c.lse, **c.kw)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        gsr.masked_attention_fwd(c.q, c.k, c.v, c.o, c.lse, **c.kw)
+    c.o.fill_(float("nan"))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(c.o, want)
+    c.k[:, :, 5997:] = float("nan")               # the last three queries alone see it
+    c.v[:, :, 5997:] = float("nan")
+    c.forward().check_forward(slice(0, 2))
+    assert torch.isnan(c.o[:, :, 2:]).all()
+    c.k[:, :, 100] = float("nan")
+    c.forward()
+    assert torch.isnan(c.o).all()

@@ -22,13 +22,13 @@ def dense(addr, B, H, S, D):
     return _Tensor(addr, H * S * D, S * D, D)
 
 
-def fwd(desc=None, lse=None, **t):
+def fwd(desc=None, lse=None, ws=None, ws_bytes=0, **t):
     d = dict(batch=2, heads_q=4, heads_kv=2, seq_q=100, seq_kv=100, head_dim=64, dtype=0, causal=1)
     d.update(desc or {})
     ops = dict(Q=dense(1 * GB, 2, 4, 100, 64), K=dense(2 * GB, 2, 2, 100, 64), V=dense(3 * GB, 2, 2, 100, 64),
                O=dense(4 * GB, 2, 4, 100, 64))
     ops.update(t)
-    return gsr.lib().masked_attention_fwd(_AttentionDesc(**d), ops["Q"], ops["K"], ops["V"], ops["O"], lse, None)
+    return gsr.lib().masked_attention_fwd(_AttentionDesc(**d), ops["Q"], ops["K"], ops["V"], ops["O"], lse, ws, ws_bytes, None)
 
 
 def bwd(desc=None, lse=9 * GB, ws=10 * GB, ws_bytes=1 << 20, **t):
@@ -64,7 +64,7 @@ def test_attention_pointers_strides_and_alignment():
     assert fwd(Q=_Tensor(1 * GB, 1 << 45, 6400, 64)) == INVALID
     assert fwd(lse=9 * GB + 2) == ALIGN
     assert fwd(dict(alibi_slopes=9 * GB + 2)) == ALIGN
-    assert gsr.lib().masked_attention_fwd(None, None, None, None, None, None, None) == INVALID
+    assert gsr.lib().masked_attention_fwd(None, None, None, None, None, None, None, 0, None) == INVALID
     assert bwd(lse=None) == INVALID
     assert bwd(ws_bytes=llm.masked_attention_bwd_workspace(2, 4, 2, 100, 100, 64) - 1) == INVALID
     assert bwd(ws=10 * GB + 8) == ALIGN
@@ -176,6 +176,31 @@ def test_masks_and_lengths_in_the_way_of_outputs():
     assert bwd(dict(alibi_slopes=6 * GB)) == ALIAS and bwd(dict(prefix_lens=10 * GB)) == ALIAS
     assert tree(lens=4 * GB) == ALIAS and tree(starts=4 * GB) == ALIAS and tree(parents=4 * GB) == ALIAS
     assert tree(table=10 * GB) == ALIAS and tree(dict(alibi_slopes=10 * GB)) == ALIAS
+
+
+def test_forward_workspace():
+    few = dict(batch=1, heads_q=4, heads_kv=2, seq_q=100, seq_kv=20000)
+    need = llm.masked_attention_fwd_workspace(1, 4, 2, 100, 20000, 64)
+    assert need > 0 and llm.masked_attention_fwd_workspace(8, 32, 8, 4096, 4096, 64) == 0
+    ops = dict(Q=dense(1 * GB, 1, 4, 100, 64), K=dense(2 * GB, 1, 2, 20000, 64), V=dense(3 * GB, 1, 2, 20000, 64),
+               O=dense(4 * GB, 1, 4, 100, 64))
+    assert fwd(few, ws=10 * GB, ws_bytes=need // 64, **ops) == INVALID
+    assert fwd(few, ws=10 * GB + 8, ws_bytes=need, **ops) == ALIGN
+    for at in (1, 2, 3, 4):
+        assert fwd(few, ws=at * GB, ws_bytes=need, **ops) == ALIAS
+    assert fwd(dict(few, alibi_slopes=10 * GB), ws=10 * GB, ws_bytes=need, **ops) == ALIAS
+    assert fwd(few, ws=9 * GB, ws_bytes=need, lse=9 * GB, **ops) == ALIAS
+    with pytest.raises(gsr.GsrError):
+        llm.masked_attention_fwd_workspace(1, 4, 3, 100, 100, 64)
+
+
+@pytest.mark.parametrize("sizes", [(1, 8, 1, 300, 300, 64), (2, 16, 2, 2000, 700, 128), (1, 32, 1, 5000, 9000, 64)])
+def test_workspaces_do_not_depend_on_masks(sizes):
+    d = dict(zip(("batch", "heads_q", "heads_kv", "seq_q", "seq_kv", "head_dim"), sizes))
+    for of in ("fwd", "bwd"):
+        c = getattr(gsr.lib(), "masked_attention_%s_workspace" % of)
+        assert len({c(_AttentionDesc(**d, **e)) for e in (dict(), dict(causal=1), dict(softcap=3.0), dict(causal=1, softcap=3.0))}) == 1
+        assert getattr(llm, "masked_attention_%s_workspace" % of)(*sizes) == c(_AttentionDesc(**d))
 
 
 def test_binding_refusals():
