@@ -13,7 +13,7 @@
 // added dQ would take; in return no result depends on the order of atomics, dQ needs no fp32 buffer,
 // and every accumulator stays in TMEM from the first product to the last.  dQ's CTAs start on the SMs that
 // run out of dK and dV items.  4 x 32 x 4096 x 128 without a mask: 2797 us, 983 TFLOP/s of the five
-// products, 1376 of the seven (72 % of the measured peak); causal 1532 and 897.
+// products, 1376 of the seven (69 % of the measured peak); causal 1532 and 897.
 //
 // fp16: P is carried as 2^12 P and dS as 2^(12 + e) dS with one e a call, so that neither goes
 // subnormal where a row has many keys or dO is small.  |dO_i . V_j - delta_i| <= 2 max|dO| max|V|

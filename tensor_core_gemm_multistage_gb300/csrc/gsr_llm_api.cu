@@ -261,12 +261,13 @@ FwdLayout fwd_layout(const gsr_attention_desc* d, bool capped, bool unequal) {
 // they leave, so all of the work (dQ's steps cost 0.72 of dK's and dV's; under a causal or document
 // mask about half of the steps are left) is shared out evenly as long as no item alone is longer than an
 // SM's share: items are cut until they are not.  Parts cost a launch and a write and read of dK and dV
-// in fp32, about 12 us, which fewer than 12 steps less (1 us each, 2 where SMs are few) do not win
-// back.  Parts are eight steps or more, or four while all parts find an SM at once.  In one piece and cut
-// (D = 128, bf16):
+// in fp32, about 12 us, which fewer than 12 steps less (1 us each, 2 where SMs are few; 8 steps
+// under a mask) do not win back.  Parts are eight steps or more, or four while all parts find an SM at
+// once.  In one piece and cut (D = 128, bf16):
 //   causal, 4 items of 128 steps 234 us, in 4 parts 75, in 16 (the rule) 34; 16 of 512 899, in 4 245, in
 //   11 122; 64 of 128 236, in 3 120; 128 of 128 239, in 2 218, in 3 227; 160 of 160 300, in 2 324;
 //   256 of 256 706, in 2 751; 8 of 32 64, in 4 29, in 8 23; 32 of 32 66, in 4 38, in 6 41
+//   64 of 16 36, in 2 31 (without a mask 36 and 40)
 //   no mask, 32 of 256 457, in 3 212; 64 of 128 235, in 2 222, in 3 232; 96 of 384 798, in 2 819
 //   4 x 4 heads of 1024 at D = 64 (128 of 8) 25 us, in 2 38
 int64_t bwd_splits(const gsr_attention_desc* d, bool unequal) {
@@ -277,7 +278,7 @@ int64_t bwd_splits(const gsr_attention_desc* d, bool unequal) {
     int64_t n = (int64_t)std::ceil((double)kSms / (1.72 * left * (double)items) - 0.2);   // a fifth over is not worth it
     const int64_t at_once = std::min(steps / 4, kSms / items);
     n = std::min({n, std::max(steps / 8, at_once), (int64_t)32});
-    return n > 1 && steps - steps / n >= 12 ? n : 1;
+    return n > 1 && steps - steps / n >= (unequal ? 8 : 12) ? n : 1;
 }
 
 // Layout of the backward pass's workspace, 256-byte pieces.
