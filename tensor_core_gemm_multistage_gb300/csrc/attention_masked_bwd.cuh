@@ -35,13 +35,15 @@ namespace gsr {
 template <class T>
 constexpr float kPShift = Elem<T>::bf16 ? 0.0f : 12.0f;      // log2 of P's factor
 
-// log2 of dS's further factor.
-template <class T>
+// log2 of dS's further factor.  A capped dS is held without its factor 4 (weights_chunk), which leaves
+// room for two more bits.
+template <class T, int MODE>
 __device__ __forceinline__ float ds_shift(const unsigned* norms) {
     if (Elem<T>::bf16) return 0.0f;
     const float n = __uint_as_float(__ldcg(norms)) * __uint_as_float(__ldcg(norms + 1));   // squares of the bound's factors
     if (!(n > 0.0f && n < INFINITY)) return 0.0f;
-    return fminf(fmaxf(floorf(2.0f - 0.5f * log2f(n)), -100.0f), 100.0f);    // 15 - 12 - 1 - log2(bound / 2)
+    const float room = kHasCap<MODE> ? 4.0f : 2.0f;                          // 15 - 12 - 1, and the cap's 2
+    return fminf(fmaxf(floorf(room - 0.5f * log2f(n)), -100.0f), 100.0f);    // less log2(bound / 2)
 }
 
 // What a row's exponent offset holds beside -lse: P's power of two, and the constant of a capped
@@ -690,7 +692,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int r = quad * 32 + lane;                  // key of the tile
         const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
         const uint32_t s_col = lane_base + Cfg::T_S + half * 64, dp_col = lane_base + Cfg::T_DP + half * 64;
-        const float shift = ds_shift<T>(p.norms), ds_mul = exp2f(shift);
+        const float shift = ds_shift<T, Cfg::MODE>(p.norms), ds_mul = exp2f(shift);
         uint32_t n_box = 0, n = 0, n_done = 0;
         bool ok = true;
         while (ok) {
@@ -1100,7 +1102,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int r = quad * 32 + lane;                  // query of the tile
         const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
         const uint32_t s_col = lane_base + Cfg::T_S + half * 64;
-        const float shift = ds_shift<T>(p.norms);
+        const float shift = ds_shift<T, Cfg::MODE>(p.norms);
         uint32_t n_box = 0, n = 0, n_done = 0;
         bool ok = true;
         while (ok) {

@@ -134,6 +134,7 @@ CASES = {
     "few_queries_two_way": dict(B=2, Hq=2, Hkv=1, Sq=130, Skv=2600, D=64, cap=3.0),
     "few_heads": dict(B=1, Hq=2, Hkv=1, Sq=1500, Skv=1500, D=128, causal=True, alibi=True, prefix=[300]),
     "few_heads_docs": dict(B=1, Hq=2, Hkv=2, Sq=2000, Skv=2000, D=64, causal=True, docs=[[3, 900, 901, 1990]], dtype=BF16),
+    "far_keys_capped": dict(B=1, Hq=2, Hkv=2, Sq=21, Skv=16808, D=64, causal=True, cap=2.0, alibi=True, seed=42),
     "small_gradients": dict(B=1, Hq=2, Hkv=1, Sq=600, Skv=600, D=128, grad=2.0 ** -11),
     "large_gradients": dict(B=1, Hq=2, Hkv=1, Sq=300, Skv=300, D=64, grad=2.0 ** 7, causal=True),
 }
