@@ -8,7 +8,8 @@
 // dK and dV of a key/value head sum over the query heads of its group.
 //
 // Three launches: one pass over the rows (delta), then dK and dV by the CTA that owns the keys and
-// dQ by the CTA that owns the queries (and a fourth where dK and dV are cut into parts).  The two
+// dQ by the CTA that owns the queries (one more where dK and dV are cut into parts; a tiny one ahead in
+// fp16).  The two
 // recompute S and dP, seven products of 128 x 128 x D instead of the five that one pass with atomically
 // added dQ would take; in return no result depends on the order of atomics, dQ needs no fp32 buffer,
 // and every accumulator stays in TMEM from the first product to the last.  dQ's CTAs start on the SMs that
@@ -92,6 +93,7 @@ __device__ __forceinline__ void max_norm(unsigned* to, float n, int lane) {
 
 template <class T, int D>
 __global__ void __launch_bounds__(256) gsr_masked_bwd_rows_kernel(const __grid_constant__ MaskedBwdParams p) {
+    grid_launch_next();                                  // dK's and dV's CTAs set up meanwhile
     constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, N = kWarpRows / AT_ONCE;
     const int lane = threadIdx.x & 31, sub = lane / LANES, piece = lane % LANES;
     const MaskArgs& mk = p.mask;
@@ -134,7 +136,10 @@ __global__ void __launch_bounds__(256) gsr_masked_bwd_rows_kernel(const __grid_c
             p.offset[row] = keys ? row_offset<T>(p.score) - lse * kLog2e : -INFINITY;
             p.neg_delta[row] = keys ? -delta : 0.0f;
         }
-        if (!Elem<T>::bf16) max_norm(p.norms, keys ? norm : 0.0f, lane);
+        if (!Elem<T>::bf16) {
+            grid_wait();                                 // the norms are zero
+            max_norm(p.norms, keys ? norm : 0.0f, lane);
+        }
         return;
     }
     id -= q_groups;
@@ -156,8 +161,18 @@ __global__ void __launch_bounds__(256) gsr_masked_bwd_rows_kernel(const __grid_c
             const float q = lanes_sum<LANES>(dot8<T>(x[n], x[n]));
             if (q < INFINITY && (rows_seen >> (n * AT_ONCE + sub) & 1u)) most = fmaxf(most, q);
         }
+        grid_wait();
         max_norm(p.norms + 1, most, lane);
+    } else if (!Elem<T>::bf16) {
+        grid_wait();                                     // dK's and dV's launch waits for this one, and so for the zeros
     }
+}
+
+// The norms' start (fp16).  The rows' launch does all but its maxima meanwhile; a memset in its place would
+// hold it up (2 x 6 heads over 3 of 333 rows, captured: 28.5 us with one, 24.6 with this).
+static __global__ void __launch_bounds__(32) gsr_masked_bwd_norms_kernel(unsigned* norms) {
+    grid_launch_next();
+    if (threadIdx.x < 2) norms[threadIdx.x] = 0u;
 }
 
 // Zero rows of a strided output (no queries, or no keys).  One warp per row.
@@ -1211,9 +1226,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
-// The rows, then dK and dV, then dQ, then the sums of parts.  dK and dV start while the rows' last CTAs
-// finish and wait for them; dQ's CTAs need the rows alone (finished when dK's and dV's CTAs have come
-// past their wait, which is when dQ's may start) and fill the SMs that run out of dK and dV items.
+// The norms' start (fp16), the rows, then dK and dV, then dQ, then the sums of parts.  The rows load while
+// the norms start; dK's and dV's CTAs set up while the rows run, and wait for them; dQ's CTAs need the
+// rows alone (finished when dK's and dV's CTAs have come past their wait, which is when dQ's may start)
+// and fill the SMs that run out of dK and dV items.
 template <class T, int D, int MODE>
 cudaError_t launch_bwd_mode(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream) {
     using Dkv = DkvCfg<T, D, MODE>;
@@ -1252,13 +1268,16 @@ cudaError_t launch_bwd_type(const MaskedBwdMaps& tm, const MaskedBwdParams& p, c
         return cudaGetLastError();
     }
     long long warps = (long long)mk.B * mk.Hq * (p.Sp / kWarpRows);
-    if (!Elem<T>::bf16) {
-        const cudaError_t e = cudaMemsetAsync(p.norms, 0, 2 * sizeof(unsigned), stream);
-        if (e != cudaSuccess) return e;
+    cudaError_t e;
+    if (Elem<T>::bf16) {
+        gsr_masked_bwd_rows_kernel<T, D><<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(p);
+        e = cudaGetLastError();
+    } else {
         warps += (long long)mk.B * mk.Hkv * ((mk.Skv + kWarpRows - 1) / kWarpRows);
+        gsr_masked_bwd_norms_kernel<<<1, 32, 0, stream>>>(p.norms);
+        if ((e = cudaGetLastError()) == cudaSuccess)
+            e = launch_early(gsr_masked_bwd_rows_kernel<T, D>, (unsigned)((warps + 7) / 8), 256, 0, stream, p);
     }
-    gsr_masked_bwd_rows_kernel<T, D><<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     switch (score_mode(p.score)) {
         case kScorePlain: return launch_bwd_mode<T, D, kScorePlain>(tm, p, stream);
