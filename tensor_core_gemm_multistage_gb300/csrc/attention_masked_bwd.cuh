@@ -93,7 +93,6 @@ __device__ __forceinline__ void max_norm(unsigned* to, float n, int lane) {
 
 template <class T, int D>
 __global__ void __launch_bounds__(256) gsr_masked_bwd_rows_kernel(const __grid_constant__ MaskedBwdParams p) {
-    grid_launch_next();                                  // dK's and dV's CTAs set up meanwhile
     constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, N = kWarpRows / AT_ONCE;
     const int lane = threadIdx.x & 31, sub = lane / LANES, piece = lane % LANES;
     const MaskArgs& mk = p.mask;
@@ -169,7 +168,7 @@ __global__ void __launch_bounds__(256) gsr_masked_bwd_rows_kernel(const __grid_c
 }
 
 // The norms' start (fp16).  The rows' launch does all but its maxima meanwhile; a memset in its place would
-// hold it up (2 x 6 heads over 3 of 333 rows, captured: 28.5 us with one, 24.6 with this).
+// hold it up (2 x 6 heads over 3 of 333 rows, captured: 28.5 us with one, 25.0 with this).
 static __global__ void __launch_bounds__(32) gsr_masked_bwd_norms_kernel(unsigned* norms) {
     grid_launch_next();
     if (threadIdx.x < 2) norms[threadIdx.x] = 0u;
@@ -1227,9 +1226,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // Launches
 // ---------------------------------------------------------------------------
 // The norms' start (fp16), the rows, then dK and dV, then dQ, then the sums of parts.  The rows load while
-// the norms start; dK's and dV's CTAs set up while the rows run, and wait for them; dQ's CTAs need the
-// rows alone (finished when dK's and dV's CTAs have come past their wait, which is when dQ's may start)
-// and fill the SMs that run out of dK and dV items.
+// the norms start.  dK's and dV's CTAs start while the rows' last ones finish, and wait for them (let in
+// while rows are still to come, they take SMs from them: 8192 tokens in 4 documents 395 us, so 408).  dQ's
+// CTAs need the rows alone (finished when dK's and dV's CTAs have come past their wait, which is when
+// dQ's may start) and fill the SMs that run out of dK and dV items.
 template <class T, int D, int MODE>
 cudaError_t launch_bwd_mode(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream) {
     using Dkv = DkvCfg<T, D, MODE>;
