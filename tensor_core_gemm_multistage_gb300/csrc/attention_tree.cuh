@@ -138,7 +138,7 @@ struct TreeCfg {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = OFF_Q + NQ * TILE_BYTES;
     static constexpr int OFF_BAR = OFF_RING + NB * TILE_BYTES;
-    static constexpr int NUM_BARS = 2 * NB + 17;
+    static constexpr int NUM_BARS = 2 * NB + 18;
     static constexpr int OFF_VALID = OFF_BAR + NUM_BARS * 8;       // per ring entry: which pieces of the tile exist
     static constexpr int OFF_ITEM = OFF_VALID + NB * 4;            // 2 x 12 ints
     static constexpr int OFF_SCAN = (OFF_ITEM + 96 + 7) / 8 * 8;   // 16 partial sums, then the CTA's first unit
@@ -194,6 +194,10 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
     auto item_read = [&](int i) { return bar(2 * NB + 10 + i); };
     const uint32_t q_full = bar(2 * NB + 12), q_free = bar(2 * NB + 13), drain = bar(2 * NB + 14), ml_full = bar(2 * NB + 15),
                    ml_free = bar(2 * NB + 16);
+    // The accumulators of an item have been read.  With one query tile both groups read both of them, so that the
+    // next item's first product, which overwrites accumulator 0, has to wait for the warps of group 1 too: the P it
+    // takes comes from group 0 alone.  Turns over once an item, and the issuing lane looks once an item.
+    const uint32_t o_read = bar(2 * NB + 17);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_MISC + 4);
     volatile int* item_box = reinterpret_cast<volatile int*>(smem + Cfg::OFF_ITEM);
@@ -232,6 +236,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
         mbar_init(ml_full, Cfg::SM_THREADS / 32);
         mbar_init(ml_free, Cfg::SM_THREADS / 32);
         mbar_init(drain, 1);
+        mbar_init(o_read, Cfg::SM_THREADS / 32);
         *abort_flag = 0u;
         fence_mbarrier_init();
     }
@@ -454,6 +459,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                         // K of step i and V of step i - 1
                         if (i < steps && !(ok = wait_full(2 * (n + i)))) break;
                         tcgen05_fence_after();
+                        // the first product of an item overwrites what the last one's rows were read from
+                        auto accumulators_read = [&] { return i != 1 || n_item == 1 || w.wait(o_read, n_item & 1u, kDevErrMmaFull); };
                         if (it.q_tiles == 1) {
                             // key tiles in turn: S(i) runs while the other group's softmax does
                             if (i < steps) {
@@ -464,7 +471,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                             if (i > 0) {
                                 const uint32_t m = n + i - 1;
                                 const int g = (i - 1) & 1;
-                                if (!(ok = wait_full(2 * m + 1) && issue_pv(g, g, m, i <= 2))) break;
+                                if (!(ok = wait_full(2 * m + 1) && accumulators_read() && issue_pv(g, g, m, i <= 2))) break;
                                 mma_commit(empty((int)((2 * m + 1) % NB)));
                                 if (i == steps) {
                                     mma_commit(odone(0, n_item - 1));
@@ -473,7 +480,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                             }
                         } else {
                             // a region per query tile: the tiles alternate on the tensor core
-                            if (i > 0 && !(ok = wait_full(2 * (n + i) - 1))) break;
+                            if (i > 0 && !(ok = wait_full(2 * (n + i) - 1) && accumulators_read())) break;
                             tcgen05_fence_after();
                             for (int q = 0; q < 2 && ok; ++q) {
                                 if (i > 0) {
@@ -731,6 +738,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
             }
             tcgen05_fence_before();
             __syncwarp();
+            if (lane == 0) mbar_arrive(o_read);
             for (uint32_t again = __ballot_sync(0xffffffffu, bad && real && it.slot < 0); again; again &= again - 1) {
                 const int src = __ffs(again) - 1;
                 tree_row<T, D>(p, it.b, tree_request(p, it.b), __shfl_sync(0xffffffffu, node, src), __shfl_sync(0xffffffffu, h, src),

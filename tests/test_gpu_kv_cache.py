@@ -283,6 +283,20 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(T):
     t.run().check()
 
 
+@pytest.mark.parametrize("kv,T,Hq,Hkv", [([1 + 7 * i % 128 for i in range(1500)], [1] * 1500, 16, 8),
+                                         ([40 + 11 * i % 90 for i in range(600)], [1 + 5 * i % 39 for i in range(600)], 16, 2)])
+def test_many_short_items_of_one_cta(kv, T, Hq, Hkv):
+    """Items of one or two key tiles follow one another on every CTA: one item's rows are read before the next one's
+    products overwrite them, so all runs give the same bits."""
+    t = Tree(kv=kv, T=T, Hq=Hq, Hkv=Hkv, D=64, page=16, dtype=BF16).run().check()
+    want = t.o.clone()
+    for _ in range(50):
+        for _ in range(10):
+            t.o.fill_(7.0)
+            gsr.tree_attention_fwd(*t.args, **t.kw)
+        assert gsr.device_status()[0] == gsr.Status.OK and torch.equal(t.o, want)
+
+
 def test_workspaces():
     t = Tree(kv=[3000, 77], T=[1, 9], Hq=8, Hkv=2, D=128, page=16).run().check()
     want = t.o.clone()
