@@ -205,7 +205,9 @@ typedef struct gsr_attention_desc {
  * K, V: batch x heads_kv x seq_kv x head_dim; lse: batch x heads_q x seq_q float32, contiguous
  * (NULL: not written), the natural log-sum-exp of the scores.  A query that sees no key gets O = 0
  * and lse = -inf.  Keys a query does not see have no influence on it, also when they hold
- * infinities or NaN.  Probabilities are rounded to the operands' type for the second product, the
+ * infinities or NaN.  An infinity or NaN in V makes its column infinite or NaN for every query that
+ * sees the key, however small the probability, and leaves the other columns and lse as they are; the
+ * time of a call grows little with them.  Probabilities are rounded to the operands' type for the second product, the
  * output once.  O must share no element with an input, lse lies apart from everything.
  *
  *   workspace  device pointer, 16-byte aligned, masked_attention_fwd_workspace(desc) bytes (0 where

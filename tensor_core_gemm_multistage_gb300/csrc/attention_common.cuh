@@ -29,6 +29,13 @@ struct Elem<__half> {
         const __half2 h = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
+    static constexpr uint32_t exponent = 0x7c00u;        // all of its bits set: infinite or NaN
+    // acc + 0 v: NaN from the first v on that is not finite
+    static __device__ __forceinline__ uint32_t fma_zero(uint32_t v, uint32_t acc) {
+        const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&v), __half2half2(__ushort_as_half(0)),
+                                  *reinterpret_cast<const __half2*>(&acc));
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
 };
 template <>
 struct Elem<__nv_bfloat16> {
@@ -38,6 +45,12 @@ struct Elem<__nv_bfloat16> {
     }
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    static constexpr uint32_t exponent = 0x7f80u;
+    static __device__ __forceinline__ uint32_t fma_zero(uint32_t v, uint32_t acc) {
+        const __nv_bfloat162 h = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v), __bfloat162bfloat162(__ushort_as_bfloat16(0)),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&acc));
         return *reinterpret_cast<const uint32_t*>(&h);
     }
 };
@@ -348,6 +361,155 @@ cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
     return e;
+}
+
+// ---------------------------------------------------------------------------
+// Infinities and NaN behind a mask
+// ---------------------------------------------------------------------------
+// A masked pair has weight 0 in the matrix products, and 0 times an infinity or NaN would put a NaN into
+// a result that does not see it.  In a tile that not every row of the product sees whole (an edge; elsewhere
+// nothing is hidden), the elements of the weighted operand that are not finite are set to zero in
+// shared memory before the product.  What they mean to the rows that do see them is added after the
+// rows have been written: there a column with such an element is infinite or NaN, whatever its weight.
+// Both steps cost by the tile and not by the pair, so a call with infinities takes about as long as one
+// without.
+
+// Whether 16-byte pieces in shared memory, a multiple of 256, hold something not finite.  By one warp.
+template <class T>
+__device__ __forceinline__ bool pieces_not_finite(const uint8_t* at, int pieces, int lane) {
+    const uint4* p = reinterpret_cast<const uint4*>(at) + lane;
+    uint32_t acc[4] = {0u, 0u, 0u, 0u};
+    for (int i = 0; i < pieces; i += 256) {
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = p[i + 32 * k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            acc[0] = Elem<T>::fma_zero(v[k].x, acc[0]);
+            acc[1] = Elem<T>::fma_zero(v[k].y, acc[1]);
+            acc[2] = Elem<T>::fma_zero(v[k].z, acc[2]);
+            acc[3] = Elem<T>::fma_zero(v[k].w, acc[3]);
+        }
+    }
+    return __any_sync(0xffffffffu, ((acc[0] | acc[1] | acc[2] | acc[3]) & (Elem<T>::exponent * 0x10001u)) != 0u);
+}
+
+// Sets what is not finite there to zero; true if there was something.  By one warp; the caller fences before the
+// product.
+template <class T>
+__device__ __forceinline__ bool zero_not_finite(uint8_t* at, int pieces, int lane) {
+    constexpr uint32_t E = Elem<T>::exponent;
+    bool any = false;
+#pragma unroll 1
+    for (int i = lane; i < pieces; i += 32) {
+        uint4 v = reinterpret_cast<uint4*>(at)[i];
+        uint32_t* w = &v.x;
+        bool found = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if ((w[k] & E) == E) {
+                w[k] &= 0xffff0000u;
+                found = true;
+            }
+            if ((w[k] >> 16 & E) == E) {
+                w[k] &= 0x0000ffffu;
+                found = true;
+            }
+        }
+        if (found) reinterpret_cast<uint4*>(at)[i] = v;
+        any |= found;
+    }
+    return __any_sync(0xffffffffu, any);
+}
+
+// One value more in a sum that is held rounded to T, or in fp32.
+template <class T>
+__device__ __forceinline__ void add_to(uint16_t* to, float x) {
+    *to = (uint16_t)Elem<T>::pack(Elem<T>::unpack(*to).x + x, 0.0f);
+}
+template <class T>
+__device__ __forceinline__ void add_to(float* to, float x) {
+    *to += x;
+}
+
+// This lane's result row: which columns rows that it sees make +inf and -inf, both for NaN.
+template <int D>
+struct Marks {
+    uint32_t plus[D / 32], minus[D / 32];
+    __device__ __forceinline__ Marks() {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) plus[c] = minus[c] = 0u;
+    }
+    // A row of the weighted operand, one for the whole warp; `sees`: this lane's result row sees it.
+    // NAN_ONLY: whatever is not finite there makes the column NaN (the weights are not finite either, or 0).
+    template <class T, bool NAN_ONLY, int ROWS>
+    __device__ __forceinline__ void take(const uint16_t (&x)[ROWS][D / 32], const bool (&sees)[ROWS]) {
+        constexpr uint32_t E = Elem<T>::exponent;
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                const uint32_t v = x[k][c];
+                const bool special = (v & E) == E, nan = special && (NAN_ONLY || (v & 0x7fffu) != E);
+                const uint32_t up = __ballot_sync(0xffffffffu, special && (nan || !(v & 0x8000u)));
+                const uint32_t down = __ballot_sync(0xffffffffu, special && (nan || (v & 0x8000u)));
+                if (sees[k]) {
+                    plus[c] |= up;
+                    minus[c] |= down;
+                }
+            }
+    }
+    // Into the row, which this lane has written; Out is uint16_t (a T) or float.
+    template <class T, class Out>
+    __device__ __forceinline__ void apply(Out* row) const {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+            for (uint32_t bits = plus[c] | minus[c]; bits; bits &= bits - 1) {
+                const int e = __ffs(bits) - 1;
+                const float x = (plus[c] >> e & 1u) ? ((minus[c] >> e & 1u) ? NAN : INFINITY) : -INFINITY;
+                add_to<T>(row + c * 32 + e, x);
+            }
+    }
+};
+
+// Whether one of rows [r0, r1), `pitch` elements apart, holds something not finite.  By one warp.
+template <class T, int D>
+__device__ __noinline__ bool rows_not_finite(const T* rows, long long pitch, int r0, int r1, int lane) {
+    constexpr int PIECES = D / 8, ROWS = 32 / PIECES;    // 16-byte pieces of a row, rows at once
+    uint32_t acc = 0u;
+    rows += lane % PIECES * 8;
+    for (int r = r0 + lane / PIECES; r < r1; r += 16 * ROWS) {
+        uint4 x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(rows + min(r + i * ROWS, r1 - 1) * pitch));
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            acc = Elem<T>::fma_zero(x[i].x, Elem<T>::fma_zero(x[i].y, Elem<T>::fma_zero(x[i].z, Elem<T>::fma_zero(x[i].w, acc))));
+    }
+    return __any_sync(0xffffffffu, (acc & (Elem<T>::exponent * 0x10001u)) != 0u);
+}
+
+// Rows [r0, r1) of the weighted operand (`pitch` elements apart), and this lane's result row, which sees those
+// in [lo, hi) (`write`: it exists).  The whole warp calls it.
+template <class T, int D, bool NAN_ONLY, class Out>
+__device__ __noinline__ void spread_not_finite(const T* rows, long long pitch, int r0, int r1, int lo, int hi, Out* row, bool write,
+                                               int lane) {
+    if (!rows_not_finite<T, D>(rows, pitch, r0, r1, lane)) return;
+    Marks<D> marks;
+    for (int r = r0; r < r1; r += 4) {
+        uint16_t x[4][D / 32];
+        bool sees[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int at = min(r + k, r1 - 1);
+            sees[k] = at >= lo && at < hi;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+                x[k][c] = __ldg(reinterpret_cast<const unsigned short*>(rows) + at * pitch + c * 32 + lane);
+        }
+        marks.template take<T, NAN_ONLY, 4>(x, sees);
+    }
+    if (write) marks.template apply<T>(row);
 }
 
 // ---------------------------------------------------------------------------

@@ -21,8 +21,13 @@
 //    leaves its part (maximum, sum, O in fp32) in the workspace, and a second launch joins them.
 //
 // Masked scores are replaced by -inf, so what K holds there is never used.  A masked V row enters
-// the product as 0 V, which is NaN where V is not finite: a row whose output is not finite is
-// computed again by its warp from the keys it sees alone (masked_row).
+// the product as 0 V, which is NaN where V is not finite.  Only edge tiles, those that not all rows of the item
+// see whole, have masked rows.  An item with a row that is not finite, and with something in the V of its edge
+// tiles that is not finite either, goes on a list, and after its last item the CTA runs those of the list again
+// with edge tiles cleaned before they are handed on ("Infinities and NaN behind a mask" in attention_common.cuh).
+// A CTA whose list is full takes over no further CTA; those left start in its place.  The second run is a copy of
+// the code of its own: what the first one would need for it in its loops costs 2 to 9 %, and cleaning every edge
+// tile at once, which needs no second run, 5 to 15 %, since V lands late in an item's last tiles.
 #pragma once
 
 #include <atomic>
@@ -54,10 +59,13 @@ struct MaskedFwdCfg {
     static constexpr int OFF_K = OFF_Q + QBUF * NQ * Q_BYTES;   // ring of 2 entries {K_t, V_(t-1)}
     static constexpr int OFF_V = OFF_K + 2 * KV_BYTES;
     static constexpr int OFF_BAR = OFF_V + 2 * KV_BYTES;
-    static constexpr int NUM_BARS = 20;
+    static constexpr int NUM_BARS = 22;
     static constexpr int OFF_CLC = OFF_BAR + NUM_BARS * 8;      // 16-byte aligned
     static constexpr int OFF_ITEM = OFF_CLC + 16;               // 2 x 12 ints
-    static constexpr int OFF_MISC = OFF_ITEM + 96;
+    static constexpr int AGAIN = 30;                            // items to run again
+    static constexpr int OFF_AGAIN = OFF_ITEM + 96;             // their count, the last four that went there, 3 words each
+    static constexpr int OFF_BAR_AGAIN = OFF_AGAIN + 24 + AGAIN * 12;   // the second run's barriers
+    static constexpr int OFF_MISC = OFF_BAR_AGAIN + NUM_BARS * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16;
     static constexpr int TMEM_COLS = 512;
     static constexpr uint32_t T_S = 0, T_O = 256, P_COL = 64;
@@ -69,44 +77,91 @@ struct MaskedFwdCfg {
     static_assert(T_O + NQ * D <= TMEM_COLS, "TMEM budget");
 };
 
-// One query row by one warp: every key it sees, in fp32.
-template <class T, int D>
-__device__ __noinline__ void masked_row(const MaskedFwdParams& p, int b, int h, int i, int lane) {
-    const int hk = h / p.mask.group;
-    float q[D / 32], acc[D / 32], m, l;
-    load_row<T, D>(static_cast<const T*>(p.Q.data) + b * p.Q.batch + h * p.Q.head + i * p.Q.row, lane, q);
-    const T* kb = static_cast<const T*>(p.K.data) + b * p.K.batch + hk * p.K.head;
-    const T* vb = static_cast<const T*>(p.V.data) + b * p.V.batch + hk * p.V.head;
-    const float slope2 = p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
-    int lo, hi;
-    row_interval(p.mask, b, i, lo, hi);
-    const int pos = i + p.mask.offset;
-    row_forward<T, D>(q, lo, hi, p.score, slope2, lane,
-                      [&](int j, const T*& k, const T*& v, float& dist) {
-                          k = kb + j * p.K.row;
-                          v = vb + j * p.V.row;
-                          dist = fabsf((float)(pos - j));
-                          return true;
-                      },
-                      acc, m, l);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[e] *= inv;
-    store_row<T, D>(static_cast<T*>(p.O.data) + b * p.O.batch + h * p.O.head + i * p.O.row, lane, acc);
-    if (p.lse && lane == 0)
-        p.lse[((long long)b * p.mask.Hq + h) * p.mask.Sq + i] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
 // Part `split` of a row in the workspace.
 __device__ __forceinline__ long long part_index(const MaskedFwdParams& p, int b, int h, int split, int i) {
     return (((long long)b * p.mask.Hq + h) * p.splits + split) * p.mask.Sq + i;
 }
 
-// This thread's row of a part (`real`), the accumulator from TMEM column `col` on if there were steps.  Kept
-// out of the kernel's own code, whose runs without parts it made 1 to 2 % slower.
+// The keys that every row of an item (two query tiles) with keys sees; a row without any among them leaves none.
+// Lane 2q brings lo and hi of tile q's first row, lane 2q + 1 of its last.
+struct Common {
+    int lo, hi;
+    // Whether not all rows see the key tile whole.
+    __device__ __forceinline__ bool edge(int key_tile) const { return key_tile * 128 < lo || (key_tile + 1) * 128 > hi; }
+};
+__device__ __forceinline__ Common common_keys(int lo, int hi) {
+    Common c{0, INT_MAX};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int first_lo = __shfl_sync(0xffffffffu, lo, 2 * q), first_hi = __shfl_sync(0xffffffffu, hi, 2 * q);
+        const int last_lo = __shfl_sync(0xffffffffu, lo, 2 * q + 1), last_hi = __shfl_sync(0xffffffffu, hi, 2 * q + 1);
+        if (first_lo < last_hi) {
+            c.lo = max(c.lo, last_lo);
+            c.hi = min(c.hi, first_hi);
+        }
+    }
+    return c;
+}
+// The interval that lane `lane` of an item brings there (empty outside [0, Sq)).
+__device__ __forceinline__ void item_interval(const MaskArgs& mk, int b, int q_base, int lane, int& lo, int& hi) {
+    lo = hi = 0;
+    const int first = q_base + (lane >> 1 & 1) * 128;
+    const int row = lane & 1 ? min(first + 128, mk.Sq) - 1 : first;
+    if (lane < 4 && first < mk.Sq) row_interval(mk, b, row, lo, hi);
+}
+
+// A softmax warp's rows of item n are written.  In the second run (SECOND) they get what they still lack: the columns
+// that V cleaned from edge tiles makes infinite or NaN.  In the first one of them is not finite, and the item goes
+// on the list if the V of its edge tiles is not finite either.
+template <class Cfg, bool SECOND>
+__device__ __noinline__ void after_item(const MaskedFwdParams& p, uint32_t n, int b, int h, int q_base, int split) {
+    using T = typename Cfg::T;
+    constexpr int D = Cfg::D;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const MaskArgs& mk = p.mask;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = (warp - 4) >> 2;
+    const int qi = q_base + q * 128 + (warp & 3) * 32 + lane;
+    int lo, hi;
+    item_interval(mk, b, q_base, lane, lo, hi);
+    const Common common = common_keys(lo, hi);
+    const int k0 = __shfl_sync(0xffffffffu, lo, 2 * q) / 128, k1 = (__shfl_sync(0xffffffffu, hi, 2 * q + 1) + 127) / 128;
+    const T* v = static_cast<const T*>(p.V.data) + b * p.V.batch + h / mk.group * p.V.head;
+    lo = hi = 0;
+    if (qi < mk.Sq) row_interval(mk, b, qi, lo, hi);
+    for (int k = k0; k < k1; ++k) {
+        if (!common.edge(k)) continue;
+        const int end = min((k + 1) * 128, mk.Skv);
+        if constexpr (SECOND) {
+            if (p.splits > 1)
+                spread_not_finite<T, D, false>(v, p.V.row, k * 128, end, lo, hi, p.parts + part_index(p, b, h, split, qi) * D,
+                                               qi < mk.Sq, lane);
+            else
+                spread_not_finite<T, D, false>(v, p.V.row, k * 128, end, lo, hi,
+                                               static_cast<uint16_t*>(p.O.data) + b * p.O.batch + h * p.O.head + (long long)qi * p.O.row,
+                                               qi < mk.Sq, lane);
+        } else {
+            if (rows_not_finite<T, D>(v, p.V.row, k * 128, end, lane)) {
+                // words: the count, then where item n puts n (n + 4 is published once every softmax warp is past n), the list
+                uint32_t* words = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_AGAIN);
+                if (lane == 0 && atomicExch(words + 1 + (n & 3u), n) != n) {
+                    uint32_t* to = words + 6 + 3 * atomicAdd(words, 1u);
+                    to[0] = b * mk.Hq + h;
+                    to[1] = q_base;
+                    to[2] = split;
+                }
+                break;
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// This thread's row of a part (`real`), the accumulator from TMEM column `col` on if there were steps; true if it is
+// not finite.  Kept out of the kernel's own code, whose runs without parts it made 1 to 2 % slower.
 template <int D>
-__device__ __noinline__ void store_part(const MaskedFwdParams& p, long long part, bool steps, bool real, uint32_t col, float m,
+__device__ __noinline__ bool store_part(const MaskedFwdParams& p, long long part, bool steps, bool real, uint32_t col, float m,
                                         float l) {
+    float z0 = 0.0f, z1 = 0.0f;                          // 0 x, NaN where x is not finite
     if (steps) {
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -114,6 +169,8 @@ __device__ __noinline__ void store_part(const MaskedFwdParams& p, long long part
             __syncwarp();
             tmem_ld_32x32b_x32(col + c * 32, rr);
             tmem_ld_wait(rr);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) ffma2(z0, z1, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]), 0.0f, 0.0f, z0, z1);
             if (real)
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
@@ -122,6 +179,7 @@ __device__ __noinline__ void store_part(const MaskedFwdParams& p, long long part
     }
     if (real) p.parts_ml[part] = make_float2(m, l);
     tcgen05_fence_before();
+    return z0 + z1 != 0.0f;
 }
 
 // Rows from their parts, one warp each, in the parts' order; lane s holds the factor of part s.
@@ -140,26 +198,19 @@ __global__ void __launch_bounds__(256) gsr_masked_fwd_join_kernel(const __grid_c
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float f = m == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
     const float l = warp_sum(f == 0.0f && ml.y == ml.y ? 0.0f : ml.y * f);
+    const float factor = ml.x == -INFINITY ? -1.0f : f;  // below 0: a part without keys that the row sees
     float acc[D / 32] = {};
 #pragma unroll 4
     for (int s = 0; s < p.splits; ++s) {
-        const float fs = __shfl_sync(0xffffffffu, f, s);
-        if (fs == 0.0f) continue;                        // may hold anything
+        const float fs = __shfl_sync(0xffffffffu, factor, s);
+        if (fs < 0.0f) continue;                         // may hold anything
         const V x = *(reinterpret_cast<const V*>(p.parts + part_index(p, b, h, s, i) * D) + lane);
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(reinterpret_cast<const float*>(&x)[e], fs, acc[e]);
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    bool bad = !(l < INFINITY);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-        bad |= !(fabsf(acc[e]) < INFINITY);
-        acc[e] *= inv;
-    }
-    if (__any_sync(0xffffffffu, bad)) {
-        masked_row<T, D>(p, b, h, i, lane);
-        return;
-    }
+    for (int e = 0; e < D / 32; ++e) acc[e] *= inv;
     store_row<T, D>(static_cast<T*>(p.O.data) + b * p.O.batch + h * p.O.head + (long long)i * p.O.row, lane, acc);
     if (p.lse && lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
@@ -176,6 +227,42 @@ __global__ void __launch_bounds__(256) gsr_masked_empty_kernel(const MaskedFwdPa
     if (p.lse && (threadIdx.x & 31) == 0) p.lse[row] = -INFINITY;
 }
 
+// The barriers of one run, from shared address `at` on.
+struct FwdBars {
+    uint32_t at;
+    __device__ __forceinline__ uint32_t bar(int i) const { return at + 8u * i; }
+    __device__ __forceinline__ uint32_t full(int s) const { return bar(0 + s); }
+    __device__ __forceinline__ uint32_t empty(int s) const { return bar(2 + s); }
+    __device__ __forceinline__ uint32_t sfull(int q) const { return bar(4 + q); }
+    __device__ __forceinline__ uint32_t pfull(int q) const { return bar(6 + q); }
+    __device__ __forceinline__ uint32_t odone(int q) const { return bar(8 + q); }
+    __device__ __forceinline__ uint32_t item_pub(int i) const { return bar(10 + i); }
+    __device__ __forceinline__ uint32_t item_read(int i) const { return bar(12 + i); }
+    __device__ __forceinline__ uint32_t qfull(int b) const { return bar(14 + b); }
+    __device__ __forceinline__ uint32_t qfree(int b) const { return bar(16 + b); }
+    __device__ __forceinline__ uint32_t clc() const { return bar(18); }
+    __device__ __forceinline__ uint32_t drain() const { return bar(19); }
+    __device__ __forceinline__ uint32_t landed() const { return bar(20); }       // a ring entry that is cleaned before it is full
+    // by one thread
+    __device__ __forceinline__ void init(int softmax_warps) const {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+            mbar_init(sfull(s), 1);
+            mbar_init(pfull(s), 128);
+            mbar_init(odone(s), 1);
+            mbar_init(item_pub(s), 1);
+            mbar_init(item_read(s), 1 + softmax_warps);          // the MMA lane and every softmax warp
+            mbar_init(qfull(s), 1);
+            mbar_init(qfree(s), 1);
+        }
+        mbar_init(clc(), 1);
+        mbar_init(drain(), 1);
+        mbar_init(landed(), 1);
+        fence_mbarrier_init();
+    }
+};
+
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
     gsr_masked_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -189,20 +276,10 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
         return;
     }
     const uint32_t sb = smem_u32(smem);
-    auto bar = [&](int i) { return sb + Cfg::OFF_BAR + 8u * i; };
-    auto full = [&](int s) { return bar(0 + s); };
-    auto empty = [&](int s) { return bar(2 + s); };
-    auto sfull = [&](int q) { return bar(4 + q); };
-    auto pfull = [&](int q) { return bar(6 + q); };
-    auto odone = [&](int q) { return bar(8 + q); };
-    auto item_pub = [&](int i) { return bar(10 + i); };
-    auto item_read = [&](int i) { return bar(12 + i); };
-    auto qfull = [&](int b) { return bar(14 + b); };
-    auto qfree = [&](int b) { return bar(16 + b); };
-    const uint32_t clc = bar(18), drain = bar(19);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_MISC + 4);
     volatile int* item_box = reinterpret_cast<volatile int*>(smem + Cfg::OFF_ITEM);
+    volatile uint32_t* again_words = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_AGAIN);   // after_item
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -229,21 +306,9 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
     };
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
-            mbar_init(sfull(s), 1);
-            mbar_init(pfull(s), 128);
-            mbar_init(odone(s), 1);
-            mbar_init(item_pub(s), 1);
-            mbar_init(item_read(s), 1 + Cfg::SM_THREADS / 32);   // the MMA lane and every softmax warp
-            mbar_init(qfull(s), 1);
-            mbar_init(qfree(s), 1);
-        }
-        mbar_init(clc, 1);
-        mbar_init(drain, 1);
+        FwdBars{sb + Cfg::OFF_BAR}.init(Cfg::SM_THREADS / 32);
+        for (int i = 0; i < 5; ++i) again_words[i] = 0u;
         *abort_flag = 0u;
-        fence_mbarrier_init();
     }
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmQ);
@@ -260,219 +325,265 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
     const uint32_t tmem_base = *tmem_slot;
     const Waiter w{p.err, p.timeout_ns, abort_flag, kDevErrKernelMaskedFwd};
 
-    if (warp < 4) {
-        reg_dec<Cfg::CONTROL_REGS>();
-        if (warp == 0) {
-            // ------------------------------------------------------------ items + TMA producer
-            // The whole warp walks the items (lanes 0-3 find the intervals of the query tiles' first
-            // and last rows); lane 0 waits, publishes and copies.
-            const uint64_t pol = l2_policy_evict_last();     // K and V are read by every query block
-            const int n_qb = (mk.Sq + NQ * Cfg::BQ - 1) / (NQ * Cfg::BQ);
-            uint32_t n_pub = 0, n_q = 0, g = 0, n_clc = 0;   // items published, Q loads, ring entries, answers
-            uint32_t armed = 0, parity = 0, q_armed = 0, q_parity = 0;
-            bool drop_q = (p.test_flags & kTestDropFirstLoad) && blockIdx.x == 0;
-            bool asked = false;
-            int item = blockIdx.x;
-            while (true) {
-                Item it{-1, 0, 0, {0, 0}, {0, 0}, -1, 0};
-                if (item >= 0) {
-                    // query blocks from the last (under a causal mask the longest) to the first, in
-                    // groups of heads whose K and V stay in L2 together
-                    const int per_group = p.head_group * n_qb * p.splits, grp = item / per_group, r_in = item - grp * per_group;
-                    const int gsz = min(mk.B * mk.Hq - grp * p.head_group, p.head_group);
-                    const int bh = grp * p.head_group + r_in % gsz;
-                    it.b = bh / mk.Hq;
-                    it.h = bh - it.b * mk.Hq;
-                    it.split = r_in / gsz % p.splits;
-                    it.q_base = (n_qb - 1 - r_in / gsz / p.splits) * NQ * Cfg::BQ;
-                    // lane 2q: first row of tile q, lane 2q + 1: its last row
-                    int lo = 0, hi = 0;
-                    const int first = it.q_base + (lane >> 1 & 1) * Cfg::BQ;
-                    const int row = lane & 1 ? min(first + Cfg::BQ, mk.Sq) - 1 : first;
-                    if (lane < 4 && first < mk.Sq) row_interval(mk, it.b, row, lo, hi);
+    auto produce = [&](auto run) {
+        constexpr bool SECOND = decltype(run)::value;
+        const FwdBars bars{sb + (SECOND ? Cfg::OFF_BAR_AGAIN : Cfg::OFF_BAR)};
+        // ------------------------------------------------------------ items + TMA producer
+        // The whole warp walks the items (lanes 0-3 find the intervals of the query tiles' first
+        // and last rows); lane 0 waits, publishes and copies.
+        const uint64_t pol = l2_policy_evict_last();     // K and V are read by every query block
+        const int n_qb = (mk.Sq + NQ * Cfg::BQ - 1) / (NQ * Cfg::BQ);
+        uint32_t n_pub = 0, n_q = 0, g = 0, n_clc = 0;   // items published, Q loads, ring entries, answers
+        uint32_t armed = 0, parity = 0, q_armed = 0, q_parity = 0;
+        bool drop_q = !SECOND && (p.test_flags & kTestDropFirstLoad) && blockIdx.x == 0;
+        bool asked = false, landing = false;
+        int item = SECOND ? 0 : blockIdx.x;              // the second run: place in the list
+        const int n_again = SECOND ? (int)again_words[0] : 0;
+        while (true) {
+            Item it{-1, 0, 0, {0, 0}, {0, 0}, -1, 0};
+            Common common{0, INT_MAX};
+            if (SECOND && item == n_again) item = -1;
+            if (item >= 0) {
+                // query blocks from the last (under a causal mask the longest) to the first, in
+                // groups of heads whose K and V stay in L2 together
+                const int per_group = p.head_group * n_qb * p.splits, grp = item / per_group, r_in = item - grp * per_group;
+                const int gsz = min(mk.B * mk.Hq - grp * p.head_group, p.head_group);
+                int bh = grp * p.head_group + r_in % gsz;
+                it.split = r_in / gsz % p.splits;
+                it.q_base = (n_qb - 1 - r_in / gsz / p.splits) * NQ * Cfg::BQ;
+                if (SECOND) {
+                    bh = (int)again_words[6 + 3 * item];
+                    it.q_base = (int)again_words[6 + 3 * item + 1];
+                    it.split = (int)again_words[6 + 3 * item + 2];
+                }
+                it.b = bh / mk.Hq;
+                it.h = bh - it.b * mk.Hq;
+                int lo, hi;
+                item_interval(mk, it.b, it.q_base, lane, lo, hi);
+                if (SECOND) common = common_keys(lo, hi);
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    const int l = __shfl_sync(0xffffffffu, lo, 2 * q), e = __shfl_sync(0xffffffffu, hi, 2 * q + 1);
+                    it.t0[q] = l / Cfg::BKV;
+                    it.t1[q] = e > l ? (e + Cfg::BKV - 1) / Cfg::BKV : it.t0[q];
+                }
+                if (kHasBias<Cfg::MODE> && mk.causal) {
+                    const int both = it.first() + it.last();
+                    it.flip = both - 1;
 #pragma unroll
                     for (int q = 0; q < NQ; ++q) {
-                        const int l = __shfl_sync(0xffffffffu, lo, 2 * q), e = __shfl_sync(0xffffffffu, hi, 2 * q + 1);
-                        it.t0[q] = l / Cfg::BKV;
-                        it.t1[q] = e > l ? (e + Cfg::BKV - 1) / Cfg::BKV : it.t0[q];
-                    }
-                    if (kHasBias<Cfg::MODE> && mk.causal) {
-                        const int both = it.first() + it.last();
-                        it.flip = both - 1;
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q) {
-                            const int t0 = it.t0[q];
-                            it.t0[q] = both - it.t1[q];
-                            it.t1[q] = both - t0;
-                        }
-                    }
-                    if (p.splits > 1) {
-                        const int from = it.first(), len = it.last() - from;
-                        const int begin = from + len * it.split / p.splits, end = from + len * (it.split + 1) / p.splits;
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q) {
-                            it.t0[q] = min(max(it.t0[q], begin), end);
-                            it.t1[q] = min(max(it.t1[q], begin), end);
-                        }
+                        const int t0 = it.t0[q];
+                        it.t0[q] = both - it.t1[q];
+                        it.t1[q] = both - t0;
                     }
                 }
-                const uint32_t box = n_pub & 1u;
-                // the box's previous item has been read by every role
-                bool ok = lane != 0 || w.wait(item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                if (lane == 0) {
-                    volatile int* v = item_box + 12 * box;
-                    v[0] = it.b;
-                    v[1] = it.h;
-                    v[2] = it.q_base;
+                if (p.splits > 1) {
+                    const int from = it.first(), len = it.last() - from;
+                    const int begin = from + len * it.split / p.splits, end = from + len * (it.split + 1) / p.splits;
 #pragma unroll
                     for (int q = 0; q < NQ; ++q) {
-                        v[3 + q] = it.t0[q];
-                        v[5 + q] = it.t1[q];
+                        it.t0[q] = min(max(it.t0[q], begin), end);
+                        it.t1[q] = min(max(it.t1[q], begin), end);
                     }
-                    v[7] = it.flip;
-                    v[8] = it.split;
-                    mbar_arrive(item_pub(box));              // release: the consumers read the box after
                 }
-                ++n_pub;
-                if (item < 0) break;
-                if (lane == 0) {
-                    const int t_begin = it.first(), t_end = it.last();
-                    if (t_begin < t_end) {
-                        const int qb = (int)(n_q % Cfg::QBUF);
-                        if (n_q >= (uint32_t)Cfg::QBUF)
-                            ok = w.wait(qfree(qb), ((n_q - Cfg::QBUF) / Cfg::QBUF) & 1u, kDevErrProducerEmpty);
-                        if (ok) {
-                            if (drop_q) {
-                                drop_q = false;              // test hook: this Q is never loaded
-                            } else {
-                                const uint32_t qbase = sb + Cfg::OFF_Q + qb * NQ * Cfg::Q_BYTES;
-                                mbar_arrive_expect_tx(qfull(qb), NQ * Cfg::Q_BYTES);
+            }
+            const uint32_t box = n_pub & 1u;
+            // the box's previous item has been read by every role
+            bool ok = lane != 0 || w.wait(bars.item_read(box), ((n_pub >> 1) & 1u) ^ 1u, kDevErrProducerEmpty);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (lane == 0) {
+                volatile int* v = item_box + 12 * box;
+                v[0] = it.b;
+                v[1] = it.h;
+                v[2] = it.q_base;
 #pragma unroll
-                                for (int q = 0; q < NQ; ++q)
-#pragma unroll
-                                    for (int c = 0; c < Cfg::DCH; ++c)
-                                        tma_load_4d(qbase + q * Cfg::Q_BYTES + c * Cfg::CHUNK_BYTES, &tmQ, qfull(qb), c * 64,
-                                                    it.q_base + q * Cfg::BQ, it.h, it.b, pol);
-                                q_armed |= 1u << qb;
-                                q_parity = (q_parity & ~(1u << qb)) | ((n_q / Cfg::QBUF) & 1u) << qb;
-                            }
-                            ++n_q;
-                        }
-                        const int hk = it.h / mk.group;
-                        // entry t: K_t (t < t_end) and V_(t-1) (t > t_begin)
-                        for (int t = t_begin; ok && t <= t_end; ++t, ++g) {
-                            const int s = (int)(g & 1u);
-                            const uint32_t ph = (g >> 1) & 1u;
-                            if (!(ok = w.wait(empty(s), ph ^ 1u, kDevErrProducerEmpty))) break;
-                            const bool has_k = t < t_end, has_v = t > t_begin;
-                            mbar_arrive_expect_tx(full(s), (has_k ? Cfg::KV_BYTES : 0) + (has_v ? Cfg::KV_BYTES : 0));
-                            if (has_k) {
-#pragma unroll
-                                for (int c = 0; c < Cfg::DCH; ++c)
-                                    tma_load_4d(sb + Cfg::OFF_K + s * Cfg::KV_BYTES + c * Cfg::CHUNK_BYTES, &tmK, full(s), c * 64,
-                                                it.key_tile(t) * Cfg::BKV, hk, it.b, pol);
-                            }
-                            if (has_v) {
-#pragma unroll
-                                for (int c = 0; c < Cfg::DCH; ++c)
-                                    tma_load_4d(sb + Cfg::OFF_V + s * Cfg::KV_BYTES + c * Cfg::CHUNK_BYTES, &tmV, full(s), c * 64,
-                                                it.key_tile(t - 1) * Cfg::BKV, hk, it.b, pol);
-                            }
-                            armed |= 1u << s;
-                            parity = (parity & ~(1u << s)) | ph << s;
-                        }
-                    }
-                    // the next item, asked for once this one's copies are issued: earlier, a CTA busy with a
-                    // long item would hold one that another could start
+                for (int q = 0; q < NQ; ++q) {
+                    v[3 + q] = it.t0[q];
+                    v[5 + q] = it.t1[q];
+                }
+                v[7] = it.flip;
+                v[8] = it.split;
+                mbar_arrive(bars.item_pub(box));              // release: the consumers read the box after
+            }
+            ++n_pub;
+            if (item < 0) break;
+            const int t_begin = it.first(), t_end = it.last(), hk = it.h / mk.group;
+            if (lane == 0) {
+                if (t_begin < t_end) {
+                    const int qb = (int)(n_q % Cfg::QBUF);
+                    if (n_q >= (uint32_t)Cfg::QBUF)
+                        ok = w.wait(bars.qfree(qb), ((n_q - Cfg::QBUF) / Cfg::QBUF) & 1u, kDevErrProducerEmpty);
                     if (ok) {
-                        fence_proxy_async_smem();            // the last answer has been read
-                        mbar_arrive_expect_tx(clc, 16);
-                        clc_try_cancel(sb + Cfg::OFF_CLC, clc);
-                        asked = true;
-                        if ((ok = w.wait(clc, n_clc & 1u, kDevErrProducerEmpty))) {
-                            asked = false;
-                            item = clc_taken(sb + Cfg::OFF_CLC);
+                        if (drop_q) {
+                            drop_q = false;              // test hook: this Q is never loaded
+                        } else {
+                            const uint32_t qbase = sb + Cfg::OFF_Q + qb * NQ * Cfg::Q_BYTES;
+                            mbar_arrive_expect_tx(bars.qfull(qb), NQ * Cfg::Q_BYTES);
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                                for (int c = 0; c < Cfg::DCH; ++c)
+                                    tma_load_4d(qbase + q * Cfg::Q_BYTES + c * Cfg::CHUNK_BYTES, &tmQ, bars.qfull(qb), c * 64,
+                                                it.q_base + q * Cfg::BQ, it.h, it.b, pol);
+                            q_armed |= 1u << qb;
+                            q_parity = (q_parity & ~(1u << qb)) | ((n_q / Cfg::QBUF) & 1u) << qb;
                         }
+                        ++n_q;
+                    }
+                    // entry t: K_t (t < t_end) and V_(t-1) (t > t_begin)
+                    for (int t = t_begin; ok && !SECOND && t <= t_end; ++t, ++g) {
+                        const int s = (int)(g & 1u);
+                        const uint32_t ph = (g >> 1) & 1u;
+                        if (!(ok = w.wait(bars.empty(s), ph ^ 1u, kDevErrProducerEmpty))) break;
+                        const bool has_k = t < t_end, has_v = t > t_begin;
+                        mbar_arrive_expect_tx(bars.full(s), (has_k ? Cfg::KV_BYTES : 0) + (has_v ? Cfg::KV_BYTES : 0));
+                        if (has_k) {
+#pragma unroll
+                            for (int c = 0; c < Cfg::DCH; ++c)
+                                tma_load_4d(sb + Cfg::OFF_K + s * Cfg::KV_BYTES + c * Cfg::CHUNK_BYTES, &tmK, bars.full(s), c * 64,
+                                            it.key_tile(t) * Cfg::BKV, hk, it.b, pol);
+                        }
+                        if (has_v) {
+#pragma unroll
+                            for (int c = 0; c < Cfg::DCH; ++c)
+                                tma_load_4d(sb + Cfg::OFF_V + s * Cfg::KV_BYTES + c * Cfg::CHUNK_BYTES, &tmV, bars.full(s), c * 64,
+                                            it.key_tile(t - 1) * Cfg::BKV, hk, it.b, pol);
+                        }
+                        armed |= 1u << s;
+                        parity = (parity & ~(1u << s)) | ph << s;
                     }
                 }
-                ++n_clc;
-                if (!__all_sync(0xffffffffu, ok)) break;
+                // the next item, asked for once this one's copies are issued: earlier, a CTA busy with a
+                // long item would hold one that another could start.  None once the list may fill up with the items
+                // in flight (4 at most).
+                if (!SECOND && again_words[0] > Cfg::AGAIN - 4) {
+                    item = -1;
+                } else if (!SECOND && ok) {
+                    fence_proxy_async_smem();            // the last answer has been read
+                    mbar_arrive_expect_tx(bars.clc(), 16);
+                    clc_try_cancel(sb + Cfg::OFF_CLC, bars.clc());
+                    asked = true;
+                    if ((ok = w.wait(bars.clc(), n_clc & 1u, kDevErrProducerEmpty))) {
+                        asked = false;
+                        item = clc_taken(sb + Cfg::OFF_CLC);
+                    }
+                }
+            }
+            if (!SECOND) ++n_clc;
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (SECOND) {
+                // entries that land on a barrier of their own and are full once their V is clean
+                for (int t = t_begin; t_begin < t_end && t <= t_end; ++t, ++g) {
+                    const int s = (int)(g & 1u);
+                    const uint32_t ph = (g >> 1) & 1u;
+                    const bool has_k = t < t_end, has_v = t > t_begin;
+                    if (lane == 0 && (ok = w.wait(bars.empty(s), ph ^ 1u, kDevErrProducerEmpty))) {
+                        mbar_arrive_expect_tx(bars.landed(), (has_k ? Cfg::KV_BYTES : 0) + (has_v ? Cfg::KV_BYTES : 0));
+                        for (int c = 0; c < Cfg::DCH; ++c) {
+                            if (has_k)
+                                tma_load_4d(sb + Cfg::OFF_K + s * Cfg::KV_BYTES + c * Cfg::CHUNK_BYTES, &tmK, bars.landed(), c * 64,
+                                            it.key_tile(t) * Cfg::BKV, hk, it.b, pol);
+                            if (has_v)
+                                tma_load_4d(sb + Cfg::OFF_V + s * Cfg::KV_BYTES + c * Cfg::CHUNK_BYTES, &tmV, bars.landed(), c * 64,
+                                            it.key_tile(t - 1) * Cfg::BKV, hk, it.b, pol);
+                        }
+                        landing = !(ok = w.wait(bars.landed(), g & 1u, kDevErrProducerEmpty));
+                    }
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (has_v && common.edge(it.key_tile(t - 1)) &&
+                        pieces_not_finite<T>(smem + Cfg::OFF_V + s * Cfg::KV_BYTES, Cfg::KV_BYTES / 16, lane)) {
+                        zero_not_finite<T>(smem + Cfg::OFF_V + s * Cfg::KV_BYTES, Cfg::KV_BYTES / 16, lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(bars.full(s));
+                }
+                if (!ok) break;
+                ++item;
+            } else {
                 item = __shfl_sync(0xffffffffu, item, 0);
             }
-            // every copy and answer under way must land before the CTA may exit
-            if (lane == 0) {
-                if (asked) w.drain(clc, (n_clc - 1) & 1u);
-                for (int b = 0; b < Cfg::QBUF; ++b)
-                    if (q_armed & (1u << b)) w.drain(qfull(b), (q_parity >> b) & 1u);
-                for (int s = 0; s < 2; ++s)
-                    if (armed & (1u << s)) w.drain(full(s), (parity >> s) & 1u);
-            }
-            __syncwarp();
-        } else if (warp == 1) {
-            // ------------------------------------------------------------ MMA issuer
-            if (lane == 0) {
-                uint32_t n_item = 0, n_q = 0, g = 0;
-                uint32_t pv_n[NQ] = {0u, 0u};                // pfull phases waited for, per query tile
-                bool ok = true;
-                while (ok) {
-                    const uint32_t box = n_item & 1u;
-                    if (!w.wait(item_pub(box), (n_item >> 1) & 1u, kDevErrMmaFull)) break;
-                    const Item it = read_item(box);
-                    mbar_arrive(item_read(box));
-                    ++n_item;
-                    if (it.b < 0) break;
-                    const int t_begin = it.first(), t_end = it.last();
-                    if (t_begin >= t_end) continue;
-                    const int qb = (int)(n_q % Cfg::QBUF);
-                    if (!w.wait(qfull(qb), (n_q / Cfg::QBUF) & 1u, kDevErrMmaFull)) break;
-                    ++n_q;
-                    tcgen05_fence_after();
-                    for (int t = t_begin; ok && t <= t_end; ++t, ++g) {
-                        const int s = (int)(g & 1u);
-                        if (!(ok = w.wait(full(s), (g >> 1) & 1u, kDevErrMmaFull))) break;   // K_t and V_(t-1)
-                        tcgen05_fence_after();
-                        const uint32_t k_s = sb + Cfg::OFF_K + s * Cfg::KV_BYTES;
-                        const uint32_t v_s = sb + Cfg::OFF_V + s * Cfg::KV_BYTES;
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q) {
-                            if (t > it.t0[q] && t <= it.t1[q]) {
-                                // O_q += P_q(t-1) V_(t-1)
-                                if (!(ok = w.wait(pfull(q), pv_n[q] & 1u, kDevErrMmaFull))) break;
-                                ++pv_n[q];
-                                tcgen05_fence_after();
-                                const uint32_t p_t = tmem_base + Cfg::T_S + q * 128 + Cfg::P_COL;
-#pragma unroll
-                                for (int k = 0; k < Cfg::BKV / 16; ++k)
-                                    mma_f16_ts(tmem_base + Cfg::T_O + q * D, p_t + k * 8,
-                                               smem_desc_sw128(v_s + k * 2048, Cfg::CHUNK_BYTES, 1024), Cfg::IDESC_PV,
-                                               (t - 1 > it.t0[q] || k > 0) ? 1u : 0u);
-                                if (t == it.t1[q]) mma_commit(odone(q));
-                            }
-                            if (t >= it.t0[q] && t < it.t1[q]) {
-                                // S_q(t) = Q_q K_t^T, over P_q(t-1): one thread's products complete in order
-                                const uint32_t q_s = sb + Cfg::OFF_Q + (qb * NQ + q) * Cfg::Q_BYTES;
-#pragma unroll
-                                for (int k = 0; k < D / 16; ++k) {
-                                    const uint32_t off = (k >> 2) * Cfg::CHUNK_BYTES + (k & 3) * 32;
-                                    mma_f16_ss(tmem_base + Cfg::T_S + q * 128, smem_desc_sw128(q_s + off, 16, 1024),
-                                               smem_desc_sw128(k_s + off, 16, 1024), Cfg::IDESC_S, k > 0 ? 1u : 0u);
-                                }
-                                mma_commit(sfull(q));
-                            }
-                        }
-                        if (!ok) break;
-                        if (t == t_end - 1) mma_commit(qfree(qb));   // the item's last Q K^T products are issued
-                        mma_commit(empty(s));
-                    }
-                }
-                mma_commit(drain);
-                w.drain(drain, 0);
-            }
-            __syncwarp();
         }
-    } else {
-        reg_inc<Cfg::SOFTMAX_REGS>();
+        // every copy and answer under way must land before the CTA may exit
+        if (lane == 0) {
+            if (asked) w.drain(bars.clc(), (n_clc - 1) & 1u);
+            if (landing) w.drain(bars.landed(), g & 1u);
+            for (int b = 0; b < Cfg::QBUF; ++b)
+                if (q_armed & (1u << b)) w.drain(bars.qfull(b), (q_parity >> b) & 1u);
+            for (int s = 0; s < 2; ++s)
+                if (armed & (1u << s)) w.drain(bars.full(s), (parity >> s) & 1u);
+        }
+        __syncwarp();
+    };
+
+    auto issue = [&](auto run) {
+        constexpr bool SECOND = decltype(run)::value;
+        const FwdBars bars{sb + (SECOND ? Cfg::OFF_BAR_AGAIN : Cfg::OFF_BAR)};
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            uint32_t n_item = 0, n_q = 0, g = 0;
+            uint32_t pv_n[NQ] = {0u, 0u};                // pfull phases waited for, per query tile
+            bool ok = true;
+            while (ok) {
+                const uint32_t box = n_item & 1u;
+                if (!w.wait(bars.item_pub(box), (n_item >> 1) & 1u, kDevErrMmaFull)) break;
+                const Item it = read_item(box);
+                mbar_arrive(bars.item_read(box));
+                ++n_item;
+                if (it.b < 0) break;
+                const int t_begin = it.first(), t_end = it.last();
+                if (t_begin >= t_end) continue;
+                const int qb = (int)(n_q % Cfg::QBUF);
+                if (!w.wait(bars.qfull(qb), (n_q / Cfg::QBUF) & 1u, kDevErrMmaFull)) break;
+                ++n_q;
+                tcgen05_fence_after();
+                for (int t = t_begin; ok && t <= t_end; ++t, ++g) {
+                    const int s = (int)(g & 1u);
+                    if (!(ok = w.wait(bars.full(s), (g >> 1) & 1u, kDevErrMmaFull))) break;   // K_t and V_(t-1)
+                    tcgen05_fence_after();
+                    const uint32_t k_s = sb + Cfg::OFF_K + s * Cfg::KV_BYTES;
+                    const uint32_t v_s = sb + Cfg::OFF_V + s * Cfg::KV_BYTES;
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        if (t > it.t0[q] && t <= it.t1[q]) {
+                            // O_q += P_q(t-1) V_(t-1)
+                            if (!(ok = w.wait(bars.pfull(q), pv_n[q] & 1u, kDevErrMmaFull))) break;
+                            ++pv_n[q];
+                            tcgen05_fence_after();
+                            const uint32_t p_t = tmem_base + Cfg::T_S + q * 128 + Cfg::P_COL;
+#pragma unroll
+                            for (int k = 0; k < Cfg::BKV / 16; ++k)
+                                mma_f16_ts(tmem_base + Cfg::T_O + q * D, p_t + k * 8,
+                                           smem_desc_sw128(v_s + k * 2048, Cfg::CHUNK_BYTES, 1024), Cfg::IDESC_PV,
+                                           (t - 1 > it.t0[q] || k > 0) ? 1u : 0u);
+                            if (t == it.t1[q]) mma_commit(bars.odone(q));
+                        }
+                        if (t >= it.t0[q] && t < it.t1[q]) {
+                            // S_q(t) = Q_q K_t^T, over P_q(t-1): one thread's products complete in order
+                            const uint32_t q_s = sb + Cfg::OFF_Q + (qb * NQ + q) * Cfg::Q_BYTES;
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = (k >> 2) * Cfg::CHUNK_BYTES + (k & 3) * 32;
+                                mma_f16_ss(tmem_base + Cfg::T_S + q * 128, smem_desc_sw128(q_s + off, 16, 1024),
+                                           smem_desc_sw128(k_s + off, 16, 1024), Cfg::IDESC_S, k > 0 ? 1u : 0u);
+                            }
+                            mma_commit(bars.sfull(q));
+                        }
+                    }
+                    if (!ok) break;
+                    if (t == t_end - 1) mma_commit(bars.qfree(qb));   // the item's last Q K^T products are issued
+                    mma_commit(bars.empty(s));
+                }
+            }
+            mma_commit(bars.drain());
+            w.drain(bars.drain(), 0);
+        }
+        __syncwarp();
+    };
+
+    auto softmax = [&](auto run) {
+        constexpr bool SECOND = decltype(run)::value;
+        const FwdBars bars{sb + (SECOND ? Cfg::OFF_BAR_AGAIN : Cfg::OFF_BAR)};
         // ------------------------------------------------------------ softmax + output (warps 4-11)
         const int q = (warp - 4) >> 2;
         const int quad = warp & 3;
@@ -487,10 +598,10 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
         bool ok = true;
         while (ok) {
             const uint32_t box = n_item & 1u;
-            if (!__all_sync(0xffffffffu, w.wait(item_pub(box), (n_item >> 1) & 1u, kDevErrEpilogueFull))) break;
+            if (!__all_sync(0xffffffffu, w.wait(bars.item_pub(box), (n_item >> 1) & 1u, kDevErrEpilogueFull))) break;
             const Item it = read_item(box);
             __syncwarp();
-            if (lane == 0) mbar_arrive(item_read(box));
+            if (lane == 0) mbar_arrive(bars.item_read(box));
             ++n_item;
             if (it.b < 0) break;
             const int qi = it.q_base + q * Cfg::BQ + r;
@@ -502,7 +613,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
 
             for (int t = t0; t < t1; ++t) {
                 // the warp agrees before any .sync.aligned TMEM access
-                if (!__all_sync(0xffffffffu, w.wait(sfull(q), s_n & 1u, kDevErrEpilogueFull))) {
+                if (!__all_sync(0xffffffffu, w.wait(bars.sfull(q), s_n & 1u, kDevErrEpilogueFull))) {
                     ok = false;
                     break;
                 }
@@ -585,23 +696,25 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                 }
                 tmem_st_wait();
                 tcgen05_fence_before();
-                mbar_arrive(pfull(q));           // P_q(t) (and a rescaled O_q) ready for the MMA
+                mbar_arrive(bars.pfull(q));           // P_q(t) (and a rescaled O_q) ready for the MMA
                 l += ls0 + ls1;
             }
             // output: O_q / l, and the log-sum-exp.  The next item's first PV_q, which overwrites
             // O_q, waits for this group's next P, issued only after these loads.
             if (ok && t0 < t1) {
-                ok = __all_sync(0xffffffffu, w.wait(odone(q), o_n & 1u, kDevErrEpilogueFull));
+                ok = __all_sync(0xffffffffu, w.wait(bars.odone(q), o_n & 1u, kDevErrEpilogueFull));
                 ++o_n;
                 tcgen05_fence_after();
             }
             if (!ok) break;
             if (p.splits > 1) {
-                store_part<D>(p, part_index(p, it.b, it.h, it.split, qi), t0 < t1, qi < mk.Sq, o_col, m, l);
+                const bool bad = store_part<D>(p, part_index(p, it.b, it.h, it.split, qi), t0 < t1, qi < mk.Sq, o_col, m, l);
+                if (SECOND || __any_sync(0xffffffffu, bad && qi < mk.Sq && l < INFINITY))
+                    after_item<Cfg, SECOND>(p, n_item, it.b, it.h, it.q_base, it.split);
                 continue;
             }
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            bool bad = !(l < INFINITY);          // l or an element of O is infinite or NaN
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            bool bad = false;                    // an element of O is infinite or NaN
             T* dst = static_cast<T*>(p.O.data) + it.b * p.O.batch + it.h * p.O.head + (long long)qi * p.O.row;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {   // one copy of the code: it runs cold, once an item
@@ -632,15 +745,37 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
             if (p.lse && qi < mk.Sq)
                 p.lse[((long long)it.b * mk.Hq + it.h) * mk.Sq + qi] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
             tcgen05_fence_before();
-            // rows that are not finite, again from the keys they see
-            __syncwarp();
-            for (uint32_t again = __ballot_sync(0xffffffffu, bad && qi < mk.Sq && lo < hi); again; again &= again - 1)
-                masked_row<T, D>(p, it.b, it.h, it.q_base + q * Cfg::BQ + quad * 32 + __ffs(again) - 1, lane);
+            // a row whose sum is not finite owes it to its scores alone
+            if (SECOND || __any_sync(0xffffffffu, bad && qi < mk.Sq && l < INFINITY))
+                after_item<Cfg, SECOND>(p, n_item, it.b, it.h, it.q_base, it.split);
         }
-    }
+    };
 
-    tcgen05_fence_before();
-    __syncthreads();
+    // Roles run<first>, then, if the list is not empty, run<second>.  At the barrier between all of the first run is
+    // written, its copies have landed and its products are done.
+    auto both = [&](auto role) {
+        role(std::false_type{});
+        tcgen05_fence_before();
+        named_bar_sync(0, Cfg::NUM_THREADS);
+        if (again_words[0] == 0u || *abort_flag != 0u) return;
+        if (threadIdx.x == 0) FwdBars{sb + Cfg::OFF_BAR_AGAIN}.init(Cfg::SM_THREADS / 32);
+        named_bar_sync(0, Cfg::NUM_THREADS);
+        role(std::true_type{});
+        tcgen05_fence_before();
+        named_bar_sync(0, Cfg::NUM_THREADS);
+    };
+    if (warp < 4) {
+        reg_dec<Cfg::CONTROL_REGS>();
+        if (warp == 0)
+            both(produce);
+        else if (warp == 1)
+            both(issue);
+        else
+            both([](auto) {});
+    } else {
+        reg_inc<Cfg::SOFTMAX_REGS>();
+        both(softmax);
+    }
     if (warp == 1) {
         __syncwarp();
         tcgen05_fence_after();

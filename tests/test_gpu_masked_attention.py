@@ -526,3 +526,139 @@ def test_keys_in_parts(D):
     c.k[:, :, 100] = float("nan")
     c.forward()
     assert torch.isnan(c.o).all()
+
+
+# ---------------------------------------------------------------------------- infinities and NaN that some rows see
+
+def natural(c):
+    """O and lse of the formula in fp64, infinities and NaN taking their course among the pairs that a row sees:
+    (O with what is not finite left out of V, whether each element meets +inf or NaN, -inf or NaN, sum of |terms|, lse)."""
+    B, Hq, Sq, D = c.q.shape
+    g, Skv, see = Hq // c.k.shape[1], c.k.shape[2], torch.tensor(c.see, device=DEV)[:, None]
+    k, v = (t.double().repeat_interleave(g, 1) for t in (c.k, c.v))
+    x = c.q.double() @ k.transpose(-1, -2) * (c.scale or D ** -0.5)
+    if c.cap:
+        x = c.cap * torch.tanh(x / c.cap)
+    if c.slopes is not None:
+        dist = torch.arange(Sq, device=DEV)[:, None] + Skv - Sq - torch.arange(Skv, device=DEV)
+        x = x - c.slopes.double()[None, :, None, None] * dist.abs()
+    x = torch.where(see, x, -torch.inf)
+    top = x.amax(-1, keepdim=True)
+    p = torch.exp(x - torch.where(top == -torch.inf, 0.0, top))
+    l = p.sum(-1, keepdim=True)
+    w = torch.where(see, p / torch.where(l == 0, 1.0, l), 0.0)
+    clean = torch.where(v.isfinite(), v, 0.0)
+    seen = see.double()
+    plus, minus = ((seen @ ((v == s) | v.isnan()).double()) > 0 for s in (torch.inf, -torch.inf))
+    return w @ clean, plus, minus, w @ clean.abs(), torch.where(top == -torch.inf, 0.0, top)[..., 0] + l[..., 0].log()
+
+
+def check_natural(c):
+    o, plus, minus, terms, lse = (t.cpu() for t in natural(c))
+    got, gl = c.o.double().cpu(), c.lse.double().cpu()
+    special = plus | minus | ~o.isfinite()
+    assert torch.equal(special, ~got.isfinite())
+    ok = ~special
+    tol = torch.from_numpy(c.tol(o.numpy(), terms.numpy(), terms.numpy()))
+    assert torch.all(((got - o).abs() <= tol)[ok])
+    if c.slopes is None:                     # with a bias a weight may be 0, and 0 inf is NaN
+        assert torch.all(got[plus & ~minus & o.isfinite()] == torch.inf)
+        assert torch.all(got[minus & ~plus & o.isfinite()] == -torch.inf)
+    assert torch.all(got[plus & minus].isnan())
+    assert torch.equal(gl.isnan(), lse.isnan()) and torch.equal(gl.isneginf(), lse.isneginf())
+    fin = lse.isfinite()
+    assert torch.all((gl - lse)[fin].abs() <= 2.0 ** -14)
+
+
+SPECIAL = {
+    "causal": dict(B=1, Hq=4, Hkv=2, Sq=700, Skv=700, D=128, causal=True),
+    "causal_short": dict(B=2, Hq=2, Hkv=1, Sq=100, Skv=300, D=64, causal=True, dtype=BF16),
+    "two_way": dict(B=1, Hq=2, Hkv=2, Sq=300, Skv=515, D=64),
+    "docs": dict(B=2, Hq=4, Hkv=2, Sq=500, Skv=500, D=64, docs=[[0, 3, 200, 200, 480], [7, 100, 257, 300, 411]], causal=True),
+    "docs_two_way": dict(B=1, Hq=2, Hkv=1, Sq=700, Skv=700, D=128, docs=[[10, 127, 128, 129, 390, 690]], dtype=BF16),
+    "prefix": dict(B=3, Hq=2, Hkv=2, Sq=400, Skv=400, D=64, causal=True, prefix=[0, 131, 300]),
+    "alibi": dict(B=1, Hq=4, Hkv=2, Sq=640, Skv=640, D=128, causal=True, alibi=True, dtype=BF16),
+    "cap": dict(B=1, Hq=2, Hkv=1, Sq=400, Skv=400, D=128, causal=True, cap=3.0),
+    "all": dict(B=2, Hq=6, Hkv=2, Sq=390, Skv=390, D=64, cap=3.0, alibi=True, causal=True, order="bshd", dtype=BF16,
+                docs=[[0, 200, 380], [5, 6, 390]], prefix=[[50, 10], [1, 300]]),
+    "parts": dict(B=1, Hq=2, Hkv=1, Sq=5, Skv=6000, D=128, causal=True),
+    "parts_capped": dict(B=1, Hq=2, Hkv=1, Sq=300, Skv=4000, D=64, causal=True, cap=2.0, alibi=True, dtype=BF16),
+}
+
+
+def spoil(t, n, values, seed):
+    """Puts `n` of the values at random places."""
+    r = np.random.default_rng(seed)
+    for i in range(n):
+        t[tuple(int(r.integers(0, k)) for k in t.shape)] = values[i % len(values)]
+
+
+@pytest.mark.parametrize("name", SPECIAL)
+def test_infinite_and_nan_values_reach_the_rows_that_see_them(name):
+    # elements of V, and one whole row of it: the columns of the rows that see them and nothing else
+    c = Case(**SPECIAL[name])
+    spoil(c.v, 12, [float("inf"), float("nan"), -float("inf")], 3)
+    c.v[0, 0, c.v.shape[2] // 2] = float("nan")
+    c.forward()
+    check_natural(c)
+
+
+@pytest.mark.parametrize("name", SPECIAL)
+def test_infinite_and_nan_queries_and_keys(name):
+    c = Case(**SPECIAL[name])
+    spoil(c.q, 3, [float("inf"), float("nan")], 5)
+    spoil(c.k, 3, [float("nan"), -float("inf")], 6)
+    c.forward()
+    check_natural(c)
+
+
+@pytest.mark.parametrize("D,dtype", [(128, F16), (64, BF16)])
+def test_an_infinite_value_takes_no_longer(D, dtype):
+    """One infinity in V, and V of NaN behind the last document, in rows of 32768 tokens: no wait of 0.02 s runs out,
+    and all other results keep their bits."""
+    S = 32768
+    g = torch.Generator(device=DEV).manual_seed(D)
+    q = torch.randn(1, 4, S, D, generator=g, device=DEV).to(dtype)
+    k, v = (torch.randn(1, 1, S, D, generator=g, device=DEV).to(dtype) for _ in range(2))
+    bounds = torch.tensor([[0, S - 100]], dtype=torch.int32, device=DEV)
+
+    def run(**kw):
+        o, lse = torch.empty_like(q), torch.empty(1, 4, S, device=DEV)
+        gsr.masked_attention_fwd(q, k, v, o, lse, **kw)
+        status, code = gsr.device_status()
+        assert status == gsr.Status.OK, hex(code)
+        return o, lse
+
+    cases = (dict(causal=True), dict(doc_bounds=bounds))
+    clean = [run(**kw) for kw in cases]
+    v[0, 0, 200, 5] = float("inf")
+    v[0, 0, S - 100:] = float("nan")
+    gsr.set_wait_timeout_ns(20_000_000)
+    try:
+        got = [run(**kw) for kw in cases]
+    finally:
+        gsr.set_wait_timeout_ns(1_000_000_000)
+    for (o, lse), (o0, lse0) in zip(got, clean):
+        assert torch.equal(lse, lse0)
+        o0[:, :, S - 100:] = o[:, :, S - 100:]
+        first = 200 if o is got[0][0] else 0
+        assert torch.all(o[:, :, first:S - 100, 5] == float("inf"))
+        o0[:, :, first:, 5] = o[:, :, first:, 5]
+        assert torch.equal(o.nan_to_num(7.0), o0.nan_to_num(7.0))
+    assert got[0][0][:, :, S - 100:].isnan().all() and torch.all(got[1][0][:, :, S - 100:] == 0)
+
+
+def test_infinities_in_every_item():
+    # far more items on each CTA than its list of items to run again holds
+    g = torch.Generator(device=DEV).manual_seed(1)
+    q = torch.randn(24, 64, 1024, 64, generator=g, device=DEV).half()
+    k, v = (torch.randn(24, 2, 1024, 64, generator=g, device=DEV).half() for _ in range(2))
+    o, clean, lse, lse0 = torch.empty_like(q), torch.empty_like(q), *(torch.empty(24, 64, 1024, device=DEV) for _ in range(2))
+    gsr.masked_attention_fwd(q, k, v, clean, lse0, causal=True)
+    v[..., 3] = float("inf")
+    for _ in range(3):
+        gsr.masked_attention_fwd(q, k, v, o, lse, causal=True)
+        status, code = gsr.device_status()
+        assert status == gsr.Status.OK, hex(code)
+        clean[..., 3] = float("inf")
+        assert torch.equal(o, clean) and torch.equal(lse, lse0)
