@@ -226,7 +226,9 @@ gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor
  * O, dQ shaped as Q; dK, dV as K).  dK and dV sum over the query heads of a group.  Results do not
  * depend on the order of execution.  P and dS are rounded to the operands' type for the matrix
  * products; in float16 dS carries a power of two that keeps it in range for any size of dO.
- * Queries without keys get dQ = 0 and add nothing, whatever their dO holds.
+ * Queries without keys get dQ = 0 and add nothing, whatever their dO holds.  Infinities and NaN in
+ * dO, Q, K and V reach the gradients of the pairs that see each other and no other elements, and a call
+ * with them takes about as long as one without.
  *
  *   workspace  masked_attention_bwd_workspace(desc) bytes, as for masked_attention_fwd.
  */

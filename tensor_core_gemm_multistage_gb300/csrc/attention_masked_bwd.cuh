@@ -22,8 +22,10 @@
 // this bound.  bf16 has fp32's range and needs neither.
 //
 // Masked pairs get P = dS = 0 by selection, but a row of dO, Q or K that is not finite turns 0
-// times itself into NaN inside a product: a result row that is not finite is computed again by its
-// warp from the pairs it sees alone (row_dq, row_dkv).
+// times itself into NaN inside a product.  Where a warp masks, its products and the rows' delta tell: a row of
+// Q (of K in dQ's kernel) that is not finite has no finite product, and a row of dO no finite delta.  The warp then
+// cleans its half of the tiles before they are weighted ("Infinities and NaN behind a mask" in
+// attention_common.cuh).
 #pragma once
 
 #include <type_traits>
@@ -133,7 +135,8 @@ __global__ void __launch_bounds__(256) gsr_masked_bwd_rows_kernel(const __grid_c
         if (lane < kWarpRows) {
             const long long row = (long long)bh * p.Sp + i;
             p.offset[row] = keys ? row_offset<T>(p.score) - lse * kLog2e : -INFINITY;
-            p.neg_delta[row] = keys ? -delta : 0.0f;
+            // where dO is not finite delta is not either, and says so of a row without keys too (dK's and dV's CTAs look)
+            p.neg_delta[row] = keys || !(fabsf(delta) < INFINITY) ? -delta : 0.0f;
         }
         if (!Elem<T>::bf16) {
             grid_wait();                                 // the norms are zero
@@ -185,81 +188,6 @@ __global__ void __launch_bounds__(256) gsr_masked_zero_kernel(Strided t, int hea
 }
 
 // ---------------------------------------------------------------------------
-// Single rows, in fp32, by one warp
-// ---------------------------------------------------------------------------
-// P_ij and dS_ij (without their powers of two).
-template <class T, int D>
-__device__ __forceinline__ void pair_grad(const ScoreArgs& sc, float slope2, int dist, const float (&q)[D / 32],
-                                          const float (&k)[D / 32], const float (&dO)[D / 32],
-                                          const float (&v)[D / 32], float offset, float neg_delta, float& P, float& dS) {
-    float grad;
-    const float y = score_of(warp_dot(q, k), sc, grad) - slope2 * fabsf((float)dist);
-    P = ex2_approx(y + (offset - row_offset<T>(sc)));
-    dS = P * (warp_dot(dO, v) + neg_delta) * grad;
-}
-
-template <class T, int D>
-__device__ __noinline__ void row_dq(const MaskedBwdParams& p, int b, int h, int i, int lane) {
-    const MaskArgs& mk = p.mask;
-    const int hk = h / mk.group;
-    float q[D / 32], dO[D / 32], k[D / 32], v[D / 32], acc[D / 32] = {};
-    load_row<T, D>(static_cast<const T*>(p.Q.data) + b * p.Q.batch + h * p.Q.head + i * p.Q.row, lane, q);
-    load_row<T, D>(static_cast<const T*>(p.dO.data) + b * p.dO.batch + h * p.dO.head + i * p.dO.row, lane, dO);
-    const T* kb = static_cast<const T*>(p.K.data) + b * p.K.batch + hk * p.K.head;
-    const T* vb = static_cast<const T*>(p.V.data) + b * p.V.batch + hk * p.V.head;
-    const float slope2 = p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
-    const long long row = ((long long)b * mk.Hq + h) * p.Sp + i;
-    const float offset = __ldcg(p.offset + row), neg_delta = __ldcg(p.neg_delta + row);
-    int lo, hi;
-    row_interval(mk, b, i, lo, hi);
-    for (int j = lo; j < hi; ++j) {
-        load_row<T, D>(kb + j * p.K.row, lane, k);
-        load_row<T, D>(vb + j * p.V.row, lane, v);
-        float P, dS;
-        pair_grad<T, D>(p.score, slope2, i + mk.offset - j, q, k, dO, v, offset, neg_delta, P, dS);
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(dS, k[e], acc[e]);
-        if (all_nan(acc)) break;
-    }
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[e] *= p.score.scale;
-    store_row<T, D>(static_cast<T*>(p.dQ.data) + b * p.dQ.batch + h * p.dQ.head + i * p.dQ.row, lane, acc);
-}
-
-// dK (or dV) of one key row.
-template <class T, int D>
-__device__ __noinline__ void row_dkv(const MaskedBwdParams& p, int b, int hk, int j, bool want_dk, int lane) {
-    const MaskArgs& mk = p.mask;
-    float q[D / 32], dO[D / 32], k[D / 32], v[D / 32], acc[D / 32] = {};
-    load_row<T, D>(static_cast<const T*>(p.K.data) + b * p.K.batch + hk * p.K.head + j * p.K.row, lane, k);
-    load_row<T, D>(static_cast<const T*>(p.V.data) + b * p.V.batch + hk * p.V.head + j * p.V.row, lane, v);
-    int first, end;
-    key_interval(mk, b, j, first, end);
-    for (int h = hk * mk.group; h < (hk + 1) * mk.group && !all_nan(acc); ++h) {
-        const T* qb = static_cast<const T*>(p.Q.data) + b * p.Q.batch + h * p.Q.head;
-        const T* ob = static_cast<const T*>(p.dO.data) + b * p.dO.batch + h * p.dO.head;
-        const float slope2 = p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
-        const long long row = ((long long)b * mk.Hq + h) * p.Sp;
-        for (int i = first; i < end; ++i) {
-            load_row<T, D>(qb + i * p.Q.row, lane, q);
-            load_row<T, D>(ob + i * p.dO.row, lane, dO);
-            float P, dS;
-            pair_grad<T, D>(p.score, slope2, i + mk.offset - j, q, k, dO, v, __ldcg(p.offset + row + i),
-                            __ldcg(p.neg_delta + row + i), P, dS);
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) acc[e] = want_dk ? fmaf(dS, q[e], acc[e]) : fmaf(P, dO[e], acc[e]);
-            if (all_nan(acc)) break;
-        }
-    }
-    if (want_dk) {
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) acc[e] *= p.score.scale;
-    }
-    const Strided& to = want_dk ? p.dK : p.dV;
-    store_row<T, D>(static_cast<T*>(to.data) + b * to.batch + hk * to.head + j * to.row, lane, acc);
-}
-
-// ---------------------------------------------------------------------------
 // Shared by the two tensor-core kernels
 // ---------------------------------------------------------------------------
 // 384 threads: warp 0 copies, one lane of warp 1 issues the products, warps 4-11 do the arithmetic
@@ -302,6 +230,29 @@ __device__ __forceinline__ void weights_chunk(uint32_t (&rr)[32], const ScoreArg
         rr[i + 1] = __float_as_uint(y1);
     }
 }
+// Whether one of a warp's 32 x 64 products, or of the 64 values at `more` (if any), is not finite.
+__device__ __forceinline__ bool products_not_finite(const uint32_t (&a)[32], const uint32_t (&b)[32], const float* more, int lane) {
+    float z0 = 0.0f, z1 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        ffma2(z0, z1, __uint_as_float(a[i]), __uint_as_float(a[i + 1]), 0.0f, 0.0f, z0, z1);
+        ffma2(z0, z1, __uint_as_float(b[i]), __uint_as_float(b[i + 1]), 0.0f, 0.0f, z0, z1);
+    }
+    if (more) {
+        const float2 v = *(reinterpret_cast<const float2*>(more) + lane);
+        ffma2(z0, z1, v.x, v.y, 0.0f, 0.0f, z0, z1);
+    }
+    return __any_sync(0xffffffffu, z0 + z1 != 0.0f);
+}
+// 64 rows of a tile's chunks in shared memory without what is not finite; true if there was something.  Kept out of
+// the kernels' own code (in it, 1 % slower).
+template <class T, int DCH>
+__device__ __noinline__ bool clean_half_tile(uint8_t* tile, int half, int lane) {
+    bool any = false;
+#pragma unroll 1
+    for (int c = 0; c < DCH; ++c) any |= zero_not_finite<T>(tile + c * kChunkBytes + half * 8192, 512, lane);
+    return any;
+}
 template <int MODE>
 constexpr float kCapFactor = kHasCap<MODE> ? 4.0f : 1.0f;
 
@@ -335,7 +286,8 @@ struct DkvCfg {
     static constexpr int NUM_BARS = 26;
     static constexpr int OFF_CLC = OFF_BAR + NUM_BARS * 8;
     static constexpr int OFF_ITEM = OFF_CLC + 16;
-    static constexpr int OFF_MISC = OFF_ITEM + 64;
+    static constexpr int OFF_CLEANED = OFF_ITEM + 64;           // 4 words
+    static constexpr int OFF_MISC = OFF_CLEANED + 16;
     static constexpr int SMEM_BYTES = OFF_MISC + 16;
     static constexpr uint32_t T_S = 0, T_DP = 128, T_DV = 256, T_DK = 256 + D;
     static constexpr uint32_t IDESC_S = idesc_16_f32(Elem<T>::bf16, kTile, kTile, false, false);
@@ -362,10 +314,9 @@ __device__ __forceinline__ void mma_overlay(uint32_t d, uint32_t a, uint32_t b, 
                    (accumulate || k > 0) ? 1u : 0u);
 }
 
-// Rows of an accumulator to a strided output, one row per thread; true if a value is not finite.
+// Rows of an accumulator to a strided output, one row per thread.
 template <class T, int D>
-__device__ __forceinline__ bool store_accumulator(uint32_t col, float factor, bool zero, bool write, T* row) {
-    bool bad = false;
+__device__ __forceinline__ void store_accumulator(uint32_t col, float factor, bool zero, bool write, T* row) {
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {                   // one copy of the code: it runs cold, once an item
         uint32_t rr[32];
@@ -381,18 +332,52 @@ __device__ __forceinline__ bool store_accumulator(uint32_t col, float factor, bo
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float a = __uint_as_float(rr[2 * i]), b = __uint_as_float(rr[2 * i + 1]);
-                bad |= !(fabsf(a) < INFINITY) | !(fabsf(b) < INFINITY);
                 v[i] = Elem<T>::pack(a * factor, b * factor);
             }
             store_64_bytes(row + c * 32, v);
         }
     }
-    return bad;
 }
 
 // Row j of part `split` of dV (which 0) or dK (1) in the workspace.
 __device__ __forceinline__ float* part_row(const MaskedBwdParams& p, int which, int split, int bh, int j, int D) {
     return p.parts + ((((long long)which * p.splits + split) * (p.mask.B * p.mask.Hkv) + bh) * p.mask.Skv + j) * D;
+}
+
+// A warp's rows of dV or dK (`which` 0 or 1), of a whole item or of part `split`, are written, and edge tiles were cleaned:
+// what their rows mean to the keys that their queries see.  Steps [begin, end) as in the kernel's Item.  dS of
+// a pair whose Q is not finite is NaN or 0, so dK's column is NaN; P is not negative.
+template <class T, int D>
+__device__ __noinline__ void spread_dkv(const MaskedBwdParams& p, int which, int b, int hk, int k0, int t0, int t1, int begin, int end,
+                                        int split) {
+    const MaskArgs& mk = p.mask;
+    const int lane = threadIdx.x & 31, j = k0 + (threadIdx.x >> 5 & 3) * 32 + lane;
+    int all_first, all_end, none, lo = 0, hi = 0;        // the queries that see all keys of the tile
+    key_interval(mk, b, k0, none, all_end);
+    key_interval(mk, b, min(k0 + kTile, mk.Skv) - 1, all_first, none);
+    if (j < mk.Skv) key_interval(mk, b, j, lo, hi);
+    for (int k = begin; k < end; ++k) {
+        const int t = t0 + k % (t1 - t0), h = hk * mk.group + k / (t1 - t0), i0 = t * kTile;
+        if (i0 >= all_first && i0 + kTile <= all_end) continue;
+        const Strided& from = which ? p.Q : p.dO;
+        const T* rows = static_cast<const T*>(from.data) + b * from.batch + h * from.head;
+        const int i1 = min(i0 + kTile, mk.Sq);
+        if (p.splits > 1) {
+            float* to = part_row(p, which, split, b * mk.Hkv + hk, j, D);
+            if (which)
+                spread_not_finite<T, D, true>(rows, from.row, i0, i1, lo, hi, to, j < mk.Skv, lane);
+            else
+                spread_not_finite<T, D, false>(rows, from.row, i0, i1, lo, hi, to, j < mk.Skv, lane);
+        } else {
+            const Strided& out = which ? p.dK : p.dV;
+            uint16_t* to = static_cast<uint16_t*>(out.data) + b * out.batch + hk * out.head + (long long)j * out.row;
+            if (which)
+                spread_not_finite<T, D, true>(rows, from.row, i0, i1, lo, hi, to, j < mk.Skv, lane);
+            else
+                spread_not_finite<T, D, false>(rows, from.row, i0, i1, lo, hi, to, j < mk.Skv, lane);
+        }
+    }
+    __syncwarp();
 }
 
 // The parts' sums, in order.  A warp takes kSumRows rows of dK or dV, the loads of kSumParts parts before
@@ -433,13 +418,6 @@ __global__ void __launch_bounds__(256) gsr_masked_dkv_sum_kernel(const __grid_co
         const int which = id >= rows;
         const long long row = id - (which ? rows : 0);
         const int bh = (int)(row / mk.Skv), j = (int)(row - (long long)bh * mk.Skv), b = bh / mk.Hkv, hk = bh - b * mk.Hkv;
-        bool bad = false;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) bad |= !(fabsf(sum[k][e]) < INFINITY);
-        if (__any_sync(0xffffffffu, bad)) {
-            row_dkv<T, D>(p, b, hk, j, which == 1, lane);
-            continue;
-        }
         const Strided& out = which ? p.dK : p.dV;
         store_row<T, D>(static_cast<T*>(out.data) + b * out.batch + hk * out.head + (long long)j * out.row, lane, sum[k]);
     }
@@ -471,6 +449,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_MISC + 4);
     volatile int* item_box = reinterpret_cast<volatile int*>(smem + Cfg::OFF_ITEM);
+    // cleaned[n & 3] == n: a tile of item n was cleaned.  (Item n + 4 is published once every warp is past n.)
+    volatile uint32_t* cleaned = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_CLEANED);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const MaskArgs& mk = p.mask;
 
@@ -506,6 +486,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         mbar_init(done, 1);
         mbar_init(clc, 1);
         mbar_init(drain, 1);
+        for (int i = 0; i < 4; ++i) cleaned[i] = 0u;
         *abort_flag = 0u;
         fence_mbarrier_init();
     }
@@ -718,7 +699,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             ++n_box;
             if (it.b < 0) break;
             const int j = it.k0 + r;
-            int first = 0, end = 0;                      // the queries that see this thread's key
+            int first = 0, end = INT_MAX;                // the queries that see this thread's key (behind the last: no mask)
             if (j < mk.Skv) key_interval(mk, it.b, j, first, end);
             const int tiles = max(it.t1 - it.t0, 1);
             int h = it.hk * mk.group + it.begin / tiles, t = it.t0 + it.begin % tiles;
@@ -743,6 +724,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 tmem_ld_32x32b_x32(s_col + 32, w1);
                 tmem_ld_wait(w0);
                 reg_tie(w1);
+                if (masked && __builtin_expect(products_not_finite(w0, w1, rows + 128, lane), 0)) {
+                    // dP takes dO as it is
+                    if (!__all_sync(0xffffffffu, w.wait(dp_full, n & 1u, kDevErrEpilogueFull))) {
+                        ok = false;
+                        break;
+                    }
+                    if (clean_half_tile<T, DCH>(smem + Cfg::OFF_Q + (n % NQ) * Cfg::TILE_BYTES, half, lane) |
+                        clean_half_tile<T, DCH>(smem + Cfg::OFF_O + (n % NO) * Cfg::TILE_BYTES, half, lane))
+                        cleaned[n_box & 3u] = n_box;
+                    fence_proxy_async_smem();
+                    if (kHasCap<Cfg::MODE>) {            // a hidden NaN would take its visible neighbour along
+                        const uint32_t v0 = between(first - i0, end - i0), v1 = between(first - i0 - 32, end - i0 - 32);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            if (!(v0 >> i & 1u)) w0[i] = 0u;
+                            if (!(v1 >> i & 1u)) w1[i] = 0u;
+                        }
+                    }
+                }
                 auto p_chunk = [&](uint32_t (&rr)[32], int c) {
                     uint32_t packed[16];
                     weights_chunk<T, Cfg::MODE, true>(rr, p.score, slope2, base - (float)(c * 32),
@@ -839,15 +839,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     }
                 }
                 tcgen05_fence_before();
-                continue;
+            } else {
+                const Strided& out = half == 0 ? p.dV : p.dK;
+                T* row = static_cast<T*>(out.data) + it.b * out.batch + it.hk * out.head + (long long)j * out.row;
+                store_accumulator<T, D>(col, factor, none, j < mk.Skv, row);
+                tcgen05_fence_before();
             }
-            const Strided& out = half == 0 ? p.dV : p.dK;
-            T* row = static_cast<T*>(out.data) + it.b * out.batch + it.hk * out.head + (long long)j * out.row;
-            const bool bad = store_accumulator<T, D>(col, factor, none, j < mk.Skv, row);
-            tcgen05_fence_before();
-            __syncwarp();
-            for (uint32_t again = __ballot_sync(0xffffffffu, bad); again; again &= again - 1)
-                row_dkv<T, D>(p, it.b, it.hk, it.k0 + quad * 32 + __ffs(again) - 1, half == 1, lane);
+            if (__builtin_expect(cleaned[n_box & 3u] == n_box, 0)) spread_dkv<T, D>(p, half, it.b, it.hk, it.k0, it.t0, it.t1, it.begin, it.end, it.split);
         }
     }
 
@@ -884,13 +882,31 @@ struct DqCfg {
     static constexpr int NUM_BARS = 26;
     static constexpr int OFF_CLC = OFF_BAR + NUM_BARS * 8;
     static constexpr int OFF_ITEM = OFF_CLC + 16;
-    static constexpr int OFF_MISC = OFF_ITEM + 64;
+    static constexpr int OFF_CLEANED = OFF_ITEM + 64;           // 4 words
+    static constexpr int OFF_MISC = OFF_CLEANED + 16;
     static constexpr int SMEM_BYTES = OFF_MISC + 16;
     static constexpr uint32_t T_S = 0, T_DP = 128, T_DQ = 384;
     static constexpr uint32_t IDESC_S = idesc_16_f32(Elem<T>::bf16, kTile, kTile, false, false);
     static constexpr uint32_t IDESC_ACC = idesc_16_f32(Elem<T>::bf16, kTile, D, false, true);
     static_assert(SMEM_BYTES <= 232448 && OFF_CLC % 16 == 0, "shared memory");
 };
+
+// A warp's rows of dQ are written, and edge tiles were cleaned: what their keys mean to the rows that see them (NaN, as in dK).
+template <class T, int D>
+__device__ __noinline__ void spread_dq(const MaskedBwdParams& p, int b, int h, int q_base, int t0, int t1) {
+    const MaskArgs& mk = p.mask;
+    const int lane = threadIdx.x & 31, qi = q_base + (threadIdx.x >> 5 & 3) * 32 + lane;
+    int all_lo, all_hi, none, lo = 0, hi = 0;            // the keys that all rows of the tile see
+    row_interval(mk, b, q_base, none, all_hi);
+    row_interval(mk, b, min(q_base + kTile, mk.Sq) - 1, all_lo, none);
+    if (qi < mk.Sq) row_interval(mk, b, qi, lo, hi);
+    const T* rows = static_cast<const T*>(p.K.data) + b * p.K.batch + h / mk.group * p.K.head;
+    uint16_t* to = static_cast<uint16_t*>(p.dQ.data) + b * p.dQ.batch + h * p.dQ.head + (long long)qi * p.dQ.row;
+    for (int t = t0; t < t1; ++t)
+        if (t * kTile < all_lo || (t + 1) * kTile > all_hi)
+            spread_not_finite<T, D, true>(rows, p.K.row, t * kTile, min((t + 1) * kTile, mk.Skv), lo, hi, to, qi < mk.Sq, lane);
+    __syncwarp();
+}
 
 template <class Cfg>
 __global__ void __launch_bounds__(kBwdThreads, 1)
@@ -919,6 +935,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_MISC + 4);
     volatile int* item_box = reinterpret_cast<volatile int*>(smem + Cfg::OFF_ITEM);
+    // cleaned[n & 3] == n: a tile of item n was cleaned.  (Item n + 4 is published once every warp is past n.)
+    volatile uint32_t* cleaned = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_CLEANED);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const MaskArgs& mk = p.mask;
 
@@ -950,6 +968,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         mbar_init(done, 1);
         mbar_init(clc, 1);
         mbar_init(drain, 1);
+        for (int i = 0; i < 4; ++i) cleaned[i] = 0u;
         *abort_flag = 0u;
         fence_mbarrier_init();
     }
@@ -1129,7 +1148,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (it.b < 0) break;
             const int qi = it.q_base + r;                // below Sp
             const long long row = ((long long)it.b * mk.Hq + it.h) * p.Sp + qi;
-            int lo = 0, hi = 0;
+            int lo = 0, hi = INT_MAX;                    // rows behind the last: no mask
             if (qi < mk.Sq) row_interval(mk, it.b, qi, lo, hi);
             const float off = __ldcg(p.offset + row) + shift, neg_delta = __ldcg(p.neg_delta + row);
             const float slope2 = kHasBias<Cfg::MODE> ? __ldg(p.score.slopes + it.h) * kLog2e : 0.0f;
@@ -1149,6 +1168,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 tcgen05_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_read);
+                if (masked && __builtin_expect(products_not_finite(w0, w1, nullptr, lane), 0)) {
+                    if (clean_half_tile<T, DCH>(smem + Cfg::OFF_K + (n % NK) * Cfg::TILE_BYTES, half, lane)) cleaned[n_box & 3u] = n_box;
+                    fence_proxy_async_smem();
+                    if (kHasCap<Cfg::MODE>) {            // a hidden NaN would take its visible neighbour along
+                        const uint32_t v0 = between(lo - k0, hi - k0), v1 = between(lo - k0 - 32, hi - k0 - 32);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            if (!(v0 >> i & 1u)) w0[i] = 0u;
+                            if (!(v1 >> i & 1u)) w1[i] = 0u;
+                        }
+                    }
+                }
                 const float base = (float)(qi + mk.offset - k0);
                 auto offset = [&](int) { return make_float2(off, off); };
                 weights_chunk<T, Cfg::MODE, false>(w0, p.score, slope2, base, offset, none);
@@ -1203,10 +1234,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             T* out = static_cast<T*>(p.dQ.data) + it.b * p.dQ.batch + it.h * p.dQ.head + (long long)qi * p.dQ.row;
             const float factor = kCapFactor<Cfg::MODE> * p.score.scale * exp2f(-kPShift<T> - shift);
             if (half == 0) {
-                const bool bad = store_accumulator<T, D>(lane_base + Cfg::T_DQ, factor, empty, qi < mk.Sq, out);
-                __syncwarp();
-                for (uint32_t again = __ballot_sync(0xffffffffu, bad); again; again &= again - 1)
-                    row_dq<T, D>(p, it.b, it.h, it.q_base + quad * 32 + __ffs(again) - 1, lane);
+                store_accumulator<T, D>(lane_base + Cfg::T_DQ, factor, empty, qi < mk.Sq, out);
+                if (__builtin_expect(cleaned[n_box & 3u] == n_box, 0)) spread_dq<T, D>(p, it.b, it.h, it.q_base, it.t0, it.t1);
             }
             tcgen05_fence_before();
         }

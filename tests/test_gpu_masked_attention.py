@@ -662,3 +662,101 @@ def test_infinities_in_every_item():
         assert status == gsr.Status.OK, hex(code)
         clean[..., 3] = float("inf")
         assert torch.equal(o, clean) and torch.equal(lse, lse0)
+
+
+def check_natural_backward(c):
+    """The gradients' formulas in fp64 with the given lse and O, infinities and NaN taking their course among the pairs
+    that see each other; rows whose lse is -inf add nothing of their own.  Tolerances as in check_backward."""
+    B, Hq, Sq, D = c.q.shape
+    Hkv, Skv = c.k.shape[1:3]
+    g, see = Hq // Hkv, torch.tensor(c.see, device=DEV)[:, None]
+    q, do, o, lse = (t.double() for t in (c.q, c.do, c.o, c.lse))
+    k, v = (t.double().repeat_interleave(g, 1) for t in (c.k, c.v))
+    clean = lambda t: torch.where(t.isfinite(), t, 0.0)
+    scale = c.scale or D ** -0.5
+    x = q @ k.transpose(-1, -2) * scale
+    t = torch.zeros_like(x)
+    if c.cap:
+        t = torch.tanh(x / c.cap)
+        x = c.cap * t
+    if c.slopes is not None:
+        dist = torch.arange(Sq, device=DEV)[:, None] + Skv - Sq - torch.arange(Skv, device=DEV)
+        x = x - c.slopes.double()[None, :, None, None] * dist.abs()
+    none = (lse == -torch.inf)[..., None] | ~see
+    P = torch.where(none, 0.0, torch.exp(x - lse[..., None]))
+    dP, delta = do @ v.transpose(-1, -2), (do * o).sum(-1, keepdim=True)
+    dS = torch.where(none, 0.0, P * (dP - delta) * (1 - t * t))
+    aS = clean(P * (clean(do).abs() @ clean(v).abs().transpose(-1, -2) + clean(do * o).abs().sum(-1, keepdim=True)))
+    fold = lambda a: a.reshape(B, Hkv, g, Skv, D).sum(2)
+    T, seen = (lambda a: a.transpose(-1, -2)), see.expand(B, Hq, Sq, Skv).double()
+    meets = lambda a, y: (a @ (~y.isfinite()).double()) > 0          # a pair that sees something not finite
+    want = (scale * dS @ clean(k), scale * fold(T(dS) @ clean(q)), fold(T(P) @ clean(do)))
+    special = (meets(seen, k), fold(meets(T(seen), q).double()) > 0, fold(meets(T(seen), do).double()) > 0)
+    mags = [(scale * a @ clean(k).abs(), scale * fold(T(a) @ clean(q).abs())) for a in (clean(dS).abs(), aS, seen)]
+    last = fold(T(clean(P)) @ clean(do).abs())
+    norm = lambda y: clean(y).norm(dim=-1).max().item()
+    low = [c.tiny * 2 * norm(do) * norm(v) * 2.0 ** -14] * 2 + [c.tiny * 2.0 ** -12]
+    for i, (got, w, sp) in enumerate(zip(c.grads, want, special)):
+        got, bad = got.double(), sp | ~w.isfinite()
+        assert torch.equal(bad, ~got.isfinite()), ("dQ dK dV".split()[i], (bad != ~got.isfinite()).sum().item())
+        a, b, plain = (m[i] for m in mags) if i < 2 else (last, last, fold(T(seen) @ clean(do).abs()))
+        w = clean(w)
+        tol = (c.u * a + 2.0 ** -13 * b) * (1 + c.u) + c.u * w.abs() + c.tiny + low[i] * plain
+        assert torch.all(((got - w).abs() <= tol) | bad), ("dQ dK dV".split()[i], ((got - w).abs() / tol)[~bad].max().item())
+
+
+@pytest.mark.parametrize("what", ["dO", "Q", "K", "V", "all"])
+@pytest.mark.parametrize("name", SPECIAL)
+def test_gradients_with_infinite_and_nan_values(name, what):
+    c = Case(**SPECIAL[name])
+    nan, inf = float("nan"), float("inf")
+    if what in ("Q", "all"):
+        spoil(c.q, 3, [inf, nan], 5)
+    if what in ("K", "all"):
+        spoil(c.k, 3, [nan, -inf], 6)
+    if what in ("V", "all"):
+        spoil(c.v, 3, [inf, nan], 7)
+    c.forward()
+    if what in ("dO", "all"):
+        spoil(c.do, 4, [inf, nan, -inf], 8)
+        c.do[0, 0, c.do.shape[2] // 3] = nan
+    c.backward()
+    check_natural_backward(c)
+
+
+@pytest.mark.parametrize("D,dtype", [(128, F16), (64, BF16)])
+def test_an_infinite_gradient_takes_no_longer(D, dtype):
+    """One infinity in dO, 8 heads over 1 of 32768 tokens: no wait of 0.02 s runs out, and what it does not reach keeps its
+    bits.  Then dO of NaN behind the last document: it reaches nothing."""
+    S, i = 32768, 20001
+    g = torch.Generator(device=DEV).manual_seed(D)
+    q, do = (torch.randn(1, 8, S, D, generator=g, device=DEV).to(dtype) for _ in range(2))
+    k, v = (torch.randn(1, 1, S, D, generator=g, device=DEV).to(dtype) for _ in range(2))
+    o, lse = torch.empty_like(q), torch.empty(1, 8, S, device=DEV)
+
+    def run(**kw):
+        grads = [torch.full_like(t, 7.0) for t in (q, k, v)]
+        gsr.masked_attention_bwd(do, q, k, v, o, lse, *grads, **kw)
+        status, code = gsr.device_status()
+        assert status == gsr.Status.OK, hex(code)
+        return grads
+
+    gsr.masked_attention_fwd(q, k, v, o, lse, causal=True)
+    clean, old = run(causal=True), do[0, 3, i, 7].item()
+    do[0, 3, i, 7] = float("inf")
+    gsr.set_wait_timeout_ns(20_000_000)
+    try:
+        dq, dk, dv = run(causal=True)
+        assert not dq[0, 3, i].isfinite().any() and not dk[:, :, :i + 1].isfinite().any()
+        assert torch.all(dv[0, 0, :i + 1, 7] == float("inf"))
+        dq[0, 3, i], dk[:, :, :i + 1], dv[0, 0, :i + 1, 7] = clean[0][0, 3, i], clean[1][:, :, :i + 1], clean[2][0, 0, :i + 1, 7]
+        assert all(torch.equal(a, b) for a, b in zip((dq, dk, dv), clean))
+        do[0, 3, i, 7] = old
+        kw = dict(doc_bounds=torch.tensor([[0, S - 100]], dtype=torch.int32, device=DEV))
+        gsr.masked_attention_fwd(q, k, v, o, lse, **kw)
+        clean = run(**kw)
+        for t in (do, q, k, v):
+            t[:, :, S - 100:] = float("nan")
+        assert all(torch.equal(a, b) for a, b in zip(run(**kw), clean))
+    finally:
+        gsr.set_wait_timeout_ns(1_000_000_000)
