@@ -259,7 +259,8 @@ gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor
  *   softcap, alibi_slopes, softmax_scale  as in gsr_attention_desc.
  *   Q, O              total_q x heads_q x head_dim with the given strides; heads_q / heads_kv <= 128.
  * kv_lens, q_starts (batch + 1), parents (total_q): device int32.  A node that sees nothing gets
- * O = 0.
+ * O = 0.  Infinities and NaN in V reach their columns of the nodes that see them, as in
+ * masked_attention_fwd, and no sibling.
  *
  *   workspace  device pointer, 16-byte aligned, tree_attention_workspace(desc) bytes, for this
  *              call alone until it has finished; or NULL, as for masked_attention_fwd.

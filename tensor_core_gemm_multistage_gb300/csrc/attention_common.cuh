@@ -145,8 +145,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // tanh(x) = 1 - 2 / (1 + e^(2x)): with r = 1 / (1 + 2^(cap_in s)) the capped score is
 // cap_out (1 - 2 r), and tanh's derivative 4 r (1 - r) has no cancellation.  The absolute error
 // of a score is a few units of cap 2^-24, which is what the softmax sees.
-__device__ __forceinline__ float cap_r(float s, float cap_in) { return rcp_approx(1.0f + ex2_approx(s * cap_in)); }
-
+//
 // Capped scores of a row are taken through z = (8/3) scale q.k / cap, so that bit 30 of a z, set where
 // its magnitude is 2 or more (or it is infinite or NaN), says that the tanh's argument is beyond 3/4.
 //
@@ -191,9 +190,9 @@ __device__ __forceinline__ uint32_t cap_scale(uint32_t (&rr)[32], float cap_z) {
     return bits;
 }
 
-// cap_r of two products, in place, with one reciprocal, 1 / a = b / (a b).  2^60 keeps a b finite and is
-// tanh = 1 to the last bit.  A NaN stays one and takes its partner along; the row is then not finite and
-// is computed again.  For the gradients' kernels, whose special-function unit has room (4 x 32 x 4096 x 128
+// r of two products, in place, with one reciprocal, 1 / a = b / (a b).  2^60 keeps a b finite and is
+// tanh = 1 to the last bit.  A NaN stays one and takes its partner along: hidden products that are not
+// finite are set to 0 first.  For the gradients' kernels, whose special-function unit has room (4 x 32 x 4096 x 128
 // capped: 3287 us, 3488 with two reciprocals; the polynomial, in two copies of the code, was slower
 // than either).
 __device__ __forceinline__ float min_nan(float a, float b) {
@@ -459,12 +458,12 @@ struct Marks {
                 }
             }
     }
-    // Into the row, which this lane has written; Out is uint16_t (a T) or float.
+    // Into column blocks [c0, c1) of the row, which this lane has written; Out is uint16_t (a T) or float.
     template <class T, class Out>
-    __device__ __forceinline__ void apply(Out* row) const {
+    __device__ __forceinline__ void apply(Out* row, int c0 = 0, int c1 = D / 32) const {
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
-            for (uint32_t bits = plus[c] | minus[c]; bits; bits &= bits - 1) {
+            for (uint32_t bits = c >= c0 && c < c1 ? plus[c] | minus[c] : 0u; bits; bits &= bits - 1) {
                 const int e = __ffs(bits) - 1;
                 const float x = (plus[c] >> e & 1u) ? ((minus[c] >> e & 1u) ? NAN : INFINITY) : -INFINITY;
                 add_to<T>(row + c * 32 + e, x);
@@ -513,24 +512,9 @@ __device__ __noinline__ void spread_not_finite(const T* rows, long long pitch, i
 }
 
 // ---------------------------------------------------------------------------
-// One row by one warp
+// Rows by one warp
 // ---------------------------------------------------------------------------
 // Lane t holds elements [t D/32, (t + 1) D/32) of a row.
-template <class T, int D>
-__device__ __forceinline__ void load_row(const T* row, int lane, float (&x)[D / 32]) {
-    if constexpr (D == 128) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(row) + lane);
-        const float2 a = Elem<T>::unpack(v.x), b = Elem<T>::unpack(v.y);
-        x[0] = a.x;
-        x[1] = a.y;
-        x[2] = b.x;
-        x[3] = b.y;
-    } else {
-        const float2 a = Elem<T>::unpack(__ldg(reinterpret_cast<const uint32_t*>(row) + lane));
-        x[0] = a.x;
-        x[1] = a.y;
-    }
-}
 template <class T, int D>
 __device__ __forceinline__ void store_row(T* row, int lane, const float (&x)[D / 32]) {
     if constexpr (D == 128)
@@ -542,63 +526,6 @@ __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
-}
-template <int N>
-__device__ __forceinline__ float warp_dot(const float (&a)[N], const float (&b)[N]) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) s = fmaf(a[i], b[i], s);
-    return warp_sum(s);
-}
-
-// The score of a raw product in log2 units, before the distance bias; `grad` is its derivative
-// with respect to scale * product.
-__device__ __forceinline__ float score_of(float s, const ScoreArgs& sc, float& grad) {
-    if (sc.cap_in == 0.0f) {
-        grad = 1.0f;
-        return s * sc.sl2;
-    }
-    const float r = cap_r(s, sc.cap_in);
-    grad = 4.0f * r * (1.0f - r);
-    return sc.cap_out * (1.0f - 2.0f * r);
-}
-
-// Whether a row's sum is NaN in every element, and so stays it: rows are computed again because they
-// are not finite, and where that is the result itself (a NaN in the query, say) the first keys tell.
-template <int N>
-__device__ __forceinline__ bool all_nan(const float (&acc)[N]) {
-    bool nan = true;
-#pragma unroll
-    for (int i = 0; i < N; ++i) nan &= acc[i] != acc[i];
-    return __all_sync(0xffffffffu, nan);
-}
-
-// Softmax-weighted sum of the values of keys [lo, hi) that `at` lets the row see, in one pass with
-// the running maximum m and sum l.  at(j, k, v, dist) gives key j's rows and its distance.
-template <class T, int D, class At>
-__device__ __forceinline__ void row_forward(const float (&q)[D / 32], int lo, int hi, const ScoreArgs& sc,
-                                            float slope2, int lane, At at, float (&acc)[D / 32], float& m,
-                                            float& l) {
-    m = -INFINITY;
-    l = 0.0f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
-    for (int j = lo; j < hi; ++j) {
-        const T *k, *v;
-        float dist, grad, x[D / 32];
-        if (!at(j, k, v, dist)) continue;
-        load_row<T, D>(k, lane, x);
-        const float y = score_of(warp_dot(q, x), sc, grad) - slope2 * dist;
-        load_row<T, D>(v, lane, x);
-        const float mn = fmaxf(m, y);
-        const float f = mn == -INFINITY ? 0.0f : ex2_approx(m - mn);
-        const float p = mn == -INFINITY ? (isnan(y) ? y : 0.0f) : ex2_approx(y - mn);
-        l = fmaf(l, f, p);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(acc[i], f, p * x[i]);
-        m = mn;
-        if (l != l || all_nan(acc)) break;
-    }
 }
 
 }  // namespace gsr

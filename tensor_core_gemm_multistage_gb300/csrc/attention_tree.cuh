@@ -30,8 +30,8 @@
 //    side (one box a chunk: pages of 8 rows 321 us where HBM needs 170, of 16 rows 214).
 //  * Rows of the last tile behind kv_lens, and pieces whose page is not in the pool, are masked, and
 //    their V rows set to zero in shared memory before the product (0 times what a page holds there
-//    may be NaN).  A row that is not finite all the same (a hidden sibling's V) is computed again
-//    from the keys it sees (tree_row).
+//    may be NaN).  Of the tiles that hold nodes of a tree, where nodes do not see their siblings, the elements of V
+//    that are not finite are ("Infinities and NaN behind a mask" in attention_common.cuh).
 #pragma once
 
 #include "attention_common.cuh"
@@ -83,41 +83,6 @@ __device__ __forceinline__ uint64_t ancestors(const int* parents, int start, int
 // The depth of node t's ancestor (or of t itself) u: its own ancestors are those of t before it.
 __device__ __forceinline__ int depth_of(uint64_t see, int u) { return __popcll(see & ((1ull << u) - 1)); }
 
-// Node t, query head h, by one warp: every key it sees, in fp32.  `half` 0 or 1 writes that half of
-// the columns, -1 all.
-template <class T, int D>
-__device__ __noinline__ void tree_row(const TreeParams& p, int b, const TreeRequest& r, int t, int h, int half, int lane) {
-    const uint64_t see = ancestors(p.parents, r.start, t);
-    const int ctx = r.ctx, pos = ctx + __popcll(see) - 1;
-    const float slope2 = p.score.slopes ? __ldg(p.score.slopes + h) * kLog2e : 0.0f;
-    const long long row = r.start + t;
-    const int hk = h / p.group;
-    float q[D / 32], acc[D / 32], m, l;
-    load_row<T, D>(static_cast<const T*>(p.Q) + row * p.q_row + h * p.q_head, lane, q);
-    const T* kb = static_cast<const T*>(p.K.data) + hk * p.K.head;
-    const T* vb = static_cast<const T*>(p.V.data) + hk * p.V.head;
-    row_forward<T, D>(q, 0, r.kv, p.score, slope2, lane,
-                      [&](int j, const T*& k, const T*& v, float& dist) {
-                          int at = j;
-                          if (j >= ctx) {
-                              const int u = j - ctx;
-                              if (u >= 64 || !(see >> u & 1)) return false;
-                              at = ctx + depth_of(see, u);
-                          }
-                          dist = (float)(pos - at);
-                          const int page = __ldg(p.table + (long long)b * p.table_width + j / p.page);
-                          if (page < 0 || page >= p.num_pages) return false;
-                          k = kb + page * p.K.batch + (j % p.page) * p.K.row;
-                          v = vb + page * p.V.batch + (j % p.page) * p.V.row;
-                          return true;
-                      },
-                      acc, m, l);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[e] *= inv;
-    if (half < 0 || half == lane >> 4) store_row<T, D>(static_cast<T*>(p.O) + row * p.o_row + h * p.o_head, lane, acc);
-}
-
 // ---------------------------------------------------------------------------
 // Configuration
 // ---------------------------------------------------------------------------
@@ -143,7 +108,8 @@ struct TreeCfg {
     static constexpr int OFF_ITEM = OFF_VALID + NB * 4;            // 2 x 12 ints
     static constexpr int OFF_SCAN = (OFF_ITEM + 96 + 7) / 8 * 8;   // 16 partial sums, then the CTA's first unit
     static constexpr int OFF_ML = OFF_SCAN + 16 * 8 + 16;          // 2 groups x 128 rows of (m, l)
-    static constexpr int OFF_MISC = OFF_ML + 2 * 128 * 8;
+    static constexpr int OFF_CLEANED = OFF_ML + 2 * 128 * 8;       // 4 words
+    static constexpr int OFF_MISC = OFF_CLEANED + 16;
     static constexpr int SMEM_BYTES = OFF_MISC + 16;
     static constexpr uint32_t T_S = 0, T_O = 256, P_COL = 64;
     static constexpr uint32_t IDESC_S = idesc_16_f32(Elem<T>::bf16, 128, 128, false, false);
@@ -160,6 +126,50 @@ __device__ __forceinline__ float* part_o(const TreeParams& p, long long slot, in
 __device__ __forceinline__ float2* part_ml(const TreeParams& p, long long slot, int row) {
     return p.parts_ml + slot * p.part_rows + row;
 }
+
+// A warp's quarter of a V tile without what is not finite; true if there was something.
+template <class T, int D>
+__device__ __noinline__ bool clean_quarter(uint8_t* at, int lane) {
+    if (!pieces_not_finite<T>(at, 4 * D, lane)) return false;
+    zero_not_finite<T>(at, 4 * D, lane);
+    fence_proxy_async_smem();
+    return true;
+}
+
+// A warp's rows of an item are written (from column block c0 of 32 on, up to c1), and tiles with nodes were cleaned: what
+// their V means to the nodes that see them.  `tile_node` is the first node of the warp's query tile, `part_row`
+// that tile's first row in slot `slot` (below 0: the item is whole); key tiles [t0, t1) are the item's.
+template <class T, int D>
+__device__ __noinline__ void spread_nodes(const TreeParams& p, int b, int hk, int tile_node, int t0, int t1, int slot, int part_row, int c0,
+                                          int c1) {
+    const int lane = threadIdx.x & 31, rq = (threadIdx.x >> 5 & 3) * 32 + lane;
+    const TreeRequest r = tree_request(p, b);
+    const int node_in = rq / p.group, node = tile_node + node_in, h = hk * p.group + rq - node_in * p.group;
+    const bool real = node_in < p.tile_nodes && node < r.nodes;
+    const uint64_t see = real ? ancestors(p.parents, r.start, node) : 0ull;
+    Marks<D> marks;
+    // from the first cleaned tile on; what is before the tree every node sees
+    for (int j0 = max(r.ctx, 0) / p.tile_keys * p.tile_keys, end = min(r.kv, r.ctx + 64); j0 < end; j0 += 4) {
+        uint16_t x[4][D / 32];
+        bool sees[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int j = min(j0 + k, end - 1), t = j / p.tile_keys, page = __ldg(p.table + (long long)b * p.table_width + j / p.page);
+            const bool there = t >= t0 && t < t1 && page >= 0 && page < p.num_pages;
+            sees[k] = there && real && (j < r.ctx || (see >> (j - r.ctx) & 1));
+            const unsigned short* v = static_cast<const unsigned short*>(p.V.data) + (there ? page : 0) * p.V.batch + (j % p.page) * p.V.row +
+                                      hk * p.V.head;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) x[k][c] = there ? __ldg(v + c * 32 + lane) : (unsigned short)0;
+        }
+        marks.template take<T, false, 4>(x, sees);
+    }
+    if (real && slot >= 0) marks.template apply<T>(part_o(p, slot, part_row + rq, D), c0, c1);
+    if (real && slot < 0)
+        marks.template apply<T>(static_cast<uint16_t*>(p.O) + (long long)(r.start + node) * p.o_row + h * p.o_head, c0, c1);
+    __syncwarp();
+}
+
 // Of a grid's CTAs as many as there are units take part, so each has one at least.  CTA c's first
 // unit of U, and the CTA that holds unit u.
 __device__ __forceinline__ int busy_ctas(long long U, int grid) { return (int)min((long long)grid, U); }
@@ -202,6 +212,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_MISC + 4);
     volatile int* item_box = reinterpret_cast<volatile int*>(smem + Cfg::OFF_ITEM);
     volatile uint32_t* valid_box = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_VALID);
+    // cleaned[n & 3] == n: a tile of item n was cleaned.  (Item n + 4 is published once every warp is past n.)
+    volatile uint32_t* cleaned = reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_CLEANED);
     long long* scan = reinterpret_cast<long long*>(smem + Cfg::OFF_SCAN);
     long long* first_box = scan + 16;                            // request, unit in it
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -237,6 +249,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
         mbar_init(ml_free, Cfg::SM_THREADS / 32);
         mbar_init(drain, 1);
         mbar_init(o_read, Cfg::SM_THREADS / 32);
+        for (int i = 0; i < 4; ++i) cleaned[i] = 0u;
         *abort_flag = 0u;
         fence_mbarrier_init();
     }
@@ -665,6 +678,10 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                     }
                     fence_proxy_async_smem();
                 }
+                // a tile with nodes, of a request that has several
+                if (it.kv - it.ctx > 1 && k0 + p.tile_keys > it.ctx &&
+                    clean_quarter<T, D>(smem + Cfg::OFF_RING + (e % NB) * Cfg::TILE_BYTES + quad * (Cfg::TILE_BYTES / 4), lane))
+                    cleaned[n_item & 3u] = n_item;
                 tmem_st_wait();
                 tcgen05_fence_before();
                 mbar_arrive(pfull(q));
@@ -679,7 +696,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                 if (lane == 0) mbar_arrive(ml_full);
             }
             if (!(ok = __all_sync(0xffffffffu, w.wait(odone(q, n_item - 1), ((n_item - 1) >> 1) & 1u, kDevErrEpilogueFull)))) break;
-            float f0 = 1.0f, f1 = 0.0f;                  // factors of the two accumulators
+            float f0 = 1.0f, f1 = 0.0f;                  // factors of the two accumulators, and whether they hold anything
+            bool use0 = true, use1 = false;
             if (turns) {
                 if (!(ok = __all_sync(0xffffffffu, w.wait(ml_full, n_ml & 1u, kDevErrEpilogueFull)))) break;
                 const float2 a = ml_box[rq], b = ml_box[128 + rq];
@@ -687,21 +705,22 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                 if (lane == 0) mbar_arrive(ml_free);
                 ++n_ml;
                 m = fmaxf(a.x, b.x);
-                f0 = m == -INFINITY ? 0.0f : ex2_approx(a.x - m);
-                f1 = m == -INFINITY ? 0.0f : ex2_approx(b.x - m);
-                l = (f0 == 0.0f && a.y == a.y ? 0.0f : a.y * f0) + (f1 == 0.0f && b.y == b.y ? 0.0f : b.y * f1);
+                f0 = a.x == -INFINITY ? 0.0f : ex2_approx(a.x - m);
+                f1 = b.x == -INFINITY ? 0.0f : ex2_approx(b.x - m);
+                use0 = a.x != -INFINITY || a.y != a.y;
+                use1 = b.x != -INFINITY || b.y != b.y;
+                l = a.y * f0 + b.y * f1;                 // a sum of nothing is 0, or NaN
             }
             tcgen05_fence_after();
             // the rows, or this CTA's part of them; of one query tile's rows each group writes half the
             // columns
-            bool bad = false;
+            const bool was_cleaned = cleaned[n_item & 3u] == n_item;
+            const int c_first = turns ? q * (D / 64) : 0, c_end = turns ? c_first + D / 64 : D / 32;
             if (busy) {
-                const float inv = it.slot >= 0 ? 1.0f : (l > 0.0f ? 1.0f / l : 0.0f);
+                const float inv = it.slot >= 0 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
                 const bool none = l == 0.0f;             // nothing seen here: O holds 0 V
-                bad = !(l < INFINITY);
                 f0 *= inv;
                 f1 *= inv;
-                const int c_first = turns ? q * (D / 64) : 0, c_end = turns ? c_first + D / 64 : D / 32;
                 const uint32_t o0 = turns ? lane_base + Cfg::T_O : o_col, o1 = lane_base + Cfg::T_O + D;
                 T* row = static_cast<T*>(p.O) + (long long)(it.start + node) * p.o_row + h * p.o_head;
                 float* part = it.slot < 0 ? nullptr : part_o(p, it.slot, (turns ? 0 : q * 128) + rq, D);
@@ -716,10 +735,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                     float y[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        // an accumulator whose factor is 0 may hold anything
-                        y[j] = f0 == 0.0f || none ? 0.0f : __uint_as_float(r0[j]) * f0;
-                        if (turns && steps > 1 && f1 != 0.0f && !none) y[j] = fmaf(__uint_as_float(r1[j]), f1, y[j]);
-                        bad |= !(fabsf(y[j]) < INFINITY);
+                        y[j] = !use0 || none ? 0.0f : __uint_as_float(r0[j]) * f0;
+                        if (turns && steps > 1 && use1 && !none) y[j] = fmaf(__uint_as_float(r1[j]), f1, y[j]);
                     }
                     if (!real) continue;
                     if (it.slot >= 0) {
@@ -739,11 +756,9 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
             tcgen05_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_read);
-            for (uint32_t again = __ballot_sync(0xffffffffu, bad && real && it.slot < 0); again; again &= again - 1) {
-                const int src = __ffs(again) - 1;
-                tree_row<T, D>(p, it.b, tree_request(p, it.b), __shfl_sync(0xffffffffu, node, src), __shfl_sync(0xffffffffu, h, src),
-                               turns ? q : -1, lane);
-            }
+            if (busy && was_cleaned)
+                spread_nodes<T, D>(p, it.b, it.hk, it.n0 + (turns ? 0 : q * p.tile_nodes), it.t0, it.t1, it.slot, turns ? 0 : q * 128, c_first,
+                                   c_end);
         }
     }
 
@@ -798,11 +813,15 @@ __global__ void __launch_bounds__(kJoinThreads) gsr_tree_join_kernel(const __gri
     if (c0 >= c1) return;                                        // written whole
     float m = -INFINITY, l = 0.0f, acc[D / 32] = {};
     auto add = [&](float pm, float pl, const float* o) {
+        if (pm == -INFINITY) {                                   // no key that the row sees: the sum is 0, or NaN
+            l += pl;
+            return;
+        }
         const float mn = fmaxf(m, pm);
-        const float f0 = mn == -INFINITY ? 0.0f : ex2_approx(m - mn), f1 = mn == -INFINITY ? 0.0f : ex2_approx(pm - mn);
-        l = l * f0 + (f1 == 0.0f && pl == pl ? 0.0f : pl * f1);
+        const float f0 = m == -INFINITY ? 0.0f : ex2_approx(m - mn), f1 = ex2_approx(pm - mn);
+        l = l * (m == -INFINITY ? 1.0f : f0) + pl * f1;          // nothing yet: 0, or NaN
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) acc[e] = acc[e] * f0 + (f1 == 0.0f ? 0.0f : o[e] * f1);
+        for (int e = 0; e < D / 32; ++e) acc[e] = acc[e] * f0 + o[e] * f1;
         m = mn;
     };
     for (int c = c0 + warp; c <= c1; c += WARPS) {
@@ -826,17 +845,9 @@ __global__ void __launch_bounds__(kJoinThreads) gsr_tree_join_kernel(const __gri
 #pragma unroll
         for (int i = 1; i < WARPS; ++i) add(sm[i][D], sm[i][D + 1], &sm[i][lane * (D / 32)]);
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    bool bad = !(l < INFINITY);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-        bad |= !(fabsf(acc[e]) < INFINITY);
-        acc[e] *= inv;
-    }
-    if (__any_sync(0xffffffffu, bad)) {
-        tree_row<T, D>(p, b, r, t, h, -1, lane);
-        return;
-    }
+    for (int e = 0; e < D / 32; ++e) acc[e] *= inv;
     store_row<T, D>(static_cast<T*>(p.O) + (long long)n * p.o_row + h * p.o_head, lane, acc);
 }
 

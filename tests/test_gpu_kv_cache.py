@@ -335,6 +335,86 @@ def test_rows_of_no_request():
     assert torch.all(t.o == 7.0)
 
 
+# ---------------------------------------------------------------------------- infinities and NaN that some nodes see
+
+def check_natural(t):
+    """The formula in fp64 with infinities and NaN taking their course among the keys that a node sees."""
+    q, kc, vc, got = (llm.f64(x) for x in (t.q, t.kc, t.vc, t.o))
+    N, Hq, D = q.shape
+    Hkv, pages, slopes = kc.shape[2], kc.shape[0], None if t.slopes is None else t.slopes.cpu().double().numpy()
+    for b, kv in enumerate(t.kv):
+        s, T = int(t.starts[b]), t.T[b]
+        ctx = kv - T
+        for u in range(T):
+            chain = [u]
+            while True:
+                up = chain[-1] - 1 if t.parents is None else t.parents[s + chain[-1]]
+                if up < 0 or up >= chain[-1]:
+                    break
+                chain.append(up)
+            keys = [(j, j) for j in range(ctx)] + [(ctx + c, ctx + d) for d, c in enumerate(reversed(chain))]
+            pg, off, at = np.array([(int(t.table[b][j // t.page]), j % t.page, where) for j, where in keys]).T
+            for h in range(Hq):
+                k, v = kc[pg, off, h * Hkv // Hq], vc[pg, off, h * Hkv // Hq]
+                with np.errstate(invalid="ignore"):
+                    x = k @ q[s + u, h] * (t.scale or D ** -0.5)
+                    if t.cap:
+                        x = t.cap * np.tanh(x / t.cap)
+                    if slopes is not None:
+                        x = x - slopes[h] * (ctx + len(chain) - 1 - at)
+                    p = np.exp(x - x.max())
+                    p /= p.sum()
+                clean = np.where(np.isfinite(v), v, 0.0)
+                want, terms = p @ clean, p @ np.abs(clean)
+                plus, minus = ((np.isnan(v) | (v == i)).any(0) for i in (np.inf, -np.inf))
+                bad, y = plus | minus | ~np.isfinite(want), got[s + u, h]
+                assert np.array_equal(bad, ~np.isfinite(y)), (b, u, h)
+                if slopes is None and np.isfinite(want).all():       # with a bias a weight may be 0
+                    assert np.all(y[plus & ~minus] == np.inf) and np.all(y[minus & ~plus] == -np.inf)
+                assert np.isnan(y[plus & minus]).all()
+                tol = (t.u + 2.0 ** -13) * terms * (1 + t.u) + t.u * np.abs(want) + t.tiny
+                assert np.all((np.abs(y - want) <= tol)[~bad])
+
+
+@pytest.mark.parametrize("what", ["V", "K", "nodes"])
+@pytest.mark.parametrize("name", ["trees", "trees_only", "trees_cap_alibi", "trees_alibi", "chain", "chain_alibi_cap", "flat", "large_group",
+                                  "odd_group", "odd_large_page", "decode_batch", "heads_first"])
+def test_infinite_and_nan_values_reach_the_nodes_that_see_them(name, what):
+    t = Tree(**TREES[name])
+    r, values = np.random.default_rng(4), [float("inf"), float("nan"), -float("inf")]
+    for i in range(12):
+        b = int(r.integers(len(t.kv)))
+        low = t.kv[b] - t.T[b] if what == "nodes" else 0         # a key of the request, or one of its nodes
+        j = int(r.integers(low, t.kv[b]))
+        at = int(t.table[b][j // t.page]), j % t.page, int(r.integers(t.kc.shape[2]))
+        if what == "K" and i < 2:
+            t.kc[at + (int(r.integers(t.kc.shape[3])),)] = float("nan")
+        elif what == "nodes" and i == 0:
+            t.vc[at] = float("nan")
+        elif what != "K":
+            t.vc[at + (int(r.integers(t.kc.shape[3])),)] = values[i % 3]
+    t.run()
+    check_natural(t)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_an_infinite_value_takes_no_longer(T):
+    # long contexts: no wait of 0.02 s runs out, and all other columns keep their bits
+    t = Tree(kv=[30000, 20000, 30000], T=[T, T, 1], Hq=16, Hkv=2, D=128, page=64, parents="flat")
+    clean = t.run().o.clone()
+    t.vc[int(t.table[0][3]), 5, :, 7] = float("inf")              # a key that request 0's nodes all see
+    j = t.kv[1] - 1                                              # request 1's last node: itself alone
+    t.vc[int(t.table[1][j // 64]), j % 64, :, 9] = float("nan")
+    gsr.set_wait_timeout_ns(20_000_000)
+    try:
+        t.run()
+    finally:
+        gsr.set_wait_timeout_ns(1_000_000_000)
+    assert torch.all(t.o[:T, :, 7] == float("inf")) and torch.all(t.o[2 * T - 1, :, 9].isnan())
+    t.o[:T, :, 7], t.o[2 * T - 1, :, 9] = clean[:T, :, 7], clean[2 * T - 1, :, 9]
+    assert torch.equal(t.o, clean)
+
+
 # ---------------------------------------------------------------------------- the path together
 
 @pytest.mark.parametrize("captured", [False, True])
