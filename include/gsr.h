@@ -225,7 +225,9 @@ gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor
  * Gradients of masked_attention_fwd: dQ, dK, dV from dO and the forward's inputs, O and lse (dO,
  * O, dQ shaped as Q; dK, dV as K).  dK and dV sum over the query heads of a group.  Results do not
  * depend on the order of execution.  P and dS are rounded to the operands' type for the matrix
- * products; in float16 dS carries a power of two that keeps it in range for any size of dO.
+ * products; in float16 dS carries powers of two, one for each query in dQ and one for each key in dK (the
+ * same for nearby keys of a document), that keep it in range whatever the size of dO there.  They take
+ * V's size by key/value head: values 2^13 below the largest of their head lose digits of dS.
  * Queries without keys get dQ = 0 and add nothing, whatever their dO holds.  Infinities and NaN in
  * dO, Q, K and V reach the gradients of the pairs that see each other and no other elements, and a call
  * with them takes about as long as one without.

@@ -8,18 +8,19 @@
 // dK and dV of a key/value head sum over the query heads of its group.
 //
 // Three launches: one pass over the rows (delta), then dK and dV by the CTA that owns the keys and
-// dQ by the CTA that owns the queries (one more where dK and dV are cut into parts; a tiny one ahead in
-// fp16).  The two
+// dQ by the CTA that owns the queries (one more where dK and dV are cut into parts).  The two
 // recompute S and dP, seven products of 128 x 128 x D instead of the five that one pass with atomically
 // added dQ would take; in return no result depends on the order of atomics, dQ needs no fp32 buffer,
 // and every accumulator stays in TMEM from the first product to the last.  dQ's CTAs start on the SMs that
 // run out of dK and dV items.  4 x 32 x 4096 x 128 without a mask: 2797 us, 983 TFLOP/s of the five
 // products, 1376 of the seven (69 % of the measured peak); causal 1532 and 897.
 //
-// fp16: P is carried as 2^12 P and dS as 2^(12 + e) dS with one e a call, so that neither goes
-// subnormal where a row has many keys or dO is small.  |dO_i . V_j - delta_i| <= 2 max|dO| max|V|
-// (Cauchy-Schwarz; O is a mean of V rows), and e is the largest power that keeps dS below 2^15 by
-// this bound.  bf16 has fp32's range and needs neither.
+// fp16: P is carried as 2^12 P and dS as 2^(12 + e) dS, so that neither goes subnormal where a row has many
+// keys or dO is small.  |dO_i . V_j - delta_i| <= 2 |dO_i| max|V| (Cauchy-Schwarz; O is a mean of V rows), and e is
+// the largest power that keeps dS below 2^15 by this bound: one for each query in dQ, and in dK one for each key,
+// for the largest dO_i of the queries that see keys of its document, so that documents and heads with small dO keep
+// their digits beside those with large ones.  Either leaves with its row of the accumulator.  max|V| is the
+// key/value head's.  bf16 has fp32's range and needs neither.
 //
 // Masked pairs get P = dS = 0 by selection, but a row of dO, Q or K that is not finite turns 0
 // times itself into NaN inside a product.  Where a warp masks, its products and the rows' delta tell: a row of
@@ -38,15 +39,64 @@ namespace gsr {
 template <class T>
 constexpr float kPShift = Elem<T>::bf16 ? 0.0f : 12.0f;      // log2 of P's factor
 
-// log2 of dS's further factor.  A capped dS is held without its factor 4 (weights_chunk), which leaves
-// room for two more bits.
+// log2 of dS's further factor, from the squares of the bound's two norms.  A capped dS is held without its factor 4
+// (weights_chunk), which leaves room for two more bits.
 template <class T, int MODE>
-__device__ __forceinline__ float ds_shift(const unsigned* norms) {
+__device__ __forceinline__ float ds_shift(float dO2, float v2) {
     if (Elem<T>::bf16) return 0.0f;
-    const float n = __uint_as_float(__ldcg(norms)) * __uint_as_float(__ldcg(norms + 1));   // squares of the bound's factors
+    const float n = dO2 * v2;
     if (!(n > 0.0f && n < INFINITY)) return 0.0f;
     const float room = kHasCap<MODE> ? 4.0f : 2.0f;                          // 15 - 12 - 1, and the cap's 2
     return fminf(fmaxf(floorf(room - 0.5f * log2f(n)), -100.0f), 100.0f);    // less log2(bound / 2)
+}
+
+// The largest of n values from `at` on that are not negative, by one warp.
+__device__ __forceinline__ float warp_max(const float* at, int n, int lane) {
+    float m = 0.0f;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(at + i));
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+}
+// max|V|^2 of a key/value head.
+__device__ __forceinline__ float v_norm(const MaskedBwdParams& p, int b, int hk, int lane) {
+    const int tiles = (p.mask.Skv + 63) / 64;
+    return warp_max(p.v_norms + ((long long)b * p.mask.Hkv + hk) * tiles, tiles, lane);
+}
+// max|dO_i|^2 over queries [first, end) of heads [h0, h1), this lane's share: rows up to a multiple of 64, tiles, rows.
+__device__ __forceinline__ float dO_norm(const MaskedBwdParams& p, int b, int h0, int h1, int first, int end, int lane) {
+    const int up = min((first + 63) / 64 * 64, end), down = max(end / 64 * 64, up);
+    const int rows = up - first, tiles = (down - up) / 64, per = rows + tiles + end - down;
+    float m = 0.0f;
+    for (int k = lane; k < per; k += 32) {
+        const bool tile = k >= rows && k < rows + tiles;
+        const int pitch = tile ? p.Sp / 64 : p.Sp;
+        const float* at = (tile ? p.tile_norms : p.row_norms) + ((long long)b * p.mask.Hq + h0) * pitch +
+                          (tile ? up / 64 + k - rows : (k < rows ? first + k : down + k - rows - tiles));
+#pragma unroll 8
+        for (int h = h0; h < h1; ++h, at += pitch) m = fmaxf(m, __ldcg(at));
+    }
+    return m;
+}
+// ds_shift of each lane's key, which queries [first, end) see, in steps of heads [h0, h1): the norm is the largest among
+// the queries that see one of the warp's keys of the lane's document.  Keys of a document have one end, and the
+// first of them the first query.
+template <class T, int MODE>
+__device__ __forceinline__ float key_shift(const MaskedBwdParams& p, int b, int hk, int h0, int h1, int first, int end, int lane) {
+    const int tiles = (p.mask.Skv + 63) / 64;
+    const float* v = p.v_norms + ((long long)b * p.mask.Hkv + hk) * tiles;
+    const float v_first = lane < tiles ? __ldcg(v + lane) : 0.0f;            // on its way meanwhile
+    float mine = 0.0f;
+    for (uint32_t left = 0xffffffffu; left;) {
+        const int lead = __ffs(left) - 1, f = __shfl_sync(0xffffffffu, first, lead), e = __shfl_sync(0xffffffffu, end, lead);
+        const uint32_t same = __ballot_sync(0xffffffffu, end == e) & left;
+        if (f < e) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(dO_norm(p, b, h0, h1, f, e, lane)));
+            if (same >> lane & 1u) mine = __uint_as_float(m);
+        }
+        left &= ~same;
+    }
+    float v2 = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v_first)));
+    if (tiles > 32) v2 = fmaxf(v2, warp_max(v + 32, tiles - 32, lane));
+    return ds_shift<T, MODE>(mine, v2);
 }
 
 // What a row's exponent offset holds beside -lse: P's power of two, and the constant of a capped
@@ -60,9 +110,9 @@ __device__ __forceinline__ float row_offset(const ScoreArgs& sc) {
 // Rows: exponent offsets, delta, and the norms that bound dS
 // ---------------------------------------------------------------------------
 // A warp takes kWarpRows rows of one head, 16 bytes a lane (D / 8 lanes a row), all loads before the
-// first sum; bound by the read of dO and O.  Rows padded to Sp first, then (fp16) the value rows.
-// Maxima are order-free, so the atomics are deterministic.
-constexpr int kWarpRows = 8;
+// first sum; bound by the read of dO and O.  Rows padded to Sp first, then (fp16) the value rows.  A CTA's warps
+// share one tile of 64 rows.
+constexpr int kWarpRows = 8, kNormRows = 8 * kWarpRows;
 
 // Row r's 8 elements of this lane; zero outside [0, rows).
 template <class T>
@@ -87,10 +137,18 @@ __device__ __forceinline__ float lanes_sum(float x) {
     for (int o = LANES / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
-__device__ __forceinline__ void max_norm(unsigned* to, float n, int lane) {
-    unsigned bits = n < INFINITY ? __float_as_uint(n) : 0u;      // infinite and NaN rows do not count
-    bits = __reduce_max_sync(0xffffffffu, bits);
-    if (lane == 0 && bits) atomicMax(to, bits);
+// Rows' norms count where they are finite.
+__device__ __forceinline__ float finite_norm(float n) { return n < INFINITY ? n : 0.0f; }
+// The largest norm of a CTA's rows.
+__device__ __forceinline__ void store_tile_norm(float* to, float n) {
+    __shared__ uint32_t most[8];
+    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(n));
+    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const uint32_t all = __reduce_max_sync(0xffffffffu, threadIdx.x < 8 ? most[threadIdx.x] : 0u);
+        if (threadIdx.x == 0) *to = __uint_as_float(all);
+    }
 }
 
 template <class T, int D>
@@ -98,7 +156,7 @@ __global__ void __launch_bounds__(256) gsr_masked_bwd_rows_kernel(const __grid_c
     constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, N = kWarpRows / AT_ONCE;
     const int lane = threadIdx.x & 31, sub = lane / LANES, piece = lane % LANES;
     const MaskArgs& mk = p.mask;
-    const int groups = p.Sp / kWarpRows, v_groups = (mk.Skv + kWarpRows - 1) / kWarpRows;
+    const int groups = p.Sp / kWarpRows, v_groups = (mk.Skv + kNormRows - 1) / kNormRows * 8;
     long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const long long q_groups = (long long)mk.B * mk.Hq * groups;
     if (id < q_groups) {
@@ -139,8 +197,9 @@ __global__ void __launch_bounds__(256) gsr_masked_bwd_rows_kernel(const __grid_c
             p.neg_delta[row] = keys || !(fabsf(delta) < INFINITY) ? -delta : 0.0f;
         }
         if (!Elem<T>::bf16) {
-            grid_wait();                                 // the norms are zero
-            max_norm(p.norms, keys ? norm : 0.0f, lane);
+            norm = keys ? finite_norm(norm) : 0.0f;
+            if (lane < kWarpRows) p.row_norms[(long long)bh * p.Sp + i] = norm;
+            store_tile_norm(p.tile_norms + id / 8, norm);
         }
         return;
     }
@@ -161,20 +220,10 @@ __global__ void __launch_bounds__(256) gsr_masked_bwd_rows_kernel(const __grid_c
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const float q = lanes_sum<LANES>(dot8<T>(x[n], x[n]));
-            if (q < INFINITY && (rows_seen >> (n * AT_ONCE + sub) & 1u)) most = fmaxf(most, q);
+            if (rows_seen >> (n * AT_ONCE + sub) & 1u) most = fmaxf(most, finite_norm(q));
         }
-        grid_wait();
-        max_norm(p.norms + 1, most, lane);
-    } else if (!Elem<T>::bf16) {
-        grid_wait();                                     // dK's and dV's launch waits for this one, and so for the zeros
+        store_tile_norm(p.v_norms + id / 8, most);
     }
-}
-
-// The norms' start (fp16).  The rows' launch does all but its maxima meanwhile; a memset in its place would
-// hold it up (2 x 6 heads over 3 of 333 rows, captured: 28.5 us with one, 25.0 with this).
-static __global__ void __launch_bounds__(32) gsr_masked_bwd_norms_kernel(unsigned* norms) {
-    grid_launch_next();
-    if (threadIdx.x < 2) norms[threadIdx.x] = 0u;
 }
 
 // Zero rows of a strided output (no queries, or no keys).  One warp per row.
@@ -687,7 +736,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int r = quad * 32 + lane;                  // key of the tile
         const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
         const uint32_t s_col = lane_base + Cfg::T_S + half * 64, dp_col = lane_base + Cfg::T_DP + half * 64;
-        const float shift = ds_shift<T, Cfg::MODE>(p.norms), ds_mul = exp2f(shift);
         uint32_t n_box = 0, n = 0, n_done = 0;
         bool ok = true;
         while (ok) {
@@ -701,6 +749,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int j = it.k0 + r;
             int first = 0, end = INT_MAX;                // the queries that see this thread's key (behind the last: no mask)
             if (j < mk.Skv) key_interval(mk, it.b, j, first, end);
+            float shift = 0.0f, ds_mul = 1.0f;
+            if (!Elem<T>::bf16 && it.begin < it.end) {
+                const int h0 = it.hk * mk.group, per = it.t1 - it.t0;
+                shift = key_shift<T, Cfg::MODE>(p, it.b, it.hk, h0 + it.begin / per, h0 + (it.end - 1) / per + 1, first,
+                                                j < mk.Skv ? end : 0, lane);
+                ds_mul = exp2f(shift);
+            }
             const int tiles = max(it.t1 - it.t0, 1);
             int h = it.hk * mk.group + it.begin / tiles, t = it.t0 + it.begin % tiles;
             for (int k = it.begin; k < it.end; ++k, ++n, ++t) {
@@ -1135,7 +1190,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int r = quad * 32 + lane;                  // query of the tile
         const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
         const uint32_t s_col = lane_base + Cfg::T_S + half * 64;
-        const float shift = ds_shift<T, Cfg::MODE>(p.norms);
         uint32_t n_box = 0, n = 0, n_done = 0;
         bool ok = true;
         while (ok) {
@@ -1150,6 +1204,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const long long row = ((long long)it.b * mk.Hq + it.h) * p.Sp + qi;
             int lo = 0, hi = INT_MAX;                    // rows behind the last: no mask
             if (qi < mk.Sq) row_interval(mk, it.b, qi, lo, hi);
+            const float shift = Elem<T>::bf16 ? 0.0f : ds_shift<T, Cfg::MODE>(__ldcg(p.row_norms + row), v_norm(p, it.b, it.h / mk.group, lane));
             const float off = __ldcg(p.offset + row) + shift, neg_delta = __ldcg(p.neg_delta + row);
             const float slope2 = kHasBias<Cfg::MODE> ? __ldg(p.score.slopes + it.h) * kLog2e : 0.0f;
             for (int t = it.t0; t < it.t1; ++t, ++n) {
@@ -1254,11 +1309,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
-// The norms' start (fp16), the rows, then dK and dV, then dQ, then the sums of parts.  The rows load while
-// the norms start.  dK's and dV's CTAs start while the rows' last ones finish, and wait for them (let in
-// while rows are still to come, they take SMs from them: 8192 tokens in 4 documents 395 us, so 408).  dQ's
-// CTAs need the rows alone (finished when dK's and dV's CTAs have come past their wait, which is when
-// dQ's may start) and fill the SMs that run out of dK and dV items.
+// The rows, then dK and dV, then dQ, then the sums of parts.  dK's and dV's CTAs start while the rows' last ones
+// finish, and wait for them (let in while rows are still to come, they take SMs from them: 8192 tokens in 4
+// documents 395 us, so 408).  dQ's CTAs need the rows alone (finished when dK's and dV's CTAs have come past
+// their wait, which is when dQ's may start) and fill the SMs that run out of dK and dV items.
 template <class T, int D, int MODE>
 cudaError_t launch_bwd_mode(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream) {
     using Dkv = DkvCfg<T, D, MODE>;
@@ -1296,17 +1350,10 @@ cudaError_t launch_bwd_type(const MaskedBwdMaps& tm, const MaskedBwdParams& p, c
             gsr_masked_zero_kernel<T, D><<<(unsigned)((q_rows + 7) / 8), 256, 0, stream>>>(p.dQ, mk.Hq, mk.Sq, q_rows);
         return cudaGetLastError();
     }
-    long long warps = (long long)mk.B * mk.Hq * (p.Sp / kWarpRows);
-    cudaError_t e;
-    if (Elem<T>::bf16) {
-        gsr_masked_bwd_rows_kernel<T, D><<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(p);
-        e = cudaGetLastError();
-    } else {
-        warps += (long long)mk.B * mk.Hkv * ((mk.Skv + kWarpRows - 1) / kWarpRows);
-        gsr_masked_bwd_norms_kernel<<<1, 32, 0, stream>>>(p.norms);
-        if ((e = cudaGetLastError()) == cudaSuccess)
-            e = launch_early(gsr_masked_bwd_rows_kernel<T, D>, (unsigned)((warps + 7) / 8), 256, 0, stream, p);
-    }
+    long long ctas = (long long)mk.B * mk.Hq * (p.Sp / kNormRows);
+    if (!Elem<T>::bf16) ctas += (long long)mk.B * mk.Hkv * ((mk.Skv + kNormRows - 1) / kNormRows);
+    gsr_masked_bwd_rows_kernel<T, D><<<(unsigned)ctas, 256, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     switch (score_mode(p.score)) {
         case kScorePlain: return launch_bwd_mode<T, D, kScorePlain>(tm, p, stream);

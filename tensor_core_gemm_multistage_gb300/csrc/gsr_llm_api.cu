@@ -283,15 +283,19 @@ int64_t bwd_splits(const gsr_attention_desc* d, bool unequal) {
 
 // Layout of the backward pass's workspace, 256-byte pieces.
 struct BwdLayout {
-    int64_t sp, splits, offset, delta, parts, total;
+    int64_t sp, splits, offset, delta, row_norms, tile_norms, v_norms, parts, total;
 };
 BwdLayout bwd_layout(const gsr_attention_desc* d, bool unequal) {
     auto piece = [](int64_t bytes) { return (bytes + 255) / 256 * 256; };
     BwdLayout w;
     w.sp = (d->seq_q + 127) / 128 * 128;
-    w.offset = 256;                                                     // the norms come first
-    w.delta = w.offset + piece(4 * d->batch * d->heads_q * w.sp);
-    w.parts = w.delta + piece(4 * d->batch * d->heads_q * w.sp);
+    const int64_t rows = 4 * d->batch * d->heads_q * w.sp;
+    w.offset = 0;
+    w.delta = w.offset + piece(rows);
+    w.row_norms = w.delta + piece(rows);
+    w.tile_norms = w.row_norms + piece(rows);
+    w.v_norms = w.tile_norms + piece(rows / 64);
+    w.parts = w.v_norms + piece(4 * d->batch * d->heads_kv * ((d->seq_kv + 63) / 64));
     w.splits = bwd_splits(d, unequal);
     w.total = w.parts + (w.splits > 1 ? piece(8 * w.splits * d->batch * d->heads_kv * d->seq_kv * d->head_dim) : 0);
     return w;
@@ -466,7 +470,9 @@ gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor
         if ((s = gsr::host::stream_scratch(dev, st, (size_t)w.total, &workspace)) != GSR_OK) return s;
     }
     char* base = static_cast<char*>(workspace);
-    p.norms = reinterpret_cast<unsigned*>(base);
+    p.row_norms = reinterpret_cast<float*>(base + w.row_norms);
+    p.tile_norms = reinterpret_cast<float*>(base + w.tile_norms);
+    p.v_norms = reinterpret_cast<float*>(base + w.v_norms);
     p.Sp = (int)w.sp;
     p.offset = reinterpret_cast<float*>(base + w.offset);
     p.neg_delta = reinterpret_cast<float*>(base + w.delta);

@@ -67,7 +67,9 @@ struct MaskedBwdParams {
     int Sp;                     // Sq rounded up to a multiple of 128
     float* offset;              // (B, Hq, Sp): row_offset less lse log2(e); -inf for rows without keys and padding
     float* neg_delta;           // (B, Hq, Sp): -rowsum(dO * O)
-    unsigned* norms;            // [0] max |dO_i|^2, [1] max |V_j|^2, as the bits of a float (fp16 only)
+    // fp16 only, squares of the rows that count and are finite, else 0: |dO_i|^2 (B, Hq, Sp), the largest of 64 of
+    // them (B, Hq, Sp / 64), the largest |V_j|^2 of 64 keys (B, Hkv, Skv / 64 rounded up)
+    float *row_norms, *tile_norms, *v_norms;
     int q_head_group, kv_head_group;   // item order of dQ, of dK and dV: heads taken together
     int splits;                 // parts of a key tile's steps
     float* parts;               // splits > 1: (2, splits, B, Hkv, Skv, D) partial dV and dK

@@ -760,3 +760,27 @@ def test_an_infinite_gradient_takes_no_longer(D, dtype):
         assert all(torch.equal(a, b) for a, b in zip(run(**kw), clean))
     finally:
         gsr.set_wait_timeout_ns(1_000_000_000)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_gradients_beside_large_ones(D, causal, dtype):
+    """Two documents and two groups of heads, with dO of sizes 2^16 apart: each document's results of each group are within
+    the bound that its own dO gives."""
+    edges = [0, 500, 1100]
+    c = Case(1, 4, 2, 1100, 1100, D, dtype=dtype, causal=causal, docs=[edges])
+    for heads, rows, size in ((slice(0, 2), slice(0, 500), 2.0 ** 10), (slice(2, 4), slice(0, 500), 2.0 ** -5),
+                              (slice(0, 2), slice(500, 1100), 2.0 ** -6), (slice(2, 4), slice(500, 1100), 2.0 ** 10)):
+        c.do[:, heads, rows] *= size
+    c.forward().backward()
+    want, terms, wide, plain = llm.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, c.see, **c.host)
+    norm = lambda t: np.sqrt((llm.f64(t) ** 2).sum(-1)).max()
+    for s, e in zip(edges, edges[1:]):
+        for kv in range(2):
+            heads = slice(2 * kv, 2 * kv + 2)
+            low = [c.tiny * 2 * norm(c.do[:, heads, s:e]) * norm(c.v[:, kv]) * 2.0 ** -14] * 2 + [c.tiny * 2.0 ** -12]
+            for name, t, w, a, b, p, x in zip(("dQ", "dK", "dV"), c.grads, want, terms, wide, plain, low):
+                got, w, a, b, p = (y[:, heads if name == "dQ" else slice(kv, kv + 1), s:e] for y in (llm.f64(t), w, a, b, p))
+                tol = c.tol(w, a, b) + x * p
+                assert np.all(np.abs(got - w) <= tol), (name, s, kv, (np.abs(got - w) / tol).max())
