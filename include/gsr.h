@@ -157,7 +157,10 @@ typedef enum gsr_dtype { GSR_F16 = 0, GSR_BF16 = 1 } gsr_dtype;
  * A batch x head x row x D operand: element strides, multiples of 8, D contiguous, data 16-byte
  * aligned.  Any order of the other three dimensions is fine (batch, row, head as a projection
  * leaves it; the parts of a fused projection's output).  A dimension of size 1 has no stride; a
- * stride of 0 (a broadcast) is refused with GSR_ERR_INVALID_ARG.
+ * stride of 0 (a broadcast) is refused with GSR_ERR_INVALID_ARG.  An output must share no element with
+ * an input or another output (GSR_ERR_ALIAS): views with the same strides are compared element by
+ * element, so the parts of one buffer may lie in any order; views whose strides differ must not meet
+ * from their first to their last byte.
  */
 typedef struct gsr_tensor {
     void* data;

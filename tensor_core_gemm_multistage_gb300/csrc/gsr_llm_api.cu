@@ -84,16 +84,46 @@ bool meets_masks(const Span& s, const gsr_attention_desc* d) {
            meet(s, words(d->prefix_lens, d->batch * (d->num_docs > 0 ? d->num_docs : 1)));
 }
 
-// Whether two 16-bit operands may share elements.  Views of one buffer that lie side by side in
-// each row of it (the parts of a fused projection: equal row strides, heads inside the row) do not.
-bool share(const Strided& a, int64_t a_heads, int64_t a_rows, const Strided& b, int64_t b_heads, int64_t b_rows,
-           int64_t batch, int64_t d) {
-    if (!meet(span_of(a, batch, a_heads, a_rows, d, 2), span_of(b, batch, b_heads, b_rows, d, 2))) return false;
-    const int64_t a_wide = (a_heads - 1) * a.head + d, b_wide = (b_heads - 1) * b.head + d, pitch = a.row;
-    if (a_rows < 2 || b_rows < 2 || a.row != b.row || (batch > 1 && (a.batch != b.batch || a.batch % pitch))) return true;
-    const int64_t apart = (int64_t)(reinterpret_cast<uintptr_t>(a.data) - reinterpret_cast<uintptr_t>(b.data)) / 2;
-    const int64_t at = ((apart % pitch) + pitch) % pitch;      // a's columns, in b's rows
-    return !(at >= b_wide && at + a_wide <= pitch);
+// Whether elements of rows of two operands coincide.  A row of one starts `apart` + sum z_k stride_k elements behind a row
+// of the other, with z_k from -low_k to high_k; strides descend.  Where dimensions lie apart, as an output's do, a sum
+// of the smaller strides is too short for more than two or three values of z_k.
+struct Steps {
+    int64_t stride, low, high;
+};
+bool rows_meet(const Steps* s, int n, int64_t apart, int64_t d) {
+    if (n == 0) return apart > -d && apart < d;
+    int64_t down = d - 1, up = d - 1;                      // how far the smaller strides and a row's elements reach
+    for (int k = 1; k < n; ++k) {
+        down += s[k].low * s[k].stride;
+        up += s[k].high * s[k].stride;
+    }
+    auto floor_div = [](int64_t a, int64_t b) { return a / b - (a % b < 0 ? 1 : 0); };
+    // apart + z stride + (-down .. up) holds 0
+    const int64_t first = std::max(-s->low, -floor_div(apart + up, s->stride)),
+                  last = std::min(s->high, floor_div(down - apart, s->stride));
+    if (last - first > 8) return true;                     // dimensions that run into each other
+    for (int64_t z = first; z <= last; ++z)
+        if (rows_meet(s + 1, n - 1, apart + z * s->stride, d)) return true;
+    return false;
+}
+
+// Whether two 16-bit operands may share elements: where their bytes meet and their strides differ, they may; where the
+// strides are the same (views of one buffer, in any order of its dimensions), they do if two rows meet.
+bool share(const Strided& a, int64_t a_batch, int64_t a_heads, int64_t a_rows, const Strided& b, int64_t b_batch, int64_t b_heads,
+           int64_t b_rows, int64_t d) {
+    if (!meet(span_of(a, a_batch, a_heads, a_rows, d, 2), span_of(b, b_batch, b_heads, b_rows, d, 2))) return false;
+    const int64_t na[3] = {a_batch, a_heads, a_rows}, nb[3] = {b_batch, b_heads, b_rows};
+    const int64_t sa[3] = {a.batch, a.head, a.row}, sb[3] = {b.batch, b.head, b.row};
+    Steps s[3];
+    int n = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (na[i] == 1 && nb[i] == 1) continue;            // a dimension of one element has no stride
+        if (na[i] > 1 && nb[i] > 1 && sa[i] != sb[i]) return true;
+        s[n++] = Steps{na[i] > 1 ? sa[i] : sb[i], nb[i] - 1, na[i] - 1};
+    }
+    std::sort(s, s + n, [](const Steps& x, const Steps& y) { return x.stride > y.stride; });
+    const intptr_t bytes = static_cast<const char*>(a.data) - static_cast<const char*>(b.data);    // both multiples of 16
+    return rows_meet(s, n, bytes / 2, d);
 }
 
 // A capped score is off by about cap 2^-23, so caps end at 1024; one so small that scale / cap
@@ -379,8 +409,8 @@ gsr_status masked_attention_fwd(const gsr_attention_desc* desc, const gsr_tensor
     if (meet(ws, o) || meet(ws, l) || meets_masks(ws, desc) || meet(ws, span_of(p.Q, B, Hq, Sq, D, 2)) ||
         meet(ws, span_of(p.K, B, Hkv, Skv, D, 2)) || meet(ws, span_of(p.V, B, Hkv, Skv, D, 2)))
         return GSR_ERR_ALIAS;
-    if (share(p.O, Hq, Sq, p.Q, Hq, Sq, B, D) || share(p.O, Hq, Sq, p.K, Hkv, Skv, B, D) ||
-        share(p.O, Hq, Sq, p.V, Hkv, Skv, B, D) || meets_masks(o, desc))
+    if (share(p.O, B, Hq, Sq, p.Q, B, Hq, Sq, D) || share(p.O, B, Hq, Sq, p.K, B, Hkv, Skv, D) ||
+        share(p.O, B, Hq, Sq, p.V, B, Hkv, Skv, D) || meets_masks(o, desc))
         return GSR_ERR_ALIAS;
     if (lse && (meet(l, span_of(p.Q, B, Hq, Sq, D, 2)) || meet(l, span_of(p.K, B, Hkv, Skv, D, 2)) ||
                 meet(l, span_of(p.V, B, Hkv, Skv, D, 2)) || meet(l, o) || meets_masks(l, desc)))
@@ -454,7 +484,7 @@ gsr_status masked_attention_bwd(const gsr_attention_desc* desc, const gsr_tensor
         if (meets_masks(sa, desc)) return GSR_ERR_ALIAS;
         for (size_t j = 0; j < i; ++j) {
             const auto& b = all[j];
-            if (share(*a.to, ah, ar, *b.to, b.q ? Hq : Hkv, b.q ? Sq : Skv, B, D)) return GSR_ERR_ALIAS;
+            if (share(*a.to, B, ah, ar, *b.to, B, b.q ? Hq : Hkv, b.q ? Sq : Skv, D)) return GSR_ERR_ALIAS;
         }
     }
     int dev = 0, sms = 0;
@@ -520,7 +550,7 @@ gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gs
     if (!cache_axes(p.K, d.num_pages, d.heads_kv, &p.k_axes) || !cache_axes(p.V, d.num_pages, d.heads_kv, &p.v_axes))
         return GSR_ERR_INVALID_ARG;
     const Span o = span_of(os, 1, d.heads_q, d.total_q, d.head_dim, 2);
-    if (share(os, d.heads_q, d.total_q, qs, d.heads_q, d.total_q, 1, d.head_dim) ||
+    if (share(os, 1, d.heads_q, d.total_q, qs, 1, d.heads_q, d.total_q, d.head_dim) ||
         meet(o, span_of(p.K, d.num_pages, d.heads_kv, d.page_size, d.head_dim, 2)) ||
         meet(o, span_of(p.V, d.num_pages, d.heads_kv, d.page_size, d.head_dim, 2)))
         return GSR_ERR_ALIAS;

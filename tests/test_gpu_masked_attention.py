@@ -784,3 +784,28 @@ def test_small_gradients_beside_large_ones(D, causal, dtype):
                 got, w, a, b, p = (y[:, heads if name == "dQ" else slice(kv, kv + 1), s:e] for y in (llm.f64(t), w, a, b, p))
                 tol = c.tol(w, a, b) + x * p
                 assert np.all(np.abs(got - w) <= tol), (name, s, kv, (np.abs(got - w) / tol).max())
+
+
+@pytest.mark.parametrize("S", [1, 150])
+@pytest.mark.parametrize("order", ["bhsd", "sbhd"])
+def test_parts_of_one_buffer(order, S):
+    # Q, K, V and O as head ranges of one buffer, their gradients as those of another
+    B, Hq, Hkv, D = 3, 4, 2, 64
+    g = torch.Generator().manual_seed(9)
+    ranges = [Hq, Hkv, Hkv, Hq]
+
+    def parts():
+        H = sum(ranges)
+        x = torch.randn(*((B, H, S, D) if order == "bhsd" else (S, B, H, D)), generator=g).to(F16).to(DEV)
+        if order == "sbhd":
+            x = x.permute(1, 2, 0, 3)
+        return x.split(ranges, 1)
+
+    c = Case(B, Hq, Hkv, S, S, D, causal=True)
+    c.q, c.k, c.v, c.o = parts()
+    c.lse = torch.empty(B, Hq, S, device=DEV)
+    *c.grads, c.do = parts()
+    gsr.masked_attention_fwd(c.q, c.k, c.v, c.o, c.lse, **c.kw)
+    c.check_forward()
+    gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *c.grads, **c.kw)
+    c.check_backward()

@@ -85,6 +85,84 @@ def test_attention_aliases():
     assert fwd(Q=part(20 * GB, 0), K=part(20 * GB, 4), V=part(20 * GB, 6), O=part(20 * GB, 2)) == ALIAS
 
 
+def views(order, parts, B, S, D, base=20 * GB):
+    """Tensors of one buffer whose dimensions lie in `order` ("b", "s", "h": the heads of all parts, or "p": the parts of
+    "h" heads each); `parts` gives each part's heads."""
+    size = {"b": B, "s": S, "h": max(parts) if "p" in order else sum(parts), "p": len(parts)}
+    stride, at = {}, D
+    for x in reversed(order):
+        stride[x], at = at, at * size[x]
+    step = lambda i: i * stride["p"] if "p" in order else sum(parts[:i]) * stride["h"]
+    return [_Tensor(base + 2 * step(i), stride["b"], stride["h"], stride["s"]) for i in range(len(parts))]
+
+
+LAYOUTS = ["bsh", "bhs", "sbh", "shb", "hbs", "hsb", "bsph", "bpsh", "bphs", "bhps", "pbhs", "sbph", "sphb", "hpsb", "bshp"]
+
+
+def shared_elements(a, b, na, nb, D):
+    """The definition: the elements of both, as offsets of 16-byte pieces."""
+    import numpy as np
+    def pieces(t, n):
+        steps = [np.arange(k) * s for k, s in zip(n, (t.stride_batch, t.stride_head, t.stride_row))]
+        return (t.data // 2 + steps[0][:, None, None, None] + steps[1][:, None, None] + steps[2][:, None] + np.arange(0, D, 8)).ravel()
+    return np.intersect1d(pieces(a, na), pieces(b, nb)).size > 0
+
+
+@pytest.fixture
+def accepted():
+    """Whether a call passes its checks: without a GPU it then fails at its first CUDA call.  With one it would go on and
+    use the addresses, which are fake."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("fake device addresses that pass the checks: only without a GPU")
+    return lambda status: status not in (INVALID, ALIGN, ALIAS)
+
+
+@pytest.mark.parametrize("sizes", [(2, 100), (1, 100), (3, 1), (1, 1), (2, 7)])
+@pytest.mark.parametrize("order", LAYOUTS)
+def test_parts_of_one_buffer_in_any_order(order, sizes, accepted):
+    """Gradients, and O beside Q, as views of one buffer: refused only where elements are shared."""
+    B, S = sizes
+    d = dict(batch=B, seq_q=S, seq_kv=S)
+    parts = [4, 2, 2] if "p" not in order else [4, 4, 4]
+    if "p" in order:
+        d["heads_kv"] = 4
+    kv = parts[1]
+    outs = dict(zip(("dQ", "dK", "dV"), views(order, parts, B, S, 64)))
+    ins = {n: dense((i + 1) * GB, B, 4 if n in ("dO", "Q", "O") else kv, S, 64) for i, n in enumerate(("dO", "Q", "K", "V", "O"))}
+    assert accepted(bwd(d, **ins, **outs))
+    q, o = views(order, [4, 4], B, S, 64)
+    fine = dict(K=dense(2 * GB, B, kv, S, 64), V=dense(3 * GB, B, kv, S, 64))
+    assert accepted(fwd(d, Q=q, O=o, **fine))
+    # O moved towards Q by a piece, by a row of D, by half a part: as the definition has it
+    n = (B, 4, S)
+    for back in (16, 128, 2 * 64 * 2, (o.data - q.data) // 2 // 16 * 16):
+        moved = _Tensor(o.data - back, o.stride_batch, o.stride_head, o.stride_row)
+        assert accepted(fwd(d, Q=q, O=moved, **fine)) == (not shared_elements(q, moved, n, n, 64)), back
+
+
+def test_random_views_share_as_the_definition_has_it(accepted):
+    import random
+    r = random.Random(5)
+    seen = set()
+    for _ in range(400):
+        B, Hq, Hkv, S, Skv = r.randint(1, 3), r.choice([1, 2, 4]), r.choice([1, 2]), r.randint(1, 5), r.randint(1, 5)
+        Hq = max(Hq, Hkv)
+        order = r.sample([0, 1, 2], 3)                             # strides that grow in this order, with gaps
+        stride, at = [0, 0, 0], 64
+        for k in order:
+            stride[k] = at + 64 * r.choice([0, 0, 1, 5])
+            at = stride[k] * (max((B, Hq, max(S, Skv))[k], 1) + r.choice([0, 1]))
+        t = lambda x: _Tensor(20 * GB + 128 * r.randrange(at // 64 + 2) + 16 * r.choice([0, 0, 0, 1]), *stride) if x else None
+        o, k = t(1), t(1)
+        d = dict(batch=B, heads_q=Hq, heads_kv=Hkv, seq_q=S, seq_kv=Skv, causal=0)
+        got = accepted(fwd(d, Q=dense(1 * GB, B, Hq, S, 64), K=k, V=dense(3 * GB, B, Hkv, Skv, 64), O=o))
+        want = not shared_elements(o, k, (B, Hq, S), (B, Hkv, Skv), 64)
+        assert got == want, (d, stride, o.data, k.data)
+        seen.add(want)
+    assert len(seen) == 2
+
+
 def test_empty_attention_is_a_no_op():
     assert fwd(dict(batch=0)) == OK and fwd(dict(seq_q=0)) == OK
     assert bwd(dict(batch=0)) == OK
