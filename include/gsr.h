@@ -313,8 +313,8 @@ gsr_status kv_block_tables(const int32_t* kv_lens, const int32_t* new_lens, cons
  * of page slots[n] / page_size.  Slots outside the cache (-1: padding) are skipped; other cache
  * rows are left as they were.  K, V: tokens x heads x head_dim (stride_row steps from token to
  * token; stride_batch unused) of any 16-bit type, head_dim a multiple of 8.  Where two tokens have
- * the same slot, the row holds pieces of either.  k_cache and v_cache may be the two halves of one
- * buffer.
+ * the same slot, the row holds pieces of either.  k_cache and v_cache may be views of one buffer
+ * that share no element, as outputs of gsr_tensor's description (else GSR_ERR_ALIAS).
  */
 gsr_status kv_cache_append(const gsr_tensor* K, const gsr_tensor* V, const int32_t* slots,
                            const gsr_tensor* k_cache, const gsr_tensor* v_cache, int64_t tokens,

@@ -690,7 +690,7 @@ gsr_status kv_cache_append(const gsr_tensor* K, const gsr_tensor* V, const int32
                            words(slots, tokens)};
     for (const Span& o : others)
         if (meet(kc, o) || meet(vc, o)) return GSR_ERR_ALIAS;
-    if (num_pages > 0 && p.Kc.data == p.Vc.data) return GSR_ERR_ALIAS;
+    if (num_pages > 0 && share(p.Kc, num_pages, heads, page_size, p.Vc, num_pages, heads, page_size, head_dim)) return GSR_ERR_ALIAS;
     int dev = 0, sms = 0;
     if ((s = gsr::host::current_device(&dev, &sms)) != GSR_OK) return s;
     p.N = (int)tokens;

@@ -230,6 +230,26 @@ def test_append_refusals():
     assert append(tokens=0) == OK
 
 
+@pytest.mark.parametrize("pages,page", [(10, 16), (1, 16), (5, 1)])
+def test_caches_that_share_rows(pages, page, accepted):
+    """k_cache and v_cache in one buffer: halves of it in any order are fine, a shift within it is not."""
+    H, D = 2, 64
+    cache = lambda at, *strides: _Tensor(40 * GB + 2 * at, *strides)       # page, head, row
+    strides = (page * H * D, D, H * D)
+    for by in (8, D, H * D, page * H * D, 3 * page * H * D + D):
+        inside = by < pages * page * H * D
+        got = append(pages=pages, page=page, kc=cache(0, *strides), vc=cache(by, *strides))
+        assert (got == ALIAS) == inside, by
+        got = append(pages=pages, page=page, kc=cache(by, *strides), vc=cache(0, *strides))
+        assert (got == ALIAS) == inside, by
+    for halves in (((2 * page * H * D, D, H * D), page * H * D),            # (pages, 2, rows, heads, D)
+                   ((2 * page * H * D, D, 2 * H * D), H * D),               # (pages, rows, 2, heads, D)
+                   ((2 * page * H * D, 2 * D, 2 * H * D), D),               # (pages, rows, heads, 2, D)
+                   ((2 * page * H * D, page * D, D), page * H * D),         # (pages, 2, heads, rows, D)
+                   ((page * H * D, D, H * D), pages * page * H * D)):       # (2, pages, rows, heads, D)
+        assert accepted(append(pages=pages, page=page, kc=cache(0, *halves[0]), vc=cache(halves[1], *halves[0])))
+
+
 def test_outputs_that_overlap_themselves():
     assert fwd(O=_Tensor(4 * GB, 25600, 64, 64)) == INVALID            # heads on rows
     assert fwd(O=_Tensor(4 * GB, 25600, 64, 128)) == INVALID           # four heads in rows of two
