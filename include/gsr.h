@@ -85,7 +85,10 @@ typedef enum gsr_status {
  * replay reads whatever the captured buffers hold then.  A captured call keeps
  * using the capture stream's library memory (error word, attention work
  * counters, small-M workspace): replays must not run at the same time as each
- * other or as other library calls on that stream.
+ * other or as other library calls on that stream.  The per-thread default stream
+ * (cudaStreamPerThread) is a stream of each calling thread's, with library memory of
+ * its own; a thread that ends calls gsr_release_stream for it first, or its memory
+ * stays until gsr_shutdown().
  */
 gsr_status gemm_scale_relu(const void* A, const void* B, void* C, int64_t M, int64_t N,
                            int64_t K, float alpha, struct CUstream_st* stream);

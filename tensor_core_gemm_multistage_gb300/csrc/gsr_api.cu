@@ -61,7 +61,10 @@ struct DeviceInfo {
 
 std::mutex g_mu;
 std::map<int, DeviceInfo> g_devices;
-std::map<std::pair<int, CUstream_st*>, StreamState> g_streams;
+// Device, and a stream's handle or, for the one handle that names a stream of each thread, that stream's id with the
+// top bit set (a handle is an address or a small number).
+using StreamKey = std::pair<int, uint64_t>;
+std::map<StreamKey, StreamState> g_streams;
 
 // Copy streams and events of the pipelined host entry point, one set per device (created on
 // first use, released by gsr_shutdown).  `m` keeps one call's enqueue sequence together.
@@ -83,6 +86,18 @@ cudaError_t g_encode_err = cudaSuccess;
 gsr_status cuda_fail(cudaError_t e) {
     t_last_cuda_error = static_cast<int>(e);
     return GSR_ERR_CUDA;
+}
+
+gsr_status stream_key(int dev, cudaStream_t stream, StreamKey* key) {
+    uint64_t id = reinterpret_cast<uintptr_t>(stream);
+    if (stream == cudaStreamPerThread) {
+        unsigned long long of_thread = 0;
+        const cudaError_t e = cudaStreamGetId(stream, &of_thread);
+        if (e != cudaSuccess) return cuda_fail(e);
+        id = of_thread | 1ull << 63;
+    }
+    *key = {dev, id};
+    return GSR_OK;
 }
 
 gsr_status load_encoder() {
@@ -220,8 +235,11 @@ gsr_status device_info(int* dev_out, DeviceInfo* info) {
 // Returns a copy of the state (pointers stay valid until gsr_shutdown or regrowth).
 gsr_status stream_state(int dev, cudaStream_t stream, size_t need_partials, size_t need_tickets,
                         StreamState* out) {
+    StreamKey key;
+    const gsr_status found = stream_key(dev, stream, &key);
+    if (found != GSR_OK) return found;
     std::lock_guard<std::mutex> lock(g_mu);
-    StreamState& s = g_streams[{dev, stream}];
+    StreamState& s = g_streams[key];
     cudaError_t e;
     if (!s.err) {
         if ((e = cudaMalloc(&s.err, kStreamWords * sizeof(int))) != cudaSuccess) {
@@ -685,8 +703,11 @@ gsr_status error_word(int dev, cudaStream_t stream, int** err) {
 }
 
 gsr_status stream_scratch(int dev, cudaStream_t stream, size_t bytes, void** scratch) {
+    StreamKey key;
+    const gsr_status found = stream_key(dev, stream, &key);
+    if (found != GSR_OK) return found;
     std::lock_guard<std::mutex> lock(g_mu);
-    StreamState& s = g_streams[{dev, stream}];
+    StreamState& s = g_streams[key];
     cudaError_t e;
     // A graph would keep the buffer's address, which a later, larger call frees.
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
@@ -980,11 +1001,14 @@ gsr_status gsr_device_status(CUstream_st* stream, int* code) {
     // the allocation-free entry point's error word (one per device; its calls run in order)
     int h_fixed = 0;
     if ((e = gsr::noalloc_take_error(st, &h_fixed)) != cudaSuccess) return cuda_fail(e);
+    StreamKey key;
+    const gsr_status found = stream_key(dev, st, &key);
+    if (found != GSR_OK) return found;
     StreamState s;
     bool have = false;
     {
         std::lock_guard<std::mutex> lock(g_mu);
-        auto it = g_streams.find({dev, stream});
+        auto it = g_streams.find(key);
         if (it != g_streams.end() && it->second.err) {
             s = it->second;
             have = true;
@@ -1011,10 +1035,13 @@ gsr_status gsr_release_stream(CUstream_st* stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
+    StreamKey key;
+    const gsr_status found = stream_key(dev, st, &key);
+    if (found != GSR_OK) return found;
     StreamState s;
     {
         std::lock_guard<std::mutex> lock(g_mu);
-        auto it = g_streams.find({dev, stream});
+        auto it = g_streams.find(key);
         if (it == g_streams.end()) return GSR_OK;
         s = it->second;
         g_streams.erase(it);

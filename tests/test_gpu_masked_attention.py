@@ -434,6 +434,39 @@ def test_threads_on_one_stream():
     assert len(wrong) == 120 and not any(wrong), wrong
 
 
+def test_threads_on_the_per_thread_stream():
+    """One handle, a stream of each thread's: calls that run at the same time have workspaces of their own."""
+    import threading
+    per_thread = 2                        # cudaStreamPerThread
+    cases = [Case(1, 8, 2, 600, 600, 64, causal=True, seed=5), Case(1, 4, 4, 633, 633, 128, seed=6, dtype=BF16)]
+    for c in cases:
+        c.forward().backward()
+    want = [[t.clone() for t in c.grads] for c in cases]
+    outs = [[[torch.full_like(t, float("nan")) for t in c.grads] for _ in range(40)] for c in cases]
+    torch.cuda.synchronize()
+    status, together = [], threading.Barrier(2)
+
+    def loop(c, grads):
+        try:
+            together.wait()
+            for g in grads:
+                gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *g, stream=per_thread, **c.kw)
+            status.append(gsr.device_status(per_thread)[0])
+            gsr.release_stream(per_thread)
+        except Exception as e:
+            status.append(e)
+
+    threads = [threading.Thread(target=loop, args=a) for a in zip(cases, outs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert status == [gsr.Status.OK] * 2, status
+    for w, grads in zip(want, outs):
+        for g in grads:
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
 def test_offsets_past_32_bits():
     """A batch row 2^31 elements behind the first, all operands the parts of one buffer: the results of
     dense copies."""
