@@ -108,18 +108,27 @@ def _vector(t, name, count, dtype, index):
 
 def _scratch(workspace, nbytes, index, stream):
     """A tensor to keep until the call returns, its address and its size: the caller's workspace; None
-    (the library's own for the stream); or, in a capture, a new one from the graph's memory."""
+    (the library's own for the stream); or, where the stream is being captured, a new one from the
+    graph's memory."""
     if workspace is not None:
         if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on cuda:%d" % index)
         return workspace, workspace.data_ptr() or None, workspace.numel() * workspace.element_size()
-    if not torch.cuda.is_current_stream_capturing():
+    handle = _handle(stream, index)
+    if handle is None:                                  # the legacy default stream cannot be captured
         return None, None, 0
-    nbytes = max(nbytes(), 16)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
-    if stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(stream, device=ws.device) if isinstance(stream, int) else stream)
-    return ws, ws.data_ptr(), nbytes
+    if torch.cuda.current_device() == index and (stream is None or handle == _handle(None, index)):
+        if not torch.cuda.is_current_stream_capturing():
+            return None, None, 0
+        return _workspace(nbytes, index)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=torch.device("cuda", index))):
+        return _workspace(nbytes, index) if torch.cuda.is_current_stream_capturing() else (None, None, 0)
+
+
+def _workspace(nbytes, index):
+    n = max(nbytes(), 16)
+    ws = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index))
+    return ws, ws.data_ptr(), n
 
 
 def _attention_desc(Q, K, softmax_scale, causal, softcap, alibi_slopes, doc_bounds, prefix_lens):

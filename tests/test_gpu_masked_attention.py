@@ -408,6 +408,30 @@ def test_a_capture_needs_a_workspace_of_its_own():
     assert all(torch.equal(a, b) for a, b in zip(c.grads, want))
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_captured_stream_that_is_not_the_current_one(handle):
+    # the workspace comes from the graph's memory where the given stream is captured
+    c = Case(1, 4, 2, 300, 300, 64, causal=True).forward().backward()
+    want = [t.clone() for t in c.grads]
+    side, other = torch.cuda.Stream(DEV), torch.cuda.Stream(DEV)
+    given = side.cuda_stream if handle else side
+    torch.cuda.synchronize()
+    gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *c.grads, stream=given, **c.kw)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        with torch.cuda.stream(other):
+            gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *c.grads, stream=given, **c.kw)
+    big = Case(2, 8, 2, 900, 900, 128).forward()              # the library's workspace of the stream grows meanwhile
+    gsr.masked_attention_bwd(big.do, big.q, big.k, big.v, big.o, big.lse, *(torch.empty_like(t) for t in (big.q, big.k, big.v)), stream=given)
+    for _ in range(2):
+        for t in c.grads:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(c.grads, want))
+
+
 def test_threads_on_one_stream():
     """Two threads' backward calls on one stream share its workspace: each call's launches stay together."""
     import threading
