@@ -142,7 +142,7 @@ gsr_status check_desc(const gsr_attention_desc* d) {
     if (d->heads_q > 0 && (d->heads_kv == 0 || d->heads_q % d->heads_kv)) return GSR_ERR_INVALID_ARG;
     if (bad_score(d->softmax_scale, d->softcap)) return GSR_ERR_INVALID_ARG;
     if (d->seq_q + d->seq_kv > INT_MAX - 512) return GSR_ERR_INVALID_ARG;      // positions are counted in int
-    if ((d->num_docs > 0) != (d->doc_bounds != nullptr)) return GSR_ERR_INVALID_ARG;
+    if (d->num_docs == 0 ? d->doc_bounds != nullptr : d->batch > 0 && !d->doc_bounds) return GSR_ERR_INVALID_ARG;
     if (d->num_docs > 0 && d->seq_q != d->seq_kv) return GSR_ERR_INVALID_ARG;   // documents mask a row with itself
     if (d->prefix_lens && !d->causal) return GSR_ERR_INVALID_ARG;               // nothing for a prefix to add
     if (misaligned(d->alibi_slopes, 4) || misaligned(d->doc_bounds, 4) || misaligned(d->prefix_lens, 4))

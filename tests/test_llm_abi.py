@@ -314,3 +314,12 @@ def test_binding_refusals():
         gsr.kv_cache_append(t[0], t[0], t, t, t)
     with pytest.raises(ValueError):
         gsr.kv_block_tables(*[torch.zeros(1, dtype=torch.int32)] * 4, t, 16, *[t] * 6)
+
+
+def test_a_batch_of_none_with_documents():
+    # the arrays of masks have no elements, and so no address
+    none = dict(batch=0, num_docs=3, prefix_lens=None)
+    assert fwd(none) == OK and bwd(none) == OK
+    assert fwd(dict(none, doc_bounds=16 * GB)) == OK
+    assert fwd(dict(batch=0, doc_bounds=16 * GB)) == INVALID
+    assert llm.masked_attention_bwd_workspace(0, 4, 2, 100, 100, 64) >= 0
