@@ -15,7 +15,7 @@ namespace {
 //
 // The arrays are small (a few KB to a few hundred KB), so the call is bound by the latency of one
 // launch.  One launch is enough because nothing is exchanged between CTAs: each sums all requests
-// for itself into shared memory (8192 of them: 8 per thread), then maps its own share of tokens
+// for itself into shared memory (8192 of them: 16 per thread), then maps its own share of tokens
 // and pages to requests by binary search.  For the same reason lengths and the free list's head
 // are written to buffers of their own: another CTA may still read the old ones.
 constexpr int kTablesThreads = 512;
