@@ -130,6 +130,7 @@ __device__ __forceinline__ float2* part_ml(const TreeParams& p, long long slot, 
 // A warp's quarter of a V tile without what is not finite; true if there was something.
 template <class T, int D>
 __device__ __noinline__ bool clean_quarter(uint8_t* at, int lane) {
+    __syncwarp();                                        // its lanes may have zeroed rows without a token
     if (!pieces_not_finite<T>(at, 4 * D, lane)) return false;
     zero_not_finite<T>(at, 4 * D, lane);
     fence_proxy_async_smem();
