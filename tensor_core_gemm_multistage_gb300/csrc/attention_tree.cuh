@@ -127,14 +127,18 @@ __device__ __forceinline__ float2* part_ml(const TreeParams& p, long long slot, 
     return p.parts_ml + slot * p.part_rows + row;
 }
 
-// A warp's quarter of a V tile without what is not finite; true if there was something.
+// A warp's quarter of a V tile without what is not finite; where there is something, *flag = n first.  With two query
+// tiles each softmax group does it before its own product: one that finds the other's zeros finds its flag too.
 template <class T, int D>
-__device__ __noinline__ bool clean_quarter(uint8_t* at, int lane) {
+__device__ __noinline__ void clean_quarter(uint8_t* at, volatile uint32_t* flag, uint32_t n, int lane) {
     __syncwarp();                                        // its lanes may have zeroed rows without a token
-    if (!pieces_not_finite<T>(at, 4 * D, lane)) return false;
-    zero_not_finite<T>(at, 4 * D, lane);
-    fence_proxy_async_smem();
-    return true;
+    if (pieces_not_finite<T>(at, 4 * D, lane)) {
+        *flag = n;
+        __threadfence_block();
+        __syncwarp();
+        zero_not_finite<T>(at, 4 * D, lane);
+    }
+    fence_proxy_async_smem();                            // the other group's zeros, too, come before this one's product
 }
 
 // A warp's rows of an item are written (from column block c0 of 32 on, up to c1), and tiles with nodes were cleaned: what
@@ -680,9 +684,9 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                     fence_proxy_async_smem();
                 }
                 // a tile with nodes, of a request that has several
-                if (it.kv - it.ctx > 1 && k0 + p.tile_keys > it.ctx &&
-                    clean_quarter<T, D>(smem + Cfg::OFF_RING + (e % NB) * Cfg::TILE_BYTES + quad * (Cfg::TILE_BYTES / 4), lane))
-                    cleaned[n_item & 3u] = n_item;
+                if (it.kv - it.ctx > 1 && k0 + p.tile_keys > it.ctx)
+                    clean_quarter<T, D>(smem + Cfg::OFF_RING + (e % NB) * Cfg::TILE_BYTES + quad * (Cfg::TILE_BYTES / 4),
+                                        cleaned + (n_item & 3u), n_item, lane);
                 tmem_st_wait();
                 tcgen05_fence_before();
                 mbar_arrive(pfull(q));

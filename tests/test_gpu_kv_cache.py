@@ -397,6 +397,22 @@ def test_infinite_and_nan_values_reach_the_nodes_that_see_them(name, what):
     check_natural(t)
 
 
+@pytest.mark.parametrize("Hq,Hkv,T", [(16, 2, 40), (21, 3, 26), (4, 2, 9)])
+def test_infinite_values_among_the_nodes_give_the_same_every_time(Hq, Hkv, T):
+    # two query tiles a request, each with its softmax group, and one: whoever cleans a tile first, all rows know
+    t = Tree(kv=[90 + 7 * i % 60 for i in range(100)], T=[T] * 100, Hq=Hq, Hkv=Hkv, D=64, page=40)
+    for b in range(100):
+        j = t.kv[b] - 1 - b % T
+        t.vc[int(t.table[b][j // 40]), j % 40, :, b % 64] = float("inf" if b % 2 else "nan")
+    want = t.run().o.clone()
+    check_natural(t)
+    for _ in range(50):
+        for _ in range(6):
+            t.o.fill_(7.0)
+            gsr.tree_attention_fwd(*t.args, **t.kw)
+        assert gsr.device_status()[0] == gsr.Status.OK and torch.equal(t.o.nan_to_num(5.0), want.nan_to_num(5.0))
+
+
 @pytest.mark.parametrize("T", [1, 40])
 def test_an_infinite_value_takes_no_longer(T):
     # long contexts: no wait of 0.02 s runs out, and all other columns keep their bits
