@@ -454,19 +454,17 @@ __global__ void __launch_bounds__(256) gsr_masked_dkv_sum_kernel(const __grid_co
         for (int k = 0; k < kSumRows; ++k)
 #pragma unroll
             for (int s = 0; s < kSumParts; ++s) {
-                const long long id = first + k;
-                x[k][s] = V{};
-                if (s0 + s < p.splits && id < 2 * rows) {    // dV's parts lie before dK's
-                    const long long part = (id < rows ? 0 : p.splits) + s0 + s, row = id < rows ? id : id - rows;
-                    x[k][s] = *(reinterpret_cast<const V*>(p.parts + (part * rows + row) * D) + lane);
-                }
+                // dV's parts lie before dK's; behind the last part or row a load of it, so that none is conditional
+                const long long id = min(first + k, 2 * rows - 1), row = id < rows ? id : id - rows;
+                const long long part = (id < rows ? 0 : p.splits) + min(s0 + s, p.splits - 1);
+                x[k][s] = *(reinterpret_cast<const V*>(p.parts + (part * rows + row) * D) + lane);
             }
 #pragma unroll
         for (int k = 0; k < kSumRows; ++k)
 #pragma unroll
             for (int s = 0; s < kSumParts; ++s)
 #pragma unroll
-                for (int e = 0; e < D / 32; ++e) sum[k][e] += reinterpret_cast<const float*>(&x[k][s])[e];
+                for (int e = 0; e < D / 32; ++e) sum[k][e] += s0 + s < p.splits ? reinterpret_cast<const float*>(&x[k][s])[e] : 0.0f;
     }
 #pragma unroll
     for (int k = 0; k < kSumRows; ++k) {
