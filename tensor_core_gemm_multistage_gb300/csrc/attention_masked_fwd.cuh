@@ -751,30 +751,43 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
         }
     };
 
-    // Roles run<first>, then, if the list is not empty, run<second>.  At the barrier between all of the first run is
-    // written, its copies have landed and its products are done.
-    auto both = [&](auto role) {
+    // Roles run once, and again if the list is not empty.  At the barrier between, all of the first run is written, its
+    // copies have landed and its products are done.  The order of the code below decides how far the second
+    // run's copy lies from the first's loops: 8192 tokens in documents, capped, 174.5 us; each role's two runs side by
+    // side, the copying and issuing warps first, 178.
+    auto first_run = [&](auto role) {
         role(std::false_type{});
         tcgen05_fence_before();
         named_bar_sync(0, Cfg::NUM_THREADS);
-        if (again_words[0] == 0u || *abort_flag != 0u) return;
+        return again_words[0] != 0u && *abort_flag == 0u;
+    };
+    auto second_run = [&](auto role) {
         if (threadIdx.x == 0) FwdBars{sb + Cfg::OFF_BAR_AGAIN}.init(Cfg::SM_THREADS / 32);
         named_bar_sync(0, Cfg::NUM_THREADS);
         role(std::true_type{});
         tcgen05_fence_before();
         named_bar_sync(0, Cfg::NUM_THREADS);
     };
-    if (warp < 4) {
-        reg_dec<Cfg::CONTROL_REGS>();
-        if (warp == 0)
-            both(produce);
-        else if (warp == 1)
-            both(issue);
-        else
-            both([](auto) {});
-    } else {
+    if (warp >= 4) {
         reg_inc<Cfg::SOFTMAX_REGS>();
-        both(softmax);
+        if (first_run(softmax)) second_run(softmax);
+    } else {
+        reg_dec<Cfg::CONTROL_REGS>();
+        bool more;
+        if (warp == 0)
+            more = first_run(produce);
+        else if (warp == 1)
+            more = first_run(issue);
+        else
+            more = first_run([](auto) {});
+        if (more) {
+            if (warp == 0)
+                second_run(produce);
+            else if (warp == 1)
+                second_run(issue);
+            else
+                second_run([](auto) {});
+        }
     }
     if (warp == 1) {
         __syncwarp();
