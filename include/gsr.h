@@ -137,7 +137,8 @@ gsr_status gemm_bias_gelu(const void* A, const void* B, const void* bias, void* 
  *   causal          nonzero: query i keeps key j only when j <= i + (seq_kv - seq_q)
  *                   (lower triangle aligned to the bottom-right corner).
  * Scores and softmax in fp32, P rounded to fp16 for the second product, output rounded
- * once to fp16.  A query with no key left (causal with seq_q > seq_kv, or seq_kv == 0)
+ * once to fp16.  masked_attention_fwd below computes the same and more, faster (4 x 32 x 4096 x
+ * 128 causal 457 us, this call 537).  A query with no key left (causal with seq_q > seq_kv, or seq_kv == 0)
  * gets O = 0 and lse = -inf.  All pointers 16-byte aligned (lse 4-byte); O and lse must
  * not overlap the inputs or each other.  Caller-owned buffers; asynchronous on `stream`;
  * errors as for gemm_scale_relu.

@@ -12,8 +12,8 @@
 // recompute S and dP, seven products of 128 x 128 x D instead of the five that one pass with atomically
 // added dQ would take; in return no result depends on the order of atomics, dQ needs no fp32 buffer,
 // and every accumulator stays in TMEM from the first product to the last.  dQ's CTAs start on the SMs that
-// run out of dK and dV items.  4 x 32 x 4096 x 128 without a mask: 2797 us, 983 TFLOP/s of the five
-// products, 1376 of the seven (69 % of the measured peak); causal 1532 and 897.
+// run out of dK and dV items.  4 x 32 x 4096 x 128 without a mask, bf16: 2850 us, 965 TFLOP/s of the five
+// products, 1350 of the seven (68 % of the measured peak); causal 1591 and 864.
 //
 // fp16: P is carried as 2^12 P and dS as 2^(12 + e) dS, so that neither goes subnormal where a row has many
 // keys or dO is small.  |dO_i . V_j - delta_i| <= 2 |dO_i| max|V| (Cauchy-Schwarz; O is a mean of V rows), and e is
@@ -1317,7 +1317,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // ---------------------------------------------------------------------------
 // The rows, then dK and dV, then dQ, then the sums of parts.  dK's and dV's CTAs start while the rows' last ones
 // finish, and wait for them (let in while rows are still to come, they take SMs from them: 8192 tokens in 4
-// documents 395 us, so 408).  dQ's CTAs need the rows alone (finished when dK's and dV's CTAs have come past
+// documents 401 us, so 414).  dQ's CTAs need the rows alone (finished when dK's and dV's CTAs have come past
 // their wait, which is when dQ's may start) and fill the SMs that run out of dK and dV items.
 template <class T, int D, int MODE>
 cudaError_t launch_bwd_mode(const MaskedBwdMaps& tm, const MaskedBwdParams& p, cudaStream_t stream) {
