@@ -866,3 +866,43 @@ def test_parts_of_one_buffer(order, S):
     c.check_forward()
     gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *c.grads, **c.kw)
     c.check_backward()
+
+
+def test_a_captured_call_follows_infinities_that_come_and_go():
+    c = Case(1, 8, 2, 700, 700, 64, causal=True, docs=[[0, 300, 690]])
+    side = torch.cuda.Stream(DEV)
+    c.forward().backward()
+    clean = [t.clone() for t in (c.o, c.lse, *c.grads)]
+    v, do = c.v.clone(), c.do.clone()
+
+    def both():
+        gsr.masked_attention_fwd(c.q, c.k, c.v, c.o, c.lse, **c.kw)
+        gsr.masked_attention_bwd(c.do, c.q, c.k, c.v, c.o, c.lse, *c.grads, **c.kw)
+
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        both()
+    first = None
+    for k in range(12):
+        c.v.copy_(v)
+        c.do.copy_(do)
+        if k % 2:
+            spoil(c.v, 6, [float("inf"), float("nan")], 2)
+            spoil(c.do, 6, [float("inf"), -float("inf")], 3)
+            c.v[:, :, 690:] = float("nan")
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (c.o, c.lse, *c.grads)]
+        if not k % 2:
+            assert all(torch.equal(a, b) for a, b in zip(got, clean))
+        elif first is None:
+            first = got
+            check_natural(c)
+            check_natural_backward(c)
+        else:
+            assert all(torch.equal(a.nan_to_num(5.0), b.nan_to_num(5.0)) and torch.equal(a.isnan(), b.isnan()) for a, b in zip(got, first))
+    assert gsr.device_status(side)[0] == gsr.Status.OK
