@@ -325,6 +325,152 @@ gsr_status kv_cache_append(const gsr_tensor* K, const gsr_tensor* V, const int32
                            int64_t heads, int64_t head_dim, int64_t num_pages, int64_t page_size,
                            struct CUstream_st* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Before and after attention: head norms with the position rotation, cache writes with both on the
+ * way, a cache of 4 bits, and which drafted tokens to keep.  Types, strides and streams as above;
+ * arithmetic in float32, each result rounded once.
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * Rows x of D values:  y = rot(x w / sqrt(mean(x^2) + eps)).
+ *
+ *   q_weight, k_weight  NULL: rows of Q (K) are not normalised; else device pointer to head_dim
+ *                  values of the rows' type, 16-byte aligned.
+ *   cos_sin        NULL: no rotation; else device pointer to table_rows x rotary_dim float32, 16-byte
+ *                  aligned: a position's rotary_dim / 2 cosines, then as many sines.  Pair i of the
+ *                  first rotary_dim columns (a multiple of 16, 16 to head_dim) turns to
+ *                  (a cos_i - b sin_i, b cos_i + a sin_i); the other columns stay.
+ *   interleaved    0: pair i is columns i and i + rotary_dim / 2; else 2 i and 2 i + 1.
+ *   positions      device pointer to batch x seq int32, a row of the table for each token; NULL: a
+ *                  token's index in its row (seq <= table_rows).  Not read without cos_sin.  A negative
+ *                  one marks padding: its rows are 0.  One behind the table makes the rows NaN.
+ *   eps            >= 0, finite.
+ */
+typedef struct gsr_rope_desc {
+    int64_t batch, heads_q, heads_kv, seq, head_dim, rotary_dim, table_rows;
+    int32_t dtype; /* gsr_dtype */
+    int32_t interleaved;
+    float eps;
+    const void* q_weight;
+    const void* k_weight;
+    const float* cos_sin;
+    const int32_t* positions;
+} gsr_rope_desc;
+
+/*
+ * Q_out = y(Q), K_out = y(K).  Q, Q_out: batch x heads_q x seq x head_dim; K, K_out with heads_kv
+ * heads.  heads_q or heads_kv may be 0 (its operands are then not looked at).  An output may be the
+ * very view of its input (a call in place); otherwise outputs share no element with anything.
+ */
+gsr_status qk_norm_rope_fwd(const gsr_rope_desc* desc, const gsr_tensor* Q, const gsr_tensor* K,
+                            const gsr_tensor* Q_out, const gsr_tensor* K_out, struct CUstream_st* stream);
+
+/*
+ * Gradients dQ, dK and, where there are weights, dq_weight, dk_weight (head_dim float32 each, written,
+ * not added to) from dQ_out, dK_out and the forward's inputs Q, K (each read only where there is a
+ * weight).  dQ may be the very view of dQ_out or of Q, dK likewise.  Padding's gradients are 0 and
+ * it adds nothing to the weights', whatever its rows hold.  Results do not depend on the order of
+ * execution.
+ *
+ *   workspace  qk_norm_rope_bwd_workspace(desc) bytes, or NULL, as for masked_attention_fwd.
+ */
+int64_t qk_norm_rope_bwd_workspace(const gsr_rope_desc* desc);
+gsr_status qk_norm_rope_bwd(const gsr_rope_desc* desc, const gsr_tensor* dQ_out, const gsr_tensor* dK_out,
+                            const gsr_tensor* Q, const gsr_tensor* K, const gsr_tensor* dQ, const gsr_tensor* dK,
+                            float* dq_weight, float* dk_weight, void* workspace, int64_t workspace_bytes,
+                            struct CUstream_st* stream);
+
+/*
+ * kv_cache_append with the norm and rotation on the way: row n of y(K) and of V goes to cache row
+ * slots[n], and Q_out = y(Q) where heads_q > 0 (in place or apart, as in qk_norm_rope_fwd).  desc: batch
+ * 1, seq tokens; cos_sin needs positions (kv_block_tables writes them).  Slots outside the cache
+ * and tokens of negative position are skipped; other cache rows are left as they were.  Caches as
+ * in kv_cache_append; no two tokens of a call have the same slot (the row would hold pieces of both).
+ */
+gsr_status kv_cache_append_rope(const gsr_rope_desc* desc, const gsr_tensor* Q, const gsr_tensor* K,
+                                const gsr_tensor* V, const int32_t* slots, const gsr_tensor* Q_out,
+                                const gsr_tensor* k_cache, const gsr_tensor* v_cache, int64_t num_pages,
+                                int64_t page_size, struct CUstream_st* stream);
+
+/*
+ * A cache of 4 bits a value: each 64 values of a row have a scale s and a minimum m, both of the
+ * rows' 16-bit type, and a value is s c + m with a code c of 0 to 15: 4.5 bits a value.
+ *
+ *   codes   page x head x row of head_dim / 2 bytes, value 2 i in byte i's low half, 2 i + 1 in its
+ *           high half.  Strides in bytes, multiples of 16, data 16-byte aligned.
+ *   params  page x head x row of head_dim / 64 pairs (s, m).  Strides in 16-bit elements, multiples of
+ *           head_dim / 32, data aligned to head_dim / 16 bytes.
+ * Rows of a head that lie together (pages, heads, rows) are read fastest.  Dimensions and overlaps
+ * as in gsr_tensor; codes and params lie in buffers of their own.
+ */
+typedef struct gsr_cache4 {
+    gsr_tensor codes, params;
+} gsr_cache4;
+
+/*
+ * kv_cache_append_rope into caches of 4 bits: m is the least of 64 values, s = (largest - m) / 15 (both
+ * rounded to the rows' type), c = (x - m) / s rounded to the nearest even and cut to 0..15, 0 where s is
+ * 0.  64 values that hold an infinity or NaN, or span more than a float32, become NaN.
+ */
+gsr_status kv_cache4_append_rope(const gsr_rope_desc* desc, const gsr_tensor* Q, const gsr_tensor* K,
+                                 const gsr_tensor* V, const int32_t* slots, const gsr_tensor* Q_out,
+                                 const gsr_cache4* k_cache, const gsr_cache4* v_cache, int64_t num_pages,
+                                 int64_t page_size, struct CUstream_st* stream);
+
+/*
+ * Rows of caches of 4 bits as 16-bit values, for a prompt that attends to what is cached: row n of K
+ * (V), tokens x heads x head_dim, is cache row slots[n]; rows of slots outside the cache are left as
+ * they were.
+ */
+gsr_status kv_cache4_read(const gsr_cache4* k_cache, const gsr_cache4* v_cache, const int32_t* slots,
+                          const gsr_tensor* K, const gsr_tensor* V, int64_t tokens, int64_t heads,
+                          int64_t head_dim, int64_t num_pages, int64_t page_size, int32_t dtype,
+                          struct CUstream_st* stream);
+
+/*
+ * tree_attention_fwd over caches of 4 bits (desc->dtype: that of Q, O and the scales; alibi_slopes
+ * NULL).  Needs no workspace.  p s is rounded to Q's type for the second product (p to float32 for the
+ * minima).  Scales are not negative.  A NaN scale or minimum in V makes its 64 columns NaN for the nodes
+ * that see the key, in K all columns, and has no influence on other nodes.
+ */
+gsr_status tree_attention4_fwd(const gsr_tree_desc* desc, const void* Q, const gsr_cache4* k_cache,
+                               const gsr_cache4* v_cache, const int32_t* block_tables, const int32_t* kv_lens,
+                               const int32_t* q_starts, const int32_t* parents, void* O,
+                               struct CUstream_st* stream);
+
+/*
+ * Which drafted tokens the target's probabilities keep, from given random numbers, and the token that
+ * follows.  Nodes as in tree_attention_fwd, but node 0 of a request is the last token that is already
+ * decided, and the drafts hang below it: node t > 0 is the draft draft_tokens[q_starts[b] + t] for the
+ * place after its parent (an earlier node; parents == NULL: a chain).  Nodes that do not hang below node 0
+ * are not reached.  Row q_starts[b] + t of target_probs is the target's distribution after node t, row
+ * q_starts[b] + t of draft_probs the one that node t's token was drawn from; draft_probs == NULL:
+ * tokens were not drawn (retrieved, or a head's best guesses).
+ *
+ * From node 0 on, children are tried in their order: with r = p, the target's row, and T = 1, child c with
+ * token x is kept if u_accept[c] T q(x) < r(x); else r = max(r - T q, 0), T = sum(r), and the next child is
+ * tried.  Without draft_probs q(x) is 1, and a refusal takes x out of r and its r(x) off T.  Below a kept
+ * child the same goes on with its row.  Where no child is kept (or there is none) the next token is the
+ * first v with r(0) + ... + r(v) > u_sample[b] sum(r), its last node's row in place of an r of zeros (-1
+ * if that is zero too).  Tokens are then distributed as the target's own.
+ *
+ *   target_probs, draft_probs  total_q x vocab float32, rows target_stride_row (draft_stride_row)
+ *                  elements apart; vocab up to 2^24.  NaN counts as 0, other values are cut to 0..1.
+ *   u_accept       total_q float32 in [0, 1).      u_sample  batch float32 in [0, 1).
+ *   path           batch x max_nodes int32: the kept drafts' nodes from the root on, then -1.
+ *   counts         batch int32: how many.          next_tokens  batch int32.
+ * A request without nodes gets 0 and -1.  Nodes behind max_nodes (at most GSR_TREE_MAX_NODES) are not
+ * tried.  Tokens outside the vocabulary are refused.  Sums are exact in fixed point, 63 - ceil(log2(vocab))
+ * bits (52 at most) behind the point: results are the same on every run.
+ */
+typedef struct gsr_verify_desc {
+    int64_t batch, total_q, vocab, max_nodes, target_stride_row, draft_stride_row;
+} gsr_verify_desc;
+gsr_status verify_drafts(const gsr_verify_desc* desc, const float* target_probs, const float* draft_probs,
+                         const int32_t* draft_tokens, const int32_t* q_starts, const int32_t* parents,
+                         const float* u_accept, const float* u_sample, int32_t* path, int32_t* counts,
+                         int32_t* next_tokens, struct CUstream_st* stream);
+
 /*
  * gemm_scale_relu with the operands in host memory: copies A and B host ->
  * device into the caller's device buffers dA and dB, runs gemm_scale_relu

@@ -23,7 +23,8 @@ SOURCES = ["gsr_api.cu", "gsr_llm_api.cu", "gemm_tiled.cu", "gemm_pair.cu", "gem
            "attention_masked_fwd_f16.cu", "attention_masked_fwd_bf16.cu", "attention_masked_bwd_f16_64.cu",
            "attention_masked_bwd_f16_128.cu", "attention_masked_bwd_bf16_64.cu", "attention_masked_bwd_bf16_128.cu",
            "attention_tree_f16_64.cu", "attention_tree_f16_128.cu", "attention_tree_bf16_64.cu",
-           "attention_tree_bf16_128.cu", "kv_cache.cu"]
+           "attention_tree_bf16_128.cu", "kv_cache.cu", "gsr_serving_api.cu", "rope.cu", "attention_tree4_f16.cu",
+           "attention_tree4_bf16.cu", "verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-I" + INCLUDE, "-I" + CSRC]

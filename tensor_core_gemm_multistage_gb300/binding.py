@@ -98,8 +98,9 @@ def lib() -> ctypes.CDLL:
         L.gsr_version.argtypes = []
         L.gsr_shutdown.restype = i32
         L.gsr_shutdown.argtypes = []
-        from . import llm
+        from . import llm, serving
         llm._declare(L)
+        serving._declare(L)
         _lib = L
         return L
 

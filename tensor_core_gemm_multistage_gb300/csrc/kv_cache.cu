@@ -1,5 +1,6 @@
 // kv_cache.cu - bookkeeping of a paged key/value cache: block tables and slot maps from request
 // lengths, and the write of new keys and values to their slots.
+#include "divider.h"
 #include "llm.h"
 
 namespace gsr {
@@ -150,17 +151,6 @@ __global__ void __launch_bounds__(kTablesThreads) gsr_block_tables_kernel(const 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendUnroll = 4;
 
-// n / d for 0 <= n < 2^31: with 2^s >= d and m = ceil(2^(31 + s) / d), n m / 2^(31 + s) exceeds n / d
-// by less than n / 2^31 / d, too little to reach the next integer.
-struct Divider {
-    uint32_t d, s;
-    uint64_t m;
-    explicit Divider(uint32_t div) : d(div), s(0) {
-        while ((1ull << s) < d) ++s;
-        m = ((1ull << (31 + s)) + d - 1) / d;
-    }
-    __device__ __forceinline__ int operator()(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> (31 + s)); }
-};
 struct AppendPlan {
     Divider row, head, page;    // pieces of a token's K and V, of a head's row; a page's rows
     int tokens;                 // tokens a CTA

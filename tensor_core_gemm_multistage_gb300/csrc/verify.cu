@@ -1,0 +1,287 @@
+// verify.cu - which drafted tokens the target's probabilities keep, and the token that follows them.
+//
+// Node c below node n, token x, is kept where u T q(x) < r(x), its siblings before it having been refused.  r is what is
+// left of the target's distribution p after n: r = p and T = 1 at first; a refusal leaves r' = max(r - T q, 0),
+// T' = sum r' where q is the distribution that x was drawn from, and r without x, T' = T - r(x) where it was not drawn
+// (q is 1 at x).  At the last kept node the next token is drawn from r: the first v with r(0) + .. + r(v) > u sum(r).
+// Tokens kept or drawn so are distributed as the target's own.
+//
+// What bounds it: one row of V floats a request, two where a draft with probabilities was refused; below some MB the
+// latency of three dependent reads and two cluster barriers.  A cluster of 8 CTAs shares a request's row (one CTA a
+// request would read 0.5 MB alone).  Sums are of fixed-point integers, 63 - log2(V) bits behind the point: no
+// order of adding changes them, so the row can be cut anywhere and the drawn token is the same on each run and
+// differs from sums in 64-bit floats only where u falls within about V 2^(log2(V) - 64) of a border.
+#include "gsr.h"
+#include "serving.h"
+
+namespace gsr {
+namespace {
+
+constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32, kVerifyCtas = 8, kVerifyAtOnce = 8;
+constexpr int kMaxNodes = GSR_TREE_MAX_NODES;
+static_assert(kMaxNodes == 64, "a warp holds two nodes a lane");
+
+enum Step : int { kStepNone, kStepSum, kStepDraw };
+
+// What a request's first CTA asks of all of them: sum (and draw from) what is left of a row.
+struct Order {
+    int step, refused;
+    int row;                        // of the target, the last kept node's
+    int with_draft;
+    int what[kMaxNodes];            // refused drafts: their rows, or without probabilities their tokens
+    double total[kMaxNodes];        // T before each refusal
+};
+
+__device__ __forceinline__ uint32_t smem_of(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t of_cta(uint32_t addr, int rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Probabilities as the sums count them: NaN is 0, the rest cut to 0..1.
+__device__ __forceinline__ float sane(float p) { return fminf(fmaxf(p, 0.0f), 1.0f); }
+__device__ __forceinline__ unsigned long long fixed(float p, float scale) { return __float2ull_rn(sane(p) * scale); }
+__device__ __forceinline__ unsigned long long warp_total(unsigned long long x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// What is left of the target's row at column v.
+struct Left {
+    const float* target;
+    const float* draft;
+    long long draft_row;
+    const Order* order;
+    float scale;
+    __device__ __forceinline__ unsigned long long operator()(int v, float p, float q) const {
+        unsigned long long r = fixed(p, scale);
+        if (order->refused == 0) return r;
+        if (!order->with_draft) {
+            for (int i = 0; i < order->refused; ++i)
+                if (order->what[i] == v) r = 0;
+            return r;
+        }
+        const unsigned long long first = fixed(q, scale);
+        r = r > first ? r - first : 0;
+        for (int i = 1; i < order->refused; ++i) {
+            const double x = order->total[i] * (double)fixed(__ldg(draft + order->what[i] * draft_row + v), scale);
+            const unsigned long long less = __double2ull_rn(x);
+            r = r > less ? r - less : 0;
+        }
+        return r;
+    }
+    // its sum over columns [lo, hi), by a warp
+    __device__ __forceinline__ unsigned long long sum(int lo, int hi, int lane) const {
+        unsigned long long total = 0;
+        const bool two = order->refused > 0 && order->with_draft;
+        const float* q = two ? draft + order->what[0] * draft_row : target;
+        for (int v0 = lo + lane; v0 < hi; v0 += 32 * kVerifyAtOnce) {
+            float p[kVerifyAtOnce], x[kVerifyAtOnce];
+#pragma unroll
+            for (int k = 0; k < kVerifyAtOnce; ++k) {
+                const int v = v0 + 32 * k;
+                p[k] = v < hi ? __ldg(target + v) : 0.0f;
+                x[k] = two && v < hi ? __ldg(q + v) : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < kVerifyAtOnce; ++k)
+                if (v0 + 32 * k < hi) total += (*this)(v0 + 32 * k, p[k], x[k]);
+        }
+        return warp_total(total);
+    }
+};
+
+__global__ void __cluster_dims__(kVerifyCtas, 1, 1) __launch_bounds__(kVerifyThreads)
+    gsr_verify_kernel(const __grid_constant__ VerifyParams p, const int seg, const float scale) {
+    __shared__ Order s_order, s_own;                 // the request's (in its first CTA), and this CTA's copy
+    __shared__ unsigned long long s_totals[kVerifyCtas], s_warps[kVerifyWarps];
+    const int rank = blockIdx.x % kVerifyCtas, b = blockIdx.x / kVerifyCtas;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool leads = rank == 0 && warp == 0;
+
+    // ---- the walk down the tree, by the first CTA's first warp: lane i holds nodes i and i + 32
+    int nodes = 0, q0 = 0, cur = 0, next = 1, kept = 0, refused = 0, parent[2], token[2];
+    float u[2], pt[2], qt[2];
+    bool gone[2] = {false, false};                   // refused below `cur`
+    double left = 1.0;                               // T
+    if (leads) {
+        q0 = __ldg(p.q_starts + b);
+        nodes = q0 < 0 ? 0 : min(min(__ldg(p.q_starts + b + 1) - q0, p.max_nodes), p.N - q0);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = lane + 32 * k;
+            parent[k] = token[k] = -1;
+            u[k] = pt[k] = qt[k] = 0.0f;
+            if (c > 0 && c < nodes) {
+                parent[k] = p.parents ? __ldg(p.parents + q0 + c) : c - 1;
+                token[k] = __ldg(p.tokens + q0 + c);
+                u[k] = __ldg(p.u_accept + q0 + c);
+                if (parent[k] >= 0 && parent[k] < c && token[k] >= 0 && token[k] < p.V) {
+                    pt[k] = sane(__ldg(p.target + (q0 + parent[k]) * p.target_row + token[k]));
+                    if (p.draft) qt[k] = sane(__ldg(p.draft + (q0 + c) * p.draft_row + token[k]));
+                }
+                if (!(u[k] > 0.0f)) u[k] = 0.0f;
+            }
+        }
+    }
+    bool have_total = true;                          // `left` is up to date
+
+    for (;;) {
+        if (leads) {
+            int step = nodes > 0 ? kStepDraw : kStepNone;
+            while (step == kStepDraw) {
+                const uint32_t lo = __ballot_sync(0xffffffffu, parent[0] == cur && lane >= next);
+                const uint32_t hi = __ballot_sync(0xffffffffu, parent[1] == cur && lane + 32 >= next);
+                if (!(lo | hi)) break;
+                const int c = lo ? __ffs(lo) - 1 : 31 + __ffs(hi), from = c & 31;
+                const int x = __shfl_sync(0xffffffffu, c < 32 ? token[0] : token[1], from);
+                const double uc = __shfl_sync(0xffffffffu, c < 32 ? u[0] : u[1], from);
+                double r = __shfl_sync(0xffffffffu, c < 32 ? pt[0] : pt[1], from);
+                double q = __shfl_sync(0xffffffffu, c < 32 ? qt[0] : qt[1], from);
+                if (!p.draft) {
+                    q = 1.0;
+                    if (__any_sync(0xffffffffu, (gone[0] && token[0] == x) || (gone[1] && token[1] == x))) r = 0.0;
+                } else if (refused > 0) {
+                    if (!have_total) {               // ask for the sum first
+                        step = kStepSum;
+                        break;
+                    }
+                    for (int i = 0; i < refused; ++i) {
+                        const float y = x >= 0 && x < p.V ? __ldg(p.draft + s_order.what[i] * p.draft_row + x) : 0.0f;
+                        r = fmax(r - s_order.total[i] * (double)sane(y), 0.0);
+                    }
+                }
+                next = c + 1;
+                if (uc * left * q < r) {
+                    if (lane == 0) p.path[(long long)b * p.max_nodes + kept] = c;
+                    ++kept;
+                    cur = c;
+                    refused = 0;
+                    left = 1.0;
+                    have_total = true;
+                    gone[0] = gone[1] = false;
+                } else {
+                    if (lane == 0) {
+                        s_order.what[refused] = p.draft ? q0 + c : x;
+                        s_order.total[refused] = left;
+                    }
+                    __syncwarp();
+                    ++refused;
+                    if (p.draft) have_total = false;
+                    else left -= r;
+                    if (lane == from) gone[c >> 5] = true;
+                }
+            }
+            if (lane == 0) {
+                s_order.step = step;
+                s_order.refused = refused;
+                s_order.row = q0 + cur;
+                s_order.with_draft = p.draft != nullptr;
+            }
+            __syncwarp();
+        }
+        cluster_sync();
+        {   // the order, from the first CTA
+            const uint32_t from = of_cta(smem_of(&s_order), 0);
+            uint32_t* to = reinterpret_cast<uint32_t*>(&s_own);
+            for (int i = threadIdx.x; i < (int)(sizeof(Order) / 4); i += kVerifyThreads) {
+                uint32_t x;
+                asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(from + 4 * i) : "memory");
+                to[i] = x;
+            }
+        }
+        __syncthreads();
+        const Left rest{p.target + s_own.row * p.target_row, p.draft, p.draft_row, &s_own, scale};
+        const int lo = min((long long)(rank * kVerifyWarps + warp) * seg, (long long)p.V), hi = min((long long)lo + seg, (long long)p.V);
+        unsigned long long mine = 0;
+        if (s_own.step != kStepNone) mine = rest.sum(lo, hi, lane);
+        if (lane == 0) s_warps[warp] = mine;
+        __syncthreads();
+        if (threadIdx.x < kVerifyCtas) {
+            unsigned long long t = 0;
+#pragma unroll
+            for (int i = 0; i < kVerifyWarps; ++i) t += s_warps[i];
+            asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(of_cta(smem_of(&s_totals[rank]), threadIdx.x)), "l"(t) : "memory");
+        }
+        cluster_sync();                              // after it no CTA reaches into another
+        unsigned long long total = 0, before = 0;
+#pragma unroll
+        for (int i = 0; i < kVerifyCtas; ++i) {
+            if (i < rank) before += s_totals[i];
+            total += s_totals[i];
+        }
+        if (s_own.step == kStepSum) {
+            left = (double)total / (double)scale;
+            have_total = true;
+            continue;
+        }
+        if (s_own.step == kStepDraw && total == 0 && s_own.refused > 0) {
+            // nothing is left (the refusal was a rounding's): draw from the target's own row
+            refused = 0;
+            next = nodes;
+            continue;
+        }
+        if (leads) {
+            for (int i = kept + lane; i < p.max_nodes; i += 32) p.path[(long long)b * p.max_nodes + i] = -1;
+            if (lane == 0) {
+                p.counts[b] = kept;
+                if (total == 0) p.next[b] = -1;
+            }
+        }
+        if (s_own.step == kStepNone || total == 0) return;
+        // ---- the first column whose running sum exceeds u total: this CTA's, a warp's part, an eighth of it
+        const float us = __ldg(p.u_sample + b);
+        unsigned long long at = us > 0.0f ? (us < 1.0f ? __double2ull_rd((double)us * (double)total) : total - 1) : 0;
+        if (at >= total) at = total - 1;
+        if (at < before || at - before >= s_totals[rank]) return;
+        at -= before;
+        int part = 0;
+        while (part < kVerifyWarps - 1 && at >= s_warps[part]) at -= s_warps[part++];
+        __syncthreads();
+        const int start = min((long long)(rank * kVerifyWarps + part) * seg, (long long)p.V), stop = min((long long)start + seg, (long long)p.V);
+        const int eighth = seg / kVerifyWarps, a0 = min(start + warp * eighth, stop), a1 = min(a0 + eighth, stop);
+        const unsigned long long piece = rest.sum(a0, a1, lane);
+        if (lane == 0) s_warps[warp] = piece;
+        __syncthreads();
+        part = 0;
+        while (part < kVerifyWarps - 1 && at >= s_warps[part]) at -= s_warps[part++];
+        if (warp != part) return;
+        const bool two = s_own.refused > 0 && s_own.with_draft;
+        for (int v0 = a0; v0 < a1; v0 += 32) {
+            const int v = v0 + lane;
+            unsigned long long x = 0;
+            if (v < a1) x = rest(v, __ldg(rest.target + v), two ? __ldg(p.draft + s_own.what[0] * p.draft_row + v) : 0.0f);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, x > at);
+            if (past) {
+                if (lane == 0) p.next[b] = v0 + __ffs(past) - 1;
+                return;
+            }
+            at -= __shfl_sync(0xffffffffu, x, 31);
+        }
+        return;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream) {
+    int bits = 0;
+    while ((1ll << bits) < p.V) ++bits;
+    const int shift = 63 - bits < 52 ? 63 - bits : 52;
+    // a warp's part of a row: whole loads of a warp for each eighth
+    const int unit = 32 * kVerifyWarps, parts = kVerifyCtas * kVerifyWarps;
+    const int seg = (int)((((long long)p.V + parts - 1) / parts + unit - 1) / unit * unit);
+    gsr_verify_kernel<<<(unsigned)(p.B * kVerifyCtas), kVerifyThreads, 0, stream>>>(p, seg, (float)(1ull << shift));
+    return cudaGetLastError();
+}
+
+}  // namespace gsr
