@@ -429,9 +429,10 @@ gsr_status kv_cache4_read(const gsr_cache4* k_cache, const gsr_cache4* v_cache, 
 
 /*
  * tree_attention_fwd over caches of 4 bits (desc->dtype: that of Q, O and the scales; alibi_slopes
- * NULL).  Needs no workspace.  p s is rounded to Q's type for the second product (p to float32 for the
- * minima).  Scales are not negative.  A NaN scale or minimum in V makes its 64 columns NaN for the nodes
- * that see the key, in K all columns, and has no influence on other nodes.
+ * NULL; page and row strides below 2^32 bytes).  Needs no workspace.  p s is rounded to float16, whatever
+ * the type, for the second product (p to float32 for the minima); where the scales of one row of V are 2^20
+ * apart, the smaller one's columns lose digits.  Scales are not negative.  A NaN scale or minimum in V makes
+ * its 64 columns NaN for the nodes that see the key, in K all columns, and has no influence on other nodes.
  */
 gsr_status tree_attention4_fwd(const gsr_tree_desc* desc, const void* Q, const gsr_cache4* k_cache,
                                const gsr_cache4* v_cache, const int32_t* block_tables, const int32_t* kv_lens,
@@ -460,8 +461,8 @@ gsr_status tree_attention4_fwd(const gsr_tree_desc* desc, const void* Q, const g
  *   path           batch x max_nodes int32: the kept drafts' nodes from the root on, then -1.
  *   counts         batch int32: how many.          next_tokens  batch int32.
  * A request without nodes gets 0 and -1.  Nodes behind max_nodes (at most GSR_TREE_MAX_NODES) are not
- * tried.  Tokens outside the vocabulary are refused.  Sums are exact in fixed point, 63 - ceil(log2(vocab))
- * bits (52 at most) behind the point: results are the same on every run.
+ * tried.  Tokens outside the vocabulary are refused.  Sums are exact in fixed point, 45 bits behind the
+ * point: results are the same on every run (a row's sum, 1 of a distribution, must stay below 2^18).
  */
 typedef struct gsr_verify_desc {
     int64_t batch, total_q, vocab, max_nodes, target_stride_row, draft_stride_row;

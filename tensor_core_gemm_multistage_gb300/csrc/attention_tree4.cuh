@@ -2,12 +2,17 @@
 // ordinary decoding).
 //
 // A key (value) is s code + m for each 64 of its dimensions, so with the codes c and C of a key and a value
-//   score_j = sum_g s_jg (q_g . (c_jg - 8)) + (m_jg + 8 s_jg) sum(q_g),
+//   score_j = sum_g s_jg (q_g . c_jg) + m_jg sum(q_g),
 //   O = sum_j p_j s_jg (C_jg - 8) + sum_j p_j (m_jg + 8 s_jg):
-// both products run on the codes themselves, which 16-bit types hold exactly, and scales and minima are applied to
-// their results and to p, in fp32.
+// both products run on the codes themselves, and scales and minima are applied to their results and to p, in fp32.
+// A code is an fp16 operand as it lies: 4 bits low in a half are the subnormal c 2^-24, the next 4 bits c 2^-20,
+// which tensor cores multiply exactly; the powers of two go into the queries, and off the sums at the end.  So
+// unpacking takes one AND for two values, and a shift for four.  The 8 (which halves what rounding p s to 16 bits
+// does to O) leaves by a product with the constant, chunk by chunk: products are many fewer than values, and left
+// to the end it would cost digits (4096 keys, fp16: 3.1e-4 of O).  Queries are held
+// as fp16 times a power of two for each row (bf16's 8 bits fit; what is 2^-25 of the row's largest loses digits).
 //
-// What bounds it: D / 2 + D / 16 bytes a key and head, twice, from HBM; per byte that is 5.7 times the
+// What bounds it: D / 2 + D / 16 bytes a key and head, twice, from HBM; per byte that is 3.6 times the
 // arithmetic of a 16-bit cache, so the instructions that unpack codes come next.  Codes are therefore unpacked
 // in registers into mma.sync operands: operands of tcgen05 come from shared memory or TMEM, and the unpacked rows
 // would be written there and read again, 93 of an SM's 128 bytes a clock at HBM's rate, before the first product.
@@ -21,6 +26,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "gsr.h"
 #include "rows16.cuh"
@@ -35,6 +41,7 @@ struct Tree4Plan {
     Divider by_page;
     int tiles;                  // tiles of query rows a request and head
     int cluster;
+    int chunks;                 // that a table's row can hold
 };
 
 template <class Type, int Dim, int Nt>
@@ -62,6 +69,16 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ float lg2_fast(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -77,36 +94,30 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-template <class T>
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    if constexpr (Pair<T>::bf16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Codes i and i + 4 of a word less 8, as two operands: the code's bits in the mantissa of 64 (fp16) or 128 (bf16),
-// and one exact subtraction.  (Left in the products, the offset costs digits where they cancel: the sums run to 72
-// times a result that is a fraction of one.)
-template <class T, int I>
-__device__ __forceinline__ uint32_t codes_of(uint32_t w) {
-    if constexpr (Pair<T>::bf16) {
-        const uint32_t v = (w >> (4 * I) & 0x000f000fu) | 0x43004300u, c = 0x43084308u;
-        const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&c));
-        return *reinterpret_cast<const uint32_t*>(&r);
-    } else {
-        const uint32_t v = ((I ? w >> (I ? 4 * I - 4 : 0) : w << 4) & 0x00f000f0u) | 0x54005400u, c = 0x54805480u;
-        const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&c));
-        return *reinterpret_cast<const uint32_t*>(&r);
-    }
-}
+// Codes 0 and 4 of a word as two operands, c 2^-24; codes 1 and 5, c 2^-20.
+__device__ __forceinline__ uint32_t codes_low(uint32_t w) { return w & 0x000f000fu; }
+__device__ __forceinline__ uint32_t codes_high(uint32_t w) { return w & 0x00f000f0u; }
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// A key's scales and minima.
+template <class T, int G>
+__device__ __forceinline__ void params_of(uint32_t at, float2 (&sm)[G]) {
+    if constexpr (G == 2) {
+        const uint2 v = lds64(at);
+        sm[0] = Pair<T>::unpack(v.x);
+        sm[1] = Pair<T>::unpack(v.y);
+    } else {
+        sm[0] = Pair<T>::unpack(lds32(at));
+    }
 }
 
 // Where 16-byte piece c of key k's codes lies in a stage: rows that a warp reads at once (keys 0 to 3, or 0, 4, 1, 5
@@ -129,54 +140,55 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
     const int rank = blockIdx.x % plan.cluster, item = blockIdx.x / plan.cluster;
     const int tile = item % plan.tiles, h = item / plan.tiles % p.Hkv, b = item / plan.tiles / p.Hkv;
 
-    const int q0 = __ldg(p.q_starts + b), drafted = __ldg(p.q_starts + b + 1) - q0;
-    const int nodes = q0 < 0 ? 0 : min(min(drafted, p.max_nodes), p.total_q - q0), rows = nodes * p.group;
-    if (tile * C::ROWS >= rows) return;                                     // the whole cluster
-    const int kv = __ldg(p.kv_lens + b), ctx = kv - drafted;               // keys before the tree
-    const int n = (int)min((long long)kv, (long long)p.table_width * p.page), chunks = n > 0 ? (n + kT4Keys - 1) / kT4Keys : 0;
     const int* table = p.table + (long long)b * p.table_width;
+    const int q0 = __ldg(p.q_starts + b), q1 = __ldg(p.q_starts + b + 1), kv = __ldg(p.kv_lens + b);
 
-    // ---- the copies of a chunk.  Eight keys lie in one page; lane i looks up that of keys 8 (i % 4) on.
-    const uint32_t ring = t4_smem(smem) + warp * kT4Stages * C::STAGE;
-    auto look_up = [&](int chunk, int& pg, int& row) {
-        const int j = chunk * kT4Keys + 8 * (lane & 3);
-        pg = -1;
-        row = 0;
-        if (chunk < chunks && j < n) {
-            const int col = plan.by_page(j);
-            row = j - col * p.page;
-            pg = __ldg(table + col);
-            if (pg < 0 || pg >= p.num_pages) pg = -1;
-        }
+    // ---- the pages of a chunk: eight keys lie in one; a lane looks after keys 8 (lane / 8) on
+    const int part = lane >> 3, j8 = lane & 7;
+    const int step = plan.cluster * kT4Warps, first = rank + plan.cluster * warp;
+    auto look_up = [&](int chunk) {                         // whatever the length is: entries of the table are there
+        const int col = plan.by_page(min(chunk, plan.chunks) * kT4Keys + 8 * part);
+        return col < p.table_width ? __ldg(table + col) : -1;
     };
-    auto copy = [&](int chunk, int stage, int pg, int row) {
+    int pages[kT4Stages + 1];                               // of the chunks in flight, and of the next two
+#pragma unroll
+    for (int i = 0; i <= kT4Stages; ++i) pages[i] = look_up(first + i * step);
+
+    const int drafted = q1 - q0, nodes = q0 < 0 ? 0 : min(min(drafted, p.max_nodes), p.total_q - q0), rows = nodes * p.group;
+    if (tile * C::ROWS >= rows) return;                                     // the whole cluster
+    const int ctx = kv - drafted;                                           // keys before the tree
+    const int n = (int)min((long long)kv, (long long)p.table_width * p.page), chunks = n > 0 ? (n + kT4Keys - 1) / kT4Keys : 0;
+
+    // ---- the copies of a chunk
+    constexpr int PIECES = C::CODES / 16, AT_ONCE = 8 / PIECES;             // 16-byte pieces of a row, rows of eight lanes
+    const uint32_t ring = t4_smem(smem) + warp * kT4Stages * C::STAGE;
+    const char* const k_codes = p.K.codes.data + (long long)(j8 / PIECES) * p.K.codes.row + h * p.K.codes.head + 16 * (j8 % PIECES);
+    const char* const v_codes = p.V.codes.data + (long long)(j8 / PIECES) * p.V.codes.row + h * p.V.codes.head + 16 * (j8 % PIECES);
+    const char* const k_params = p.K.params.data + j8 * p.K.params.row + h * p.K.params.head;
+    const char* const v_params = p.V.params.data + j8 * p.V.params.row + h * p.V.params.head;
+    auto at_row = [](const char* base, const Bytes& t, uint32_t page, uint32_t row) {      // strides are below 2^32
+        return base + (unsigned long long)page * (uint32_t)t.page + (unsigned long long)row * (uint32_t)t.row;
+    };
+    auto there_is = [&](int page) { return page >= 0 && page < p.num_pages; };
+    auto copy = [&](int chunk, int stage, int pg) {
         const uint32_t at = ring + stage * C::STAGE;
-        constexpr int PIECES = C::CODES / 16, KEYS = 32 / PIECES;           // 16-byte pieces of a row, keys at once
+        const int key = chunk * kT4Keys + 8 * part, real = there_is(pg) ? n - key : 0;    // of these eight keys, those that are there
+        const uint32_t page = there_is(pg) ? pg : 0, row = key - plan.by_page(key) * p.page;   // the others' addresses are a page's all the same
+        const char *k = at_row(k_codes, p.K.codes, page, row), *v = at_row(v_codes, p.V.codes, page, row);
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            const int k = i * KEYS + lane / PIECES, c = lane % PIECES;
-            const int page = __shfl_sync(0xffffffffu, pg, k >> 3), r = __shfl_sync(0xffffffffu, row, k >> 3) + (k & 7);
-            const bool real = page >= 0 && chunk * kT4Keys + k < n;
-            const char* from_k = p.K.codes.data + page * p.K.codes.page + h * p.K.codes.head + r * p.K.codes.row + 16 * c;
-            const char* from_v = p.V.codes.data + page * p.V.codes.page + h * p.V.codes.head + r * p.V.codes.row + 16 * c;
-            copy_async<16>(at + code_at<D>(k, c), real ? from_k : p.Q, real);
-            copy_async<16>(at + kT4Keys * C::CODES + code_at<D>(k, c), real ? from_v : p.Q, real);
+            const int r = j8 / PIECES + i * AT_ONCE;
+            const uint32_t to = at + code_at<D>(8 * part + r, j8 % PIECES);
+            copy_async<16>(to, k + i * AT_ONCE * p.K.codes.row, r < real);
+            copy_async<16>(to + kT4Keys * C::CODES, v + i * AT_ONCE * p.V.codes.row, r < real);
         }
-        const int page = __shfl_sync(0xffffffffu, pg, lane >> 3), r = __shfl_sync(0xffffffffu, row, lane >> 3) + (lane & 7);
-        const bool real = page >= 0 && chunk * kT4Keys + lane < n;
-        const char* from_k = p.K.params.data + page * p.K.params.page + h * p.K.params.head + r * p.K.params.row;
-        const char* from_v = p.V.params.data + page * p.V.params.page + h * p.V.params.head + r * p.V.params.row;
         const uint32_t params = at + 2 * kT4Keys * C::CODES + lane * C::PARAMS;
-        copy_async<C::PARAMS>(params, real ? from_k : p.Q, real);
-        copy_async<C::PARAMS>(params + kT4Keys * C::PARAMS, real ? from_v : p.Q, real);
+        copy_async<C::PARAMS>(params, at_row(k_params, p.K.params, page, row), j8 < real);
+        copy_async<C::PARAMS>(params + kT4Keys * C::PARAMS, at_row(v_params, p.V.params, page, row), j8 < real);
     };
-    const int step = plan.cluster * kT4Warps, first = rank + plan.cluster * warp;
-    int pages[kT4Stages], page_rows[kT4Stages];           // of the chunks in flight, and of the next one
-#pragma unroll
-    for (int i = 0; i < kT4Stages; ++i) look_up(first + i * step, pages[i], page_rows[i]);
 #pragma unroll
     for (int i = 0; i < kT4Stages - 1; ++i) {
-        if (first + i * step < chunks) copy(first + i * step, i, pages[i], page_rows[i]);
+        if (first + i * step < chunks) copy(first + i * step, i, pages[i]);
         copies_commit();
     }
 
@@ -195,27 +207,52 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
         s_sees[threadIdx.x] = bits;
     }
 
-    // ---- queries: the products' second operand, columns n of 8, and their sums of each 64 dimensions
+    // ---- queries: the products' second operand, columns n of 8, their sums of each 64 dimensions, and the factor of scores
     uint32_t qf[G][2][2][NT][2];
-    float qsum[G][NT][2];
+    float qsum[G][NT][2], factor[NT][2];
+    const float plain = p.score.cap_out != 0.0f ? p.score.cap_in : p.score.sl2;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int r = tile * C::ROWS + 8 * nt + g, node = r / p.group;
         const T* q = static_cast<const T*>(p.Q) + (q0 + node) * p.q_row + (h * p.group + r % p.group) * p.q_head;
+        uint4 raw[G][2];
+#pragma unroll
+        for (int gi = 0; gi < G; ++gi)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                raw[gi][w] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < rows) raw[gi][w] = *reinterpret_cast<const uint4*>(q + 64 * gi + 16 * t + 8 * w);
+            }
+        uint32_t largest = 0u;                             // bits of the largest |q|
+#pragma unroll
+        for (int gi = 0; gi < G; ++gi)
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = Pair<T>::unpack((&raw[gi][w].x)[i]);
+                    largest = max(largest, max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))));
+                }
+        largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
+        largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
+        // the row times 2^e is below 2^11 beside c 2^-20, and 16 times that beside c 2^-24
+        const int e = min(max(10 - ((int)(largest >> 23) - 127), -100), 100);
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
         for (int gi = 0; gi < G; ++gi) {
             float sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (r < rows) v = *reinterpret_cast<const uint4*>(q + 64 * gi + 16 * t + 8 * w);
-                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                float x[8];
+                unpack8<T>(raw[gi][w], x);
+                // dimensions i and i + 4 together, as codes come out of a word; the even ones beside c 2^-24
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 f = Pair<T>::unpack(x[i]);
-                    sum += f.x + f.y;
-                    // dimensions i and i + 4 together, as codes come out of a word
-                    qf[gi][w][i >> 1][nt][i & 1] = __byte_perm(x[i >> 1], x[2 + (i >> 1)], i & 1 ? 0x7632 : 0x5410);
+                    const float f = i & 1 ? up : 16.0f * up;
+                    const uint32_t held = Pair<__half>::pack(x[i] * f, x[i + 4] * f);
+                    qf[gi][w][i >> 1][nt][i & 1] = held;
+                    const float2 back = Pair<__half>::unpack(held);
+                    sum += (back.x + back.y) * (i & 1 ? 0x1p-20f : 0x1p-24f);
                 }
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
@@ -223,16 +260,18 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
             qsum[gi][nt][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
             qsum[gi][nt][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
         }
+        factor[nt][0] = plain * 0x1p20f * __shfl_sync(0xffffffffu, down, 8 * t);
+        factor[nt][1] = plain * 0x1p20f * __shfl_sync(0xffffffffu, down, 8 * t + 4);
     }
     __syncthreads();
 
     // ---- the warp's chunks
-    float o[G][4][NT][4], m[NT][2], l[NT][2], mid[G][NT][2];
+    float o[G][4][NT][4], base[NT][2], l[NT][2], mid[G][NT][2];     // sums of 2^(score - base)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            m[nt][e] = -INFINITY;
+            base[nt][e] = -3.402823466e38f;
             l[nt][e] = 0.0f;
 #pragma unroll
             for (int gi = 0; gi < G; ++gi) mid[gi][nt][e] = 0.0f;
@@ -252,8 +291,8 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
         copies_wait<kT4Stages - 2>();
         __syncwarp();
         const uint32_t at = ring + stage * C::STAGE;
-        const bool full = (chunk + 1) * kT4Keys <= whole && !__any_sync(0xffffffffu, pages[0] < 0);
-        const uint32_t there = __ballot_sync(0xffffffffu, pages[0] >= 0);          // bit i: the page of keys 8 i on
+        const uint32_t there = __ballot_sync(0xffffffffu, there_is(pages[0]));          // bit 8 i: the page of keys 8 i on
+        const bool full = (chunk + 1) * kT4Keys <= whole && there == 0xffffffffu;
 
         // scores in log2 units: rows of products 2 mt (c0, c1) and 2 mt + 1 (c2, c3) of 8 keys
         float z[2][NT][4];
@@ -272,51 +311,71 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     const uint32_t xw = w ? x.y : x.x, yw = w ? y.y : y.x;
-                    const uint32_t a0 = codes_of<T, 0>(xw), a1 = codes_of<T, 0>(yw), a2 = codes_of<T, 1>(xw), a3 = codes_of<T, 1>(yw);
-                    const uint32_t b0 = codes_of<T, 2>(xw), b1 = codes_of<T, 2>(yw), b2 = codes_of<T, 3>(xw), b3 = codes_of<T, 3>(yw);
+                    const uint32_t x8 = xw >> 8, y8 = yw >> 8;
+                    const uint32_t a0 = codes_low(xw), a1 = codes_low(yw), a2 = codes_high(xw), a3 = codes_high(yw);
+                    const uint32_t b0 = codes_low(x8), b1 = codes_low(y8), b2 = codes_high(x8), b3 = codes_high(y8);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma_16x8x16<T>(acc[gi][nt], a0, a1, a2, a3, qf[gi][w][0][nt][0], qf[gi][w][0][nt][1]);
-                        mma_16x8x16<T>(acc[gi][nt], b0, b1, b2, b3, qf[gi][w][1][nt][0], qf[gi][w][1][nt][1]);
+                        mma_16x8x16(acc[gi][nt], a0, a1, a2, a3, qf[gi][w][0][nt][0], qf[gi][w][0][nt][1]);
+                        mma_16x8x16(acc[gi][nt], b0, b1, b2, b3, qf[gi][w][1][nt][0], qf[gi][w][1][nt][1]);
                     }
                 }
             }
             const uint32_t kp = at + 2 * kT4Keys * C::CODES;
+            float2 s0[G], s1[G];
+            params_of<T, G>(kp + k0 * C::PARAMS, s0);
+            params_of<T, G>(kp + k1 * C::PARAMS, s1);
 #pragma unroll
-            for (int gi = 0; gi < G; ++gi) {
-                const float2 s0 = Pair<T>::unpack(lds32(kp + k0 * C::PARAMS + 4 * gi)), s1 = Pair<T>::unpack(lds32(kp + k1 * C::PARAMS + 4 * gi));
-                const float m0 = fmaf(8.0f, s0.x, s0.y), m1 = fmaf(8.0f, s1.x, s1.y);
+            for (int gi = 0; gi < G; ++gi)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float s = fmaf(e < 2 ? s0.x : s1.x, acc[gi][nt][e], (e < 2 ? m0 : m1) * qsum[gi][nt][e & 1]);
-                        z[mt][nt][e] = gi ? z[mt][nt][e] + s : s;
+                        const float2 sm = e < 2 ? s0[gi] : s1[gi];
+                        const float x = gi ? fmaf(sm.y, qsum[gi][nt][e & 1], z[mt][nt][e]) : sm.y * qsum[gi][nt][e & 1];
+                        z[mt][nt][e] = fmaf(sm.x, acc[gi][nt][e], x);
                     }
-            }
+        }
+        // with s the largest of a value's scales, p s' = 2^(score + log2 s - base) (s' / s): what is rounded to fp16 for the
+        // second product stays in range whatever the values' size
+        float2 sm[4][G];
+        float log_s[4], inv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            params_of<T, G>(at + 2 * kT4Keys * C::CODES + kT4Keys * C::PARAMS + (8 * i + kappa) * C::PARAMS, sm[i]);
+            float s = fmaxf(sm[i][0].x, 0x1p-24f);
+            if (G == 2) s = fmaxf(s, sm[i][G - 1].x);
+            s = fminf(s, 0x1p124f);
+            log_s[i] = lg2_fast(s);
+            inv[i] = rcp_fast(s);
         }
         if (p.score.cap_out != 0.0f) {                     // cap tanh(x / cap), tanh(x) = 1 - 2 / (1 + e^2x)
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        z[mt][nt][e] = p.score.cap_out * (1.0f - __fdividef(2.0f, 1.0f + exp2f(z[mt][nt][e] * p.score.cap_in)));
+                    for (int e = 0; e < 2; ++e) {
+                        float& x = z[i >> 1][nt][2 * (i & 1) + e];
+                        x = fmaf(p.score.cap_out, 1.0f - __fdividef(2.0f, 1.0f + exp2_fast(x * factor[nt][e])), log_s[i]);
+                    }
         } else {
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) z[mt][nt][e] *= p.score.sl2;
+                    for (int e = 0; e < 2; ++e) {
+                        float& x = z[i >> 1][nt][2 * (i & 1) + e];
+                        x = fmaf(x, factor[nt][e], log_s[i]);
+                    }
         }
         uint32_t hidden = 0u;                              // bit 4 (2 mt + e / 2) + 2 nt + e % 2: the query does not see the key
         if (!full) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int j = chunk * kT4Keys + 8 * i + kappa;
-                const bool real = j < n && (there >> i & 1u);
+                const bool real = j < n && (there >> (8 * i) & 1u);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -331,50 +390,26 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
             }
         }
 
-        // values' scales: with 2^k the largest power of two in a key's scales, p s = 2^(score + k - M) (s / 2^k), so that
-        // what is rounded to T for the second product is at most 2 whatever the values' size
-        const uint32_t vp = at + 2 * kT4Keys * C::CODES + kT4Keys * C::PARAMS;
-        float2 sm[4][G];
-        float inv[4], top[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float largest = 0.0f;
-#pragma unroll
-            for (int gi = 0; gi < G; ++gi) {
-                sm[i][gi] = Pair<T>::unpack(lds32(vp + (8 * i + kappa) * C::PARAMS + 4 * gi));
-                largest = fmaxf(largest, sm[i][gi].x);
-            }
-            const int k = min(max((int)(__float_as_uint(largest) >> 23) - 127, -24), 60);
-            inv[i] = __uint_as_float((uint32_t)(127 - k) << 23);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float& x = z[i >> 1][nt][2 * (i & 1) + e];
-                    x += (float)k;
-                    top[nt][e] = fmaxf(top[nt][e], x);
-                }
-        }
-        float base[NT][2];
+        // The base moves only where a score is 2^8 above what it was set for: 2^6 below the largest then, so that p s
+        // stays under 2^14 and what is 2^-20 of the largest is still a normal fp16.
+        float top[NT][2];
         bool grew = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int s = 4; s < 32; s <<= 1) top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], s));
-                grew |= top[nt][e] > m[nt][e];
+                top[nt][e] = fmaxf(fmaxf(z[0][nt][e], z[0][nt][2 + e]), fmaxf(z[1][nt][e], z[1][nt][2 + e]));
+                grew |= top[nt][e] > base[nt][e] + 14.0f;
             }
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float next = fmaxf(m[nt][e], top[nt][e]);
-                    const float f = next == -INFINITY ? 1.0f : exp2_fast(m[nt][e] - next);
-                    m[nt][e] = next;
+#pragma unroll
+                    for (int s = 4; s < 32; s <<= 1) top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], s));
+                    const float next = fmaxf(base[nt][e], top[nt][e] - 6.0f), f = exp2_fast(base[nt][e] - next);
+                    base[nt][e] = next;
                     l[nt][e] *= f;
 #pragma unroll
                     for (int gi = 0; gi < G; ++gi) {
@@ -387,40 +422,41 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
                     }
                 }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) base[nt][e] = m[nt][e] == -INFINITY ? 0.0f : m[nt][e];
 
-        uint32_t pf[G][2][NT][2];                          // p s / 2^k, the second product's second operand
+        uint32_t pf[G][2][NT][2];                          // p s, the second product's second operand
+        auto weigh = [&](auto masked) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float ratio[G], centre[G];
+            for (int i = 0; i < 4; ++i) {
+                float ratio[G], centre[G];
 #pragma unroll
-            for (int gi = 0; gi < G; ++gi) {
-                ratio[gi] = sm[i][gi].x * inv[i];
-                centre[gi] = fmaf(8.0f, sm[i][gi].x, sm[i][gi].y) * inv[i];
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float e2[2], w[G][2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    e2[e] = exp2_fast(z[i >> 1][nt][2 * (i & 1) + e] - base[nt][e]);
-                    l[nt][e] = fmaf(e2[e], inv[i], l[nt][e]);
-                    const bool out = !full && (hidden >> (4 * i + 2 * nt + e) & 1u);       // whatever its scale holds
-#pragma unroll
-                    for (int gi = 0; gi < G; ++gi) {
-                        w[gi][e] = out ? 0.0f : e2[e] * ratio[gi];
-                        mid[gi][nt][e] = out ? mid[gi][nt][e] : fmaf(e2[e], centre[gi], mid[gi][nt][e]);
-                    }
+                for (int gi = 0; gi < G; ++gi) {
+                    ratio[gi] = sm[i][gi].x * inv[i];
+                    centre[gi] = fmaf(8.0f, ratio[gi], sm[i][gi].y * inv[i]);
                 }
 #pragma unroll
-                for (int gi = 0; gi < G; ++gi) pf[gi][i >> 1][nt][i & 1] = transpose8(Pair<T>::pack(w[gi][0], w[gi][1]));
+                for (int nt = 0; nt < NT; ++nt) {
+                    float w[G][2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float x = exp2_fast(z[i >> 1][nt][2 * (i & 1) + e] - base[nt][e]);
+                        l[nt][e] = fmaf(x, inv[i], l[nt][e]);
+                        const bool out = decltype(masked)::value && (hidden >> (4 * i + 2 * nt + e) & 1u);     // whatever its scale holds
+#pragma unroll
+                        for (int gi = 0; gi < G; ++gi) {
+                            w[gi][e] = out ? 0.0f : x * ratio[gi];
+                            mid[gi][nt][e] = out ? mid[gi][nt][e] : fmaf(x, centre[gi], mid[gi][nt][e]);
+                        }
+                    }
+#pragma unroll
+                    for (int gi = 0; gi < G; ++gi) pf[gi][i >> 1][nt][i & 1] = transpose8(Pair<__half>::pack(w[gi][0], w[gi][1]));
+                }
             }
-        }
+        };
+        if (full) weigh(std::false_type{});
+        else weigh(std::true_type{});
 
         // O^T += codes^T p: rows are dimensions 64 gi + 8 g + 2 i (c0, c1) and the next one (c2, c3)
+        constexpr uint32_t LOW8 = 0x80088008u, HIGH8 = 0x80808080u;         // -8 as the codes are held
         const uint32_t vc = at + kT4Keys * C::CODES;
 #pragma unroll
         for (int gi = 0; gi < G; ++gi)
@@ -434,24 +470,23 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const uint32_t p0 = pf[gi][mt][nt][0], p1 = pf[gi][mt][nt][1];
-                    mma_16x8x16<T>(o[gi][0][nt], codes_of<T, 0>(a_lo), codes_of<T, 1>(a_lo), codes_of<T, 0>(b_lo), codes_of<T, 1>(b_lo), p0, p1);
-                    mma_16x8x16<T>(o[gi][1][nt], codes_of<T, 2>(a_lo), codes_of<T, 3>(a_lo), codes_of<T, 2>(b_lo), codes_of<T, 3>(b_lo), p0, p1);
-                    mma_16x8x16<T>(o[gi][2][nt], codes_of<T, 0>(a_hi), codes_of<T, 1>(a_hi), codes_of<T, 0>(b_hi), codes_of<T, 1>(b_hi), p0, p1);
-                    mma_16x8x16<T>(o[gi][3][nt], codes_of<T, 2>(a_hi), codes_of<T, 3>(a_hi), codes_of<T, 2>(b_hi), codes_of<T, 3>(b_hi), p0, p1);
+                    mma_16x8x16(o[gi][0][nt], codes_low(a_lo), codes_high(a_lo), codes_low(b_lo), codes_high(b_lo), p0, p1);
+                    mma_16x8x16(o[gi][1][nt], codes_low(a_lo >> 8), codes_high(a_lo >> 8), codes_low(b_lo >> 8), codes_high(b_lo >> 8), p0, p1);
+                    mma_16x8x16(o[gi][2][nt], codes_low(a_hi), codes_high(a_hi), codes_low(b_hi), codes_high(b_hi), p0, p1);
+                    mma_16x8x16(o[gi][3][nt], codes_low(a_hi >> 8), codes_high(a_hi >> 8), codes_low(b_hi >> 8), codes_high(b_hi >> 8), p0, p1);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mma_16x8x16(o[gi][i][nt], LOW8, HIGH8, LOW8, HIGH8, p0, p1);
                 }
             }
 
         // the next copy takes the stage that was read in the last turn
         __syncwarp();
         const int ahead = chunk + (kT4Stages - 1) * step, to = stage == 0 ? kT4Stages - 1 : stage - 1;
-        if (ahead < chunks) copy(ahead, to, pages[kT4Stages - 1], page_rows[kT4Stages - 1]);
+        if (ahead < chunks) copy(ahead, to, pages[kT4Stages - 1]);
         copies_commit();
 #pragma unroll
-        for (int i = 0; i < kT4Stages - 1; ++i) {
-            pages[i] = pages[i + 1];
-            page_rows[i] = page_rows[i + 1];
-        }
-        look_up(chunk + kT4Stages * step, pages[kT4Stages - 1], page_rows[kT4Stages - 1]);
+        for (int i = 0; i < kT4Stages; ++i) pages[i] = pages[i + 1];
+        pages[kT4Stages] = look_up(chunk + (kT4Stages + 1) * step);
         stage = stage == kT4Stages - 1 ? 0 : stage + 1;
     }
     copies_wait<0>();
@@ -471,7 +506,7 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
             }
             float* to = state + warp * C::PART + (8 * nt + 2 * t + e) * C::PITCH;
             if (g == 0) {
-                to[0] = l[nt][e] == 0.0f ? -INFINITY : (m[nt][e] == -INFINITY ? 0.0f : m[nt][e]);
+                to[0] = l[nt][e] == 0.0f ? -INFINITY : base[nt][e];
                 to[1] = l[nt][e];
             }
 #pragma unroll
@@ -479,7 +514,8 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
                 const float back = mid[gi][nt][e];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<float2*>(to + 2 + 64 * gi + 8 * g + 2 * i) = make_float2(o[gi][i][nt][e] + back, o[gi][i][nt][2 + e] + back);
+                    *reinterpret_cast<float2*>(to + 2 + 64 * gi + 8 * g + 2 * i) =
+                        make_float2(fmaf(o[gi][i][nt][e], 0x1p24f, back), fmaf(o[gi][i][nt][2 + e], 0x1p20f, back));
             }
         }
     __syncthreads();
@@ -555,9 +591,10 @@ cudaError_t launch_tree4_cfg(const Tree4Params& p, int sms, cudaStream_t stream)
         if ((e = cudaFuncSetAttribute(gsr_tree4_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::RING)) != cudaSuccess) return e;
         if (dev <= 63) done.fetch_or(1ull << dev, std::memory_order_release);
     }
-    Tree4Plan plan{Divider((uint32_t)p.page), (p.max_nodes * p.group + C::ROWS - 1) / C::ROWS, 1};
+    Tree4Plan plan{Divider((uint32_t)p.page), (p.max_nodes * p.group + C::ROWS - 1) / C::ROWS, 1, 0};
     const long long items = (long long)p.B * p.Hkv * plan.tiles;
     const long long chunks = ((long long)p.table_width * p.page + kT4Keys - 1) / kT4Keys;
+    plan.chunks = (int)chunks;
     while (plan.cluster < 8 && items * plan.cluster < 4ll * sms && chunks > (long long)plan.cluster * kT4Warps) plan.cluster *= 2;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];

@@ -371,6 +371,9 @@ gsr_status tree_attention4_fwd(const gsr_tree_desc* desc, const void* Q, const g
         (s = cache4(k_cache, d.num_pages, d.heads_kv, d.page_size, d.head_dim, &p.K, &ck)) != GSR_OK ||
         (s = cache4(v_cache, d.num_pages, d.heads_kv, d.page_size, d.head_dim, &p.V, &cv)) != GSR_OK)
         return s;
+    for (const gsr::Cache4* c : {&p.K, &p.V})
+        for (const gsr::Bytes* t : {&c->codes, &c->params})
+            if (t->page > UINT32_MAX || t->row > UINT32_MAX) return GSR_ERR_INVALID_ARG;
     const Span o = span_of(os, 1, d.heads_q, d.total_q, d.head_dim, 2);
     if (share(os, 1, d.heads_q, d.total_q, qs, 1, d.heads_q, d.total_q, d.head_dim)) return GSR_ERR_ALIAS;
     for (const CacheCheck* c : {&ck, &cv})
@@ -402,6 +405,10 @@ gsr_status tree_attention4_fwd(const gsr_tree_desc* desc, const void* Q, const g
     p.kv_lens = kv_lens;
     p.q_starts = q_starts;
     p.parents = parents;
+    if (d.num_pages == 0) {             // no key is there: addresses that no copy reads
+        const gsr::Bytes none{static_cast<char*>(const_cast<void*>(Q)), 0, 0, 0};
+        p.K = p.V = gsr::Cache4{none, none};
+    }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return launched(d.dtype == GSR_BF16 ? gsr::launch_tree4_bf16(p, sms, st) : gsr::launch_tree4_f16(p, sms, st));
 }

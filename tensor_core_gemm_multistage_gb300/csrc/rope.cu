@@ -27,33 +27,26 @@ __device__ __forceinline__ LanePart lane_part(int l, int R, bool interleaved) {
     return {l, l + rc, true};                    // column i turns with i + R / 2
 }
 
-struct Angles {
-    float c[8], s[8];
-};
-__device__ __forceinline__ void load_angles(Angles& a, const float* table, long long pos, int R, int l) {
-    const float4* c = reinterpret_cast<const float4*>(table + pos * R + 8 * l);
-    const float4* s = reinterpret_cast<const float4*>(table + pos * R + R / 2 + 8 * l);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float4 x = __ldg(c + i), y = __ldg(s + i);
-        a.c[4 * i] = x.x; a.c[4 * i + 1] = x.y; a.c[4 * i + 2] = x.z; a.c[4 * i + 3] = x.w;
-        a.s[4 * i] = y.x; a.s[4 * i + 1] = y.y; a.s[4 * i + 2] = y.z; a.s[4 * i + 3] = y.w;
-    }
-}
 // Each product and sum rounded by itself, so that codes of 4 bits do not hang on a contraction.
 __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
     const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
     b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
     a = x;
 }
-// v[0..7] is piece c0, v[8..15] piece c1.
-__device__ __forceinline__ void rotate(float (&v)[16], const Angles& a, bool interleaved, float sign) {
-    if (interleaved) {
+// v[0..7] is piece c0, v[8..15] piece c1; `cosines` the lane's eight of its token, its sines R / 2 behind.  They are loaded for
+// each row, from L1 after the first: held in registers they cost a third of the warps.
+__device__ __forceinline__ void rotate(float (&v)[16], const float* cosines, int R, bool interleaved, float sign) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) turn(v[2 * i], v[2 * i + 1], a.c[i], sign * a.s[i]);
-    } else {
+    for (int half = 0; half < 2; ++half) {
+        const float4 c4 = __ldg(reinterpret_cast<const float4*>(cosines) + half);
+        const float4 s4 = __ldg(reinterpret_cast<const float4*>(cosines + R / 2) + half);
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) turn(v[i], v[8 + i], a.c[i], sign * a.s[i]);
+        for (int i = 0; i < 4; ++i) {
+            const int k = 4 * half + i;
+            if (interleaved) turn(v[2 * k], v[2 * k + 1], c[i], sign * s[i]);
+            else turn(v[k], v[8 + k], c[i], sign * s[i]);
+        }
     }
 }
 template <int LANES>
@@ -66,6 +59,11 @@ template <class T>
 __device__ __forceinline__ void load_part(const T* row, const LanePart& at, uint4& lo, uint4& hi) {
     lo = reinterpret_cast<const uint4*>(row)[at.c0];     // not the read-only path: a call may work in place
     hi = reinterpret_cast<const uint4*>(row)[at.c1];
+}
+template <class T>
+__device__ __forceinline__ void load_weight(const T* w, const LanePart& at, float (&to)[16]) {
+    unpack8<T>(__ldg(reinterpret_cast<const uint4*>(w) + at.c0), to);
+    unpack8<T>(__ldg(reinterpret_cast<const uint4*>(w) + at.c1), to + 8);
 }
 template <class T>
 __device__ __forceinline__ void store_part(T* row, const LanePart& at, const float (&v)[16]) {
@@ -153,7 +151,7 @@ __device__ __forceinline__ void store_row4(const Cache4& cache, long long page, 
 }
 
 template <class T, int D, int SINK>
-__global__ void __launch_bounds__(kThreads) gsr_rope_kernel(const __grid_constant__ RopeAppendParams a,
+__global__ void __launch_bounds__(kThreads, 3) gsr_rope_kernel(const __grid_constant__ RopeAppendParams a,
                                                             const __grid_constant__ RopePlan plan) {
     constexpr int LANES = D / 16, ROWS = 32 / LANES, STEPS = 4;      // rows at once, rows a lane has in flight
     const RopeParams& p = a.f;
@@ -187,12 +185,9 @@ __global__ void __launch_bounds__(kThreads) gsr_rope_kernel(const __grid_constan
         page = plan.by_page(slot);
         row = slot - (int)page * a.page;
     }
-    Angles angles;
     const bool known = !p.table || (pos >= 0 && pos < p.rows);
-    if (at.turns && known) load_angles(angles, p.table, pos, p.R, l);
+    const float* cosines = p.table + (known ? (long long)pos * p.R + 8 * l : 0);
     const T* w = static_cast<const T*>(is_q ? p.q_weight : is_v ? nullptr : p.k_weight);
-    uint4 w0, w1;
-    if (w) load_part(w, at, w0, w1);
 
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
@@ -209,12 +204,11 @@ __global__ void __launch_bounds__(kThreads) gsr_rope_kernel(const __grid_constan
             for (int k = 0; k < 16; ++k) sum = fmaf(v[k], v[k], sum);
             const float r = rsqrtf(row_sum<LANES>(sum) * (1.0f / D) + p.eps);
             float weight[16];
-            unpack8<T>(w0, weight);
-            unpack8<T>(w1, weight + 8);
+            load_weight(w, at, weight);
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = v[k] * r * weight[k];
         }
-        if (at.turns && known) rotate(v, angles, p.interleaved, 1.0f);
+        if (at.turns && known) rotate(v, cosines, p.R, p.interleaved, 1.0f);
         if (!known && !is_v) {
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = pos < 0 ? 0.0f : NAN;
@@ -266,11 +260,9 @@ cudaError_t launch_rope_type(const RopeAppendParams& a, bool bf16, int sms, cuda
 // r is computed again from x, which has to be read anyway, so the forward pass stores nothing.  A CTA sums dw
 // over its rows in registers (fp32, a lane's 16 columns), then over its warps; a second launch adds the CTAs'
 // sums in their order, so that results repeat.
-constexpr int kBwdSteps = 2;
-
 struct RopeBwdPlan {
     Divider by_q, by_k, by_seq;
-    int per, q_units, k_units;
+    int q_units, k_units;               // steps of as many rows as a warp holds at once
 };
 
 template <class T, int D>
@@ -287,70 +279,64 @@ __global__ void __launch_bounds__(kThreads, 2) gsr_rope_bwd_kernel(const __grid_
         const T* w = static_cast<const T*>(part ? p.k_weight : p.q_weight);
         const int units = part ? plan.k_units : plan.q_units, heads = part ? p.Hkv : p.Hq;
         const Divider& by = part ? plan.by_k : plan.by_q;
-        uint4 w0, w1;
         float dw[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) dw[k] = 0.0f;
-        if (w) load_part(w, at, w0, w1);
+        // a step's rows are loaded before the arithmetic of the step before it
+        struct Rows {
+            uint4 g[2], x[2];
+            long long to;               // where this lane's row of dX starts
+            int pos;
+            bool live;
+        };
+        auto load = [&](int unit, Rows& r) {
+            r.g[0] = r.g[1] = r.x[0] = r.x[1] = make_uint4(0u, 0u, 0u, 0u);
+            r.live = false;
+            if (unit >= units) return;
+            const int token = by(unit), h = (unit - token * (int)by.d) * ROWS + lane / LANES, b = plan.by_seq(token), s = token - b * p.S;
+            r.pos = p.table && p.positions ? __ldg(p.positions + token) : s;
+            r.live = h < heads;
+            if (!r.live) return;
+            load_part(static_cast<const T*>(G.data) + b * G.batch + s * G.row + h * G.head, at, r.g[0], r.g[1]);
+            if (w) load_part(static_cast<const T*>(X.data) + b * X.batch + s * X.row + h * X.head, at, r.x[0], r.x[1]);
+            r.to = b * dX.batch + s * dX.row + h * dX.head;
+        };
+        const int first = blockIdx.x * kWarps + warp, stride = gridDim.x * kWarps;
+        Rows now, next;
+        load(first, now);
 #pragma unroll 1
-        for (int unit = blockIdx.x * kWarps + warp; unit < units; unit += gridDim.x * kWarps) {
-            const int token = by(unit), block = unit - token * (int)by.d, b = plan.by_seq(token), s = token - b * p.S;
-            const int h0 = block * plan.per + lane / LANES, end = min(heads, (block + 1) * plan.per);
-            const T* from_g = static_cast<const T*>(G.data) + b * G.batch + s * G.row;
-            const T* from_x = static_cast<const T*>(X.data) + b * X.batch + s * X.row;
-            T* to = static_cast<T*>(dX.data) + b * dX.batch + s * dX.row;
-            int pos = s;
-            if (p.table && p.positions) pos = __ldg(p.positions + token);
-            const bool known = !p.table || (pos >= 0 && pos < p.rows);
-            Angles angles;
-            if (at.turns && known) load_angles(angles, p.table, pos, p.R, l);
-#pragma unroll 1
-            for (int first = block * plan.per; first < end; first += kBwdSteps * ROWS) {
-                uint4 g[kBwdSteps][2], x[kBwdSteps][2];
+        for (int unit = first; unit < units; unit += stride) {
+            load(unit + stride, next);
+            const bool known = !p.table || (now.pos >= 0 && now.pos < p.rows), counts = now.live && (!p.table || now.pos >= 0);
+            float dy[16];
+            unpack8<T>(now.g[0], dy);
+            unpack8<T>(now.g[1], dy + 8);
+            if (at.turns && known) rotate(dy, p.table + (long long)now.pos * p.R + 8 * l, p.R, p.interleaved, -1.0f);
+            if (!known) {
 #pragma unroll
-                for (int i = 0; i < kBwdSteps; ++i) {
-                    const int h = h0 + (first - block * plan.per) + i * ROWS;
-                    g[i][0] = g[i][1] = x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
-                    if (h < end) {
-                        load_part(from_g + h * G.head, at, g[i][0], g[i][1]);
-                        if (w) load_part(from_x + h * X.head, at, x[i][0], x[i][1]);
-                    }
+                for (int k = 0; k < 16; ++k) dy[k] = counts ? NAN : 0.0f;
+            }
+            if (w) {
+                float v[16], weight[16];
+                unpack8<T>(now.x[0], v);
+                unpack8<T>(now.x[1], v + 8);
+                load_weight(w, at, weight);
+                float square = 0.0f, dot = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    square = fmaf(v[k], v[k], square);
+                    dot = fmaf(dy[k] * weight[k], v[k], dot);
                 }
+                const float r = rsqrtf(row_sum<LANES>(square) * (1.0f / D) + p.eps);
+                const float back = row_sum<LANES>(dot) * (1.0f / D) * r * r * r;
 #pragma unroll
-                for (int i = 0; i < kBwdSteps; ++i) {
-                    const int h = h0 + (first - block * plan.per) + i * ROWS;
-                    float dy[16];
-                    unpack8<T>(g[i][0], dy);
-                    unpack8<T>(g[i][1], dy + 8);
-                    if (at.turns && known) rotate(dy, angles, p.interleaved, -1.0f);
-                    if (!known) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) dy[k] = pos < 0 || h >= end ? 0.0f : NAN;
-                    }
-                    if (w) {
-                        float v[16], weight[16];
-                        unpack8<T>(x[i][0], v);
-                        unpack8<T>(x[i][1], v + 8);
-                        unpack8<T>(w0, weight);
-                        unpack8<T>(w1, weight + 8);
-                        float square = 0.0f, dot = 0.0f;
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            square = fmaf(v[k], v[k], square);
-                            dot = fmaf(dy[k] * weight[k], v[k], dot);
-                        }
-                        const float r = rsqrtf(row_sum<LANES>(square) * (1.0f / D) + p.eps);
-                        const float back = row_sum<LANES>(dot) * (1.0f / D) * r * r * r;
-                        const bool counts = pos >= 0 || !p.table;      // padding adds nothing, whatever it holds
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            if (counts) dw[k] = fmaf(dy[k] * v[k], r, dw[k]);
-                            dy[k] = counts ? r * dy[k] * weight[k] - v[k] * back : 0.0f;
-                        }
-                    }
-                    if (h < end) store_part(to + h * dX.head, at, dy);
+                for (int k = 0; k < 16; ++k) {
+                    if (counts) dw[k] = fmaf(dy[k] * v[k], r, dw[k]);       // padding adds nothing, whatever it holds
+                    dy[k] = counts ? r * dy[k] * weight[k] - v[k] * back : 0.0f;
                 }
             }
+            if (now.live) store_part(static_cast<T*>(dX.data) + now.to, at, dy);
+            now = next;
         }
         if (!w) continue;
 #pragma unroll
@@ -400,9 +386,8 @@ cudaError_t launch_bwd(const RopeBwdParams& a, cudaStream_t stream) {
     const long long tokens = (long long)p.B * p.S;
     cudaError_t e = cudaSuccess;
     if (a.ctas > 0) {
-        RopeBwdPlan plan{Divider(1), Divider(1), Divider((uint32_t)p.S), 0, 0, 0};
-        plan.per = rope_unit_heads(tokens, p.Hq + p.Hkv, D, (int)(a.ctas / 2));
-        const int q_blocks = (p.Hq + plan.per - 1) / plan.per, k_blocks = (p.Hkv + plan.per - 1) / plan.per;
+        RopeBwdPlan plan{Divider(1), Divider(1), Divider((uint32_t)p.S), 0, 0};
+        const int step = 512 / D, q_blocks = (p.Hq + step - 1) / step, k_blocks = (p.Hkv + step - 1) / step;
         if (q_blocks) plan.by_q = Divider((uint32_t)q_blocks);
         if (k_blocks) plan.by_k = Divider((uint32_t)k_blocks);
         plan.q_units = (int)(tokens * q_blocks);

@@ -8,9 +8,9 @@
 //
 // What bounds it: one row of V floats a request, two where a draft with probabilities was refused; below some MB the
 // latency of three dependent reads and two cluster barriers.  A cluster of 8 CTAs shares a request's row (one CTA a
-// request would read 0.5 MB alone).  Sums are of fixed-point integers, 63 - log2(V) bits behind the point: no
-// order of adding changes them, so the row can be cut anywhere and the drawn token is the same on each run and
-// differs from sums in 64-bit floats only where u falls within about V 2^(log2(V) - 64) of a border.
+// request would read 0.5 MB alone).  Sums are of fixed-point integers, 45 bits behind the point: no order of adding
+// changes them, so the row can be cut anywhere and the drawn token is the same on each run; it differs from sums
+// in 64-bit floats only where u falls within about V 2^-46 of a border.
 #include "gsr.h"
 #include "serving.h"
 
@@ -43,60 +43,90 @@ __device__ __forceinline__ void cluster_sync() {
 }
 // Probabilities as the sums count them: NaN is 0, the rest cut to 0..1.
 __device__ __forceinline__ float sane(float p) { return fminf(fmaxf(p, 0.0f), 1.0f); }
-__device__ __forceinline__ unsigned long long fixed(float p, float scale) { return __float2ull_rn(sane(p) * scale); }
+// p in units of 2^-45, hi 2^23 + lo: two sums with a constant round p to 2^-22 and what is left to 2^-45 and leave the integers in
+// their low bits (a conversion to 64 bits costs four times as much).  Larger p, larger or equal result.
+struct Fixed {
+    int hi, lo;
+};
+__device__ __forceinline__ Fixed fixed(float p) {
+    const float x = sane(p), a = __fadd_rn(x, 2.0f);                       // 2..3: steps of 2^-22
+    const float rest = __fsub_rn(x, __fsub_rn(a, 2.0f));                   // exact, at most 2^-23
+    const float b = __fadd_rn(rest, 0x1.8p-22f);                           // 2^-22..2^-21: steps of 2^-45
+    return {__float_as_int(a) - __float_as_int(2.0f), __float_as_int(b) - __float_as_int(0x1.8p-22f)};
+}
+__device__ __forceinline__ long long whole(Fixed f) { return (long long)f.hi * (1 << 23) + f.lo; }
+constexpr double kOne = 35184372088832.0;           // 2^45
 __device__ __forceinline__ unsigned long long warp_total(unsigned long long x) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
-// What is left of the target's row at column v.
+// What is left of the target's row.
 struct Left {
     const float* target;
     const float* draft;
     long long draft_row;
     const Order* order;
-    float scale;
-    __device__ __forceinline__ unsigned long long operator()(int v, float p, float q) const {
-        unsigned long long r = fixed(p, scale);
-        if (order->refused == 0) return r;
-        if (!order->with_draft) {
-            for (int i = 0; i < order->refused; ++i)
+    int refused;
+    bool two;                                       // the first refused draft's row goes off the target's
+    const float* first;
+    // at column v
+    __device__ __forceinline__ long long at(int v, float p, float q) const {
+        long long r = whole(fixed(p));
+        if (!two) {
+            for (int i = 0; i < refused; ++i)
                 if (order->what[i] == v) r = 0;
             return r;
         }
-        const unsigned long long first = fixed(q, scale);
-        r = r > first ? r - first : 0;
-        for (int i = 1; i < order->refused; ++i) {
-            const double x = order->total[i] * (double)fixed(__ldg(draft + order->what[i] * draft_row + v), scale);
-            const unsigned long long less = __double2ull_rn(x);
-            r = r > less ? r - less : 0;
+        r = max(r - whole(fixed(q)), 0ll);
+        for (int i = 1; i < refused; ++i) {
+            const double less = order->total[i] * (double)whole(fixed(__ldg(draft + order->what[i] * draft_row + v)));
+            r = max(r - __double2ll_rn(less), 0ll);
         }
         return r;
     }
-    // its sum over columns [lo, hi), by a warp
-    __device__ __forceinline__ unsigned long long sum(int lo, int hi, int lane) const {
-        unsigned long long total = 0;
-        const bool two = order->refused > 0 && order->with_draft;
-        const float* q = two ? draft + order->what[0] * draft_row : target;
-        for (int v0 = lo + lane; v0 < hi; v0 += 32 * kVerifyAtOnce) {
-            float p[kVerifyAtOnce], x[kVerifyAtOnce];
+    // a lane's columns v0, v0 + 32, ..: their sum, and each one in x where it is asked for
+    template <bool KEEP>
+    __device__ __forceinline__ long long some(int v0, int hi, long long (&x)[kVerifyAtOnce]) const {
+        float p[kVerifyAtOnce], q[kVerifyAtOnce];
+#pragma unroll
+        for (int k = 0; k < kVerifyAtOnce; ++k) {
+            const int v = v0 + 32 * k;
+            p[k] = v < hi ? __ldg(target + v) : 0.0f;
+            q[k] = two && v < hi ? __ldg(first + v) : 0.0f;
+        }
+        if (!KEEP && refused <= (two ? 1 : 0)) {    // nothing but max(p - q, 0)
+            int hi_sum = 0, lo_sum = 0;
 #pragma unroll
             for (int k = 0; k < kVerifyAtOnce; ++k) {
-                const int v = v0 + 32 * k;
-                p[k] = v < hi ? __ldg(target + v) : 0.0f;
-                x[k] = two && v < hi ? __ldg(q + v) : 0.0f;
+                const Fixed a = fixed(p[k]), b = fixed(q[k]);
+                if (sane(p[k]) > sane(q[k])) {
+                    hi_sum += a.hi - b.hi;
+                    lo_sum += a.lo - b.lo;
+                }
             }
-#pragma unroll
-            for (int k = 0; k < kVerifyAtOnce; ++k)
-                if (v0 + 32 * k < hi) total += (*this)(v0 + 32 * k, p[k], x[k]);
+            return (long long)hi_sum * (1 << 23) + lo_sum;
         }
-        return warp_total(total);
+        long long total = 0;
+#pragma unroll
+        for (int k = 0; k < kVerifyAtOnce; ++k) {
+            const long long r = v0 + 32 * k < hi ? at(v0 + 32 * k, p[k], q[k]) : 0;
+            if (KEEP) x[k] = r;
+            total += r;
+        }
+        return total;
+    }
+    // the sum over columns [lo, hi), by a warp
+    __device__ __forceinline__ unsigned long long sum(int lo, int hi, int lane) const {
+        long long total = 0, x[kVerifyAtOnce];
+        for (int v0 = lo + lane; v0 < hi; v0 += 32 * kVerifyAtOnce) total += some<false>(v0, hi, x);
+        return warp_total((unsigned long long)total);
     }
 };
 
-__global__ void __cluster_dims__(kVerifyCtas, 1, 1) __launch_bounds__(kVerifyThreads)
-    gsr_verify_kernel(const __grid_constant__ VerifyParams p, const int seg, const float scale) {
+__global__ void __cluster_dims__(kVerifyCtas, 1, 1) __launch_bounds__(kVerifyThreads, 2)
+    gsr_verify_kernel(const __grid_constant__ VerifyParams p, const int seg) {
     __shared__ Order s_order, s_own;                 // the request's (in its first CTA), and this CTA's copy
     __shared__ unsigned long long s_totals[kVerifyCtas], s_warps[kVerifyWarps];
     const int rank = blockIdx.x % kVerifyCtas, b = blockIdx.x / kVerifyCtas;
@@ -195,7 +225,9 @@ __global__ void __cluster_dims__(kVerifyCtas, 1, 1) __launch_bounds__(kVerifyThr
             }
         }
         __syncthreads();
-        const Left rest{p.target + s_own.row * p.target_row, p.draft, p.draft_row, &s_own, scale};
+        const bool two = s_own.refused > 0 && s_own.with_draft;
+        const Left rest{p.target + s_own.row * p.target_row, p.draft, p.draft_row, &s_own, s_own.refused, two,
+                        two ? p.draft + s_own.what[0] * p.draft_row : nullptr};
         const int lo = min((long long)(rank * kVerifyWarps + warp) * seg, (long long)p.V), hi = min((long long)lo + seg, (long long)p.V);
         unsigned long long mine = 0;
         if (s_own.step != kStepNone) mine = rest.sum(lo, hi, lane);
@@ -215,7 +247,7 @@ __global__ void __cluster_dims__(kVerifyCtas, 1, 1) __launch_bounds__(kVerifyThr
             total += s_totals[i];
         }
         if (s_own.step == kStepSum) {
-            left = (double)total / (double)scale;
+            left = (double)total / kOne;
             have_total = true;
             continue;
         }
@@ -244,28 +276,31 @@ __global__ void __cluster_dims__(kVerifyCtas, 1, 1) __launch_bounds__(kVerifyThr
         __syncthreads();
         const int start = min((long long)(rank * kVerifyWarps + part) * seg, (long long)p.V), stop = min((long long)start + seg, (long long)p.V);
         const int eighth = seg / kVerifyWarps, a0 = min(start + warp * eighth, stop), a1 = min(a0 + eighth, stop);
-        const unsigned long long piece = rest.sum(a0, a1, lane);
+        long long x[kVerifyAtOnce];                  // where an eighth is a lane's eight columns, they are kept
+        const bool keep = eighth <= 32 * kVerifyAtOnce;
+        const unsigned long long piece = keep ? warp_total((unsigned long long)rest.some<true>(a0 + lane, a1, x)) : rest.sum(a0, a1, lane);
         if (lane == 0) s_warps[warp] = piece;
         __syncthreads();
         part = 0;
         while (part < kVerifyWarps - 1 && at >= s_warps[part]) at -= s_warps[part++];
         if (warp != part) return;
-        const bool two = s_own.refused > 0 && s_own.with_draft;
-        for (int v0 = a0; v0 < a1; v0 += 32) {
-            const int v = v0 + lane;
-            unsigned long long x = 0;
-            if (v < a1) x = rest(v, __ldg(rest.target + v), two ? __ldg(p.draft + s_own.what[0] * p.draft_row + v) : 0.0f);
+        for (int v0 = a0; v0 < a1; v0 += 32 * kVerifyAtOnce) {
+            if (!keep) rest.some<true>(v0 + lane, a1, x);
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
+            for (int k = 0; k < kVerifyAtOnce; ++k) {
+                unsigned long long run = (unsigned long long)x[k];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const unsigned long long y = __shfl_up_sync(0xffffffffu, run, o);
+                    if (lane >= o) run += y;
+                }
+                const uint32_t past = __ballot_sync(0xffffffffu, run > at);
+                if (past) {
+                    if (lane == 0) p.next[b] = v0 + 32 * k + __ffs(past) - 1;
+                    return;
+                }
+                at -= __shfl_sync(0xffffffffu, run, 31);
             }
-            const uint32_t past = __ballot_sync(0xffffffffu, x > at);
-            if (past) {
-                if (lane == 0) p.next[b] = v0 + __ffs(past) - 1;
-                return;
-            }
-            at -= __shfl_sync(0xffffffffu, x, 31);
         }
         return;
     }
@@ -274,13 +309,10 @@ __global__ void __cluster_dims__(kVerifyCtas, 1, 1) __launch_bounds__(kVerifyThr
 }  // namespace
 
 cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream) {
-    int bits = 0;
-    while ((1ll << bits) < p.V) ++bits;
-    const int shift = 63 - bits < 52 ? 63 - bits : 52;
     // a warp's part of a row: whole loads of a warp for each eighth
     const int unit = 32 * kVerifyWarps, parts = kVerifyCtas * kVerifyWarps;
     const int seg = (int)((((long long)p.V + parts - 1) / parts + unit - 1) / unit * unit);
-    gsr_verify_kernel<<<(unsigned)(p.B * kVerifyCtas), kVerifyThreads, 0, stream>>>(p, seg, (float)(1ull << shift));
+    gsr_verify_kernel<<<(unsigned)(p.B * kVerifyCtas), kVerifyThreads, 0, stream>>>(p, seg);
     return cudaGetLastError();
 }
 
