@@ -125,7 +125,7 @@ struct Left {
     }
 };
 
-__global__ void __cluster_dims__(kVerifyCtas, 1, 1) __launch_bounds__(kVerifyThreads, 2)
+__global__ void __cluster_dims__(kVerifyCtas, 1, 1) __launch_bounds__(kVerifyThreads, 4)
     gsr_verify_kernel(const __grid_constant__ VerifyParams p, const int seg) {
     __shared__ Order s_order, s_own;                 // the request's (in its first CTA), and this CTA's copy
     __shared__ unsigned long long s_totals[kVerifyCtas], s_warps[kVerifyWarps];
