@@ -96,7 +96,7 @@ struct Left {
             p[k] = v < hi ? __ldg(target + v) : 0.0f;
             q[k] = two && v < hi ? __ldg(first + v) : 0.0f;
         }
-        if (!KEEP && refused <= (two ? 1 : 0)) {    // nothing but max(p - q, 0)
+        if (!KEEP && (!two || refused == 1)) {      // nothing but max(p - q, 0)
             int hi_sum = 0, lo_sum = 0;
 #pragma unroll
             for (int k = 0; k < kVerifyAtOnce; ++k) {
@@ -121,6 +121,11 @@ struct Left {
     __device__ __forceinline__ unsigned long long sum(int lo, int hi, int lane) const {
         long long total = 0, x[kVerifyAtOnce];
         for (int v0 = lo + lane; v0 < hi; v0 += 32 * kVerifyAtOnce) total += some<false>(v0, hi, x);
+        if (!two)                                   // less the refused tokens, each of them once in the list
+            for (int i = lane; i < refused; i += 32) {
+                const int v = order->what[i];
+                if (v >= lo && v < hi) total -= whole(fixed(__ldg(target + v)));
+            }
         return warp_total((unsigned long long)total);
     }
 };
@@ -195,12 +200,15 @@ __global__ void __cluster_dims__(kVerifyCtas, 1, 1) __launch_bounds__(kVerifyThr
                     have_total = true;
                     gone[0] = gone[1] = false;
                 } else {
-                    if (lane == 0) {
-                        s_order.what[refused] = p.draft ? q0 + c : x;
-                        s_order.total[refused] = left;
+                    // without probabilities a token is listed once
+                    if (p.draft || r > 0.0) {
+                        if (lane == 0) {
+                            s_order.what[refused] = p.draft ? q0 + c : x;
+                            s_order.total[refused] = left;
+                        }
+                        __syncwarp();
+                        ++refused;
                     }
-                    __syncwarp();
-                    ++refused;
                     if (p.draft) have_total = false;
                     else left -= r;
                     if (lane == from) gone[c >> 5] = true;
