@@ -35,7 +35,7 @@
 namespace gsr {
 namespace {
 
-constexpr int kT4Warps = 8, kT4Threads = 32 * kT4Warps, kT4Stages = 3, kT4Keys = 32;
+constexpr int kT4Warps = 4, kT4Threads = 32 * kT4Warps, kT4Keys = 32;
 
 struct Tree4Plan {
     Divider by_page;
@@ -48,9 +48,12 @@ template <class Type, int Dim, int Nt>
 struct T4Cfg {
     using T = Type;
     static constexpr int D = Dim, NT = Nt, G = D / 64, ROWS = 8 * NT;
+    static constexpr int STAGES = NT == 1 ? 2 : 3;
     static constexpr int CODES = D / 2, PARAMS = D / 16;             // bytes of a row
     static constexpr int STAGE = kT4Keys * 2 * (CODES + PARAMS);
-    static constexpr int RING = kT4Warps * kT4Stages * STAGE;
+    static constexpr int RING = kT4Warps * STAGES * STAGE;
+    static constexpr int FACTORS = kT4Keys * (D == 128 ? 40 : 24);   // bytes of a warp's chunk: see key_factors
+    static constexpr int SMEM = RING + kT4Warps * FACTORS;
     static constexpr int PITCH = D + 2;                              // floats of a row's state: M, l, D sums
     static constexpr int PART = ROWS * PITCH;                        // floats of a warp's states
     static_assert((kT4Warps + 1) * PART * 4 <= RING, "states are joined in the ring");
@@ -108,28 +111,95 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
-// A key's scales and minima.
-template <class T, int G>
-__device__ __forceinline__ void params_of(uint32_t at, float2 (&sm)[G]) {
-    if constexpr (G == 2) {
-        const uint2 v = lds64(at);
-        sm[0] = Pair<T>::unpack(v.x);
-        sm[1] = Pair<T>::unpack(v.y);
+__device__ __forceinline__ float4 lds128(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, float x, float y, float z, float w) {
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t a, float x, float y) {
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+}
+// Two 16 x 16 blocks of bytes, transposed: rows of 16 bytes at the addresses of lanes 0 to 15 and 16 to 31.  Lane 4 g + t
+// gets column g of rows 4 t to 4 t + 3 in v[0], column g + 8 in v[1], the second block's in v[2] and v[3].
+__device__ __forceinline__ void load_transposed(uint32_t (&v)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(a)
+                 : "memory");
+}
+
+// Where 16-byte piece c of key k's codes lies in a stage: neither the eight keys that a transposed load reads at once nor
+// the four keys 2 apart that a product's rows are read from meet in a bank.
+template <int D>
+__device__ __forceinline__ int code_at(int k, int c) {
+    if constexpr (D == 128) return ((k & ~3) | (k & 1) << 1 | (k >> 1 & 1)) * 64 + (c ^ ((k >> 2 & 1) << 1 | (k & 1))) * 16;
+    return ((k & 16) | (k & 1) << 3 | (k >> 1 & 7)) * 32 + (c ^ (k & 1)) * 16;
+}
+// Keys in the order in which products have them as rows: the even ones of 16, then the odd ones.
+__device__ __forceinline__ int row_of(int k) { return (k & 16) | (k & 1) << 3 | (k >> 1 & 7); }
+
+// A chunk's keys as the arithmetic takes them, each prepared by one lane, since four lanes of the products need each:
+// of K scales and minima; of V, with s the largest of the key's scales, their ratios to it, (m + 8 s') / s, log2 s, 1 / s.
+// With p s' = 2^(score + log2 s - base) (s' / s), what is rounded to fp16 for the second product stays in range
+// whatever the values' size.
+template <class T, int D>
+__device__ __forceinline__ void key_factors(uint32_t params_k, uint32_t params_v, uint32_t to, int lane) {
+    const int row = row_of(lane);
+    auto largest = [](float s) { return fminf(fmaxf(s, 0x1p-24f), 0x1p124f); };
+    if constexpr (D == 128) {
+        const uint2 k = lds64(params_k + 8 * lane), v = lds64(params_v + 8 * lane);
+        const float2 k0 = Pair<T>::unpack(k.x), k1 = Pair<T>::unpack(k.y), v0 = Pair<T>::unpack(v.x), v1 = Pair<T>::unpack(v.y);
+        const float s = largest(fmaxf(v0.x, v1.x)), inv = rcp_fast(s), r0 = v0.x * inv, r1 = v1.x * inv;
+        sts128(to + 16 * row, k0.x, k1.x, k0.y, k1.y);
+        sts128(to + 512 + 16 * row, r0, r1, fmaf(8.0f, r0, v0.y * inv), fmaf(8.0f, r1, v1.y * inv));
+        sts64(to + 1024 + 8 * row, lg2_fast(s), inv);
     } else {
-        sm[0] = Pair<T>::unpack(lds32(at));
+        const float2 k = Pair<T>::unpack(lds32(params_k + 4 * lane)), v = Pair<T>::unpack(lds32(params_v + 4 * lane));
+        const float s = largest(v.x), inv = rcp_fast(s), r = v.x * inv;
+        sts64(to + 8 * row, k.x, k.y);
+        sts128(to + 256 + 16 * row, r, fmaf(8.0f, r, v.y * inv), lg2_fast(s), inv);
+    }
+    __syncwarp();
+}
+template <int D, int G>
+__device__ __forceinline__ void factors_k(uint32_t at, int row, float (&s)[G], float (&m)[G]) {
+    if constexpr (D == 128) {
+        const float4 x = lds128(at + 16 * row);
+        s[0] = x.x;
+        s[1] = x.y;
+        m[0] = x.z;
+        m[1] = x.w;
+    } else {
+        const uint2 x = lds64(at + 8 * row);
+        s[0] = __uint_as_float(x.x);
+        m[0] = __uint_as_float(x.y);
+    }
+}
+template <int D, int G>
+__device__ __forceinline__ void factors_v(uint32_t at, int row, float (&ratio)[G], float (&centre)[G], float& log_s, float& inv) {
+    if constexpr (D == 128) {
+        const float4 x = lds128(at + 512 + 16 * row);
+        const uint2 y = lds64(at + 1024 + 8 * row);
+        ratio[0] = x.x;
+        ratio[1] = x.y;
+        centre[0] = x.z;
+        centre[1] = x.w;
+        log_s = __uint_as_float(y.x);
+        inv = __uint_as_float(y.y);
+    } else {
+        const float4 x = lds128(at + 256 + 16 * row);
+        ratio[0] = x.x;
+        centre[0] = x.y;
+        log_s = x.z;
+        inv = x.w;
     }
 }
 
-// Where 16-byte piece c of key k's codes lies in a stage: rows that a warp reads at once (keys 0 to 3, or 0, 4, 1, 5
-// of 8) meet in no bank.
-template <int D>
-__device__ __forceinline__ int code_at(int k, int c) {
-    if constexpr (D == 128) return k * 64 + (c ^ ((k >> 1 ^ k >> 2) & 1) << 1) * 16;
-    return (k ^ (k & 4) >> 1) * 32 + c * 16;
-}
-
 template <class C>
-__global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 4 : 2)
     gsr_tree4_kernel(const __grid_constant__ Tree4Params p, const __grid_constant__ Tree4Plan plan) {
     using T = typename C::T;
     constexpr int D = C::D, G = C::G, NT = C::NT;
@@ -150,9 +220,9 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
         const int col = plan.by_page(min(chunk, plan.chunks) * kT4Keys + 8 * part);
         return col < p.table_width ? __ldg(table + col) : -1;
     };
-    int pages[kT4Stages + 1];                               // of the chunks in flight, and of the next two
+    int pages[C::STAGES + 1];                               // of the chunks in flight, and of the next two
 #pragma unroll
-    for (int i = 0; i <= kT4Stages; ++i) pages[i] = look_up(first + i * step);
+    for (int i = 0; i <= C::STAGES; ++i) pages[i] = look_up(first + i * step);
 
     const int drafted = q1 - q0, nodes = q0 < 0 ? 0 : min(min(drafted, p.max_nodes), p.total_q - q0), rows = nodes * p.group;
     if (tile * C::ROWS >= rows) return;                                     // the whole cluster
@@ -161,7 +231,7 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
 
     // ---- the copies of a chunk
     constexpr int PIECES = C::CODES / 16, AT_ONCE = 8 / PIECES;             // 16-byte pieces of a row, rows of eight lanes
-    const uint32_t ring = t4_smem(smem) + warp * kT4Stages * C::STAGE;
+    const uint32_t ring = t4_smem(smem) + warp * C::STAGES * C::STAGE;
     const char* const k_codes = p.K.codes.data + (long long)(j8 / PIECES) * p.K.codes.row + h * p.K.codes.head + 16 * (j8 % PIECES);
     const char* const v_codes = p.V.codes.data + (long long)(j8 / PIECES) * p.V.codes.row + h * p.V.codes.head + 16 * (j8 % PIECES);
     const char* const k_params = p.K.params.data + j8 * p.K.params.row + h * p.K.params.head;
@@ -175,6 +245,19 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
         const int key = chunk * kT4Keys + 8 * part, real = there_is(pg) ? n - key : 0;    // of these eight keys, those that are there
         const uint32_t page = there_is(pg) ? pg : 0, row = key - plan.by_page(key) * p.page;   // the others' addresses are a page's all the same
         const char *k = at_row(k_codes, p.K.codes, page, row), *v = at_row(v_codes, p.V.codes, page, row);
+        const uint32_t params = at + 2 * kT4Keys * C::CODES + lane * C::PARAMS;
+        const char *pk = at_row(k_params, p.K.params, page, row), *pv = at_row(v_params, p.V.params, page, row);
+        if (__all_sync(0xffffffffu, real >= 8)) {
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                const uint32_t to = at + code_at<D>(8 * part + j8 / PIECES + i * AT_ONCE, j8 % PIECES);
+                copy_async<16>(to, k + i * AT_ONCE * p.K.codes.row, true);
+                copy_async<16>(to + kT4Keys * C::CODES, v + i * AT_ONCE * p.V.codes.row, true);
+            }
+            copy_async<C::PARAMS>(params, pk, true);
+            copy_async<C::PARAMS>(params + kT4Keys * C::PARAMS, pv, true);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
             const int r = j8 / PIECES + i * AT_ONCE;
@@ -182,12 +265,11 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
             copy_async<16>(to, k + i * AT_ONCE * p.K.codes.row, r < real);
             copy_async<16>(to + kT4Keys * C::CODES, v + i * AT_ONCE * p.V.codes.row, r < real);
         }
-        const uint32_t params = at + 2 * kT4Keys * C::CODES + lane * C::PARAMS;
-        copy_async<C::PARAMS>(params, at_row(k_params, p.K.params, page, row), j8 < real);
-        copy_async<C::PARAMS>(params + kT4Keys * C::PARAMS, at_row(v_params, p.V.params, page, row), j8 < real);
+        copy_async<C::PARAMS>(params, pk, j8 < real);
+        copy_async<C::PARAMS>(params + kT4Keys * C::PARAMS, pv, j8 < real);
     };
 #pragma unroll
-    for (int i = 0; i < kT4Stages - 1; ++i) {
+    for (int i = 0; i < C::STAGES - 1; ++i) {
         if (first + i * step < chunks) copy(first + i * step, i, pages[i]);
         copies_commit();
     }
@@ -283,23 +365,31 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[gi][i][nt][e] = 0.0f;
     }
-    const int kappa = (g >> 1) + 4 * (g & 1);              // the key of 8 that row g of a product is
+    const uint32_t factors = t4_smem(smem) + C::RING + warp * C::FACTORS;
     const int whole = min(ctx, n);                         // keys below it are seen by all, where their pages are there
     int stage = 0;
 #pragma unroll 1
     for (int chunk = first; chunk < chunks; chunk += step) {
-        copies_wait<kT4Stages - 2>();
+        copies_wait<C::STAGES - 2>();
         __syncwarp();
-        const uint32_t at = ring + stage * C::STAGE;
+        // the next copy takes the stage that was read in the last turn
         const uint32_t there = __ballot_sync(0xffffffffu, there_is(pages[0]));          // bit 8 i: the page of keys 8 i on
+        const int ahead = chunk + (C::STAGES - 1) * step;
+        if (ahead < chunks) copy(ahead, stage == 0 ? C::STAGES - 1 : stage - 1, pages[C::STAGES - 1]);
+        copies_commit();
+#pragma unroll
+        for (int i = 0; i < C::STAGES; ++i) pages[i] = pages[i + 1];
+        pages[C::STAGES] = look_up(chunk + (C::STAGES + 1) * step);
+        const uint32_t at = ring + stage * C::STAGE;
         const bool full = (chunk + 1) * kT4Keys <= whole && there == 0xffffffffu;
+        key_factors<T, D>(at + 2 * kT4Keys * C::CODES, at + 2 * kT4Keys * C::CODES + kT4Keys * C::PARAMS, factors, lane);
 
-        // scores in log2 units: rows of products 2 mt (c0, c1) and 2 mt + 1 (c2, c3) of 8 keys
+        // scores in log2 units: of keys 16 mt + 2 g (c0, c1) and the next one (c2, c3)
         float z[2][NT][4];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
             float acc[G][NT][4];
-            const int k0 = 16 * mt + kappa, k1 = k0 + 8;
+            const int k0 = 16 * mt + 2 * g, k1 = k0 + 1;
 #pragma unroll
             for (int gi = 0; gi < G; ++gi) {
 #pragma unroll
@@ -321,34 +411,23 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
                     }
                 }
             }
-            const uint32_t kp = at + 2 * kT4Keys * C::CODES;
-            float2 s0[G], s1[G];
-            params_of<T, G>(kp + k0 * C::PARAMS, s0);
-            params_of<T, G>(kp + k1 * C::PARAMS, s1);
+            float s0[G], m0[G], s1[G], m1[G];
+            factors_k<D>(factors, 16 * mt + g, s0, m0);
+            factors_k<D>(factors, 16 * mt + 8 + g, s1, m1);
 #pragma unroll
             for (int gi = 0; gi < G; ++gi)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 sm = e < 2 ? s0[gi] : s1[gi];
-                        const float x = gi ? fmaf(sm.y, qsum[gi][nt][e & 1], z[mt][nt][e]) : sm.y * qsum[gi][nt][e & 1];
-                        z[mt][nt][e] = fmaf(sm.x, acc[gi][nt][e], x);
+                        const float s = e < 2 ? s0[gi] : s1[gi], m = e < 2 ? m0[gi] : m1[gi];
+                        const float x = gi ? fmaf(m, qsum[gi][nt][e & 1], z[mt][nt][e]) : m * qsum[gi][nt][e & 1];
+                        z[mt][nt][e] = fmaf(s, acc[gi][nt][e], x);
                     }
         }
-        // with s the largest of a value's scales, p s' = 2^(score + log2 s - base) (s' / s): what is rounded to fp16 for the
-        // second product stays in range whatever the values' size
-        float2 sm[4][G];
-        float log_s[4], inv[4];
+        float ratio[4][G], centre[4][G], log_s[4], inv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            params_of<T, G>(at + 2 * kT4Keys * C::CODES + kT4Keys * C::PARAMS + (8 * i + kappa) * C::PARAMS, sm[i]);
-            float s = fmaxf(sm[i][0].x, 0x1p-24f);
-            if (G == 2) s = fmaxf(s, sm[i][G - 1].x);
-            s = fminf(s, 0x1p124f);
-            log_s[i] = lg2_fast(s);
-            inv[i] = rcp_fast(s);
-        }
+        for (int i = 0; i < 4; ++i) factors_v<D>(factors, 8 * i + g, ratio[i], centre[i], log_s[i], inv[i]);
         if (p.score.cap_out != 0.0f) {                     // cap tanh(x / cap), tanh(x) = 1 - 2 / (1 + e^2x)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -374,8 +453,8 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
         if (!full) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int j = chunk * kT4Keys + 8 * i + kappa;
-                const bool real = j < n && (there >> (8 * i) & 1u);
+                const int k = 16 * (i >> 1) + 2 * g + (i & 1), j = chunk * kT4Keys + k;
+                const bool real = j < n && (there >> (k & 24) & 1u);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -427,12 +506,6 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
         auto weigh = [&](auto masked) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float ratio[G], centre[G];
-#pragma unroll
-                for (int gi = 0; gi < G; ++gi) {
-                    ratio[gi] = sm[i][gi].x * inv[i];
-                    centre[gi] = fmaf(8.0f, ratio[gi], sm[i][gi].y * inv[i]);
-                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float w[G][2];
@@ -443,8 +516,8 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
                         const bool out = decltype(masked)::value && (hidden >> (4 * i + 2 * nt + e) & 1u);     // whatever its scale holds
 #pragma unroll
                         for (int gi = 0; gi < G; ++gi) {
-                            w[gi][e] = out ? 0.0f : x * ratio[gi];
-                            mid[gi][nt][e] = out ? mid[gi][nt][e] : fmaf(x, centre[gi], mid[gi][nt][e]);
+                            w[gi][e] = out ? 0.0f : x * ratio[i][gi];
+                            mid[gi][nt][e] = out ? mid[gi][nt][e] : fmaf(x, centre[i][gi], mid[gi][nt][e]);
                         }
                     }
 #pragma unroll
@@ -455,7 +528,7 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
         if (full) weigh(std::false_type{});
         else weigh(std::true_type{});
 
-        // O^T += codes^T p: rows are dimensions 64 gi + 8 g + 2 i (c0, c1) and the next one (c2, c3)
+        // O^T += codes^T p: product i of a group has dimensions 16 i + 2 g (c0, c1) and the next one (c2, c3) as rows
         constexpr uint32_t LOW8 = 0x80088008u, HIGH8 = 0x80808080u;         // -8 as the codes are held
         const uint32_t vc = at + kT4Keys * C::CODES;
 #pragma unroll
@@ -463,31 +536,19 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
                 uint32_t v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = lds32(vc + code_at<D>(16 * mt + 4 * i + t, 2 * gi + (g >> 2)) + 4 * (g & 3));
-                const uint32_t a_lo = __byte_perm(v[0], v[1], 0x5410), a_hi = __byte_perm(v[0], v[1], 0x7632);
-                const uint32_t b_lo = __byte_perm(v[2], v[3], 0x5410), b_hi = __byte_perm(v[2], v[3], 0x7632);
+                load_transposed(v, vc + code_at<D>(16 * mt + (lane & 15), 2 * gi + (lane >> 4)));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const uint32_t p0 = pf[gi][mt][nt][0], p1 = pf[gi][mt][nt][1];
-                    mma_16x8x16(o[gi][0][nt], codes_low(a_lo), codes_high(a_lo), codes_low(b_lo), codes_high(b_lo), p0, p1);
-                    mma_16x8x16(o[gi][1][nt], codes_low(a_lo >> 8), codes_high(a_lo >> 8), codes_low(b_lo >> 8), codes_high(b_lo >> 8), p0, p1);
-                    mma_16x8x16(o[gi][2][nt], codes_low(a_hi), codes_high(a_hi), codes_low(b_hi), codes_high(b_hi), p0, p1);
-                    mma_16x8x16(o[gi][3][nt], codes_low(a_hi >> 8), codes_high(a_hi >> 8), codes_low(b_hi >> 8), codes_high(b_hi >> 8), p0, p1);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mma_16x8x16(o[gi][i][nt], LOW8, HIGH8, LOW8, HIGH8, p0, p1);
+                    for (int i = 0; i < 4; ++i) {
+                        mma_16x8x16(o[gi][i][nt], codes_low(v[i]), codes_high(v[i]), codes_low(v[i] >> 8), codes_high(v[i] >> 8), p0, p1);
+                        mma_16x8x16(o[gi][i][nt], LOW8, HIGH8, LOW8, HIGH8, p0, p1);
+                    }
                 }
             }
 
-        // the next copy takes the stage that was read in the last turn
-        __syncwarp();
-        const int ahead = chunk + (kT4Stages - 1) * step, to = stage == 0 ? kT4Stages - 1 : stage - 1;
-        if (ahead < chunks) copy(ahead, to, pages[kT4Stages - 1]);
-        copies_commit();
-#pragma unroll
-        for (int i = 0; i < kT4Stages; ++i) pages[i] = pages[i + 1];
-        pages[kT4Stages] = look_up(chunk + (kT4Stages + 1) * step);
-        stage = stage == kT4Stages - 1 ? 0 : stage + 1;
+        stage = stage == C::STAGES - 1 ? 0 : stage + 1;
     }
     copies_wait<0>();
 
@@ -514,7 +575,7 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 2 : 1)
                 const float back = mid[gi][nt][e];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<float2*>(to + 2 + 64 * gi + 8 * g + 2 * i) =
+                    *reinterpret_cast<float2*>(to + 2 + 64 * gi + 16 * i + 2 * g) =
                         make_float2(fmaf(o[gi][i][nt][e], 0x1p24f, back), fmaf(o[gi][i][nt][2 + e], 0x1p20f, back));
             }
         }
@@ -588,14 +649,14 @@ cudaError_t launch_tree4_cfg(const Tree4Params& p, int sms, cudaStream_t stream)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev > 63 || !(done.load(std::memory_order_acquire) >> dev & 1)) {
-        if ((e = cudaFuncSetAttribute(gsr_tree4_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::RING)) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(gsr_tree4_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
         if (dev <= 63) done.fetch_or(1ull << dev, std::memory_order_release);
     }
     Tree4Plan plan{Divider((uint32_t)p.page), (p.max_nodes * p.group + C::ROWS - 1) / C::ROWS, 1, 0};
     const long long items = (long long)p.B * p.Hkv * plan.tiles;
     const long long chunks = ((long long)p.table_width * p.page + kT4Keys - 1) / kT4Keys;
     plan.chunks = (int)chunks;
-    while (plan.cluster < 8 && items * plan.cluster < 4ll * sms && chunks > (long long)plan.cluster * kT4Warps) plan.cluster *= 2;
+    while (plan.cluster < 8 && items * plan.cluster < 8ll * sms && chunks > (long long)plan.cluster * kT4Warps) plan.cluster *= 2;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -603,7 +664,7 @@ cudaError_t launch_tree4_cfg(const Tree4Params& p, int sms, cudaStream_t stream)
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)(items * plan.cluster));
     cfg.blockDim = dim3(kT4Threads);
-    cfg.dynamicSmemBytes = C::RING;
+    cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
