@@ -429,15 +429,19 @@ gsr_status kv_cache4_read(const gsr_cache4* k_cache, const gsr_cache4* v_cache, 
 
 /*
  * tree_attention_fwd over caches of 4 bits (desc->dtype: that of Q, O and the scales; alibi_slopes
- * NULL; page and row strides below 2^32 bytes).  Needs no workspace.  p s is rounded to float16, whatever
- * the type, for the second product (p to float32 for the minima); where the scales of one row of V are 2^20
+ * NULL; page and row strides below 2^32 bytes).  p s is rounded to float16, whatever the type, for the
+ * second product (p to float32 for the minima); where the scales of one row of V are 2^20
  * apart, the smaller one's columns lose digits.  Scales are not negative.  A NaN scale or minimum in V makes
  * its 64 columns NaN for the nodes that see the key, in K all columns, and has no influence on other nodes.
+ *
+ *   workspace  tree_attention4_workspace(desc) bytes (0 where there is little work; it depends on the sizes
+ *              alone), or NULL, as for masked_attention_fwd.
  */
+int64_t tree_attention4_workspace(const gsr_tree_desc* desc);
 gsr_status tree_attention4_fwd(const gsr_tree_desc* desc, const void* Q, const gsr_cache4* k_cache,
                                const gsr_cache4* v_cache, const int32_t* block_tables, const int32_t* kv_lens,
-                               const int32_t* q_starts, const int32_t* parents, void* O,
-                               struct CUstream_st* stream);
+                               const int32_t* q_starts, const int32_t* parents, void* O, void* workspace,
+                               int64_t workspace_bytes, struct CUstream_st* stream);
 
 /*
  * Which drafted tokens the target's probabilities keep, from given random numbers, and the token that

@@ -17,7 +17,8 @@ from .llm import (TREE_MAX_NODES, kv_block_tables, kv_cache_append, masked_atten
                   masked_attention_bwd_workspace, masked_attention_fwd, masked_attention_fwd_workspace,
                   tree_attention_fwd, tree_attention_workspace)
 from .serving import (Cache4, kv_cache4, kv_cache4_append_rope, kv_cache4_read, kv_cache_append_rope, qk_norm_rope_bwd,
-                      qk_norm_rope_bwd_workspace, qk_norm_rope_fwd, rope_table, tree_attention4_fwd, verify_drafts)
+                      qk_norm_rope_bwd_workspace, qk_norm_rope_fwd, rope_table, tree_attention4_fwd,
+                      tree_attention4_workspace, verify_drafts)
 from ._build import build
 
 __all__ = [
@@ -28,7 +29,8 @@ __all__ = [
     "TREE_MAX_NODES", "kv_block_tables", "kv_cache_append", "masked_attention_bwd", "masked_attention_bwd_workspace",
     "masked_attention_fwd", "masked_attention_fwd_workspace", "tree_attention_fwd", "tree_attention_workspace",
     "Cache4", "kv_cache4", "kv_cache4_append_rope", "kv_cache4_read", "kv_cache_append_rope", "qk_norm_rope_bwd",
-    "qk_norm_rope_bwd_workspace", "qk_norm_rope_fwd", "rope_table", "tree_attention4_fwd", "verify_drafts",
+    "qk_norm_rope_bwd_workspace", "qk_norm_rope_fwd", "rope_table", "tree_attention4_fwd",
+    "tree_attention4_workspace", "verify_drafts",
     "release_stream", "select_path", "set_path_override", "set_raster_group", "set_split_k", "set_test_flags", "set_wait_timeout_ns", "shutdown",
     "status_string", "version",
 ]

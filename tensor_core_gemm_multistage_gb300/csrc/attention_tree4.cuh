@@ -19,36 +19,64 @@
 // Keys are the products' rows (16 at once) and the queries of a group their columns (8): no row of the product is
 // spent on padding where a group has 4 or 8 heads.
 //
-// Split: a cluster of CTAs shares the keys of one request, head and tile of 8 NT query rows, in chunks of 32
-// that warps take in turn; each warp copies its own chunks (cp.async, three in flight), with its own softmax
-// state.  States are joined in shared memory, over the cluster by distributed shared memory: one launch, no
-// workspace, no order that changes.
+// Split.  A CTA's four warps take 32-key chunks of one request, head and tile of 8 NT query rows in turn; each warp
+// copies its own chunks (cp.async) and has its own softmax state, and the states are joined in shared memory.
+//  * Little work: a cluster of CTAs shares an item's chunks and joins their states by distributed shared
+//    memory.  One launch, no workspace.
+//  * Much: the chunks of all items are laid end to end and shared out evenly over as many CTAs as the SMs hold at
+//    once, whatever the lengths (each CTA finds its range by one sum over the requests).  An item that one CTA covers
+//    is written at once, else its CTAs leave their states in the workspace, two a CTA at most, and a second
+//    launch joins them in the CTAs' order.  Clusters cost 8 us a wave of CTAs there, and their waves leave SMs idle
+//    (48 requests of 4000 to 8000 tokens: 91 us in clusters).
+// No order changes from run to run.
 #pragma once
 
 #include <atomic>
+#include <climits>
 #include <type_traits>
 
 #include "gsr.h"
+#include "ptx_attention.cuh"
 #include "rows16.cuh"
 #include "serving.h"
 
 namespace gsr {
 namespace {
 
-constexpr int kT4Warps = 4, kT4Threads = 32 * kT4Warps, kT4Keys = 32;
+constexpr int kT4Threads = 32 * kT4Warps;
 
 struct Tree4Plan {
     Divider by_page;
     int tiles;                  // tiles of query rows a request and head
-    int cluster;
+    int cluster;                // CTAs that share an item; 0: shared out evenly
     int chunks;                 // that a table's row can hold
 };
+
+// What a request has: query rows (nodes x group) from q0 on, cached tokens `kv`, of them `ctx` before the tree,
+// `n` in the table; units of work: chunks (one at least) of each of its items.
+struct T4Request {
+    int q0, rows, nodes, ctx, n, chunks, tiles;
+    __device__ __forceinline__ long long units(int heads) const { return (long long)heads * tiles * max(chunks, 1); }
+};
+template <int ROWS>
+__device__ __forceinline__ T4Request t4_request(const Tree4Params& p, int b) {
+    const int q0 = __ldg(p.q_starts + b), q1 = __ldg(p.q_starts + b + 1), kv = __ldg(p.kv_lens + b);
+    T4Request r;
+    r.q0 = q0;
+    r.nodes = q0 < 0 ? 0 : max(min(min(q1 - q0, p.max_nodes), p.total_q - q0), 0);
+    r.rows = r.nodes * p.group;
+    r.tiles = (r.rows + ROWS - 1) / ROWS;
+    r.ctx = kv - (q1 - q0);
+    r.n = (int)min((long long)kv, (long long)p.table_width * p.page);
+    r.chunks = r.n > 0 ? (r.n + kT4Keys - 1) / kT4Keys : 0;
+    return r;
+}
 
 template <class Type, int Dim, int Nt>
 struct T4Cfg {
     using T = Type;
     static constexpr int D = Dim, NT = Nt, G = D / 64, ROWS = 8 * NT;
-    static constexpr int STAGES = NT == 1 ? 2 : 3;
+    static constexpr int STAGES = NT == 1 ? 2 : 3, CTAS = NT == 1 ? 4 : 2;     // CTAs on an SM
     static constexpr int CODES = D / 2, PARAMS = D / 16;             // bytes of a row
     static constexpr int STAGE = kT4Keys * 2 * (CODES + PARAMS);
     static constexpr int RING = kT4Warps * STAGES * STAGE;
@@ -198,24 +226,41 @@ __device__ __forceinline__ void factors_v(uint32_t at, int row, float (&ratio)[G
     }
 }
 
-template <class C>
-__global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 4 : 2)
-    gsr_tree4_kernel(const __grid_constant__ Tree4Params p, const __grid_constant__ Tree4Plan plan) {
+// States of row q from `count` places, each state_of(i, place): largest M, and sums weighed by 2^(M_i - M).
+template <class C, class State>
+__device__ __forceinline__ void t4_join(State state_of, int count, int q, int d, float& most, float& sum, float2& v) {
+    most = -INFINITY;
+    for (int i = 0; i < count; ++i) most = fmaxf(most, state_of(i, q * C::PITCH));
+    sum = 0.0f;
+    v = make_float2(0.0f, 0.0f);
+    if (most == -INFINITY) return;
+    for (int i = 0; i < count; ++i) {
+        const float mi = state_of(i, q * C::PITCH);
+        if (mi == -INFINITY) continue;                 // that part saw nothing; its sums are not written
+        const float f = exp2_fast(mi - most);
+        sum = fmaf(f, state_of(i, q * C::PITCH + 1), sum);
+        v.x = fmaf(f, state_of(i, q * C::PITCH + 2 + d), v.x);
+        v.y = fmaf(f, state_of(i, q * C::PITCH + 3 + d), v.y);
+    }
+}
+
+struct T4Shared {
+    uint64_t sees[GSR_TREE_MAX_NODES];       // bit u of sees[t]: node t sees node u
+    int parent[GSR_TREE_MAX_NODES];
+};
+
+// Chunks first + i step (of this warp) below `end` of an item; false where the tile has no rows.  out(write, q, d, most, sum, v): the CTA's joined state of row q, dimensions d and d + 1 (write(q, d, x, y,
+// sum) puts them into O).
+template <class C, class Out>
+__device__ __forceinline__ bool t4_part(const Tree4Params& p, const Tree4Plan& plan, char* smem, T4Shared& sh, int b, int h, int tile, int first,
+                                        int step, int end, Out out) {
     using T = typename C::T;
     constexpr int D = C::D, G = C::G, NT = C::NT;
-    extern __shared__ __align__(128) char smem[];
-    __shared__ uint64_t s_sees[GSR_TREE_MAX_NODES];
-    __shared__ int s_parent[GSR_TREE_MAX_NODES];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int rank = blockIdx.x % plan.cluster, item = blockIdx.x / plan.cluster;
-    const int tile = item % plan.tiles, h = item / plan.tiles % p.Hkv, b = item / plan.tiles / p.Hkv;
-
     const int* table = p.table + (long long)b * p.table_width;
-    const int q0 = __ldg(p.q_starts + b), q1 = __ldg(p.q_starts + b + 1), kv = __ldg(p.kv_lens + b);
 
     // ---- the pages of a chunk: eight keys lie in one; a lane looks after keys 8 (lane / 8) on
     const int part = lane >> 3, j8 = lane & 7;
-    const int step = plan.cluster * kT4Warps, first = rank + plan.cluster * warp;
     auto look_up = [&](int chunk) {                         // whatever the length is: entries of the table are there
         const int col = plan.by_page(min(chunk, plan.chunks) * kT4Keys + 8 * part);
         return col < p.table_width ? __ldg(table + col) : -1;
@@ -224,10 +269,9 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 4 : 2)
 #pragma unroll
     for (int i = 0; i <= C::STAGES; ++i) pages[i] = look_up(first + i * step);
 
-    const int drafted = q1 - q0, nodes = q0 < 0 ? 0 : min(min(drafted, p.max_nodes), p.total_q - q0), rows = nodes * p.group;
-    if (tile * C::ROWS >= rows) return;                                     // the whole cluster
-    const int ctx = kv - drafted;                                           // keys before the tree
-    const int n = (int)min((long long)kv, (long long)p.table_width * p.page), chunks = n > 0 ? (n + kT4Keys - 1) / kT4Keys : 0;
+    const T4Request req = t4_request<C::ROWS>(p, b);
+    const int q0 = req.q0, nodes = req.nodes, rows = req.rows, ctx = req.ctx, n = req.n, chunks = min(req.chunks, end);
+    if (tile * C::ROWS >= rows) return false;
 
     // ---- the copies of a chunk
     constexpr int PIECES = C::CODES / 16, AT_ONCE = 8 / PIECES;             // 16-byte pieces of a row, rows of eight lanes
@@ -274,19 +318,19 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 4 : 2)
         copies_commit();
     }
 
-    // ---- which nodes see which: bit u of s_sees[t]
-    if (threadIdx.x < nodes) s_parent[threadIdx.x] = p.parents ? __ldg(p.parents + q0 + threadIdx.x) : (int)threadIdx.x - 1;
+    // ---- which nodes see which
+    if (threadIdx.x < nodes) sh.parent[threadIdx.x] = p.parents ? __ldg(p.parents + q0 + threadIdx.x) : (int)threadIdx.x - 1;
     __syncthreads();
     if (threadIdx.x < nodes) {
         int u = threadIdx.x;
         uint64_t bits = 1ull << u;
         if (!p.parents) bits = bits * 2 - 1;
         else
-            for (int up = s_parent[u]; up >= 0 && up < u; up = s_parent[u]) {
+            for (int up = sh.parent[u]; up >= 0 && up < u; up = sh.parent[u]) {
                 bits |= 1ull << up;
                 u = up;
             }
-        s_sees[threadIdx.x] = bits;
+        sh.sees[threadIdx.x] = bits;
     }
 
     // ---- queries: the products' second operand, columns n of 8, their sums of each 64 dimensions, and the factor of scores
@@ -460,7 +504,7 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 4 : 2)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int node = min((tile * C::ROWS + 8 * nt + 2 * t + e) / p.group, nodes - 1);
-                        const bool sees = real && (j < ctx || (j - ctx < nodes && (s_sees[node] >> (j - ctx) & 1ull)));
+                        const bool sees = real && (j < ctx || (j - ctx < nodes && (sh.sees[node] >> (j - ctx) & 1ull)));
                         if (!sees) {
                             hidden |= 1u << (4 * i + 2 * nt + e);
                             z[i >> 1][nt][2 * (i & 1) + e] = -INFINITY;
@@ -588,94 +632,266 @@ __global__ void __launch_bounds__(kT4Threads, C::NT == 1 ? 4 : 2)
         T* out = static_cast<T*>(p.O) + (q0 + node) * p.o_row + (h * p.group + r % p.group) * p.o_head + d;
         *reinterpret_cast<uint32_t*>(out) = Pair<T>::pack(x * f, y * f);
     };
-    // states of row q from `count` places, each state_of(i)[...]: largest M, and sums weighed by 2^(M_i - M)
-    auto join = [&](auto state_of, int count, int q, int d, float& most, float& sum, float2& v) {
-        most = -INFINITY;
-        for (int i = 0; i < count; ++i) most = fmaxf(most, state_of(i, q * C::PITCH));
-        sum = 0.0f;
-        v = make_float2(0.0f, 0.0f);
-        if (most == -INFINITY) return;
-        for (int i = 0; i < count; ++i) {
-            const float mi = state_of(i, q * C::PITCH);
-            if (mi == -INFINITY) continue;                 // that part saw nothing; its sums are not written
-            const float f = exp2_fast(mi - most);
-            sum = fmaf(f, state_of(i, q * C::PITCH + 1), sum);
-            v.x = fmaf(f, state_of(i, q * C::PITCH + 2 + d), v.x);
-            v.y = fmaf(f, state_of(i, q * C::PITCH + 3 + d), v.y);
-        }
-    };
-    auto of_warp = [&](int i, int at) { return state[i * C::PART + at]; };
-    float* mine = state + kT4Warps * C::PART;
     for (int i = threadIdx.x; i < C::ROWS * PAIRS; i += kT4Threads) {
         const int q = i / PAIRS, d = 2 * (i % PAIRS);
         float most, sum;
         float2 v;
-        join(of_warp, kT4Warps, q, d, most, sum, v);
-        if (plan.cluster == 1) write(q, d, v.x, v.y, sum);
-        else {
-            if (d == 0) {
-                mine[q * C::PITCH] = most;
-                mine[q * C::PITCH + 1] = sum;
-            }
-            *reinterpret_cast<float2*>(mine + q * C::PITCH + 2 + d) = v;
-        }
+        t4_join<C>([&](int i, int at) { return state[i * C::PART + at]; }, kT4Warps, q, d, most, sum, v);
+        out(write, q, d, most, sum, v);
     }
-    if (plan.cluster == 1) return;
-    // ---- and over the cluster, each CTA a share of the outputs
+    return true;
+}
+
+template <class C>
+__global__ void __launch_bounds__(kT4Threads, C::CTAS)
+    gsr_tree4_cluster_kernel(const __grid_constant__ Tree4Params p, const __grid_constant__ Tree4Plan plan) {
+    extern __shared__ __align__(128) char smem[];
+    __shared__ T4Shared sh;
+    constexpr int PAIRS = C::D / 2;
+    const int rank = blockIdx.x % plan.cluster, item = blockIdx.x / plan.cluster;
+    const int tile = item % plan.tiles, h = item / plan.tiles % p.Hkv, b = item / plan.tiles / p.Hkv;
+    float* mine = reinterpret_cast<float*>(smem) + kT4Warps * C::PART;
+    const bool some = t4_part<C>(p, plan, smem, sh, b, h, tile, rank + plan.cluster * (threadIdx.x >> 5), plan.cluster * kT4Warps, INT_MAX,
+               [&](auto write, int q, int d, float most, float sum, float2 v) {
+                   if (plan.cluster == 1) {
+                       write(q, d, v.x, v.y, sum);
+                       return;
+                   }
+                   if (d == 0) *reinterpret_cast<float2*>(mine + q * C::PITCH) = make_float2(most, sum);
+                   *reinterpret_cast<float2*>(mine + q * C::PITCH + 2 + d) = v;
+               });
+    if (plan.cluster == 1 || !some) return;                 // the whole cluster
+    // ---- over the cluster, each CTA a share of the outputs
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const T4Request req = t4_request<C::ROWS>(p, b);
     const uint32_t here = t4_smem(mine);
-    auto of_cta = [&](int i, int at) {
-        uint32_t a;
-        float x;
-        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(here + 4 * at), "r"(i));
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
-        return x;
-    };
     for (int i = rank * kT4Threads + threadIdx.x; i < C::ROWS * PAIRS; i += plan.cluster * kT4Threads) {
-        const int q = i / PAIRS, d = 2 * (i % PAIRS);
-        float most, sum;
-        float2 v;
-        join(of_cta, plan.cluster, q, d, most, sum, v);
-        write(q, d, v.x, v.y, sum);
+        const int q = i / PAIRS, d = 2 * (i % PAIRS), r = tile * C::ROWS + q;
+        // all of the states at once: one trip to the other CTAs
+        float2 ms[kT4MaxCluster], v[kT4MaxCluster];
+#pragma unroll
+        for (int k = 0; k < kT4MaxCluster; ++k) {
+            ms[k] = make_float2(-INFINITY, 0.0f);
+            v[k] = make_float2(0.0f, 0.0f);
+            if (k < plan.cluster) {
+                uint32_t a;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(here + 4 * q * C::PITCH), "r"(k));
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(ms[k].x), "=f"(ms[k].y) : "r"(a) : "memory");
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v[k].x), "=f"(v[k].y) : "r"(a + 8 + 4 * d) : "memory");
+            }
+        }
+        float most = -INFINITY, sum = 0.0f;
+        float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kT4MaxCluster; ++k) most = fmaxf(most, ms[k].x);
+#pragma unroll
+        for (int k = 0; k < kT4MaxCluster; ++k) {
+            if (ms[k].x == -INFINITY) continue;
+            const float f = exp2_fast(ms[k].x - most);
+            sum = fmaf(f, ms[k].y, sum);
+            o.x = fmaf(f, v[k].x, o.x);
+            o.y = fmaf(f, v[k].y, o.y);
+        }
+        if (r >= req.rows) continue;
+        const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+        typename C::T* to = static_cast<typename C::T*>(p.O) + (req.q0 + r / p.group) * p.o_row + (h * p.group + r % p.group) * p.o_head + d;
+        *reinterpret_cast<uint32_t*>(to) = Pair<typename C::T>::pack(o.x * f, o.y * f);
     }
     // no CTA leaves while another reads its states
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Of a grid's CTAs as many as there are units take part.  CTA c's first unit of U, and the CTA that holds unit u.
+__device__ __forceinline__ int t4_busy(long long U, int grid) { return (int)min(U, (long long)grid); }
+__device__ __forceinline__ long long t4_first(long long U, int c, int G) { return U * c / G; }
+__device__ __forceinline__ int t4_cta_of(long long U, long long u, int G) { return (int)(((u + 1) * G - 1) / U); }
+
 template <class C>
-cudaError_t launch_tree4_cfg(const Tree4Params& p, int sms, cudaStream_t stream) {
-    static std::atomic<uint64_t> done{0};                  // devices whose kernel has its shared memory
+__global__ void __launch_bounds__(kT4Threads, C::CTAS)
+    gsr_tree4_even_kernel(const __grid_constant__ Tree4Params p, const __grid_constant__ Tree4Plan plan) {
+    extern __shared__ __align__(128) char smem[];
+    __shared__ T4Shared sh;
+    __shared__ long long s_sums[kT4Warps], s_first[2];
+    grid_launch_next();                                     // the joining CTAs, as SMs fall free
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // ---- this CTA's range of units
+    const int per = (p.B + kT4Threads - 1) / kT4Threads, b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) sum += t4_request<C::ROWS>(p, b).units(p.Hkv);
+    long long upto = sum;                                   // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) s_sums[warp] = upto;
+    __syncthreads();
+    long long U = 0;
+#pragma unroll
+    for (int i = 0; i < kT4Warps; ++i) {
+        if (i < warp) upto += s_sums[i];
+        U += s_sums[i];
+    }
+    const int busy = t4_busy(U, gridDim.x);
+    const bool takes = (int)blockIdx.x < busy;
+    const long long u_begin = takes ? t4_first(U, blockIdx.x, busy) : U, u_end = takes ? t4_first(U, blockIdx.x + 1, busy) : U;
+    long long before = upto - sum;
+    for (int b = b0; b < b1; ++b) {
+        const long long units = t4_request<C::ROWS>(p, b).units(p.Hkv);
+        if (blockIdx.x == 0) p.unit_starts[b] = before;     // for the joining launch
+        if (before <= u_begin && u_begin < before + units) {
+            s_first[0] = b;
+            s_first[1] = u_begin - before;
+        }
+        before += units;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == kT4Threads - 1) p.unit_starts[p.B] = U;
+    __syncthreads();
+    int b = takes ? (int)s_first[0] : p.B;
+    long long off = takes ? s_first[1] : 0;
+    for (long long u = u_begin; u < u_end && b < p.B;) {
+        const T4Request req = t4_request<C::ROWS>(p, b);
+        if (off >= req.units(p.Hkv)) {                      // the range goes on in a later request
+            off = 0;
+            ++b;
+            continue;
+        }
+        const int chunks = max(req.chunks, 1), index = (int)(off / chunks), h = index / req.tiles, tile = index - h * req.tiles;
+        const int c0 = (int)(off - (long long)index * chunks), c1 = (int)min((long long)chunks, c0 + (u_end - u));
+        const bool all = c0 == 0 && c1 == chunks;
+        float* slot = p.parts + (2ll * blockIdx.x + (u > u_begin ? 1 : 0)) * C::PART;
+        t4_part<C>(p, plan, smem, sh, b, h, tile, c0 + warp, kT4Warps, c1, [&](auto write, int q, int d, float most, float sum, float2 v) {
+            if (all) {
+                write(q, d, v.x, v.y, sum);
+                return;
+            }
+            if (d == 0) *reinterpret_cast<float2*>(slot + q * C::PITCH) = make_float2(most, sum);
+            *reinterpret_cast<float2*>(slot + q * C::PITCH + 2 + d) = v;
+        });
+        u += c1 - c0;
+        off += c1 - c0;
+        __syncthreads();                                    // the states have been read: the ring is free
+    }
+}
+
+// A query row and head of an item that several CTAs share, by WARPS warps: the states in the order of the CTAs, warp by
+// warp, then the warps'.
+template <class C, int WARPS>
+__global__ void __launch_bounds__(128) gsr_tree4_join_kernel(const __grid_constant__ Tree4Params p, int grid) {
+    using T = typename C::T;
+    constexpr int D = C::D, E = D / 32, ROWS = 4 / WARPS;
+    __shared__ float sm[4][D + 2];
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS;
+    const long long id = (long long)blockIdx.x * ROWS + (threadIdx.x >> 5) / WARPS;
+    const int row = (int)min(id / p.Hq, (long long)p.total_q), h = (int)(id % p.Hq), hk = h / p.group;
+    int left = 0, right = p.B;                              // first request that ends behind the row
+    while (left < right) {
+        const int mid = (left + right) >> 1;
+        if (__ldg(p.q_starts + mid + 1) <= row) left = mid + 1;
+        else right = mid;
+    }
+    const int b = min(left, p.B - 1);
+    const T4Request req = t4_request<C::ROWS>(p, b);
+    const int t = row - req.q0, r = t * p.group + h - hk * p.group, tile = r / C::ROWS, chunks = max(req.chunks, 1);
+    grid_wait();                                            // every CTA: this launch then ends after the parts'
+    bool mine = row < p.total_q && left < p.B && t >= 0 && t < req.nodes;
+    int c0 = 0, c1 = 0;
+    long long s = 0, U = p.unit_starts[p.B];
+    const int busy = t4_busy(U, grid);
+    if (mine) {
+        s = p.unit_starts[b] + ((long long)hk * req.tiles + tile) * chunks;
+        c0 = max(t4_cta_of(U, s, busy), 0);
+        c1 = min(t4_cta_of(U, s + chunks - 1, busy), busy - 1);
+        mine = c0 < c1;                                     // else written whole
+    }
+    float m = -INFINITY, l = 0.0f, acc[E] = {};
+    auto add = [&](float pm, float pl, const float* o) {
+        if (pm == -INFINITY) return;                        // saw nothing
+        const float next = fmaxf(m, pm), f0 = m == -INFINITY ? 0.0f : exp2_fast(m - next), f1 = exp2_fast(pm - next);
+        l = m == -INFINITY ? pl * f1 : l * f0 + pl * f1;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = m == -INFINITY ? o[e] * f1 : acc[e] * f0 + o[e] * f1;
+        m = next;
+    };
+    if (mine)
+        for (int c = c0 + warp; c <= c1; c += WARPS) {
+            const float* at = p.parts + (2ll * c + (t4_first(U, c, busy) < s ? 1 : 0)) * C::PART + (r - tile * C::ROWS) * C::PITCH;
+            float x[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = at[2 + lane * E + e];
+            add(at[0], at[1], x);
+        }
+    if (WARPS > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sm[warp][lane * E + e] = acc[e];
+        if (lane == 0) {
+            sm[warp][D] = m;
+            sm[warp][D + 1] = l;
+        }
+        __syncthreads();
+        if (warp != 0) return;
+#pragma unroll
+        for (int i = 1; i < WARPS; ++i) add(sm[i][D], sm[i][D + 1], &sm[i][lane * E]);
+    }
+    if (!mine) return;
+    const float f = l == 0.0f ? 0.0f : 1.0f / l;
+    uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<T*>(p.O) + row * p.o_row + h * p.o_head + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) to[e / 2] = Pair<T>::pack(acc[e] * f, acc[e + 1] * f);
+}
+
+// Shared memory that a kernel may use, said once a device.
+template <class K>
+cudaError_t t4_allow(K kernel, int bytes, std::atomic<uint64_t>& done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev > 63 || !(done.load(std::memory_order_acquire) >> dev & 1)) {
-        if ((e = cudaFuncSetAttribute(gsr_tree4_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
-        if (dev <= 63) done.fetch_or(1ull << dev, std::memory_order_release);
-    }
-    Tree4Plan plan{Divider((uint32_t)p.page), (p.max_nodes * p.group + C::ROWS - 1) / C::ROWS, 1, 0};
-    const long long items = (long long)p.B * p.Hkv * plan.tiles;
-    const long long chunks = ((long long)p.table_width * p.page + kT4Keys - 1) / kT4Keys;
-    plan.chunks = (int)chunks;
-    while (plan.cluster < 8 && items * plan.cluster < 8ll * sms && chunks > (long long)plan.cluster * kT4Warps) plan.cluster *= 2;
+    if (e != cudaSuccess || (dev <= 63 && (done.load(std::memory_order_acquire) >> dev & 1))) return e;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+    if (dev <= 63) done.fetch_or(1ull << dev, std::memory_order_release);
+    return cudaSuccess;
+}
+
+template <class C>
+cudaError_t launch_tree4_cfg(const Tree4Params& p, const Tree4Split& split, cudaStream_t stream) {
+    static std::atomic<uint64_t> cluster_done{0}, even_done{0};
+    static_assert(C::CTAS == Tree4Split::ctas_an_sm(C::NT) && C::ROWS == 8 * C::NT && C::PART * 4 == Tree4Split::state_bytes(C::NT, C::D), "");
+    cudaError_t e;
+    const Tree4Plan plan{Divider((uint32_t)p.page), split.tiles, split.cluster, split.chunks};
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)plan.cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(items * plan.cluster));
+    cudaLaunchAttribute attr;
+    cfg.gridDim = dim3((unsigned)split.grid);
     cfg.blockDim = dim3(kT4Threads);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
-    cfg.attrs = attr;
+    if (split.cluster) {
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)split.cluster;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if ((e = t4_allow(gsr_tree4_cluster_kernel<C>, C::SMEM, cluster_done)) != cudaSuccess) return e;
+        return cudaLaunchKernelEx(&cfg, gsr_tree4_cluster_kernel<C>, p, plan);
+    }
+    if ((e = t4_allow(gsr_tree4_even_kernel<C>, C::SMEM, even_done)) != cudaSuccess ||
+        (e = cudaLaunchKernelEx(&cfg, gsr_tree4_even_kernel<C>, p, plan)) != cudaSuccess)
+        return e;
+    // the joining CTAs start while the parts' last CTAs finish, and wait for them there
+    const long long rows = (long long)p.total_q * p.Hq;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gsr_tree4_kernel<C>, p, plan);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    cfg.gridDim = dim3((unsigned)(rows >= 2048 ? (rows + 3) / 4 : rows));
+    return rows >= 2048 ? cudaLaunchKernelEx(&cfg, gsr_tree4_join_kernel<C, 1>, p, split.grid)
+                        : cudaLaunchKernelEx(&cfg, gsr_tree4_join_kernel<C, 4>, p, split.grid);
 }
 
 template <class T>
-cudaError_t launch_tree4_type(const Tree4Params& p, int sms, cudaStream_t stream) {
-    const bool wide = p.max_nodes * p.group > 8;           // more rows than one column tile holds
-    if (p.D == 64) return wide ? launch_tree4_cfg<T4Cfg<T, 64, 2>>(p, sms, stream) : launch_tree4_cfg<T4Cfg<T, 64, 1>>(p, sms, stream);
-    return wide ? launch_tree4_cfg<T4Cfg<T, 128, 2>>(p, sms, stream) : launch_tree4_cfg<T4Cfg<T, 128, 1>>(p, sms, stream);
+cudaError_t launch_tree4_type(const Tree4Params& p, const Tree4Split& split, cudaStream_t stream) {
+    if (p.D == 64) return split.nt == 2 ? launch_tree4_cfg<T4Cfg<T, 64, 2>>(p, split, stream) : launch_tree4_cfg<T4Cfg<T, 64, 1>>(p, split, stream);
+    return split.nt == 2 ? launch_tree4_cfg<T4Cfg<T, 128, 2>>(p, split, stream) : launch_tree4_cfg<T4Cfg<T, 128, 1>>(p, split, stream);
 }
 
 }  // namespace

@@ -3,6 +3,6 @@
 
 namespace gsr {
 
-cudaError_t launch_tree4_bf16(const Tree4Params& p, int sms, cudaStream_t stream) { return launch_tree4_type<__nv_bfloat16>(p, sms, stream); }
+cudaError_t launch_tree4_bf16(const Tree4Params& p, const Tree4Split& split, cudaStream_t stream) { return launch_tree4_type<__nv_bfloat16>(p, split, stream); }
 
 }  // namespace gsr

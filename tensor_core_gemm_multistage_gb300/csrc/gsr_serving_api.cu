@@ -211,6 +211,17 @@ gsr_status append_rope(const gsr_rope_desc* d, const gsr_tensor* Q, const gsr_te
     return launched(gsr::launch_rope_append(p, d->dtype == GSR_BF16, cache16 == nullptr, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+gsr_status check_tree4_desc(const gsr_tree_desc* desc) {
+    const gsr_status s = check_tree_desc(desc);
+    if (s != GSR_OK) return s;
+    if (desc->alibi_slopes) return GSR_ERR_INVALID_ARG;
+    // CTAs are counted in int, eight an item at most
+    return (double)desc->batch * (double)desc->heads_q * (double)desc->max_nodes > INT_MAX / 8 ? GSR_ERR_INVALID_ARG : GSR_OK;
+}
+gsr::Tree4Split tree4_split(const gsr_tree_desc& d) {
+    return gsr::tree4_split(d.batch, d.heads_kv, d.heads_q / d.heads_kv, d.head_dim, d.max_nodes, d.table_width, d.page_size, (int)kSms);
+}
+
 int64_t rope_bwd_bytes(const gsr_rope_desc* d, int* ctas) {
     *ctas = gsr::rope_bwd_ctas(d->batch, d->heads_q, d->heads_kv, d->seq, (int)d->head_dim, (int)kSms);
     return (int64_t)2 * *ctas * d->head_dim * 4;
@@ -350,16 +361,15 @@ gsr_status kv_cache4_read(const gsr_cache4* k_cache, const gsr_cache4* v_cache, 
 
 gsr_status tree_attention4_fwd(const gsr_tree_desc* desc, const void* Q, const gsr_cache4* k_cache, const gsr_cache4* v_cache,
                                const int32_t* block_tables, const int32_t* kv_lens, const int32_t* q_starts, const int32_t* parents,
-                               void* O, CUstream_st* stream) {
-    gsr_status s = check_tree_desc(desc);
+                               void* O, void* workspace, int64_t workspace_bytes, CUstream_st* stream) {
+    gsr_status s = check_tree4_desc(desc);
     if (s != GSR_OK) return s;
     const gsr_tree_desc& d = *desc;
-    if (d.alibi_slopes) return GSR_ERR_INVALID_ARG;
-    // CTAs are counted in int, eight an item at most
-    if ((double)d.batch * (double)d.heads_q * (double)d.max_nodes > INT_MAX / 8) return GSR_ERR_INVALID_ARG;
     if (d.batch == 0 || d.total_q == 0 || d.heads_q == 0) return GSR_OK;
     if (!Q || !O || !kv_lens || !q_starts || (d.table_width > 0 && !block_tables)) return GSR_ERR_INVALID_ARG;
-    if (misaligned(Q, 16) || misaligned(O, 16)) return GSR_ERR_ALIGNMENT;
+    if (misaligned(Q, 16) || misaligned(O, 16) || misaligned(workspace, 16)) return GSR_ERR_ALIGNMENT;
+    const gsr::Tree4Split split = tree4_split(d);
+    if (workspace && workspace_bytes < split.workspace) return GSR_ERR_INVALID_ARG;
     for (const void* a : {(const void*)kv_lens, (const void*)q_starts, (const void*)parents, (const void*)block_tables})
         if (misaligned(a, 4)) return GSR_ERR_ALIGNMENT;
     gsr::Tree4Params p{};
@@ -376,12 +386,14 @@ gsr_status tree_attention4_fwd(const gsr_tree_desc* desc, const void* Q, const g
             if (t->page > UINT32_MAX || t->row > UINT32_MAX) return GSR_ERR_INVALID_ARG;
     const Span o = span_of(os, 1, d.heads_q, d.total_q, d.head_dim, 2);
     if (share(os, 1, d.heads_q, d.total_q, qs, 1, d.heads_q, d.total_q, d.head_dim)) return GSR_ERR_ALIAS;
+    const Span ws = words(workspace, split.workspace / 4);
+    if (meet(ws, o) || meet(ws, span_of(qs, 1, d.heads_q, d.total_q, d.head_dim, 2))) return GSR_ERR_ALIAS;
     for (const CacheCheck* c : {&ck, &cv})
         for (const Span& x : spans_of(*c, d.num_pages, d.heads_kv, d.page_size, d.head_dim).s)
-            if (meet(o, x)) return GSR_ERR_ALIAS;
+            if (meet(o, x) || meet(ws, x)) return GSR_ERR_ALIAS;
     for (const Span& in : {words(kv_lens, d.batch), words(q_starts, d.batch + 1), words(parents, d.total_q),
                            words(block_tables, d.batch * d.table_width)})
-        if (meet(o, in)) return GSR_ERR_ALIAS;
+        if (meet(o, in) || meet(ws, in)) return GSR_ERR_ALIAS;
     int dev = 0, sms = 0;
     if ((s = current_device(&dev, &sms)) != GSR_OK) return s;
     p.B = (int)d.batch;
@@ -410,7 +422,19 @@ gsr_status tree_attention4_fwd(const gsr_tree_desc* desc, const void* Q, const g
         p.K = p.V = gsr::Cache4{none, none};
     }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return launched(d.dtype == GSR_BF16 ? gsr::launch_tree4_bf16(p, sms, st) : gsr::launch_tree4_f16(p, sms, st));
+    std::unique_lock<std::mutex> lock(g_scratch_mu, std::defer_lock);
+    if (!workspace && split.workspace > 0) {
+        lock.lock();
+        if ((s = stream_scratch(dev, st, (size_t)split.workspace, &workspace)) != GSR_OK) return s;
+    }
+    p.unit_starts = static_cast<long long*>(workspace);
+    p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + split.starts);
+    return launched(d.dtype == GSR_BF16 ? gsr::launch_tree4_bf16(p, split, st) : gsr::launch_tree4_f16(p, split, st));
+}
+
+int64_t tree_attention4_workspace(const gsr_tree_desc* desc) {
+    if (check_tree4_desc(desc) != GSR_OK) return -1;
+    return desc->heads_q > 0 && desc->batch > 0 ? tree4_split(*desc).workspace : 0;
 }
 
 gsr_status verify_drafts(const gsr_verify_desc* desc, const float* target_probs, const float* draft_probs, const int32_t* draft_tokens,

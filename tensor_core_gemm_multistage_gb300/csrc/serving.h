@@ -72,9 +72,53 @@ struct Tree4Params {
     long long o_row, o_head;
     Cache4 K, V;
     const int *table, *kv_lens, *q_starts, *parents;
+    long long* unit_starts;            // workspace, where work is shared out evenly: (B + 1) first units,
+    float* parts;                      // and two states a CTA
 };
-cudaError_t launch_tree4_f16(const Tree4Params& p, int sms, cudaStream_t stream);
-cudaError_t launch_tree4_bf16(const Tree4Params& p, int sms, cudaStream_t stream);
+
+// How the work of attention over 4 bits is split, by sizes alone.
+constexpr int kT4Warps = 4, kT4Keys = 32, kT4MaxCluster = 8;
+struct Tree4Split {
+    int nt, tiles;                     // column tiles of 8 query rows a CTA; row tiles a request and head
+    int cluster, grid, chunks;         // CTAs that share an item (0: shared out evenly); CTAs; chunks a table's row holds
+    long long starts, workspace;       // bytes
+    static constexpr int ctas_an_sm(int nt) { return nt == 1 ? 4 : 2; }
+    static constexpr int state_bytes(int nt, int D) { return 8 * nt * (D + 2) * 4; }
+};
+// A cluster an item, or all chunks shared out evenly, whichever the estimate has sooner: a chunk takes the whole GPU
+// 0.9 ns (1.4 of 16 rows; D = 64: about half), a wave of clusters 6 us more, sharing out 9 us (its second launch
+// and the sums).  Lengths are taken as the most that the table holds.  In clusters and evenly (us; batch, key/value
+// heads, tokens, rows a head):
+//   TODO
+inline Tree4Split tree4_split(long long B, long long Hkv, long long group, long long D, long long max_nodes, long long table_width,
+                              long long page, int sms) {
+    Tree4Split s{};
+    s.nt = max_nodes * group > 8 ? 2 : 1;
+    const long long rows = 8 * s.nt, chunks = (table_width * page + kT4Keys - 1) / kT4Keys;
+    s.tiles = (int)((max_nodes * group + rows - 1) / rows);
+    s.chunks = (int)chunks;
+    const double items = (double)B * (double)Hkv * s.tiles, slots = (double)(Tree4Split::ctas_an_sm(s.nt) * sms);
+    const double work = items * (double)(chunks > 0 ? chunks : 1) * (s.nt == 1 ? 0.9e-3 : 1.4e-3) * (D == 64 ? 0.55 : 1.0);     // us
+    double best = 1e30;
+    for (int c = 1; c <= kT4MaxCluster; c *= 2) {
+        if (c > 1 && chunks <= (long long)c / 2 * kT4Warps) break;
+        const double ctas = items * c, waves = (double)(long long)((ctas + slots - 1) / slots), t = waves * (work * slots / ctas + 6.0);
+        if (t < best) {
+            best = t;
+            s.cluster = c;
+            s.grid = (int)ctas;
+        }
+    }
+    if (9.0 + work < best) {
+        s.cluster = 0;
+        s.grid = (int)slots;
+        s.starts = ((B + 1) * 8 + 255) / 256 * 256;
+        s.workspace = s.starts + 2ll * s.grid * Tree4Split::state_bytes(s.nt, (int)D);
+    }
+    return s;
+}
+cudaError_t launch_tree4_f16(const Tree4Params& p, const Tree4Split& split, cudaStream_t stream);
+cudaError_t launch_tree4_bf16(const Tree4Params& p, const Tree4Split& split, cudaStream_t stream);
 
 struct VerifyParams {
     int B, N, V, max_nodes;

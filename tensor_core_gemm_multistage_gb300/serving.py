@@ -53,7 +53,9 @@ def _declare(L) -> None:
     L.kv_cache4_read.restype = i32
     L.kv_cache4_read.argtypes = [c4, c4, vp, ts, ts] + [i64] * 5 + [ctypes.c_int32, vp]
     L.tree_attention4_fwd.restype = i32
-    L.tree_attention4_fwd.argtypes = [ctypes.POINTER(_TreeDesc), vp, c4, c4] + [vp] * 6
+    L.tree_attention4_fwd.argtypes = [ctypes.POINTER(_TreeDesc), vp, c4, c4] + [vp] * 6 + [i64, vp]
+    L.tree_attention4_workspace.restype = i64
+    L.tree_attention4_workspace.argtypes = [ctypes.POINTER(_TreeDesc)]
     L.verify_drafts.restype = i32
     L.verify_drafts.argtypes = [ctypes.POINTER(_VerifyDesc)] + [vp] * 11
 
@@ -245,10 +247,11 @@ def kv_cache4_read(k_cache, v_cache, slots, K, V, stream=None):
 
 
 def tree_attention4_fwd(Q, k_cache, v_cache, block_tables, kv_lens, q_starts, parents, O, max_nodes: int,
-                        softmax_scale: float = 0.0, softcap: float = 0.0, stream=None):
+                        softmax_scale: float = 0.0, softcap: float = 0.0, workspace=None, stream=None):
     """tree_attention_fwd over caches of 4 bits (Cache4, or pairs of their tensors); returns O.
 
-    Q, O (N, Hq, D) of the params' type; the other arguments as there.  No distance bias, no workspace.
+    Q, O (N, Hq, D) of the params' type; the other arguments as there, without a distance bias.  ``workspace``: as for
+    masked_attention_fwd, tree_attention4_workspace bytes (0 for little work).
     """
     code, dev, dt, i32 = _dtype_code(Q, "Q"), Q.get_device(), Q.dtype, torch.int32
     if Q.dim() != 3 or dev < 0:
@@ -267,11 +270,24 @@ def tree_attention4_fwd(Q, k_cache, v_cache, block_tables, kv_lens, q_starts, pa
         raise ValueError("block_tables must be (requests, width)")
     B, W = block_tables.shape
     d = _TreeDesc(B, N, Hq, heads, D, pages, page, W, max_nodes, qr, qh, orow, oh, code, softmax_scale, softcap, None)
-    _call(dev, stream, "tree_attention4_fwd", lib().tree_attention4_fwd, d, Q.data_ptr() or None,
+    L, scratch, size = lib(), None, 0
+    need = L.tree_attention4_workspace(d)
+    if need > 0 or workspace is not None:
+        ws, scratch, size = _scratch(workspace, lambda: need, dev, stream)
+    _call(dev, stream, "tree_attention4_fwd", L.tree_attention4_fwd, d, Q.data_ptr() or None,
           _cache4(k_cache, "k_cache", cache, dt, dev), _cache4(v_cache, "v_cache", cache, dt, dev),
           _vector(block_tables, "block_tables", B * W, i32, dev), _vector(kv_lens, "kv_lens", B, i32, dev),
-          _vector(q_starts, "q_starts", B + 1, i32, dev), _vector(parents, "parents", N, i32, dev), O.data_ptr() or None)
+          _vector(q_starts, "q_starts", B + 1, i32, dev), _vector(parents, "parents", N, i32, dev), O.data_ptr() or None,
+          scratch, size)
     return O
+
+
+def tree_attention4_workspace(B: int, N: int, Hq: int, Hkv: int, D: int, pages: int, page_size: int, W: int, max_nodes: int) -> int:
+    """Bytes of workspace a tree_attention4_fwd call of these sizes needs; 0 for little work."""
+    n = lib().tree_attention4_workspace(_TreeDesc(B, N, Hq, Hkv, D, pages, page_size, W, max_nodes))
+    if n < 0:
+        raise GsrError(Status.ERR_INVALID_ARG, "tree_attention4_workspace")
+    return n
 
 
 def _probs(t, name, N, V, index):

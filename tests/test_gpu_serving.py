@@ -423,14 +423,14 @@ def test_read_is_what_the_codes_stand_for():
 
 class Tree4:
     def __init__(self, kv, T, Hq, Hkv, D, page, dtype=F16, cap=0.0, parents="random", seed=0, scale=0.0, layout="heads", extra_rows=0,
-                 v_scale=1.0, k_shift=0.0):
+                 v_scale=1.0, k_shift=0.0, width=0):
         r, g = np.random.default_rng(seed + 5), torch.Generator().manual_seed(seed)
         self.kv, self.T, self.page, self.dtype, self.D = kv, T, page, dtype, D
         B = len(kv)
         need = [-(-n // page) for n in kv]
         pool = sum(need) + 3
         order = [int(x) for x in r.permutation(pool)]
-        self.table = np.full((B, max(need + [1]) + 1), -1)
+        self.table = np.full((B, max(need + [1, width]) + 1), -1)
         at = 0
         for b in range(B):
             self.table[b, :need[b]] = order[at:at + need[b]]
@@ -451,12 +451,16 @@ class Tree4:
             self.parents = [-1] * N
         self.cap, self.scale, self.max_nodes = cap, scale, max(T + [1])
 
-    def run(self, stream=None):
+    def workspace(self):
+        return gsr.tree_attention4_workspace(len(self.kv), self.N, self.q.shape[1], self.caches[0].codes.shape[2], self.D, self.caches[0].codes.shape[0],
+                                             self.page, self.table.shape[1], self.max_nodes)
+
+    def run(self, stream=None, **kw):
         self.o = torch.full_like(self.q, 7.0)
         self.args = (self.q, *self.caches, i32(self.table), i32(self.kv), i32(self.starts),
                      None if self.parents is None else i32(self.parents), self.o, self.max_nodes)
         self.kw = dict(softmax_scale=self.scale, softcap=self.cap)
-        gsr.tree_attention4_fwd(*self.args, **self.kw, stream=stream)
+        gsr.tree_attention4_fwd(*self.args, **self.kw, stream=stream, **kw)
         return self
 
     def want(self):
@@ -504,9 +508,13 @@ TREES = {
 }
 
 
+@pytest.mark.parametrize("even", [False, True])
 @pytest.mark.parametrize("name", TREES)
-def test_tree_attention4(name):
-    Tree4(**TREES[name]).run().check()
+def test_tree_attention4(name, even):
+    """In clusters, and shared out evenly: a table that could hold much is taken for much work."""
+    t = Tree4(**TREES[name], width=2 ** 21 // TREES[name]["page"] if even else 0)
+    assert (t.workspace() > 0) == (even or name == "decode_long")
+    t.run().check()
 
 
 def _random_trees(n, seed):
@@ -523,9 +531,50 @@ def _random_trees(n, seed):
     return out
 
 
+@pytest.mark.parametrize("even", [False, True])
 @pytest.mark.parametrize("c", _random_trees(14, 12))
-def test_random_trees4(c):
-    Tree4(**c).run().check()
+def test_random_trees4(c, even):
+    Tree4(**c, width=2 ** 21 // c["page"] if even else 0).run().check()
+
+
+def test_many_requests_shared_out_evenly():
+    """More requests than a CTA has threads, some without keys or rows; and one long request among them."""
+    r = np.random.default_rng(1)
+    T = [int(x) for x in r.integers(0, 4, 700)]
+    t = Tree4(kv=[n + int(x) for n, x in zip(T, r.integers(0, 90, 700))], T=T, Hq=8, Hkv=2, D=64, page=16, width=4000)
+    assert t.workspace() > 0
+    t.run().check()
+    Tree4(kv=[70000] + [5] * 30, T=[1] * 31, Hq=8, Hkv=2, D=128, page=64, dtype=BF16).run().check()
+
+
+def test_workspaces():
+    t = Tree4(kv=[3000, 77], T=[1, 9], Hq=8, Hkv=2, D=128, page=16, width=2 ** 17).run().check()
+    want, size = t.o.clone(), t.workspace()
+    assert size > 0
+    own = torch.full((size + 64,), 255, dtype=torch.uint8, device=DEV)
+    assert torch.equal(t.run(workspace=own[:size]).o, want) and torch.all(own[size:] == 255)
+    with pytest.raises(gsr.GsrError):
+        t.run(workspace=own[:size - 16])
+    s = torch.cuda.Stream(DEV)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        t.o.fill_(7.0)
+        torch.cuda.synchronize()
+        gsr.tree_attention4_fwd(*t.args, **t.kw, stream=s)
+        s.synchronize()
+        assert torch.equal(t.o, want)
+        gsr.release_stream(s)
+    # a graph takes a workspace of its own: replays beside eager calls of the same stream's
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gsr.tree_attention4_fwd(*t.args, **t.kw)
+    for _ in range(3):
+        t.o.fill_(7.0)
+        graph.replay()
+        assert torch.equal(t.o, want)
+        other = torch.empty_like(t.o)
+        gsr.tree_attention4_fwd(*t.args[:7], other, t.args[8], **t.kw)
+        assert torch.equal(other, want)
 
 
 def test_keys_nothing_sees_have_no_influence():
@@ -579,9 +628,10 @@ def test_pages_outside_the_pool_and_lengths_that_are_cut():
 
 def test_repeatable_and_on_two_streams_at_once():
     ts = [Tree4(kv=[5000, 300, 77], T=[1, 8, 30], Hq=8, Hkv=2, D=128, page=16, seed=1),
+          Tree4(kv=[5000, 300, 77], T=[1, 8, 30], Hq=8, Hkv=2, D=128, page=16, seed=1, width=2 ** 17),
           Tree4(kv=[900] * 9, T=[2] * 9, Hq=16, Hkv=4, D=64, page=32, dtype=BF16, seed=2)]
     first = [t.run().o.clone() for t in ts]
-    streams = [torch.cuda.Stream(DEV), torch.cuda.Stream(DEV)]
+    streams = [torch.cuda.Stream(DEV) for _ in ts]
     torch.cuda.synchronize()
     for _ in range(4):
         for t, s in zip(ts, streams):

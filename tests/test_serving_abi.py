@@ -152,11 +152,11 @@ def test_read_refusals(accepted):
     assert read(K=_Tensor(GB * 21 // 4, 0, 64, 128)) == ALIAS and read(K=_Tensor(8 * GB, 0, 64, 128)) == ALIAS
 
 
-def tree(desc=None, q=1 * GB, k=None, v=None, table=6 * GB, lens=7 * GB, starts=8 * GB, parents=9 * GB, o=3 * GB):
+def tree(desc=None, q=1 * GB, k=None, v=None, table=6 * GB, lens=7 * GB, starts=8 * GB, parents=9 * GB, o=3 * GB, ws=None, ws_bytes=0):
     d = dict(batch=2, total_q=6, heads_q=4, heads_kv=2, head_dim=64, num_pages=10, page_size=16, table_width=5,
              max_nodes=3, q_stride_row=256, q_stride_head=64, o_stride_row=256, o_stride_head=64)
     d.update(desc or {})
-    return gsr.lib().tree_attention4_fwd(_TreeDesc(**d), q, k or cache4(4 * GB), v or cache4(5 * GB), table, lens, starts, parents, o, None)
+    return gsr.lib().tree_attention4_fwd(_TreeDesc(**d), q, k or cache4(4 * GB), v or cache4(5 * GB), table, lens, starts, parents, o, ws, ws_bytes, None)
 
 
 def test_tree4_refusals(accepted):
