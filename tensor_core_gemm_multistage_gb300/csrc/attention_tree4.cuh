@@ -531,7 +531,8 @@ __device__ __forceinline__ bool t4_part(const Tree4Params& p, const Tree4Plan& p
                 for (int e = 0; e < 2; ++e) {
 #pragma unroll
                     for (int s = 4; s < 32; s <<= 1) top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], s));
-                    const float next = fmaxf(base[nt][e], top[nt][e] - 6.0f), f = exp2_fast(base[nt][e] - next);
+                    // by the query's own scores alone: no other query has a say in its roundings
+                    const float next = top[nt][e] > base[nt][e] + 14.0f ? top[nt][e] - 6.0f : base[nt][e], f = exp2_fast(base[nt][e] - next);
                     base[nt][e] = next;
                     l[nt][e] *= f;
 #pragma unroll
@@ -701,8 +702,8 @@ __global__ void __launch_bounds__(kT4Threads, C::CTAS)
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Of a grid's CTAs as many as there are units take part.  CTA c's first unit of U, and the CTA that holds unit u.
-__device__ __forceinline__ int t4_busy(long long U, int grid) { return (int)min(U, (long long)grid); }
+// Of a grid's CTAs as many take part as have eight units, two chunks a warp, or one.  CTA c's first unit of U, and the CTA that holds unit u.
+__device__ __forceinline__ int t4_busy(long long U, int grid) { return (int)max(min(U / 8, (long long)grid), min(U, 1ll)); }
 __device__ __forceinline__ long long t4_first(long long U, int c, int G) { return U * c / G; }
 __device__ __forceinline__ int t4_cta_of(long long U, long long u, int G) { return (int)(((u + 1) * G - 1) / U); }
 
@@ -779,7 +780,7 @@ __global__ void __launch_bounds__(kT4Threads, C::CTAS)
 template <class C, int WARPS>
 __global__ void __launch_bounds__(128) gsr_tree4_join_kernel(const __grid_constant__ Tree4Params p, int grid) {
     using T = typename C::T;
-    constexpr int D = C::D, E = D / 32, ROWS = 4 / WARPS;
+    constexpr int D = C::D, E = D / 32, ROWS = 4 / WARPS, AHEAD = WARPS > 1 ? 8 : 2;
     __shared__ float sm[4][D + 2];
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS;
     const long long id = (long long)blockIdx.x * ROWS + (threadIdx.x >> 5) / WARPS;
@@ -796,13 +797,15 @@ __global__ void __launch_bounds__(128) gsr_tree4_join_kernel(const __grid_consta
     grid_wait();                                            // every CTA: this launch then ends after the parts'
     bool mine = row < p.total_q && left < p.B && t >= 0 && t < req.nodes;
     int c0 = 0, c1 = 0;
-    long long s = 0, U = p.unit_starts[p.B];
+    bool starts_later = false;                              // the item does, than its first CTA's range
+    const long long U = p.unit_starts[p.B];
     const int busy = t4_busy(U, grid);
     if (mine) {
-        s = p.unit_starts[b] + ((long long)hk * req.tiles + tile) * chunks;
+        const long long s = p.unit_starts[b] + ((long long)hk * req.tiles + tile) * chunks;
         c0 = max(t4_cta_of(U, s, busy), 0);
         c1 = min(t4_cta_of(U, s + chunks - 1, busy), busy - 1);
         mine = c0 < c1;                                     // else written whole
+        starts_later = t4_first(U, c0, busy) < s;
     }
     float m = -INFINITY, l = 0.0f, acc[E] = {};
     auto add = [&](float pm, float pl, const float* o) {
@@ -814,12 +817,26 @@ __global__ void __launch_bounds__(128) gsr_tree4_join_kernel(const __grid_consta
         m = next;
     };
     if (mine)
-        for (int c = c0 + warp; c <= c1; c += WARPS) {
-            const float* at = p.parts + (2ll * c + (t4_first(U, c, busy) < s ? 1 : 0)) * C::PART + (r - tile * C::ROWS) * C::PITCH;
-            float x[E];
+        for (int first = c0 + warp; first <= c1; first += WARPS * AHEAD) {
+            float2 ml[AHEAD];
+            float x[AHEAD][E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = at[2 + lane * E + e];
-            add(at[0], at[1], x);
+            for (int k = 0; k < AHEAD; ++k) {               // all loads, then the sums in order
+                const int c = first + k * WARPS;
+                ml[k] = make_float2(-INFINITY, 0.0f);
+                if (c > c1) continue;
+                // an item that starts behind the CTA's first unit has its second slot
+                const float* at = p.parts + (2ll * c + (c == c0 && starts_later ? 1 : 0)) * C::PART + (r - tile * C::ROWS) * C::PITCH;
+                ml[k] = *reinterpret_cast<const float2*>(at);
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float2 v = *reinterpret_cast<const float2*>(at + 2 + lane * E + e);
+                    x[k][e] = v.x;
+                    x[k][e + 1] = v.y;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) add(ml[k].x, ml[k].y, x[k]);
         }
     if (WARPS > 1) {
 #pragma unroll

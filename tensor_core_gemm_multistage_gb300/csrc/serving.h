@@ -3,6 +3,9 @@
 // installed; not part of the ABI.
 #pragma once
 
+#include <algorithm>
+#include <cmath>
+
 #include "divider.h"
 #include "llm.h"
 
@@ -85,11 +88,16 @@ struct Tree4Split {
     static constexpr int ctas_an_sm(int nt) { return nt == 1 ? 4 : 2; }
     static constexpr int state_bytes(int nt, int D) { return 8 * nt * (D + 2) * 4; }
 };
-// A cluster an item, or all chunks shared out evenly, whichever the estimate has sooner: a chunk takes the whole GPU
-// 0.9 ns (1.4 of 16 rows; D = 64: about half), a wave of clusters 6 us more, sharing out 9 us (its second launch
-// and the sums).  Lengths are taken as the most that the table holds.  In clusters and evenly (us; batch, key/value
-// heads, tokens, rows a head):
-//   TODO
+// A cluster an item, or all chunks shared out evenly, whichever the estimate has sooner, lengths taken as the most that
+// the table holds.  A warp takes 0.9 us a chunk by itself and 2.3 us on a full SM (16 rows: 1.5 and 1.7; D = 64: 0.55 of
+// it); a wave of clusters costs 5 us more, of single CTAs 4; sharing out 11 us and 4 for each item of a CTA, and with
+// two items for every CTA it has nothing left to even out.  Measured, us (requests, key/value heads, tokens to;
+// rows a head, D = 128), in clusters of 1, 2, 4, 8, evenly:
+//   1, 8, 2000; 4       17.8  12.5   9.0   7.1   12.4        48, 8, 500; 4      11.9  17.3  21.6  37.8   20.5
+//   1, 8, 32000; 4     210   109    59    32.5   18.2        48, 8, 2000; 4     30.4  33.6  36.3  49.1   33.3
+//   4, 8, 8000; 4       56.6  32.7  19.2  15.9   19.1        48, 8, 8000; 4    109    92.5  89.9  99     87.1
+//   16, 8, 2000; 4      17.9  15.1  14.3  19.0   19.0        256, 8, 1000; 4    63.2  85.6 123   195     79.5
+//   2, 8, 4096; 160     52.5  49.7  52.1  63.4   42.1        16, 8, 4096; 160  211   251   319   455    222
 inline Tree4Split tree4_split(long long B, long long Hkv, long long group, long long D, long long max_nodes, long long table_width,
                               long long page, int sms) {
     Tree4Split s{};
@@ -97,19 +105,20 @@ inline Tree4Split tree4_split(long long B, long long Hkv, long long group, long 
     const long long rows = 8 * s.nt, chunks = (table_width * page + kT4Keys - 1) / kT4Keys;
     s.tiles = (int)((max_nodes * group + rows - 1) / rows);
     s.chunks = (int)chunks;
-    const double items = (double)B * (double)Hkv * s.tiles, slots = (double)(Tree4Split::ctas_an_sm(s.nt) * sms);
-    const double work = items * (double)(chunks > 0 ? chunks : 1) * (s.nt == 1 ? 0.9e-3 : 1.4e-3) * (D == 64 ? 0.55 : 1.0);     // us
+    const double items = (double)B * (double)Hkv * s.tiles, slots = (double)(Tree4Split::ctas_an_sm(s.nt) * sms), scale = D == 64 ? 0.55 : 1.0;
+    const double alone = (s.nt == 1 ? 0.9 : 1.5) * scale, full = (s.nt == 1 ? 2.3 : 1.7) * scale;
     double best = 1e30;
     for (int c = 1; c <= kT4MaxCluster; c *= 2) {
         if (c > 1 && chunks <= (long long)c / 2 * kT4Warps) break;
-        const double ctas = items * c, waves = (double)(long long)((ctas + slots - 1) / slots), t = waves * (work * slots / ctas + 6.0);
+        const double ctas = items * c, r = ctas / slots, waves = r > 2.0 ? r + 0.3 : std::ceil(r), steps = std::ceil((double)chunks / (c * kT4Warps));
+        const double t = waves * (steps * std::max(alone, full * std::pow(std::min(r, 1.0), 0.7)) + (c > 1 ? 5.0 : 4.0));
         if (t < best) {
             best = t;
             s.cluster = c;
             s.grid = (int)ctas;
         }
     }
-    if (9.0 + work < best) {
+    if (items < 2 * slots && 11.0 + 4.0 * items / slots + items * (double)chunks * full / (slots * kT4Warps) < best) {
         s.cluster = 0;
         s.grid = (int)slots;
         s.starts = ((B + 1) * 8 + 255) / 256 * 256;

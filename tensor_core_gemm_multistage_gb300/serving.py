@@ -60,6 +60,24 @@ def _declare(L) -> None:
     L.verify_drafts.argtypes = [ctypes.POINTER(_VerifyDesc)] + [vp] * 11
 
 
+def _call_scratch(index, stream, name, function, size_of, workspace, d, *args):
+    """function(d, *args, workspace, its bytes, stream).  Without the caller's workspace the library keeps one for the
+    stream, which it refuses to do in a capture: only then is there one to be made from the graph's memory."""
+    if workspace is None:
+        try:
+            _call(index, stream, name, function, d, *args, None, 0)
+            return
+        except GsrError as e:
+            if e.status != Status.ERR_INVALID_ARG or size_of(d) <= 0:
+                raise
+            ws, scratch, size = _scratch(None, lambda: size_of(d), index, stream)
+            if scratch is None:
+                raise
+    else:
+        ws, scratch, size = _scratch(workspace, None, index, stream)
+    _call(index, stream, name, function, d, *args, scratch, size)
+
+
 def rope_table(rows: int, rotary_dim: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
     """(rows, rotary_dim) float32 for ``cos_sin``: position p's cosines of p theta^(-2 i / rotary_dim), then
     their sines, computed in 64 bits (a far position's angle has too few digits in 32)."""
@@ -133,11 +151,10 @@ def qk_norm_rope_bwd(dQ_out, dK_out, Q, K, dQ, dK, cos_sin=None, positions=None,
     if not (K is None) == (dK is None) == (dK_out is None):
         raise ValueError("K, dK_out and dK go together")
     L, D, f32 = lib(), qs[3], torch.float32
-    ws, scratch, size = _scratch(workspace, lambda: L.qk_norm_rope_bwd_workspace(d), dev, stream)
-    _call(dev, stream, "qk_norm_rope_bwd", L.qk_norm_rope_bwd, d, _operand(dQ_out, "dQ_out", qs, dt, dev),
+    _call_scratch(dev, stream, "qk_norm_rope_bwd", L.qk_norm_rope_bwd, L.qk_norm_rope_bwd_workspace, workspace, d, _operand(dQ_out, "dQ_out", qs, dt, dev),
           _optional(dK_out, "dK_out", ks, dt, dev), _operand(Q, "Q", qs, dt, dev), _optional(K, "K", ks, dt, dev),
           _operand(dQ, "dQ", qs, dt, dev), _optional(dK, "dK", ks, dt, dev), _vector(dq_weight, "dq_weight", D, f32, dev),
-          _vector(dk_weight, "dk_weight", D, f32, dev), scratch, size)
+          _vector(dk_weight, "dk_weight", D, f32, dev))
     return dQ, dK, dq_weight, dk_weight
 
 
@@ -270,15 +287,11 @@ def tree_attention4_fwd(Q, k_cache, v_cache, block_tables, kv_lens, q_starts, pa
         raise ValueError("block_tables must be (requests, width)")
     B, W = block_tables.shape
     d = _TreeDesc(B, N, Hq, heads, D, pages, page, W, max_nodes, qr, qh, orow, oh, code, softmax_scale, softcap, None)
-    L, scratch, size = lib(), None, 0
-    need = L.tree_attention4_workspace(d)
-    if need > 0 or workspace is not None:
-        ws, scratch, size = _scratch(workspace, lambda: need, dev, stream)
-    _call(dev, stream, "tree_attention4_fwd", L.tree_attention4_fwd, d, Q.data_ptr() or None,
+    L = lib()
+    _call_scratch(dev, stream, "tree_attention4_fwd", L.tree_attention4_fwd, L.tree_attention4_workspace, workspace, d, Q.data_ptr() or None,
           _cache4(k_cache, "k_cache", cache, dt, dev), _cache4(v_cache, "v_cache", cache, dt, dev),
           _vector(block_tables, "block_tables", B * W, i32, dev), _vector(kv_lens, "kv_lens", B, i32, dev),
-          _vector(q_starts, "q_starts", B + 1, i32, dev), _vector(parents, "parents", N, i32, dev), O.data_ptr() or None,
-          scratch, size)
+          _vector(q_starts, "q_starts", B + 1, i32, dev), _vector(parents, "parents", N, i32, dev), O.data_ptr() or None)
     return O
 
 

@@ -167,6 +167,17 @@ def test_tree4_refusals(accepted):
         assert tree(bad) == INVALID, bad
     assert tree(q=None) == INVALID and tree(table=None) == INVALID and tree(lens=None) == INVALID
     assert tree(q=GB + 8) == ALIGN and tree(parents=9 * GB + 1) == ALIGN
+    much = dict(batch=48, total_q=48, heads_q=32, heads_kv=8, table_width=4096, max_nodes=1, q_stride_row=2048, o_stride_row=2048)
+    size = gsr.tree_attention4_workspace(48, 48, 32, 8, 64, 10, 16, 4096, 1)
+    assert gsr.tree_attention4_workspace(2, 6, 4, 2, 64, 10, 16, 5, 3) == 0 and size > 0
+    big = lambda a: cache4(a, H=8)
+    assert accepted(tree(much, k=big(4 * GB), v=big(5 * GB), ws=10 * GB, ws_bytes=size))
+    assert tree(much, k=big(4 * GB), v=big(5 * GB), ws=10 * GB, ws_bytes=size - 1) == INVALID
+    assert tree(much, k=big(4 * GB), v=big(5 * GB), ws=10 * GB + 8, ws_bytes=size) == ALIGN
+    for at in (1, 3, 4, 5, 6, 7, 8, 9):
+        assert tree(much, k=big(4 * GB), v=big(5 * GB), ws=at * GB, ws_bytes=size) == ALIAS, at
+    with pytest.raises(gsr.GsrError):
+        gsr.tree_attention4_workspace(2, 6, 4, 3, 64, 10, 16, 5, 3)
     assert tree(o=1 * GB) == ALIAS and tree(o=4 * GB) == ALIAS and tree(o=GB * 17 // 4) == ALIAS and tree(o=7 * GB) == ALIAS
     assert tree(dict(batch=0)) == OK and tree(dict(total_q=0)) == OK
 
