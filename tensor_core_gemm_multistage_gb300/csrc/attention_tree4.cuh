@@ -8,8 +8,9 @@
 // A code is an fp16 operand as it lies: 4 bits low in a half are the subnormal c 2^-24, the next 4 bits c 2^-20,
 // which tensor cores multiply exactly; the powers of two go into the queries, and off the sums at the end.  So
 // unpacking takes one AND for two values, and a shift for four.  The 8 (which halves what rounding p s to 16 bits
-// does to O) leaves by a product with the constant, chunk by chunk: products are many fewer than values, and left
-// to the end it would cost digits (4096 keys, fp16: 3.1e-4 of O).  Queries are held
+// does to O) leaves chunk by chunk with the sum of the rounded p s, a product with ones: left to the end it would cost
+// digits (4096 keys, fp16: 3.1e-4 of O), and as products with the constant -8 it took 171 us where this takes 161 (16
+// trees of 40 nodes over 4096 tokens, 8 heads of 4 queries each).  Queries are held
 // as fp16 times a power of two for each row (bf16's 8 bits fit; what is 2^-25 of the row's largest loses digits).
 //
 // What bounds it: D / 2 + D / 16 bytes a key and head, twice, from HBM; per byte that is 3.6 times the
@@ -574,10 +575,19 @@ __device__ __forceinline__ bool t4_part(const Tree4Params& p, const Tree4Plan& p
         else weigh(std::true_type{});
 
         // O^T += codes^T p: product i of a group has dimensions 16 i + 2 g (c0, c1) and the next one (c2, c3) as rows
-        constexpr uint32_t LOW8 = 0x80088008u, HIGH8 = 0x80808080u;         // -8 as the codes are held
+        // the 8 leaves with the sum of what was rounded, a product with ones
+        constexpr uint32_t ONE = 0x3c003c00u;
         const uint32_t vc = at + kT4Keys * C::CODES;
 #pragma unroll
-        for (int gi = 0; gi < G; ++gi)
+        for (int gi = 0; gi < G; ++gi) {
+            float sums[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sums[nt][e] = 0.0f;
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) mma_16x8x16(sums[nt], ONE, ONE, ONE, ONE, pf[gi][mt][nt][0], pf[gi][mt][nt][1]);
+            }
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
                 uint32_t v[4];
@@ -586,12 +596,19 @@ __device__ __forceinline__ bool t4_part(const Tree4Params& p, const Tree4Plan& p
                 for (int nt = 0; nt < NT; ++nt) {
                     const uint32_t p0 = pf[gi][mt][nt][0], p1 = pf[gi][mt][nt][1];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 4; ++i)
                         mma_16x8x16(o[gi][i][nt], codes_low(v[i]), codes_high(v[i]), codes_low(v[i] >> 8), codes_high(v[i] >> 8), p0, p1);
-                        mma_16x8x16(o[gi][i][nt], LOW8, HIGH8, LOW8, HIGH8, p0, p1);
-                    }
                 }
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float(&x)[4] = o[gi][i][nt];
+                    ffma2(x[0], x[1], sums[nt][0], sums[nt][1], -0x1p-21f, -0x1p-21f, x[0], x[1]);
+                    ffma2(x[2], x[3], sums[nt][2], sums[nt][3], -0x1p-17f, -0x1p-17f, x[2], x[3]);
+                }
+        }
 
         stage = stage == C::STAGES - 1 ? 0 : stage + 1;
     }
