@@ -9,7 +9,7 @@
 // which tensor cores multiply exactly; the powers of two go into the queries, and off the sums at the end.  So
 // unpacking takes one AND for two values, and a shift for four.  The 8 (which halves what rounding p s to 16 bits
 // does to O) leaves chunk by chunk with the sum of the rounded p s, a product with ones: left to the end it would cost
-// digits (4096 keys, fp16: 3.1e-4 of O), and as products with the constant -8 it took 171 us where this takes 161 (16
+// digits (4096 keys, fp16: 3.1e-4 of O), and as products with the constant -8 it took 10 us more of 161 (16
 // trees of 40 nodes over 4096 tokens, 8 heads of 4 queries each).  Queries are held
 // as fp16 times a power of two for each row (bf16's 8 bits fit; what is 2^-25 of the row's largest loses digits).
 //
@@ -464,10 +464,12 @@ __device__ __forceinline__ bool t4_part(const Tree4Params& p, const Tree4Plan& p
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 4; e += 2) {       // two queries at once
                         const float s = e < 2 ? s0[gi] : s1[gi], m = e < 2 ? m0[gi] : m1[gi];
-                        const float x = gi ? fmaf(m, qsum[gi][nt][e & 1], z[mt][nt][e]) : m * qsum[gi][nt][e & 1];
-                        z[mt][nt][e] = fmaf(s, acc[gi][nt][e], x);
+                        float(&x)[4] = z[mt][nt];
+                        if (gi) ffma2(x[e], x[e + 1], m, m, qsum[gi][nt][0], qsum[gi][nt][1], x[e], x[e + 1]);
+                        else fmul2(x[e], x[e + 1], m, m, qsum[gi][nt][0], qsum[gi][nt][1]);
+                        ffma2(x[e], x[e + 1], s, s, acc[gi][nt][e], acc[gi][nt][e + 1], x[e], x[e + 1]);
                     }
         }
         float ratio[4][G], centre[4][G], log_s[4], inv[4];
@@ -487,12 +489,10 @@ __device__ __forceinline__ bool t4_part(const Tree4Params& p, const Tree4Plan& p
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float& x = z[i >> 1][nt][2 * (i & 1) + e];
-                        x = fmaf(x, factor[nt][e], log_s[i]);
-                    }
+                for (int nt = 0; nt < NT; ++nt) {
+                    float* x = &z[i >> 1][nt][2 * (i & 1)];
+                    ffma2(x[0], x[1], x[0], x[1], factor[nt][0], factor[nt][1], log_s[i], log_s[i]);
+                }
         }
         uint32_t hidden = 0u;                              // bit 4 (2 mt + e / 2) + 2 nt + e % 2: the query does not see the key
         if (!full) {
@@ -554,20 +554,21 @@ __device__ __forceinline__ bool t4_part(const Tree4Params& p, const Tree4Plan& p
             for (int i = 0; i < 4; ++i) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float w[G][2];
+                    float* x = &z[i >> 1][nt][2 * (i & 1)];
+                    fadd2(x[0], x[1], -base[nt][0], -base[nt][1]);
+                    x[0] = exp2_fast(x[0]);
+                    x[1] = exp2_fast(x[1]);
+                    ffma2(l[nt][0], l[nt][1], x[0], x[1], inv[i], inv[i], l[nt][0], l[nt][1]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float x = exp2_fast(z[i >> 1][nt][2 * (i & 1) + e] - base[nt][e]);
-                        l[nt][e] = fmaf(x, inv[i], l[nt][e]);
-                        const bool out = decltype(masked)::value && (hidden >> (4 * i + 2 * nt + e) & 1u);     // whatever its scale holds
+                    for (int gi = 0; gi < G; ++gi) {
+                        float w[2], c[2] = {centre[i][gi], centre[i][gi]};
+                        fmul2(w[0], w[1], x[0], x[1], ratio[i][gi], ratio[i][gi]);
 #pragma unroll
-                        for (int gi = 0; gi < G; ++gi) {
-                            w[gi][e] = out ? 0.0f : x * ratio[i][gi];
-                            mid[gi][nt][e] = out ? mid[gi][nt][e] : fmaf(x, centre[i][gi], mid[gi][nt][e]);
-                        }
+                        for (int e = 0; e < 2; ++e)
+                            if (decltype(masked)::value && (hidden >> (4 * i + 2 * nt + e) & 1u)) w[e] = c[e] = 0.0f;      // whatever its scale holds
+                        ffma2(mid[gi][nt][0], mid[gi][nt][1], x[0], x[1], c[0], c[1], mid[gi][nt][0], mid[gi][nt][1]);
+                        pf[gi][i >> 1][nt][i & 1] = transpose8(Pair<__half>::pack(w[0], w[1]));
                     }
-#pragma unroll
-                    for (int gi = 0; gi < G; ++gi) pf[gi][i >> 1][nt][i & 1] = transpose8(Pair<__half>::pack(w[gi][0], w[gi][1]));
                 }
             }
         };
