@@ -77,7 +77,7 @@ template <class Type, int Dim, int Nt>
 struct T4Cfg {
     using T = Type;
     static constexpr int D = Dim, NT = Nt, G = D / 64, ROWS = 8 * NT;
-    static constexpr int STAGES = NT == 1 ? 2 : 3, CTAS = NT == 1 ? 4 : 2;     // CTAs on an SM
+    static constexpr int STAGES = NT == 1 ? 2 : 3, CTAS = Tree4Split::ctas_an_sm(NT, Dim);
     static constexpr int CODES = D / 2, PARAMS = D / 16;             // bytes of a row
     static constexpr int STAGE = kT4Keys * 2 * (CODES + PARAMS);
     static constexpr int RING = kT4Warps * STAGES * STAGE;
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(kT4Threads, C::CTAS)
 template <class C, int WARPS>
 __global__ void __launch_bounds__(128) gsr_tree4_join_kernel(const __grid_constant__ Tree4Params p, int grid) {
     using T = typename C::T;
-    constexpr int D = C::D, E = D / 32, ROWS = 4 / WARPS, AHEAD = WARPS > 1 ? 8 : 2;
+    constexpr int D = C::D, E = D / 32, ROWS = 4 / WARPS, AHEAD = WARPS > 1 ? 8 : 4;
     __shared__ float sm[4][D + 2];
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS;
     const long long id = (long long)blockIdx.x * ROWS + (threadIdx.x >> 5) / WARPS;
@@ -889,7 +889,7 @@ cudaError_t t4_allow(K kernel, int bytes, std::atomic<uint64_t>& done) {
 template <class C>
 cudaError_t launch_tree4_cfg(const Tree4Params& p, const Tree4Split& split, cudaStream_t stream) {
     static std::atomic<uint64_t> cluster_done{0}, even_done{0};
-    static_assert(C::CTAS == Tree4Split::ctas_an_sm(C::NT) && C::ROWS == 8 * C::NT && C::PART * 4 == Tree4Split::state_bytes(C::NT, C::D), "");
+    static_assert(C::ROWS == 8 * C::NT && C::PART * 4 == Tree4Split::state_bytes(C::NT, C::D), "");
     cudaError_t e;
     const Tree4Plan plan{Divider((uint32_t)p.page), split.tiles, split.cluster, split.chunks};
     cudaLaunchConfig_t cfg{};
@@ -911,16 +911,18 @@ cudaError_t launch_tree4_cfg(const Tree4Params& p, const Tree4Split& split, cuda
         (e = cudaLaunchKernelEx(&cfg, gsr_tree4_even_kernel<C>, p, plan)) != cudaSuccess)
         return e;
     // the joining CTAs start while the parts' last CTAs finish, and wait for them there
-    const long long rows = (long long)p.total_q * p.Hq;
+    // eight states an item or more by four warps a row, few by one
+    const long long rows = (long long)p.total_q * p.Hq, items = (long long)p.B * p.Hkv * split.tiles;
+    const bool many = split.grid >= 8 * items;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    cfg.gridDim = dim3((unsigned)(rows >= 2048 ? (rows + 3) / 4 : rows));
-    return rows >= 2048 ? cudaLaunchKernelEx(&cfg, gsr_tree4_join_kernel<C, 1>, p, split.grid)
-                        : cudaLaunchKernelEx(&cfg, gsr_tree4_join_kernel<C, 4>, p, split.grid);
+    cfg.gridDim = dim3((unsigned)(many ? rows : (rows + 3) / 4));
+    return many ? cudaLaunchKernelEx(&cfg, gsr_tree4_join_kernel<C, 4>, p, split.grid)
+                : cudaLaunchKernelEx(&cfg, gsr_tree4_join_kernel<C, 1>, p, split.grid);
 }
 
 template <class T>

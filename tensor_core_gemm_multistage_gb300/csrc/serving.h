@@ -85,7 +85,8 @@ struct Tree4Split {
     int nt, tiles;                     // column tiles of 8 query rows a CTA; row tiles a request and head
     int cluster, grid, chunks;         // CTAs that share an item (0: shared out evenly); CTAs; chunks a table's row holds
     long long starts, workspace;       // bytes
-    static constexpr int ctas_an_sm(int nt) { return nt == 1 ? 4 : 2; }
+    // 16 rows at D = 64: 36 us for 41 with two (64 requests of 8 nodes over 1000 tokens); at D = 128 registers spill (209 for 187)
+    static constexpr int ctas_an_sm(int nt, int D) { return nt == 1 ? 4 : D == 64 ? 3 : 2; }
     static constexpr int state_bytes(int nt, int D) { return 8 * nt * (D + 2) * 4; }
 };
 // A cluster an item, or all chunks shared out evenly, whichever the estimate has sooner, lengths taken as the most that
@@ -105,7 +106,7 @@ inline Tree4Split tree4_split(long long B, long long Hkv, long long group, long 
     const long long rows = 8 * s.nt, chunks = (table_width * page + kT4Keys - 1) / kT4Keys;
     s.tiles = (int)((max_nodes * group + rows - 1) / rows);
     s.chunks = (int)chunks;
-    const double items = (double)B * (double)Hkv * s.tiles, slots = (double)(Tree4Split::ctas_an_sm(s.nt) * sms), scale = D == 64 ? 0.55 : 1.0;
+    const double items = (double)B * (double)Hkv * s.tiles, slots = (double)(Tree4Split::ctas_an_sm(s.nt, (int)D) * sms), scale = D == 64 ? 0.55 : 1.0;
     const double alone = (s.nt == 1 ? 0.9 : 1.5) * scale, full = (s.nt == 1 ? 2.3 : 1.7) * scale;
     double best = 1e30;
     for (int c = 1; c <= kT4MaxCluster; c *= 2) {
