@@ -563,7 +563,7 @@ gsr_status gsr_device_status(struct CUstream_st* stream, int* code);
 /*
  * Releases the library's state for the (current device, stream) pair: the
  * stream's 16 bytes of words and the workspaces of small-M calls, masked attention, its
- * gradients and tree attention, if any ran on it.
+ * gradients, tree attention over 16 and 4 bits and the gradient of norms, if any ran on it.
  * Waits for the stream first (queued kernels may still use them).  For callers
  * that create and destroy streams: call it before destroying a stream the
  * library was used on, from no other thread launching on that stream at the same

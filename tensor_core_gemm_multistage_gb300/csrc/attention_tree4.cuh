@@ -17,6 +17,10 @@
 // arithmetic of a 16-bit cache, so the instructions that unpack codes come next.  Codes are therefore unpacked
 // in registers into mma.sync operands: operands of tcgen05 come from shared memory or TMEM, and the unpacked rows
 // would be written there and read again, 93 of an SM's 128 bytes a clock at HBM's rate, before the first product.
+// Where many rows share a key that would be no hindrance; but 128 rows on tcgen05, two CTAs an SM, took 175 us for 16
+// trees of 40 nodes: product, scores, p s and product follow one another, 6500 clocks for 64 keys.  Measured, D = 128, 8
+// heads of keys, 32 of queries: 48 requests of 4000 to 8000 tokens 75 us (4.3 TB/s), 16 trees of 40 nodes over up to 4096
+// tokens 155 us (148 TFLOP/s; a warp's own latencies, with two warps a scheduler).
 // Keys are the products' rows (16 at once) and the queries of a group their columns (8): no row of the product is
 // spent on padding where a group has 4 or 8 heads.
 //
@@ -27,8 +31,8 @@
 //  * Much: the chunks of all items are laid end to end and shared out evenly over as many CTAs as the SMs hold at
 //    once, whatever the lengths (each CTA finds its range by one sum over the requests).  An item that one CTA covers
 //    is written at once, else its CTAs leave their states in the workspace, two a CTA at most, and a second
-//    launch joins them in the CTAs' order.  Clusters cost 8 us a wave of CTAs there, and their waves leave SMs idle
-//    (48 requests of 4000 to 8000 tokens: 91 us in clusters).
+//    launch joins them in the CTAs' order.  (Clusters there cost a start and a join a wave, and waves leave SMs idle: 84 us
+//    for 79, 48 requests.)
 // No order changes from run to run.
 #pragma once
 

@@ -94,11 +94,12 @@ struct Tree4Split {
 // it); a wave of clusters costs 5 us more, of single CTAs 4; sharing out 11 us and 4 for each item of a CTA, and with
 // two items for every CTA it has nothing left to even out.  Measured, us (requests, key/value heads, tokens to;
 // rows a head, D = 128), in clusters of 1, 2, 4, 8, evenly:
-//   1, 8, 2000; 4       17.8  12.5   9.0   7.1   12.4        48, 8, 500; 4      11.9  17.3  21.6  37.8   20.5
-//   1, 8, 32000; 4     210   109    59    32.5   18.2        48, 8, 2000; 4     30.4  33.6  36.3  49.1   33.3
-//   4, 8, 8000; 4       56.6  32.7  19.2  15.9   19.1        48, 8, 8000; 4    109    92.5  89.9  99     87.1
-//   16, 8, 2000; 4      17.9  15.1  14.3  19.0   19.0        256, 8, 1000; 4    63.2  85.6 123   195     79.5
-//   2, 8, 4096; 160     52.5  49.7  52.1  63.4   42.1        16, 8, 4096; 160  211   251   319   455    222
+//   1, 8, 2000; 4       16.9  12.1   8.8   6.9   12.4        48, 8, 500; 4      11.5  17.0  21.1  37.0   18.5
+//   1, 8, 32000; 4     198   103    55.4  30.9   17.7        48, 8, 2000; 4     28.3  31.7  34.6  47.7   30.0
+//   4, 8, 8000; 4       53.5  31.0  18.6  15.1   18.5        48, 8, 8000; 4    100    86.3  83.7  94.2   79.5
+//   16, 8, 2000; 4      17.1  14.5  14.0  18.3   18.4        256, 8, 1000; 4    59.7  82.5 120   192     76.9
+//   2, 8, 4096; 160     46.8  46.2  49.6  60.6   38.4        16, 8, 4096; 160  187   229   297   433     204
+//   8, 2, 1000; 16      14.8  12.5   9.8   8.6   16.8        16, 8, 4096; 64    89.6 102   121   177     88.7
 inline Tree4Split tree4_split(long long B, long long Hkv, long long group, long long D, long long max_nodes, long long table_width,
                               long long page, int sms) {
     Tree4Split s{};
