@@ -311,19 +311,17 @@ __device__ __forceinline__ uint32_t codes_of(const f2* v, float s, float m) {
     // (conversions run at an eighth of the rate).
     constexpr uint32_t MAGIC = 0x4b400000u;
     const float magic = __uint_as_float(MAGIC), inv = __fdividef(1.0f, 15.0f * s), shift = -m * inv;
-    // twice, with what it may be off by added and taken away: alike unless a border lies between
-    const float margin = 0x1p-16f + 0x1p-16f * fabsf(shift);
-    const f2 fifteen = both(15.0f), above = both(magic + 0.0f), slack = both(margin), lack = both(-margin);
-    uint32_t u = 0u;
+    const f2 fifteen = both(15.0f), above = both(magic), below = both(-magic);
+    float worst = 0.0f;                                     // distance from an integer: a border is at a half
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 x = parts_of(v[i]);
-        const f2 y = two(__saturatef(fmaf(x.x, inv, shift)), __saturatef(fmaf(x.y, inv, shift)));
-        const float2 a = parts_of(add2(fma2(y, fifteen, slack), above)), b = parts_of(add2(fma2(y, fifteen, lack), above));
+        const f2 y = two(__saturatef(fmaf(x.x, inv, shift)), __saturatef(fmaf(x.y, inv, shift))), c = fma2(y, fifteen, above);
+        const float2 a = parts_of(c), off = parts_of(fma2(y, both(-15.0f), add2(c, below)));
+        worst = max3(worst, fabsf(off.x), fabsf(off.y));
         w += __float_as_uint(a.x) * (1u << (8 * i)) + __float_as_uint(a.y) * (16u << (8 * i));
-        u += __float_as_uint(b.x) * (1u << (8 * i)) + __float_as_uint(b.y) * (16u << (8 * i));
     }
-    if (s > 1e-30f && s < 1e30f && w == u && margin < 0.25f) return w - MAGIC * 0x11111111u;
+    if (s > 1e-30f && s < 1e30f && worst < 0.5f - 0x1p-16f - 0x1p-16f * fabsf(shift)) return w - MAGIC * 0x11111111u;
     w = 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
