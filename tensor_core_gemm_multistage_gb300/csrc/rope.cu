@@ -21,6 +21,7 @@
 namespace gsr {
 namespace {
 
+// Five CTAs of 128 threads with 102 registers take as long forwards, and spill in the gradient (72 us for 50) and the writes.
 constexpr int kThreads = 256, kWarps = kThreads / 32, kCtasAnSm = 2;
 
 // ---------------------------------------------------------------------------

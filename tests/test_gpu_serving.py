@@ -642,6 +642,43 @@ def test_repeatable_and_on_two_streams_at_once():
     assert all(torch.equal(t.o, f) for t, f in zip(ts, first))
 
 
+@pytest.mark.parametrize("even", [False, True])
+def test_rows_before_the_first_sequence(even):
+    """Rows of no request in front of the first and behind the last are left as they were; the others' results stay."""
+    t = Tree4(kv=[300, 77, 40], T=[5, 1, 9], Hq=8, Hkv=2, D=128, page=16, extra_rows=5, width=2 ** 17 if even else 0)
+    want, N = t.run().check().o[:-5].clone(), t.N - 5
+    t.q = torch.cat([t.q[N:N + 3], t.q[:N], t.q[N + 3:]])
+    t.parents = [-1] * 3 + t.parents[:N] + [-1] * 2
+    t.starts = t.starts + 3
+    t.run()
+    assert torch.equal(t.o[3:-2], want) and torch.all(t.o[:3] == 7.0) and torch.all(t.o[-2:] == 7.0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_caches_of_views(D):
+    """Keys and values side by side in one tensor, every second page of a larger one: written, read and attended alike."""
+    t = Tree4(kv=[150, 61], T=[3, 20], Hq=8, Hkv=2, D=D, page=16, dtype=BF16).run().check()
+    want, pool = t.o.clone(), t.caches[0].codes.shape[0]
+    slots = torch.arange(pool * 16, dtype=torch.int32, device=DEV)
+    k, v = (torch.empty(pool * 16, 2, D, dtype=BF16, device=DEV) for _ in range(2))
+    gsr.kv_cache4_read(*t.caches, slots, k, v)
+    codes = torch.zeros(2 * pool + 1, 2, 2, 16, D // 2, dtype=torch.uint8, device=DEV)
+    params = torch.zeros(2 * pool + 1, 2, 2, 16, D // 64, 2, dtype=BF16, device=DEV)
+    t.caches, old = [gsr.Cache4(codes[1::2, i].transpose(1, 2), params[1::2, i].transpose(1, 2)) for i in range(2)], t.caches
+    for new, o in zip(t.caches, old):
+        new.codes.copy_(o.codes)
+        new.params.copy_(o.params)
+    assert torch.equal(t.run().o, want)
+    k2, v2 = torch.empty_like(k), torch.empty_like(v)
+    gsr.kv_cache4_read(*t.caches, slots, k2, v2)
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+    gsr.kv_cache4_append_rope(v, k, slots, *t.caches)
+    gsr.kv_cache4_append_rope(v, k, slots, *old)
+    for new, o in zip(t.caches, old):
+        assert torch.equal(new.codes, o.codes) and torch.equal(new.params, o.params)
+    assert not codes[::2].any() and not params[::2].any()
+
+
 def test_a_cache_past_32_bits():
     t = Tree4(kv=[150, 61], T=[3, 1], Hq=8, Hkv=8, D=128, page=16, dtype=BF16).run().check()
     want, pool = t.o.clone(), t.caches[0].codes.shape[0]
