@@ -65,9 +65,13 @@ def _handle(stream, index):
     return (stream if isinstance(stream, int) else stream.cuda_stream) or None
 
 
+# behind torch.cuda.current_device, without its look whether CUDA is there (a CUDA tensor is)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _call(index, stream, name, function, *args):
     """function(*args, stream handle) with the device current; raises GsrError unless it returns GSR_OK."""
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         s = function(*args, _handle(stream, index))
     else:
         with torch.cuda.device(index):

@@ -4,12 +4,14 @@ checks and marshalling only; include/gsr.h has the full contract of each entry p
 from __future__ import annotations
 
 import ctypes
+import struct
+from types import SimpleNamespace
 from typing import NamedTuple
 
 import torch
 
 from .binding import GsrError, Status, lib
-from .llm import _cache, _call, _dtype_code, _operand, _scratch, _Tensor, _TreeDesc, _vector
+from .llm import _call, _dtype_code, _scratch, _Tensor, _TreeDesc, _vector
 
 
 class _RopeDesc(ctypes.Structure):
@@ -60,6 +62,31 @@ def _declare(L) -> None:
     L.verify_drafts.argtypes = [ctypes.POINTER(_VerifyDesc)] + [vp] * 11
 
 
+# The structures as bytes, for calls: a small call waits for its marshalling, and packing takes half of the time that
+# making a ctypes.Structure does (norm and rotation of two operands 7.9 us, 10.6 with structures; 2.6 of them the launch).
+_pack_tensor = struct.Struct("@P3q").pack
+_pack_cache4 = struct.Struct("@P3qP3q").pack
+_pack_rope = struct.Struct("@7q2if4P").pack
+_pack_tree = struct.Struct("@13qi2fP").pack
+_pack_verify = struct.Struct("@6q").pack
+_entry = None
+
+
+def _entries():
+    """The entry points, taking addresses or bytes for every pointer."""
+    global _entry
+    if _entry is None:
+        L, made = lib(), SimpleNamespace()
+        for name in ("qk_norm_rope_fwd", "qk_norm_rope_bwd_workspace", "qk_norm_rope_bwd", "kv_cache_append_rope", "kv_cache4_append_rope",
+                     "kv_cache4_read", "tree_attention4_fwd", "tree_attention4_workspace", "verify_drafts"):
+            declared, function = getattr(L, name), L[name]          # a second object of the same function
+            function.restype = declared.restype
+            function.argtypes = [t if t in (ctypes.c_int64, ctypes.c_int32) else ctypes.c_void_p for t in declared.argtypes]
+            setattr(made, name, function)
+        _entry = made
+    return _entry
+
+
 def _call_scratch(index, stream, name, function, size_of, workspace, d, *args):
     """function(d, *args, workspace, its bytes, stream).  Without the caller's workspace the library keeps one for the
     stream, which it refuses to do in a capture: only then is there one to be made from the graph's memory."""
@@ -92,10 +119,10 @@ def _rope_desc(B, Hq, Hkv, S, D, dtype, code, index, cos_sin, positions, q_weigh
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be (positions, rotary_dim), got %s" % (tuple(cos_sin.shape),))
         rows, R = cos_sin.shape
-    return _RopeDesc(B, Hq, Hkv, S, D, R, rows, code, 1 if interleaved else 0, eps,
-                     _vector(q_weight, "q_weight", D, dtype, index), _vector(k_weight, "k_weight", D, dtype, index),
-                     _vector(cos_sin, "cos_sin", rows * R, torch.float32, index),
-                     _vector(positions, "positions", B * S, torch.int32, index))
+    return _pack_rope(B, Hq, Hkv, S, D, R, rows, code, 1 if interleaved else 0, eps,
+                      _vector(q_weight, "q_weight", D, dtype, index) or 0, _vector(k_weight, "k_weight", D, dtype, index) or 0,
+                      _vector(cos_sin, "cos_sin", rows * R, torch.float32, index) or 0,
+                      _vector(positions, "positions", B * S, torch.int32, index) or 0)
 
 
 def _qk_desc(Q, K, cos_sin, positions, q_weight, k_weight, eps, interleaved):
@@ -105,7 +132,8 @@ def _qk_desc(Q, K, cos_sin, positions, q_weight, k_weight, eps, interleaved):
         raise ValueError("Q must be a CUDA tensor")
     if Q.dim() != 4:
         raise ValueError("Q must be 4-D (batch, heads, seq, head_dim)")
-    B, Hq, S, D = Q.shape
+    qs = Q.shape
+    B, Hq, S, D = qs
     if K is None:
         Hkv = 0
     elif K.dim() != 4:
@@ -113,11 +141,21 @@ def _qk_desc(Q, K, cos_sin, positions, q_weight, k_weight, eps, interleaved):
     else:
         Hkv = K.shape[1]
     d = _rope_desc(B, Hq, Hkv, S, D, Q.dtype, code, index, cos_sin, positions, q_weight, k_weight, eps, interleaved)
-    return d, Q.shape, (B, Hkv, S, D), Q.dtype, index
+    return d, qs, (B, Hkv, S, D), Q.dtype, index
 
 
-def _optional(t, name, shape, dtype, index):
-    return _operand(t, name, shape, dtype, index) if t is not None else None
+def _operand(t, name, shape, dtype, index, pages=False):
+    """The C view of a 4-D operand (batch, head, row, D) of the given shape, or a cache (page, row, head, D); or None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError("%s must be %s on cuda:%d, got %s on %s" % (name, dtype, index, t.dtype, t.device))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    batch, head, row, one = t.stride()
+    if one != 1 and shape[3] > 1:
+        raise ValueError("%s: the last dimension must be contiguous" % name)
+    return _pack_tensor(t.data_ptr(), batch, row, head) if pages else _pack_tensor(t.data_ptr(), batch, head, row)
 
 
 def qk_norm_rope_fwd(Q, K, Q_out, K_out, cos_sin=None, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -134,8 +172,8 @@ def qk_norm_rope_fwd(Q, K, Q_out, K_out, cos_sin=None, positions=None, q_weight=
     d, qs, ks, dt, dev = _qk_desc(Q, K, cos_sin, positions, q_weight, k_weight, eps, interleaved)
     if (K is None) != (K_out is None):
         raise ValueError("K and K_out go together")
-    _call(dev, stream, "qk_norm_rope_fwd", lib().qk_norm_rope_fwd, d, _operand(Q, "Q", qs, dt, dev), _optional(K, "K", ks, dt, dev),
-          _operand(Q_out, "Q_out", qs, dt, dev), _optional(K_out, "K_out", ks, dt, dev))
+    _call(dev, stream, "qk_norm_rope_fwd", _entries().qk_norm_rope_fwd, d, _operand(Q, "Q", qs, dt, dev), _operand(K, "K", ks, dt, dev),
+          _operand(Q_out, "Q_out", qs, dt, dev), _operand(K_out, "K_out", ks, dt, dev))
     return Q_out, K_out
 
 
@@ -150,10 +188,10 @@ def qk_norm_rope_bwd(dQ_out, dK_out, Q, K, dQ, dK, cos_sin=None, positions=None,
     d, qs, ks, dt, dev = _qk_desc(Q, K, cos_sin, positions, q_weight, k_weight, eps, interleaved)
     if not (K is None) == (dK is None) == (dK_out is None):
         raise ValueError("K, dK_out and dK go together")
-    L, D, f32 = lib(), qs[3], torch.float32
+    L, D, f32 = _entries(), qs[3], torch.float32
     _call_scratch(dev, stream, "qk_norm_rope_bwd", L.qk_norm_rope_bwd, L.qk_norm_rope_bwd_workspace, workspace, d, _operand(dQ_out, "dQ_out", qs, dt, dev),
-          _optional(dK_out, "dK_out", ks, dt, dev), _operand(Q, "Q", qs, dt, dev), _optional(K, "K", ks, dt, dev),
-          _operand(dQ, "dQ", qs, dt, dev), _optional(dK, "dK", ks, dt, dev), _vector(dq_weight, "dq_weight", D, f32, dev),
+          _operand(dK_out, "dK_out", ks, dt, dev), _operand(Q, "Q", qs, dt, dev), _operand(K, "K", ks, dt, dev),
+          _operand(dQ, "dQ", qs, dt, dev), _operand(dK, "dK", ks, dt, dev), _vector(dq_weight, "dq_weight", D, f32, dev),
           _vector(dk_weight, "dk_weight", D, f32, dev))
     return dQ, dK, dq_weight, dk_weight
 
@@ -188,7 +226,7 @@ def _cache4(c, name, shape, dtype, index):
     (cp, cr, ch, c1), (pp, pr, ph, pg, p1) = codes.stride(), params.stride()
     if c1 != 1 or p1 != 1 or (pg != 2 and D > 64):
         raise ValueError("%s: a row's codes, and its params, must be contiguous" % name)
-    return _Cache4(_Tensor(codes.data_ptr() or None, cp, ch, cr), _Tensor(params.data_ptr() or None, pp, ph, pr))
+    return _pack_cache4(codes.data_ptr(), cp, ch, cr, params.data_ptr(), pp, ph, pr)
 
 
 def _rows(t, name, shape, dtype, index):
@@ -200,7 +238,7 @@ def _rows(t, name, shape, dtype, index):
     row, head, one = t.stride()
     if one != 1 and shape[2] > 1:
         raise ValueError("%s: the last dimension must be contiguous" % name)
-    return _Tensor(t.data_ptr() or None, 0, head, row)
+    return _pack_tensor(t.data_ptr(), 0, head, row)
 
 
 def _append_args(K, V, slots, Q, Q_out, cos_sin, positions, q_weight, k_weight, eps, interleaved, D, heads):
@@ -233,8 +271,8 @@ def kv_cache_append_rope(K, V, slots, k_cache, v_cache, positions=None, cos_sin=
     if len(cache) != 4:
         raise ValueError("k_cache must be (pages, page_size, heads, head_dim), got %s" % (tuple(cache),))
     d, rows, dt, dev = _append_args(K, V, slots, Q, Q_out, cos_sin, positions, q_weight, k_weight, eps, interleaved, cache[3], cache[2])
-    _call(dev, stream, "kv_cache_append_rope", lib().kv_cache_append_rope, d, *rows, _cache(k_cache, "k_cache", cache, dt, dev),
-          _cache(v_cache, "v_cache", cache, dt, dev), cache[0], cache[1])
+    _call(dev, stream, "kv_cache_append_rope", _entries().kv_cache_append_rope, d, *rows, _operand(k_cache, "k_cache", cache, dt, dev, True),
+          _operand(v_cache, "v_cache", cache, dt, dev, True), cache[0], cache[1])
 
 
 def kv_cache4_append_rope(K, V, slots, k_cache, v_cache, positions=None, cos_sin=None, Q=None, Q_out=None, q_weight=None,
@@ -246,7 +284,7 @@ def kv_cache4_append_rope(K, V, slots, k_cache, v_cache, positions=None, cos_sin
     pages, page, heads, half = k_cache[0].shape
     cache = (pages, page, heads, 2 * half)
     d, rows, dt, dev = _append_args(K, V, slots, Q, Q_out, cos_sin, positions, q_weight, k_weight, eps, interleaved, 2 * half, heads)
-    _call(dev, stream, "kv_cache4_append_rope", lib().kv_cache4_append_rope, d, *rows, _cache4(k_cache, "k_cache", cache, dt, dev),
+    _call(dev, stream, "kv_cache4_append_rope", _entries().kv_cache4_append_rope, d, *rows, _cache4(k_cache, "k_cache", cache, dt, dev),
           _cache4(v_cache, "v_cache", cache, dt, dev), pages, page)
 
 
@@ -257,7 +295,7 @@ def kv_cache4_read(k_cache, v_cache, slots, K, V, stream=None):
     if dev < 0:
         raise ValueError("K must be a CUDA tensor")
     cache, rows = (pages, page, heads, 2 * half), (N, heads, 2 * half)
-    _call(dev, stream, "kv_cache4_read", lib().kv_cache4_read, _cache4(k_cache, "k_cache", cache, dt, dev),
+    _call(dev, stream, "kv_cache4_read", _entries().kv_cache4_read, _cache4(k_cache, "k_cache", cache, dt, dev),
           _cache4(v_cache, "v_cache", cache, dt, dev), _vector(slots, "slots", N, torch.int32, dev), _rows(K, "K", rows, dt, dev),
           _rows(V, "V", rows, dt, dev), N, heads, 2 * half, pages, page, code)
     return K, V
@@ -286,8 +324,8 @@ def tree_attention4_fwd(Q, k_cache, v_cache, block_tables, kv_lens, q_starts, pa
     if block_tables.dim() != 2:
         raise ValueError("block_tables must be (requests, width)")
     B, W = block_tables.shape
-    d = _TreeDesc(B, N, Hq, heads, D, pages, page, W, max_nodes, qr, qh, orow, oh, code, softmax_scale, softcap, None)
-    L = lib()
+    d = _pack_tree(B, N, Hq, heads, D, pages, page, W, max_nodes, qr, qh, orow, oh, code, softmax_scale, softcap, 0)
+    L = _entries()
     _call_scratch(dev, stream, "tree_attention4_fwd", L.tree_attention4_fwd, L.tree_attention4_workspace, workspace, d, Q.data_ptr() or None,
           _cache4(k_cache, "k_cache", cache, dt, dev), _cache4(v_cache, "v_cache", cache, dt, dev),
           _vector(block_tables, "block_tables", B * W, i32, dev), _vector(kv_lens, "kv_lens", B, i32, dev),
@@ -332,7 +370,7 @@ def verify_drafts(target_probs, draft_tokens, q_starts, parents, u_accept, u_sam
         raise ValueError("path must be (%d, max_nodes), got %s" % (B, tuple(path.shape)))
     (tp, ts), (dp, dr) = _probs(target_probs, "target_probs", N, V, dev), _probs(draft_probs, "draft_probs", N, V, dev)
     T = path.shape[1]
-    _call(dev, stream, "verify_drafts", lib().verify_drafts, _VerifyDesc(B, N, V, T, ts, dr), tp, dp,
+    _call(dev, stream, "verify_drafts", _entries().verify_drafts, _pack_verify(B, N, V, T, ts, dr), tp, dp,
           _vector(draft_tokens, "draft_tokens", N, i32, dev), _vector(q_starts, "q_starts", B + 1, i32, dev),
           _vector(parents, "parents", N, i32, dev), _vector(u_accept, "u_accept", N, f32, dev),
           _vector(u_sample, "u_sample", B, f32, dev), _vector(path, "path", B * T, i32, dev), _vector(counts, "counts", B, i32, dev),
