@@ -332,7 +332,7 @@ __device__ __forceinline__ uint32_t codes_of(const f2* v, float s, float m) {
     }
     return w;
 }
-// What bounds these writes is the arithmetic: 24576 tokens of 8 x 128 with K's rotation 52 us (129 MB, 2.5 TB/s; 64 % of the
+// What bounds these writes is the arithmetic: 24576 tokens of 8 x 128 with K's rotation 51 us (129 MB, 2.5 TB/s; 64 % of the
 // issue slots, 48 % of the integer pipe), minimum, maximum and codes of every value on top of the rotation.
 //
 // Per 64 values minimum m and scale s = (maximum - m) / 15, both rounded to T, and codes rint((x - m) / s) cut to
