@@ -368,7 +368,8 @@ gsr_status qk_norm_rope_fwd(const gsr_rope_desc* desc, const gsr_tensor* Q, cons
 /*
  * Gradients dQ, dK and, where there are weights, dq_weight, dk_weight (head_dim float32 each, written,
  * not added to) from dQ_out, dK_out and the forward's inputs Q, K (each read only where there is a
- * weight).  dQ may be the very view of dQ_out or of Q, dK likewise.  Padding's gradients are 0 and
+ * weight).  A weight whose operand has no heads gets a gradient of 0, or none (NULL).  dQ may be the very
+ * view of dQ_out or of Q, dK likewise.  Padding's gradients are 0 and
  * it adds nothing to the weights', whatever its rows hold.  Results do not depend on the order of
  * execution.
  *

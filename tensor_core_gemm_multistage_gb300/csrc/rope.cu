@@ -646,7 +646,8 @@ __device__ __forceinline__ void rope_bwd_part(const RopeBwdParams& a, const Rope
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (!weight) return;
+    // What the call has parts for: a weight whose rows have no heads may come without its gradient.
+    if (!(K_PART ? a.dk_weight : a.dq_weight)) return;
     float sum[16];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {

@@ -39,8 +39,8 @@ cudaError_t launch_rope_fwd(const RopeParams& p, bool bf16, int sms, cudaStream_
 struct RopeBwdParams {
     RopeParams f;
     Strided dQ, dK;
-    float *dq_weight, *dk_weight;      // D values each, where there are weights
-    float* parts;                      // (2, ctas, D) sums of a CTA's rows
+    float *dq_weight, *dk_weight;      // D values each, where there are weights; null: not wanted
+    float* parts;                      // (2, ctas, D) sums of a CTA's rows; may be null where neither is wanted
     int ctas;
 };
 int rope_bwd_ctas(long long batch, long long heads_q, long long heads_kv, long long seq, int D, int sms);

@@ -193,6 +193,33 @@ def test_in_place_and_without_keys():
         assert torch.equal(r.q, want[0]) and torch.equal(r.k, want[1])
 
 
+@pytest.mark.parametrize("own_workspace", [False, True])
+@pytest.mark.parametrize("wanted", [False, True])
+@pytest.mark.parametrize("weights", ["both", "k", "q", None])
+@pytest.mark.parametrize("absent", ["k", "q"])
+def test_gradient_with_an_operand_of_no_heads(absent, weights, wanted, own_workspace):
+    """Its weight may be there, with its gradient (0) or without; the other operand's gradients are those of the full call."""
+    r = Rope(B=2, Hq=6, Hkv=3, S=21, D=64, R=32, weights=weights, layout="plain")
+    full = r.run_bwd() + r.dw
+    keep, gone = (0, 1) if absent == "k" else (1, 0)
+    ops = [[r.do[0], r.do[1]], [r.q, r.k], [torch.full_like(t, 7.0) for t in (r.q, r.k)]]
+    for pair in ops:
+        pair[gone] = None if absent == "k" else pair[gone][:, :0]
+    dw = [None if t is None else torch.full_like(t, 7.0) for t in r.dw]
+    if not wanted:
+        dw[gone] = None
+    ws = None
+    if own_workspace:
+        ws = torch.empty(gsr.qk_norm_rope_bwd_workspace(2, 6 if absent == "k" else 0, 0 if absent == "k" else 3, 21, 64), dtype=torch.uint8, device=DEV)
+    gsr.qk_norm_rope_bwd(*ops[0], *ops[1], *ops[2], **r.kw_args, dq_weight=dw[0], dk_weight=dw[1], workspace=ws)
+    assert torch.equal(ops[2][keep], full[keep])
+    if dw[keep] is not None:                # the same sums, cut between CTAs by the heads that are there
+        cos, sin, _ = r.angles()
+        _, (want, terms) = serving.norm_rope_bwd(r.do[keep], (r.q, r.k)[keep], llm.f64((r.qw, r.kw)[keep]), cos, sin, r.R)
+        assert np.all(np.abs(llm.f64(dw[keep]) - want) <= 2.0 ** -16 * terms)
+    assert dw[gone] is None or torch.all(dw[gone] == 0)
+
+
 def test_gradient_repeats_whatever_the_workspace_and_stream():
     r = Rope(B=3, Hq=8, Hkv=2, S=700 // 4, D=128, R=128, dtype=BF16)
     want = [t.clone() for t in r.run_bwd() + r.dw]
