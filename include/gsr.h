@@ -411,7 +411,8 @@ typedef struct gsr_cache4 {
 /*
  * kv_cache_append_rope into caches of 4 bits: m is the least of 64 values, s = (largest - m) / 15 (both
  * rounded to the rows' type), c = (x - m) / s rounded to the nearest even and cut to 0..15, 0 where s is
- * 0.  64 values that hold an infinity or NaN, or span more than a float32, become NaN.
+ * 0.  64 values that hold an infinity or NaN, span more than a float32, or whose minimum or scale is beyond the
+ * rows' type (keys after their norm or rotation) become NaN.
  */
 gsr_status kv_cache4_append_rope(const gsr_rope_desc* desc, const gsr_tensor* Q, const gsr_tensor* K,
                                  const gsr_tensor* V, const int32_t* slots, const gsr_tensor* Q_out,

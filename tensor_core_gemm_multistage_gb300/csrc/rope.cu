@@ -336,7 +336,8 @@ __device__ __forceinline__ uint32_t codes_of(const f2* v, float s, float m) {
 // issue slots, 48 % of the integer pipe), minimum, maximum and codes of every value on top of the rotation.
 //
 // Per 64 values minimum m and scale s = (maximum - m) / 15, both rounded to T, and codes rint((x - m) / s) cut to
-// 0..15.  A group that holds infinities or NaN, or spans more than a float, is NaN as a whole.
+// 0..15.  A group that holds infinities or NaN, spans more than a float, or has a minimum or scale beyond T is NaN as a whole
+// (an infinite minimum with a finite scale would stand for 64 infinities, and a key of them can drop out of a softmax unseen).
 template <class T, int D>
 __device__ __forceinline__ void store_row4(char* codes, char* params, const LanePart& at, int l, bool live, const f2 (&v)[8]) {
     constexpr int LANES = D / 16;
@@ -362,9 +363,10 @@ __device__ __forceinline__ void store_row4(char* codes, char* params, const Lane
         const float x = __shfl_xor_sync(0xffffffffu, hi, o);
         hi = max3(hi, x, x);
     }
-    const float span = hi - lo;                            // NaN, or infinite, with what is not finite
-    const bool fine = span <= 3.402823466e38f;
-    const uint32_t pair = Pair<T>::pack(fine ? __fmul_rn(span, 1.0f / 15.0f) : NAN, fine ? lo : NAN);
+    const float scale = __fmul_rn(hi - lo, 1.0f / 15.0f);  // NaN, or infinite, with what is not finite
+    constexpr float END = Pair<T>::bf16 ? 0x1.ffp127f : 65520.0f;      // what rounds to an infinity of T
+    const bool fine = scale < END && fabsf(lo) < END;
+    const uint32_t pair = Pair<T>::pack(fine ? scale : NAN, fine ? lo : NAN);
     const uint32_t p0 = D > 64 ? __shfl_sync(0xffffffffu, pair, 4 * g0, LANES) : pair;
     const uint32_t p1 = D > 64 ? __shfl_sync(0xffffffffu, pair, 4 * g1, LANES) : pair;
     const float2 s0 = Pair<T>::unpack(p0), s1 = Pair<T>::unpack(p1);

@@ -426,6 +426,47 @@ def test_rows_that_are_hard_to_hold(D, dtype):
             assert torch.all((a - b).abs() <= tol), n
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_minimum_beyond_the_type(D, dtype):
+    """Keys whose norm or rotation takes them past the type's end: 64 values with such a minimum are NaN, and a node that sees
+    the key; past the upper end the codes still hold them."""
+    N, G, top = 6, D // 64, torch.finfo(dtype).max
+    k = torch.zeros(N, 1, D)
+    for n, x in enumerate((1.0, -1.0, 1.0, -1.0)):
+        k[n, 0, 3 if n < 2 else D - 3] = x
+    k[4:] = 0.5
+    table, w = torch.zeros(1, D), None
+    if dtype == F16:                          # a row of one value is sqrt(D) w there
+        k, w = k.to(dtype).to(DEV), torch.full((D,), 60000.0, dtype=dtype, device=DEV)
+        table[:, :D // 2] = 1.0
+        peak = 60000.0 * D ** 0.5
+    else:                                     # float32 holds 1.0025 of bfloat16's largest value, which rounds to an infinity
+        k[:4] *= top
+        k, peak = k.to(dtype).to(DEV), 1.0025 * top
+        table[:, :D // 2] = 1.0025
+    kc, vc = (gsr.kv_cache4(1, 16, 1, D, dtype, DEV) for _ in range(2))
+    v = torch.linspace(-1, 1, D).to(dtype).to(DEV).expand(N, 1, D).contiguous()
+    pos, slots = i32([0] * N), i32(list(range(N)))
+    gsr.kv_cache4_append_rope(k, v, slots, kc, vc, positions=pos, cos_sin=table.to(DEV), k_weight=w)
+    params, codes = kc.params[0, :N, 0].double().cpu(), kc.codes[0, :N, 0].cpu()
+    for n in range(4):
+        lost = n % 2 == 1                     # the minimum is -peak
+        for g in range(G):
+            here = g == (0 if n < 2 else G - 1)
+            s, m = params[n, g].tolist()
+            if here and lost:
+                assert np.isnan(s) and np.isnan(m), (n, g)
+            else:
+                assert m == 0.0 and s == pytest.approx(peak / 15 if here else 0.0, rel=2 * unit(dtype)), (n, g)
+    assert torch.isfinite(params[4:]).all() and codes[0, 1] == 0xf0 and codes[2, D // 2 - 2] == 0xf0
+    # attention: a request that sees row 0 alone, and one that sees row 1 as well
+    table4, o = i32([[0], [0]]), torch.empty(2, 1, D, dtype=dtype, device=DEV)
+    q = torch.full((2, 1, D), 2.0 ** -8 if dtype == F16 else 2.0 ** -120, dtype=dtype, device=DEV)
+    gsr.tree_attention4_fwd(q, kc, vc, table4, i32([1, 2]), i32([0, 1, 2]), None, o, 1)
+    assert torch.isfinite(o[0]).all() and torch.isnan(o[1]).all()
+
+
 def test_read_is_what_the_codes_stand_for():
     for D, dtype in ((64, F16), (128, BF16)):
         g = torch.Generator().manual_seed(D)
