@@ -299,7 +299,9 @@ gsr_status tree_attention_fwd(const gsr_tree_desc* desc, const void* Q, const gs
  *   kv_lens_out    batch: kv_lens + new_lens.           free_head_out  1: free_head + pages taken.
  *   q_starts       batch + 1: where each request's new tokens start among all of them.
  *   positions, slots  max_tokens: each new token's position in its request and its row in the
- *                  cache, page x page_size + row; -1 behind the last token.
+ *                  cache, page x page_size + row; -1 behind the last token.  Positions count tokens as they
+ *                  are stored, kv_lens + index: a prompt's or a chain's.  Nodes of a tree that branches stand
+ *                  elsewhere, at kv_lens + depth (see tree_attention_fwd).
  *   counts         3: new tokens, pages taken, pages missing.
  * Pages are missing when the free list ends or a request outgrows table_width; their table
  * entries (those inside the table) and their tokens' slots are -1.  All int32 device arrays;
@@ -384,9 +386,11 @@ gsr_status qk_norm_rope_bwd(const gsr_rope_desc* desc, const gsr_tensor* dQ_out,
 /*
  * kv_cache_append with the norm and rotation on the way: row n of y(K) and of V goes to cache row
  * slots[n], and Q_out = y(Q) where heads_q > 0 (in place or apart, as in qk_norm_rope_fwd).  desc: batch
- * 1, seq tokens; cos_sin needs positions (kv_block_tables writes them).  Slots outside the cache
- * and tokens of negative position are skipped; other cache rows are left as they were.  Caches as
- * in kv_cache_append; no two tokens of a call have the same slot (the row would hold pieces of both).
+ * 1, seq tokens; cos_sin needs positions.  Those of prompts, chains and single tokens are
+ * kv_block_tables'; a node of a tree that branches stands at the tokens before the tree + its depth, as
+ * tree_attention_fwd has it, so that siblings are turned alike and a kept path is turned as the chain that it
+ * becomes.  Slots outside the cache and tokens of negative position are skipped; other cache rows are left as they
+ * were.  Caches as in kv_cache_append; no two tokens of a call have the same slot (the row would hold pieces of both).
  */
 gsr_status kv_cache_append_rope(const gsr_rope_desc* desc, const gsr_tensor* Q, const gsr_tensor* K,
                                 const gsr_tensor* V, const int32_t* slots, const gsr_tensor* Q_out,
@@ -466,6 +470,10 @@ gsr_status tree_attention4_fwd(const gsr_tree_desc* desc, const void* Q, const g
  *   u_accept       total_q float32 in [0, 1).      u_sample  batch float32 in [0, 1).
  *   path           batch x max_nodes int32: the kept drafts' nodes from the root on, then -1.
  *   counts         batch int32: how many.          next_tokens  batch int32.
+ * Kept nodes' cache rows lie where the tree was written.  Before the next step the caller moves them together, in
+ * K and V: row L + path[i] of the request to row L + 1 + i, L tokens before node 0.  Rows of 4 bits are moved as codes
+ * and params (read and written again they would get other codes).
+ *
  * A request without nodes gets 0 and -1.  Nodes behind max_nodes (at most GSR_TREE_MAX_NODES) are not
  * tried.  Tokens outside the vocabulary are refused.  Sums are exact in fixed point, 45 bits behind the
  * point: results are the same on every run (a row's sum, 1 of a distribution, must stay below 2^18).

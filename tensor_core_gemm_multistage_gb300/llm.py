@@ -291,8 +291,8 @@ def kv_block_tables(kv_lens, new_lens, free_blocks, free_head, block_tables, pag
     Each request has kv_lens[b] cached tokens and gets new_lens[b] more.  Writes the entries of the
     pages it takes from free_blocks (from entry free_head[0] on) into block_tables, and kv_lens_out,
     free_head_out, q_starts (B + 1), positions and slots of the packed new tokens (-1 behind the
-    last), counts = (new tokens, pages taken, pages missing).  All int32; nothing is read back to the
-    host.  Returns slots.
+    last; positions as tokens are stored, which a branching tree's nodes do not have), counts = (new
+    tokens, pages taken, pages missing).  All int32; nothing is read back to the host.  Returns slots.
     """
     i32, dev = torch.int32, kv_lens.get_device()
     if dev < 0:

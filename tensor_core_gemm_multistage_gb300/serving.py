@@ -265,7 +265,8 @@ def kv_cache_append_rope(K, V, slots, k_cache, v_cache, positions=None, cos_sin=
     """kv_cache_append with K's norm and rotation on the way, and Q's into Q_out (N, Hq, D) where Q is given.
 
     K, V (N, H, D), slots (N,) int32 (negative: skipped), caches (pages, page_size, H, D); positions (N,) int32
-    (negative: padding).  ``cos_sin``, weights, ``eps`` and ``interleaved`` as in qk_norm_rope_fwd; Q_out may be Q.
+    (negative: padding): kv_block_tables' for prompts, chains and single tokens, the tokens before the tree + a
+    node's depth for trees.  ``cos_sin``, weights, ``eps`` and ``interleaved`` as in qk_norm_rope_fwd; Q_out may be Q.
     """
     cache = k_cache.shape
     if len(cache) != 4:
@@ -360,6 +361,7 @@ def verify_drafts(target_probs, draft_tokens, q_starts, parents, u_accept, u_sam
     node; draft_probs: the one each node's token was drawn from (None: tokens were not drawn).  draft_tokens (N,)
     int32; u_accept (N,), u_sample (B,) float32 in [0, 1).  Writes path (B, max_nodes) int32, the kept drafts' nodes
     and then -1; counts (B,) and next_tokens (B,).  Kept and drawn tokens are distributed as the target's.
+    The kept nodes' cache rows are the caller's to move together before the next step (a Cache4's codes and params).
     """
     dev, i32, f32 = target_probs.get_device(), torch.int32, torch.float32
     if dev < 0 or target_probs.dim() != 2:

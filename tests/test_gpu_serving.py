@@ -1046,3 +1046,126 @@ def test_serving_steps_with_drafts(captured):
         for b in range(B):                    # pages behind the kept tokens go back in this test by never being used again
             blocks[b, -(-int(lens[b]) // page):] = -1
     assert int(head) <= 30
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_a_branching_tree_is_its_paths(four):
+    """Nodes at the positions that their depth gives them: rotated queries, cache rows and answers of every path from the root to a
+    leaf are those of the same tokens written as a chain; so are the answers after the kept rows were moved together."""
+    B, Hq, Hkv, D, page, W, V, T = 2, 4, 2, 64, 16, 4, 50, 7
+    ctxs, parents = [21, 5], [[-1, 0, 0, 1, 1, 3, 2], [-1, 0, 1, 0, 3, 3, 5]]
+    g = torch.Generator(device=DEV).manual_seed(9)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV).to(F16)
+    cs, w = gsr.rope_table(100, D, device=DEV), (1 + 0.2 * rnd(2, D).float()).to(F16)
+    prompts, nodes = [rnd(n, Hq + 2 * Hkv, D) for n in ctxs], [rnd(T, Hq + 2 * Hkv, D) for _ in ctxs]
+    last = rnd(B, Hq + 2 * Hkv, D)
+    append, attend = (gsr.kv_cache4_append_rope, gsr.tree_attention4_fwd) if four else (gsr.kv_cache_append_rope, gsr.tree_attention_fwd)
+
+    class Server:
+        def __init__(self, seed):
+            gen = torch.Generator().manual_seed(seed)
+            if four:
+                self.caches = [gsr.kv_cache4(20, page, Hkv, D, F16, DEV) for _ in range(2)]
+                self.parts = [t for c in self.caches for t in c]
+            else:
+                self.caches = self.parts = [torch.zeros(20, page, Hkv, D, dtype=F16, device=DEV) for _ in range(2)]
+            self.free, self.table = torch.randperm(20, generator=gen).to(torch.int32).to(DEV), torch.full((B, W), -1, dtype=torch.int32, device=DEV)
+            self.lens, self.head = i32([0] * B), i32([0])
+
+        def step(self, new, parents=None, depth=None):
+            """Rows of each request; returns rotated queries, answers and the rows' slots."""
+            counts = [len(x) for x in new]
+            N = sum(counts) + 2                     # padding behind the last
+            rows = torch.cat(new + [torch.zeros(2, Hq + 2 * Hkv, D, dtype=F16, device=DEV)])
+            lens_out, head_out, q_starts, positions, slots = i32([0] * B), i32([0]), i32([0] * (B + 1)), i32([0] * N), i32([0] * N)
+            gsr.kv_block_tables(self.lens, i32(counts), self.free, self.head, self.table, page, lens_out, head_out, q_starts, positions, slots,
+                                i32([0] * 3))
+            if depth is not None:
+                request = torch.tensor([b for b in range(B) for _ in range(counts[b])] + [0, 0], device=DEV)
+                index = torch.arange(N, device=DEV) - q_starts[request]
+                depth = torch.tensor([x for d in depth for x in d] + [0, 0], device=DEV)
+                positions = torch.where(positions < 0, positions, positions - index + depth).to(torch.int32)
+            q, o = torch.full((N, Hq, D), 7.0, dtype=F16, device=DEV), torch.full((N, Hq, D), 7.0, dtype=F16, device=DEV)
+            append(rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:], slots, *self.caches, positions=positions, cos_sin=cs, Q=rows[:, :Hq], Q_out=q,
+                   q_weight=w[0], k_weight=w[1])
+            if max(counts) <= T:
+                up = None if parents is None else i32([x for p in parents for x in p] + [-1, -1])
+                attend(q, *self.caches, self.table, lens_out, q_starts, up, o, T)
+            self.lens_out, self.head, self.q_starts = lens_out, head_out, q_starts
+            return q, o, slots
+
+        def rows(self, slots):
+            slots = slots.long()
+            return [t[slots // page, slots % page] for t in self.parts]
+
+        def tolerance(self, q, parents):
+            """Of an answer, twice: both sides are within it of fp64's answer over the rows that the caches hold."""
+            k, v = ((serving.values4(c.codes.cpu().numpy(), c.params) for c in self.caches) if four
+                    else ((llm.f64(c), np.abs(llm.f64(c))) for c in self.caches))
+            args = (self.table.cpu().numpy(), self.lens_out.tolist(), self.q_starts.tolist(), None if parents is None else [x for p in parents for x in p],
+                    0.0, 0.0, None, T)
+            n, u = self.q_starts.tolist()[-1], unit(F16)
+            want, terms = llm.tree_attention(q, k[0], v[0], *args)[0][:n], llm.tree_attention(q, k[0], v[1], *args)[1][:n]
+            return 2 * ((u + 2.0 ** -13) * terms * (1 + u) + u * np.abs(want) + 2.0 ** -25)
+
+    depth, tree = [], Server(1)
+    for p in parents:
+        d = []
+        for up in p:
+            d.append(0 if up < 0 else d[up] + 1)
+        depth.append(d)
+    assert any(d != list(range(T)) for d in depth)
+    tree.step(prompts)
+    tree.lens.copy_(tree.lens_out)
+    q, o, slots = tree.step(nodes, parents, depth)
+    tol, held = tree.tolerance(q, parents), tree.rows(slots[:B * T])
+    assert torch.all(q[B * T:] == 0) and torch.all(o[B * T:] == 7.0)
+    paths = []
+    for p in parents:
+        ways = []
+        for leaf in range(T):
+            way = [leaf]
+            while p[way[0]] >= 0:
+                way.insert(0, p[way[0]])
+            ways.append(way)
+        paths.append(ways)
+    for leaf in range(T):
+        chain = Server(2 + leaf)
+        chain.step(prompts)
+        chain.lens.copy_(chain.lens_out)
+        ways = [ways[leaf] for ways in paths]
+        cq, co, cslots = chain.step([x[way] for x, way in zip(nodes, ways)])
+        at = torch.tensor([b * T + n for b in range(B) for n in ways[b]], device=DEV)
+        assert torch.equal(cq[:-2], q[at])
+        assert all(torch.equal(a, b[at]) for a, b in zip(chain.rows(cslots[:-2]), held))
+        assert np.all(np.abs(llm.f64(co[:-2]) - llm.f64(o[at])) <= tol[at.cpu().numpy()])
+    # a path of each request is kept: node 0 and two or three drafts below it
+    tokens, probs = i32(list(range(B * T))), torch.full((B * T, V), 0.5 / V, device=DEV)
+    ways = [paths[0][5], paths[1][6]]
+    for b, way in enumerate(ways):
+        for up, n in zip(way, way[1:]):
+            probs[b * T + up] *= 0.0
+            probs[b * T + up, b * T + n] = 1.0
+        probs[b * T + way[-1]] = 0.0
+        probs[b * T + way[-1], V - 1] = 1.0
+    path, kept, following = torch.full((B, T), 9, dtype=torch.int32, device=DEV), i32([9] * B), i32([9] * B)
+    gsr.verify_drafts(probs, tokens, tree.q_starts, i32(parents).flatten(), torch.full((B * T,), 0.5, device=DEV), torch.full((B,), 0.5, device=DEV),
+                      path, kept, following)
+    assert [path[b, :kept[b]].tolist() for b in range(B)] == [way[1:] for way in ways] and following.tolist() == [V - 1] * B
+    b, i = (path >= 0).nonzero(as_tuple=True)
+    src, dst = tree.lens[b] + path[b, i], tree.lens[b] + i + 1
+    row = lambda r: (tree.table[b, r // page].long(), r % page)
+    for t in tree.parts:
+        t[row(dst)] = t[row(src)]
+    tree.lens.add_(kept + 1)
+    # the next token after them, and after the same tokens as a chain
+    chain = Server(20)
+    chain.step(prompts)
+    chain.lens.copy_(chain.lens_out)
+    chain.step([x[way] for x, way in zip(nodes, ways)])
+    chain.lens.copy_(chain.lens_out)
+    new = [last[b:b + 1] for b in range(B)]
+    (q, o, slots), (cq, co, cslots) = tree.step(new), chain.step(new)
+    assert tree.lens_out.tolist() == chain.lens_out.tolist() and torch.equal(q, cq)
+    assert all(torch.equal(x, y) for x, y in zip(tree.rows(slots[:B]), chain.rows(cslots[:B])))
+    assert np.all(np.abs(llm.f64(o[:B]) - llm.f64(co[:B])) <= tree.tolerance(q, None))
