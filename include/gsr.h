@@ -437,7 +437,8 @@ gsr_status kv_cache4_read(const gsr_cache4* k_cache, const gsr_cache4* v_cache, 
  * tree_attention_fwd over caches of 4 bits (desc->dtype: that of Q, O and the scales; alibi_slopes
  * NULL; page and row strides below 2^32 bytes).  p s is rounded to float16, whatever the type, for the
  * second product (p to float32 for the minima); where the scales of one row of V are 2^20
- * apart, the smaller one's columns lose digits.  Scales are not negative.  A NaN scale or minimum in V makes
+ * apart, the smaller one's columns lose digits.  A query's values 2^25 below its largest lose digits, and
+ * bfloat16 queries that reach 2^112 get NaN.  Scales are not negative.  A NaN scale or minimum in V makes
  * its 64 columns NaN for the nodes that see the key, in K all columns, and has no influence on other nodes.
  *
  *   workspace  tree_attention4_workspace(desc) bytes (0 where there is little work; it depends on the sizes

@@ -11,7 +11,8 @@
 // does to O) leaves chunk by chunk with the sum of the rounded p s, a product with ones: left to the end it would cost
 // digits (4096 keys, fp16: 3.1e-4 of O), and as products with the constant -8 it took 10 us more of 161 (16
 // trees of 40 nodes over 4096 tokens, 8 heads of 4 queries each).  Queries are held
-// as fp16 times a power of two for each row (bf16's 8 bits fit; what is 2^-25 of the row's largest loses digits).
+// as fp16 times a power of two for each row (bf16's 8 bits fit; what is 2^-25 of the row's largest loses digits; from
+// 2^112 on, where the power of two that undoes it would overflow, a row is NaN).
 //
 // What bounds it: D / 2 + D / 16 bytes a key and head, twice, from HBM; per byte that is 3.6 times the
 // arithmetic of a 16-bit cache, so the instructions that unpack codes come next.  Codes are therefore unpacked
@@ -366,8 +367,8 @@ __device__ __forceinline__ bool t4_part(const Tree4Params& p, const Tree4Plan& p
                 }
         largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
         largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
-        // the row times 2^e is below 2^11 beside c 2^-20, and 16 times that beside c 2^-24
-        const int e = min(max(10 - ((int)(largest >> 23) - 127), -100), 100);
+        // the row times 2^e is below 2^11 beside c 2^-20, and 16 times that beside c 2^-24; 16 2^e and 2^-e 2^20 are floats
+        const int e = min(max(10 - ((int)(largest >> 23) - 127), -100), 123);
         const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
         for (int gi = 0; gi < G; ++gi) {

@@ -585,6 +585,15 @@ def test_tree_attention4(name, even):
     t.run().check()
 
 
+@pytest.mark.parametrize("up", [100, -100, -122])
+def test_queries_of_any_size(up):
+    """Queries times 2^up over keys times 2^-up: the scores, and so the answers, are those of ordinary sizes."""
+    t = Tree4(kv=[300, 41], T=[9, 1], Hq=8, Hkv=2, D=128, page=16, dtype=BF16)
+    t.q = (t.q.double() * 2.0 ** up).to(BF16)
+    t.caches[0].params.copy_((t.caches[0].params.double() * 2.0 ** -up).to(BF16))
+    t.run().check()
+
+
 def _random_trees(n, seed):
     r = np.random.default_rng(seed)
     out = []
