@@ -227,6 +227,22 @@ def test_binding_refusals():
         gsr.kv_cache4(1, 16, 1, 96)
 
 
+def test_packed_structures():
+    """Calls pack the structures as bytes: sizes, and each field's place, are those of the declared ones."""
+    import ctypes
+    from tensor_core_gemm_multistage_gb300 import serving
+    for pack, kind in ((serving._pack_tensor, _Tensor), (serving._pack_cache4, _Cache4), (serving._pack_rope, _RopeDesc),
+                       (serving._pack_tree, _TreeDesc), (serving._pack_verify, _VerifyDesc)):
+        fields = [f for name, t in kind._fields_ for f in (t._fields_ if issubclass(t, ctypes.Structure) else [(name, t)])]
+        made, values = pack(*range(1, len(fields) + 1)), []
+        assert len(made) == ctypes.sizeof(kind)
+        held = kind.from_buffer_copy(made)
+        for name, t in kind._fields_:
+            x = getattr(held, name)
+            values += [getattr(x, n) for n, _ in t._fields_] if issubclass(t, ctypes.Structure) else [x]
+        assert values == list(range(1, len(fields) + 1))
+
+
 def test_tables_of_angles():
     import math
     import torch
