@@ -21,9 +21,11 @@
 // Where many rows share a key that would be no hindrance; but 128 rows on tcgen05, two CTAs an SM, took 175 us for 16
 // trees of 40 nodes: product, scores, p s and product follow one another, 6500 clocks for 64 keys.  Measured, D = 128, 8
 // heads of keys, 32 of queries: 48 requests of 4000 to 8000 tokens 75 us (4.3 TB/s), 16 trees of 40 nodes over up to 4096
-// tokens 155 us (148 TFLOP/s; a warp's own latencies, with two warps a scheduler).
-// Keys are the products' rows (16 at once) and the queries of a group their columns (8): no row of the product is
-// spent on padding where a group has 4 or 8 heads.
+// tokens 155 us (148 TFLOP/s; a warp's own latencies, with two warps a scheduler). The 75 us are no unit's limit either: issue 57 %,
+// integer pipe 48 %, tensor cores 25 %, with four CTAs of 128 registers an SM.
+// Keys are the products' rows (16 at once) and the rows of queries that share them, nodes x group, their columns (8): no row
+// is padding whatever the group, and no column where nodes x group is a multiple of 8.  With one token and 4 queries a key
+// head half of the columns are padding, and of the lanes that compute scores and probabilities after them.
 //
 // Split.  A CTA's four warps take 32-key chunks of one request, head and tile of 8 NT query rows in turn; each warp
 // copies its own chunks (cp.async) and has its own softmax state, and the states are joined in shared memory.
@@ -255,8 +257,8 @@ struct T4Shared {
     int parent[GSR_TREE_MAX_NODES];
 };
 
-// Chunks first + i step (of this warp) below `end` of an item; false where the tile has no rows.  out(write, q, d, most, sum, v): the CTA's joined state of row q, dimensions d and d + 1 (write(q, d, x, y,
-// sum) puts them into O).
+// Chunks first + i step (of this warp) below `end` of an item; false where the tile has no rows.  out(write, q, d, most,
+// sum, v): the CTA's joined state of row q, dimensions d and d + 1 (write(q, d, x, y, sum) puts them into O).
 template <class C, class Out>
 __device__ __forceinline__ bool t4_part(const Tree4Params& p, const Tree4Plan& plan, char* smem, T4Shared& sh, int b, int h, int tile, int first,
                                         int step, int end, Out out) {

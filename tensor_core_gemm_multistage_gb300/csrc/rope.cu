@@ -332,8 +332,9 @@ __device__ __forceinline__ uint32_t codes_of(const f2* v, float s, float m) {
     }
     return w;
 }
-// What bounds these writes is the arithmetic: 24576 tokens of 8 x 128 with K's rotation 51 us (129 MB, 2.5 TB/s; 64 % of the
-// issue slots, 48 % of the integer pipe), minimum, maximum and codes of every value on top of the rotation.
+// These writes follow the number of instructions, minimum, maximum and codes of every value on top of the rotation: 24576
+// tokens of 8 x 128 with K's rotation 51 us (129 MB, 2.5 TB/s). No unit is full (64 % of the issue slots, 48 % of the integer
+// pipe): two CTAs of 128 registers an SM do not cover a warp's own latencies.
 //
 // Per 64 values minimum m and scale s = (maximum - m) / 15, both rounded to T, and codes rint((x - m) / s) cut to
 // 0..15.  A group that holds infinities or NaN, spans more than a float, or has a minimum or scale beyond T is NaN as a whole
@@ -738,8 +739,8 @@ cudaError_t launch_bwd(const RopeBwdParams& a, cudaStream_t stream) {
 // ---------------------------------------------------------------------------
 // Rows of a cache of 4 bits, read back
 // ---------------------------------------------------------------------------
-// 24576 tokens of 8 x 128 in 24 us: 129 MB, four fifths of a copy's rate.  A lane takes 16 values: 8 bytes of codes become 32 bytes.  s x code is exact in fp32, so a value is rounded
-// once there and once to T.
+// 24576 tokens of 8 x 128 in 24 us: 129 MB, four fifths of a copy's rate.  A lane takes 16 values: 8 bytes of codes become
+// 32 bytes.  s x code is exact in fp32, so a value is rounded once there and once to T.
 template <class T, int D>
 __global__ void __launch_bounds__(kThreads) gsr_read4_kernel(const __grid_constant__ Read4Params p, const Divider by_head,
                                                              const Divider by_page, long long rows) {
